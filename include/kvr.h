@@ -459,6 +459,161 @@ int kvr_profile_launches(kvr_ctx* ctx, int* cls, float* ms, int max_n, int* n);
 
 const char* kvr_last_error(const kvr_ctx* ctx);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Paged 4-bit cache.  K and V of many sequences in pages of KVR_PAGE_TOKENS
+ * tokens, 4 bits per value, with page tables and lengths that live on the
+ * device: a step (plan, then per layer append and attend) needs no host
+ * read-back and can be captured into a CUDA graph.  (The pages name a cache
+ * of one row per token and layer; packing it into 4 bits and pages is a
+ * property of this library.)
+ *
+ * Values.  Each group of 32 elements along the head dimension of one token's
+ * k or v holds s = min(fp16(max|x| / 7), 8188) and codes
+ * c = clamp(round_to_even(x / s), -8, 7); the cache stands for c * s.  A group
+ * of zeros (or too small for an fp16 scale) has s = 0 and stands for zeros.
+ * A group that holds a NaN or an infinity has s = NaN: a query head that sees
+ * the token reads NaN (in v's groups of that token at least), rows and heads
+ * that do not see it are unaffected.
+ *
+ * Configuration (kvr_pages_config):
+ *   n_pages     pages shared by all sequences (1 .. 2^24).
+ *   n_layers, n_q_heads, n_kv_heads, head_dim   as kvr_config (head_dim 64 or
+ *               128, at most 64 query heads per KV head).
+ *   max_seqs    sequences (1 .. 2048); sequence b owns row b of the table.
+ *   max_len     longest sequence in tokens (1 .. 2^22).
+ *   max_rows    most rows of one step (1 .. 2^22).
+ *   act         type of q, k, v, gains and outputs: KVR_ACT_BF16, KVR_ACT_F16.
+ *   rope_theta  rotate-half RoPE base.  norm_eps  epsilon of the q/k norms.
+ *
+ * Memory.  kvr_pages_pool_bytes is the size of the pool:
+ *   [n_layers][n_pages][n_kv_heads][chunk], a chunk being one page of one KV
+ *   head (64 * head_dim / 2 bytes of K codes, as many of V codes, 64 *
+ *   head_dim / 32 fp16 scales of K, as many of V; the order inside is the
+ *   kernels' own, kvr_page_read gives the values).
+ * kvr_pages_work_bytes is the size of the work area: tables, lengths, row
+ *   maps, the positions' cosines and sines, partial results, status.
+ * Both 256-byte aligned, owned by the caller, used by one handle only.  Both
+ * functions return 0 for an invalid configuration.  kvr_pages_create writes
+ * the work area (all pages free, no sequence has tokens) and synchronises the
+ * device, which has to be the buffers' own; the pool needs no initial value.
+ *
+ * Streams.  plan, append, read and attend are asynchronous on their stream
+ * and make no host decision from device data, so they can be captured; their
+ * calls on one handle must be ordered (one stream, or events between them),
+ * and so must replays of graphs that captured them: the work area holds the
+ * state and the partial results of one call at a time.  A handle is not
+ * thread-safe.  The calls may be made with any device current; the stream is
+ * one of the handle's device.
+ *
+ * Errors as for a context: a negative code, and kvr_pages_error says why.  A
+ * call refused by its checks launches nothing.
+ */
+#define KVR_PAGE_TOKENS 64
+#define KVR_ACT_BF16 0
+#define KVR_ACT_F16 1
+
+typedef struct kvr_pages_config {
+  int n_pages;
+  int n_layers;
+  int n_q_heads;
+  int n_kv_heads;
+  int head_dim;
+  int max_seqs;
+  int max_len;
+  int max_rows;
+  int act;
+  float rope_theta;
+  float norm_eps;
+} kvr_pages_config;
+
+typedef struct kvr_pages kvr_pages;
+
+size_t kvr_pages_pool_bytes(const kvr_pages_config* cfg);
+size_t kvr_pages_work_bytes(const kvr_pages_config* cfg);
+int kvr_pages_create(const kvr_pages_config* cfg, void* pool, size_t pool_bytes, void* work,
+                     size_t work_bytes, kvr_pages** out);
+int kvr_pages_destroy(kvr_pages* pages);
+
+/* Device addresses of the state, for inspection (reads ordered after the
+ * stream's calls; the caller writes none of them). */
+typedef struct kvr_page_tables {
+  const int32_t* table;     /* [max_seqs][table_width] page of each 64 tokens, -1 where none is held */
+  const int32_t* lens;      /* [max_seqs] tokens of each sequence                                    */
+  const int32_t* free_list; /* [n_pages] stack of free pages, count[0] of them                       */
+  const int32_t* count;     /* [1]                                                                   */
+  const int32_t* cu_rows;   /* [max_seqs + 1] first row of each sequence of the last plan            */
+  const int32_t* row_seq;   /* [max_rows] sequence, position and slot (page * 64 + place) of each    */
+  const int32_t* row_pos;   /* [max_rows] row of the last plan; -1 for rows behind the last one      */
+  const int32_t* row_slot;  /* [max_rows]                                                            */
+  int table_width;          /* ceil(max_len / 64)                                                    */
+} kvr_page_tables;
+int kvr_pages_tables(const kvr_pages* pages, kvr_page_tables* out);
+
+/*
+ * Plan a step, on the device.  keep, add: device int32 [n_seq].  Sequence b
+ * (b < n_seq) keeps its first keep[b] tokens (all of them, fewer after
+ * rejected drafts, 0 when it ended or starts again) and gains add[b] rows
+ * (0 for one that has none this step); sequences n_seq .. max_seqs - 1 keep
+ * what they have.  Pages that the new length does not need return to the free
+ * list, pages that it lacks are taken from it.  Row i of sequence b is row
+ * cu_rows[b] + i of the step, at position keep[b] + i.
+ *   rows     rows of the step's buffers, 0 <= rows <= max_rows; the sum of
+ *            add may be smaller (a padded batch): the rows behind are skipped
+ *            by append, read and attend, which leave their outputs as they were.
+ *   max_add  no add[b] is larger; <= 0 stands for rows.  A close bound lets
+ *            kvr_page_attend launch fewer kernels.
+ * Order of the pages: the r-th released page (by sequence, then by place in
+ * it; released first) goes to free_list[count + released - 1 - r], the t-th
+ * taken page comes from free_list[count + released - 1 - t].
+ * A plan whose keep or add are out of range (keep[b] < 0 or > lens[b],
+ * add[b] < 0 or > max_add, keep[b] + add[b] > max_len, sum of add > rows), or
+ * that lacks free pages, changes neither lengths nor pages: the step then has
+ * no rows, and kvr_pages_sync reports it.
+ */
+int kvr_page_plan(kvr_pages* pages, int n_seq, const int32_t* keep, const int32_t* add, int rows,
+                  int max_add, void* stream);
+
+/*
+ * The planned rows of one layer: q and k normed per head (x / sqrt(mean x^2 +
+ * eps) * gain; norm_q, norm_k: [head_dim], null for none), rotated by the
+ * row's position (rotate = 1) and rounded once to the activation type; q goes
+ * to q_out [rows][n_q_heads][head_dim], k (so rounded) and v (as it is) are
+ * quantised into the row's slot.
+ *   q, k, v   [rows] with the heads of a row contiguous and a row stride in
+ *             elements (a multiple of 8): views of one projection output work.
+ *             q and q_out may both be null (k and v only); q_out may be q if
+ *             its stride is n_q_heads * head_dim.
+ * All pointers 16-byte aligned.  rows must be the plan's.
+ */
+int kvr_page_append(kvr_pages* pages, int layer, const void* q, long long q_stride, const void* k,
+                    long long k_stride, const void* v, long long v_stride, const void* norm_q,
+                    const void* norm_k, int rotate, void* q_out, int rows, void* stream);
+
+/* The values that the cache holds for the planned rows of one layer, rounded
+ * to the activation type: k_out, v_out [rows][n_kv_heads][head_dim]. */
+int kvr_page_read(kvr_pages* pages, int layer, void* k_out, void* v_out, int rows, void* stream);
+
+/*
+ * Causal grouped-query attention of the planned rows over the pages of their
+ * sequences: out = softmax(scale * q K^T) V, the row at position p sees the
+ * tokens 0 .. p of its sequence (its own included: append first).
+ *   q        [rows] rows of n_q_heads * head_dim, row stride q_stride elements
+ *            (a multiple of 8); out [rows][n_q_heads][head_dim], apart from q.
+ *   out_f16  1: the rows, rounded to the activation type, are stored as fp16.
+ *   scale    a positive number.
+ * The same call gives the same bits (no atomic adds).  rows must be the plan's.
+ */
+int kvr_page_attend(kvr_pages* pages, int layer, const void* q, long long q_stride, void* out,
+                    int out_f16, float scale, int rows, void* stream);
+
+/* Wait for `stream` and report what its calls could not: KVR_ERR_ARG or
+ * KVR_ERR_CAPACITY for a plan that was refused on the device (see
+ * kvr_page_plan; the first one since the last call), KVR_ERR_TIMEOUT for a
+ * device-side wait that gave up.  Clears both. */
+int kvr_pages_sync(kvr_pages* pages, void* stream);
+const char* kvr_pages_error(const kvr_pages* pages);
+
 #ifdef __cplusplus
 }
 #endif

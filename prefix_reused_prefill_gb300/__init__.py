@@ -6,3 +6,4 @@ is no CPU fallback: importing the binding without the built library raises.
 """
 from .kvr import (KVR_OK, KvrError, Kvr, config_for_shape, layer_weight_structs,  # noqa: F401
                   load_library)
+from .pages import PagedKv, paged_config  # noqa: F401

@@ -1,0 +1,137 @@
+// Internal declarations of the paged 4-bit cache (include/kvr.h).
+#pragma once
+
+#include "kvr_internal.cuh"
+
+namespace kvr {
+
+constexpr int kPage = KVR_PAGE_TOKENS;   // tokens of a page
+constexpr int kPageGroup = 32;           // elements along the head dimension that share a scale
+constexpr float kPageScaleMax = 8188.f;  // 8 * 8188 = 65504: every value c * s has an fp16 number's magnitude
+constexpr int kPageMaxSeqs = 2048;
+
+// One page of one KV head ("chunk"), in the order the tensor-core fragments
+// want it.  Key = token within the page, g = 0..7 and t = 0..3 the lane
+// coordinates of an m16n8k16 fragment, j the groups of 32 dims.
+//   K codes  [key][t][j] 32-bit words: dims 32 j + 8 t + 0..7 of the key.  Dims
+//            2r and 2r + 1 of the eight sit in nibbles r and r + 4, so one bit
+//            mask on a word gives two neighbouring dims as a 16-bit pair.
+//   V codes  [key / 8][g][t][j] words: keys 8 (key / 8) + 2t (low half) and
+//            2t + 1 (high half), nibble n of a half is dim 32 j + 4 g + n.
+//            (Every 16-bit unit belongs to one token: an append never shares a
+//            store with another token.)
+//   K scales [key][j] fp16.
+//   V scales [key / 16][t][(key / 8) % 2][j] pairs of fp16 (keys 2t, 2t + 1).
+// A code is held with 8 added.
+template <int D>
+struct Chunk {
+  static constexpr int kGroups = D / kPageGroup;
+  static constexpr int kCodes = kPage * D / 2;
+  static constexpr int kScales = kPage * kGroups * 2;
+  static constexpr int kV = kCodes;
+  static constexpr int kKs = 2 * kCodes;
+  static constexpr int kVs = 2 * kCodes + kScales;
+  static constexpr int kBytes = 2 * (kCodes + kScales);
+
+  static __host__ __device__ __forceinline__ int k_word(int key, int t, int j) {
+    return ((key * 4 + t) * kGroups + j) * 4;
+  }
+  static __host__ __device__ __forceinline__ int v_unit(int key, int g, int j) {
+    return kV + ((((key >> 3) * 8 + g) * 4 + ((key >> 1) & 3)) * kGroups + j) * 4 + (key & 1) * 2;
+  }
+  static __host__ __device__ __forceinline__ int k_scale(int key, int j) { return kKs + (key * kGroups + j) * 2; }
+  static __host__ __device__ __forceinline__ int v_scale(int key, int j) {
+    return kVs + ((((key >> 4) * 4 + ((key >> 1) & 3)) * 2 + ((key >> 3) & 1)) * kGroups + j) * 4 + (key & 1) * 2;
+  }
+};
+
+inline size_t page_chunk_bytes(int d) { return d == 128 ? Chunk<128>::kBytes : Chunk<64>::kBytes; }
+
+// What every kernel of the paged cache gets (device pointers of the work area).
+struct PagesDev {
+  uint8_t* pool;
+  long long layer_off;   // bytes before this layer
+  int32_t* table;        // [max_seqs][width]
+  int32_t* lens;
+  int32_t* free_list;
+  int32_t* count;
+  int32_t* cu;           // [max_seqs + 1]
+  int32_t* row_seq;
+  int32_t* row_pos;
+  int32_t* row_slot;
+  int32_t* info;         // [2]: sequences and rows of the last plan
+  const float2* rope;    // [max_len][d / 2] (cos, sin)
+  int* status;           // a wait that gave up
+  int* refused;          // the first refused plan's error code
+  int n_pages, width, max_len, max_rows;
+  int Hq, Hkv, G, d;
+  int f16;               // activations are fp16 (else bf16)
+};
+
+struct PageAppend {
+  const void* q;
+  const void* k;
+  const void* v;
+  long long qs, ks, vs;      // row strides in elements
+  const void* norm_q;
+  const void* norm_k;
+  void* q_out;
+  int rotate, rows;
+  float eps;
+};
+
+// Attention of the sequences with G * rows <= many (the split kernel).
+struct PageAttend {
+  const void* q;
+  long long qs;
+  void* out;
+  int out_f16;
+  int rows;
+  int many;
+  float scale_log2;
+  float* part;       // partial outputs
+  float2* ml;        // their (max in log2 units, sum)
+  int* counters;     // arrivals, zero between launches
+};
+
+constexpr int kPageAttnWarps = 8;
+constexpr int kPageAttnRows = 16;      // rows of a tile: two 8-column tensor-core tiles at most
+constexpr int kPageAttnMaxCtas = 160;
+// partial results of the split kernel: two per warp and two per CTA
+constexpr int kPageAttnSlots = kPageAttnMaxCtas * (2 * kPageAttnWarps + 2);
+
+cudaError_t page_plan_setup();
+// every page free, the first ones on top
+cudaError_t launch_page_init(const PagesDev& p, cudaStream_t st);
+cudaError_t launch_page_rope(const RopeFreq& fr, int max_len, int d, float2* table, cudaStream_t st);
+cudaError_t launch_page_plan(const PagesDev& p, int n_seq, const int32_t* keep, const int32_t* add, int rows,
+                             int max_add, cudaStream_t st);
+cudaError_t launch_page_append(const PagesDev& p, const PageAppend& a, cudaStream_t st);
+cudaError_t launch_page_read(const PagesDev& p, void* k_out, void* v_out, int rows, cudaStream_t st);
+cudaError_t page_attn_setup();
+cudaError_t launch_page_attn(const PagesDev& p, const PageAttend& a, int nt, int ctas, cudaStream_t st);
+
+}  // namespace kvr
+
+#ifdef __CUDACC__
+namespace kvr {
+namespace dev {
+
+// two activations of either 16-bit type
+template <bool F16>
+__device__ __forceinline__ float2 act2(uint32_t u) {
+  if (F16) return __half22float2(*reinterpret_cast<__half2*>(&u));
+  return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&u));
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t pack_act(float lo, float hi) {
+  if (F16) {
+    __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&h);
+  }
+  return pack_bf16x2(lo, hi);
+}
+
+}  // namespace dev
+}  // namespace kvr
+#endif

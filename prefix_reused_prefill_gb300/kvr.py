@@ -31,7 +31,10 @@ EXPORTED = ["kvr_arena_bytes", "kvr_scratch_bytes", "kvr_ctx_create", "kvr_ctx_i
             "kvr_profile_launches",
             "kvr_last_error", "kvr_slot_match_static", "kvr_trace_set", "kvr_verify_accept",
             "kvr_config_hash", "kvr_slot_spill_bytes", "kvr_slot_spill", "kvr_slot_restore",
-            "kvr_prefill_batch", "kvr_selftest_wait", "kvr_verify_accept_batch"]
+            "kvr_prefill_batch", "kvr_selftest_wait", "kvr_verify_accept_batch",
+            "kvr_pages_pool_bytes", "kvr_pages_work_bytes", "kvr_pages_create", "kvr_pages_destroy",
+            "kvr_pages_tables", "kvr_pages_sync", "kvr_pages_error", "kvr_page_plan", "kvr_page_append",
+            "kvr_page_read", "kvr_page_attend"]
 
 
 class KvrError(RuntimeError):
@@ -62,6 +65,18 @@ class KvrHeadWeights(ctypes.Structure):
                 ("vocab", ctypes.c_int)]
 
 
+class KvrPagesConfig(ctypes.Structure):
+    _fields_ = [("n_pages", ctypes.c_int), ("n_layers", ctypes.c_int), ("n_q_heads", ctypes.c_int),
+                ("n_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("max_seqs", ctypes.c_int),
+                ("max_len", ctypes.c_int), ("max_rows", ctypes.c_int), ("act", ctypes.c_int),
+                ("rope_theta", ctypes.c_float), ("norm_eps", ctypes.c_float)]
+
+
+class KvrPageTables(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_void_p) for f in ("table", "lens", "free_list", "count", "cu_rows", "row_seq",
+                                               "row_pos", "row_slot")] + [("table_width", ctypes.c_int)]
+
+
 _lib = None
 
 
@@ -73,7 +88,7 @@ def load_library(path: str = LIB_PATH):
         raise ImportError(f"libkvr.so not built at {path}: run __graft_entry__.build()")
     lib = ctypes.CDLL(path)
     P, I, Z, V = ctypes.POINTER, ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p
-    i32p = P(ctypes.c_int32)
+    i32p, LL = P(ctypes.c_int32), ctypes.c_longlong
     sig = {
         "kvr_arena_bytes": (Z, [P(KvrConfig), I]),
         "kvr_scratch_bytes": (Z, [P(KvrConfig)]),
@@ -106,6 +121,17 @@ def load_library(path: str = LIB_PATH):
         "kvr_slot_spill_bytes": (Z, [V, I]),
         "kvr_slot_spill": (I, [V, I, ctypes.c_uint64, V, Z, V]),
         "kvr_slot_restore": (I, [V, I, ctypes.c_uint64, V, Z, V]),
+        "kvr_pages_pool_bytes": (Z, [P(KvrPagesConfig)]),
+        "kvr_pages_work_bytes": (Z, [P(KvrPagesConfig)]),
+        "kvr_pages_create": (I, [P(KvrPagesConfig), V, Z, V, Z, P(V)]),
+        "kvr_pages_destroy": (I, [V]),
+        "kvr_pages_tables": (I, [V, P(KvrPageTables)]),
+        "kvr_pages_sync": (I, [V, V]),
+        "kvr_pages_error": (ctypes.c_char_p, [V]),
+        "kvr_page_plan": (I, [V, I, V, V, I, I, V]),
+        "kvr_page_append": (I, [V, I, V, LL, V, LL, V, LL, V, V, I, V, I, V]),
+        "kvr_page_read": (I, [V, I, V, V, I, V]),
+        "kvr_page_attend": (I, [V, I, V, LL, V, I, ctypes.c_float, I, V]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
