@@ -3,18 +3,15 @@
 //
 //   o_r = sum_k p_rk v_k / sum_k p_rk,   p_rk = 2^(scale log2(e) q_r k_k - m_r)
 // over the keys k that row r sees, with the running maximum m_r of one pass.
-// With k_k = sK_kj (c - 8) per group j of 32 dims, the score is
-//   sum_j sK_kj (sum_(d in j) q_d c_kd - 8 sum_(d in j) q_d).
-// The tensor cores multiply the 4-bit codes themselves: a nibble in bits 0-3
-// (4-7) of a 16-bit half IS the fp16 subnormal c 2^-24 (c 2^-20), one AND per
-// two codes.  (Their sums align a subnormal as if it were 2^-14 in size, which
-// costs a score at most 2^-13 of max|q| sK: measured, 2^-14 of the term.)  The
-// scale multiplies the fp32 sum of its group.
-// The values are summed over thousands of keys, where such a cut and the bias of
-// 8 would add up: there a code becomes the fp16 number c - 8 (the nibble under
-// the exponent of 1024 or 64, less 1032 or 72: exact), and
-//   o_d = sum_k (p_k sV_kj) (c_kd - 8)
-// with the scale on the weights: p and p sV are fp16 (2^-11 each, relative to
+// With k_k = sK_kj (c - 8) per group j of 32 dims, the score is the sum over j of
+// sK_kj (sum_(d in j) q_d (c_kd - 8)), and with v_k = sV_kj (c - 8)
+//   o_d = sum_k (p_k sV_kj) (c_kd - 8).
+// The tensor cores multiply the codes, as fp16 numbers c - 8: the nibble under the
+// exponent of 1024 or 64 (one AND-OR for two codes), less 1032 or 72, exactly.
+// (The nibble alone is an fp16 subnormal and needs no subtraction, but sums of
+// such products are cut at 2^-14 of the code unit, and with the bias of 8 that
+// adds up over thousands of keys.)  The K scale multiplies the fp32 sum of its
+// group, the V scale the weights: p and p sV are fp16 (2^-11 each, relative to
 // the weight; the row's sum takes p unrounded), p held with a factor 4 so that
 // p sV stays in range (p <= 1, sV <= 8188).  q is scaled per row by a power of
 // two so that any bf16 q is an fp16 number.
@@ -23,30 +20,36 @@
 // the rows, at most 8 or 16 of a tile, fill the narrow N side.
 //
 // Bound by HBM: a page of one KV head is 9216 contiguous bytes (head dim 128),
-// fetched by one bulk copy.  The work, all (sequence, row tile, KV head, page)
-// units in this order, is cut into equal runs, one for each CTA and in it one
-// for each warp, whatever the lengths are; every warp streams its run through a
-// ring of its own.  A segment (the pages of one sequence, tile and head) that
-// one warp covers alone is finished by it; otherwise the warps' parts are
-// merged by the CTA, and the CTAs' parts by the last of them to arrive, in the
-// order of the pages.
+// fetched as two bulk copies, K and V.  The work, all (sequence, row tile, KV
+// head, page) units in this order, is cut into equal runs, one for each CTA and
+// in it one for each warp, whatever the lengths are; every warp streams its run
+// through a ring of its own.  A segment (the pages of one sequence, tile and
+// head) that one warp covers alone is finished by it; otherwise the warps'
+// parts are merged by the CTA, and the CTAs' parts by the last of them to
+// arrive, in the order of the pages.  Where there are few segments, each of a
+// page or two per warp, a CTA takes a whole one instead: the second page costs
+// less than a merge across CTAs.
+#include <type_traits>
+
 #include "kvr_pages.cuh"
 
 namespace kvr {
 
 namespace {
 
-constexpr int kWarps = kPageAttnWarps;
-constexpr int kThreads = 32 * kWarps;
-
+// 16 warps where their registers allow it (tiles of 8 rows): one warp alone
+// waits for its loads and products most of the time.
 template <int D, int NT>
 struct Cfg {
-  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kWarps = NT == 1 ? 16 : 8;
+  static constexpr int kThreads = 32 * kWarps;
   static constexpr int kGroups = D / 32;
-  static constexpr int kChunk = Chunk<D>::kBytes;
+  static constexpr int kHalf = Chunk<D>::kHalf;
+  static constexpr int kStages = 48 / kWarps * (128 / D);   // halves of pages
   static constexpr int kRows = 8 * NT;
-  static constexpr int kRing = kStages * kChunk;
-  static constexpr int kSlot = kPageAttnRows * D;   // floats of a partial result
+  static constexpr int kRing = kStages * kHalf;
+  static constexpr int kSlot = kRows * D;                   // floats of a partial result
+  static_assert(kSlot * 4 + kRows * 8 <= kRing, "a partial result fits the ring");
 };
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
@@ -69,6 +72,15 @@ __device__ __forceinline__ void mma(float* d, uint32_t a0, uint32_t a1, uint32_t
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// d = a * b
+__device__ __forceinline__ void mma_first(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -82,12 +94,24 @@ __device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
   __half2 r = __hadd2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
   return *reinterpret_cast<uint32_t*>(&r);
 }
-// codes in bits 0-3 and 4-7 of both halves as the fp16 numbers c - 8
-__device__ __forceinline__ uint32_t centred_lo(uint32_t w) {
-  return hadd2((w & 0x000f000fu) | 0x64006400u, 0xe408e408u);   // 1024 + c - 1032
+// a register with a constant that the compiler does not form anew at each use
+__device__ __forceinline__ uint32_t held(uint32_t x) {
+  asm volatile("" : "+r"(x));
+  return x;
 }
-__device__ __forceinline__ uint32_t centred_hi(uint32_t w) {
-  return hadd2((w & 0x00f000f0u) | 0x54005400u, 0xd480d480u);   // 64 + c - 72
+// codes in bits 0-3 (4-7) of both halves as the fp16 numbers c - 8; k1024 and k64
+// hold those numbers in both halves
+template <uint32_t kMask>
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t bits) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(w), "n"(kMask), "r"(bits));
+  return r;
+}
+__device__ __forceinline__ uint32_t centred_lo(uint32_t w, uint32_t k1024) {
+  return hadd2(and_or<0x000f000fu>(w, k1024), 0xe408e408u);   // 1024 + c - 1032
+}
+__device__ __forceinline__ uint32_t centred_hi(uint32_t w, uint32_t k64) {
+  return hadd2(and_or<0x00f000f0u>(w, k64), 0xd480d480u);     // 64 + c - 72
 }
 template <int W>
 __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t* w) {
@@ -119,6 +143,11 @@ struct Place {
   int row0, m, P;          // first row and rows of the sequence, its tokens before them
 };
 
+// the segment of a partial result: its units, and the rows it belongs to
+struct Rec {
+  int pages, tile, kv, row0, m;
+};
+
 // a partial result: [rows of a tile][D] floats, and (m, l) per row
 struct Slot {
   float* o;
@@ -126,69 +155,106 @@ struct Slot {
 };
 
 template <int D, int NT, bool F16>
-__global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const PagesDev p, const PageAttend a) {
+__global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
+page_attn_kernel(const PagesDev p, const PageAttend a) {
   using C = Cfg<D, NT>;
   using K = Chunk<D>;
-  constexpr int kG = C::kGroups;
+  constexpr int kG = C::kGroups, kWarps = C::kWarps, kThreads = C::kThreads;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t full_bar[kWarps][C::kStages];
   __shared__ int first_unit[kPageMaxSeqs + 1];   // units before each sequence
-  __shared__ int scan[kWarps];
-  // partial results of this CTA in the order of the pages: two per warp
+  __shared__ int scan_u[kWarps], scan_s[kWarps], scan_p[kWarps];
+  // partial results of this CTA in the order of the pages: two per warp, one in
+  // the work area (a segment that ended inside the run) and one in its ring
   __shared__ int rec_seg[2 * kWarps];            // first unit of the segment, -1 for none
-  __shared__ int rec_seg_n[2 * kWarps];          // its units
-  __shared__ int last_flag;
+  __shared__ Rec rec_of[2 * kWarps];
+  __shared__ int rec_list[2 * kWarps], seg_at[2 * kWarps + 1], seg_count;
+  __shared__ int own[2];                         // this CTA's run
+  __shared__ int last_flag[2];
   __shared__ int abort_flag;
   volatile int* abort_v = &abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
+  const int cta = blockIdx.x;
 
   dev::pdl_trigger();
-  if (tid < kWarps * C::kStages) dev::mbar_init(dev::smem_u32(&full_bar[0][0] + tid), 1);
+  if (tid < kWarps * C::kStages) {
+    dev::mbar_init(dev::smem_u32(&full_bar[0][0] + tid), 1);
+    dev::fence_mbar_init();
+  }
   if (tid < 2 * kWarps) rec_seg[tid] = -1;
-  if (tid < kWarps * C::kStages) dev::fence_mbar_init();
   dev::pdl_wait();
   if (tid == 0) abort_flag = dev::status_set(p.status) ? 1 : 0;
 
-  // ---- units before every sequence
+  // ---- units before every sequence.  (The first sequences' values are asked for
+  // along with the number of sequences: any entry of the tables can be read.)
+  int row0 = 0, row1 = 0, len = 0;
+  auto fetch = [&](int b) {
+    if (b < p.max_seqs) {
+      row0 = p.cu[b];
+      row1 = p.cu[b + 1];
+      len = p.lens[b];
+    }
+  };
+  fetch(tid);
   const int n = p.info[0];
   const int rows_all = min(a.rows, p.info[1]);
-  auto seq_rows = [&](int b) { return max(0, min(p.cu[b + 1], rows_all) - p.cu[b]); };
-  int carry = 0;
+  int units = 0, segs = 0, most_pages = 0;
   for (int base = 0; base < n; base += kThreads) {
     const int b = base + tid;
-    int u = 0;
-    if (b < n) {
-      const int m = seq_rows(b);
-      if (m > 0 && p.G * m <= a.many)
-        u = ((p.G * m + C::kRows - 1) / C::kRows) * p.Hkv * ((p.lens[b] + kPage - 1) / kPage);
+    int u = 0, sg = 0, pages = 0;
+    if (base) fetch(b);
+    const int m = min(row1, rows_all) - row0;
+    if (b < n && m > 0 && p.G * m <= a.many) {
+      pages = (len + kPage - 1) / kPage;
+      sg = ((p.G * m + C::kRows - 1) / C::kRows) * p.Hkv;
+      u = sg * pages;
     }
-    int inc = u;
+    int iu = u, is = sg;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, inc, d);
-      if (lane >= d) inc += o;
+      const int ou = __shfl_up_sync(0xffffffffu, iu, d), os = __shfl_up_sync(0xffffffffu, is, d);
+      if (lane >= d) {
+        iu += ou;
+        is += os;
+      }
+    }
+    const int mp = __reduce_max_sync(0xffffffffu, pages);
+    __syncthreads();
+    if (lane == 31) {
+      scan_u[warp] = iu;
+      scan_s[warp] = is;
+      scan_p[warp] = mp;
     }
     __syncthreads();
-    if (lane == 31) scan[warp] = inc;
-    __syncthreads();
-    int before = carry;
+    int before_u = units, before_s = segs;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) before += scan[w];
-      carry += scan[w];
+      if (w < warp) {
+        before_u += scan_u[w];
+        before_s += scan_s[w];
+      }
+      units += scan_u[w];
+      segs += scan_s[w];
+      most_pages = max(most_pages, scan_p[w]);
     }
-    if (b < n) first_unit[b] = before + inc - u;
+    if (b < n) first_unit[b] = before_u + iu - u;
+    // the segment of this CTA, should each CTA take one
+    const int k = cta - (before_s + is - sg);
+    if (k >= 0 && k < sg) {
+      own[0] = before_u + iu - u + k * pages;
+      own[1] = own[0] + pages;
+    }
   }
-  if (tid == 0) first_unit[n] = carry;
+  if (tid == 0) first_unit[n] = units;
   __syncthreads();
-  const int units = carry;
   if (units == 0 || *abort_v) return;
-  // every warp gets a unit before another CTA is taken
-  const int ctas = min((int)gridDim.x, (units + kWarps - 1) / kWarps);
-  const int cta = blockIdx.x;
+  const bool whole_segs = segs <= (int)gridDim.x && most_pages <= 2 * kWarps;
+  // else every warp gets a unit before another CTA is taken
+  const int ctas = whole_segs ? segs : min((int)gridDim.x, (units + kWarps - 1) / kWarps);
   if (cta >= ctas) return;
-  const int c0 = (int)((long long)units * cta / ctas), c1 = (int)((long long)units * (cta + 1) / ctas);
+  const int c0 = whole_segs ? own[0] : (int)((long long)units * cta / ctas);
+  const int c1 = whole_segs ? own[1] : (int)((long long)units * (cta + 1) / ctas);
   const int w0 = c0 + (int)((long long)(c1 - c0) * warp / kWarps);
   const int w1 = c0 + (int)((long long)(c1 - c0) * (warp + 1) / kWarps);
 
@@ -200,24 +266,27 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const PagesDev p
       else hi = mid;
     }
     Place s;
+    const int row0 = p.cu[lo], row1 = p.cu[lo + 1], len = p.lens[lo];
     s.b = lo;
-    s.m = seq_rows(lo);
-    s.row0 = p.cu[lo];
-    const int len = p.lens[lo];
-    // the sequence's rows by the plan, some of which may lie past the buffers
-    s.P = len - (p.cu[lo + 1] - s.row0);
+    s.row0 = row0;
+    s.m = min(row1, rows_all) - row0;
+    // (the sequence's rows by the plan, some of which may lie past the buffers)
+    s.P = len - (row1 - row0);
     s.pages = (len + kPage - 1) / kPage;
-    const int r = u - first_unit[lo];
-    s.page = r % s.pages;
-    s.kv = (r / s.pages) % p.Hkv;
-    s.tile = r / s.pages / p.Hkv;
+    const uint32_t r = u - first_unit[lo], seg = r / (uint32_t)s.pages;
+    s.page = r - seg * s.pages;
+    s.tile = dev::div_by(seg, p.mul_hkv);
+    s.kv = seg - s.tile * p.Hkv;
     return s;
   };
+  // row r of a tile: its token in the sequence and head in the group
+  auto token_of = [&](int rho) { return dev::div_by(rho, p.mul_g); };
   // output row (token, query head) of row r of a tile, -1 past the last
-  auto out_row = [&](const Place& s, int r) -> long long {
-    const int rho = s.tile * C::kRows + r;
-    if (rho >= p.G * s.m) return -1;
-    return (long long)(s.row0 + rho / p.G) * p.Hq + s.kv * p.G + rho % p.G;
+  auto out_row = [&](int tile, int kv, int row0, int m, int r) -> long long {
+    const int rho = tile * C::kRows + r;
+    if (rho >= p.G * m) return -1;
+    const int tok = token_of(rho);
+    return (long long)(row0 + tok) * p.Hq + kv * p.G + rho - tok * p.G;
   };
   auto store4 = [&](long long row, int d, float x, float y, float z, float w) {
     uint2 v;
@@ -228,15 +297,17 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const PagesDev p
     }
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * D + d) = v;
   };
-  // partial results: [gridDim.x][2 kWarps] of the warps, then [gridDim.x][2] of the CTAs
+  // partial results: in the work area [gridDim.x][kWarps] of the warps, then
+  // [gridDim.x][2] of the CTAs
+  auto global_slot = [&](long long at) { return Slot{a.part + at * C::kSlot, a.ml + at * C::kRows}; };
   auto warp_slot = [&](int i) {
-    const long long at = (long long)cta * 2 * kWarps + i;
-    return Slot{a.part + at * C::kSlot, a.ml + at * kPageAttnRows};
+    if (i & 1) {
+      float* o = reinterpret_cast<float*>(smem + (i >> 1) * C::kRing);
+      return Slot{o, reinterpret_cast<float2*>(o + C::kSlot)};
+    }
+    return global_slot((long long)cta * kWarps + (i >> 1));
   };
-  auto cta_slot = [&](int c, int i) {
-    const long long at = (long long)gridDim.x * 2 * kWarps + (long long)c * 2 + i;
-    return Slot{a.part + at * C::kSlot, a.ml + at * kPageAttnRows};
-  };
+  auto cta_slot = [&](int c, int i) { return global_slot((long long)gridDim.x * kWarps + (long long)c * 2 + i); };
 
   // ---- this warp's run
   bool ok = true;
@@ -244,118 +315,72 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const PagesDev p
     const uint32_t ring = dev::smem_u32(smem) + warp * C::kRing;
     const uint32_t bars = dev::smem_u32(&full_bar[warp][0]);
     const uint8_t* layer = p.pool + p.layer_off;
-    // addresses of the next 32 units to fetch, one per lane
+    // offsets of the next 32 units to fetch, one per lane
     long long src = 0;
-    int queued = w0;   // first unit past the queue
-    int issued = w0;
+    int queued = 0;                       // first unit past the queue, from w0
+    const int halves = 2 * (w1 - w0);
+    int issued = 0, stage_in = 0;         // halves requested, and the stage of the next
     auto issue = [&]() {
-      if (issued == queued) {
-        const int u = queued + lane;
+      if (issued >> 1 == queued) {
+        const int u = w0 + queued + lane;
         if (u < w1) {
           const Place s = place_of(u);
-          src = ((long long)p.table[(long long)s.b * p.width + s.page] * p.Hkv + s.kv) * C::kChunk;
+          src = ((long long)p.table[(long long)s.b * p.width + s.page] * p.Hkv + s.kv) * K::kBytes;
         }
         queued += 32;
       }
-      const long long off = __shfl_sync(0xffffffffu, src, (issued - w0) & 31);
+      const long long off = __shfl_sync(0xffffffffu, src, (issued >> 1) & 31) + (issued & 1) * C::kHalf;
       if (lane == 0) {
-        const int st = (issued - w0) % C::kStages;
-        dev::mbar_arrive_expect_tx(bars + 8 * st, C::kChunk);
-        bulk_load(ring + st * C::kChunk, layer + off, C::kChunk, bars + 8 * st);
+        dev::mbar_arrive_expect_tx(bars + 8 * stage_in, C::kHalf);
+        bulk_load(ring + stage_in * C::kHalf, layer + off, C::kHalf, bars + 8 * stage_in);
       }
       ++issued;
+      if (++stage_in == C::kStages) stage_in = 0;
     };
-    while (issued < w1 && issued - w0 < C::kStages) issue();
+    while (issued < halves && issued < C::kStages) issue();
+    // the next half to use: its stage and the parity of that stage's phase
+    int stage = 0;
+    uint32_t parity = 0;
+    auto arrived = [&]() {
+      const bool got = dev::mbar_wait(bars + 8 * stage, parity, p.status) && !*abort_v;
+      return __all_sync(0xffffffffu, got);
+    };
+    auto used = [&]() {
+      __syncwarp();
+      if (++stage == C::kStages) {
+        stage = 0;
+        parity ^= 1;
+      }
+      if (issued < halves) issue();
+    };
 
     Place s = place_of(w0);
     uint32_t qb[NT][kG][4];       // dims 32 j + 8 t + 0..7 of row 8 n + g, the B side of the K codes
-    float bias[NT][kG][2];        // -8 sum of q over the group, rows 8 n + 2 t, + 1 (units 2^-20)
     float f[NT][2];               // sums -> scores in log2 units
     int see[NT][2];               // last key these rows see
     float m_run[NT][2], l_run[NT][2];
     float o[NT][2 * kG][4];       // O^T tiles 2 j, 2 j + 1: rows g, g + 8 are dims 32 j + 4 g + 0, 1 and + 2, 3
     bool fresh = true;
-    int part_no = 0;              // partial results of this warp so far
+    const uint32_t k1024 = held(0x64006400u), k64 = held(0x54005400u);
 
-    for (int u = w0; u < w1 && ok; ++u) {
-      if (fresh) {
-        fresh = false;
+    // row 8 nn + g of the tile: this lane's dims of it
+    auto load_q = [&](const Place& at, int nn, uint4* raw) {
+      const int rho = at.tile * C::kRows + 8 * nn + g;
+      const int tok = token_of(rho);
+      const uint16_t* src_q = static_cast<const uint16_t*>(a.q) + (long long)(at.row0 + tok) * a.qs +
+                              (at.kv * p.G + rho - tok * p.G) * D + 8 * t;
 #pragma unroll
-        for (int nn = 0; nn < NT; ++nn) {
-          // row 8 nn + g of the tile: this lane's dims of it
-          const int rho = s.tile * C::kRows + 8 * nn + g;
-          uint4 raw[kG];
-          const bool live = rho < p.G * s.m;
-#pragma unroll
-          for (int j = 0; j < kG; ++j) {
-            raw[j] = make_uint4(0, 0, 0, 0);
-            if (live)
-              raw[j] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
-                                                       (long long)(s.row0 + rho / p.G) * a.qs +
-                                                       (s.kv * p.G + rho % p.G) * D + 32 * j + 8 * t);
-          }
-          float top = 0.f;
-#pragma unroll
-          for (int j = 0; j < kG; ++j) {
-            const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 x = dev::act2<F16>(w[i]);
-              top = fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y)));
-            }
-          }
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          // 2^e with |q| 2^e in [2^10, 2^11); e from the exponent field, kept
-          // where both 2^e and its inverse are normal numbers.  The nibble in
-          // bits 0-3 counts 2^-24, so its q carries another factor of 16.
-          int e = 137 - (int)(__float_as_uint(top) >> 23);
-          e = top > 0.f ? max(-100, min(100, e)) : 0;
-          const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-          float neg[kG];
-#pragma unroll
-          for (int j = 0; j < kG; ++j) {
-            const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
-            float sum = 0.f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 x = dev::act2<F16>(w[i]);
-              const __half2 h = __floats2half2_rn(x.x * up, x.y * up);
-              const float2 hf = __half22float2(h);
-              sum += hf.x + hf.y;
-              qb[nn][j][i] = i & 1 ? *reinterpret_cast<const uint32_t*>(&h)
-                                   : dev::pack_act<true>(hf.x * 16.f, hf.y * 16.f);
-            }
-            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            neg[j] = sum * (-8.f / 1048576.f);
-          }
-          const float back = __uint_as_float((uint32_t)(127 - e) << 23) * 1048576.f * a.scale_log2;
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int from = (2 * t + c) * 4;
-#pragma unroll
-            for (int j = 0; j < kG; ++j) bias[nn][j][c] = __shfl_sync(0xffffffffu, neg[j], from);
-            f[nn][c] = __shfl_sync(0xffffffffu, back, from);
-            const int rc = s.tile * C::kRows + 8 * nn + 2 * t + c;
-            see[nn][c] = rc < p.G * s.m ? s.P + rc / p.G : -1;
-            m_run[nn][c] = -INFINITY;
-            l_run[nn][c] = 0.f;
-          }
-#pragma unroll
-          for (int i = 0; i < 2 * kG; ++i)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) o[nn][i][c] = 0.f;
-        }
+      for (int j = 0; j < kG; ++j) {
+        raw[j] = make_uint4(0, 0, 0, 0);
+        if (rho < p.G * at.m) raw[j] = *reinterpret_cast<const uint4*>(src_q + 32 * j);
       }
-      const int st = (u - w0) % C::kStages;
-      ok = dev::mbar_wait(bars + 8 * st, ((u - w0) / C::kStages) & 1, p.status);
-      ok = __all_sync(0xffffffffu, ok && !*abort_v);
-      if (!ok) break;
-      const uint32_t page = ring + st * C::kChunk;
+    };
+    // one page; kMasked: some row of the tile does not see all of it
+    auto page_step = [&](auto masked) {
+      constexpr bool kMasked = decltype(masked)::value;
+      if (!arrived()) return false;
+      uint32_t page = ring + stage * C::kHalf;
       const int key_base = s.page * kPage;
-      // every row of the tile sees the whole page
-      const bool whole = key_base + kPage <= s.P + 1;
 
       // ---- scores of 64 keys
       float sc[4][NT][4];
@@ -374,14 +399,12 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const PagesDev p
 #pragma unroll
         for (int j = 0; j < kG; ++j) {
           const uint32_t x0 = w0k[j], x1 = w1k[j], y0 = x0 >> 8, y1 = x1 >> 8;
-          const uint32_t a0 = x0 & 0x000f000fu, a1 = x1 & 0x000f000fu, a2 = x0 & 0x00f000f0u,
-                         a3 = x1 & 0x00f000f0u;
-          const uint32_t b0 = y0 & 0x000f000fu, b1 = y1 & 0x000f000fu, b2 = y0 & 0x00f000f0u,
-                         b3 = y1 & 0x00f000f0u;
+          const uint32_t a0 = centred_lo(x0, k1024), a1 = centred_lo(x1, k1024), a2 = centred_hi(x0, k64), a3 = centred_hi(x1, k64);
+          const uint32_t b0 = centred_lo(y0, k1024), b1 = centred_lo(y1, k1024), b2 = centred_hi(y0, k64), b3 = centred_hi(y1, k64);
 #pragma unroll
           for (int nn = 0; nn < NT; ++nn) {
-            float acc[4] = {bias[nn][j][0], bias[nn][j][1], bias[nn][j][0], bias[nn][j][1]};
-            mma(acc, a0, a1, a2, a3, qb[nn][j][0], qb[nn][j][1]);
+            float acc[4];
+            mma_first(acc, a0, a1, a2, a3, qb[nn][j][0], qb[nn][j][1]);
             mma(acc, b0, b1, b2, b3, qb[nn][j][2], qb[nn][j][3]);
             sc[mt][nn][0] = fmaf(acc[0], s0[j], sc[mt][nn][0]);
             sc[mt][nn][1] = fmaf(acc[1], s0[j], sc[mt][nn][1]);
@@ -390,24 +413,26 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const PagesDev p
           }
         }
       }
+      used();
       // ---- running maximum and weights
       uint32_t pw[4][NT][2];
 #pragma unroll
       for (int nn = 0; nn < NT; ++nn) {
+        // (the factors f are positive: the maximum is taken before them)
         float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            float x = sc[mt][nn][c] * f[nn][c & 1];
-            if (!whole && key_base + 16 * mt + g + 8 * (c >> 1) > see[nn][c & 1]) x = -INFINITY;
-            sc[mt][nn][c] = x;
-            mx[c & 1] = fmaxf(mx[c & 1], x);
+            if (kMasked && key_base + 16 * mt + g + 8 * (c >> 1) > see[nn][c & 1]) sc[mt][nn][c] = -INFINITY;
+            mx[c & 1] = fmaxf(mx[c & 1], sc[mt][nn][c]);
           }
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+        for (int c = 0; c < 2; ++c) {
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], d));
+          mx[c] *= f[nn][c];
+        }
         const bool moved = mx[0] > m_run[nn][0] || mx[1] > m_run[nn][1];
         if (__any_sync(0xffffffffu, moved)) {
           float corr[2];
@@ -432,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const PagesDev p
           float e[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            e[c] = ex2_approx(sc[mt][nn][c] - sub[c & 1]);
+            e[c] = ex2_approx(fmaf(sc[mt][nn][c], f[nn][c & 1], -sub[c & 1]));
             l_run[nn][c & 1] += e[c];
           }
           pw[mt][nn][0] = transpose8x8(dev::pack_act<true>(e[0], e[1]));
@@ -440,6 +465,8 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const PagesDev p
         }
       }
       // ---- weighted values
+      if (!arrived()) return false;
+      page = ring + stage * C::kHalf - C::kHalf;   // (the V half's offsets count from the page)
 #pragma unroll
       for (int mt = 0; mt < 4; ++mt) {
         uint32_t v0[kG], v1[kG], s0[kG], s1[kG];
@@ -450,12 +477,12 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const PagesDev p
 #pragma unroll
         for (int j = 0; j < kG; ++j) {
           const uint32_t x0 = v0[j], x1 = v1[j], y0 = x0 >> 8, y1 = x1 >> 8;
-          const uint32_t e0 = centred_lo(x0), e1 = centred_hi(x0), e2 = centred_lo(x1), e3 = centred_hi(x1);
-          const uint32_t f0 = centred_lo(y0), f1 = centred_hi(y0), f2 = centred_lo(y1), f3 = centred_hi(y1);
+          const uint32_t e0 = centred_lo(x0, k1024), e1 = centred_hi(x0, k64), e2 = centred_lo(x1, k1024), e3 = centred_hi(x1, k64);
+          const uint32_t f0 = centred_lo(y0, k1024), f1 = centred_hi(y0, k64), f2 = centred_lo(y1, k1024), f3 = centred_hi(y1, k64);
 #pragma unroll
           for (int nn = 0; nn < NT; ++nn) {
             uint32_t b0 = hmul2(pw[mt][nn][0], s0[j]), b1 = hmul2(pw[mt][nn][1], s1[j]);
-            if (!whole) {
+            if (kMasked) {
               // a weight of zero takes nothing, whatever stands in a place
               // behind the row's last key (an unwritten scale, a NaN)
               const uint32_t p0 = pw[mt][nn][0], p1 = pw[mt][nn][1];
@@ -467,15 +494,69 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const PagesDev p
           }
         }
       }
-      __syncwarp();
-      if (issued < w1) issue();
+      used();
+      return true;
+    };
+
+    for (int u = w0; u < w1 && ok; ++u) {
+      if (fresh) {
+        fresh = false;
+#pragma unroll
+        for (int nn = 0; nn < NT; ++nn) {
+          uint4 raw[kG];
+          load_q(s, nn, raw);
+          float top = 0.f;
+#pragma unroll
+          for (int j = 0; j < kG; ++j) {
+            const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 x = dev::act2<F16>(w[i]);
+              top = fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y)));
+            }
+          }
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          // 2^e with |q| 2^e in [2^10, 2^11); e from the exponent field, kept
+          // where both 2^e and its inverse are normal numbers
+          int e = 137 - (int)(__float_as_uint(top) >> 23);
+          e = top > 0.f ? max(-100, min(100, e)) : 0;
+          const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+          for (int j = 0; j < kG; ++j) {
+            const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 x = dev::act2<F16>(w[i]);
+              qb[nn][j][i] = dev::pack_act<true>(x.x * up, x.y * up);
+            }
+          }
+          const float back = __uint_as_float((uint32_t)(127 - e) << 23) * a.scale_log2;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int from = (2 * t + c) * 4;
+            f[nn][c] = __shfl_sync(0xffffffffu, back, from);
+            const int rc = s.tile * C::kRows + 8 * nn + 2 * t + c;
+            see[nn][c] = rc < p.G * s.m ? s.P + token_of(rc) : -1;
+            m_run[nn][c] = -INFINITY;
+            l_run[nn][c] = 0.f;
+          }
+#pragma unroll
+          for (int i = 0; i < 2 * kG; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) o[nn][i][c] = 0.f;
+        }
+      }
+      // every row of the tile sees the whole page
+      ok = (s.page + 1) * kPage <= s.P + 1 ? page_step(std::false_type()) : page_step(std::true_type());
+      if (!ok) break;
 
       // ---- the end of the segment or of the run
       const bool seg_end = s.page + 1 == s.pages;
       if (seg_end || u + 1 == w1) {
         const int seg0 = u - s.page;
         const bool alone = seg_end && seg0 >= w0;
-        const int rec = 2 * warp + part_no;
+        const int rec = 2 * warp + (u + 1 == w1 ? 1 : 0);
         const Slot out = warp_slot(rec);
 #pragma unroll
         for (int nn = 0; nn < NT; ++nn) {
@@ -488,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const PagesDev p
             for (int d = 4; d < 32; d <<= 1) l[c] += __shfl_xor_sync(0xffffffffu, l[c], d);
             // (a NaN sum stays one)
             inv[c] = alone ? (l[c] == 0.f ? 0.f : 1.f / l[c]) : 1.f;
-            row[c] = alone ? out_row(s, 8 * nn + 2 * t + c) : 0;
+            row[c] = alone ? out_row(s.tile, s.kv, s.row0, s.m, 8 * nn + 2 * t + c) : 0;
           }
 #pragma unroll
           for (int j = 0; j < kG; ++j) {
@@ -512,9 +593,8 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const PagesDev p
         if (!alone) {
           if (lane == 0) {
             rec_seg[rec] = seg0;
-            rec_seg_n[rec] = s.pages;
+            rec_of[rec] = {s.pages, s.tile, s.kv, s.row0, s.m};
           }
-          ++part_no;
         }
         fresh = true;
         if (u + 1 < w1) s = place_of(u + 1);
@@ -526,102 +606,137 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const PagesDev p
       // a wait gave up: the copies in flight still land in this CTA's memory
       *abort_v = 1;
       const unsigned long long deadline = dev::globaltimer_ns() + kWaitLimitNs;
-      for (int st = 0; st < C::kStages && st < issued - w0; ++st) {
-        const int last = ((issued - 1 - w0 - st) / C::kStages) * C::kStages + st;
-        dev::mbar_wait_until(bars + 8 * st, (uint32_t)(last / C::kStages) & 1, deadline);
+      for (int st = 0; st < C::kStages && st < issued; ++st) {
+        const int last = (issued - 1 - st) / C::kStages;
+        dev::mbar_wait_until(bars + 8 * st, (uint32_t)last & 1, deadline);
       }
     }
   }
-  __threadfence_block();
   __syncthreads();
   if (*abort_v) return;
 
   // ---- merge the warps' parts, then the CTAs': `count` parts given by
-  // slot(i), element (row, 4 dims) after element
-  auto merge = [&](int count, auto slot, auto done) {
-    for (int e = tid; e < C::kRows * (D / 4); e += kThreads) {
+  // slot(i); element (row r, dims d .. d + 3)
+  auto merge = [&](int r, int d, int count, auto slot, auto load2, auto load4, auto done) {
+    float m = -INFINITY;
+#pragma unroll 8
+    for (int i = 0; i < count; ++i) m = fmaxf(m, load2(slot(i).ml + r).x);
+    float l = 0.f;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int i = 0; i < count; ++i) {
+      const Slot s = slot(i);
+      const float2 ml = load2(s.ml + r);
+      const float4 y = load4(reinterpret_cast<const float4*>(s.o + r * D + d));
+      // a part in which the row saw nothing (m = -inf, or -inf throughout
+      // because its scores are NaN) counts its sum and its values as they are
+      const float w = ml.x == -INFINITY ? 1.f : ex2_approx(ml.x - m);
+      l = fmaf(w, ml.y, l);
+      x.x = fmaf(w, y.x, x.x);
+      x.y = fmaf(w, y.y, x.y);
+      x.z = fmaf(w, y.z, x.z);
+      x.w = fmaf(w, y.w, x.w);
+    }
+    done(x, m, l);
+  };
+  auto finish = [&](const Rec& s, int r, int d, float4 x, float l) {
+    const long long row = out_row(s.tile, s.kv, s.row0, s.m, r);
+    if (row < 0) return;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    store4(row, d, x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+  };
+  auto owner = [&](int u) { return (int)(((long long)(u + 1) * ctas - 1) / units); };
+  // the filled records in order, and the first record of each segment
+  static_assert(2 * kWarps <= 32, "one record per lane");
+  if (warp == 0) {
+    const bool has = lane < 2 * kWarps && rec_seg[lane] >= 0;
+    uint32_t mask = __ballot_sync(0xffffffffu, has);
+    const uint32_t below = (1u << lane) - 1;
+    if (has) rec_list[__popc(mask & below)] = lane;
+    const int records = __popc(mask);
+    __syncwarp();
+    const bool starts =
+        lane < records && (lane == 0 || rec_seg[rec_list[lane]] != rec_seg[rec_list[lane - 1]]);
+    mask = __ballot_sync(0xffffffffu, starts);
+    if (starts) seg_at[__popc(mask & below)] = lane;
+    if (lane == 0) {
+      seg_count = __popc(mask);
+      seg_at[__popc(mask)] = records;
+    }
+  }
+  __syncthreads();
+  constexpr int kElems = C::kRows * (D / 4);
+  const int n_seg = seg_count;
+  for (int i = tid; i < n_seg * kElems; i += kThreads) {
+    const int k = i / kElems, r = i % kElems / (D / 4), d = 4 * (i % (D / 4));
+    const int first = seg_at[k], seg0 = rec_seg[rec_list[first]];
+    const Rec s = rec_of[rec_list[first]];
+    const bool local = seg0 >= c0 && seg0 + s.pages <= c1;
+    merge(
+        r, d, seg_at[k + 1] - first, [&](int j) { return warp_slot(rec_list[first + j]); },
+        [](const float2* x) { return *x; }, [](const float4* x) { return *x; },
+        [&](float4 x, float m, float l) {
+          if (local) {
+            finish(s, r, d, x, l);
+          } else {
+            // the CTA that holds the segment's first unit leaves its part in its
+            // second slot, the others in their first
+            const Slot out = cta_slot(cta, seg0 >= c0 ? 1 : 0);
+            *reinterpret_cast<float4*>(out.o + r * D + d) = x;
+            if (d == 0) out.ml[r] = make_float2(m, l);
+          }
+        });
+  }
+  if (n_seg == 0) return;
+  // segments shared with the CTAs before (0) and after (1)
+  int shared_seg[2] = {-1, -1};
+  Rec shared_rec[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int at = rec_list[seg_at[i == 0 ? 0 : n_seg - 1]];
+    const int seg0 = rec_seg[at];
+    shared_rec[i] = rec_of[at];
+    if (i == 0 ? seg0 < c0 : (seg0 >= c0 && seg0 + shared_rec[i].pages > c1)) shared_seg[i] = seg0;
+  }
+  if (shared_seg[0] < 0 && shared_seg[1] < 0) return;
+  __syncthreads();   // (the add below releases what the CTA wrote)
+  if (tid % 32 == 0 && tid / 32 < 2) {
+    const int i = tid / 32, seg0 = shared_seg[i];
+    last_flag[i] = 0;
+    if (seg0 >= 0) {
+      const int ca = owner(seg0), cb = owner(seg0 + shared_rec[i].pages - 1);
+      if (dev::atom_add_acq_rel(a.counters + ca, 1) == cb - ca) {
+        a.counters[ca] = 0;
+        last_flag[i] = 1;
+      }
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (!last_flag[i]) continue;
+    const Rec s = shared_rec[i];
+    const int ca = owner(shared_seg[i]), cb = owner(shared_seg[i] + s.pages - 1);
+    for (int e = tid; e < kElems; e += kThreads) {
       const int r = e / (D / 4), d = 4 * (e % (D / 4));
-      float m = -INFINITY;
-      for (int i = 0; i < count; ++i) m = fmaxf(m, __ldcg(&slot(i).ml[r]).x);
-      float l = 0.f;
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int i = 0; i < count; ++i) {
-        const Slot s = slot(i);
-        const float2 ml = __ldcg(s.ml + r);
-        const float4 y = __ldcg(reinterpret_cast<const float4*>(s.o + r * D + d));
-        // a part in which the row saw nothing (m = -inf, or -inf throughout
-        // because its scores are NaN) counts its sum and its values as they are
-        const float w = ml.x == -INFINITY ? 1.f : exp2f(ml.x - m);
-        l = fmaf(w, ml.y, l);
-        x.x = fmaf(w, y.x, x.x);
-        x.y = fmaf(w, y.y, x.y);
-        x.z = fmaf(w, y.z, x.z);
-        x.w = fmaf(w, y.w, x.w);
-      }
-      done(r, d, x, m, l);
+      merge(
+          r, d, cb - ca + 1, [&](int k) { return cta_slot(ca + k, k == 0 ? 1 : 0); },
+          [](const float2* x) { return __ldcg(x); }, [](const float4* x) { return __ldcg(x); },
+          [&](float4 x, float m, float l) { finish(s, r, d, x, l); });
     }
-  };
-  auto finish = [&](const Place& s) {
-    return [&, s](int r, int d, float4 x, float m, float l) {
-      const long long row = out_row(s, r);
-      if (row < 0) return;
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      store4(row, d, x.x * inv, x.y * inv, x.z * inv, x.w * inv);
-    };
-  };
-  for (int i = 0; i < 2 * kWarps;) {
-    const int seg0 = rec_seg[i];
-    if (seg0 < 0) {
-      ++i;
-      continue;
-    }
-    // the records of one segment, in order; empty ones between them are skipped
-    const int first = i, seg_n = rec_seg_n[i];
-    int count = 0;
-    uint32_t used = 0;
-    for (; i < 2 * kWarps && (rec_seg[i] < 0 || rec_seg[i] == seg0); ++i)
-      if (rec_seg[i] == seg0) {
-        used |= 1u << (i - first);
-        ++count;
-      }
-    const Place s = place_of(seg0);
-    auto mine = [&](int k) { return warp_slot(first + (int)__fns(used, 0, k + 1)); };
-    if (seg0 >= c0 && seg0 + seg_n <= c1) {
-      merge(count, mine, finish(s));
-      continue;
-    }
-    // the CTAs of the segment: the one that holds its first unit leaves its
-    // part in its second slot, the others in their first
-    auto owner = [&](int u) { return (int)(((long long)(u + 1) * ctas - 1) / units); };
-    const int ca = owner(seg0), cb = owner(seg0 + seg_n - 1);
-    const Slot out = cta_slot(cta, cta == ca ? 1 : 0);
-    merge(count, mine, [&](int r, int d, float4 x, float m, float l) {
-      *reinterpret_cast<float4*>(out.o + r * D + d) = x;
-      if (d == 0) out.ml[r] = make_float2(m, l);
-    });
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) {
-      last_flag = dev::atom_add_acq_rel(a.counters + ca, 1) == cb - ca;
-      if (last_flag) a.counters[ca] = 0;
-    }
-    __syncthreads();
-    if (last_flag) {
-      __threadfence();
-      merge(cb - ca + 1, [&](int k) { return cta_slot(ca + k, k == 0 ? 1 : 0); }, finish(s));
-    }
-    __syncthreads();
   }
 }
 
 template <int D, int NT, bool F16>
 cudaError_t setup_one() {
+  using C = Cfg<D, NT>;
   return cudaFuncSetAttribute(page_attn_kernel<D, NT, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              kWarps * Cfg<D, NT>::kRing);
+                              C::kWarps * C::kRing);
 }
 template <int D, int NT, bool F16>
 cudaError_t launch_one(const PagesDev& p, const PageAttend& a, int ctas, cudaStream_t st) {
-  return launch_k(page_attn_kernel<D, NT, F16>, dim3(ctas), kThreads, (size_t)kWarps * Cfg<D, NT>::kRing, st, p, a);
+  using C = Cfg<D, NT>;
+  return launch_k(page_attn_kernel<D, NT, F16>, dim3(ctas), C::kThreads, (size_t)C::kWarps * C::kRing, st, p, a);
 }
 
 }  // namespace

@@ -67,8 +67,8 @@ Layout layout(const kvr_pages_config* c) {
   L.row_slot = take((size_t)c->max_rows * 4);
   L.table = take((size_t)c->max_seqs * L.width * 4);
   L.rope = take((size_t)c->max_len * (c->head_dim / 2) * sizeof(float2));
-  L.ml = take((size_t)kPageAttnSlots * kPageAttnRows * sizeof(float2));
-  L.part = take((size_t)kPageAttnSlots * kPageAttnRows * c->head_dim * sizeof(float));
+  L.ml = take((size_t)kPageAttnPartRows * sizeof(float2));
+  L.part = take((size_t)kPageAttnPartRows * c->head_dim * sizeof(float));
   L.total = at;
   return L;
 }
@@ -155,6 +155,10 @@ int kvr_pages_create(const kvr_pages_config* cfg, void* pool, size_t pool_bytes,
   d.Hkv = cfg->n_kv_heads;
   d.G = d.Hq / d.Hkv;
   d.d = cfg->head_dim;
+  d.max_seqs = cfg->max_seqs;
+  auto mul = [](int x) { return x == 1 ? 0u : (uint32_t)(((1ull << 32) + x - 1) / x); };
+  d.mul_hkv = mul(d.Hkv);
+  d.mul_g = mul(d.G);
   d.f16 = cfg->act == KVR_ACT_F16;
   c->layer_bytes = (size_t)cfg->n_pages * cfg->n_kv_heads * page_chunk_bytes(cfg->head_dim);
   memset(&c->attend, 0, sizeof c->attend);

@@ -22,16 +22,18 @@ constexpr int kPageMaxSeqs = 2048;
 //            store with another token.)
 //   K scales [key][j] fp16.
 //   V scales [key / 16][t][(key / 8) % 2][j] pairs of fp16 (keys 2t, 2t + 1).
-// A code is held with 8 added.
+// A code is held with 8 added.  K codes and scales come first, so that K and V
+// can be fetched apart, each as one run of kHalf bytes.
 template <int D>
 struct Chunk {
   static constexpr int kGroups = D / kPageGroup;
   static constexpr int kCodes = kPage * D / 2;
   static constexpr int kScales = kPage * kGroups * 2;
-  static constexpr int kV = kCodes;
-  static constexpr int kKs = 2 * kCodes;
-  static constexpr int kVs = 2 * kCodes + kScales;
-  static constexpr int kBytes = 2 * (kCodes + kScales);
+  static constexpr int kKs = kCodes;
+  static constexpr int kHalf = kCodes + kScales;
+  static constexpr int kV = kHalf;
+  static constexpr int kVs = kHalf + kCodes;
+  static constexpr int kBytes = 2 * kHalf;
 
   static __host__ __device__ __forceinline__ int k_word(int key, int t, int j) {
     return ((key * 4 + t) * kGroups + j) * 4;
@@ -63,8 +65,9 @@ struct PagesDev {
   const float2* rope;    // [max_len][d / 2] (cos, sin)
   int* status;           // a wait that gave up
   int* refused;          // the first refused plan's error code
-  int n_pages, width, max_len, max_rows;
+  int n_pages, width, max_len, max_rows, max_seqs;
   int Hq, Hkv, G, d;
+  uint32_t mul_hkv, mul_g;   // for dev::div_by
   int f16;               // activations are fp16 (else bf16)
 };
 
@@ -94,11 +97,10 @@ struct PageAttend {
   int* counters;     // arrivals, zero between launches
 };
 
-constexpr int kPageAttnWarps = 8;
-constexpr int kPageAttnRows = 16;      // rows of a tile: two 8-column tensor-core tiles at most
 constexpr int kPageAttnMaxCtas = 160;
-// partial results of the split kernel: two per warp and two per CTA
-constexpr int kPageAttnSlots = kPageAttnMaxCtas * (2 * kPageAttnWarps + 2);
+// partial results of the split kernel, in rows: two tiles per warp (16 warps
+// with tiles of 8 rows, 8 warps with 16 rows) and two per CTA
+constexpr int kPageAttnPartRows = kPageAttnMaxCtas * (2 * 128 + 2 * 16);
 
 cudaError_t page_plan_setup();
 // every page free, the first ones on top
@@ -116,6 +118,9 @@ cudaError_t launch_page_attn(const PagesDev& p, const PageAttend& a, int nt, int
 #ifdef __CUDACC__
 namespace kvr {
 namespace dev {
+
+// n / d for n < 2^32 / d, with mul = ceil(2^32 / d) (0 stands for d = 1)
+__device__ __forceinline__ int div_by(int n, uint32_t mul) { return mul ? (int)__umulhi((uint32_t)n, mul) : n; }
 
 // two activations of either 16-bit type
 template <bool F16>

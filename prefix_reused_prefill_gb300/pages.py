@@ -99,7 +99,8 @@ class PagedKv:
             raise KvrError(rc, self.lib.kvr_pages_error(self.ctx).decode())
 
     def _stream(self, stream):
-        return (stream if stream is not None else torch.cuda.current_stream(self.device)).cuda_stream
+        # (the raw handle: a Stream object costs 2 us)
+        return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(self._index)
 
     def _rows_arg(self, name: str, x: torch.Tensor, heads: int) -> int:
         """Row stride of x [rows][heads][head_dim], the heads of a row contiguous."""

@@ -10,11 +10,9 @@ Bounds, per element (u = half a step of the output type, 2^-9 relative for bf16'
   type: s/2 + 7 s 2^-11 + 2 eps/2 |y|, plus the 2^-20 of y.
 * attend, on known K and V: the weights p and p s are fp16 (eps/2 = 2^-11 each; below 2^-14 half of 2^-24
   absolutely, where the largest p is 4), the scores are fp32 sums whose error moves a weight by less than
-  2^-11 for the scores here (the code products of one group of dims are cut at 2^-13 of max|q| s, which with
-  max|q| <= 9, s <= 1.3, scale 1/8 and four groups is 2^-10.5 at the very most, for rows of which it is the largest
-  element that is cut; the fp32 sums of |scale q k| <= 60 add 2^-20 of them), the output is rounded once.  The values
-  are summed in n / 16 + 2 fp32 additions that may each drop 2^-22 of the running sum, itself at most max|v|:
-  (3 * 2^-11) sum w|v| + n (2^-27 max|v| + 2^-24) + (n / 16 + 2) 2^-22 max|v| + eps/2 |o|.
+  2^-13 for the scores here (|scale q k| <= 90, 2^-20 relative), the output is rounded once.  The values are summed
+  in n / 16 + 2 fp32 additions that may each drop 2^-22 of the running sum, itself at most max|v|:
+  (2 * 2^-11 + 2^-13) sum w|v| + n (2^-27 max|v| + 2^-24) + (n / 16 + 2) 2^-22 max|v| + eps/2 |o|.
 """
 import numpy as np
 import pytest
@@ -225,7 +223,8 @@ def test_append_in_place():
 # --------------------------------------------------------------------------- attend
 def bound(n, mag, v, ref, u):
     top = np.abs(v).max()
-    return 3 * 2.0 ** -11 * mag + n * (2.0 ** -27 * top + 2.0 ** -24) + (n / 16 + 2) * 2.0 ** -22 * top + u * np.abs(ref)
+    return ((2 * 2.0 ** -11 + 2.0 ** -13) * mag + n * (2.0 ** -27 * top + 2.0 ** -24)
+            + (n / 16 + 2) * 2.0 ** -22 * top + u * np.abs(ref))
 
 
 class World:
