@@ -1,7 +1,6 @@
 // C ABI of the paged 4-bit cache (include/kvr.h): checks, the work area's
 // layout, and which kernels a call launches.
 #include <algorithm>
-#include <climits>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -16,6 +15,7 @@ struct kvr_pages {
   kvr_pages_config cfg;
   PagesDev dev;
   PageAttend attend;      // the work buffers of the attention
+  PageAttendTc attend_tc;
   int device = 0;
   int ctas = 0;           // one per SM
   int rows = 0, max_add = 0, n_seq = 0;   // of the last plan
@@ -26,6 +26,10 @@ struct kvr_pages {
 namespace {
 
 constexpr size_t kAlign = 256;
+// rows of a sequence and KV head (rows * group) up to which the split kernel
+// takes the sequence
+constexpr int kPageMany = 64;
+constexpr int kPageMinUnits = 3;
 inline size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 bool valid(const kvr_pages_config* c) {
@@ -42,7 +46,7 @@ bool valid(const kvr_pages_config* c) {
 }
 
 struct Layout {
-  size_t status, info, count, counters, lens, cu, free_list, row_seq, row_pos, row_slot, table, rope, ml, part, total;
+  size_t status, info, count, counters, lens, cu, free_list, row_seq, row_pos, row_slot, table, rope, ml, part, ml_tc, part_tc, total;
   int width;
 };
 Layout layout(const kvr_pages_config* c) {
@@ -57,7 +61,7 @@ Layout layout(const kvr_pages_config* c) {
   // zeroed by kvr_pages_create, in one piece: status .. cu
   L.status = take(8);
   L.info = take(8);
-  L.counters = take(kPageAttnMaxCtas * 4);
+  L.counters = take(2 * kPageAttnMaxCtas * 4);
   L.lens = take((size_t)c->max_seqs * 4);
   L.cu = take((size_t)(c->max_seqs + 1) * 4);
   L.count = take(4);
@@ -69,6 +73,8 @@ Layout layout(const kvr_pages_config* c) {
   L.rope = take((size_t)c->max_len * (c->head_dim / 2) * sizeof(float2));
   L.ml = take((size_t)kPageAttnPartRows * sizeof(float2));
   L.part = take((size_t)kPageAttnPartRows * c->head_dim * sizeof(float));
+  L.ml_tc = take((size_t)kPageTcPartRows * sizeof(float2));
+  L.part_tc = take((size_t)kPageTcPartRows * c->head_dim * sizeof(float));
   L.total = at;
   return L;
 }
@@ -165,12 +171,17 @@ int kvr_pages_create(const kvr_pages_config* cfg, void* pool, size_t pool_bytes,
   c->attend.part = reinterpret_cast<float*>(w + L.part);
   c->attend.ml = reinterpret_cast<float2*>(w + L.ml);
   c->attend.counters = reinterpret_cast<int*>(w + L.counters);
+  memset(&c->attend_tc, 0, sizeof c->attend_tc);
+  c->attend_tc.part = reinterpret_cast<float*>(w + L.part_tc);
+  c->attend_tc.ml = reinterpret_cast<float2*>(w + L.ml_tc);
+  c->attend_tc.counters = c->attend.counters + kPageAttnMaxCtas;
   int sms = 0;
   cudaError_t e = cudaGetDevice(&c->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, c->device);
   c->ctas = std::min(sms, kPageAttnMaxCtas);
   if (e == cudaSuccess) e = page_plan_setup();
   if (e == cudaSuccess) e = page_attn_setup();
+  if (e == cudaSuccess) e = page_attn_tc_setup();
   if (e == cudaSuccess) e = cudaMemset(w + L.status, 0, L.count - L.status);
   if (e == cudaSuccess) e = cudaMemset(w + L.table, 0xff, (size_t)cfg->max_seqs * L.width * 4);
   if (e == cudaSuccess) e = cudaMemset(w + L.row_seq, 0xff, L.table - L.row_seq);
@@ -272,10 +283,27 @@ int kvr_page_attend(kvr_pages* c, int layer, const void* q, long long q_stride, 
   a.out_f16 = out_f16 || d.f16;
   a.rows = rows;
   a.scale_log2 = (float)((double)scale * 1.4426950408889634);
-  a.many = INT_MAX;
+  a.many = kPageMany;
+  const long long most = (long long)d.G * c->max_add;   // rows of a sequence and KV head, at most
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
   OnDevice on(c->device);
-  const int nt = (long long)d.G * c->max_add <= 8 ? 1 : 2;
-  const cudaError_t e = launch_page_attn(d, a, nt, c->ctas, static_cast<cudaStream_t>(stream));
+  cudaError_t e = cudaSuccess;
+  if (most > kPageMany) {
+    PageAttendTc b = c->attend_tc;
+    b.q = q;
+    b.qs = q_stride;
+    b.out = out;
+    b.out_f16 = a.out_f16;
+    b.rows = rows;
+    b.many = kPageMany;
+    b.min_units = kPageMinUnits;
+    b.scale_log2 = a.scale_log2;
+    e = launch_page_attn_tc(d, b, c->ctas, st);
+    if (e != cudaSuccess) return cuda_fail(c, e, "page attention launch");
+  }
+  // (one sequence with that many rows leaves nothing for the other kernel, but
+  // the rows of a captured plan may be fewer when it is replayed)
+  e = launch_page_attn(d, a, std::min<long long>(most, kPageMany) <= 8 ? 1 : 2, c->ctas, st);
   return e == cudaSuccess ? KVR_OK : cuda_fail(c, e, "page attention launch");
 }
 
@@ -289,7 +317,7 @@ int kvr_pages_sync(kvr_pages* c, void* stream) {
   if (e == cudaSuccess && (word[0] || word[1])) {
     e = cudaMemsetAsync(c->dev.status, 0, 8, st);
     // a launch that gave up may have left arrivals behind
-    if (e == cudaSuccess && word[0]) e = cudaMemsetAsync(c->attend.counters, 0, kPageAttnMaxCtas * 4, st);
+    if (e == cudaSuccess && word[0]) e = cudaMemsetAsync(c->attend.counters, 0, 2 * kPageAttnMaxCtas * 4, st);
     if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   }
   if (e != cudaSuccess) return cuda_fail(c, e, "page status readback");

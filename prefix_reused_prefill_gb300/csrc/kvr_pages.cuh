@@ -97,7 +97,23 @@ struct PageAttend {
   int* counters;     // arrivals, zero between launches
 };
 
+// ... and of the sequences with more (the tensor-memory kernel).
+struct PageAttendTc {
+  const void* q;
+  long long qs;
+  void* out;
+  int out_f16;
+  int rows;
+  int many;
+  int min_units;     // key blocks a CTA takes at least
+  float scale_log2;
+  float* part;       // [CTAs][2][256 rows][d]
+  float2* ml;        // [CTAs][2][256 rows]
+  int* counters;     // arrivals, zero between launches
+};
+
 constexpr int kPageAttnMaxCtas = 160;
+constexpr int kPageTcPartRows = kPageAttnMaxCtas * 2 * 256;
 // partial results of the split kernel, in rows: two tiles per warp (16 warps
 // with tiles of 8 rows, 8 warps with 16 rows) and two per CTA
 constexpr int kPageAttnPartRows = kPageAttnMaxCtas * (2 * 128 + 2 * 16);
@@ -112,6 +128,8 @@ cudaError_t launch_page_append(const PagesDev& p, const PageAppend& a, cudaStrea
 cudaError_t launch_page_read(const PagesDev& p, void* k_out, void* v_out, int rows, cudaStream_t st);
 cudaError_t page_attn_setup();
 cudaError_t launch_page_attn(const PagesDev& p, const PageAttend& a, int nt, int ctas, cudaStream_t st);
+cudaError_t page_attn_tc_setup();
+cudaError_t launch_page_attn_tc(const PagesDev& p, const PageAttendTc& a, int ctas, cudaStream_t st);
 
 }  // namespace kvr
 
