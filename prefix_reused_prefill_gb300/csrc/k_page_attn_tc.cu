@@ -14,9 +14,9 @@
 // of both tiles, 512 columns; while the softmax of one tile runs, the tensor
 // core works for the other.  Warp roles (13 warps, four on a scheduler at most, so
 // that a thread may hold 128 registers):
-//   0-3, 4-7   softmax of tile 0 / 1, a thread per row: S from tensor memory in
-//              halves of 64 keys (the second half twice: the registers hold one),
-//              P back over S; Q into shared memory at the start of a segment
+//   0-3, 4-7   softmax of tile 0 / 1, a thread per row: S from tensor memory 32
+//              keys at a time, P back over the part of S already read; Q into
+//              shared memory at the start of a segment
 //   8-11       a quarter of each block's keys, global -> registers (one block
 //              ahead) -> the fp16 tiles: K [128 keys][d] and V as [d][128 keys]
 //              (both K-major with the 128-byte swizzle), two stages each
@@ -71,31 +71,69 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
 __device__ __forceinline__ uint32_t idesc_f16(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// The product warp runs as one (every lane the same control flow, the elected
+// lane's instructions predicated), so that the operands stay in uniform
+// registers: from a branch of one lane each product cost about 117 cycles to
+// issue instead of the 64 that it takes.
+__device__ __forceinline__ uint32_t elect() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e;
+}
+__device__ __forceinline__ void mma_ss(uint32_t elected, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, e;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(elected)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t elected, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, e;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(elected)
       : "memory");
 }
-__device__ __forceinline__ void commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+__device__ __forceinline__ void commit(uint32_t elected, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "setp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(bar),
+      "r"(elected)
+      : "memory");
 }
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// two fp32 lanes in one instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)),
+        "l"(*reinterpret_cast<unsigned long long*>(&c)));
+  return *reinterpret_cast<float2*>(&r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
+  return *reinterpret_cast<float2*>(&r);
+}
 __device__ __forceinline__ void ld32(uint32_t taddr, uint32_t* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
@@ -109,15 +147,20 @@ __device__ __forceinline__ void ld32(uint32_t taddr, uint32_t* r) {
 }
 __device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void st32(uint32_t taddr, const uint32_t* r) {
+__device__ __forceinline__ void ld16(uint32_t taddr, uint32_t* r) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
-      "%30, %31, %32};" ::"r"(taddr),
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
@@ -347,6 +390,7 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
   auto wait = [&](uint64_t& bar, uint32_t parity) {
     return dev::mbar_wait(dev::smem_u32(&bar), parity & 1, p.status) && !*abort_v;
   };
+  auto all_wait = [&](uint64_t& bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)); };
   auto slot_o = [&](int c, int i) { return a.part + ((long long)c * 2 + i) * C::kSlot; };
   auto slot_ml = [&](int c, int i) { return a.ml + ((long long)c * 2 + i) * kPairRows; };
   // 8 dims of an output row
@@ -366,46 +410,47 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
   bool ok = true;
   if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- products
-    if (lane == 0) {
+    {
+      const uint32_t el = elect();
       const uint32_t id_qk = idesc_f16(kTile, kKeys), id_pv = idesc_f16(kTile, D);
       uint32_t it = 0, segs[2] = {0, 0}, done[2] = {0, 0};   // blocks; segments and blocks of each tile
       auto scores = [&](int t, uint32_t i) {
         const uint64_t qd = sw128_desc(q_base + t * C::kQTile), kd = sw128_desc(k_base + (i & 1) * C::kKTile);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          mma_ss(tmem + s_col(t), qd + (kk >> 2) * (C::kQAtom >> 4) + 2 * (kk & 3),
+          mma_ss(el, tmem + s_col(t), qd + (kk >> 2) * (C::kQAtom >> 4) + 2 * (kk & 3),
                  kd + (kk >> 2) * (C::kKAtom >> 4) + 2 * (kk & 3), id_qk, kk > 0 ? 1u : 0u);
-        commit(dev::smem_u32(&s_full[t]));
+        commit(el, dev::smem_u32(&s_full[t]));
       };
       ok = for_segments([&](const Seg& s, int j0, int j1) {
         const int tiles = kPairRows * s.tile + kTile < s.R ? 2 : 1;
-        if (!wait(k_full[it & 1], it >> 1)) return false;
+        if (!all_wait(k_full[it & 1], it >> 1)) return false;
         for (int t = 0; t < tiles; ++t) {
-          if (!wait(q_full[t], segs[t]++)) return false;
+          if (!all_wait(q_full[t], segs[t]++)) return false;
           fence_after();
           scores(t, it);
         }
-        commit(dev::smem_u32(&k_empty[it & 1]));
+        commit(el, dev::smem_u32(&k_empty[it & 1]));
         for (int j = j0; j < j1; ++j, ++it) {
           const bool more = j + 1 < j1;
           for (int t = 0; t < tiles; ++t) {
-            if (t == 0 && !wait(v_full[it & 1], it >> 1)) return false;
-            if (!wait(p_full[t], done[t])) return false;
+            if (t == 0 && !all_wait(v_full[it & 1], it >> 1)) return false;
+            if (!all_wait(p_full[t], done[t])) return false;
             fence_after();
             const uint64_t vd = sw128_desc(v_base + (it & 1) * C::kVTile);
 #pragma unroll
             for (int kk = 0; kk < kKeys / 16; ++kk)
-              mma_ts(tmem + o_col(t), tmem + s_col(t) + 8u * (uint32_t)kk,
+              mma_ts(el, tmem + o_col(t), tmem + s_col(t) + 8u * (uint32_t)kk,
                      vd + (kk >> 2) * (C::kVAtom >> 4) + 2 * (kk & 3), id_pv, (j > j0 || kk > 0) ? 1u : 0u);
-            commit(dev::smem_u32(&pv_done[t]));
-            if (t + 1 == tiles) commit(dev::smem_u32(&v_empty[it & 1]));
+            commit(el, dev::smem_u32(&pv_done[t]));
+            if (t + 1 == tiles) commit(el, dev::smem_u32(&v_empty[it & 1]));
             if (more) {
               // the next scores go over P, which this product still reads
-              if (t == 0 && !wait(k_full[(it + 1) & 1], (it + 1) >> 1)) return false;
-              if (!wait(pv_done[t], done[t])) return false;
+              if (t == 0 && !all_wait(k_full[(it + 1) & 1], (it + 1) >> 1)) return false;
+              if (!all_wait(pv_done[t], done[t])) return false;
               fence_after();
               scores(t, it + 1);
-              if (t + 1 == tiles) commit(dev::smem_u32(&k_empty[(it + 1) & 1]));
+              if (t + 1 == tiles) commit(el, dev::smem_u32(&k_empty[(it + 1) & 1]));
             }
             ++done[t];
           }
@@ -414,7 +459,7 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
       });
       if (!ok) {
         // a wait gave up: the products in flight end before their memory goes
-        commit(dev::smem_u32(&drained));
+        commit(el, dev::smem_u32(&drained));
         dev::mbar_wait_until(dev::smem_u32(&drained), 0, dev::globaltimer_ns() + kWaitLimitNs);
       }
     }
@@ -477,7 +522,7 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
       fetch_v(next_page);
       next_page = page_of(j0 + 1);
       for (int j = j0; j < j1; ++j, ++it) {
-        if (it >= 2 && !__all_sync(0xffffffffu, wait(k_empty[it & 1], (it >> 1) - 1))) return false;
+        if (it >= 2 && !all_wait(k_empty[it & 1], (it >> 1) - 1)) return false;
         const uint32_t k_tile = k_base + (it & 1) * C::kKTile;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -498,7 +543,7 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
         __syncwarp();
         if (lane == 0) dev::mbar_arrive(dev::smem_u32(&k_full[it & 1]));
         if (j + 1 < j1) fetch_k(next_page);
-        if (it >= 2 && !__all_sync(0xffffffffu, wait(v_empty[it & 1], (it >> 1) - 1))) return false;
+        if (it >= 2 && !all_wait(v_empty[it & 1], (it >> 1) - 1)) return false;
         const uint32_t v_tile = v_base + (it & 1) * C::kVTile + (kb >> 3) * C::kVAtom;
         // keys past the sequence weigh nothing and must not be NaN
         const int left = s.len - (kKeys * j + 8 * kb);
@@ -547,17 +592,20 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
         // q, scaled by a power of two with max|q| 2^e in [2^10, 2^11), as fp16
         const uint16_t* src =
             static_cast<const uint16_t*>(a.q) + (long long)(s.row0 + tok) * a.qs + (s.kv * p.G + rho - tok * p.G) * D;
-        float top = 0.f;
-        if (live) {
-#pragma unroll 4
-          for (int c = 0; c < D / 8; ++c) {
-            const uint4 u = *reinterpret_cast<const uint4*>(src + 8 * c);
-            const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+        uint4 u[D / 8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 y = dev::act2<F16>(x[i]);
-              top = max3(top, fabsf(y.x), fabsf(y.y));
-            }
+        for (int c = 0; c < D / 8; ++c) {
+          u[c] = make_uint4(0, 0, 0, 0);
+          if (live) u[c] = *reinterpret_cast<const uint4*>(src + 8 * c);
+        }
+        float top = 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          const uint32_t x[4] = {u[c].x, u[c].y, u[c].z, u[c].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 y = dev::act2<F16>(x[i]);
+            top = max3(top, fabsf(y.x), fabsf(y.y));
           }
         }
         int e = 137 - (int)(__float_as_uint(top) >> 23);
@@ -565,11 +613,9 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
         const float up = __uint_as_float((uint32_t)(127 + e) << 23);
         f = __uint_as_float((uint32_t)(127 - e) << 23) * a.scale_log2;
         const uint32_t tile = q_base + t * C::kQTile;
-#pragma unroll 4
+#pragma unroll
         for (int c = 0; c < D / 8; ++c) {
-          uint4 u = make_uint4(0, 0, 0, 0);
-          if (live) u = *reinterpret_cast<const uint4*>(src + 8 * c);
-          uint32_t x[4] = {u.x, u.y, u.z, u.w};
+          uint32_t x[4] = {u[c].x, u[c].y, u[c].z, u[c].w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float2 y = dev::act2<F16>(x[i]);
@@ -585,79 +631,97 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
       const int all_see = s.P + (int)((uint32_t)rho0 / (uint32_t)p.G);
       const int see = live ? s.P + tok : -1;
       float m_ref = -INFINITY, l = 0.f;
+      float sub = 0.f;                         // the reference, 0 before the first
+      float2 sum = make_float2(0.f, 0.f);
+      // A row's score passed its reference by more than 2^8 in the part of the
+      // block from key 32 c on: move the references, and what was formed under
+      // them (O, the sums, the block's earlier weights) along.
+      auto move_reference = [&](float top, int c, bool has_o) {
+        const float m_new = top > m_ref + kLazyMax ? top : m_ref;
+        const float factor = m_new != m_ref && m_ref != -INFINITY ? ex2_approx(m_ref - m_new) : 1.f;
+        m_ref = m_new;
+        sub = m_new == -INFINITY ? 0.f : m_new;
+        l *= factor;
+        sum.x *= factor;
+        sum.y *= factor;
+        if (has_o) {
+          if (!all_wait(pv_done[t], blocks - 1)) return false;
+          fence_after();
+#pragma unroll 1
+          for (int d = 0; d < D; d += 16) {
+            uint32_t x[16];
+            ld16(o_addr + d, x);
+            wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * factor);
+            st16(o_addr + d, x);
+          }
+        }
+        wait_st();   // (the weights stored so far are read back)
+#pragma unroll 1
+        for (int d = 0; d < c; ++d) {
+          uint32_t x[16];
+          ld16(s_addr + 16 * d, x);
+          wait_ld();
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float2 y = dev::act2<true>(x[k]);
+            x[k] = dev::pack_act<true>(y.x * factor, y.y * factor);
+          }
+          st16(s_addr + 16 * d, x);
+        }
+        return true;
+      };
       auto block = [&](int j, auto masked) {
         constexpr bool kMasked = decltype(masked)::value;
         const int seen = see - kKeys * j + 1;   // keys of the block that the row sees
-        uint32_t v[64];
-        auto half = [&](int h) {
-          ld32(s_addr + 64 * h, v);
-          ld32(s_addr + 64 * h + 32, v + 32);
+        const float2 f2 = make_float2(f, f);
+        uint32_t v[2][32];
+        ld32(s_addr, v[0]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t* x = v[c & 1];
           wait_ld();
+          if (c < 3) ld32(s_addr + 32 * (c + 1), v[(c + 1) & 1]);
           if (kMasked) {
 #pragma unroll
-            for (int k = 0; k < 64; ++k)
-              if (64 * h + k >= seen) v[k] = 0xff800000u;
+            for (int k = 0; k < 32; ++k)
+              if (32 * c + k >= seen) x[k] = 0xff800000u;
           }
-        };
-        float mx[2] = {-INFINITY, -INFINITY};
-        half(1);
+          float mx[2] = {__uint_as_float(x[0]), __uint_as_float(x[1])};
 #pragma unroll
-        for (int k = 0; k < 64; k += 4) {
-          mx[0] = max3(mx[0], __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
-          mx[1] = max3(mx[1], __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
-        }
-        half(0);
-#pragma unroll
-        for (int k = 0; k < 64; k += 4) {
-          mx[0] = max3(mx[0], __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
-          mx[1] = max3(mx[1], __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
-        }
-        const float top = fmaxf(mx[0], mx[1]) * f;
-        const bool move = top > m_ref + kLazyMax;
-        const float m_new = move ? top : m_ref;
-        const float factor = move && m_ref != -INFINITY ? ex2_approx(m_ref - m_new) : 1.f;
-        const float sub = m_new == -INFINITY ? 0.f : m_new;
-        float sum[2] = {0.f, 0.f};
-        uint32_t pk[32];
-        auto weights = [&](int h) {
-#pragma unroll
-          for (int k = 0; k < 64; k += 2) {
-            const float e0 = ex2_approx(fmaf(__uint_as_float(v[k]), f, -sub));
-            const float e1 = ex2_approx(fmaf(__uint_as_float(v[k + 1]), f, -sub));
-            sum[0] += e0;
-            sum[1] += e1;
-            pk[k / 2] = dev::pack_act<true>(e0, e1);
+          for (int k = 2; k < 30; k += 4) {
+            mx[0] = max3(mx[0], __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+            mx[1] = max3(mx[1], __uint_as_float(x[k + 2]), __uint_as_float(x[k + 3]));
           }
-          st32(s_addr + 32 * h, pk);
-        };
-        weights(0);
-        half(1);
-        weights(1);
-        bool good = true;
-        if (j > j0 && __any_sync(0xffffffffu, factor != 1.f)) {
-          good = __all_sync(0xffffffffu, wait(pv_done[t], blocks - 1));
-          if (good) {
-            fence_after();
-#pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              uint32_t x[32];
-              ld32(o_addr + c, x);
-              wait_ld();
-#pragma unroll
-              for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * factor);
-              st32(o_addr + c, x);
-            }
+          const float top = max3(mx[0], mx[1], fmaxf(__uint_as_float(x[30]), __uint_as_float(x[31]))) * f;
+          if (__any_sync(0xffffffffu, top > m_ref + kLazyMax)) {
+            wait_ld();   // (the loads of the slow path come after the one in flight)
+            if (!move_reference(top, c, j > j0)) return false;
           }
+          const float2 neg = make_float2(-sub, -sub);
+          uint32_t pk[16];
+          float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) {
+            float2 e = fma2(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), f2, neg);
+            e.x = ex2_approx(e.x);
+            e.y = ex2_approx(e.y);
+            part[(k >> 1) & 1] = add2(part[(k >> 1) & 1], e);
+            pk[k / 2] = dev::pack_act<true>(e.x, e.y);
+          }
+          sum = add2(sum, add2(part[0], part[1]));
+          st16(s_addr + 16 * c, pk);
         }
         wait_st();
-        l = l * factor + (sum[0] + sum[1]);
-        m_ref = m_new;
-        return good;
+        l += sum.x + sum.y;
+        sum = make_float2(0.f, 0.f);
+        return true;
       };
       for (int j = j0; j < j1; ++j) {
-        if (!__all_sync(0xffffffffu, wait(s_full[t], blocks))) return false;
+        if (!all_wait(s_full[t], blocks)) return false;
         fence_after();
-        const bool whole = kKeys * (j + 1) <= all_see + 1;
+        const bool whole = kKeys * (j + 1) <= all_see + 1;   // every row of the tile sees the block
         if (!(whole ? block(j, std::false_type()) : block(j, std::true_type()))) return false;
         fence_before();
         __syncwarp();
@@ -665,7 +729,7 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
         ++blocks;
       }
       // O, divided by its sum where this CTA has the whole segment
-      if (!__all_sync(0xffffffffu, wait(pv_done[t], blocks - 1))) return false;
+      if (!all_wait(pv_done[t], blocks - 1)) return false;
       fence_after();
       const bool whole_seg = j0 == 0 && j1 == s.nb;
       const float inv = whole_seg ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
@@ -745,33 +809,63 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
     const Seg s = seg[i];
     const int ca = owner(seg0[i]), parts = owner(seg0[i] + s.nb - 1) - ca + 1;
     const int rows = min(kPairRows, s.R - kPairRows * s.tile);
-    for (int e = tid; e < rows * (D / 8); e += kThreads) {
-      const int r = e / (D / 8), d = 8 * (e % (D / 8));
-      float m = -INFINITY;
-#pragma unroll 4
-      for (int k = 0; k < parts; ++k) m = fmaxf(m, __ldcg(slot_ml(ca + k, k == 0) + r).x);
-      float l = 0.f, x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-      for (int k = 0; k < parts; ++k) {
-        const float2 ml = __ldcg(slot_ml(ca + k, k == 0) + r);
-        const float4* src = reinterpret_cast<const float4*>(slot_o(ca + k, k == 0) + (long long)r * D + d);
-        const float4 y = __ldcg(src), z = __ldcg(src + 1);
-        // (a part in which the row saw nothing counts as it is: zeros, or NaN)
-        const float w = ml.x == -INFINITY ? 1.f : ex2_approx(ml.x - m);
-        l = fmaf(w, ml.y, l);
-        x[0] = fmaf(w, y.x, x[0]);
-        x[1] = fmaf(w, y.y, x[1]);
-        x[2] = fmaf(w, y.z, x[2]);
-        x[3] = fmaf(w, y.w, x[3]);
-        x[4] = fmaf(w, z.x, x[4]);
-        x[5] = fmaf(w, z.y, x[5]);
-        x[6] = fmaf(w, z.z, x[6]);
-        x[7] = fmaf(w, z.w, x[7]);
-      }
-      const float inv = l == 0.f ? 0.f : 1.f / l;
+    // a warp takes four rows at a time, a lane 4 (2) dims of each: the parts'
+    // loads of all four are in flight together
+    constexpr int kPer = D / 32;
+    for (int r0 = 4 * warp; r0 < rows; r0 += 4 * (kThreads / 32)) {
+      float m[4], l[4], x[4][kPer];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] *= inv;
-      store8(s, kPairRows * s.tile + r, d, x);
+      for (int q = 0; q < 4; ++q) {
+        m[q] = -INFINITY;
+        l[q] = 0.f;
+#pragma unroll
+        for (int d = 0; d < kPer; ++d) x[q][d] = 0.f;
+      }
+#pragma unroll 2
+      for (int k = 0; k < parts; ++k) {
+        const float2* mls = slot_ml(ca + k, k == 0) + r0;
+        const float* os = slot_o(ca + k, k == 0) + (long long)r0 * D + kPer * lane;
+        float2 ml[4];
+        float y[4][kPer];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          ml[q] = __ldcg(mls + q);   // (the slots have whole tiles of rows)
+          if (kPer == 4) {
+            const float4 z = __ldcg(reinterpret_cast<const float4*>(os + q * D));
+            y[q][0] = z.x; y[q][1] = z.y; y[q][kPer - 2] = z.z; y[q][kPer - 1] = z.w;
+          } else {
+            const float2 z = __ldcg(reinterpret_cast<const float2*>(os + q * D));
+            y[q][0] = z.x; y[q][1] = z.y;
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          // (a part in which the row saw nothing counts as it is: zeros, or NaN)
+          const float m_new = fmaxf(m[q], ml[q].x);
+          const float old = m[q] == m_new ? 1.f : ex2_approx(m[q] - m_new);
+          const float w = ml[q].x == -INFINITY ? 1.f : ex2_approx(ml[q].x - m_new);
+          m[q] = m_new;
+          l[q] = fmaf(l[q], old, w * ml[q].y);
+#pragma unroll
+          for (int d = 0; d < kPer; ++d) x[q][d] = fmaf(x[q][d], old, w * y[q][d]);
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (r0 + q >= rows) break;
+        const float inv = l[q] == 0.f ? 0.f : 1.f / l[q];
+        const int rho = kPairRows * s.tile + r0 + q;
+        const int tok = (int)((uint32_t)rho / (uint32_t)p.G);
+        uint16_t* dst = static_cast<uint16_t*>(a.out) +
+                        ((long long)(s.row0 + tok) * p.Hq + s.kv * p.G + rho - tok * p.G) * D + kPer * lane;
+        uint32_t v[kPer / 2];
+#pragma unroll
+        for (int d = 0; d < kPer; d += 2)
+          v[d / 2] = F16 || !a.out_f16 ? dev::pack_act<F16>(x[q][d] * inv, x[q][d + 1] * inv)
+                                       : dev::pack_act2(x[q][d] * inv, x[q][d + 1] * inv, true);
+        if (kPer == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(v[0], v[kPer / 2 - 1]);
+        else *reinterpret_cast<uint32_t*>(dst) = v[0];
+      }
     }
   }
 }
