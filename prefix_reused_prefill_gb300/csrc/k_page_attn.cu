@@ -154,6 +154,73 @@ struct Slot {
   float2* ml;
 };
 
+// Merge the parts of the segments that CTAs of the tensor-memory kernel share:
+// a warp takes four rows, a lane D / 32 dims of each, and all four rows' loads
+// are in flight together.  The whole grid shares the rows of all segments.
+template <int D, bool F16>
+__device__ void merge_tc(const PagesDev& p, const PageAttend& a, int warp_id, int warps) {
+  constexpr int kPer = D / 32, kGroups4 = kPageTcRows / 4;
+  const int lane = threadIdx.x & 31, r0 = 4 * (warp_id % kGroups4);
+  for (int ca = warp_id / kGroups4; ca < (int)gridDim.x; ca += warps / kGroups4) {
+    const PageShared s = a.shared[ca];
+    const int rows = min(kPageTcRows, s.R - kPageTcRows * s.tile);
+    if (s.parts == 0 || r0 >= rows) continue;
+    float m[4], l[4], x[4][kPer];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      m[q] = -INFINITY;
+      l[q] = 0.f;
+#pragma unroll
+      for (int d = 0; d < kPer; ++d) x[q][d] = 0.f;
+    }
+#pragma unroll 2
+    for (int k = 0; k < s.parts; ++k) {
+      const long long at = ((long long)(ca + k) * 2 + (k == 0 ? 1 : 0)) * kPageTcRows + r0;
+      float2 ml[4];
+      float y[4][kPer];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {   // (a slot has whole tiles of rows)
+        ml[q] = __ldcg(a.tc_ml + at + q);
+        const float* src = a.tc_part + (at + q) * D + kPer * lane;
+        if (kPer == 4) {
+          const float4 z = __ldcg(reinterpret_cast<const float4*>(src));
+          y[q][0] = z.x; y[q][1] = z.y; y[q][kPer - 2] = z.z; y[q][kPer - 1] = z.w;
+        } else {
+          const float2 z = __ldcg(reinterpret_cast<const float2*>(src));
+          y[q][0] = z.x; y[q][1] = z.y;
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        // (a part in which the row saw nothing counts as it is: zeros, or NaN)
+        const float m_new = fmaxf(m[q], ml[q].x);
+        const float old = m[q] == m_new ? 1.f : ex2_approx(m[q] - m_new);
+        const float w = ml[q].x == -INFINITY ? 1.f : ex2_approx(ml[q].x - m_new);
+        m[q] = m_new;
+        l[q] = fmaf(l[q], old, w * ml[q].y);
+#pragma unroll
+        for (int d = 0; d < kPer; ++d) x[q][d] = fmaf(x[q][d], old, w * y[q][d]);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (r0 + q >= rows) break;
+      const float inv = l[q] == 0.f ? 0.f : 1.f / l[q];
+      const int rho = kPageTcRows * s.tile + r0 + q;
+      const int tok = (int)((uint32_t)rho / (uint32_t)p.G);
+      uint16_t* dst = static_cast<uint16_t*>(a.out) +
+                      ((long long)(s.row0 + tok) * p.Hq + s.kv * p.G + rho - tok * p.G) * D + kPer * lane;
+      uint32_t v[kPer / 2];
+#pragma unroll
+      for (int d = 0; d < kPer; d += 2)
+        v[d / 2] = F16 || !a.out_f16 ? dev::pack_act<F16>(x[q][d] * inv, x[q][d + 1] * inv)
+                                     : dev::pack_act2(x[q][d] * inv, x[q][d + 1] * inv, true);
+      if (kPer == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(v[0], v[kPer / 2 - 1]);
+      else *reinterpret_cast<uint32_t*>(dst) = v[0];
+    }
+  }
+}
+
 template <int D, int NT, bool F16>
 __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
 page_attn_kernel(const PagesDev p, const PageAttend a) {
@@ -248,7 +315,9 @@ page_attn_kernel(const PagesDev p, const PageAttend a) {
   }
   if (tid == 0) first_unit[n] = units;
   __syncthreads();
-  if (units == 0 || *abort_v) return;
+  if (*abort_v) return;
+  if (a.shared) merge_tc<D, F16>(p, a, cta * kWarps + warp, (int)gridDim.x * kWarps);
+  if (units == 0) return;
   const bool whole_segs = segs <= (int)gridDim.x && most_pages <= 2 * kWarps;
   // else every warp gets a unit before another CTA is taken
   const int ctas = whole_segs ? segs : min((int)gridDim.x, (units + kWarps - 1) / kWarps);

@@ -12,19 +12,23 @@
 // of one 128-row tile over it, so a CTA runs two row tiles over each block: one
 // dequantisation feeds four products.  Tensor memory holds S (P over it) and O
 // of both tiles, 512 columns; while the softmax of one tile runs, the tensor
-// core works for the other.  Warp roles (13 warps, four on a scheduler at most, so
-// that a thread may hold 128 registers):
-//   0-3, 4-7   softmax of tile 0 / 1, a thread per row: S from tensor memory 32
-//              keys at a time, P back over the part of S already read; Q into
-//              shared memory at the start of a segment
-//   8-11       a quarter of each block's keys, global -> registers (one block
+// core works for the other.  Warp roles (20 warps, 96 registers a thread):
+//   0-7, 8-15  softmax of tile 0 / 1, two threads per row, one for each 64 keys of
+//              the block: S from tensor memory 8 keys at a time, weights under the
+//              row's present reference, one vote of the two warps that share
+//              rows whether a score passed it (then the reference moves and the
+//              block is formed again), P back over the thread's own half of S.
+//              Q into shared memory at the start of a segment.  The first warp
+//              of a tile also issues the tile's products: its softmax, P V and
+//              the next scores follow one another anyway.
+//   16-19      a quarter of each block's keys, global -> registers (one block
 //              ahead) -> the fp16 tiles: K [128 keys][d] and V as [d][128 keys]
 //              (both K-major with the 128-byte swizzle), two stages each
-//   12         one thread issues the products
 // The work, all (sequence, pair of row tiles, KV head, key block) units in this
-// order, is cut into equal runs, one per CTA, whatever the lengths are; parts of
-// a segment (one sequence, pair and head) that several CTAs hold are merged by
-// the last of them to arrive, in the order of the keys.
+// order, is cut into equal runs, one per CTA, whatever the lengths are; the parts
+// of a segment (one sequence, pair and head) that several CTAs hold go to the
+// work area, and the launch that follows (k_page_attn.cu) merges them with the
+// whole card: one CTA took longer for that than for its run.
 //
 // A NaN scale: of K, it makes the key's score NaN.  Of V, it would reach rows
 // that do not see the key (0 * NaN), so the key's score becomes NaN instead and
@@ -39,10 +43,10 @@ namespace kvr {
 namespace {
 
 constexpr int kTile = 128;
-constexpr int kPairRows = 2 * kTile;
+constexpr int kPairRows = kPageTcRows;
 constexpr int kKeys = 128;
-constexpr int kDecodeWarp = 8, kMmaWarp = 12;
-constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kDecodeWarp = 16;
+constexpr int kThreads = 32 * (kDecodeWarp + 4);
 constexpr float kLazyMax = 8.0f;
 
 template <int D>
@@ -56,7 +60,6 @@ struct Tc {
   static constexpr int kVAtom = D * 128;
   static constexpr int kStages = 2;
   static constexpr int kSmem = 2 * kQTile + kStages * (kKTile + kVTile) + 1024;
-  static constexpr int kSlot = kPairRows * D;    // floats of a partial result
 };
 // tensor memory columns
 __device__ __forceinline__ uint32_t s_col(int t) { return (uint32_t)(128 * t); }
@@ -71,7 +74,7 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
 __device__ __forceinline__ uint32_t idesc_f16(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-// The product warp runs as one (every lane the same control flow, the elected
+// A warp that issues products runs as one (every lane the same control flow, the elected
 // lane's instructions predicated), so that the operands stay in uniform
 // registers: from a branch of one lane each product cost about 117 cycles to
 // issue instead of the 64 that it takes.
@@ -163,6 +166,27 @@ __device__ __forceinline__ void st16(uint32_t taddr, const uint32_t* r) {
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+__device__ __forceinline__ void ld8(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+// barrier of n threads; whether p holds for any of them
+__device__ __forceinline__ bool any_of(int id, int n, bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(n), "r"((uint32_t)p)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void named_sync(int id, int n) {
+  asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   __half2 r = __hmul2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
   return *reinterpret_cast<uint32_t*>(&r);
@@ -227,12 +251,12 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
   using K = Chunk<D>;
   constexpr int kG = C::kGroups;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], drained;
+  __shared__ __align__(8) uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], drained[2];
   __shared__ __align__(8) uint64_t k_full[C::kStages], k_empty[C::kStages], v_full[C::kStages], v_empty[C::kStages];
   __shared__ long long first_unit[kPageMaxSeqs + 1];   // units before each sequence
   __shared__ int start[4];                             // this CTA's first unit: sequence, tile, head, block
   __shared__ uint32_t tmem_slot;
-  __shared__ int last_flag[2];
+  __shared__ float exchange[2][2][kTile];              // [tile][half of the block][row]
   __shared__ int abort_flag;
   volatile int* abort_v = &abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -243,17 +267,17 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
   dev::pdl_trigger();
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      dev::mbar_init(dev::smem_u32(&q_full[i]), 4);
+      dev::mbar_init(dev::smem_u32(&q_full[i]), 8);
       dev::mbar_init(dev::smem_u32(&s_full[i]), 1);
-      dev::mbar_init(dev::smem_u32(&p_full[i]), 4);
+      dev::mbar_init(dev::smem_u32(&p_full[i]), 8);
       dev::mbar_init(dev::smem_u32(&pv_done[i]), 1);
+      dev::mbar_init(dev::smem_u32(&drained[i]), 1);
     }
-    dev::mbar_init(dev::smem_u32(&drained), 1);
     for (int i = 0; i < C::kStages; ++i) {
       dev::mbar_init(dev::smem_u32(&k_full[i]), 4);
-      dev::mbar_init(dev::smem_u32(&k_empty[i]), 1);
+      dev::mbar_init(dev::smem_u32(&k_empty[i]), 2);   // (one for each tile)
       dev::mbar_init(dev::smem_u32(&v_full[i]), 4);
-      dev::mbar_init(dev::smem_u32(&v_empty[i]), 1);
+      dev::mbar_init(dev::smem_u32(&v_empty[i]), 2);
     }
     dev::fence_mbar_init();
   }
@@ -306,9 +330,18 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
   }
   __syncthreads();
   const long long units = first_unit[n];
-  if (units == 0 || *abort_v) return;
+  auto describe = [&](const PageShared& x) {
+    if (tid == 0) a.shared[cta] = x;
+  };
+  if (units == 0 || *abort_v) {
+    describe(PageShared{});
+    return;
+  }
   const int ctas = (int)min((long long)gridDim.x, (units + a.min_units - 1) / a.min_units);
-  if (cta >= ctas) return;
+  if (cta >= ctas) {
+    describe(PageShared{});
+    return;
+  }
   const long long c0 = units * cta / ctas, c1 = units * (cta + 1) / ctas;
   // the segment that holds unit u, found by one warp
   auto locate = [&](long long u) {
@@ -340,14 +373,14 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
       rem -= __shfl_sync(0xffffffffu, inc, 31);
     }
     s.nb = blocks_of(s, s.tile);
-    s.kv = (int)(rem / s.nb);
+    s.kv = (int)((uint32_t)rem / (uint32_t)s.nb);   // (rem < blocks * heads of a pair)
     start[0] = s.b;
     start[1] = s.tile;
     start[2] = s.kv;
-    start[3] = (int)(rem % s.nb);
+    start[3] = (int)rem - s.kv * s.nb;
   };
   if (warp == 0) locate(c0);
-  if (warp == kMmaWarp) {
+  if (warp == kDecodeWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(dev::smem_u32(&tmem_slot)));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
@@ -391,79 +424,8 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
     return dev::mbar_wait(dev::smem_u32(&bar), parity & 1, p.status) && !*abort_v;
   };
   auto all_wait = [&](uint64_t& bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)); };
-  auto slot_o = [&](int c, int i) { return a.part + ((long long)c * 2 + i) * C::kSlot; };
-  auto slot_ml = [&](int c, int i) { return a.ml + ((long long)c * 2 + i) * kPairRows; };
-  // 8 dims of an output row
-  auto store8 = [&](const Seg& s, int rho, int d, const float* x) {
-    const int tok = (int)((uint32_t)rho / (uint32_t)p.G);
-    const long long row = (long long)(s.row0 + tok) * p.Hq + s.kv * p.G + rho - tok * p.G;
-    uint4 v;
-    if (F16 || !a.out_f16)
-      v = make_uint4(dev::pack_act<F16>(x[0], x[1]), dev::pack_act<F16>(x[2], x[3]), dev::pack_act<F16>(x[4], x[5]),
-                     dev::pack_act<F16>(x[6], x[7]));
-    else
-      v = make_uint4(dev::pack_act2(x[0], x[1], true), dev::pack_act2(x[2], x[3], true),
-                     dev::pack_act2(x[4], x[5], true), dev::pack_act2(x[6], x[7], true));
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row * D + d) = v;
-  };
-
   bool ok = true;
-  if (warp == kMmaWarp) {
-    // ---------------------------------------------------------------- products
-    {
-      const uint32_t el = elect();
-      const uint32_t id_qk = idesc_f16(kTile, kKeys), id_pv = idesc_f16(kTile, D);
-      uint32_t it = 0, segs[2] = {0, 0}, done[2] = {0, 0};   // blocks; segments and blocks of each tile
-      auto scores = [&](int t, uint32_t i) {
-        const uint64_t qd = sw128_desc(q_base + t * C::kQTile), kd = sw128_desc(k_base + (i & 1) * C::kKTile);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          mma_ss(el, tmem + s_col(t), qd + (kk >> 2) * (C::kQAtom >> 4) + 2 * (kk & 3),
-                 kd + (kk >> 2) * (C::kKAtom >> 4) + 2 * (kk & 3), id_qk, kk > 0 ? 1u : 0u);
-        commit(el, dev::smem_u32(&s_full[t]));
-      };
-      ok = for_segments([&](const Seg& s, int j0, int j1) {
-        const int tiles = kPairRows * s.tile + kTile < s.R ? 2 : 1;
-        if (!all_wait(k_full[it & 1], it >> 1)) return false;
-        for (int t = 0; t < tiles; ++t) {
-          if (!all_wait(q_full[t], segs[t]++)) return false;
-          fence_after();
-          scores(t, it);
-        }
-        commit(el, dev::smem_u32(&k_empty[it & 1]));
-        for (int j = j0; j < j1; ++j, ++it) {
-          const bool more = j + 1 < j1;
-          for (int t = 0; t < tiles; ++t) {
-            if (t == 0 && !all_wait(v_full[it & 1], it >> 1)) return false;
-            if (!all_wait(p_full[t], done[t])) return false;
-            fence_after();
-            const uint64_t vd = sw128_desc(v_base + (it & 1) * C::kVTile);
-#pragma unroll
-            for (int kk = 0; kk < kKeys / 16; ++kk)
-              mma_ts(el, tmem + o_col(t), tmem + s_col(t) + 8u * (uint32_t)kk,
-                     vd + (kk >> 2) * (C::kVAtom >> 4) + 2 * (kk & 3), id_pv, (j > j0 || kk > 0) ? 1u : 0u);
-            commit(el, dev::smem_u32(&pv_done[t]));
-            if (t + 1 == tiles) commit(el, dev::smem_u32(&v_empty[it & 1]));
-            if (more) {
-              // the next scores go over P, which this product still reads
-              if (t == 0 && !all_wait(k_full[(it + 1) & 1], (it + 1) >> 1)) return false;
-              if (!all_wait(pv_done[t], done[t])) return false;
-              fence_after();
-              scores(t, it + 1);
-              if (t + 1 == tiles) commit(el, dev::smem_u32(&k_empty[(it + 1) & 1]));
-            }
-            ++done[t];
-          }
-        }
-        return true;
-      });
-      if (!ok) {
-        // a wait gave up: the products in flight end before their memory goes
-        commit(el, dev::smem_u32(&drained));
-        dev::mbar_wait_until(dev::smem_u32(&drained), 0, dev::globaltimer_ns() + kWaitLimitNs);
-      }
-    }
-  } else if (warp >= kDecodeWarp) {
+  if (warp >= kDecodeWarp) {
     // ---------------------------------------------------------------- tiles
     // K: a lane has dims 32 j + 8 t .. + 7 of a key; lanes 0-3 and 4-7 of a
     // store hold keys 4 apart, whose chunks the swizzle puts side by side.
@@ -576,31 +538,57 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
     });
   } else {
     // ---------------------------------------------------------------- softmax
-    const int t = warp >> 2;                   // row tile
-    const int r = 32 * (warp & 3) + lane;      // row of it
+    const int t = warp >> 3, h = (warp >> 2) & 1;   // row tile, half of the block's keys (and of O's dims)
+    const int r = 32 * (warp & 3) + lane;           // row of the tile
+    const int pair = 1 + 4 * t + (warp & 3);        // barrier of the two warps with the same rows
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    const uint32_t s_addr = lanes + s_col(t), o_addr = lanes + o_col(t);
-    uint32_t blocks = 0;                       // blocks of this tile so far
-    ok = for_segments([&](const Seg& s, int j0, int j1) {
+    const uint32_t s_addr = lanes + s_col(t) + 64 * h, o_addr = lanes + o_col(t) + D / 2 * h;
+    const uint32_t q_tile = q_base + t * C::kQTile;
+    uint32_t blocks = 0;                            // blocks of this tile so far
+    uint32_t it = 0, segs = 0;                      // all blocks of the run; segments of this tile
+    const bool issuer = (warp & 7) == 0;
+    const uint32_t el = elect();
+    const uint32_t id_qk = idesc_f16(kTile, kKeys), id_pv = idesc_f16(kTile, D);
+    // S = Q K^T of block i of the run; both tiles free the K stage (frees = 2
+    // where there is one tile)
+    auto scores = [&](uint32_t i, int frees) {
+      const uint64_t qd = sw128_desc(q_tile), kd = sw128_desc(k_base + (i & 1) * C::kKTile);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+        mma_ss(el, tmem + s_col(t), qd + (kk >> 2) * (C::kQAtom >> 4) + 2 * (kk & 3),
+               kd + (kk >> 2) * (C::kKAtom >> 4) + 2 * (kk & 3), id_qk, kk > 0 ? 1u : 0u);
+      commit(el, dev::smem_u32(&s_full[t]));
+      for (int x = 0; x < frees; ++x) commit(el, dev::smem_u32(&k_empty[i & 1]));
+    };
+    // ok stays false once a wait gave up: the warp then skips its work but
+    // still meets its partner at every barrier
+    for_segments([&](const Seg& s, int j0, int j1) {
       const int rho0 = kPairRows * s.tile + kTile * t;
-      if (rho0 >= s.R) return true;            // one tile only
+      if (rho0 >= s.R) {                            // one tile only
+        it += j1 - j0;
+        return true;
+      }
+      const int frees = t == 0 && kPairRows * s.tile + kTile >= s.R ? 2 : 1;
+      // every warp of the tile is done with the last segment: with the exchange
+      // and with its part of the Q tile, which O went through
+      named_sync(9 + t, 256);
       const int rho = rho0 + r;
       const bool live = rho < s.R;
       const int tok = live ? (int)((uint32_t)rho / (uint32_t)p.G) : 0;
       float f;
       {
         // q, scaled by a power of two with max|q| 2^e in [2^10, 2^11), as fp16
-        const uint16_t* src =
-            static_cast<const uint16_t*>(a.q) + (long long)(s.row0 + tok) * a.qs + (s.kv * p.G + rho - tok * p.G) * D;
-        uint4 u[D / 8];
+        const uint16_t* src = static_cast<const uint16_t*>(a.q) + (long long)(s.row0 + tok) * a.qs +
+                              (s.kv * p.G + rho - tok * p.G) * D + D / 2 * h;
+        uint4 u[D / 16];
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
+        for (int c = 0; c < D / 16; ++c) {
           u[c] = make_uint4(0, 0, 0, 0);
           if (live) u[c] = *reinterpret_cast<const uint4*>(src + 8 * c);
         }
         float top = 0.f;
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
+        for (int c = 0; c < D / 16; ++c) {
           const uint32_t x[4] = {u[c].x, u[c].y, u[c].z, u[c].w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -608,265 +596,239 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
             top = max3(top, fabsf(y.x), fabsf(y.y));
           }
         }
+        exchange[t][h][r] = top;
+        named_sync(pair, 64);
+        top = fmaxf(top, exchange[t][h ^ 1][r]);
         int e = 137 - (int)(__float_as_uint(top) >> 23);
         e = top > 0.f ? max(-100, min(100, e)) : 0;
         const float up = __uint_as_float((uint32_t)(127 + e) << 23);
         f = __uint_as_float((uint32_t)(127 - e) << 23) * a.scale_log2;
-        const uint32_t tile = q_base + t * C::kQTile;
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
+        for (int c = 0; c < D / 16; ++c) {
           uint32_t x[4] = {u[c].x, u[c].y, u[c].z, u[c].w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float2 y = dev::act2<F16>(x[i]);
             x[i] = dev::pack_act<true>(y.x * up, y.y * up);
           }
-          sts128(tile + (c >> 3) * C::kQAtom + dev::swz128(r, c & 7), x[0], x[1], x[2], x[3]);
+          const int chunk = D / 16 * h + c;
+          sts128(q_tile + (chunk >> 3) * C::kQAtom + dev::swz128(r, chunk & 7), x[0], x[1], x[2], x[3]);
         }
         fence_smem();
         __syncwarp();
-        if (lane == 0) dev::mbar_arrive(dev::smem_u32(&q_full[t]));
+        if (lane == 0 && ok) dev::mbar_arrive(dev::smem_u32(&q_full[t]));
+        if (issuer && ok) {
+          ok = all_wait(q_full[t], segs) && all_wait(k_full[it & 1], it >> 1);
+          fence_after();
+          if (ok) scores(it, frees);
+        }
+        ++segs;
       }
       // the earliest row of the tile sees everything up to here
       const int all_see = s.P + (int)((uint32_t)rho0 / (uint32_t)p.G);
       const int see = live ? s.P + tok : -1;
-      float m_ref = -INFINITY, l = 0.f;
-      float sub = 0.f;                         // the reference, 0 before the first
-      float2 sum = make_float2(0.f, 0.f);
-      // A row's score passed its reference by more than 2^8 in the part of the
-      // block from key 32 c on: move the references, and what was formed under
-      // them (O, the sums, the block's earlier weights) along.
-      auto move_reference = [&](float top, int c, bool has_o) {
-        const float m_new = top > m_ref + kLazyMax ? top : m_ref;
-        const float factor = m_new != m_ref && m_ref != -INFINITY ? ex2_approx(m_ref - m_new) : 1.f;
-        m_ref = m_new;
-        sub = m_new == -INFINITY ? 0.f : m_new;
-        l *= factor;
-        sum.x *= factor;
-        sum.y *= factor;
-        if (has_o) {
-          if (!all_wait(pv_done[t], blocks - 1)) return false;
-          fence_after();
-#pragma unroll 1
-          for (int d = 0; d < D; d += 16) {
-            uint32_t x[16];
-            ld16(o_addr + d, x);
-            wait_ld();
-#pragma unroll
-            for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * factor);
-            st16(o_addr + d, x);
-          }
-        }
-        wait_st();   // (the weights stored so far are read back)
-#pragma unroll 1
-        for (int d = 0; d < c; ++d) {
-          uint32_t x[16];
-          ld16(s_addr + 16 * d, x);
-          wait_ld();
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const float2 y = dev::act2<true>(x[k]);
-            x[k] = dev::pack_act<true>(y.x * factor, y.y * factor);
-          }
-          st16(s_addr + 16 * d, x);
-        }
-        return true;
-      };
-      auto block = [&](int j, auto masked) {
+      float m_ref = -INFINITY, l = 0.f, sub = 0.f;   // (sub: the reference, 0 before the first)
+      // the 64 weights of one half row under the present reference, and the
+      // largest score; the S columns stay as they are
+      auto weights = [&](int j, auto masked, uint32_t* pk, float& sum) {
         constexpr bool kMasked = decltype(masked)::value;
-        const int seen = see - kKeys * j + 1;   // keys of the block that the row sees
-        const float2 f2 = make_float2(f, f);
-        uint32_t v[2][32];
-        ld32(s_addr, v[0]);
+        const int seen = see - kKeys * j - 64 * h + 1;   // keys of the half that the row sees
+        const float2 f2 = make_float2(f, f), neg = make_float2(-sub, -sub);
+        float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        float mx[2] = {-INFINITY, -INFINITY};
+        uint32_t v[2][8];
+        ld8(s_addr, v[0]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 8; ++c) {
           uint32_t* x = v[c & 1];
           wait_ld();
-          if (c < 3) ld32(s_addr + 32 * (c + 1), v[(c + 1) & 1]);
+          if (c < 7) ld8(s_addr + 8 * (c + 1), v[(c + 1) & 1]);
           if (kMasked) {
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (32 * c + k >= seen) x[k] = 0xff800000u;
+            for (int k = 0; k < 8; ++k)
+              if (8 * c + k >= seen) x[k] = 0xff800000u;
           }
-          float mx[2] = {__uint_as_float(x[0]), __uint_as_float(x[1])};
 #pragma unroll
-          for (int k = 2; k < 30; k += 4) {
+          for (int k = 0; k < 8; k += 4) {
             mx[0] = max3(mx[0], __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
             mx[1] = max3(mx[1], __uint_as_float(x[k + 2]), __uint_as_float(x[k + 3]));
           }
-          const float top = max3(mx[0], mx[1], fmaxf(__uint_as_float(x[30]), __uint_as_float(x[31]))) * f;
-          if (__any_sync(0xffffffffu, top > m_ref + kLazyMax)) {
-            wait_ld();   // (the loads of the slow path come after the one in flight)
-            if (!move_reference(top, c, j > j0)) return false;
-          }
-          const float2 neg = make_float2(-sub, -sub);
-          uint32_t pk[16];
-          float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-          for (int k = 0; k < 32; k += 2) {
+          for (int k = 0; k < 8; k += 2) {
             float2 e = fma2(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), f2, neg);
             e.x = ex2_approx(e.x);
             e.y = ex2_approx(e.y);
             part[(k >> 1) & 1] = add2(part[(k >> 1) & 1], e);
-            pk[k / 2] = dev::pack_act<true>(e.x, e.y);
+            pk[4 * c + k / 2] = dev::pack_act<true>(e.x, e.y);
           }
-          sum = add2(sum, add2(part[0], part[1]));
-          st16(s_addr + 16 * c, pk);
         }
-        wait_st();
-        l += sum.x + sum.y;
-        sum = make_float2(0.f, 0.f);
-        return true;
+        part[0] = add2(part[0], part[1]);
+        sum = part[0].x + part[0].y;
+        return fmaxf(mx[0], mx[1]) * f;
       };
       for (int j = j0; j < j1; ++j) {
-        if (!all_wait(s_full[t], blocks)) return false;
+        if (ok) ok = all_wait(s_full[t], blocks);
         fence_after();
-        const bool whole = kKeys * (j + 1) <= all_see + 1;   // every row of the tile sees the block
-        if (!(whole ? block(j, std::false_type()) : block(j, std::true_type()))) return false;
+        // every row of the tile sees the block?
+        const bool whole = kKeys * (j + 1) <= all_see + 1;
+        uint32_t pk[32];
+        float sum = 0.f, top = -INFINITY;
+        auto form = [&]() {
+          if (!ok) return;
+          top = whole ? weights(j, std::false_type(), pk, sum) : weights(j, std::true_type(), pk, sum);
+        };
+        form();
+        // a row's score passed its reference by more than 2^8 (the first block
+        // of a segment always does)
+        if (any_of(pair, 64, ok && top > m_ref + kLazyMax)) {
+          exchange[t][h][r] = top;
+          named_sync(pair, 64);
+          top = fmaxf(top, exchange[t][h ^ 1][r]);
+          const float m_new = top > m_ref + kLazyMax ? top : m_ref;
+          const float factor = m_new != m_ref && m_ref != -INFINITY ? ex2_approx(m_ref - m_new) : 1.f;
+          m_ref = m_new;
+          sub = m_new == -INFINITY ? 0.f : m_new;
+          l *= factor;
+          if (ok && j > j0) {
+            ok = all_wait(pv_done[t], blocks - 1);
+            fence_after();
+            if (ok) {
+#pragma unroll 1
+              for (int d = 0; d < D / 2; d += 16) {
+                uint32_t x[16];
+                ld16(o_addr + d, x);
+                wait_ld();
+#pragma unroll
+                for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * factor);
+                st16(o_addr + d, x);
+              }
+            }
+          }
+          form();
+        }
+        l += sum;
+        if (ok) {
+          st16(s_addr, pk);
+          st16(s_addr + 16, pk + 16);
+          wait_st();
+        }
         fence_before();
         __syncwarp();
-        if (lane == 0) dev::mbar_arrive(dev::smem_u32(&p_full[t]));
+        if (lane == 0 && ok) dev::mbar_arrive(dev::smem_u32(&p_full[t]));
+        if (issuer && ok) {
+          ok = all_wait(p_full[t], blocks) && all_wait(v_full[it & 1], it >> 1);
+          fence_after();
+          if (ok) {
+            const uint64_t vd = sw128_desc(v_base + (it & 1) * C::kVTile);
+#pragma unroll
+            for (int kk = 0; kk < kKeys / 16; ++kk)
+              mma_ts(el, tmem + o_col(t), tmem + s_col(t) + 64u * (kk >> 2) + 8u * (kk & 3),
+                     vd + (kk >> 2) * (C::kVAtom >> 4) + 2 * (kk & 3), id_pv, (j > j0 || kk > 0) ? 1u : 0u);
+            commit(el, dev::smem_u32(&pv_done[t]));
+            for (int x = 0; x < frees; ++x) commit(el, dev::smem_u32(&v_empty[it & 1]));
+            if (j + 1 < j1) {
+              // the next scores go over P, which this product still reads
+              ok = all_wait(k_full[(it + 1) & 1], (it + 1) >> 1) && all_wait(pv_done[t], blocks);
+              fence_after();
+              if (ok) scores(it + 1, frees);
+            }
+          }
+        }
         ++blocks;
+        ++it;
       }
-      // O, divided by its sum where this CTA has the whole segment
-      if (!all_wait(pv_done[t], blocks - 1)) return false;
+      // the row's sum; O, divided by it where this CTA has the whole segment
+      named_sync(pair, 64);   // (the last exchange has been read)
+      exchange[t][h][r] = l;
+      named_sync(pair, 64);
+      l += exchange[t][h ^ 1][r];
+      if (ok) ok = all_wait(pv_done[t], blocks - 1);
       fence_after();
+      if (!ok) return true;
       const bool whole_seg = j0 == 0 && j1 == s.nb;
       const float inv = whole_seg ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-      const int slot = j0 == 0 ? 1 : 0;
-      const int pr = kTile * t + r;
+      const long long slot = ((long long)cta * 2 + (j0 == 0 ? 1 : 0)) * kPairRows + kTile * t;
+      if (!whole_seg && h == 0) a.ml[slot + r] = live ? make_float2(m_ref, l) : make_float2(-INFINITY, 0.f);
+      // 32 dims at a time through this warp's part of the Q tile (the last
+      // scores are formed), so that stores to global memory are whole lines
+      const uint32_t stage = q_tile + (uint32_t)(C::kQTile / 8) * (uint32_t)(warp & 7);
+      constexpr int kCols = D / 4;               // dims of a pass: two passes for the thread's half
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        uint32_t x[32];
-        ld32(o_addr + c, x);
+      for (int c = 0; c < D / 2; c += kCols) {
+        uint32_t x[kCols];
+        if (kCols == 32) ld32(o_addr + c, x);
+        else ld16(o_addr + c, x);
         wait_ld();
-        if (!live) continue;
-        float y[32];
+        __syncwarp();
 #pragma unroll
-        for (int k = 0; k < 32; ++k) y[k] = __uint_as_float(x[k]) * inv;
-        if (whole_seg) {
+        for (int k = 0; k < kCols / 4; ++k)
+          sts128(stage + r % 32 * (kCols * 4) + ((k ^ (r & (kCols / 4 - 1))) << 4),
+                 __float_as_uint(__uint_as_float(x[4 * k]) * inv), __float_as_uint(__uint_as_float(x[4 * k + 1]) * inv),
+                 __float_as_uint(__uint_as_float(x[4 * k + 2]) * inv),
+                 __float_as_uint(__uint_as_float(x[4 * k + 3]) * inv));
+        __syncwarp();
+        constexpr int kLanes = kCols / 4;        // lanes of a row
 #pragma unroll
-          for (int k = 0; k < 32; k += 8) store8(s, rho, c + k, y + k);
-        } else {
-          float* dst = slot_o(cta, slot) + (long long)pr * D + c;
-#pragma unroll
-          for (int k = 0; k < 32; k += 4)
-            *reinterpret_cast<float4*>(dst + k) = make_float4(y[k], y[k + 1], y[k + 2], y[k + 3]);
+        for (int i = 0; i < kLanes; ++i) {
+          const int rr = 32 / kLanes * i + lane / kLanes, k = lane % kLanes;
+          const int row = 32 * (warp & 3) + rr, rho2 = rho0 + row;
+          const uint4 y = dev::lds128(stage + rr * (kCols * 4) + ((k ^ (rr & (kLanes - 1))) << 4));
+          if (rho2 >= s.R) continue;
+          const int dim = D / 2 * h + c + 4 * k;
+          if (whole_seg) {
+            const int tok2 = (int)((uint32_t)rho2 / (uint32_t)p.G);
+            const long long o_row = (long long)(s.row0 + tok2) * p.Hq + s.kv * p.G + rho2 - tok2 * p.G;
+            const float y0 = __uint_as_float(y.x), y1 = __uint_as_float(y.y), y2 = __uint_as_float(y.z),
+                        y3 = __uint_as_float(y.w);
+            const uint2 w = F16 || !a.out_f16 ? make_uint2(dev::pack_act<F16>(y0, y1), dev::pack_act<F16>(y2, y3))
+                                              : make_uint2(dev::pack_act2(y0, y1, true), dev::pack_act2(y2, y3, true));
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + o_row * D + dim) = w;
+          } else {
+            *reinterpret_cast<uint4*>(a.part + (slot + row) * D + dim) = y;
+          }
         }
       }
-      if (!whole_seg) slot_ml(cta, slot)[pr] = live ? make_float2(m_ref, l) : make_float2(-INFINITY, 0.f);
       fence_before();   // (the next segment's products write O and S)
       return true;
     });
+    if (issuer && !ok) {
+      // a wait gave up: the products in flight end before their memory goes
+      commit(el, dev::smem_u32(&drained[t]));
+      dev::mbar_wait_until(dev::smem_u32(&drained[t]), 0, dev::globaltimer_ns() + kWaitLimitNs);
+    }
   }
   if (!ok) *abort_v = 1;
   fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == kDecodeWarp) {
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
   }
-  if (*abort_v) return;
+  if (*abort_v) {
+    describe(PageShared{});
+    return;
+  }
 
-  // ---- segments shared with the CTAs before (0) and after (1)
-  long long seg0[2] = {-1, -1};
-  Seg seg[2];
-  {
+  // ---- the segment that goes on in the next CTA
+  if (warp == 0) {
+    PageShared x = {};
+    auto owner = [&](long long u) { return (int)(((u + 1) * ctas - 1) / units); };
     Seg s = first_seg;
     int j = first_block;
     for (long long u = c0; u < c1;) {
       const int je = (int)min((long long)s.nb, j + (c1 - u));
-      if (j > 0) {
-        seg0[0] = u - j;
-        seg[0] = s;
-      } else if (je < s.nb) {
-        seg0[1] = u;
-        seg[1] = s;
+      if (j == 0 && je < s.nb) {
+        x.parts = owner(u + s.nb - 1) - cta + 1;
+        x.row0 = s.row0;
+        x.R = s.R;
+        x.tile = s.tile;
+        x.kv = s.kv;
       }
       u += je - j;
       j = 0;
       if (u < c1) advance(s);
     }
-  }
-  if (seg0[0] < 0 && seg0[1] < 0) return;
-  auto owner = [&](long long u) { return (int)(((u + 1) * ctas - 1) / units); };
-  if (tid == 0) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      last_flag[i] = 0;
-      if (seg0[i] < 0) continue;
-      const int ca = owner(seg0[i]), cb = owner(seg0[i] + seg[i].nb - 1);
-      if (dev::atom_add_acq_rel(a.counters + ca, 1) == cb - ca) {
-        a.counters[ca] = 0;
-        last_flag[i] = 1;
-      }
-    }
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    if (!last_flag[i]) continue;
-    const Seg s = seg[i];
-    const int ca = owner(seg0[i]), parts = owner(seg0[i] + s.nb - 1) - ca + 1;
-    const int rows = min(kPairRows, s.R - kPairRows * s.tile);
-    // a warp takes four rows at a time, a lane 4 (2) dims of each: the parts'
-    // loads of all four are in flight together
-    constexpr int kPer = D / 32;
-    for (int r0 = 4 * warp; r0 < rows; r0 += 4 * (kThreads / 32)) {
-      float m[4], l[4], x[4][kPer];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        m[q] = -INFINITY;
-        l[q] = 0.f;
-#pragma unroll
-        for (int d = 0; d < kPer; ++d) x[q][d] = 0.f;
-      }
-#pragma unroll 2
-      for (int k = 0; k < parts; ++k) {
-        const float2* mls = slot_ml(ca + k, k == 0) + r0;
-        const float* os = slot_o(ca + k, k == 0) + (long long)r0 * D + kPer * lane;
-        float2 ml[4];
-        float y[4][kPer];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          ml[q] = __ldcg(mls + q);   // (the slots have whole tiles of rows)
-          if (kPer == 4) {
-            const float4 z = __ldcg(reinterpret_cast<const float4*>(os + q * D));
-            y[q][0] = z.x; y[q][1] = z.y; y[q][kPer - 2] = z.z; y[q][kPer - 1] = z.w;
-          } else {
-            const float2 z = __ldcg(reinterpret_cast<const float2*>(os + q * D));
-            y[q][0] = z.x; y[q][1] = z.y;
-          }
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          // (a part in which the row saw nothing counts as it is: zeros, or NaN)
-          const float m_new = fmaxf(m[q], ml[q].x);
-          const float old = m[q] == m_new ? 1.f : ex2_approx(m[q] - m_new);
-          const float w = ml[q].x == -INFINITY ? 1.f : ex2_approx(ml[q].x - m_new);
-          m[q] = m_new;
-          l[q] = fmaf(l[q], old, w * ml[q].y);
-#pragma unroll
-          for (int d = 0; d < kPer; ++d) x[q][d] = fmaf(x[q][d], old, w * y[q][d]);
-        }
-      }
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (r0 + q >= rows) break;
-        const float inv = l[q] == 0.f ? 0.f : 1.f / l[q];
-        const int rho = kPairRows * s.tile + r0 + q;
-        const int tok = (int)((uint32_t)rho / (uint32_t)p.G);
-        uint16_t* dst = static_cast<uint16_t*>(a.out) +
-                        ((long long)(s.row0 + tok) * p.Hq + s.kv * p.G + rho - tok * p.G) * D + kPer * lane;
-        uint32_t v[kPer / 2];
-#pragma unroll
-        for (int d = 0; d < kPer; d += 2)
-          v[d / 2] = F16 || !a.out_f16 ? dev::pack_act<F16>(x[q][d] * inv, x[q][d + 1] * inv)
-                                       : dev::pack_act2(x[q][d] * inv, x[q][d + 1] * inv, true);
-        if (kPer == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(v[0], v[kPer / 2 - 1]);
-        else *reinterpret_cast<uint32_t*>(dst) = v[0];
-      }
-    }
+    describe(x);
   }
 }
 

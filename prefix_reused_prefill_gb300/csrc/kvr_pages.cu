@@ -46,7 +46,7 @@ bool valid(const kvr_pages_config* c) {
 }
 
 struct Layout {
-  size_t status, info, count, counters, lens, cu, free_list, row_seq, row_pos, row_slot, table, rope, ml, part, ml_tc, part_tc, total;
+  size_t status, info, count, counters, lens, cu, free_list, row_seq, row_pos, row_slot, table, rope, ml, part, ml_tc, part_tc, shared, total;
   int width;
 };
 Layout layout(const kvr_pages_config* c) {
@@ -61,7 +61,7 @@ Layout layout(const kvr_pages_config* c) {
   // zeroed by kvr_pages_create, in one piece: status .. cu
   L.status = take(8);
   L.info = take(8);
-  L.counters = take(2 * kPageAttnMaxCtas * 4);
+  L.counters = take(kPageAttnMaxCtas * 4);
   L.lens = take((size_t)c->max_seqs * 4);
   L.cu = take((size_t)(c->max_seqs + 1) * 4);
   L.count = take(4);
@@ -75,6 +75,7 @@ Layout layout(const kvr_pages_config* c) {
   L.part = take((size_t)kPageAttnPartRows * c->head_dim * sizeof(float));
   L.ml_tc = take((size_t)kPageTcPartRows * sizeof(float2));
   L.part_tc = take((size_t)kPageTcPartRows * c->head_dim * sizeof(float));
+  L.shared = take((size_t)kPageAttnMaxCtas * sizeof(PageShared));
   L.total = at;
   return L;
 }
@@ -174,7 +175,7 @@ int kvr_pages_create(const kvr_pages_config* cfg, void* pool, size_t pool_bytes,
   memset(&c->attend_tc, 0, sizeof c->attend_tc);
   c->attend_tc.part = reinterpret_cast<float*>(w + L.part_tc);
   c->attend_tc.ml = reinterpret_cast<float2*>(w + L.ml_tc);
-  c->attend_tc.counters = c->attend.counters + kPageAttnMaxCtas;
+  c->attend_tc.shared = reinterpret_cast<PageShared*>(w + L.shared);
   int sms = 0;
   cudaError_t e = cudaGetDevice(&c->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, c->device);
@@ -300,9 +301,10 @@ int kvr_page_attend(kvr_pages* c, int layer, const void* q, long long q_stride, 
     b.scale_log2 = a.scale_log2;
     e = launch_page_attn_tc(d, b, c->ctas, st);
     if (e != cudaSuccess) return cuda_fail(c, e, "page attention launch");
+    a.shared = b.shared;
+    a.tc_part = b.part;
+    a.tc_ml = b.ml;
   }
-  // (one sequence with that many rows leaves nothing for the other kernel, but
-  // the rows of a captured plan may be fewer when it is replayed)
   e = launch_page_attn(d, a, std::min<long long>(most, kPageMany) <= 8 ? 1 : 2, c->ctas, st);
   return e == cudaSuccess ? KVR_OK : cuda_fail(c, e, "page attention launch");
 }
@@ -317,7 +319,7 @@ int kvr_pages_sync(kvr_pages* c, void* stream) {
   if (e == cudaSuccess && (word[0] || word[1])) {
     e = cudaMemsetAsync(c->dev.status, 0, 8, st);
     // a launch that gave up may have left arrivals behind
-    if (e == cudaSuccess && word[0]) e = cudaMemsetAsync(c->attend.counters, 0, 2 * kPageAttnMaxCtas * 4, st);
+    if (e == cudaSuccess && word[0]) e = cudaMemsetAsync(c->attend.counters, 0, kPageAttnMaxCtas * 4, st);
     if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   }
   if (e != cudaSuccess) return cuda_fail(c, e, "page status readback");

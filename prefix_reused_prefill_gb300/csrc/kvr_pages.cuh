@@ -83,7 +83,16 @@ struct PageAppend {
   float eps;
 };
 
-// Attention of the sequences with G * rows <= many (the split kernel).
+// A segment of the tensor-memory kernel (a sequence, pair of row tiles and KV
+// head) that several of its CTAs share: the first of them describes it.
+struct PageShared {
+  int parts;               // CTAs that share it, from this one on; 0: none
+  int row0, R, tile, kv;   // first row and G * rows of the sequence
+  int pad[3];
+};
+
+// Attention of the sequences with G * rows <= many (the split kernel).  The
+// same launch merges what the tensor-memory kernel left in parts before it.
 struct PageAttend {
   const void* q;
   long long qs;
@@ -95,6 +104,9 @@ struct PageAttend {
   float* part;       // partial outputs
   float2* ml;        // their (max in log2 units, sum)
   int* counters;     // arrivals, zero between launches
+  const PageShared* shared;   // [CTAs] of the tensor-memory kernel, null where it did not run
+  const float* tc_part;
+  const float2* tc_ml;
 };
 
 // ... and of the sequences with more (the tensor-memory kernel).
@@ -107,13 +119,16 @@ struct PageAttendTc {
   int many;
   int min_units;     // key blocks a CTA takes at least
   float scale_log2;
-  float* part;       // [CTAs][2][256 rows][d]
-  float2* ml;        // [CTAs][2][256 rows]
-  int* counters;     // arrivals, zero between launches
+  // parts of segments: [CTAs][2][256 rows], first the one that began in an
+  // earlier CTA, then the one that goes on in the next
+  float* part;       // [d]
+  float2* ml;        // (reference in log2 units, sum)
+  PageShared* shared;
 };
+constexpr int kPageTcRows = 256;
 
 constexpr int kPageAttnMaxCtas = 160;
-constexpr int kPageTcPartRows = kPageAttnMaxCtas * 2 * 256;
+constexpr int kPageTcPartRows = kPageAttnMaxCtas * 2 * kPageTcRows;
 // partial results of the split kernel, in rows: two tiles per warp (16 warps
 // with tiles of 8 rows, 8 warps with 16 rows) and two per CTA
 constexpr int kPageAttnPartRows = kPageAttnMaxCtas * (2 * 128 + 2 * 16);
