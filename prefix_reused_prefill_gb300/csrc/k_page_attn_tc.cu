@@ -549,26 +549,32 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
     const bool issuer = (warp & 7) == 0;
     const uint32_t el = elect();
     const uint32_t id_qk = idesc_f16(kTile, kKeys), id_pv = idesc_f16(kTile, D);
-    // S = Q K^T of block i of the run; both tiles free the K stage (frees = 2
-    // where there is one tile)
-    auto scores = [&](uint32_t i, int frees) {
+    // S = Q K^T of block i of the run; each tile frees the K stage
+    auto scores = [&](uint32_t i) {
       const uint64_t qd = sw128_desc(q_tile), kd = sw128_desc(k_base + (i & 1) * C::kKTile);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
         mma_ss(el, tmem + s_col(t), qd + (kk >> 2) * (C::kQAtom >> 4) + 2 * (kk & 3),
                kd + (kk >> 2) * (C::kKAtom >> 4) + 2 * (kk & 3), id_qk, kk > 0 ? 1u : 0u);
       commit(el, dev::smem_u32(&s_full[t]));
-      for (int x = 0; x < frees; ++x) commit(el, dev::smem_u32(&k_empty[i & 1]));
+      commit(el, dev::smem_u32(&k_empty[i & 1]));
     };
     // ok stays false once a wait gave up: the warp then skips its work but
     // still meets its partner at every barrier
     for_segments([&](const Seg& s, int j0, int j1) {
       const int rho0 = kPairRows * s.tile + kTile * t;
-      if (rho0 >= s.R) {                            // one tile only
-        it += j1 - j0;
+      if (rho0 >= s.R) {
+        // one tile only: the other's issuer passes every stage on unread.  (It
+        // must not run ahead: a phase is told by its parity, so a wait is good
+        // for the stage's present or next use only.)
+        for (int j = j0; issuer && j < j1 && ok; ++j, ++it) {
+          ok = all_wait(k_full[it & 1], it >> 1);
+          if (lane == 0 && ok) dev::mbar_arrive(dev::smem_u32(&k_empty[it & 1]));
+          ok = ok && all_wait(v_full[it & 1], it >> 1);
+          if (lane == 0 && ok) dev::mbar_arrive(dev::smem_u32(&v_empty[it & 1]));
+        }
         return true;
       }
-      const int frees = t == 0 && kPairRows * s.tile + kTile >= s.R ? 2 : 1;
       // every warp of the tile is done with the last segment: with the exchange
       // and with its part of the Q tile, which O went through
       named_sync(9 + t, 256);
@@ -620,7 +626,7 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
         if (issuer && ok) {
           ok = all_wait(q_full[t], segs) && all_wait(k_full[it & 1], it >> 1);
           fence_after();
-          if (ok) scores(it, frees);
+          if (ok) scores(it);
         }
         ++segs;
       }
@@ -725,12 +731,12 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
               mma_ts(el, tmem + o_col(t), tmem + s_col(t) + 64u * (kk >> 2) + 8u * (kk & 3),
                      vd + (kk >> 2) * (C::kVAtom >> 4) + 2 * (kk & 3), id_pv, (j > j0 || kk > 0) ? 1u : 0u);
             commit(el, dev::smem_u32(&pv_done[t]));
-            for (int x = 0; x < frees; ++x) commit(el, dev::smem_u32(&v_empty[it & 1]));
+            commit(el, dev::smem_u32(&v_empty[it & 1]));
             if (j + 1 < j1) {
               // the next scores go over P, which this product still reads
               ok = all_wait(k_full[(it + 1) & 1], (it + 1) >> 1) && all_wait(pv_done[t], blocks);
               fence_after();
-              if (ok) scores(it + 1, frees);
+              if (ok) scores(it + 1);
             }
           }
         }

@@ -321,6 +321,23 @@ def test_attend_rows(act, heads, kv_heads, d, keep, add):
     w.pg.kvr_pages_sync()
 
 
+@pytest.mark.parametrize("d,heads,kv_heads", [(64, 32, 8), (128, 16, 4)])
+@pytest.mark.parametrize("rows", [[20, 40], [40, 20], [17, 33, 100, 20], [30]])
+def test_attend_many_segments_in_a_run(d, heads, kv_heads, rows):
+    """More work than CTAs: a run goes through whole sequences with one and with two row tiles (80 and 160 rows of a
+    KV head), in either order, over several key blocks each."""
+    n = 36
+    w = World(heads, kv_heads, d, "bf16", seed=17, max_seqs=n, n_pages=n * 12, max_rows=n * 600, max_len=800)
+    keep = [300 + 37 * (b % 9) for b in range(n)]
+    add = [rows[b % len(rows)] for b in range(n)]
+    w.step([0] * n, keep)
+    w.step(keep, add)
+    q = w.q(1.5)
+    out = w.pg.kvr_page_attend(1, q.cuda())
+    w.pg.kvr_pages_sync()
+    w.check(q, out)
+
+
 def test_attend_peaked_flat_and_scaled():
     w = World(28, 4, 128, "bf16", seed=9)
     w.step([0, 0], [300, 140], k_scale=2.0)
