@@ -161,10 +161,15 @@ template <int D, bool F16>
 __device__ void merge_tc(const PagesDev& p, const PageAttend& a, int warp_id, int warps) {
   constexpr int kPer = D / 32, kGroups4 = kPageTcRows / 4;
   const int lane = threadIdx.x & 31, r0 = 4 * (warp_id % kGroups4);
-  for (int ca = warp_id / kGroups4; ca < (int)gridDim.x; ca += warps / kGroups4) {
+  // the segments that start in CTAs first, first + step, ..; a lane looks at each
+  const int first = warp_id / kGroups4, step = warps / kGroups4;
+  const int mine = first + step * lane;
+  uint32_t todo = __ballot_sync(0xffffffffu, mine < (int)gridDim.x && a.shared[mine].parts > 0);
+  for (; todo; todo &= todo - 1) {
+    const int ca = first + step * (__ffs(todo) - 1);
     const PageShared s = a.shared[ca];
     const int rows = min(kPageTcRows, s.R - kPageTcRows * s.tile);
-    if (s.parts == 0 || r0 >= rows) continue;
+    if (r0 >= rows) continue;
     float m[4], l[4], x[4][kPer];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -173,7 +178,7 @@ __device__ void merge_tc(const PagesDev& p, const PageAttend& a, int warp_id, in
 #pragma unroll
       for (int d = 0; d < kPer; ++d) x[q][d] = 0.f;
     }
-#pragma unroll 2
+#pragma unroll 4
     for (int k = 0; k < s.parts; ++k) {
       const long long at = ((long long)(ca + k) * 2 + (k == 0 ? 1 : 0)) * kPageTcRows + r0;
       float2 ml[4];

@@ -285,16 +285,21 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
   if (tid == 0) *abort_v = dev::status_set(p.status) ? 1 : 0;
 
   // ---- units before every sequence: a warp per sequence sums its pairs' blocks
+  // (the first sequences' values are asked for along with their number)
+  const int ahead = min(warp, p.max_seqs - 1);
+  const int ahead0 = p.cu[ahead], ahead1 = p.cu[ahead + 1], ahead_len = p.lens[ahead];
   const int n = p.info[0];
   const int rows_all = min(a.rows, p.info[1]);
-  auto load_seq = [&](int b, Seg& s) {
-    const int row0 = p.cu[b], row1 = p.cu[b + 1];
+  auto set_seq = [&](Seg& s, int b, int row0, int row1, int len) {
     s.b = b;
     s.row0 = row0;
     s.m = max(0, min(row1, rows_all) - row0);
-    s.len = p.lens[b];
-    s.P = s.len - (row1 - row0);
+    s.len = len;
+    s.P = len - (row1 - row0);
     s.R = p.G * s.m;
+  };
+  auto load_seq = [&](int b, Seg& s) {
+    set_seq(s, b, p.cu[b], p.cu[b + 1], p.lens[b]);
     return s.R > a.many;
   };
   auto blocks_of = [&](const Seg& s, int tile) {
@@ -304,7 +309,9 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
   for (int b = warp; b < n; b += kThreads / 32) {
     Seg s;
     long long u = 0;
-    if (load_seq(b, s))
+    if (b == warp) set_seq(s, b, ahead0, ahead1, ahead_len);
+    else load_seq(b, s);
+    if (s.R > a.many)
       for (int r = lane; r < (s.R + kPairRows - 1) / kPairRows; r += 32) u += blocks_of(s, r);
 #pragma unroll
     for (int d = 16; d; d >>= 1) u += __shfl_xor_sync(0xffffffffu, u, d);
@@ -337,12 +344,20 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
     describe(PageShared{});
     return;
   }
-  const int ctas = (int)min((long long)gridDim.x, (units + a.min_units - 1) / a.min_units);
+  const int ctas = units >= (long long)gridDim.x * a.min_units ? (int)gridDim.x
+                                                               : ((int)units + a.min_units - 1) / a.min_units;
   if (cta >= ctas) {
     describe(PageShared{});
     return;
   }
-  const long long c0 = units * cta / ctas, c1 = units * (cta + 1) / ctas;
+  // runs of `each` units, the first `odd` of them one longer
+  const long long each = units < (1ll << 31) ? (uint32_t)units / (uint32_t)ctas : units / ctas;
+  const int odd = (int)(units - each * ctas);
+  const long long c0 = each * cta + min(cta, odd), c1 = c0 + each + (cta < odd ? 1 : 0);
+  auto owner = [&](long long u) {
+    const long long longer = (each + 1) * odd;
+    return (int)(u < longer ? u / (each + 1) : odd + (u - longer) / each);
+  };
   // the segment that holds unit u, found by one warp
   auto locate = [&](long long u) {
     int lo = 0, hi = n;
@@ -583,19 +598,33 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
       const int tok = live ? (int)((uint32_t)rho / (uint32_t)p.G) : 0;
       float f;
       {
-        // q, scaled by a power of two with max|q| 2^e in [2^10, 2^11), as fp16
-        const uint16_t* src = static_cast<const uint16_t*>(a.q) + (long long)(s.row0 + tok) * a.qs +
-                              (s.kv * p.G + rho - tok * p.G) * D + D / 2 * h;
-        uint4 u[D / 16];
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-          u[c] = make_uint4(0, 0, 0, 0);
-          if (live) u[c] = *reinterpret_cast<const uint4*>(src + 8 * c);
+        // q, scaled by a power of two with max|q| 2^e in [2^10, 2^11), as fp16: as
+        // it is into the tile first, then in place.  (Short loops: code that runs
+        // once is paid for by its fetch from memory, 16 bytes an instruction.)
+        constexpr int kHalfChunks = D / 16;        // 16-byte chunks of half a row
+        const uint32_t atom = q_tile + (D == 128 ? h * C::kQAtom : 0);
+        const int first = D == 128 ? 0 : 4 * h;    // chunk within the 64 dims of an atom
+        // a warp's 32 half rows, whole lines at a time
+#pragma unroll 1
+        for (int i = 0; i < kHalfChunks; ++i) {
+          const int rr = 32 * (warp & 3) + 32 / kHalfChunks * i + lane / kHalfChunks, c = lane % kHalfChunks;
+          const int rho2 = min(rho0 + rr, s.R - 1);
+          const int tok2 = (int)((uint32_t)rho2 / (uint32_t)p.G);
+          const uint16_t* src = static_cast<const uint16_t*>(a.q) + (long long)(s.row0 + tok2) * a.qs +
+                                (s.kv * p.G + rho2 - tok2 * p.G) * D + D / 2 * h + 8 * c;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(atom + rr * 128 +
+                                                                             (((first + c) ^ (rr & 7)) << 4)),
+                       "l"(src), "r"(rho0 + rr < s.R ? 16 : 0)
+                       : "memory");
         }
+        asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+        __syncwarp();
+        const uint32_t row = atom + r * 128;
         float top = 0.f;
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-          const uint32_t x[4] = {u[c].x, u[c].y, u[c].z, u[c].w};
+#pragma unroll 2
+        for (int c = 0; c < kHalfChunks; ++c) {
+          const uint4 u = dev::lds128(row + (((first + c) ^ (r & 7)) << 4));
+          const uint32_t x[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float2 y = dev::act2<F16>(x[i]);
@@ -609,16 +638,17 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
         e = top > 0.f ? max(-100, min(100, e)) : 0;
         const float up = __uint_as_float((uint32_t)(127 + e) << 23);
         f = __uint_as_float((uint32_t)(127 - e) << 23) * a.scale_log2;
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-          uint32_t x[4] = {u[c].x, u[c].y, u[c].z, u[c].w};
+#pragma unroll 2
+        for (int c = 0; c < kHalfChunks; ++c) {
+          const uint32_t at = row + (((first + c) ^ (r & 7)) << 4);
+          const uint4 u = dev::lds128(at);
+          uint32_t x[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float2 y = dev::act2<F16>(x[i]);
             x[i] = dev::pack_act<true>(y.x * up, y.y * up);
           }
-          const int chunk = D / 16 * h + c;
-          sts128(q_tile + (chunk >> 3) * C::kQAtom + dev::swz128(r, chunk & 7), x[0], x[1], x[2], x[3]);
+          sts128(at, x[0], x[1], x[2], x[3]);
         }
         fence_smem();
         __syncwarp();
@@ -679,14 +709,11 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
         const bool whole = kKeys * (j + 1) <= all_see + 1;
         uint32_t pk[32];
         float sum = 0.f, top = -INFINITY;
-        auto form = [&]() {
-          if (!ok) return;
-          top = whole ? weights(j, std::false_type(), pk, sum) : weights(j, std::true_type(), pk, sum);
-        };
-        form();
-        // a row's score passed its reference by more than 2^8 (the first block
-        // of a segment always does)
-        if (any_of(pair, 64, ok && top > m_ref + kLazyMax)) {
+        for (;;) {
+          if (ok) top = whole ? weights(j, std::false_type(), pk, sum) : weights(j, std::true_type(), pk, sum);
+          // has a row's score passed its reference by more than 2^8?  (The first
+          // block of a segment always does; the second vote on a block never.)
+          if (!any_of(pair, 64, ok && top > m_ref + kLazyMax)) break;
           exchange[t][h][r] = top;
           named_sync(pair, 64);
           top = fmaxf(top, exchange[t][h ^ 1][r]);
@@ -710,7 +737,6 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
               }
             }
           }
-          form();
         }
         l += sum;
         if (ok) {
@@ -774,7 +800,7 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
                  __float_as_uint(__uint_as_float(x[4 * k + 3]) * inv));
         __syncwarp();
         constexpr int kLanes = kCols / 4;        // lanes of a row
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < kLanes; ++i) {
           const int rr = 32 / kLanes * i + lane / kLanes, k = lane % kLanes;
           const int row = 32 * (warp & 3) + rr, rho2 = rho0 + row;
@@ -818,7 +844,6 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
   // ---- the segment that goes on in the next CTA
   if (warp == 0) {
     PageShared x = {};
-    auto owner = [&](long long u) { return (int)(((u + 1) * ctas - 1) / units); };
     Seg s = first_seg;
     int j = first_block;
     for (long long u = c0; u < c1;) {
