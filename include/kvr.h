@@ -607,6 +607,29 @@ int kvr_page_read(kvr_pages* pages, int layer, void* k_out, void* v_out, int row
 int kvr_page_attend(kvr_pages* pages, int layer, const void* q, long long q_stride, void* out,
                     int out_f16, float scale, int rows, void* stream);
 
+/*
+ * The planned rows through a context's layer stack with K and V in pages
+ * instead of slots: per layer the QKV projection (rounded to bf16), append
+ * (norm_q, norm_k, rotation), attend, then the rest of the layer as in
+ * kvr_prefill_suffix.  The context's slots are neither read nor changed.
+ *   pages     its n_layers, heads and head_dim are the context's, its act is
+ *             KVR_ACT_BF16; rope_theta and norm_eps are the pages' own.
+ *   rows      the plan's; at most the context's max_rows.
+ *   hidden    device bf16 [rows][hidden]; rows behind the planned ones (a
+ *             padded batch) may hold anything and give outputs of no meaning.
+ *   norm_q, norm_k   host arrays of n_layers device pointers, each bf16
+ *             [head_dim] or null; the arrays may be null (no norms).
+ *   qkv       device bf16 [rows][(n_q_heads + 2 n_kv_heads) * head_dim],
+ *             16-byte aligned: working memory of the call.
+ *   out       device bf16 [rows][hidden].
+ * Errors are the context's (kvr_last_error).  As kvr_prefill_suffix the call
+ * is asynchronous; kvr_sync_status and kvr_pages_sync report what the device
+ * found.
+ */
+int kvr_prefill_pages(kvr_ctx* ctx, kvr_pages* pages, int rows, const void* hidden,
+                      const kvr_layer_weights* w, const void* const* norm_q, const void* const* norm_k,
+                      void* qkv, void* out, void* stream);
+
 /* Wait for `stream` and report what its calls could not: KVR_ERR_ARG or
  * KVR_ERR_CAPACITY for a plan that was refused on the device (see
  * kvr_page_plan; the first one since the last call), KVR_ERR_TIMEOUT for a

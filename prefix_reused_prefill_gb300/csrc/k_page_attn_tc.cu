@@ -121,22 +121,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-// two fp32 lanes in one instruction
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  unsigned long long r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(r)
-      : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)),
-        "l"(*reinterpret_cast<unsigned long long*>(&c)));
-  return *reinterpret_cast<float2*>(&r);
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  unsigned long long r;
-  asm("add.rn.f32x2 %0, %1, %2;"
-      : "=l"(r)
-      : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
-  return *reinterpret_cast<float2*>(&r);
-}
 __device__ __forceinline__ void ld32(uint32_t taddr, uint32_t* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
@@ -691,14 +675,14 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
           }
 #pragma unroll
           for (int k = 0; k < 8; k += 2) {
-            float2 e = fma2(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), f2, neg);
+            float2 e = dev::fma2(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), f2, neg);
             e.x = ex2_approx(e.x);
             e.y = ex2_approx(e.y);
-            part[(k >> 1) & 1] = add2(part[(k >> 1) & 1], e);
+            part[(k >> 1) & 1] = dev::add2(part[(k >> 1) & 1], e);
             pk[4 * c + k / 2] = dev::pack_act<true>(e.x, e.y);
           }
         }
-        part[0] = add2(part[0], part[1]);
+        part[0] = dev::add2(part[0], part[1]);
         sum = part[0].x + part[0].y;
         return fmaxf(mx[0], mx[1]) * f;
       };

@@ -19,6 +19,7 @@
 #include <cudaTypedefs.h>
 
 #include "kvr_internal.cuh"
+#include "kvr_pages.cuh"
 
 using namespace kvr;
 
@@ -441,6 +442,7 @@ struct Fused {
   const __nv_bfloat16* norm_gain = nullptr;  // Resid: RMSNorm the new rows into c->a
   float2* best = nullptr;                 // Argmax
   int fmt = -1;                           // WeightFmt; -1: the layers' format
+  int ldout = 0;                          // Cast: row stride of out (0: hidden)
 };
 
 // Small-m int4 passes: the GEMV with its fused epilogue.  A residual
@@ -501,7 +503,7 @@ int project_gemv_int4(kvr_ctx* c, cudaStream_t st, const Seg* segs, int nseg, co
   p.h = c->h;
   p.H = cfg.hidden;
   p.out = fz.out;
-  p.ldout = cfg.hidden;
+  p.ldout = fz.ldout ? fz.ldout : cfg.hidden;
   p.z = c->z;
   p.F = cfg.ffn;
   p.slot_stride = kv_offset(c, 1, 0, 0);
@@ -909,13 +911,51 @@ int run_pass(kvr_ctx* c, const RowMap& rows, const void* hidden, const kvr_layer
   return KVR_OK;
 }
 
+// K and V in pages instead of slots (kvr_prefill_pages)
+struct Paged {
+  kvr_pages* pages;
+  const void* const* norm_q;
+  const void* const* norm_k;
+  __nv_bfloat16* qkv;
+};
+
+// One layer's QKV projection, append and attention over pages: q, k and v leave
+// the projection as bf16 rows, append norms and rotates them, the attention
+// leaves its rows in c->o as the O projection wants them.
+int paged_layer(kvr_ctx* c, cudaStream_t st, const Paged& pg, const kvr_layer_weights& W, int l, int m) {
+  const kvr_config& k = c->cfg;
+  const int d = k.head_dim, qd = k.n_q_heads * d, kd = k.n_kv_heads * d, cols = qd + 2 * kd;
+  Seg segs[3] = {{W.wq, W.sq, qd}, {W.wk, W.sk, kd}, {W.wv, W.sv, kd}};
+  Fused fz;
+  fz.epi = kGemvEpiCast;
+  fz.out = pg.qkv;
+  fz.ldout = cols;
+  int rc = project(c, st, segs, 3, Act::A, k.hidden, m,
+                   [&](const float* part, long long plane, int ks, int ldo, int c0, int mb) {
+                     return launch_epi_cast(part, plane, ks, ldo, c0, mb, cols, pg.qkv, false, st);
+                   }, fz, /*swiglu=*/false, /*exact=*/true);
+  if (rc) return rc;
+  {
+    Timed t(c, kEpi, st);
+    rc = kvr_page_append(pg.pages, l, pg.qkv, cols, pg.qkv + qd, cols, pg.qkv + qd + kd, cols,
+                         pg.norm_q ? pg.norm_q[l] : nullptr, pg.norm_k ? pg.norm_k[l] : nullptr, 1, c->q, m, st);
+  }
+  if (rc) return fail(c, rc, "append: %s", kvr_pages_error(pg.pages));
+  {
+    Timed t(c, kAttn, st);
+    rc = kvr_page_attend(pg.pages, l, c->q, qd, c->o, c->act16 ? 1 : 0, 1.f / sqrtf((float)d), m, st);
+  }
+  return rc ? fail(c, rc, "attend: %s", kvr_pages_error(pg.pages)) : KVR_OK;
+}
+
 // The layer stack for the rows of one call.
 // out (bf16 [m][hidden]) may be null; head_gain: RMSNorm the last layer's rows
-// with it into c->a (the output head's input)
+// with it into c->a (the output head's input); pg: K and V in pages (rows then
+// only counts them)
 int run_stack(kvr_ctx* c, const RowMap& rows, const void* hidden,
               const kvr_layer_weights* w, void* out, cudaStream_t st,
-              const __nv_bfloat16* head_gain = nullptr) {
-  if (pass_fits(c, rows)) return run_pass(c, rows, hidden, w, out, st, head_gain);
+              const __nv_bfloat16* head_gain = nullptr, const Paged* pg = nullptr) {
+  if (!pg && pass_fits(c, rows)) return run_pass(c, rows, hidden, w, out, st, head_gain);
   const kvr_config& k = c->cfg;
   const int m = rows.m, H = k.hidden, d = k.head_dim;
   const int Hq = k.n_q_heads, Hkv = k.n_kv_heads, F = k.ffn;
@@ -941,8 +981,9 @@ int run_stack(kvr_ctx* c, const RowMap& rows, const void* hidden,
   for (int l = 0; l < k.n_layers; ++l) {
     const kvr_layer_weights& W = w[l];
     const bool last = l == k.n_layers - 1;
+    int rc = KVR_OK;
     // Q, K, V (+ RoPE, append)
-    {
+    if (!pg) {
       Seg segs[3] = {{W.wq, W.sq, Hq * d}, {W.wk, W.sk, Hkv * d}, {W.wv, W.sv, Hkv * d}};
       // K/V of slot 0 of this layer; each row adds its slot's stride
       const long long koff = kv_offset(c, 0, l, 0), voff = kv_offset(c, 0, l, 1);
@@ -952,15 +993,16 @@ int run_stack(kvr_ctx* c, const RowMap& rows, const void* hidden,
       fz.rows = &rows;
       fz.k_off = koff;
       fz.v_off = voff;
-      int rc = project(c, st, segs, 3, Act::A, H, m, [&](const float* part, long long plane, int ks,
+      rc = project(c, st, segs, 3, Act::A, H, m, [&](const float* part, long long plane, int ks,
                                                           int ldo, int c0, int mb) {
         return launch_epi_qkv(part, plane, ks, ldo, c0, mb, rows, Hq, Hkv, d, c->rope, c->q, arena,
                               koff, voff, sstride, k.capacity, st);
       }, fz, /*swiglu=*/false, /*exact=*/true);
       if (rc) return rc;
     }
-    int rc = KVR_OK;
-    if (!rows.batch) {
+    if (pg) {
+      rc = paged_layer(c, st, *pg, W, l, m);
+    } else if (!rows.batch) {
       rc = attention(c, st, rows.slot[0], l, rows);
     } else {
       // conversations with many rows take the tcgen05 kernel one by one; the
@@ -1747,6 +1789,39 @@ int kvr_verify_accept_batch(kvr_ctx* c, int n_seq, const int* slots, const int* 
     at += lens[j];
   }
   return KVR_OK;
+}
+
+int kvr_prefill_pages(kvr_ctx* c, kvr_pages* pages, int rows_n, const void* hidden, const kvr_layer_weights* w,
+                      const void* const* norm_q, const void* const* norm_k, void* qkv, void* out, void* stream) {
+  if (!c) return KVR_ERR_ARG;
+  if (!pages || !hidden || !qkv || !out) return fail(c, KVR_ERR_ARG, "null pages, hidden, qkv or out");
+  if (((uintptr_t)hidden & 15) || ((uintptr_t)out & 15) || ((uintptr_t)qkv & 15))
+    return fail(c, KVR_ERR_ARG, "hidden, qkv and out must be 16-byte aligned");
+  const kvr_config& k = c->cfg;
+  const kvr_pages_config& g = pages_config(pages);
+  if (g.n_layers != k.n_layers || g.n_q_heads != k.n_q_heads || g.n_kv_heads != k.n_kv_heads ||
+      g.head_dim != k.head_dim || g.act != KVR_ACT_BF16)
+    return fail(c, KVR_ERR_ARG, "the pages' layers, heads or activation type are not the context's");
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(c, e, "current device");
+  if (dev != pages_device(pages)) return fail(c, KVR_ERR_ARG, "the pages are on device %d", pages_device(pages));
+  if (rows_n != pages_rows(pages))
+    return fail(c, KVR_ERR_ARG, "%d rows, but the plan has %d", rows_n, pages_rows(pages));
+  if (rows_n > k.max_rows) return fail(c, KVR_ERR_CAPACITY, "%d rows exceed max_rows %d", rows_n, k.max_rows);
+  if (!weights_ok(c, w)) return fail(c, KVR_ERR_ARG, "missing or misaligned weight pointer");
+  for (const void* const* norms : {norm_q, norm_k})
+    for (int l = 0; norms && l < k.n_layers; ++l)
+      if ((uintptr_t)norms[l] & 15) return fail(c, KVR_ERR_ARG, "misaligned norm pointer");
+  if (c->fault == 2) return fail(c, KVR_ERR_FAULT, "injected launch fault");
+  if (rows_n == 0) return KVR_OK;
+  RowMap rows;
+  memset(&rows, 0, sizeof rows);
+  rows.m = rows_n;
+  rows.n_branch = 1;
+  rows.off[1] = rows_n;
+  const Paged pg = {pages, norm_q, norm_k, static_cast<__nv_bfloat16*>(qkv)};
+  return run_stack(c, rows, hidden, w, out, static_cast<cudaStream_t>(stream), nullptr, &pg);
 }
 
 int kvr_sync_status(kvr_ctx* c, void* stream) {

@@ -120,6 +120,10 @@ bool stride_ok(long long stride, long long row) { return stride >= row && stride
 
 }  // namespace
 
+const kvr_pages_config& kvr::pages_config(const kvr_pages* c) { return c->cfg; }
+int kvr::pages_device(const kvr_pages* c) { return c->device; }
+int kvr::pages_rows(const kvr_pages* c) { return c->rows; }
+
 extern "C" {
 
 size_t kvr_pages_pool_bytes(const kvr_pages_config* c) {

@@ -47,6 +47,11 @@ struct Chunk {
   }
 };
 
+// the handle's configuration, device and planned rows (kvr_pages.cu)
+const kvr_pages_config& pages_config(const kvr_pages* pages);
+int pages_device(const kvr_pages* pages);
+int pages_rows(const kvr_pages* pages);
+
 inline size_t page_chunk_bytes(int d) { return d == 128 ? Chunk<128>::kBytes : Chunk<64>::kBytes; }
 
 // What every kernel of the paged cache gets (device pointers of the work area).
@@ -154,6 +159,30 @@ namespace dev {
 
 // n / d for n < 2^32 / d, with mul = ceil(2^32 / d) (0 stands for d = 1)
 __device__ __forceinline__ int div_by(int n, uint32_t mul) { return mul ? (int)__umulhi((uint32_t)n, mul) : n; }
+
+// two fp32 lanes in one instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)),
+        "l"(*reinterpret_cast<unsigned long long*>(&c)));
+  return *reinterpret_cast<float2*>(&r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
+  return *reinterpret_cast<float2*>(&r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
+  return *reinterpret_cast<float2*>(&r);
+}
 
 // two activations of either 16-bit type
 template <bool F16>

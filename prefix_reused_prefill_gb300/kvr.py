@@ -34,7 +34,7 @@ EXPORTED = ["kvr_arena_bytes", "kvr_scratch_bytes", "kvr_ctx_create", "kvr_ctx_i
             "kvr_prefill_batch", "kvr_selftest_wait", "kvr_verify_accept_batch",
             "kvr_pages_pool_bytes", "kvr_pages_work_bytes", "kvr_pages_create", "kvr_pages_destroy",
             "kvr_pages_tables", "kvr_pages_sync", "kvr_pages_error", "kvr_page_plan", "kvr_page_append",
-            "kvr_page_read", "kvr_page_attend"]
+            "kvr_page_read", "kvr_page_attend", "kvr_prefill_pages"]
 
 
 class KvrError(RuntimeError):
@@ -131,6 +131,7 @@ def load_library(path: str = LIB_PATH):
         "kvr_page_plan": (I, [V, I, V, V, I, I, V]),
         "kvr_page_append": (I, [V, I, V, LL, V, LL, V, LL, V, V, I, V, I, V]),
         "kvr_page_read": (I, [V, I, V, V, I, V]),
+        "kvr_prefill_pages": (I, [V, V, I, V, P(KvrLayerWeights), P(V), P(V), V, V, V]),
         "kvr_page_attend": (I, [V, I, V, LL, V, I, ctypes.c_float, I, V]),
     }
     for name, (res, args) in sig.items():
@@ -412,6 +413,34 @@ class Kvr:
         self._check(self.lib.kvr_prefill_branches(self.ctx, slot, len(lens), lens_c, _i32(tokens),
                                                   hidden.data_ptr(), arr, out.data_ptr(),
                                                   self._stream(stream)))
+        return out
+
+    def kvr_prefill_pages(self, pages, hidden, weights, norm_q=None, norm_k=None, out=None, qkv=None,
+                          stream=None):
+        """The rows that ``pages`` (a PagedKv) has planned through the stack, their K and V in its pages.
+        norm_q, norm_k: per layer a bf16 [head_dim] gain; out and qkv may be given to be reused."""
+        c = self.cfg
+        arr = weights[0] if isinstance(weights, tuple) else weights
+        m, cols = hidden.shape[0], (c.n_q_heads + 2 * c.n_kv_heads) * c.head_dim
+        if qkv is None:
+            qkv = torch.empty((m, cols), dtype=torch.bfloat16, device=self.device)
+        if out is None:
+            out = torch.empty((m, c.hidden), dtype=torch.bfloat16, device=self.device)
+        for name, x, n in (("hidden", hidden, c.hidden), ("qkv", qkv, cols), ("out", out, c.hidden)):
+            if x.dtype != torch.bfloat16 or not x.is_cuda or not x.is_contiguous() or x.shape != (m, n):
+                raise KvrError(-1, f"{name} must be a contiguous bf16 device tensor [{m}][{n}]")
+
+        def gains(name, g):
+            if g is None:
+                return None
+            if len(g) != c.n_layers or any(x.dtype != torch.bfloat16 or not x.is_cuda or not x.is_contiguous()
+                                           or x.shape != (c.head_dim,) for x in g):
+                raise KvrError(-1, f"{name} must be {c.n_layers} bf16 device tensors [{c.head_dim}]")
+            return (ctypes.c_void_p * c.n_layers)(*[x.data_ptr() for x in g])
+
+        self._check(self.lib.kvr_prefill_pages(self.ctx, pages.ctx, m, hidden.data_ptr(), arr,
+                                               gains("norm_q", norm_q), gains("norm_k", norm_k), qkv.data_ptr(),
+                                               out.data_ptr(), self._stream(stream)))
         return out
 
     def kvr_sync_status(self, stream=None):
