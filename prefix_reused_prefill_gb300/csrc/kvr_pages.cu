@@ -26,9 +26,14 @@ struct kvr_pages {
 namespace {
 
 constexpr size_t kAlign = 256;
-// rows of a sequence and KV head (rows * group) up to which the split kernel
-// takes the sequence
-constexpr int kPageMany = 64;
+// Rows of a sequence and KV head (rows * group) up to which the split kernel
+// takes the sequence: 64 where every sequence of the step has so few (four
+// conversations of 8 rows, group 7, over 15k tokens: 60 us, 63 us by the
+// tensor-memory kernel), but 16 where that kernel runs anyway (12 conversations
+// of 1 to 120 rows, group 4, over up to 4k tokens: 33 us, 40 us with 64).
+constexpr int kPageMany = 64, kPageManyBeside = 16;
+// key blocks a CTA of the tensor-memory kernel takes at least: 254 rows over
+// 1668 tokens are flat from 1 to 5 (46 to 49 us), 55 us with 8
 constexpr int kPageMinUnits = 3;
 inline size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
@@ -288,8 +293,8 @@ int kvr_page_attend(kvr_pages* c, int layer, const void* q, long long q_stride, 
   a.out_f16 = out_f16 || d.f16;
   a.rows = rows;
   a.scale_log2 = (float)((double)scale * 1.4426950408889634);
-  a.many = kPageMany;
   const long long most = (long long)d.G * c->max_add;   // rows of a sequence and KV head, at most
+  a.many = most > kPageMany ? kPageManyBeside : kPageMany;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   OnDevice on(c->device);
   cudaError_t e = cudaSuccess;
@@ -300,7 +305,7 @@ int kvr_page_attend(kvr_pages* c, int layer, const void* q, long long q_stride, 
     b.out = out;
     b.out_f16 = a.out_f16;
     b.rows = rows;
-    b.many = kPageMany;
+    b.many = a.many;
     b.min_units = kPageMinUnits;
     b.scale_log2 = a.scale_log2;
     e = launch_page_attn_tc(d, b, c->ctas, st);
@@ -309,7 +314,7 @@ int kvr_page_attend(kvr_pages* c, int layer, const void* q, long long q_stride, 
     a.tc_part = b.part;
     a.tc_ml = b.ml;
   }
-  e = launch_page_attn(d, a, std::min<long long>(most, kPageMany) <= 8 ? 1 : 2, c->ctas, st);
+  e = launch_page_attn(d, a, std::min<long long>(most, a.many) <= 8 ? 1 : 2, c->ctas, st);
   return e == cudaSuccess ? KVR_OK : cuda_fail(c, e, "page attention launch");
 }
 

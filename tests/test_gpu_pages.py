@@ -13,7 +13,8 @@ Bounds, per element (u = half a step of the output type, 2^-9 relative for bf16'
   2^-13 for the scores here (|scale q k| <= 90, 2^-20 relative), the output is rounded once.  The values are summed
   in n / 16 + 2 fp32 additions that may each drop 2^-22 of the running sum, itself at most max|v|:
   (2 * 2^-11 + 2^-13) sum w|v| + n (2^-27 max|v| + 2^-24) + (n / 16 + 2) 2^-22 max|v| + eps/2 |o|.
-  Sequences with more than 64 rows of a KV head (the tensor-memory kernel) read k as fp16 too: c s has 14 bits, each
+  Sequences with many rows of a KV head (the tensor-memory kernel: more than 64, or more than 16 in a step where one has
+  more than 64) read k as fp16 too: c s has 14 bits, each
   rounded by at most 2^-11.  A score is off by the sum of d such errors times scale q_d: at most
   6 * 2^-11 scale |q k|_2 but for odds of 2 exp(-18) (Hoeffding), and a weight by twice that of its row's largest.
   There a weight is rounded once more (2^-11) when its row's reference moves within a block.
@@ -225,7 +226,7 @@ def test_append_in_place():
 
 
 # --------------------------------------------------------------------------- attend
-MANY = 64
+MANY, BESIDE = 64, 16
 
 
 def bound(n, mag, v, ref, u, spread=0.0):
@@ -277,7 +278,8 @@ class World:
                     k, v = self.k[b][:, :n], self.v[b][:, :n]
                     ref, mag = op.attend(qn[row], k, v, scale)
                     spread = 0.0
-                    if m * self.heads // self.kv_heads > MANY:
+                    group = self.heads // self.kv_heads
+                    if m * group > (BESIDE if self.rows * group > MANY else MANY):
                         kk = np.repeat(k, self.heads // self.kv_heads, axis=0)
                         spread = scale * np.sqrt(np.max((kk * qn[row][:, None]) ** 2 @ np.ones(self.d), axis=1))[:, None]
                     tol = bound(n, mag, v, ref, u, spread)
