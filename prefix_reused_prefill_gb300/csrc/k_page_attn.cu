@@ -29,8 +29,6 @@
 // arrive, in the order of the pages.  Where there are few segments, each of a
 // page or two per warp, a CTA takes a whole one instead: the second page costs
 // less than a merge across CTAs.
-#include <type_traits>
-
 #include "kvr_pages.cuh"
 
 namespace kvr {
@@ -63,10 +61,12 @@ __device__ __forceinline__ float ex2_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// d += a (16x16 fp16) * b (16x8 fp16)
+// d += a (16x16 fp16) * b (16x8 fp16).  (Not volatile, and the loads below are
+// ordinary ones: the compiler interleaves the products of several keys and dims
+// with the loads and decoding of the next.)
 __device__ __forceinline__ void mma(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -75,7 +75,7 @@ __device__ __forceinline__ void mma(float* d, uint32_t a0, uint32_t a1, uint32_t
 // d = a * b
 __device__ __forceinline__ void mma_first(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                           uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%10, %10, %10, %10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
@@ -114,24 +114,24 @@ __device__ __forceinline__ uint32_t centred_hi(uint32_t w, uint32_t k64) {
   return hadd2(and_or<0x00f000f0u>(w, k64), 0xd480d480u);     // 64 + c - 72
 }
 template <int W>
-__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t* w) {
+__device__ __forceinline__ void lds_words(const uint8_t* at, uint32_t* w) {
   if (W == 4) {
-    const uint4 v = dev::lds128(addr);
+    const uint4 v = *reinterpret_cast<const uint4*>(at);
     w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
   } else {
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+    const uint2 v = *reinterpret_cast<const uint2*>(at);
+    w[0] = v.x; w[1] = v.y;
   }
 }
 // the scales of one key's groups
 template <int W>
-__device__ __forceinline__ void lds_scales(uint32_t addr, float* s) {
+__device__ __forceinline__ void lds_scales(const uint8_t* at, float* s) {
   if (W == 4) {
-    uint32_t a, b;
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(addr));
-    const float2 x = dev::act2<true>(a), y = dev::act2<true>(b);
+    const uint2 v = *reinterpret_cast<const uint2*>(at);
+    const float2 x = dev::act2<true>(v.x), y = dev::act2<true>(v.y);
     s[0] = x.x; s[1] = x.y; s[2] = y.x; s[3] = y.y;
   } else {
-    const float2 x = dev::act2<true>(dev::lds32(addr));
+    const float2 x = dev::act2<true>(*reinterpret_cast<const uint32_t*>(at));
     s[0] = x.x; s[1] = x.y;
   }
 }
@@ -147,6 +147,27 @@ struct Place {
 struct Rec {
   int pages, tile, kv, row0, m;
 };
+
+template <int N>
+struct Vec {
+  float v[N];
+  float2 xy;
+};
+// N neighbouring floats, not from L1
+template <int N>
+__device__ __forceinline__ Vec<N> load_past_l1(const void* p) {
+  Vec<N> r;
+  if (N == 4) {
+    asm volatile("ld.relaxed.gpu.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(r.v[0]), "=f"(r.v[1]), "=f"(r.v[N - 2]), "=f"(r.v[N - 1])
+                 : "l"(p)
+                 : "memory");
+  } else {
+    asm volatile("ld.relaxed.gpu.v2.f32 {%0, %1}, [%2];" : "=f"(r.v[0]), "=f"(r.v[1]) : "l"(p) : "memory");
+  }
+  r.xy = make_float2(r.v[0], r.v[1]);
+  return r;
+}
 
 // a partial result: [rows of a tile][D] floats, and (m, l) per row
 struct Slot {
@@ -327,10 +348,12 @@ page_attn_kernel(const PagesDev p, const PageAttend a) {
   // else every warp gets a unit before another CTA is taken
   const int ctas = whole_segs ? segs : min((int)gridDim.x, (units + kWarps - 1) / kWarps);
   if (cta >= ctas) return;
-  const int c0 = whole_segs ? own[0] : (int)((long long)units * cta / ctas);
-  const int c1 = whole_segs ? own[1] : (int)((long long)units * (cta + 1) / ctas);
-  const int w0 = c0 + (int)((long long)(c1 - c0) * warp / kWarps);
-  const int w1 = c0 + (int)((long long)(c1 - c0) * (warp + 1) / kWarps);
+  // runs of `each` units, the first `odd` CTAs' one longer
+  const int each = (int)((uint32_t)units / (uint32_t)ctas), odd = units - each * ctas;
+  const int c0 = whole_segs ? own[0] : each * cta + min(cta, odd);
+  const int c1 = whole_segs ? own[1] : c0 + each + (cta < odd ? 1 : 0);
+  const int w0 = c0 + (c1 - c0) * warp / kWarps;   // (a run has less than 2^27 units)
+  const int w1 = c0 + (c1 - c0) * (warp + 1) / kWarps;
 
   auto place_of = [&](int u) {
     int lo = 0, hi = n;
@@ -352,6 +375,17 @@ page_attn_kernel(const PagesDev p, const PageAttend a) {
     s.tile = dev::div_by(seg, p.mul_hkv);
     s.kv = seg - s.tile * p.Hkv;
     return s;
+  };
+  // the next segment
+  auto advance = [&](Place& s) {
+    s.page = 0;
+    if (++s.kv < p.Hkv) return;
+    s.kv = 0;
+    if (C::kRows * ++s.tile < p.G * s.m) return;
+    int u = first_unit[s.b + 1];
+    do ++s.b;
+    while (first_unit[s.b + 1] == u);
+    s = place_of(u);
   };
   // row r of a tile: its token in the sequence and head in the group
   auto token_of = [&](int rho) { return dev::div_by(rho, p.mul_g); };
@@ -389,35 +423,35 @@ page_attn_kernel(const PagesDev p, const PageAttend a) {
     const uint32_t ring = dev::smem_u32(smem) + warp * C::kRing;
     const uint32_t bars = dev::smem_u32(&full_bar[warp][0]);
     const uint8_t* layer = p.pool + p.layer_off;
-    // offsets of the next 32 units to fetch, one per lane
-    long long src = 0;
-    int queued = 0;                       // first unit past the queue, from w0
+    // chunks (page * KV heads + head) of the next 32 units to fetch, one per lane
+    int src = 0;
     const int halves = 2 * (w1 - w0);
-    int issued = 0, stage_in = 0;         // halves requested, and the stage of the next
+    int issued = 0;                       // halves requested
+    uint32_t stage_in = 0;                // the stage of the next one, and its offset in the ring
     auto issue = [&]() {
-      if (issued >> 1 == queued) {
-        const int u = w0 + queued + lane;
+      if ((issued & 63) == 0) {
+        const int u = w0 + (issued >> 1) + lane;
         if (u < w1) {
           const Place s = place_of(u);
-          src = ((long long)p.table[(long long)s.b * p.width + s.page] * p.Hkv + s.kv) * K::kBytes;
+          src = p.table[(long long)s.b * p.width + s.page] * p.Hkv + s.kv;
         }
-        queued += 32;
       }
-      const long long off = __shfl_sync(0xffffffffu, src, (issued >> 1) & 31) + (issued & 1) * C::kHalf;
+      const uint8_t* from =
+          layer + (long long)__shfl_sync(0xffffffffu, src, (issued >> 1) & 31) * K::kBytes + (issued & 1) * C::kHalf;
       if (lane == 0) {
         dev::mbar_arrive_expect_tx(bars + 8 * stage_in, C::kHalf);
-        bulk_load(ring + stage_in * C::kHalf, layer + off, C::kHalf, bars + 8 * stage_in);
+        bulk_load(ring + stage_in * C::kHalf, from, C::kHalf, bars + 8 * stage_in);
       }
       ++issued;
-      if (++stage_in == C::kStages) stage_in = 0;
+      stage_in = stage_in + 1 == C::kStages ? 0 : stage_in + 1;
     };
     while (issued < halves && issued < C::kStages) issue();
     // the next half to use: its stage and the parity of that stage's phase
-    int stage = 0;
-    uint32_t parity = 0;
+    uint32_t stage = 0, parity = 0;
     auto arrived = [&]() {
+      if (__all_sync(0xffffffffu, dev::mbar_try_wait(bars + 8 * stage, parity))) return true;
       const bool got = dev::mbar_wait(bars + 8 * stage, parity, p.status) && !*abort_v;
-      return __all_sync(0xffffffffu, got);
+      return (bool)__all_sync(0xffffffffu, got);
     };
     auto used = [&]() {
       __syncwarp();
@@ -449,13 +483,13 @@ page_attn_kernel(const PagesDev p, const PageAttend a) {
         if (rho < p.G * at.m) raw[j] = *reinterpret_cast<const uint4*>(src_q + 32 * j);
       }
     };
-    // one page; kMasked: some row of the tile does not see all of it
-    auto page_step = [&](auto masked) {
-      constexpr bool kMasked = decltype(masked)::value;
-      if (!arrived()) return false;
-      uint32_t page = ring + stage * C::kHalf;
+    // one page
+    auto page_step = [&]() {
       const int key_base = s.page * kPage;
-
+      // every row of the tile sees the whole page?
+      const bool whole = key_base + kPage <= s.P + 1;
+      if (!arrived()) return false;
+      const uint8_t* page = smem + warp * C::kRing + stage * C::kHalf;
       // ---- scores of 64 keys
       float sc[4][NT][4];
 #pragma unroll
@@ -473,8 +507,10 @@ page_attn_kernel(const PagesDev p, const PageAttend a) {
 #pragma unroll
         for (int j = 0; j < kG; ++j) {
           const uint32_t x0 = w0k[j], x1 = w1k[j], y0 = x0 >> 8, y1 = x1 >> 8;
-          const uint32_t a0 = centred_lo(x0, k1024), a1 = centred_lo(x1, k1024), a2 = centred_hi(x0, k64), a3 = centred_hi(x1, k64);
-          const uint32_t b0 = centred_lo(y0, k1024), b1 = centred_lo(y1, k1024), b2 = centred_hi(y0, k64), b3 = centred_hi(y1, k64);
+          const uint32_t a0 = centred_lo(x0, k1024), a1 = centred_lo(x1, k1024), a2 = centred_hi(x0, k64),
+                         a3 = centred_hi(x1, k64);
+          const uint32_t b0 = centred_lo(y0, k1024), b1 = centred_lo(y1, k1024), b2 = centred_hi(y0, k64),
+                         b3 = centred_hi(y1, k64);
 #pragma unroll
           for (int nn = 0; nn < NT; ++nn) {
             float acc[4];
@@ -488,6 +524,15 @@ page_attn_kernel(const PagesDev p, const PageAttend a) {
         }
       }
       used();
+      if (!whole) {
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+          for (int nn = 0; nn < NT; ++nn)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if (key_base + 16 * mt + g + 8 * (c >> 1) > see[nn][c & 1]) sc[mt][nn][c] = -INFINITY;
+      }
       // ---- running maximum and weights
       uint32_t pw[4][NT][2];
 #pragma unroll
@@ -497,10 +542,7 @@ page_attn_kernel(const PagesDev p, const PageAttend a) {
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            if (kMasked && key_base + 16 * mt + g + 8 * (c >> 1) > see[nn][c & 1]) sc[mt][nn][c] = -INFINITY;
-            mx[c & 1] = fmaxf(mx[c & 1], sc[mt][nn][c]);
-          }
+          for (int c = 0; c < 4; ++c) mx[c & 1] = fmaxf(mx[c & 1], sc[mt][nn][c]);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
 #pragma unroll
@@ -513,7 +555,7 @@ page_attn_kernel(const PagesDev p, const PageAttend a) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             const float m_new = fmaxf(m_run[nn][c], mx[c]);
-            corr[c] = m_run[nn][c] == -INFINITY ? 0.f : exp2f(m_run[nn][c] - m_new);
+            corr[c] = m_run[nn][c] == -INFINITY ? 0.f : ex2_approx(m_run[nn][c] - m_new);
             m_run[nn][c] = m_new;
             l_run[nn][c] *= corr[c];
           }
@@ -540,7 +582,7 @@ page_attn_kernel(const PagesDev p, const PageAttend a) {
       }
       // ---- weighted values
       if (!arrived()) return false;
-      page = ring + stage * C::kHalf - C::kHalf;   // (the V half's offsets count from the page)
+      page = smem + warp * C::kRing + stage * C::kHalf - C::kHalf;   // (the V half's offsets count from the page)
 #pragma unroll
       for (int mt = 0; mt < 4; ++mt) {
         uint32_t v0[kG], v1[kG], s0[kG], s1[kG];
@@ -548,23 +590,40 @@ page_attn_kernel(const PagesDev p, const PageAttend a) {
         lds_words<kG>(page + K::kV + (((2 * mt + 1) * 8 + g) * 4 + t) * kG * 4, v1);
         lds_words<kG>(page + K::kVs + ((mt * 4 + t) * 2 + 0) * kG * 4, s0);
         lds_words<kG>(page + K::kVs + ((mt * 4 + t) * 2 + 1) * kG * 4, s1);
+        uint32_t b0[kG][NT], b1[kG][NT];
+#pragma unroll
+        for (int nn = 0; nn < NT; ++nn)
+#pragma unroll
+          for (int j = 0; j < kG; ++j) {
+            b0[j][nn] = hmul2(pw[mt][nn][0], s0[j]);
+            b1[j][nn] = hmul2(pw[mt][nn][1], s1[j]);
+          }
+        if (!whole) {
+          // a weight of zero takes nothing, whatever stands in a place behind the
+          // row's last key (an unwritten scale, a NaN)
+#pragma unroll
+          for (int nn = 0; nn < NT; ++nn) {
+            const uint32_t p0 = pw[mt][nn][0], p1 = pw[mt][nn][1];
+            const uint32_t keep0 = ((p0 & 0xffffu) ? 0xffffu : 0u) | ((p0 >> 16) ? 0xffff0000u : 0u);
+            const uint32_t keep1 = ((p1 & 0xffffu) ? 0xffffu : 0u) | ((p1 >> 16) ? 0xffff0000u : 0u);
+#pragma unroll
+            for (int j = 0; j < kG; ++j) {
+              b0[j][nn] &= keep0;
+              b1[j][nn] &= keep1;
+            }
+          }
+        }
 #pragma unroll
         for (int j = 0; j < kG; ++j) {
           const uint32_t x0 = v0[j], x1 = v1[j], y0 = x0 >> 8, y1 = x1 >> 8;
-          const uint32_t e0 = centred_lo(x0, k1024), e1 = centred_hi(x0, k64), e2 = centred_lo(x1, k1024), e3 = centred_hi(x1, k64);
-          const uint32_t f0 = centred_lo(y0, k1024), f1 = centred_hi(y0, k64), f2 = centred_lo(y1, k1024), f3 = centred_hi(y1, k64);
+          const uint32_t e0 = centred_lo(x0, k1024), e1 = centred_hi(x0, k64), e2 = centred_lo(x1, k1024),
+                         e3 = centred_hi(x1, k64);
+          const uint32_t f0 = centred_lo(y0, k1024), f1 = centred_hi(y0, k64), f2 = centred_lo(y1, k1024),
+                         f3 = centred_hi(y1, k64);
 #pragma unroll
           for (int nn = 0; nn < NT; ++nn) {
-            uint32_t b0 = hmul2(pw[mt][nn][0], s0[j]), b1 = hmul2(pw[mt][nn][1], s1[j]);
-            if (kMasked) {
-              // a weight of zero takes nothing, whatever stands in a place
-              // behind the row's last key (an unwritten scale, a NaN)
-              const uint32_t p0 = pw[mt][nn][0], p1 = pw[mt][nn][1];
-              b0 &= ((p0 & 0xffffu) ? 0xffffu : 0u) | ((p0 >> 16) ? 0xffff0000u : 0u);
-              b1 &= ((p1 & 0xffffu) ? 0xffffu : 0u) | ((p1 >> 16) ? 0xffff0000u : 0u);
-            }
-            mma(o[nn][2 * j], e0, e1, e2, e3, b0, b1);
-            mma(o[nn][2 * j + 1], f0, f1, f2, f3, b0, b1);
+            mma(o[nn][2 * j], e0, e1, e2, e3, b0[j][nn], b1[j][nn]);
+            mma(o[nn][2 * j + 1], f0, f1, f2, f3, b0[j][nn], b1[j][nn]);
           }
         }
       }
@@ -621,8 +680,7 @@ page_attn_kernel(const PagesDev p, const PageAttend a) {
             for (int c = 0; c < 4; ++c) o[nn][i][c] = 0.f;
         }
       }
-      // every row of the tile sees the whole page
-      ok = (s.page + 1) * kPage <= s.P + 1 ? page_step(std::false_type()) : page_step(std::true_type());
+      ok = page_step();
       if (!ok) break;
 
       // ---- the end of the segment or of the run
@@ -671,7 +729,7 @@ page_attn_kernel(const PagesDev p, const PageAttend a) {
           }
         }
         fresh = true;
-        if (u + 1 < w1) s = place_of(u + 1);
+        if (u + 1 < w1) advance(s);
       } else {
         ++s.page;
       }
@@ -680,7 +738,7 @@ page_attn_kernel(const PagesDev p, const PageAttend a) {
       // a wait gave up: the copies in flight still land in this CTA's memory
       *abort_v = 1;
       const unsigned long long deadline = dev::globaltimer_ns() + kWaitLimitNs;
-      for (int st = 0; st < C::kStages && st < issued; ++st) {
+      for (int st = 0; st < (int)C::kStages && st < issued; ++st) {
         const int last = (issued - 1 - st) / C::kStages;
         dev::mbar_wait_until(bars + 8 * st, (uint32_t)last & 1, deadline);
       }
@@ -689,37 +747,11 @@ page_attn_kernel(const PagesDev p, const PageAttend a) {
   __syncthreads();
   if (*abort_v) return;
 
-  // ---- merge the warps' parts, then the CTAs': `count` parts given by
-  // slot(i); element (row r, dims d .. d + 3)
-  auto merge = [&](int r, int d, int count, auto slot, auto load2, auto load4, auto done) {
-    float m = -INFINITY;
-#pragma unroll 8
-    for (int i = 0; i < count; ++i) m = fmaxf(m, load2(slot(i).ml + r).x);
-    float l = 0.f;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int i = 0; i < count; ++i) {
-      const Slot s = slot(i);
-      const float2 ml = load2(s.ml + r);
-      const float4 y = load4(reinterpret_cast<const float4*>(s.o + r * D + d));
-      // a part in which the row saw nothing (m = -inf, or -inf throughout
-      // because its scores are NaN) counts its sum and its values as they are
-      const float w = ml.x == -INFINITY ? 1.f : ex2_approx(ml.x - m);
-      l = fmaf(w, ml.y, l);
-      x.x = fmaf(w, y.x, x.x);
-      x.y = fmaf(w, y.y, x.y);
-      x.z = fmaf(w, y.z, x.z);
-      x.w = fmaf(w, y.w, x.w);
-    }
-    done(x, m, l);
+  // ---- merge the warps' parts, then the CTAs'
+  auto owner = [&](int u) {
+    const int longer = (each + 1) * odd;
+    return u < longer ? u / (each + 1) : odd + (u - longer) / each;
   };
-  auto finish = [&](const Rec& s, int r, int d, float4 x, float l) {
-    const long long row = out_row(s.tile, s.kv, s.row0, s.m, r);
-    if (row < 0) return;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    store4(row, d, x.x * inv, x.y * inv, x.z * inv, x.w * inv);
-  };
-  auto owner = [&](int u) { return (int)(((long long)(u + 1) * ctas - 1) / units); };
   // the filled records in order, and the first record of each segment
   static_assert(2 * kWarps <= 32, "one record per lane");
   if (warp == 0) {
@@ -739,65 +771,83 @@ page_attn_kernel(const PagesDev p, const PageAttend a) {
     }
   }
   __syncthreads();
-  constexpr int kElems = C::kRows * (D / 4);
-  const int n_seg = seg_count;
-  for (int i = tid; i < n_seg * kElems; i += kThreads) {
-    const int k = i / kElems, r = i % kElems / (D / 4), d = 4 * (i % (D / 4));
-    const int first = seg_at[k], seg0 = rec_seg[rec_list[first]];
-    const Rec s = rec_of[rec_list[first]];
-    const bool local = seg0 >= c0 && seg0 + s.pages <= c1;
-    merge(
-        r, d, seg_at[k + 1] - first, [&](int j) { return warp_slot(rec_list[first + j]); },
-        [](const float2* x) { return *x; }, [](const float4* x) { return *x; },
-        [&](float4 x, float m, float l) {
-          if (local) {
-            finish(s, r, d, x, l);
-          } else {
-            // the CTA that holds the segment's first unit leaves its part in its
-            // second slot, the others in their first
-            const Slot out = cta_slot(cta, seg0 >= c0 ? 1 : 0);
-            *reinterpret_cast<float4*>(out.o + r * D + d) = x;
-            if (d == 0) out.ml[r] = make_float2(m, l);
-          }
-        });
-  }
-  if (n_seg == 0) return;
-  // segments shared with the CTAs before (0) and after (1)
-  int shared_seg[2] = {-1, -1};
-  Rec shared_rec[2];
+  int jobs = seg_count;
+  if (jobs == 0) return;
+  // Round 0: the CTA's own parts of each segment, to the output or, where other
+  // CTAs share it (the first and the last segment at most), to the work area.
+  // Round 1: what the last CTA to arrive finds there.  A warp takes a row, a lane
+  // D / 32 dims of it.  (Reads go past L1: other CTAs wrote some of them.)
+#pragma unroll 1
+  for (int round = 0;; ++round) {
+#pragma unroll 1
+    for (int x = warp; x < jobs * C::kRows; x += kWarps) {
+      const int k = x / C::kRows, r = x % C::kRows;
+      if (round && !last_flag[k]) continue;
+      const int first = seg_at[round && k ? seg_count - 1 : k], at = rec_list[first], seg0 = rec_seg[at];
+      const Rec s = rec_of[at];
+      const bool local = seg0 >= c0 && seg0 + s.pages <= c1;
+      const int ca = round ? owner(seg0) : 0;
+      const int count = round ? owner(seg0 + s.pages - 1) - ca + 1 : seg_at[k + 1] - first;
+      constexpr int kPer = D / 32;
+      float m = -INFINITY, l = 0.f, o[kPer];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int at = rec_list[seg_at[i == 0 ? 0 : n_seg - 1]];
-    const int seg0 = rec_seg[at];
-    shared_rec[i] = rec_of[at];
-    if (i == 0 ? seg0 < c0 : (seg0 >= c0 && seg0 + shared_rec[i].pages > c1)) shared_seg[i] = seg0;
-  }
-  if (shared_seg[0] < 0 && shared_seg[1] < 0) return;
-  __syncthreads();   // (the add below releases what the CTA wrote)
-  if (tid % 32 == 0 && tid / 32 < 2) {
-    const int i = tid / 32, seg0 = shared_seg[i];
-    last_flag[i] = 0;
-    if (seg0 >= 0) {
-      const int ca = owner(seg0), cb = owner(seg0 + shared_rec[i].pages - 1);
-      if (dev::atom_add_acq_rel(a.counters + ca, 1) == cb - ca) {
-        a.counters[ca] = 0;
-        last_flag[i] = 1;
+      for (int d = 0; d < kPer; ++d) o[d] = 0.f;
+#pragma unroll 8
+      for (int i = 0; i < count; ++i) {
+        // (the CTA that holds a segment's first unit leaves its part in its
+        // second slot, the others in their first)
+        const Slot sl = round ? cta_slot(ca + i, i == 0 ? 1 : 0) : warp_slot(rec_list[first + i]);
+        const float2 ml = load_past_l1<2>(sl.ml + r).xy;
+        const Vec<kPer> y = load_past_l1<kPer>(sl.o + r * D + kPer * lane);
+        // a part in which the row saw nothing (m = -inf, or -inf throughout
+        // because its scores are NaN) counts its sum and its values as they are
+        const float m_new = fmaxf(m, ml.x);
+        const float old = m == m_new ? 1.f : ex2_approx(m - m_new);
+        const float w = ml.x == -INFINITY ? 1.f : ex2_approx(ml.x - m_new);
+        m = m_new;
+        l = fmaf(l, old, w * ml.y);
+#pragma unroll
+        for (int d = 0; d < kPer; ++d) o[d] = fmaf(o[d], old, w * y.v[d]);
+      }
+      if (round || local) {
+        const long long row = out_row(s.tile, s.kv, s.row0, s.m, r);
+        if (row < 0) continue;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        uint16_t* dst = static_cast<uint16_t*>(a.out) + row * D + kPer * lane;
+#pragma unroll
+        for (int d = 0; d < kPer; d += 2)
+          reinterpret_cast<uint32_t*>(dst)[d / 2] = F16 || !a.out_f16
+                                                        ? dev::pack_act<F16>(o[d] * inv, o[d + 1] * inv)
+                                                        : dev::pack_act2(o[d] * inv, o[d + 1] * inv, true);
+      } else {
+        const Slot out = cta_slot(cta, seg0 >= c0 ? 1 : 0);
+#pragma unroll
+        for (int d = 0; d < kPer; ++d) out.o[r * D + kPer * lane + d] = o[d];
+        if (lane == 0) out.ml[r] = make_float2(m, l);
       }
     }
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    if (!last_flag[i]) continue;
-    const Rec s = shared_rec[i];
-    const int ca = owner(shared_seg[i]), cb = owner(shared_seg[i] + s.pages - 1);
-    for (int e = tid; e < kElems; e += kThreads) {
-      const int r = e / (D / 4), d = 4 * (e % (D / 4));
-      merge(
-          r, d, cb - ca + 1, [&](int k) { return cta_slot(ca + k, k == 0 ? 1 : 0); },
-          [](const float2* x) { return __ldcg(x); }, [](const float4* x) { return __ldcg(x); },
-          [&](float4 x, float m, float l) { finish(s, r, d, x, l); });
+    if (round) return;
+    // the first segment may have begun in an earlier CTA, the last may go on in
+    // the next (one that does both counts as the first)
+    const int s_first = rec_seg[rec_list[0]], s_last = rec_seg[rec_list[seg_at[seg_count - 1]]];
+    const bool with_before = s_first < c0;
+    const bool with_after = s_last >= c0 && s_last + rec_of[rec_list[seg_at[seg_count - 1]]].pages > c1;
+    if (!with_before && !with_after) return;
+    __syncthreads();   // (the add below releases what the CTA wrote)
+    if (tid < 2) {
+      last_flag[tid] = 0;
+      if (tid ? with_after : with_before) {
+        const int seg0 = tid ? s_last : s_first;
+        const int ca = owner(seg0), cb = owner(seg0 + rec_of[rec_list[tid ? seg_at[seg_count - 1] : 0]].pages - 1);
+        if (dev::atom_add_acq_rel(a.counters + ca, 1) == cb - ca) {
+          a.counters[ca] = 0;
+          last_flag[tid] = 1;
+        }
+      }
     }
+    __syncthreads();
+    if (!last_flag[0] && !last_flag[1]) return;
+    jobs = 2;
   }
 }
 

@@ -17,7 +17,6 @@ Bounds, per element (u = half a step of the output type, 2^-9 relative for bf16'
   more than 64) read k as fp16 too: c s has 14 bits, each
   rounded by at most 2^-11.  A score is off by the sum of d such errors times scale q_d: at most
   6 * 2^-11 scale |q k|_2 but for odds of 2 exp(-18) (Hoeffding), and a weight by twice that of its row's largest.
-  There a weight is rounded once more (2^-11) when its row's reference moves within a block.
 """
 import numpy as np
 import pytest
@@ -232,8 +231,7 @@ MANY, BESIDE = 64, 16
 def bound(n, mag, v, ref, u, spread=0.0):
     """spread: the largest scale |q k|_2 of each head [heads][1], for rows whose k is rounded."""
     top = np.abs(v).max()
-    more = 2.0 ** -11 * (12 * spread + 1) if np.any(spread) else 0.0
-    return ((2 * 2.0 ** -11 + 2.0 ** -13 + more) * mag + n * (2.0 ** -27 * top + 2.0 ** -24)
+    return ((2 * 2.0 ** -11 + 2.0 ** -13 + 12 * 2.0 ** -11 * spread) * mag + n * (2.0 ** -27 * top + 2.0 ** -24)
             + (n / 16 + 2) * 2.0 ** -22 * top + u * np.abs(ref))
 
 
