@@ -222,14 +222,21 @@ cudaError_t launch_page_plan(const PagesDev& p, int n_seq, const int32_t* keep, 
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = (size_t)6 * n_seq * sizeof(int);
   cfg.stream = st;
+  // (a launch of one CTA is a cluster of one without being told so)
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ctas;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  int n_attr = 0;
+  if (pdl_enabled()) {
+    attr[n_attr].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n_attr++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (ctas > 1) {
+    attr[n_attr].id = cudaLaunchAttributeClusterDimension;
+    attr[n_attr].val.clusterDim.x = ctas;
+    attr[n_attr].val.clusterDim.y = attr[n_attr].val.clusterDim.z = 1;
+    ++n_attr;
+  }
   cfg.attrs = attr;
-  cfg.numAttrs = pdl_enabled() ? 2 : 1;
+  cfg.numAttrs = n_attr;
   return cudaLaunchKernelEx(&cfg, page_plan_kernel, p, n_seq, keep, add, rows, max_add);
 }
 

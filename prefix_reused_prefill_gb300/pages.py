@@ -23,6 +23,7 @@ import torch
 from .kvr import KVR_OK, KvrError, KvrPagesConfig, KvrPageTables, load_library
 
 PAGE_TOKENS = 64
+_raw_stream = torch._C._cuda_getCurrentRawStream   # the current stream's handle (a Stream object costs 2 us)
 _ACTS = {"bf16": (0, torch.bfloat16), "fp16": (1, torch.float16)}
 
 
@@ -99,8 +100,7 @@ class PagedKv:
             raise KvrError(rc, self.lib.kvr_pages_error(self.ctx).decode())
 
     def _stream(self, stream):
-        # (the raw handle: a Stream object costs 2 us)
-        return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(self._index)
+        return stream.cuda_stream if stream is not None else _raw_stream(self._index)
 
     def _rows_arg(self, name: str, x: torch.Tensor, heads: int) -> int:
         """Row stride of x [rows][heads][head_dim], the heads of a row contiguous."""
@@ -136,13 +136,15 @@ class PagedKv:
     def kvr_page_plan(self, keep: torch.Tensor, add: torch.Tensor, rows: int, max_add: int = 0, stream=None):
         """Sequence b keeps keep[b] tokens and gains add[b] rows (device int32 [n_seq]); the step's buffers
         have ``rows`` rows, no add[b] is larger than max_add (0: no closer bound than rows)."""
-        n = keep.shape[0]
-        for x in (keep, add):
-            if x.dtype is not torch.int32 or x.get_device() != self._index or x.shape != (n,) \
-                    or (n > 1 and x.stride(0) != 1):
-                raise KvrError(-1, f"keep and add must be contiguous int32 vectors of one length on {self.device}")
-        self._check(self.lib.kvr_page_plan(self.ctx, n, keep.data_ptr(), add.data_ptr(), rows, max_add,
-                                           self._stream(stream)))
+        n = keep.numel()
+        if keep.dtype is not torch.int32 or add.dtype is not torch.int32 or keep.get_device() != self._index \
+                or add.get_device() != self._index or keep.dim() != 1 or add.dim() != 1 or add.numel() != n \
+                or not keep.is_contiguous() or not add.is_contiguous():
+            raise KvrError(-1, f"keep and add must be contiguous int32 vectors of one length on {self.device}")
+        rc = self.lib.kvr_page_plan(self.ctx, n, keep.data_ptr(), add.data_ptr(), rows, max_add,
+                                    stream.cuda_stream if stream is not None else _raw_stream(self._index))
+        if rc:
+            self._check(rc)
         self._rows = rows
 
     def kvr_page_append(self, layer: int, q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
