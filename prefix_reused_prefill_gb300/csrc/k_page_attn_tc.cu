@@ -4,9 +4,15 @@
 // S = Q K^T and O += P V in blocks of 128 keys, softmax in one pass with a lazy
 // running maximum (a row's O is rescaled only when its maximum grows by more
 // than 2^8).  K and V become fp16 tiles in shared memory: c - 8 exactly (as in
-// k_page_attn.cu), times the scale, rounded once (2^-11; the product has at most
-// 14 bits); q is scaled per row by a power of two so that any bf16 q is an fp16
-// number; P is fp16 (2^-11).  Sums, maxima and O are fp32.
+// k_page_attn.cu), times the scale: a product of at most 14 bits.  For bf16
+// activations it is rounded once (2^-11, an eighth of what the output's own type
+// drops).  For fp16 that rounding would be as large as the output's, and the
+// scores' twice as large, so K and V are two fp16 terms each, the second the exact rest
+// of the first, and every product runs once for each: 5.6e-4 -> 2.6e-4 of the
+// outputs in the mean square at scores of deviation 2 (2.1e-4 is the output's rounding), for
+// 36 instead of 33 us in a mixed batch of 64-wide heads and 1035 instead of 767 us
+// in the long prompts below.  q is scaled per row by a power of two so that any
+// bf16 q is an fp16 number; P is fp16 (2^-11).  Sums, maxima and O are fp32.
 //
 // Writing a 4-bit block as fp16 costs about as many instructions as the softmax
 // of one 128-row tile over it, so a CTA runs two row tiles over each block: one
@@ -23,7 +29,8 @@
 //              the next scores follow one another anyway.
 //   16-19      a quarter of each block's keys, global -> registers (one block
 //              ahead) -> the fp16 tiles: K [128 keys][d] and V as [d][128 keys]
-//              (both K-major with the 128-byte swizzle), two stages each
+//              (both K-major with the 128-byte swizzle), two stages each (one
+//              where two terms of 128-wide heads fill the shared memory)
 // The work, all (sequence, pair of row tiles, KV head, key block) units in this
 // order, is cut into equal runs, one per CTA, whatever the lengths are; the parts
 // of a segment (one sequence, pair and head) that several CTAs hold go to the
@@ -34,6 +41,14 @@
 // that do not see the key (0 * NaN), so the key's score becomes NaN instead and
 // the value 0: rows that see it read NaN.
 // Every wait is bounded; a CTA whose wait gave up frees its tensor memory.
+//
+// Two prompts of up to 2047 rows over up to 14001 tokens (32 heads in groups of 4,
+// d = 128, bf16, 766 GFLOP): 767 us, 1.0 PFLOP/s, 53 % of what a library product
+// reaches.  A block of 128 keys takes a CTA about 4500 cycles: 2080 of products,
+// the rest of what the two tiles' softmax warps (exp2 of 32768 scores, half of
+// them at a time) and the four writing warps take from the same four schedulers.
+// 254 rows over 1668 tokens: 41 us, of which the run is 12, the rest the start
+// (6k cycles to the first product), Q, the parts' way to memory and the merge.
 #include <type_traits>
 
 #include "kvr_pages.cuh"
@@ -49,16 +64,19 @@ constexpr int kDecodeWarp = 16;
 constexpr int kThreads = 32 * (kDecodeWarp + 4);
 constexpr float kLazyMax = 8.0f;
 
-template <int D>
+template <int D, bool F16>
 struct Tc {
+  static constexpr int kTerms = F16 ? 2 : 1;     // fp16 terms of a K or V element
   static constexpr int kGroups = D / 32;
   static constexpr int kQTile = kTile * D * 2;   // d / 64 atoms of [128 rows][64 dims]
   static constexpr int kQAtom = kTile * 128;
-  static constexpr int kKTile = kKeys * D * 2;   // d / 64 atoms of [128 keys][64 dims]
+  static constexpr int kKTerm = kKeys * D * 2;   // d / 64 atoms of [128 keys][64 dims]
+  static constexpr int kKTile = kTerms * kKTerm;
   static constexpr int kKAtom = kKeys * 128;
-  static constexpr int kVTile = D * kKeys * 2;   // 2 atoms of [d dims][64 keys]
+  static constexpr int kVTerm = D * kKeys * 2;   // 2 atoms of [d dims][64 keys]
+  static constexpr int kVTile = kTerms * kVTerm;
   static constexpr int kVAtom = D * 128;
-  static constexpr int kStages = 2;
+  static constexpr int kStages = F16 && D == 128 ? 1 : 2;
   static constexpr int kSmem = 2 * kQTile + kStages * (kKTile + kVTile) + 1024;
 };
 // tensor memory columns
@@ -188,22 +206,33 @@ __device__ __forceinline__ uint32_t held(uint32_t x) {
   asm volatile("" : "+r"(x));
   return x;
 }
-// the four code pairs of a word as fp16 numbers c - 8, times s
+// a b - c, rounded once
+__device__ __forceinline__ uint32_t hfms2(uint32_t a, uint32_t b, uint32_t c) {
+  __half2 r = __hfma2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b),
+                      __hneg2(*reinterpret_cast<__half2*>(&c)));
+  return *reinterpret_cast<uint32_t*>(&r);
+}
+// the four code pairs of a word as fp16 numbers c - 8, times s: rounded, and what
+// the rounding dropped (a number of at most 4 bits; 2^-24 is the least)
+template <int kTerms>
 struct Pairs {
-  uint32_t v[4];
+  uint32_t v[kTerms][4];
 };
-__device__ __forceinline__ Pairs decode(uint32_t w, uint32_t s, uint32_t k1024, uint32_t k64) {
+template <int kTerms>
+__device__ __forceinline__ Pairs<kTerms> decode(uint32_t w, uint32_t s, uint32_t k1024, uint32_t k64) {
   const uint32_t y = w >> 8;
   uint32_t a, b, c, d;
   asm("lop3.b32 %0, %1, 0x000f000f, %2, 0xea;" : "=r"(a) : "r"(w), "r"(k1024));
   asm("lop3.b32 %0, %1, 0x00f000f0, %2, 0xea;" : "=r"(b) : "r"(w), "r"(k64));
   asm("lop3.b32 %0, %1, 0x000f000f, %2, 0xea;" : "=r"(c) : "r"(y), "r"(k1024));
   asm("lop3.b32 %0, %1, 0x00f000f0, %2, 0xea;" : "=r"(d) : "r"(y), "r"(k64));
-  Pairs p;
-  p.v[0] = hmul2(hadd2(a, 0xe408e408u), s);
-  p.v[1] = hmul2(hadd2(b, 0xd480d480u), s);
-  p.v[2] = hmul2(hadd2(c, 0xe408e408u), s);
-  p.v[3] = hmul2(hadd2(d, 0xd480d480u), s);
+  const uint32_t x[4] = {hadd2(a, 0xe408e408u), hadd2(b, 0xd480d480u), hadd2(c, 0xe408e408u), hadd2(d, 0xd480d480u)};
+  Pairs<kTerms> p;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    p.v[0][i] = hmul2(x[i], s);
+    if (kTerms == 2) p.v[kTerms - 1][i] = hfms2(x[i], s, p.v[0][i]);
+  }
   return p;
 }
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -231,12 +260,12 @@ struct Seg {
 template <int D, bool F16>
 __global__ void __launch_bounds__(kThreads, 1)
 page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
-  using C = Tc<D>;
+  using C = Tc<D, F16>;
   using K = Chunk<D>;
-  constexpr int kG = C::kGroups;
+  constexpr int kG = C::kGroups, kTerms = C::kTerms, kStages = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], drained[2];
-  __shared__ __align__(8) uint64_t k_full[C::kStages], k_empty[C::kStages], v_full[C::kStages], v_empty[C::kStages];
+  __shared__ __align__(8) uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
   __shared__ long long first_unit[kPageMaxSeqs + 1];   // units before each sequence
   __shared__ int start[4];                             // this CTA's first unit: sequence, tile, head, block
   __shared__ uint32_t tmem_slot;
@@ -246,7 +275,7 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x;
   const uint32_t base = (dev::smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t q_base = base, k_base = q_base + 2 * C::kQTile, v_base = k_base + C::kStages * C::kKTile;
+  const uint32_t q_base = base, k_base = q_base + 2 * C::kQTile, v_base = k_base + kStages * C::kKTile;
 
   dev::pdl_trigger();
   if (tid == 0) {
@@ -257,7 +286,7 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
       dev::mbar_init(dev::smem_u32(&pv_done[i]), 1);
       dev::mbar_init(dev::smem_u32(&drained[i]), 1);
     }
-    for (int i = 0; i < C::kStages; ++i) {
+    for (int i = 0; i < kStages; ++i) {
       dev::mbar_init(dev::smem_u32(&k_full[i]), 4);
       dev::mbar_init(dev::smem_u32(&k_empty[i]), 2);   // (one for each tile)
       dev::mbar_init(dev::smem_u32(&v_full[i]), 4);
@@ -422,8 +451,9 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
   auto wait = [&](uint64_t& bar, uint32_t parity) {
     return dev::mbar_wait(dev::smem_u32(&bar), parity & 1, p.status) && !*abort_v;
   };
-  // (the first look apart: with every look asking for the abort flag too, the
-  // 766 GFLOP of the head's example took 835 us instead of 773)
+  // (the first look apart: with every look asking for the abort flag too, two
+  // prompts of 2047 rows over up to 14001 tokens, 766 GFLOP, took 835 us
+  // instead of 773)
   auto all_wait = [&](uint64_t& bar, uint32_t parity) {
     if (__all_sync(0xffffffffu, dev::mbar_try_wait(dev::smem_u32(&bar), parity & 1))) return true;
     return (bool)__all_sync(0xffffffffu, wait(bar, parity));
@@ -488,8 +518,8 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
       fetch_v(next_page);
       next_page = page_of(j0 + 1);
       for (int j = j0; j < j1; ++j, ++it) {
-        if (it >= 2 && !all_wait(k_empty[it & 1], (it >> 1) - 1)) return false;
-        const uint32_t k_tile = k_base + (it & 1) * C::kKTile;
+        if (it >= kStages && !all_wait(k_empty[it % kStages], it / kStages - 1)) return false;
+        const uint32_t k_tile = k_base + (it % kStages) * C::kKTile;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int key = 32 * w + 8 * i + key_in;
@@ -500,17 +530,19 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
           for (int jj = 0; jj < kG; ++jj) {
             uint32_t s2 = __byte_perm(ks[i][jj / 2], 0, jj & 1 ? 0x3232 : 0x1010);
             if (bad) s2 = 0x7fff7fffu;
-            const Pairs x = decode(kc[i][jj], s2, k1024, k64);
-            sts128(k_tile + (jj >> 1) * C::kKAtom + dev::swz128(key, 4 * (jj & 1) + t), x.v[0], x.v[1], x.v[2],
-                   x.v[3]);
+            const Pairs<kTerms> x = decode<kTerms>(kc[i][jj], s2, k1024, k64);
+#pragma unroll
+            for (int m = 0; m < kTerms; ++m)
+              sts128(k_tile + m * C::kKTerm + (jj >> 1) * C::kKAtom + dev::swz128(key, 4 * (jj & 1) + t), x.v[m][0],
+                     x.v[m][1], x.v[m][2], x.v[m][3]);
           }
         }
         fence_smem();
         __syncwarp();
-        if (lane == 0) dev::mbar_arrive(dev::smem_u32(&k_full[it & 1]));
+        if (lane == 0) dev::mbar_arrive(dev::smem_u32(&k_full[it % kStages]));
         if (j + 1 < j1) fetch_k(next_page);
-        if (it >= 2 && !all_wait(v_empty[it & 1], (it >> 1) - 1)) return false;
-        const uint32_t v_tile = v_base + (it & 1) * C::kVTile + (kb >> 3) * C::kVAtom;
+        if (it >= kStages && !all_wait(v_empty[it % kStages], it / kStages - 1)) return false;
+        const uint32_t v_tile = v_base + (it % kStages) * C::kVTile + (kb >> 3) * C::kVAtom;
         // keys past the sequence weigh nothing and must not be NaN
         const int left = s.len - (kKeys * j + 8 * kb);
         if (left < 8) {
@@ -523,16 +555,19 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
         }
 #pragma unroll
         for (int jj = 0; jj < kG; ++jj) {
-          Pairs x[4];
+          Pairs<kTerms> x[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = decode(vc[i][jj], number2(vs[i][jj]), k1024, k64);
+          for (int i = 0; i < 4; ++i) x[i] = decode<kTerms>(vc[i][jj], number2(vs[i][jj]), k1024, k64);
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            sts128(v_tile + dev::swz128(32 * jj + 4 * g + e, kbp), x[0].v[e], x[1].v[e], x[2].v[e], x[3].v[e]);
+          for (int m = 0; m < kTerms; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              sts128(v_tile + m * C::kVTerm + dev::swz128(32 * jj + 4 * g + e, kbp), x[0].v[m][e], x[1].v[m][e],
+                     x[2].v[m][e], x[3].v[m][e]);
         }
         fence_smem();
         __syncwarp();
-        if (lane == 0) dev::mbar_arrive(dev::smem_u32(&v_full[it & 1]));
+        if (lane == 0) dev::mbar_arrive(dev::smem_u32(&v_full[it % kStages]));
         if (j + 1 < j1) {
           fetch_v(next_page);
           next_page = page_of(j + 2);
@@ -555,13 +590,16 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
     const uint32_t id_qk = idesc_f16(kTile, kKeys), id_pv = idesc_f16(kTile, D);
     // S = Q K^T of block i of the run; each tile frees the K stage
     auto scores = [&](uint32_t i) {
-      const uint64_t qd = sw128_desc(q_tile), kd = sw128_desc(k_base + (i & 1) * C::kKTile);
+      const uint64_t qd = sw128_desc(q_tile), kd = sw128_desc(k_base + (i % kStages) * C::kKTile);
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk)
-        mma_ss(el, tmem + s_col(t), qd + (kk >> 2) * (C::kQAtom >> 4) + 2 * (kk & 3),
-               kd + (kk >> 2) * (C::kKAtom >> 4) + 2 * (kk & 3), id_qk, kk > 0 ? 1u : 0u);
+      for (int m = 0; m < kTerms; ++m)
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_ss(el, tmem + s_col(t), qd + (kk >> 2) * (C::kQAtom >> 4) + 2 * (kk & 3),
+                 kd + m * (C::kKTerm >> 4) + (kk >> 2) * (C::kKAtom >> 4) + 2 * (kk & 3), id_qk,
+                 m > 0 || kk > 0 ? 1u : 0u);
       commit(el, dev::smem_u32(&s_full[t]));
-      commit(el, dev::smem_u32(&k_empty[i & 1]));
+      commit(el, dev::smem_u32(&k_empty[i % kStages]));
     };
     // ok stays false once a wait gave up: the warp then skips its work but
     // still meets its partner at every barrier
@@ -572,10 +610,10 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
         // must not run ahead: a phase is told by its parity, so a wait is good
         // for the stage's present or next use only.)
         for (int j = j0; issuer && j < j1 && ok; ++j, ++it) {
-          ok = all_wait(k_full[it & 1], it >> 1);
-          if (lane == 0 && ok) dev::mbar_arrive(dev::smem_u32(&k_empty[it & 1]));
-          ok = ok && all_wait(v_full[it & 1], it >> 1);
-          if (lane == 0 && ok) dev::mbar_arrive(dev::smem_u32(&v_empty[it & 1]));
+          ok = all_wait(k_full[it % kStages], it / kStages);
+          if (lane == 0 && ok) dev::mbar_arrive(dev::smem_u32(&k_empty[it % kStages]));
+          ok = ok && all_wait(v_full[it % kStages], it / kStages);
+          if (lane == 0 && ok) dev::mbar_arrive(dev::smem_u32(&v_empty[it % kStages]));
         }
         return true;
       }
@@ -643,7 +681,7 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
         __syncwarp();
         if (lane == 0 && ok) dev::mbar_arrive(dev::smem_u32(&q_full[t]));
         if (issuer && ok) {
-          ok = all_wait(q_full[t], segs) && all_wait(k_full[it & 1], it >> 1);
+          ok = all_wait(q_full[t], segs) && all_wait(k_full[it % kStages], it / kStages);
           fence_after();
           if (ok) scores(it);
         }
@@ -737,19 +775,22 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
         __syncwarp();
         if (lane == 0 && ok) dev::mbar_arrive(dev::smem_u32(&p_full[t]));
         if (issuer && ok) {
-          ok = all_wait(p_full[t], blocks) && all_wait(v_full[it & 1], it >> 1);
+          ok = all_wait(p_full[t], blocks) && all_wait(v_full[it % kStages], it / kStages);
           fence_after();
           if (ok) {
-            const uint64_t vd = sw128_desc(v_base + (it & 1) * C::kVTile);
+            const uint64_t vd = sw128_desc(v_base + (it % kStages) * C::kVTile);
 #pragma unroll
-            for (int kk = 0; kk < kKeys / 16; ++kk)
-              mma_ts(el, tmem + o_col(t), tmem + s_col(t) + 64u * (kk >> 2) + 8u * (kk & 3),
-                     vd + (kk >> 2) * (C::kVAtom >> 4) + 2 * (kk & 3), id_pv, (j > j0 || kk > 0) ? 1u : 0u);
+            for (int m = 0; m < kTerms; ++m)
+#pragma unroll
+              for (int kk = 0; kk < kKeys / 16; ++kk)
+                mma_ts(el, tmem + o_col(t), tmem + s_col(t) + 64u * (kk >> 2) + 8u * (kk & 3),
+                       vd + m * (C::kVTerm >> 4) + (kk >> 2) * (C::kVAtom >> 4) + 2 * (kk & 3), id_pv,
+                       (j > j0 || m > 0 || kk > 0) ? 1u : 0u);
             commit(el, dev::smem_u32(&pv_done[t]));
-            commit(el, dev::smem_u32(&v_empty[it & 1]));
+            commit(el, dev::smem_u32(&v_empty[it % kStages]));
             if (j + 1 < j1) {
               // the next scores go over P, which this product still reads
-              ok = all_wait(k_full[(it + 1) & 1], (it + 1) >> 1) && all_wait(pv_done[t], blocks);
+              ok = all_wait(k_full[(it + 1) % kStages], (it + 1) / kStages) && all_wait(pv_done[t], blocks);
               fence_after();
               if (ok) scores(it + 1);
             }
@@ -854,7 +895,7 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
 
 template <int D, bool F16>
 cudaError_t setup_one() {
-  return cudaFuncSetAttribute(page_attn_tc_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, Tc<D>::kSmem);
+  return cudaFuncSetAttribute(page_attn_tc_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, Tc<D, F16>::kSmem);
 }
 
 }  // namespace
@@ -869,10 +910,10 @@ cudaError_t page_attn_tc_setup() {
 
 cudaError_t launch_page_attn_tc(const PagesDev& p, const PageAttendTc& a, int ctas, cudaStream_t st) {
   if (p.d == 128)
-    return p.f16 ? launch_k(page_attn_tc_kernel<128, true>, dim3(ctas), kThreads, Tc<128>::kSmem, st, p, a)
-                 : launch_k(page_attn_tc_kernel<128, false>, dim3(ctas), kThreads, Tc<128>::kSmem, st, p, a);
-  return p.f16 ? launch_k(page_attn_tc_kernel<64, true>, dim3(ctas), kThreads, Tc<64>::kSmem, st, p, a)
-               : launch_k(page_attn_tc_kernel<64, false>, dim3(ctas), kThreads, Tc<64>::kSmem, st, p, a);
+    return p.f16 ? launch_k(page_attn_tc_kernel<128, true>, dim3(ctas), kThreads, Tc<128, true>::kSmem, st, p, a)
+                 : launch_k(page_attn_tc_kernel<128, false>, dim3(ctas), kThreads, Tc<128, false>::kSmem, st, p, a);
+  return p.f16 ? launch_k(page_attn_tc_kernel<64, true>, dim3(ctas), kThreads, Tc<64, true>::kSmem, st, p, a)
+               : launch_k(page_attn_tc_kernel<64, false>, dim3(ctas), kThreads, Tc<64, false>::kSmem, st, p, a);
 }
 
 }  // namespace kvr

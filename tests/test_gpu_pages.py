@@ -14,7 +14,7 @@ Bounds, per element (u = half a step of the output type, 2^-9 relative for bf16'
   in n / 16 + 2 fp32 additions that may each drop 2^-22 of the running sum, itself at most max|v|:
   (2 * 2^-11 + 2^-13) sum w|v| + n (2^-27 max|v| + 2^-24) + (n / 16 + 2) 2^-22 max|v| + eps/2 |o|.
   Sequences with many rows of a KV head (the tensor-memory kernel: more than 64, or more than 16 in a step where one has
-  more than 64) read k as fp16 too: c s has 14 bits, each
+  more than 64) read k as fp16 too where the activations are bf16: c s has 14 bits, each
   rounded by at most 2^-11.  A score is off by the sum of d such errors times scale q_d: at most
   6 * 2^-11 scale |q k|_2 but for odds of 2 exp(-18) (Hoeffding), and a weight by twice that of its row's largest.
 """
@@ -277,7 +277,7 @@ class World:
                     ref, mag = op.attend(qn[row], k, v, scale)
                     spread = 0.0
                     group = self.heads // self.kv_heads
-                    if m * group > (BESIDE if self.rows * group > MANY else MANY):
+                    if self.act == "bf16" and m * group > (BESIDE if self.rows * group > MANY else MANY):
                         kk = np.repeat(k, self.heads // self.kv_heads, axis=0)
                         spread = scale * np.sqrt(np.max((kk * qn[row][:, None]) ** 2 @ np.ones(self.d), axis=1))[:, None]
                     tol = bound(n, mag, v, ref, u, spread)
@@ -319,6 +319,23 @@ def test_attend_rows(act, heads, kv_heads, d, keep, add):
         q = w.q(1.5)
         w.check(q, w.pg.kvr_page_attend(1, q.cuda()))
     w.pg.kvr_pages_sync()
+
+
+@pytest.mark.parametrize("heads,kv_heads,d", [(8, 2, 64), (6, 2, 128)])
+def test_attend_rows_in_fp16_round_weights_and_outputs_only(heads, kv_heads, d):
+    """Root mean square error, relative to the outputs': an fp16 rounding is off by at most 2^-11 of the value, evenly
+    spread, so by 2^-11 / sqrt(3) in the mean square; that of the weights, with values of random sign, and that of the
+    output are independent: sqrt(2 / 3) 2^-11 together, and a hundredth for the sums in 32 bits."""
+    w = World(heads, kv_heads, d, "fp16", seed=7)
+    w.step([0] * 8, [400] + [0] * 7)
+    w.step([400] + [0] * 7, [150] + [0] * 7)
+    q = w.q(3.0)
+    got, qn = f64(w.pg.kvr_page_attend(1, q.cuda())), f64(q)
+    err = size = 0.0
+    for i in range(150):
+        ref, _ = op.attend(qn[i], w.k[0][:, :401 + i], w.v[0][:, :401 + i], d ** -0.5)
+        err, size = err + ((got[i] - ref) ** 2).sum(), size + (ref ** 2).sum()
+    assert (err / size) ** 0.5 <= 1.01 * (2 / 3) ** 0.5 * 2.0 ** -11
 
 
 @pytest.mark.parametrize("d,heads,kv_heads", [(64, 32, 8), (128, 16, 4)])
