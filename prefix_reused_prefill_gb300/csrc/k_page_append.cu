@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
 page_append_kernel(const PagesDev p, const PageAppend a) {
   using C = Chunk<D>;
   using L = Lanes<D>;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   const int l = lane % L::kPer, t = l & 3;
   const int row = (int)blockIdx.x * L::kRows + lane / L::kPer;
   dev::pdl_trigger();
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(32 * kWarps)
 page_read_kernel(const PagesDev p, void* k_out, void* v_out, int rows) {
   using C = Chunk<D>;
   using L = Lanes<D>;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   const int l = lane % L::kPer, t = l & 3;
   const int row = (int)blockIdx.x * L::kRows + lane / L::kPer;
   dev::pdl_trigger();

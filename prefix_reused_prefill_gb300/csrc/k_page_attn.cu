@@ -266,7 +266,7 @@ page_attn_kernel(const PagesDev p, const PageAttend a) {
   __shared__ int last_flag[2];
   __shared__ int abort_flag;
   volatile int* abort_v = &abort_flag;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
   const int cta = blockIdx.x;
 

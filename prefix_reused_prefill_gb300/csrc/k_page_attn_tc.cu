@@ -86,9 +86,10 @@ __device__ __forceinline__ uint32_t o_col(int t) { return (uint32_t)(256 + 128 *
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
-  return (uint64_t)((saddr >> 4) & 0x3FFFu) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
-}
+// The low word of the descriptor of a tile with the 128-byte swizzle; the high word
+// is the same for all (8 rows of 128 bytes apart, version 1, that swizzle).
+constexpr uint32_t kDescHigh = 64u | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t sw128_desc(uint32_t saddr) { return ((saddr >> 4) & 0x3FFFu) | (1u << 16); }
 __device__ __forceinline__ uint32_t idesc_f16(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
@@ -101,24 +102,27 @@ __device__ __forceinline__ uint32_t elect() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
   return e;
 }
-__device__ __forceinline__ void mma_ss(uint32_t elected, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+__device__ __forceinline__ void mma_ss(uint32_t elected, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
                                        uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 x, y;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "setp.ne.b32 e, %5, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(elected)
+      "mov.b64 x, {%1, %6};\n\t"
+      "mov.b64 y, {%2, %6};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(elected), "r"(kDescHigh)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t elected, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+__device__ __forceinline__ void mma_ts(uint32_t elected, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
                                        uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 y;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "setp.ne.b32 e, %5, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(elected)
+      "mov.b64 y, {%2, %6};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(elected), "r"(kDescHigh)
       : "memory");
 }
 __device__ __forceinline__ void commit(uint32_t elected, uint32_t bar) {
@@ -272,7 +276,8 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
   __shared__ float exchange[2][2][kTile];              // [tile][half of the block][row]
   __shared__ int abort_flag;
   volatile int* abort_v = &abort_flag;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // (the shuffle tells the compiler that a warp's number is one for its lanes)
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int cta = blockIdx.x;
   const uint32_t base = (dev::smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t q_base = base, k_base = q_base + 2 * C::kQTile, v_base = k_base + kStages * C::kKTile;
@@ -458,6 +463,13 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
     if (__all_sync(0xffffffffu, dev::mbar_try_wait(dev::smem_u32(&bar), parity & 1))) return true;
     return (bool)__all_sync(0xffffffffu, wait(bar, parity));
   };
+  // both of two waits, the first look at them together
+  auto all_wait2 = [&](uint64_t& bar, uint32_t parity, uint64_t& bar2, uint32_t parity2) {
+    const bool one = dev::mbar_try_wait(dev::smem_u32(&bar), parity & 1);
+    const bool two = dev::mbar_try_wait(dev::smem_u32(&bar2), parity2 & 1);
+    if (__all_sync(0xffffffffu, one && two)) return true;
+    return all_wait(bar, parity) && all_wait(bar2, parity2);
+  };
   bool ok = true;
   if (warp >= kDecodeWarp) {
     // ---------------------------------------------------------------- tiles
@@ -590,7 +602,7 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
     const uint32_t id_qk = idesc_f16(kTile, kKeys), id_pv = idesc_f16(kTile, D);
     // S = Q K^T of block i of the run; each tile frees the K stage
     auto scores = [&](uint32_t i) {
-      const uint64_t qd = sw128_desc(q_tile), kd = sw128_desc(k_base + (i % kStages) * C::kKTile);
+      const uint32_t qd = sw128_desc(q_tile), kd = sw128_desc(k_base + (i % kStages) * C::kKTile);
 #pragma unroll
       for (int m = 0; m < kTerms; ++m)
 #pragma unroll
@@ -775,10 +787,10 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
         __syncwarp();
         if (lane == 0 && ok) dev::mbar_arrive(dev::smem_u32(&p_full[t]));
         if (issuer && ok) {
-          ok = all_wait(p_full[t], blocks) && all_wait(v_full[it % kStages], it / kStages);
+          ok = all_wait2(v_full[it % kStages], it / kStages, p_full[t], blocks);
           fence_after();
           if (ok) {
-            const uint64_t vd = sw128_desc(v_base + (it % kStages) * C::kVTile);
+            const uint32_t vd = sw128_desc(v_base + (it % kStages) * C::kVTile);
 #pragma unroll
             for (int m = 0; m < kTerms; ++m)
 #pragma unroll
@@ -790,7 +802,7 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
             commit(el, dev::smem_u32(&v_empty[it % kStages]));
             if (j + 1 < j1) {
               // the next scores go over P, which this product still reads
-              ok = all_wait(k_full[(it + 1) % kStages], (it + 1) / kStages) && all_wait(pv_done[t], blocks);
+              ok = all_wait2(k_full[(it + 1) % kStages], (it + 1) / kStages, pv_done[t], blocks);
               fence_after();
               if (ok) scores(it + 1);
             }

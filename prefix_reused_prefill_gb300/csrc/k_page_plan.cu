@@ -62,7 +62,7 @@ page_plan_kernel(const PagesDev p, int n, const int32_t* keep, const int32_t* ad
   __shared__ Sums warp_sum[kWarps];
   __shared__ int bad;
   cg::cluster_group cluster = cg::this_cluster();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int gtid = (int)blockIdx.x * kThreads + tid, gthreads = (int)gridDim.x * kThreads;
   dev::pdl_trigger();
   if (tid == 0) bad = 0;
