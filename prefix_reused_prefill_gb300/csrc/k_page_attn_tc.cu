@@ -10,7 +10,7 @@
 // scores' twice as large, so K and V are two fp16 terms each, the second the exact rest
 // of the first, and every product runs once for each: 5.6e-4 -> 2.6e-4 of the
 // outputs in the mean square at scores of deviation 2 (2.1e-4 is the output's rounding), for
-// 36 instead of 33 us in a mixed batch of 64-wide heads and 1035 instead of 767 us
+// 33.5 instead of 32 us in a mixed batch of 64-wide heads and 915 instead of 673 us
 // in the long prompts below.  q is scaled per row by a power of two so that any
 // bf16 q is an fp16 number; P is fp16 (2^-11).  Sums, maxima and O are fp32.
 //
@@ -43,11 +43,16 @@
 // Every wait is bounded; a CTA whose wait gave up frees its tensor memory.
 //
 // Two prompts of up to 2047 rows over up to 14001 tokens (32 heads in groups of 4,
-// d = 128, bf16, 766 GFLOP): 767 us, 1.0 PFLOP/s, 53 % of what a library product
-// reaches.  A block of 128 keys takes a CTA about 4500 cycles: 2080 of products,
-// the rest of what the two tiles' softmax warps (exp2 of 32768 scores, half of
-// them at a time) and the four writing warps take from the same four schedulers.
-// 254 rows over 1668 tokens: 41 us, of which the run is 12, the rest the start
+// d = 128, bf16, 766 GFLOP): 673 us, 1.14 PFLOP/s, 61 % of what a library product
+// reaches.  A block of 128 keys takes a CTA about 4000 cycles, 2080 of them
+// products.  Each tile's chain is what lasts so long: 2000 of softmax (1400 for the weights,
+// the other tile and the writing warps on the same schedulers), 940 until P V is
+// done (520 of products, the rest the commit's way to the waiting warp), which the next
+// scores must wait for as they go over P, and 750 for them.  (Scores of the
+// upper 64 keys issued before that wait, P all in the lower columns: 784 us, a
+// product of 64 keys lasts as long as one of 128.  64-key blocks with two S:
+// slower too.)
+// 254 rows over 1668 tokens: 38 us, of which the run is about 11, the rest the start
 // (6k cycles to the first product), Q, the parts' way to memory and the merge.
 #include <type_traits>
 

@@ -28,13 +28,14 @@ namespace {
 constexpr size_t kAlign = 256;
 // Rows of a sequence and KV head (rows * group) up to which the split kernel
 // takes the sequence: 64 where every sequence of the step has so few (four
-// conversations of 8 rows, group 7, over 15k tokens: 60 us, 63 us by the
+// conversations of 8 rows, group 7, over 15k tokens: 52 us, 55 us by the
 // tensor-memory kernel), but 16 where that kernel runs anyway (12 conversations
-// of 1 to 120 rows, group 4, over up to 4k tokens: 33 us, 40 us with 64).
+// of 1 to 120 rows, group 4, over up to 4k tokens: 32 us, 46 us with 32).
 constexpr int kPageMany = 64, kPageManyBeside = 16;
 // key blocks a CTA of the tensor-memory kernel takes at least: 254 rows over
-// 1668 tokens are flat from 1 to 5 (46 to 49 us), 55 us with 8
-constexpr int kPageMinUnits = 3;
+// 1668 tokens take 37.8 us with 2, 38.3 with 3 and 39.7 with 5, where fewer CTAs
+// run longer but leave fewer parts to merge; 18 rows over 2048: 24.0, 25.0, 27.6
+constexpr int kPageMinUnits = 2;
 inline size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 bool valid(const kvr_pages_config* c) {
