@@ -576,10 +576,12 @@ int kvr_page_plan(kvr_pages* pages, int n_seq, const int32_t* keep, const int32_
 
 /*
  * The planned rows of one layer: q and k normed per head (x / sqrt(mean x^2 +
- * eps) * gain; norm_q, norm_k: [head_dim], null for none), rotated by the
- * row's position (rotate = 1) and rounded once to the activation type; q goes
- * to q_out [rows][n_q_heads][head_dim], k (so rounded) and v (as it is) are
- * quantised into the row's slot.
+ * eps) * gain; norm_q, norm_k: [head_dim], null for none; the squares' sum is a
+ * 32-bit number), rotated by the row's position (rotate = 1) and rounded to
+ * the activation type; q, in 32-bit arithmetic, goes to q_out
+ * [rows][n_q_heads][head_dim], k (formed to more bits and rounded to 32, then to
+ * the type, as a value on the other side of a border would take another code)
+ * and v (as it is) are quantised into the row's slot.
  *   q, k, v   [rows] with the heads of a row contiguous and a row stride in
  *             elements (a multiple of 8): views of one projection output work.
  *             q and q_out may both be null (k and v only); q_out may be q if

@@ -1,20 +1,24 @@
 // The planned rows of one layer (kvr_page_append): per head
 //   y = x / sqrt(mean x^2 + eps) * gain      (q and k, where a gain is given)
 //   (y_j, y_(j + d/2)) -> (y_j c - y_(j+d/2) s, y_(j+d/2) c + y_j s)
-// in 32 bits, rounded once to the activation type, q written out, k and v
-// quantised into their page: one read of the projection's output and one write.
+// rounded to the activation type, q written out, k and v quantised into their
+// page: one read of the projection's output and one write.  q is formed in 32
+// bits, k in sums of two floats: a rounding to the other side of a border may move a
+// code, and that is 1 / 7 of the group's largest value.
 //
-// Bound by HBM bytes.  d / 16 lanes hold a head's vector, lane l the elements
-// 8 l .. 8 l + 7 of both halves: 16-byte loads and stores, the rotation pairs in
-// one lane, a group of 32 in four neighbouring lanes, a K code word in one
-// lane.  A warp takes 32 / (d / 16) consecutive rows of the same head, which in
-// a prompt are neighbouring tokens of a page, so that the 2-byte units of V
-// (a unit never holds two tokens) meet in one 32-byte sector; it keeps the
-// rows' cosines and sines in registers over the heads it walks.
+// d / 16 lanes hold a head's vector, lane l the elements 8 l .. 8 l + 7 of both
+// halves: 16-byte loads and stores, the rotation pairs in one lane, a group of
+// 32 in four neighbouring lanes, a K code word in one lane.  A warp takes
+// 32 / (d / 16) consecutive rows of the same head, which in a prompt are
+// neighbouring tokens of a page, so that the 2-byte units of V (a unit never
+// holds two tokens) meet in one 32-byte sector.
 //
-// 8.2k rows of 32 + 2 * 8 heads of 128 with norms: 42 us, 4.2 TB/s of 176 MB, 62 % of
-// a plain copy's rate; the quantising costs 3 us of it.  One to 254 rows: 3 to
-// 4 us, a launch.
+// 8.2k rows of 32 + 2 * 8 heads of 128 with norms: 48.6 us, 3.6 TB/s of 176 MB, 53 %
+// of a plain copy's rate.  Of that k's second floats take 7 us (with them k is
+// that of 64 bits in all of 50 million values, in 32 bits two or three codes
+// in 8 million moved), the rest is arithmetic too: issue slots 66 % busy, and more
+// loads in flight (through shared memory) or more and smaller CTAs change
+// nothing.  One to 254 rows: 3.3 to 4 us, a launch.
 #include "kvr_pages.cuh"
 
 namespace kvr {
@@ -46,39 +50,150 @@ __device__ __forceinline__ uint4 pack8(const float2* x) {
 // one, and leaves that integer in the low bits
 constexpr float kRound = 12582912.f;
 
-// code (with 8 added) of x under the scale s: x / s rounded, halves to the even
-// code, at most [-8, 7].  x times 1 / s can be off by 2^-23 of itself, and a
-// quotient exactly halfway is common (16-bit values over a 16-bit scale): the
-// remainder x - n s, which an FMA gives exactly, tells where n is to be moved.
-__device__ __forceinline__ uint32_t code_of(float x, float s, float inv, float half) {
+// minus the code of x under the scale s, whatever they are: x / s rounded, halves to
+// the even number, at most [-8, 7].  A quotient exactly halfway goes to the even
+// one by the remainder.
+__device__ __forceinline__ float minus_code(float x, float s, float inv) {
+  const float half = s > 0.f ? 0.5f * s : INFINITY;
   float t = fminf(fmaxf(x * inv, -9.f), 9.f) + kRound;
   const float d = fmaf(kRound - t, s, x);
   if (fabsf(d) >= half && (fabsf(d) > half || (__float_as_uint(t) & 1u))) t += d > 0.f ? 1.f : -1.f;
-  t = fminf(fmaxf(t, kRound - 8.f), kRound + 7.f);
-  return __float_as_uint(t) - (__float_as_uint(kRound) - 8u);
+  return fminf(fmaxf(kRound - t, -7.f), 8.f);
 }
 
-// codes of 8 of the 32 elements of a group held by 4 neighbouring lanes, and the
-// group's scale
-__device__ __forceinline__ __half quantise8(const float2* x, uint32_t* code) {
-  // |x| as bits, so that NaN ranks above infinity and infinity above numbers
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    top = max(top, max(__float_as_uint(x[i].x) & 0x7fffffffu, __float_as_uint(x[i].y) & 0x7fffffffu));
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-  const bool bad = top >= 0x7f800000u;
-  const __half s = __float2half_rn(bad ? 0.f : fminf(__fdiv_rn(__uint_as_float(top), 7.f), kPageScaleMax));
+// the larger of |a| and |b|, element by element; NaN where either is
+template <bool F16>
+__device__ __forceinline__ uint32_t abs_max2(uint32_t a, uint32_t b) {
+  a &= 0x7fff7fffu;
+  b &= 0x7fff7fffu;
+  if (F16) {
+    const __half2 m = __hmax2_nan(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&m);
+  }
+  const __nv_bfloat162 m = __hmax2_nan(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&m);
+}
+
+// Codes of 8 of the 32 elements of a group held by 4 neighbouring lanes (u: as they
+// are, x: as floats), and the group's scale.  of_k: a word of K (elements 0, 2, 4,
+// 6 in its lower half); else two units of V, 4 elements each, side by side.
+template <bool F16>
+__device__ __forceinline__ __half quantise8(uint4 u, const float2* x, bool of_k, uint32_t& word) {
+  uint32_t m = abs_max2<F16>(abs_max2<F16>(u.x, u.y), abs_max2<F16>(u.z, u.w));
+  m = abs_max2<F16>(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = abs_max2<F16>(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  const float2 tops = dev::act2<F16>(m);
+  const bool bad = !(tops.x < INFINITY && tops.y < INFINITY);
+  const float top = fmaxf(tops.x, tops.y);
+  const __half s = __float2half_rn(bad ? 0.f : fminf(__fdiv_rn(top, 7.f), kPageScaleMax));
   const float sf = __half2float(s);
-  // (without a scale every code is 0: no remainder passes an infinite half)
-  const float inv = sf > 0.f ? __frcp_rn(sf) : 0.f, half = sf > 0.f ? 0.5f * sf : INFINITY;
+  const float inv = sf > 0.f ? __frcp_rn(sf) : 0.f;   // (without a scale every code is 0)
+  // -round(x / s), halves to the even number.  x times 1 / s can be off by 2^-23 of
+  // itself, and a quotient exactly halfway is common (16-bit values over a 16-bit
+  // scale; 4 groups of 100): the remainder x - n s, which an FMA gives exactly, is
+  // either exactly half of s or 2^-12 s from it, so rounded to 2^-14 s it is added to n
+  // without error.  A scale that is neither cut nor subnormal is top / 7 to 2^-11: no
+  // code passes 7.
+  constexpr float kFine = 768.f;   // 1.5 2^9: sums with it are multiples of 2^-14
+  float2 n[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    code[2 * i] = code_of(bad ? 0.f : x[i].x, sf, inv, half);
-    code[2 * i + 1] = code_of(bad ? 0.f : x[i].y, sf, inv, half);
+    const float2 whole = make_float2(kRound, kRound), fine = make_float2(kFine, kFine);
+    const float2 t = dev::fma2(x[i], make_float2(inv, inv), whole);
+    const float2 d = dev::fma2(dev::sub2(whole, t), make_float2(sf, sf), x[i]);
+    const float2 e = dev::sub2(dev::fma2(d, make_float2(inv, inv), fine), fine);
+    n[i] = dev::sub2(whole, dev::add2(t, e));
+  }
+  if (bad || sf == kPageScaleMax || (sf > 0.f && sf < 6.103515625e-5f)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float v = i & 1 ? x[i / 2].y : x[i / 2].x;
+      const float c = minus_code(bad ? 0.f : v, sf, inv);
+      if (i & 1) n[i / 2].y = c;
+      else n[i / 2].x = c;
+    }
+  }
+  // the codes (with 8 added) as exact sums of powers of 16
+  if (of_k) {
+    float2 sum = make_float2(8388608.f + 0x8888, 8388608.f + 0x8888);
+    sum = dev::sub2(sum, n[0]);
+    sum = dev::fma2(n[1], make_float2(-16.f, -16.f), sum);
+    sum = dev::fma2(n[2], make_float2(-256.f, -256.f), sum);
+    sum = dev::fma2(n[3], make_float2(-4096.f, -4096.f), sum);
+    word = __byte_perm(__float_as_uint(sum.x), __float_as_uint(sum.y), 0x5410);
+  } else {
+    uint32_t w[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float2 sum = dev::fma2(n[2 * e], make_float2(-1.f, -16.f), make_float2(8388608.f + 0x8888, 0.f));
+      sum = dev::fma2(n[2 * e + 1], make_float2(-256.f, -4096.f), sum);
+      w[e] = __float_as_uint(sum.x + sum.y);
+    }
+    word = __byte_perm(w[0], w[1], 0x5410);
   }
   return bad ? __ushort_as_half((unsigned short)0x7fffu) : s;
+}
+
+// Numbers as sums hi + lo of two floats (2^-45 or so), for k next to the border of
+// two activation values: k is rounded to that type and then to a code, and on the
+// other side of both borders it would move by a whole scale, 1 / 7 of the
+// group's largest.
+// a + b = hi + lo, exactly
+__device__ __forceinline__ void two_sum(float2 a, float2 b, float2& hi, float2& lo) {
+  hi = dev::add2(a, b);
+  const float2 v = dev::sub2(hi, a);
+  lo = dev::add2(dev::sub2(a, dev::sub2(hi, v)), dev::sub2(b, v));
+}
+__device__ __forceinline__ void two_sum(float a, float b, float& hi, float& lo) {
+  hi = a + b;
+  const float v = hi - a;
+  lo = (a - (hi - v)) + (b - v);
+}
+// 1 / sqrt(mean x^2 + eps) over the d elements of a head, 16 of them here
+template <int D>
+__device__ __forceinline__ float2 exact_rsqrt(const float2* x, float eps) {
+  float2 s = dev::mul2(x[0], x[0]), rest = make_float2(0.f, 0.f);   // (16-bit numbers: exact squares)
+#pragma unroll
+  for (int i = 1; i < 8; ++i) {
+    float2 lo;
+    two_sum(s, dev::mul2(x[i], x[i]), s, lo);
+    rest = dev::add2(rest, lo);
+  }
+  float hi, lo;
+  two_sum(s.x, s.y, hi, lo);
+  lo += rest.x + rest.y;
+#pragma unroll
+  for (int m = 1; m < Lanes<D>::kPer; m <<= 1) {
+    const float other = __shfl_xor_sync(0xffffffffu, hi, m), other_lo = __shfl_xor_sync(0xffffffffu, lo, m);
+    float e;
+    two_sum(hi, other, hi, e);
+    lo += other_lo + e;
+  }
+  float e;
+  two_sum(hi * (1.f / D), eps, hi, e);
+  lo = fmaf(lo, 1.f / D, e);
+  // one step of Newton's from the approximate root, the residual 1 - v r^2 formed
+  // from the exact product v r
+  const float r = rsqrtf(hi), p = hi * r, pe = fmaf(hi, r, -p);
+  const float off = fmaf(-fmaf(lo, r, pe), r, fmaf(-p, r, 1.f));
+  return make_float2(r, 0.5f * r * off);
+}
+// (a c - b s) r with cosines c, sines s and r of two parts each; na = -a, nb = -b
+__device__ __forceinline__ float2 exact_turn(float2 a, float2 na, float2 b, float2 nb, float2 c, float2 s, float2 c_lo,
+                                             float2 s_lo, bool scaled, float2 r) {
+  const float2 p = dev::mul2(a, c), q = dev::mul2(nb, s);
+  float2 hi, lo;
+  two_sum(p, q, hi, lo);
+  lo = dev::sub2(lo, dev::add2(dev::fma2(na, c, p), dev::fma2(b, s, q)));   // (less what p and q are too large)
+  lo = dev::fma2(a, c_lo, lo);
+  lo = dev::fma2(nb, s_lo, lo);
+  if (scaled) {
+    const float2 rr = make_float2(r.x, r.x), y = dev::mul2(hi, rr);
+    lo = dev::fma2(lo, rr, dev::mul2(hi, make_float2(r.y, r.y)));
+    lo = dev::sub2(lo, dev::fma2(hi, make_float2(-r.x, -r.x), y));
+    hi = y;
+  }
+  return dev::add2(hi, lo);
 }
 
 template <int D, bool F16>
@@ -96,24 +211,16 @@ page_append_kernel(const PagesDev p, const PageAppend a) {
   const bool live = row < total;
   const int pos = live ? p.row_pos[row] : 0;
   const int slot = live ? p.row_slot[row] : 0;
-  float2 cs[4], sn[4];   // cosines and sines of dims 8 l .. 8 l + 7
-  if (a.rotate) {
-    const float4* src = reinterpret_cast<const float4*>(p.rope + (long long)pos * (D / 2) + 8 * l);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 v = src[i];
-      cs[i] = make_float2(v.x, v.z);
-      sn[i] = make_float2(v.y, v.w);
-    }
-  }
+  // cosines and sines of this lane's dims 8 l .. 8 l + 7 (read anew for each head,
+  // from L1: in registers they would cost every head more than that)
+  const float4* turns = reinterpret_cast<const float4*>(p.rope + (long long)pos * (D / 2) + 8 * l);
+  const uint4* turns_rest = reinterpret_cast<const uint4*>(p.rope_rest + (long long)pos * (D / 2) + 8 * l);
   const int h0 = a.q ? 0 : p.Hq;
   const int heads = p.Hq + 2 * p.Hkv;
   uint8_t* page = p.pool + p.layer_off + (long long)(slot / kPage) * p.Hkv * C::kBytes;
   const int key = slot % kPage;
   // this lane's elements of head h of its row.  The next head's are asked for
-  // before this one's are used (in the example of the head 61 us without, 51 us
-  // so, 44 us with the exact division replaced and four CTAs on an SM; without
-  // any quantising 41 us)
+  // before this one's are used (61 -> 51 us in the example of the head)
   auto fetch = [&](int h, uint4& lo, uint4& hi) {
     if (!live || h >= heads) return;
     const uint16_t* src;
@@ -135,9 +242,8 @@ page_append_kernel(const PagesDev p, const PageAppend a) {
     float2 x[8];
     unpack8<F16>(u0, x);
     unpack8<F16>(u1, x + 4);
-    if (is_q || is_k) {
-      const void* gain = is_q ? a.norm_q : a.norm_k;
-      if (gain) {
+    if (is_q) {
+      if (a.norm_q) {
         float2 s2 = dev::mul2(x[0], x[0]);
 #pragma unroll
         for (int i = 1; i < 8; ++i) s2 = dev::fma2(x[i], x[i], s2);
@@ -145,7 +251,7 @@ page_append_kernel(const PagesDev p, const PageAppend a) {
 #pragma unroll
         for (int m = 1; m < L::kPer; m <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
         const float r = rsqrtf(ss * (1.f / D) + a.eps);   // (2 ulp)
-        const uint16_t* gp = static_cast<const uint16_t*>(gain) + 8 * l;
+        const uint16_t* gp = static_cast<const uint16_t*>(a.norm_q) + 8 * l;
         float2 g[8];
         unpack8<F16>(*reinterpret_cast<const uint4*>(gp), g);
         unpack8<F16>(*reinterpret_cast<const uint4*>(gp + D / 2), g + 4);
@@ -155,21 +261,51 @@ page_append_kernel(const PagesDev p, const PageAppend a) {
       if (a.rotate) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2 lo = x[i], hi = x[4 + i];
-          x[i] = dev::fma2(lo, cs[i], dev::mul2(hi, make_float2(-sn[i].x, -sn[i].y)));
-          x[4 + i] = dev::fma2(hi, cs[i], dev::mul2(lo, sn[i]));
+          const float4 v = turns[i];
+          const float2 lo = x[i], hi = x[4 + i], c = make_float2(v.x, v.z);
+          x[i] = dev::fma2(lo, c, dev::mul2(hi, make_float2(-v.y, -v.w)));
+          x[4 + i] = dev::fma2(hi, c, dev::mul2(lo, make_float2(v.y, v.w)));
+        }
+      }
+      if (live) {
+        uint16_t* dst = static_cast<uint16_t*>(a.q_out) + ((long long)row * p.Hq + hh) * D + 8 * l;
+        *reinterpret_cast<uint4*>(dst) = pack8<F16>(x);
+        *reinterpret_cast<uint4*>(dst + D / 2) = pack8<F16>(x + 4);
+      }
+      continue;
+    }
+    if (is_k && (a.norm_k || a.rotate)) {
+      float2 root = make_float2(1.f, 0.f);
+      if (a.norm_k) {
+        root = exact_rsqrt<D>(x, a.eps);
+        const uint16_t* gp = static_cast<const uint16_t*>(a.norm_k) + 8 * l;
+        const uint4 g[2] = {*reinterpret_cast<const uint4*>(gp), *reinterpret_cast<const uint4*>(gp + D / 2)};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = dev::mul2(x[i], dev::act2<F16>(reinterpret_cast<const uint32_t*>(g)[i]));
+      }
+      if (a.rotate) {
+        const uint4 w[2] = {turns_rest[0], turns_rest[1]};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 v = turns[i];
+          const float2 e = dev::act2<true>(reinterpret_cast<const uint32_t*>(w)[2 * i]);
+          const float2 f = dev::act2<true>(reinterpret_cast<const uint32_t*>(w)[2 * i + 1]);
+          const float2 unit = make_float2(5.9604644775390625e-8f, 5.9604644775390625e-8f);   // 2^-24
+          const float2 c_lo = dev::mul2(make_float2(e.x, f.x), unit), s_lo = dev::mul2(make_float2(e.y, f.y), unit);
+          const float2 c = make_float2(v.x, v.z), s = make_float2(v.y, v.w), lo = x[i], hi = x[4 + i];
+          const float2 nlo = dev::neg2(lo), nhi = dev::neg2(hi);
+          x[i] = exact_turn(lo, nlo, hi, nhi, c, s, c_lo, s_lo, a.norm_k, root);
+          x[4 + i] = exact_turn(hi, nhi, nlo, lo, c, s, c_lo, s_lo, a.norm_k, root);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 rr = make_float2(root.x, root.x), y = dev::mul2(x[i], rr);
+          x[i] = dev::add2(y, dev::fma2(x[i], make_float2(root.y, root.y), dev::fma2(x[i], rr, dev::neg2(y))));
         }
       }
       u0 = pack8<F16>(x);
       u1 = pack8<F16>(x + 4);
-      if (is_q) {
-        if (live) {
-          uint16_t* dst = static_cast<uint16_t*>(a.q_out) + ((long long)row * p.Hq + hh) * D + 8 * l;
-          *reinterpret_cast<uint4*>(dst) = u0;
-          *reinterpret_cast<uint4*>(dst + D / 2) = u1;
-        }
-        continue;
-      }
       // the values that the cache quantises are those of the activation type
       unpack8<F16>(u0, x);
       unpack8<F16>(u1, x + 4);
@@ -178,21 +314,15 @@ page_append_kernel(const PagesDev p, const PageAppend a) {
 #pragma unroll
     for (int part = 0; part < 2; ++part) {
       const int j = part * (C::kGroups / 2) + l / 4;
-      uint32_t c[8];
-      const __half s = quantise8(x + 4 * part, c);
+      uint32_t word;
+      const __half s = quantise8<F16>(part ? u1 : u0, x + 4 * part, is_k, word);
       if (!live) continue;
       if (is_k) {
-        uint32_t w = 0;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) w |= (c[2 * r] << (4 * r)) | (c[2 * r + 1] << (4 * r + 16));
-        *reinterpret_cast<uint32_t*>(chunk + C::k_word(key, t, j)) = w;
+        *reinterpret_cast<uint32_t*>(chunk + C::k_word(key, t, j)) = word;
         if (t == 0) *reinterpret_cast<__half*>(chunk + C::k_scale(key, j)) = s;
       } else {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint32_t w = c[4 * e] | (c[4 * e + 1] << 4) | (c[4 * e + 2] << 8) | (c[4 * e + 3] << 12);
-          *reinterpret_cast<uint16_t*>(chunk + C::v_unit(key, 2 * t + e, j)) = (uint16_t)w;
-        }
+        *reinterpret_cast<uint16_t*>(chunk + C::v_unit(key, 2 * t, j)) = (uint16_t)word;
+        *reinterpret_cast<uint16_t*>(chunk + C::v_unit(key, 2 * t + 1, j)) = (uint16_t)(word >> 16);
         if (t == 0) *reinterpret_cast<__half*>(chunk + C::v_scale(key, j)) = s;
       }
     }

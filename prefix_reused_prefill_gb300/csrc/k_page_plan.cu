@@ -189,13 +189,16 @@ __global__ void page_init_kernel(PagesDev p) {
   if (i == 0) *p.count = p.n_pages;
 }
 
-// cos and sin of pos * theta^(-2j/d), in double, rounded once to float
-__global__ void page_rope_kernel(RopeFreq fr, int max_len, int half, float2* table) {
+// cos and sin of pos * theta^(-2j/d), in double, rounded once to float, and the
+// rest of each (at most 2^-25) times 2^24
+__global__ void page_rope_kernel(RopeFreq fr, int max_len, int half, float2* table, __half2* rest) {
   const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
   if (i >= (long long)max_len * half) return;
   double s, c;
   sincos((double)(i / half) * fr.inv[i % half], &s, &c);
-  table[i] = make_float2((float)c, (float)s);
+  const float2 v = make_float2((float)c, (float)s);
+  table[i] = v;
+  rest[i] = __floats2half2_rn((float)((c - v.x) * 16777216.0), (float)((s - v.y) * 16777216.0));
 }
 
 }  // namespace
@@ -210,9 +213,9 @@ cudaError_t launch_page_init(const PagesDev& p, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_page_rope(const RopeFreq& fr, int max_len, int d, float2* table, cudaStream_t st) {
+cudaError_t launch_page_rope(const RopeFreq& fr, int max_len, int d, float2* table, __half2* rest, cudaStream_t st) {
   const long long n = (long long)max_len * (d / 2);
-  page_rope_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(fr, max_len, d / 2, table);
+  page_rope_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(fr, max_len, d / 2, table, rest);
   return cudaGetLastError();
 }
 

@@ -52,7 +52,7 @@ bool valid(const kvr_pages_config* c) {
 }
 
 struct Layout {
-  size_t status, info, count, counters, lens, cu, free_list, row_seq, row_pos, row_slot, table, rope, ml, part, ml_tc, part_tc, shared, total;
+  size_t status, info, count, counters, lens, cu, free_list, row_seq, row_pos, row_slot, table, rope, rope_rest, ml, part, ml_tc, part_tc, shared, total;
   int width;
 };
 Layout layout(const kvr_pages_config* c) {
@@ -77,6 +77,7 @@ Layout layout(const kvr_pages_config* c) {
   L.row_slot = take((size_t)c->max_rows * 4);
   L.table = take((size_t)c->max_seqs * L.width * 4);
   L.rope = take((size_t)c->max_len * (c->head_dim / 2) * sizeof(float2));
+  L.rope_rest = take((size_t)c->max_len * (c->head_dim / 2) * sizeof(__half2));
   L.ml = take((size_t)kPageAttnPartRows * sizeof(float2));
   L.part = take((size_t)kPageAttnPartRows * c->head_dim * sizeof(float));
   L.ml_tc = take((size_t)kPageTcPartRows * sizeof(float2));
@@ -162,6 +163,7 @@ int kvr_pages_create(const kvr_pages_config* cfg, void* pool, size_t pool_bytes,
   d.row_slot = reinterpret_cast<int32_t*>(w + L.row_slot);
   d.info = reinterpret_cast<int32_t*>(w + L.info);
   d.rope = reinterpret_cast<const float2*>(w + L.rope);
+  d.rope_rest = reinterpret_cast<const __half2*>(w + L.rope_rest);
   d.status = reinterpret_cast<int*>(w + L.status);
   d.refused = d.status + 1;
   d.n_pages = cfg->n_pages;
@@ -199,7 +201,7 @@ int kvr_pages_create(const kvr_pages_config* cfg, void* pool, size_t pool_bytes,
   if (e == cudaSuccess) e = launch_page_init(d, nullptr);
   if (e == cudaSuccess)
     e = launch_page_rope(rope_freq(cfg->rope_theta, cfg->head_dim), cfg->max_len, cfg->head_dim,
-                         reinterpret_cast<float2*>(w + L.rope), nullptr);
+                         reinterpret_cast<float2*>(w + L.rope), reinterpret_cast<__half2*>(w + L.rope_rest), nullptr);
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
   if (e != cudaSuccess) {
     delete c;

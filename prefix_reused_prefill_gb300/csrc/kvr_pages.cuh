@@ -68,6 +68,7 @@ struct PagesDev {
   int32_t* row_slot;
   int32_t* info;         // [2]: sequences and rows of the last plan
   const float2* rope;    // [max_len][d / 2] (cos, sin)
+  const __half2* rope_rest;   // what those rounded off, times 2^24
   int* status;           // a wait that gave up
   int* refused;          // the first refused plan's error code
   int n_pages, width, max_len, max_rows, max_seqs;
@@ -141,7 +142,7 @@ constexpr int kPageAttnPartRows = kPageAttnMaxCtas * (2 * 128 + 2 * 16);
 cudaError_t page_plan_setup();
 // every page free, the first ones on top
 cudaError_t launch_page_init(const PagesDev& p, cudaStream_t st);
-cudaError_t launch_page_rope(const RopeFreq& fr, int max_len, int d, float2* table, cudaStream_t st);
+cudaError_t launch_page_rope(const RopeFreq& fr, int max_len, int d, float2* table, __half2* rest, cudaStream_t st);
 cudaError_t launch_page_plan(const PagesDev& p, int n_seq, const int32_t* keep, const int32_t* add, int rows,
                              int max_add, cudaStream_t st);
 cudaError_t launch_page_append(const PagesDev& p, const PageAppend& a, cudaStream_t st);
@@ -183,6 +184,9 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
   return *reinterpret_cast<float2*>(&r);
 }
+
+__device__ __forceinline__ float2 neg2(float2 a) { return mul2(a, make_float2(-1.f, -1.f)); }
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) { return fma2(b, make_float2(-1.f, -1.f), a); }
 
 // two activations of either 16-bit type
 template <bool F16>

@@ -199,6 +199,26 @@ def test_stored_values_are_exact(act, d):
         assert torch.equal(got.nan_to_num(), ref.nan_to_num())
 
 
+@pytest.mark.parametrize("act", ["bf16", "fp16"])
+@pytest.mark.parametrize("d,norm,rotate", [(128, True, True), (64, True, True), (128, False, True), (64, True, False)])
+def test_keys_are_those_of_64_bits(act, d, norm, rotate):
+    """A normed and rotated key next to the border of two activation values or codes takes the side that 64 bits
+    (then 32, then the type) give: it is formed to about 2^-45, which decides all but one in 2^35 of the values here."""
+    rng = np.random.Generator(np.random.PCG64([d, norm, rotate]))
+    pg = handle(2, 2, d, act, rope_theta=1e6, norm_eps=1e-6)
+    pg.kvr_page_plan(ints([0, 0]), ints([500, 12]), 512)
+    pg.kvr_page_plan(ints([500, 12]), ints([0, 500]), 500)
+    k, v = rand(rng, (500, 2, d), act, 2.0), rand(rng, (500, 2, d), act, 0.3)
+    gain = rand(rng, (d,), act) + 1 if norm else None
+    pg.kvr_page_append(0, None, k.cuda(), v.cuda(), None, gain.cuda() if norm else None, rotate=rotate)
+    got = [x.cpu() for x in pg.kvr_page_read(0)]
+    pg.kvr_pages_sync()
+    y = np.stack([op.norm_rotate(f64(k[i]), 12 + i, 1e6, f64(gain) if norm else None, 1e-6, rotate) for i in range(500)])
+    y = f64(torch.from_numpy(y).float().to(TYPES[act]))
+    for x, ref in zip(got, (y, f64(v))):
+        assert torch.equal(x, torch.from_numpy(op.values(ref)).to(TYPES[act]))
+
+
 def test_padded_rows_stay_as_they_were():
     rng = np.random.Generator(np.random.PCG64(5))
     pg = handle(8, 2, 64)
