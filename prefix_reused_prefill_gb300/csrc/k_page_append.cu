@@ -13,19 +13,21 @@
 // neighbouring tokens of a page, so that the 2-byte units of V (a unit never
 // holds two tokens) meet in one 32-byte sector.
 //
-// 8.2k rows of 32 + 2 * 8 heads of 128 with norms: 48.6 us, 3.6 TB/s of 176 MB, 53 %
+// 8.2k rows of 32 + 2 * 8 heads of 128 with norms: 48.0 us, 3.7 TB/s of 176 MB, 54 %
 // of a plain copy's rate.  Of that k's second floats take 7 us (with them k is
 // that of 64 bits in all of 50 million values, in 32 bits two or three codes
 // in 8 million moved), the rest is arithmetic too: issue slots 66 % busy, and more
-// loads in flight (through shared memory) or more and smaller CTAs change
-// nothing.  One to 254 rows: 3.3 to 4 us, a launch.
+// loads in flight (through shared memory) or more CTAs with fewer heads each change
+// nothing.  One to 254 rows: 3 to 4 us, a launch.
 #include "kvr_pages.cuh"
 
 namespace kvr {
 
 namespace {
 
-constexpr int kWarps = 8;
+// 7 CTAs of 4 warps on an SM: 72 registers, which nothing is spilled from (each
+// spilled word is a store past L1: 100 bytes of them a thread made it 66 us and more)
+constexpr int kWarps = 4;
 
 template <int D>
 struct Lanes {
@@ -197,7 +199,7 @@ __device__ __forceinline__ float2 exact_turn(float2 a, float2 na, float2 b, floa
 }
 
 template <int D, bool F16>
-__global__ void __launch_bounds__(32 * kWarps, 4)
+__global__ void __launch_bounds__(32 * kWarps, 7)
 page_append_kernel(const PagesDev p, const PageAppend a) {
   using C = Chunk<D>;
   using L = Lanes<D>;
