@@ -605,6 +605,9 @@ int kvr_page_read(kvr_pages* pages, int layer, void* k_out, void* v_out, int row
  *   out_f16  1: the rows, rounded to the activation type, are stored as fp16.
  *   scale    a positive number.
  * The same call gives the same bits (no atomic adds).  rows must be the plan's.
+ * A captured call keeps the max_add of the plan before it: replayed after a
+ * plan with a larger one it may leave out the rows of long additions, which
+ * kvr_pages_sync reports.
  */
 int kvr_page_attend(kvr_pages* pages, int layer, const void* q, long long q_stride, void* out,
                     int out_f16, float scale, int rows, void* stream);

@@ -307,6 +307,8 @@ page_attn_kernel(const PagesDev p, const PageAttend a) {
     int u = 0, sg = 0, pages = 0;
     if (base) fetch(b);
     const int m = min(row1, rows_all) - row0;
+    // (the launch, captured under another plan, knew of no sequence so long)
+    if (cta == 0 && b < n && p.G * m > a.many && !a.shared && *p.refused == 0) *p.refused = KVR_ERR_UNSUPPORTED;
     if (b < n && m > 0 && p.G * m <= a.many) {
       pages = (len + kPage - 1) / kPage;
       sg = ((p.G * m + C::kRows - 1) / C::kRows) * p.Hkv;

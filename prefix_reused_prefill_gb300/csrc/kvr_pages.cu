@@ -337,6 +337,8 @@ int kvr_pages_sync(kvr_pages* c, void* stream) {
   if (e != cudaSuccess) return cuda_fail(c, e, "page status readback");
   if (word[0]) return fail(c, KVR_ERR_TIMEOUT, "a device-side wait gave up (status %d)", word[0]);
   if (word[1] == KVR_ERR_CAPACITY) return fail(c, KVR_ERR_CAPACITY, "a plan lacked free pages and was not carried out");
+  if (word[1] == KVR_ERR_UNSUPPORTED)
+    return fail(c, KVR_ERR_ARG, "an attend was captured under a smaller max_add than its step's; rows were left out");
   if (word[1]) return fail(c, KVR_ERR_ARG, "a plan's keep or add were out of range; it was not carried out");
   return KVR_OK;
 }

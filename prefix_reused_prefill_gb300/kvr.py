@@ -422,10 +422,11 @@ class Kvr:
         c = self.cfg
         arr = weights[0] if isinstance(weights, tuple) else weights
         m, cols = hidden.shape[0], (c.n_q_heads + 2 * c.n_kv_heads) * c.head_dim
-        if qkv is None:
-            qkv = torch.empty((m, cols), dtype=torch.bfloat16, device=self.device)
-        if out is None:
-            out = torch.empty((m, c.hidden), dtype=torch.bfloat16, device=self.device)
+        with torch.cuda.stream(stream):   # (where one is given) memory that it may write at once
+            if qkv is None:
+                qkv = torch.empty((m, cols), dtype=torch.bfloat16, device=self.device)
+            if out is None:
+                out = torch.empty((m, c.hidden), dtype=torch.bfloat16, device=self.device)
         for name, x, n in (("hidden", hidden, c.hidden), ("qkv", qkv, cols), ("out", out, c.hidden)):
             if x.dtype != torch.bfloat16 or not x.is_cuda or not x.is_contiguous() or x.shape != (m, n):
                 raise KvrError(-1, f"{name} must be a contiguous bf16 device tensor [{m}][{n}]")

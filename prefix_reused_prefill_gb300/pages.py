@@ -124,10 +124,13 @@ class PagedKv:
             raise KvrError(-1, f"{name} must be {self.dtype} [{self.cfg.head_dim}] on {self.device}")
         return x.data_ptr()
 
-    def _out(self, name: str, x: Optional[torch.Tensor], heads: int, dtype) -> torch.Tensor:
+    def _out(self, name: str, x: Optional[torch.Tensor], heads: int, dtype, stream) -> torch.Tensor:
         shape = (self._rows, heads, self.cfg.head_dim)
         if x is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
+            if stream is None:
+                return torch.empty(shape, dtype=dtype, device=self.device)
+            with torch.cuda.stream(stream):   # memory that the stream may write at once
+                return torch.empty(shape, dtype=dtype, device=self.device)
         if x.dtype is not dtype or x.get_device() != self._index or x.shape != shape or not x.is_contiguous():
             raise KvrError(-1, f"{name} must be a contiguous {dtype} tensor of shape {shape} on {self.device}")
         return x
@@ -156,7 +159,7 @@ class PagedKv:
         qs, qp, op = 0, None, None
         if q is not None:
             qs, qp = self._rows_arg("q", q, c.n_q_heads), q.data_ptr()
-            out = self._out("out", out, c.n_q_heads, self.dtype)
+            out = self._out("out", out, c.n_q_heads, self.dtype, stream)
             op = out.data_ptr()
         elif out is not None:
             raise KvrError(-1, "out without q")
@@ -167,8 +170,8 @@ class PagedKv:
 
     def kvr_page_read(self, layer: int, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
         """What the cache holds for the planned rows: k and v [rows][n_kv_heads][head_dim]."""
-        k = self._out("k", None, self.cfg.n_kv_heads, self.dtype)
-        v = self._out("v", None, self.cfg.n_kv_heads, self.dtype)
+        k = self._out("k", None, self.cfg.n_kv_heads, self.dtype, stream)
+        v = self._out("v", None, self.cfg.n_kv_heads, self.dtype, stream)
         self._check(self.lib.kvr_page_read(self.ctx, layer, k.data_ptr(), v.data_ptr(), self._rows,
                                            self._stream(stream)))
         return k, v
@@ -178,7 +181,7 @@ class PagedKv:
         """Causal attention of the planned rows over their sequences (scale: 1 / sqrt(head_dim))."""
         H = self.cfg.n_q_heads
         qs = self._rows_arg("q", q, H)
-        out = self._out("out", out, H, self.dtype)
+        out = self._out("out", out, H, self.dtype, stream)
         self._check(self.lib.kvr_page_attend(self.ctx, layer, q.data_ptr(), qs, out.data_ptr(), 0,
                                              self._scale if scale is None else scale, self._rows,
                                              self._stream(stream)))

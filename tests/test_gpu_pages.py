@@ -598,6 +598,50 @@ def test_calls_on_another_stream():
 
 
 # --------------------------------------------------------------------------- refusals
+def test_results_on_another_stream_take_memory_of_that_stream():
+    pg = handle(8, 2, 64)
+    pg.kvr_page_plan(ints([0]), ints([200]), 200)
+    q, k, v = (torch.ones(200, h, 64, dtype=torch.bfloat16, device="cuda") for h in (8, 2, 2))
+    pg.kvr_page_append(0, None, k, v)
+    side = torch.cuda.Stream()
+    for call in (lambda: pg.kvr_page_attend(0, q, stream=side), lambda: pg.kvr_page_append(0, q, k, v, stream=side)):
+        torch.cuda.synchronize()
+        x = torch.full_like(q, 5)
+        torch.cuda._sleep(100_000_000)
+        y = x.clone()                       # waits behind the sleep; x's memory is free for this stream's next tensor
+        del x
+        out = call()
+        torch.cuda.synchronize()
+        assert (y == 5).all() and not (out == 5).any()
+    pg.kvr_pages_sync()
+
+
+def test_a_captured_attend_after_a_plan_of_longer_additions_is_reported():
+    pg = handle(8, 2, 64)
+    pg.kvr_page_plan(ints([0] * 8), ints([5] * 8), 40, 5)
+    rng = np.random.Generator(np.random.PCG64(11))
+    q, k, v = (rand(rng, (40, h, 64), "bf16").cuda() for h in (8, 2, 2))
+    pg.kvr_page_append(0, None, k, v)
+    out = torch.empty_like(q)
+    pg.kvr_page_attend(0, q, out=out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pg.kvr_page_attend(0, q, out=out)
+    graph.replay()
+    pg.kvr_pages_sync()
+    pg.kvr_page_plan(ints([0] * 8), ints([38, 2] + [0] * 6), 40, 38)
+    pg.kvr_page_append(0, None, k, v)
+    want = pg.kvr_page_attend(0, q)
+    pg.kvr_pages_sync()
+    out.fill_(7)
+    graph.replay()
+    assert code_of(pg.kvr_pages_sync) == -1
+    assert (out[:38] == 7).all() and torch.equal(out[38:], want[38:])
+    assert torch.equal(pg.kvr_page_attend(0, q), want)
+    pg.kvr_pages_sync()
+
+
 def test_refused_calls_change_nothing():
     rng = np.random.Generator(np.random.PCG64(30))
     pg = handle(8, 2, 64, max_seqs=4)
