@@ -13,12 +13,12 @@
 // neighbouring tokens of a page, so that the 2-byte units of V (a unit never
 // holds two tokens) meet in one 32-byte sector.
 //
-// 8.2k rows of 32 + 2 * 8 heads of 128 with norms: 48.0 us, 3.7 TB/s of 176 MB, 54 %
-// of a plain copy's rate.  Of that k's second floats take 7 us (with them k is
+// 8.2k rows of 32 + 2 * 8 heads of 128 with norms: 42.9 us, 4.1 TB/s of 176 MB, 61 %
+// of a plain copy's rate.  Of that k's second floats take 6 us (with them k is
 // that of 64 bits in all of 50 million values, in 32 bits two or three codes
-// in 8 million moved), the rest is arithmetic too: issue slots 66 % busy, and more
-// loads in flight (through shared memory) or more CTAs with fewer heads each change
-// nothing.  One to 254 rows: 3 to 4 us, a launch.
+// in 8 million moved), the rest is arithmetic too, and more loads in flight
+// (through shared memory) or more CTAs for q change nothing.  q, k and v in one loop
+// of the same CTAs: 47.8.  One to 254 rows: 3 to 4 us, a launch.
 #include "kvr_pages.cuh"
 
 namespace kvr {
@@ -213,38 +213,46 @@ page_append_kernel(const PagesDev p, const PageAppend a) {
   const bool live = row < total;
   const int pos = live ? p.row_pos[row] : 0;
   const int slot = live ? p.row_slot[row] : 0;
-  // cosines and sines of this lane's dims 8 l .. 8 l + 7 (read anew for each head,
-  // from L1: in registers they would cost every head more than that)
+  // cosines and sines of this lane's dims 8 l .. 8 l + 7
   const float4* turns = reinterpret_cast<const float4*>(p.rope + (long long)pos * (D / 2) + 8 * l);
   const uint4* turns_rest = reinterpret_cast<const uint4*>(p.rope_rest + (long long)pos * (D / 2) + 8 * l);
-  const int h0 = a.q ? 0 : p.Hq;
-  const int heads = p.Hq + 2 * p.Hkv;
   uint8_t* page = p.pool + p.layer_off + (long long)(slot / kPage) * p.Hkv * C::kBytes;
   const int key = slot % kPage;
-  // this lane's elements of head h of its row.  The next head's are asked for
-  // before this one's are used (61 -> 51 us in the example of the head)
-  auto fetch = [&](int h, uint4& lo, uint4& hi) {
-    if (!live || h >= heads) return;
-    const uint16_t* src;
-    if (h < p.Hq) src = static_cast<const uint16_t*>(a.q) + (long long)row * a.qs + h * D;
-    else if (h < p.Hq + p.Hkv) src = static_cast<const uint16_t*>(a.k) + (long long)row * a.ks + (h - p.Hq) * D;
-    else src = static_cast<const uint16_t*>(a.v) + (long long)row * a.vs + (h - p.Hq - p.Hkv) * D;
-    lo = __ldcs(reinterpret_cast<const uint4*>(src + 8 * l));
-    hi = __ldcs(reinterpret_cast<const uint4*>(src + 8 * l + D / 2));
+  // body(head, this lane's elements of it) for this warp's share of n heads, those of
+  // the CTAs y of ny.  The next head's are asked for before this one's are used
+  // (61 -> 51 us in the example of the head).
+  auto for_heads = [&](const void* base, long long stride, int n, int y, int ny, auto body) {
+    const uint16_t* src = static_cast<const uint16_t*>(base) + (long long)row * stride + 8 * l;
+    uint4 next0 = make_uint4(0, 0, 0, 0), next1 = next0;
+    auto fetch = [&](int h) {
+      if (!live || h >= n) return;
+      next0 = __ldcs(reinterpret_cast<const uint4*>(src + h * D));
+      next1 = __ldcs(reinterpret_cast<const uint4*>(src + h * D + D / 2));
+    };
+    int h = y * kWarps + warp;
+    fetch(h);
+    for (; h < n; h += kWarps * ny) {
+      const uint4 u0 = next0, u1 = next1;
+      fetch(h + kWarps * ny);
+      body(h, u0, u1);
+    }
   };
-  const int step = kWarps * (int)gridDim.y;
-  int h = h0 + (int)blockIdx.y * kWarps + warp;
-  uint4 next0 = make_uint4(0, 0, 0, 0), next1 = next0;
-  fetch(h, next0, next1);
-  for (; h < heads; h += step) {
-    const bool is_q = h < p.Hq, is_k = !is_q && h < p.Hq + p.Hkv;
-    const int hh = is_q ? h : (is_k ? h - p.Hq : h - p.Hq - p.Hkv);
-    uint4 u0 = next0, u1 = next1;
-    fetch(h + step, next0, next1);
-    float2 x[8];
-    unpack8<F16>(u0, x);
-    unpack8<F16>(u1, x + 4);
-    if (is_q) {
+  // q, k and v in CTAs of their own: each then has the registers that it needs
+  const int y = (int)blockIdx.y;
+  if (y < a.ctas_q) {
+    float2 cs[4], sn[4];
+    if (a.rotate) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 v = turns[i];
+        cs[i] = make_float2(v.x, v.z);
+        sn[i] = make_float2(v.y, v.w);
+      }
+    }
+    for_heads(a.q, a.qs, p.Hq, y, a.ctas_q, [&](int h, uint4 u0, uint4 u1) {
+      float2 x[8];
+      unpack8<F16>(u0, x);
+      unpack8<F16>(u1, x + 4);
       if (a.norm_q) {
         float2 s2 = dev::mul2(x[0], x[0]);
 #pragma unroll
@@ -263,71 +271,86 @@ page_append_kernel(const PagesDev p, const PageAppend a) {
       if (a.rotate) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float4 v = turns[i];
-          const float2 lo = x[i], hi = x[4 + i], c = make_float2(v.x, v.z);
-          x[i] = dev::fma2(lo, c, dev::mul2(hi, make_float2(-v.y, -v.w)));
-          x[4 + i] = dev::fma2(hi, c, dev::mul2(lo, make_float2(v.y, v.w)));
+          const float2 lo = x[i], hi = x[4 + i];
+          x[i] = dev::fma2(lo, cs[i], dev::mul2(hi, make_float2(-sn[i].x, -sn[i].y)));
+          x[4 + i] = dev::fma2(hi, cs[i], dev::mul2(lo, sn[i]));
         }
       }
       if (live) {
-        uint16_t* dst = static_cast<uint16_t*>(a.q_out) + ((long long)row * p.Hq + hh) * D + 8 * l;
+        uint16_t* dst = static_cast<uint16_t*>(a.q_out) + ((long long)row * p.Hq + h) * D + 8 * l;
         *reinterpret_cast<uint4*>(dst) = pack8<F16>(x);
         *reinterpret_cast<uint4*>(dst + D / 2) = pack8<F16>(x + 4);
       }
-      continue;
-    }
-    if (is_k && (a.norm_k || a.rotate)) {
-      float2 root = make_float2(1.f, 0.f);
-      if (a.norm_k) {
-        root = exact_rsqrt<D>(x, a.eps);
-        const uint16_t* gp = static_cast<const uint16_t*>(a.norm_k) + 8 * l;
-        const uint4 g[2] = {*reinterpret_cast<const uint4*>(gp), *reinterpret_cast<const uint4*>(gp + D / 2)};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = dev::mul2(x[i], dev::act2<F16>(reinterpret_cast<const uint32_t*>(g)[i]));
-      }
-      if (a.rotate) {
-        const uint4 w[2] = {turns_rest[0], turns_rest[1]};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float4 v = turns[i];
-          const float2 e = dev::act2<true>(reinterpret_cast<const uint32_t*>(w)[2 * i]);
-          const float2 f = dev::act2<true>(reinterpret_cast<const uint32_t*>(w)[2 * i + 1]);
-          const float2 unit = make_float2(5.9604644775390625e-8f, 5.9604644775390625e-8f);   // 2^-24
-          const float2 c_lo = dev::mul2(make_float2(e.x, f.x), unit), s_lo = dev::mul2(make_float2(e.y, f.y), unit);
-          const float2 c = make_float2(v.x, v.z), s = make_float2(v.y, v.w), lo = x[i], hi = x[4 + i];
-          const float2 nlo = dev::neg2(lo), nhi = dev::neg2(hi);
-          x[i] = exact_turn(lo, nlo, hi, nhi, c, s, c_lo, s_lo, a.norm_k, root);
-          x[4 + i] = exact_turn(hi, nhi, nlo, lo, c, s, c_lo, s_lo, a.norm_k, root);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 rr = make_float2(root.x, root.x), y = dev::mul2(x[i], rr);
-          x[i] = dev::add2(y, dev::fma2(x[i], make_float2(root.y, root.y), dev::fma2(x[i], rr, dev::neg2(y))));
-        }
-      }
-      u0 = pack8<F16>(x);
-      u1 = pack8<F16>(x + 4);
-      // the values that the cache quantises are those of the activation type
+    });
+  } else if (y < a.ctas_q + a.ctas_kv) {
+    for_heads(a.k, a.ks, p.Hkv, y - a.ctas_q, a.ctas_kv, [&](int h, uint4 u0, uint4 u1) {
+      float2 x[8];
       unpack8<F16>(u0, x);
       unpack8<F16>(u1, x + 4);
-    }
-    uint8_t* chunk = page + (long long)hh * C::kBytes;
+      if (a.norm_k || a.rotate) {
+        float2 root = make_float2(1.f, 0.f);
+        if (a.norm_k) {
+          root = exact_rsqrt<D>(x, a.eps);
+          const uint16_t* gp = static_cast<const uint16_t*>(a.norm_k) + 8 * l;
+          const uint4 g[2] = {*reinterpret_cast<const uint4*>(gp), *reinterpret_cast<const uint4*>(gp + D / 2)};
 #pragma unroll
-    for (int part = 0; part < 2; ++part) {
-      const int j = part * (C::kGroups / 2) + l / 4;
-      uint32_t word;
-      const __half s = quantise8<F16>(part ? u1 : u0, x + 4 * part, is_k, word);
-      if (!live) continue;
-      if (is_k) {
+          for (int i = 0; i < 8; ++i) x[i] = dev::mul2(x[i], dev::act2<F16>(reinterpret_cast<const uint32_t*>(g)[i]));
+        }
+        if (a.rotate) {
+          const uint4 w[2] = {turns_rest[0], turns_rest[1]};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 v = turns[i];
+            const float2 e = dev::act2<true>(reinterpret_cast<const uint32_t*>(w)[2 * i]);
+            const float2 f = dev::act2<true>(reinterpret_cast<const uint32_t*>(w)[2 * i + 1]);
+            const float2 unit = make_float2(5.9604644775390625e-8f, 5.9604644775390625e-8f);   // 2^-24
+            const float2 c_lo = dev::mul2(make_float2(e.x, f.x), unit), s_lo = dev::mul2(make_float2(e.y, f.y), unit);
+            const float2 c = make_float2(v.x, v.z), s = make_float2(v.y, v.w), lo = x[i], hi = x[4 + i];
+            const float2 nlo = dev::neg2(lo), nhi = dev::neg2(hi);
+            x[i] = exact_turn(lo, nlo, hi, nhi, c, s, c_lo, s_lo, a.norm_k, root);
+            x[4 + i] = exact_turn(hi, nhi, nlo, lo, c, s, c_lo, s_lo, a.norm_k, root);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float2 rr = make_float2(root.x, root.x), z = dev::mul2(x[i], rr);
+            x[i] = dev::add2(z, dev::fma2(x[i], make_float2(root.y, root.y), dev::fma2(x[i], rr, dev::neg2(z))));
+          }
+        }
+        u0 = pack8<F16>(x);
+        u1 = pack8<F16>(x + 4);
+        // the values that the cache quantises are those of the activation type
+        unpack8<F16>(u0, x);
+        unpack8<F16>(u1, x + 4);
+      }
+      uint8_t* chunk = page + (long long)h * C::kBytes;
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {
+        const int j = part * (C::kGroups / 2) + l / 4;
+        uint32_t word;
+        const __half s = quantise8<F16>(part ? u1 : u0, x + 4 * part, true, word);
+        if (!live) continue;
         *reinterpret_cast<uint32_t*>(chunk + C::k_word(key, t, j)) = word;
         if (t == 0) *reinterpret_cast<__half*>(chunk + C::k_scale(key, j)) = s;
-      } else {
+      }
+    });
+  } else {
+    for_heads(a.v, a.vs, p.Hkv, y - a.ctas_q - a.ctas_kv, a.ctas_kv, [&](int h, uint4 u0, uint4 u1) {
+      float2 x[8];
+      unpack8<F16>(u0, x);
+      unpack8<F16>(u1, x + 4);
+      uint8_t* chunk = page + (long long)h * C::kBytes;
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {
+        const int j = part * (C::kGroups / 2) + l / 4;
+        uint32_t word;
+        const __half s = quantise8<F16>(part ? u1 : u0, x + 4 * part, false, word);
+        if (!live) continue;
         *reinterpret_cast<uint16_t*>(chunk + C::v_unit(key, 2 * t, j)) = (uint16_t)word;
         *reinterpret_cast<uint16_t*>(chunk + C::v_unit(key, 2 * t + 1, j)) = (uint16_t)(word >> 16);
         if (t == 0) *reinterpret_cast<__half*>(chunk + C::v_scale(key, j)) = s;
       }
-    }
+    });
   }
 }
 
@@ -384,9 +407,12 @@ dim3 row_grid(int rows, int per, int heads) {
 
 }  // namespace
 
-cudaError_t launch_page_append(const PagesDev& p, const PageAppend& a, cudaStream_t st) {
-  const int heads = (a.q ? p.Hq : 0) + 2 * p.Hkv;
-  const dim3 grid = row_grid(a.rows, p.d == 128 ? Lanes<128>::kRows : Lanes<64>::kRows, heads);
+cudaError_t launch_page_append(const PagesDev& p, PageAppend a, cudaStream_t st) {
+  const int per = p.d == 128 ? Lanes<128>::kRows : Lanes<64>::kRows;
+  dim3 grid = row_grid(a.rows, per, p.Hkv);
+  a.ctas_kv = (int)grid.y;
+  a.ctas_q = a.q ? (int)row_grid(a.rows, per, p.Hq).y : 0;
+  grid.y = (unsigned)(a.ctas_q + 2 * a.ctas_kv);
   if (p.d == 128)
     return p.f16 ? launch_k(page_append_kernel<128, true>, grid, 32 * kWarps, 0, st, p, a)
                  : launch_k(page_append_kernel<128, false>, grid, 32 * kWarps, 0, st, p, a);

@@ -87,6 +87,7 @@ struct PageAppend {
   void* q_out;
   int rotate, rows;
   float eps;
+  int ctas_q, ctas_kv;       // CTAs of a row group for the heads of q, and of k and v each
 };
 
 // A segment of the tensor-memory kernel (a sequence, pair of row tiles and KV
@@ -145,7 +146,7 @@ cudaError_t launch_page_init(const PagesDev& p, cudaStream_t st);
 cudaError_t launch_page_rope(const RopeFreq& fr, int max_len, int d, float2* table, __half2* rest, cudaStream_t st);
 cudaError_t launch_page_plan(const PagesDev& p, int n_seq, const int32_t* keep, const int32_t* add, int rows,
                              int max_add, cudaStream_t st);
-cudaError_t launch_page_append(const PagesDev& p, const PageAppend& a, cudaStream_t st);
+cudaError_t launch_page_append(const PagesDev& p, PageAppend a, cudaStream_t st);
 cudaError_t launch_page_read(const PagesDev& p, void* k_out, void* v_out, int rows, cudaStream_t st);
 cudaError_t page_attn_setup();
 cudaError_t launch_page_attn(const PagesDev& p, const PageAttend& a, int nt, int ctas, cudaStream_t st);
