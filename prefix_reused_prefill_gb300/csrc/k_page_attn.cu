@@ -17,7 +17,7 @@
 // two so that any bf16 q is an fp16 number.
 //
 // Keys are the M side of both products (m16n8k16, S^T = K Q^T and O^T = V^T P^T):
-// the rows, at most 8 or 16 of a tile, fill the narrow N side.
+// the rows, at most 8 of a tile, fill the narrow N side.
 //
 // Bound by HBM: a page of one KV head is 9216 contiguous bytes (head dim 128),
 // fetched as two bulk copies, K and V.  The work, all (sequence, row tile, KV
@@ -36,24 +36,24 @@
 // Of both about 3 us go before the first page and 5 to 8 us to the last pages, the
 // parts and their merge; between them an SM takes about 400 cycles a page, 300 at
 // the copy's rate.  One sequence over 726: 9.8 us.  Four of 8 rows over 15360
-// (groups of 7): 52 us, where four tiles of 16 rows each decode the pages anew
-// (800 cycles a page and tile).
+// (groups of 7): 50 us, where seven tiles of 8 rows each decode the pages anew.
 #include "kvr_pages.cuh"
 
 namespace kvr {
 
 namespace {
 
-// 16 warps where their registers allow it (tiles of 8 rows): one warp alone
-// waits for its loads and products most of the time.
-template <int D, int NT>
+// 16 warps: one alone waits for its loads and products most of the time.  (Tiles of
+// 16 rows, with the registers of 8 warps, take 830 cycles a page instead of 430 and
+// had half the warps for start and merge: 14 rows over 15360 tokens 51 us, 19 so.)
+template <int D>
 struct Cfg {
-  static constexpr int kWarps = NT == 1 ? 16 : 8;
+  static constexpr int kWarps = 16;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kGroups = D / 32;
   static constexpr int kHalf = Chunk<D>::kHalf;
   static constexpr int kStages = 48 / kWarps * (128 / D);   // halves of pages
-  static constexpr int kRows = 8 * NT;
+  static constexpr int kRows = 8;
   static constexpr int kRing = kStages * kHalf;
   static constexpr int kSlot = kRows * D;                   // floats of a partial result
   static_assert(kSlot * 4 + kRows * 8 <= kRing, "a partial result fits the ring");
@@ -185,14 +185,15 @@ struct Slot {
 };
 
 // Merge the parts of the segments that CTAs of the tensor-memory kernel share:
-// a warp takes four rows, a lane D / 32 dims of each, and all four rows' loads
-// are in flight together.  The whole grid shares the rows of all segments.
+// a warp takes two rows, a lane D / 32 dims of each, and the loads of four parts of
+// both are in flight together (four rows: 41 instead of 33 us where 84 rows over
+// 15360 tokens have parts of 60 CTAs).  The whole grid shares the rows of all segments.
 template <int D, bool F16>
 __device__ void merge_tc(const PagesDev& p, const PageAttend& a, int warp_id, int warps) {
-  constexpr int kPer = D / 32, kGroups4 = kPageTcRows / 4;
-  const int lane = threadIdx.x & 31, r0 = 4 * (warp_id % kGroups4);
+  constexpr int kPer = D / 32, kRows = 2, kGroups = kPageTcRows / kRows;
+  const int lane = threadIdx.x & 31, r0 = kRows * (warp_id % kGroups);
   // the segments that start in CTAs first, first + step, ..; a lane looks at each
-  const int first = warp_id / kGroups4, step = warps / kGroups4;
+  const int first = warp_id / kGroups, step = warps / kGroups;
   const int mine = first + step * lane;
   uint32_t todo = __ballot_sync(0xffffffffu, mine < (int)gridDim.x && a.shared[mine].parts > 0);
   for (; todo; todo &= todo - 1) {
@@ -200,9 +201,9 @@ __device__ void merge_tc(const PagesDev& p, const PageAttend& a, int warp_id, in
     const PageShared s = a.shared[ca];
     const int rows = min(kPageTcRows, s.R - kPageTcRows * s.tile);
     if (r0 >= rows) continue;
-    float m[4], l[4], x[4][kPer];
+    float m[kRows], l[kRows], x[kRows][kPer];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < kRows; ++q) {
       m[q] = -INFINITY;
       l[q] = 0.f;
 #pragma unroll
@@ -211,10 +212,10 @@ __device__ void merge_tc(const PagesDev& p, const PageAttend& a, int warp_id, in
 #pragma unroll 4
     for (int k = 0; k < s.parts; ++k) {
       const long long at = ((long long)(ca + k) * 2 + (k == 0 ? 1 : 0)) * kPageTcRows + r0;
-      float2 ml[4];
-      float y[4][kPer];
+      float2 ml[kRows];
+      float y[kRows][kPer];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {   // (a slot has whole tiles of rows)
+      for (int q = 0; q < kRows; ++q) {   // (a slot has whole tiles of rows)
         ml[q] = __ldcg(a.tc_ml + at + q);
         const float* src = a.tc_part + (at + q) * D + kPer * lane;
         if (kPer == 4) {
@@ -226,7 +227,7 @@ __device__ void merge_tc(const PagesDev& p, const PageAttend& a, int warp_id, in
         }
       }
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+      for (int q = 0; q < kRows; ++q) {
         // (a part in which the row saw nothing counts as it is: zeros, or NaN)
         const float m_new = fmaxf(m[q], ml[q].x);
         const float old = m[q] == m_new ? 1.f : ex2_approx(m[q] - m_new);
@@ -238,7 +239,7 @@ __device__ void merge_tc(const PagesDev& p, const PageAttend& a, int warp_id, in
       }
     }
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < kRows; ++q) {
       if (r0 + q >= rows) break;
       const float inv = l[q] == 0.f ? 0.f : 1.f / l[q];
       const int rho = kPageTcRows * s.tile + r0 + q;
@@ -256,10 +257,10 @@ __device__ void merge_tc(const PagesDev& p, const PageAttend& a, int warp_id, in
   }
 }
 
-template <int D, int NT, bool F16>
-__global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
+template <int D, bool F16>
+__global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 page_attn_kernel(const PagesDev p, const PageAttend a) {
-  using C = Cfg<D, NT>;
+  using C = Cfg<D>;
   using K = Chunk<D>;
   constexpr int kG = C::kGroups, kWarps = C::kWarps, kThreads = C::kThreads;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -474,17 +475,17 @@ page_attn_kernel(const PagesDev p, const PageAttend a) {
     };
 
     Place s = place_of(w0);
-    uint32_t qb[NT][kG][4];       // dims 32 j + 8 t + 0..7 of row 8 n + g, the B side of the K codes
-    float f[NT][2];               // sums -> scores in log2 units
-    int see[NT][2];               // last key these rows see
-    float m_run[NT][2], l_run[NT][2];
-    float o[NT][2 * kG][4];       // O^T tiles 2 j, 2 j + 1: rows g, g + 8 are dims 32 j + 4 g + 0, 1 and + 2, 3
+    uint32_t qb[kG][4];       // dims 32 j + 8 t + 0..7 of row 8 n + g, the B side of the K codes
+    float f[2];               // sums -> scores in log2 units
+    int see[2];               // last key these rows see
+    float m_run[2], l_run[2];
+    float o[2 * kG][4];       // O^T tiles 2 j, 2 j + 1: rows g, g + 8 are dims 32 j + 4 g + 0, 1 and + 2, 3
     bool fresh = true;
     const uint32_t k1024 = held(0x64006400u), k64 = held(0x54005400u);
 
-    // row 8 nn + g of the tile: this lane's dims of it
-    auto load_q = [&](const Place& at, int nn, uint4* raw) {
-      const int rho = at.tile * C::kRows + 8 * nn + g;
+    // row g of the tile: this lane's dims of it
+    auto load_q = [&](const Place& at, uint4* raw) {
+      const int rho = at.tile * C::kRows + g;
       const int tok = token_of(rho);
       const uint16_t* src_q = static_cast<const uint16_t*>(a.q) + (long long)(at.row0 + tok) * a.qs +
                               (at.kv * p.G + rho - tok * p.G) * D + 8 * t;
@@ -502,7 +503,7 @@ page_attn_kernel(const PagesDev p, const PageAttend a) {
       if (!arrived()) return false;
       const uint8_t* page = smem + warp * C::kRing + stage * C::kHalf;
       // ---- scores of 64 keys
-      float sc[4][NT][4];
+      float sc[4][4];
 #pragma unroll
       for (int mt = 0; mt < 4; ++mt) {
         uint32_t w0k[kG], w1k[kG];
@@ -512,9 +513,7 @@ page_attn_kernel(const PagesDev p, const PageAttend a) {
         lds_scales<kG>(page + K::k_scale(16 * mt + g, 0), s0);
         lds_scales<kG>(page + K::k_scale(16 * mt + 8 + g, 0), s1);
 #pragma unroll
-        for (int nn = 0; nn < NT; ++nn)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) sc[mt][nn][c] = 0.f;
+        for (int c = 0; c < 4; ++c) sc[mt][c] = 0.f;
 #pragma unroll
         for (int j = 0; j < kG; ++j) {
           const uint32_t x0 = w0k[j], x1 = w1k[j], y0 = x0 >> 8, y1 = x1 >> 8;
@@ -522,16 +521,13 @@ page_attn_kernel(const PagesDev p, const PageAttend a) {
                          a3 = centred_hi(x1, k64);
           const uint32_t b0 = centred_lo(y0, k1024), b1 = centred_lo(y1, k1024), b2 = centred_hi(y0, k64),
                          b3 = centred_hi(y1, k64);
-#pragma unroll
-          for (int nn = 0; nn < NT; ++nn) {
-            float acc[4];
-            mma_first(acc, a0, a1, a2, a3, qb[nn][j][0], qb[nn][j][1]);
-            mma(acc, b0, b1, b2, b3, qb[nn][j][2], qb[nn][j][3]);
-            sc[mt][nn][0] = fmaf(acc[0], s0[j], sc[mt][nn][0]);
-            sc[mt][nn][1] = fmaf(acc[1], s0[j], sc[mt][nn][1]);
-            sc[mt][nn][2] = fmaf(acc[2], s1[j], sc[mt][nn][2]);
-            sc[mt][nn][3] = fmaf(acc[3], s1[j], sc[mt][nn][3]);
-          }
+          float acc[4];
+          mma_first(acc, a0, a1, a2, a3, qb[j][0], qb[j][1]);
+          mma(acc, b0, b1, b2, b3, qb[j][2], qb[j][3]);
+          sc[mt][0] = fmaf(acc[0], s0[j], sc[mt][0]);
+          sc[mt][1] = fmaf(acc[1], s0[j], sc[mt][1]);
+          sc[mt][2] = fmaf(acc[2], s1[j], sc[mt][2]);
+          sc[mt][3] = fmaf(acc[3], s1[j], sc[mt][3]);
         }
       }
       used();
@@ -539,57 +535,52 @@ page_attn_kernel(const PagesDev p, const PageAttend a) {
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-          for (int nn = 0; nn < NT; ++nn)
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              if (key_base + 16 * mt + g + 8 * (c >> 1) > see[nn][c & 1]) sc[mt][nn][c] = -INFINITY;
+          for (int c = 0; c < 4; ++c)
+            if (key_base + 16 * mt + g + 8 * (c >> 1) > see[c & 1]) sc[mt][c] = -INFINITY;
       }
       // ---- running maximum and weights
-      uint32_t pw[4][NT][2];
+      uint32_t pw[4][2];
+      // (the factors f are positive: the maximum is taken before them)
+      float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-      for (int nn = 0; nn < NT; ++nn) {
-        // (the factors f are positive: the maximum is taken before them)
-        float mx[2] = {-INFINITY, -INFINITY};
+      for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt)
+        for (int c = 0; c < 4; ++c) mx[c & 1] = fmaxf(mx[c & 1], sc[mt][c]);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) mx[c & 1] = fmaxf(mx[c & 1], sc[mt][nn][c]);
+      for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], d));
+        mx[c] *= f[c];
+      }
+      const bool moved = mx[0] > m_run[0] || mx[1] > m_run[1];
+      if (__any_sync(0xffffffffu, moved)) {
+        float corr[2];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-#pragma unroll
-          for (int d = 4; d < 32; d <<= 1) mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], d));
-          mx[c] *= f[nn][c];
+          const float m_new = fmaxf(m_run[c], mx[c]);
+          corr[c] = m_run[c] == -INFINITY ? 0.f : ex2_approx(m_run[c] - m_new);
+          m_run[c] = m_new;
+          l_run[c] *= corr[c];
         }
-        const bool moved = mx[0] > m_run[nn][0] || mx[1] > m_run[nn][1];
-        if (__any_sync(0xffffffffu, moved)) {
-          float corr[2];
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const float m_new = fmaxf(m_run[nn][c], mx[c]);
-            corr[c] = m_run[nn][c] == -INFINITY ? 0.f : ex2_approx(m_run[nn][c] - m_new);
-            m_run[nn][c] = m_new;
-            l_run[nn][c] *= corr[c];
-          }
+        for (int i = 0; i < 2 * kG; ++i)
 #pragma unroll
-          for (int i = 0; i < 2 * kG; ++i)
+          for (int c = 0; c < 4; ++c) o[i][c] *= corr[c & 1];
+      }
+      // weights with a factor of 4 (in O and in l alike)
+      float sub[2];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) o[nn][i][c] *= corr[c & 1];
+      for (int c = 0; c < 2; ++c) sub[c] = m_run[c] == -INFINITY ? 0.f : m_run[c] - 2.f;
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) {
+        float e[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          e[c] = ex2_approx(fmaf(sc[mt][c], f[c & 1], -sub[c & 1]));
+          l_run[c & 1] += e[c];
         }
-        // weights with a factor of 4 (in O and in l alike)
-        float sub[2];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) sub[c] = m_run[nn][c] == -INFINITY ? 0.f : m_run[nn][c] - 2.f;
-#pragma unroll
-        for (int mt = 0; mt < 4; ++mt) {
-          float e[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            e[c] = ex2_approx(fmaf(sc[mt][nn][c], f[nn][c & 1], -sub[c & 1]));
-            l_run[nn][c & 1] += e[c];
-          }
-          pw[mt][nn][0] = transpose8x8(dev::pack_act<true>(e[0], e[1]));
-          pw[mt][nn][1] = transpose8x8(dev::pack_act<true>(e[2], e[3]));
-        }
+        pw[mt][0] = transpose8x8(dev::pack_act<true>(e[0], e[1]));
+        pw[mt][1] = transpose8x8(dev::pack_act<true>(e[2], e[3]));
       }
       // ---- weighted values
       if (!arrived()) return false;
@@ -601,27 +592,22 @@ page_attn_kernel(const PagesDev p, const PageAttend a) {
         lds_words<kG>(page + K::kV + (((2 * mt + 1) * 8 + g) * 4 + t) * kG * 4, v1);
         lds_words<kG>(page + K::kVs + ((mt * 4 + t) * 2 + 0) * kG * 4, s0);
         lds_words<kG>(page + K::kVs + ((mt * 4 + t) * 2 + 1) * kG * 4, s1);
-        uint32_t b0[kG][NT], b1[kG][NT];
+        uint32_t b0[kG], b1[kG];
 #pragma unroll
-        for (int nn = 0; nn < NT; ++nn)
-#pragma unroll
-          for (int j = 0; j < kG; ++j) {
-            b0[j][nn] = hmul2(pw[mt][nn][0], s0[j]);
-            b1[j][nn] = hmul2(pw[mt][nn][1], s1[j]);
-          }
+        for (int j = 0; j < kG; ++j) {
+          b0[j] = hmul2(pw[mt][0], s0[j]);
+          b1[j] = hmul2(pw[mt][1], s1[j]);
+        }
         if (!whole) {
           // a weight of zero takes nothing, whatever stands in a place behind the
           // row's last key (an unwritten scale, a NaN)
+          const uint32_t p0 = pw[mt][0], p1 = pw[mt][1];
+          const uint32_t keep0 = ((p0 & 0xffffu) ? 0xffffu : 0u) | ((p0 >> 16) ? 0xffff0000u : 0u);
+          const uint32_t keep1 = ((p1 & 0xffffu) ? 0xffffu : 0u) | ((p1 >> 16) ? 0xffff0000u : 0u);
 #pragma unroll
-          for (int nn = 0; nn < NT; ++nn) {
-            const uint32_t p0 = pw[mt][nn][0], p1 = pw[mt][nn][1];
-            const uint32_t keep0 = ((p0 & 0xffffu) ? 0xffffu : 0u) | ((p0 >> 16) ? 0xffff0000u : 0u);
-            const uint32_t keep1 = ((p1 & 0xffffu) ? 0xffffu : 0u) | ((p1 >> 16) ? 0xffff0000u : 0u);
-#pragma unroll
-            for (int j = 0; j < kG; ++j) {
-              b0[j][nn] &= keep0;
-              b1[j][nn] &= keep1;
-            }
+          for (int j = 0; j < kG; ++j) {
+            b0[j] &= keep0;
+            b1[j] &= keep1;
           }
         }
 #pragma unroll
@@ -631,11 +617,8 @@ page_attn_kernel(const PagesDev p, const PageAttend a) {
                          e3 = centred_hi(x1, k64);
           const uint32_t f0 = centred_lo(y0, k1024), f1 = centred_hi(y0, k64), f2 = centred_lo(y1, k1024),
                          f3 = centred_hi(y1, k64);
-#pragma unroll
-          for (int nn = 0; nn < NT; ++nn) {
-            mma(o[nn][2 * j], e0, e1, e2, e3, b0[j][nn], b1[j][nn]);
-            mma(o[nn][2 * j + 1], f0, f1, f2, f3, b0[j][nn], b1[j][nn]);
-          }
+          mma(o[2 * j], e0, e1, e2, e3, b0[j], b1[j]);
+          mma(o[2 * j + 1], f0, f1, f2, f3, b0[j], b1[j]);
         }
       }
       used();
@@ -645,51 +628,48 @@ page_attn_kernel(const PagesDev p, const PageAttend a) {
     for (int u = w0; u < w1 && ok; ++u) {
       if (fresh) {
         fresh = false;
+        uint4 raw[kG];
+        load_q(s, raw);
+        float top = 0.f;
 #pragma unroll
-        for (int nn = 0; nn < NT; ++nn) {
-          uint4 raw[kG];
-          load_q(s, nn, raw);
-          float top = 0.f;
+        for (int j = 0; j < kG; ++j) {
+          const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
 #pragma unroll
-          for (int j = 0; j < kG; ++j) {
-            const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 x = dev::act2<F16>(w[i]);
-              top = fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y)));
-            }
+          for (int i = 0; i < 4; ++i) {
+            const float2 x = dev::act2<F16>(w[i]);
+            top = fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y)));
           }
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          // 2^e with |q| 2^e in [2^10, 2^11); e from the exponent field, kept
-          // where both 2^e and its inverse are normal numbers
-          int e = 137 - (int)(__float_as_uint(top) >> 23);
-          e = top > 0.f ? max(-100, min(100, e)) : 0;
-          const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-#pragma unroll
-          for (int j = 0; j < kG; ++j) {
-            const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 x = dev::act2<F16>(w[i]);
-              qb[nn][j][i] = dev::pack_act<true>(x.x * up, x.y * up);
-            }
-          }
-          const float back = __uint_as_float((uint32_t)(127 - e) << 23) * a.scale_log2;
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int from = (2 * t + c) * 4;
-            f[nn][c] = __shfl_sync(0xffffffffu, back, from);
-            const int rc = s.tile * C::kRows + 8 * nn + 2 * t + c;
-            see[nn][c] = rc < p.G * s.m ? s.P + token_of(rc) : -1;
-            m_run[nn][c] = -INFINITY;
-            l_run[nn][c] = 0.f;
-          }
-#pragma unroll
-          for (int i = 0; i < 2 * kG; ++i)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) o[nn][i][c] = 0.f;
         }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // 2^e with |q| 2^e in [2^10, 2^11); e from the exponent field, kept
+        // where both 2^e and its inverse are normal numbers
+        int e = 137 - (int)(__float_as_uint(top) >> 23);
+        e = top > 0.f ? max(-100, min(100, e)) : 0;
+        const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+        for (int j = 0; j < kG; ++j) {
+          const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 x = dev::act2<F16>(w[i]);
+            qb[j][i] = dev::pack_act<true>(x.x * up, x.y * up);
+          }
+        }
+        const float back = __uint_as_float((uint32_t)(127 - e) << 23) * a.scale_log2;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int from = (2 * t + c) * 4;
+          f[c] = __shfl_sync(0xffffffffu, back, from);
+          const int rc = s.tile * C::kRows + 2 * t + c;
+          see[c] = rc < p.G * s.m ? s.P + token_of(rc) : -1;
+          m_run[c] = -INFINITY;
+          l_run[c] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 2 * kG; ++i)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) o[i][c] = 0.f;
       }
       ok = page_step();
       if (!ok) break;
@@ -701,37 +681,34 @@ page_attn_kernel(const PagesDev p, const PageAttend a) {
         const bool alone = seg_end && seg0 >= w0;
         const int rec = 2 * warp + (u + 1 == w1 ? 1 : 0);
         const Slot out = warp_slot(rec);
+        float l[2], inv[2];
+        long long row[2];
 #pragma unroll
-        for (int nn = 0; nn < NT; ++nn) {
-          float l[2], inv[2];
-          long long row[2];
+        for (int c = 0; c < 2; ++c) {
+          l[c] = l_run[c];
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) l[c] += __shfl_xor_sync(0xffffffffu, l[c], d);
+          // (a NaN sum stays one)
+          inv[c] = alone ? (l[c] == 0.f ? 0.f : 1.f / l[c]) : 1.f;
+          row[c] = alone ? out_row(s.tile, s.kv, s.row0, s.m, 2 * t + c) : 0;
+        }
+#pragma unroll
+        for (int j = 0; j < kG; ++j) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            l[c] = l_run[nn][c];
-#pragma unroll
-            for (int d = 4; d < 32; d <<= 1) l[c] += __shfl_xor_sync(0xffffffffu, l[c], d);
-            // (a NaN sum stays one)
-            inv[c] = alone ? (l[c] == 0.f ? 0.f : 1.f / l[c]) : 1.f;
-            row[c] = alone ? out_row(s.tile, s.kv, s.row0, s.m, 8 * nn + 2 * t + c) : 0;
-          }
-#pragma unroll
-          for (int j = 0; j < kG; ++j) {
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const float x = o[nn][2 * j][c] * inv[c], y = o[nn][2 * j][2 + c] * inv[c];
-              const float z = o[nn][2 * j + 1][c] * inv[c], w = o[nn][2 * j + 1][2 + c] * inv[c];
-              if (alone) {
-                if (row[c] >= 0) store4(row[c], 32 * j + 4 * g, x, y, z, w);
-              } else {
-                *reinterpret_cast<float4*>(out.o + (8 * nn + 2 * t + c) * D + 32 * j + 4 * g) =
-                    make_float4(x, y, z, w);
-              }
+            const float x = o[2 * j][c] * inv[c], y = o[2 * j][2 + c] * inv[c];
+            const float z = o[2 * j + 1][c] * inv[c], w = o[2 * j + 1][2 + c] * inv[c];
+            if (alone) {
+              if (row[c] >= 0) store4(row[c], 32 * j + 4 * g, x, y, z, w);
+            } else {
+              *reinterpret_cast<float4*>(out.o + (2 * t + c) * D + 32 * j + 4 * g) =
+                  make_float4(x, y, z, w);
             }
           }
-          if (!alone && g == 0) {
+        }
+        if (!alone && g == 0) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) out.ml[8 * nn + 2 * t + c] = make_float2(m_run[nn][c], l[c]);
-          }
+          for (int c = 0; c < 2; ++c) out.ml[2 * t + c] = make_float2(m_run[c], l[c]);
         }
         if (!alone) {
           if (lane == 0) {
@@ -862,39 +839,31 @@ page_attn_kernel(const PagesDev p, const PageAttend a) {
   }
 }
 
-template <int D, int NT, bool F16>
+template <int D, bool F16>
 cudaError_t setup_one() {
-  using C = Cfg<D, NT>;
-  return cudaFuncSetAttribute(page_attn_kernel<D, NT, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  using C = Cfg<D>;
+  return cudaFuncSetAttribute(page_attn_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               C::kWarps * C::kRing);
 }
-template <int D, int NT, bool F16>
+template <int D, bool F16>
 cudaError_t launch_one(const PagesDev& p, const PageAttend& a, int ctas, cudaStream_t st) {
-  using C = Cfg<D, NT>;
-  return launch_k(page_attn_kernel<D, NT, F16>, dim3(ctas), C::kThreads, (size_t)C::kWarps * C::kRing, st, p, a);
+  using C = Cfg<D>;
+  return launch_k(page_attn_kernel<D, F16>, dim3(ctas), C::kThreads, (size_t)C::kWarps * C::kRing, st, p, a);
 }
 
 }  // namespace
 
 cudaError_t page_attn_setup() {
-  cudaError_t e = setup_one<128, 1, false>();
-  if (e == cudaSuccess) e = setup_one<128, 2, false>();
-  if (e == cudaSuccess) e = setup_one<64, 1, false>();
-  if (e == cudaSuccess) e = setup_one<64, 2, false>();
-  if (e == cudaSuccess) e = setup_one<128, 1, true>();
-  if (e == cudaSuccess) e = setup_one<128, 2, true>();
-  if (e == cudaSuccess) e = setup_one<64, 1, true>();
-  if (e == cudaSuccess) e = setup_one<64, 2, true>();
+  cudaError_t e = setup_one<128, false>();
+  if (e == cudaSuccess) e = setup_one<64, false>();
+  if (e == cudaSuccess) e = setup_one<128, true>();
+  if (e == cudaSuccess) e = setup_one<64, true>();
   return e;
 }
 
-cudaError_t launch_page_attn(const PagesDev& p, const PageAttend& a, int nt, int ctas, cudaStream_t st) {
-  if (p.d == 128) {
-    if (p.f16) return nt == 1 ? launch_one<128, 1, true>(p, a, ctas, st) : launch_one<128, 2, true>(p, a, ctas, st);
-    return nt == 1 ? launch_one<128, 1, false>(p, a, ctas, st) : launch_one<128, 2, false>(p, a, ctas, st);
-  }
-  if (p.f16) return nt == 1 ? launch_one<64, 1, true>(p, a, ctas, st) : launch_one<64, 2, true>(p, a, ctas, st);
-  return nt == 1 ? launch_one<64, 1, false>(p, a, ctas, st) : launch_one<64, 2, false>(p, a, ctas, st);
+cudaError_t launch_page_attn(const PagesDev& p, const PageAttend& a, int ctas, cudaStream_t st) {
+  if (p.d == 128) return p.f16 ? launch_one<128, true>(p, a, ctas, st) : launch_one<128, false>(p, a, ctas, st);
+  return p.f16 ? launch_one<64, true>(p, a, ctas, st) : launch_one<64, false>(p, a, ctas, st);
 }
 
 }  // namespace kvr

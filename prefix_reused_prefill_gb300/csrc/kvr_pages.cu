@@ -317,7 +317,7 @@ int kvr_page_attend(kvr_pages* c, int layer, const void* q, long long q_stride, 
     a.tc_part = b.part;
     a.tc_ml = b.ml;
   }
-  e = launch_page_attn(d, a, std::min<long long>(most, a.many) <= 8 ? 1 : 2, c->ctas, st);
+  e = launch_page_attn(d, a, c->ctas, st);
   return e == cudaSuccess ? KVR_OK : cuda_fail(c, e, "page attention launch");
 }
 

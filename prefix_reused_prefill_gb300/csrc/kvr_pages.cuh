@@ -136,9 +136,9 @@ constexpr int kPageTcRows = 256;
 
 constexpr int kPageAttnMaxCtas = 160;
 constexpr int kPageTcPartRows = kPageAttnMaxCtas * 2 * kPageTcRows;
-// partial results of the split kernel, in rows: two tiles per warp (16 warps
-// with tiles of 8 rows, 8 warps with 16 rows) and two per CTA
-constexpr int kPageAttnPartRows = kPageAttnMaxCtas * (2 * 128 + 2 * 16);
+// partial results of the split kernel, in rows: two tiles of 8 for each of 16 warps
+// and two per CTA
+constexpr int kPageAttnPartRows = kPageAttnMaxCtas * (2 * 128 + 2 * 8);
 
 cudaError_t page_plan_setup();
 // every page free, the first ones on top
@@ -149,7 +149,7 @@ cudaError_t launch_page_plan(const PagesDev& p, int n_seq, const int32_t* keep, 
 cudaError_t launch_page_append(const PagesDev& p, PageAppend a, cudaStream_t st);
 cudaError_t launch_page_read(const PagesDev& p, void* k_out, void* v_out, int rows, cudaStream_t st);
 cudaError_t page_attn_setup();
-cudaError_t launch_page_attn(const PagesDev& p, const PageAttend& a, int nt, int ctas, cudaStream_t st);
+cudaError_t launch_page_attn(const PagesDev& p, const PageAttend& a, int ctas, cudaStream_t st);
 cudaError_t page_attn_tc_setup();
 cudaError_t launch_page_attn_tc(const PagesDev& p, const PageAttendTc& a, int ctas, cudaStream_t st);
 
