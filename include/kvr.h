@@ -481,7 +481,8 @@ const char* kvr_last_error(const kvr_ctx* ctx);
  *   n_layers, n_q_heads, n_kv_heads, head_dim   as kvr_config (head_dim 64 or
  *               128, at most 64 query heads per KV head).
  *   max_seqs    sequences (1 .. 2048); sequence b owns row b of the table.
- *   max_len     longest sequence in tokens (1 .. 2^22).
+ *   max_len     longest sequence in tokens (1 .. 2^22; a close bound lets
+ *               kvr_page_attend launch fewer kernels).
  *   max_rows    most rows of one step (1 .. 2^22).
  *   act         type of q, k, v, gains and outputs: KVR_ACT_BF16, KVR_ACT_F16.
  *   rope_theta  rotate-half RoPE base.  norm_eps  epsilon of the q/k norms.

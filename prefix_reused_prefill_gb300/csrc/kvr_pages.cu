@@ -28,10 +28,17 @@ namespace {
 constexpr size_t kAlign = 256;
 // Rows of a sequence and KV head (rows * group) up to which the split kernel
 // takes the sequence: 64 where every sequence of the step has so few (four
-// conversations of 8 rows, group 7, over 15k tokens: 52 us, 55 us by the
+// conversations of 8 rows, group 7, over 15k tokens: 50 us, 55 us by the
 // tensor-memory kernel), but 16 where that kernel runs anyway (12 conversations
 // of 1 to 120 rows, group 4, over up to 4k tokens: 32 us, 46 us with 32).
 constexpr int kPageMany = 64, kPageManyBeside = 16;
+// Pages (of one KV head and 8 rows) per CTA up to which the split kernel takes all
+// the step's rows: it needs one launch and about 12 us, the tensor-memory kernel
+// two and 22, but a page costs it 430 cycles for each 8 rows.  126 rows (group 7)
+// over 1024 / 8192 / 16000 / 32000 tokens, 7 to 213 pages a CTA: 12.1 / 23.6 / 34.4 /
+// 55.7 us, by the tensor-memory kernel 22.4 / 29.5 / 34.6 / 39.6.  (The host
+// knows how long the sequences can be, not how long they are.)
+constexpr int kPageFew = 100;
 // key blocks a CTA of the tensor-memory kernel takes at least: 254 rows over
 // 1668 tokens take 37.8 us with 2, 38.3 with 3 and 39.7 with 5, where fewer CTAs
 // run longer but leave fewer parts to merge; 18 rows over 2048: 24.0, 25.0, 27.6
@@ -52,7 +59,8 @@ bool valid(const kvr_pages_config* c) {
 }
 
 struct Layout {
-  size_t status, info, count, counters, lens, cu, free_list, row_seq, row_pos, row_slot, table, rope, rope_rest, ml, part, ml_tc, part_tc, shared, total;
+  size_t status, info, count, counters, lens, cu, free_list, row_seq, row_pos, row_slot, table, rope, rope_rest, ml,
+      part, ml_tc, part_tc, shared, total;
   int width;
 };
 Layout layout(const kvr_pages_config* c) {
@@ -297,11 +305,14 @@ int kvr_page_attend(kvr_pages* c, int layer, const void* q, long long q_stride, 
   a.rows = rows;
   a.scale_log2 = (float)((double)scale * 1.4426950408889634);
   const long long most = (long long)d.G * c->max_add;   // rows of a sequence and KV head, at most
-  a.many = most > kPageMany ? kPageManyBeside : kPageMany;
+  const long long tiles = ((long long)d.G * rows + 7) / 8 + c->n_seq;   // of 8 rows, at most
+  const bool few = tiles * d.width * d.Hkv <= (long long)kPageFew * c->ctas;
+  const bool split_only = few || most <= kPageMany;
+  a.many = !split_only ? kPageManyBeside : (int)std::max<long long>(most, kPageMany);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   OnDevice on(c->device);
   cudaError_t e = cudaSuccess;
-  if (most > kPageMany) {
+  if (!split_only) {
     PageAttendTc b = c->attend_tc;
     b.q = q;
     b.qs = q_stride;

@@ -14,7 +14,7 @@ Bounds, per element (u = half a step of the output type, 2^-9 relative for bf16'
   in n / 16 + 2 fp32 additions that may each drop 2^-22 of the running sum, itself at most max|v|:
   (2 * 2^-11 + 2^-13) sum w|v| + n (2^-27 max|v| + 2^-24) + (n / 16 + 2) 2^-22 max|v| + eps/2 |o|.
   Sequences with many rows of a KV head (the tensor-memory kernel: more than 64, or more than 16 in a step where one has
-  more than 64) read k as fp16 too where the activations are bf16: c s has 14 bits, each
+  more than 64, where the sequences may be long) read k as fp16 too where the activations are bf16: c s has 14 bits, each
   rounded by at most 2^-11.  A score is off by the sum of d such errors times scale q_d: at most
   6 * 2^-11 scale |q k|_2 but for odds of 2 exp(-18) (Hoeffding), and a weight by twice that of its row's largest.
 """
@@ -50,7 +50,9 @@ def rand(rng, shape, act, scale=1.0):
     return torch.from_numpy(rng.standard_normal(shape).astype(np.float32) * scale).to(TYPES[act])
 
 
-def handle(heads=8, kv_heads=2, d=64, act="bf16", n_pages=64, max_seqs=8, max_len=1024, max_rows=512, n_layers=2, **kw):
+def handle(heads=8, kv_heads=2, d=64, act="bf16", n_pages=64, max_seqs=8, max_len=1 << 17, max_rows=512,
+           n_layers=2, **kw):
+    """(max_len: at the default the step may be long, and many rows go to the tensor-memory kernel.)"""
     from prefix_reused_prefill_gb300 import PagedKv, paged_config
     return PagedKv(paged_config(n_pages=n_pages, n_layers=n_layers, n_q_heads=heads, n_kv_heads=kv_heads, head_dim=d,
                                 max_seqs=max_seqs, max_len=max_len, max_rows=max_rows, act=act, **kw))
@@ -112,7 +114,7 @@ def test_plan_follows_the_oracle(n, max_rows, n_pages):
 
 def test_plan_takes_the_state_itself_as_keep():
     """keep may be the handle's own lengths: every sequence goes on."""
-    pg, t = handle(), op.Tables(64, 8, 1024)
+    pg, t = handle(max_len=1024), op.Tables(64, 8, 1024)
     for add in ([3, 0, 70, 1, 0, 0, 5, 64], [1] * 8, [0, 0, 64, 0, 1, 0, 0, 1]):
         t.plan(list(t.lens), add, 512)
         pg.kvr_page_plan(pg.state.lens, ints(add), 512)
@@ -257,6 +259,7 @@ def bound(n, mag, v, ref, u, spread=0.0):
 
 class World:
     """A handle and, beside it, the values that each sequence's cache stands for (k without rotation)."""
+    rounds_k = True
 
     def __init__(self, heads, kv_heads, d, act, seed=0, layer=1, **kw):
         self.pg = handle(heads, kv_heads, d, act, **kw)
@@ -297,7 +300,8 @@ class World:
                     ref, mag = op.attend(qn[row], k, v, scale)
                     spread = 0.0
                     group = self.heads // self.kv_heads
-                    if self.act == "bf16" and m * group > (BESIDE if self.rows * group > MANY else MANY):
+                    many = BESIDE if self.rows * group > MANY else MANY
+                    if self.rounds_k and self.act == "bf16" and m * group > many:
                         kk = np.repeat(k, self.heads // self.kv_heads, axis=0)
                         spread = scale * np.sqrt(np.max((kk * qn[row][:, None]) ** 2 @ np.ones(self.d), axis=1))[:, None]
                     tol = bound(n, mag, v, ref, u, spread)
@@ -341,6 +345,21 @@ def test_attend_rows(act, heads, kv_heads, d, keep, add):
     w.pg.kvr_pages_sync()
 
 
+@pytest.mark.parametrize("act", ["bf16", "fp16"])
+@pytest.mark.parametrize("heads,kv_heads,d", [(8, 2, 64), (28, 4, 128), (16, 1, 128)])
+@pytest.mark.parametrize("keep,add", [([0], [200]), ([130], [129]), ([5, 0, 130, 64, 200], [3, 0, 7, 1, 40])])
+def test_attend_rows_of_sequences_that_cannot_be_long(act, heads, kv_heads, d, keep, add):
+    """(one launch, k as it is)"""
+    w = World(heads, kv_heads, d, act, seed=sum(add), max_len=384)
+    w.rounds_k = False
+    if sum(keep):
+        w.step([0] * len(keep), keep)
+    w.step(keep, add)
+    q = w.q(1.5)
+    w.check(q, w.pg.kvr_page_attend(1, q.cuda()))
+    w.pg.kvr_pages_sync()
+
+
 @pytest.mark.parametrize("heads,kv_heads,d", [(8, 2, 64), (6, 2, 128)])
 def test_attend_rows_in_fp16_round_weights_and_outputs_only(heads, kv_heads, d):
     """Root mean square error, relative to the outputs': an fp16 rounding is off by at most 2^-11 of the value, evenly
@@ -364,7 +383,7 @@ def test_attend_many_segments_in_a_run(d, heads, kv_heads, rows):
     """More work than CTAs: a run goes through whole sequences with one and with two row tiles (80 and 160 rows of a
     KV head), in either order, over several key blocks each."""
     n = 36
-    w = World(heads, kv_heads, d, "bf16", seed=17, max_seqs=n, n_pages=n * 12, max_rows=n * 600, max_len=800)
+    w = World(heads, kv_heads, d, "bf16", seed=17, max_seqs=n, n_pages=n * 12, max_rows=n * 600)
     keep = [300 + 37 * (b % 9) for b in range(n)]
     add = [rows[b % len(rows)] for b in range(n)]
     w.step([0] * n, keep)
@@ -532,13 +551,14 @@ def test_steps_of_a_server(heads, kv_heads, d):
     pg.kvr_pages_sync()
 
 
-def test_captured_steps_and_two_graphs():
+@pytest.mark.parametrize("max_len", [400, 1 << 17])
+def test_captured_steps_and_two_graphs(max_len):
     """A captured step (plan, append, attend) replayed over growing lengths gives the bits of eager calls; a second
     graph of another handle and an eager step in between do not disturb it."""
     rng = np.random.Generator(np.random.PCG64(21))
     made = []
     for _ in range(3):
-        pg = handle(8, 2, 64, max_seqs=4, max_len=400)
+        pg = handle(8, 2, 64, max_seqs=4, max_len=max_len)
         pg.kvr_page_plan(ints([0] * 4), ints([60, 1, 130, 7]), 198)
         k, v = (rand(np.random.Generator(np.random.PCG64([22, i])), (198, 2, 64), "bf16").cuda() for i in range(2))
         pg.kvr_page_append(0, None, k, v)

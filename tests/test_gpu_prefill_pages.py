@@ -40,7 +40,7 @@ def make(shape, max_rows=160, n_layers=None, **kw):
     kv = Kvr(config_for_shape(shape, 1, 256, max_rows, n_layers=n_layers), device="cuda")
     pg = PagedKv(paged_config(**{**dict(
         n_pages=32, n_layers=kv.cfg.n_layers, n_q_heads=shape.n_q_heads, n_kv_heads=shape.n_kv_heads,
-        head_dim=shape.head_dim, max_seqs=3, max_len=512, max_rows=max_rows, rope_theta=shape.rope_theta), **kw}))
+        head_dim=shape.head_dim, max_seqs=3, max_len=1 << 17, max_rows=max_rows, rope_theta=shape.rope_theta), **kw}))
     return kv, pg
 
 
