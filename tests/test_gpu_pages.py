@@ -394,6 +394,52 @@ def test_attend_many_segments_in_a_run(d, heads, kv_heads, rows):
     w.check(q, out)
 
 
+@pytest.mark.parametrize("long_rows", [1, 120])
+def test_attend_all_the_sequences_there_can_be(long_rows):
+    """2048 sequences of a few tokens, one of them with many rows."""
+    w = World(4, 1, 64, "bf16", seed=31, max_seqs=2048, n_pages=2100, max_rows=8192)
+    keep = [int(x) for x in w.rng.integers(0, 4, 2048)]
+    add = [int(x) for x in w.rng.integers(0, 2, 2048)]
+    keep[1500], add[1500], add[2047] = 130, long_rows, 1
+    w.step([0] * 2048, keep)
+    w.step(keep, add, pad=5)
+    q = w.q(1.5)
+    w.check(q, w.pg.kvr_page_attend(1, q.cuda()))
+    w.pg.kvr_pages_sync()
+
+
+@pytest.mark.parametrize("max_len", [512, 1 << 17])
+@pytest.mark.parametrize("keep,add", [([300], [1]), ([63, 0], [3, 5])])
+def test_attend_groups_of_64(keep, add, max_len):
+    w = World(64, 1, 128, "bf16", seed=33, max_len=max_len)
+    w.step([0] * len(keep), keep)
+    w.step(keep, add)
+    q = w.q(1.5)
+    w.check(q, w.pg.kvr_page_attend(1, q.cuda()))
+    w.pg.kvr_pages_sync()
+
+
+def test_two_handles_at_once_on_two_streams():
+    """Each handle has its own work area: calls of both in flight together give the bits of calls one after another."""
+    made = []
+    for i in range(2):
+        w = World(8, 2, 64, "bf16", seed=40 + i, layer=0)
+        w.step([0] * 8, [100 + 50 * i] + [20] * 7)
+        w.step([100 + 50 * i] + [20] * 7, [150, 1, 3, 1, 1, 1, 40, 1])
+        q = w.q(1.5).cuda()
+        made.append((w.pg, q, w.pg.kvr_page_attend(0, q)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in made]
+    got = [[], []]
+    for _ in range(20):
+        for i, (pg, q, _) in enumerate(made):
+            got[i].append(pg.kvr_page_attend(0, q, stream=streams[i]))
+    torch.cuda.synchronize()
+    for i, (pg, _, want) in enumerate(made):
+        assert all(torch.equal(x, want) for x in got[i])
+        pg.kvr_pages_sync()
+
+
 def test_attend_peaked_flat_and_scaled():
     w = World(28, 4, 128, "bf16", seed=9)
     w.step([0, 0], [300, 140], k_scale=2.0)
