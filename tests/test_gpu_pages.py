@@ -379,11 +379,12 @@ def test_attend_rows_in_fp16_round_weights_and_outputs_only(heads, kv_heads, d):
 
 @pytest.mark.parametrize("d,heads,kv_heads", [(64, 32, 8), (128, 16, 4)])
 @pytest.mark.parametrize("rows", [[20, 40], [40, 20], [17, 33, 100, 20], [30]])
-def test_attend_many_segments_in_a_run(d, heads, kv_heads, rows):
+@pytest.mark.parametrize("act", ["bf16", "fp16"])
+def test_attend_many_segments_in_a_run(act, d, heads, kv_heads, rows):
     """More work than CTAs: a run goes through whole sequences with one and with two row tiles (80 and 160 rows of a
     KV head), in either order, over several key blocks each."""
     n = 36
-    w = World(heads, kv_heads, d, "bf16", seed=17, max_seqs=n, n_pages=n * 12, max_rows=n * 600)
+    w = World(heads, kv_heads, d, act, seed=17, max_seqs=n, n_pages=n * 12, max_rows=n * 600)
     keep = [300 + 37 * (b % 9) for b in range(n)]
     add = [rows[b % len(rows)] for b in range(n)]
     w.step([0] * n, keep)
