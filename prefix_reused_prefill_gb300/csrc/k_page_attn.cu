@@ -761,9 +761,9 @@ page_attn_kernel(const PagesDev p, const PageAttend a) {
   __syncthreads();
   int jobs = seg_count;
   if (jobs == 0) return;
-  // Round 0: the CTA's own parts of each segment, to the output or, where other
+  // First time round: the CTA's own parts of each segment, to the output or, where other
   // CTAs share it (the first and the last segment at most), to the work area.
-  // Round 1: what the last CTA to arrive finds there.  A warp takes a row, a lane
+  // Second time: what the last CTA to arrive finds there.  A warp takes a row, a lane
   // D / 32 dims of it.  (Reads go past L1: other CTAs wrote some of them.)
 #pragma unroll 1
   for (int round = 0;; ++round) {

@@ -30,7 +30,9 @@ constexpr size_t kAlign = 256;
 // takes the sequence: 64 where every sequence of the step has so few (four
 // conversations of 8 rows, group 7, over 15k tokens: 50 us, 55 us by the
 // tensor-memory kernel), but 16 where that kernel runs anyway (12 conversations
-// of 1 to 120 rows, group 4, over up to 4k tokens: 32 us, 46 us with 32).
+// of 1 to 120 rows, group 4, over up to 4k tokens: 31 us, 36 us with 32; large
+// batches lean the other way: 48 of 7 to 70 rows, group 7, over up to 8k 135 us,
+// 124 with 32).
 constexpr int kPageMany = 64, kPageManyBeside = 16;
 // Pages (of one KV head and 8 rows) per CTA up to which the split kernel takes all
 // the step's rows: it needs one launch and about 12 us, the tensor-memory kernel
