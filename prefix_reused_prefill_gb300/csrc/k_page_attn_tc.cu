@@ -52,7 +52,7 @@
 // upper 64 keys issued before that wait, P all in the lower columns: 784 us, a
 // product of 64 keys lasts as long as one of 128.  64-key blocks with two S:
 // slower too.)
-// 254 rows over 1668 tokens: 38 us, of which the run is about 11, the rest the start
+// 254 rows over 1668 tokens: 35.5 us, of which the run is about 11, the rest the start
 // (6k cycles to the first product), Q, the parts' way to memory and the merge.
 #include <type_traits>
 
