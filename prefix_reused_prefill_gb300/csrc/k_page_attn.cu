@@ -11,10 +11,13 @@
 // (The nibble alone is an fp16 subnormal and needs no subtraction, but sums of
 // such products are cut at 2^-14 of the code unit, and with the bias of 8 that
 // adds up over thousands of keys.)  The K scale multiplies the fp32 sum of its
-// group, the V scale the weights: p and p sV are fp16 (2^-11 each, relative to
-// the weight; the row's sum takes p unrounded), p held with a factor 4 so that
-// p sV stays in range (p <= 1, sV <= 8188).  q is scaled per row by a power of
-// two so that any bf16 q is an fp16 number.
+// group, the V scale the codes: (c - 8) sV and p are fp16 (2^-11 each, relative to
+// themselves; the row's sum takes p unrounded).  (c - 8) sV loses nothing where it is
+// small, as sV is a multiple of 2^-24 itself, and p has a factor of 2^15, so that what fp16
+// drops is below 2^-38 of the largest weight in a run: attention stays linear in V.
+// (p sV instead has a quarter of the products with sV and took 71.8 instead of 74 us in
+// the first example below, but lost weights below 2^-27 / sV: the tail under a sink.)
+// q is scaled per row by a power of two so that any bf16 q is an fp16 number.
 //
 // Keys are the M side of both products (m16n8k16, S^T = K Q^T and O^T = V^T P^T):
 // the rows, at most 8 of a tile, fill the narrow N side.
@@ -30,13 +33,15 @@
 // page or two per warp, a CTA takes a whole one instead: the second page costs
 // less than a merge across CTAs.
 //
-// 64 sequences of one token over up to 8191 (32 heads in groups of 4, d = 128): 71 us,
-// 4.1 TB/s of 289 MB, 60 % of a plain copy's rate (a bare streaming loop over the
-// same pages: 6.3 TB/s).  Two over 131070 (28 heads in groups of 7): 46 us, 3.3 TB/s.
+// 64 sequences of one token over up to 8191 (32 heads in groups of 4, d = 128): 74 us,
+// 3.9 TB/s of 289 MB, 58 % of a plain copy's rate (a bare streaming loop over the
+// same pages: 6.3 TB/s).  Two over 131070 (28 heads in groups of 7): 48 us, 3.2 TB/s.
 // Of both about 3 us go before the first page and 5 to 8 us to the last pages, the
-// parts and their merge; between them an SM takes about 400 cycles a page, 300 at
-// the copy's rate.  One sequence over 726: 9.8 us.  Four of 8 rows over 15360
-// (groups of 7): 50 us, where seven tiles of 8 rows each decode the pages anew.
+// parts and their merge; between them an SM takes about 415 cycles a page, 300 at
+// the copy's rate.  One sequence over 726: 10.0 us.  Four of 8 rows over 15360
+// (groups of 7): 55 us, where seven tiles of 8 rows each decode the pages anew.
+#include <climits>
+
 #include "kvr_pages.cuh"
 
 namespace kvr {
@@ -103,6 +108,13 @@ __device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
   __half2 r = __hadd2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
   return *reinterpret_cast<uint32_t*>(&r);
 }
+// a number or, for NaN, 0 (scales are not negative)
+__device__ __forceinline__ uint32_t number2(uint32_t s) {
+  __half2 r = __hmax2(*reinterpret_cast<__half2*>(&s), __float2half2_rn(0.f));
+  return *reinterpret_cast<uint32_t*>(&r);
+}
+// the halves of a pair that the first n of two stand for
+__device__ __forceinline__ uint32_t first_of_pair(int n) { return n > 1 ? 0xffffffffu : n == 1 ? 0xffffu : 0u; }
 // a register with a constant that the compiler does not form anew at each use
 __device__ __forceinline__ uint32_t held(uint32_t x) {
   asm volatile("" : "+r"(x));
@@ -121,6 +133,11 @@ __device__ __forceinline__ uint32_t centred_lo(uint32_t w, uint32_t k1024) {
 }
 __device__ __forceinline__ uint32_t centred_hi(uint32_t w, uint32_t k64) {
   return hadd2(and_or<0x00f000f0u>(w, k64), 0xd480d480u);     // 64 + c - 72
+}
+template <int W>
+__device__ __forceinline__ void sts_words(uint8_t* at, const uint32_t* w) {
+  if (W == 4) *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[W - 2], w[W - 1]);
+  else *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
 }
 template <int W>
 __device__ __forceinline__ void lds_words(const uint8_t* at, uint32_t* w) {
@@ -178,7 +195,8 @@ __device__ __forceinline__ Vec<N> load_past_l1(const void* p) {
   return r;
 }
 
-// a partial result: [rows of a tile][D] floats, and (m, l) per row
+// a partial result: [rows of a tile][D] floats, and per row the exponent that its
+// weights are taken under and their sum
 struct Slot {
   float* o;
   float2* ml;
@@ -478,7 +496,10 @@ page_attn_kernel(const PagesDev p, const PageAttend a) {
     uint32_t qb[kG][4];       // dims 32 j + 8 t + 0..7 of row 8 n + g, the B side of the K codes
     float f[2];               // sums -> scores in log2 units
     int see[2];               // last key these rows see
-    float m_run[2], l_run[2];
+    float m_run[2] = {-INFINITY, -INFINITY}, l_run[2];
+    // The exponent that a row's weights are taken under: 15 below the maximum, which fp16 has
+    // room for (in O and in l alike).  Both are rounded up, so no weight passes 2^15.
+    auto ref_of = [](float m) { return __fadd_ru(m, -15.f); };
     float o[2 * kG][4];       // O^T tiles 2 j, 2 j + 1: rows g, g + 8 are dims 32 j + 4 g + 0, 1 and + 2, 3
     bool fresh = true;
     const uint32_t k1024 = held(0x64006400u), k64 = held(0x54005400u);
@@ -550,7 +571,7 @@ page_attn_kernel(const PagesDev p, const PageAttend a) {
       for (int c = 0; c < 2; ++c) {
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], d));
-        mx[c] *= f[c];
+        mx[c] = ceilf(__fmul_ru(mx[c], f[c]));
       }
       const bool moved = mx[0] > m_run[0] || mx[1] > m_run[1];
       if (__any_sync(0xffffffffu, moved)) {
@@ -558,7 +579,7 @@ page_attn_kernel(const PagesDev p, const PageAttend a) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const float m_new = fmaxf(m_run[c], mx[c]);
-          corr[c] = m_run[c] == -INFINITY ? 0.f : ex2_approx(m_run[c] - m_new);
+          corr[c] = m_run[c] == -INFINITY ? 0.f : ex2_approx(ref_of(m_run[c]) - ref_of(m_new));
           m_run[c] = m_new;
           l_run[c] *= corr[c];
         }
@@ -567,10 +588,9 @@ page_attn_kernel(const PagesDev p, const PageAttend a) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) o[i][c] *= corr[c & 1];
       }
-      // weights with a factor of 4 (in O and in l alike)
       float sub[2];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) sub[c] = m_run[c] == -INFINITY ? 0.f : m_run[c] - 2.f;
+      for (int c = 0; c < 2; ++c) sub[c] = m_run[c] == -INFINITY ? 0.f : ref_of(m_run[c]);
 #pragma unroll
       for (int mt = 0; mt < 4; ++mt) {
         float e[4];
@@ -584,6 +604,28 @@ page_attn_kernel(const PagesDev p, const PageAttend a) {
       }
       // ---- weighted values
       if (!arrived()) return false;
+      if (!whole) {
+        // Places behind the last token hold anything: no value.  A NaN among the scales of a
+        // key, of which 0 times would reach every row, becomes the sum of the rows that see it.
+        // (A lane looks at two keys' scales.  Little code: it is fetched anew nearly every time.)
+        uint8_t* at = smem + warp * C::kRing + stage * C::kHalf + (K::kVs - C::kHalf) + lane * kG * 4;
+        const int key = key_base + 16 * (lane >> 3) + 8 * (lane & 1) + (lane & 6);
+        const uint32_t there = first_of_pair(s.P + s.m - key);
+        uint32_t sv[kG], bad = 0;
+        lds_words<kG>(at, sv);
+#pragma unroll
+        for (int j = 0; j < kG; ++j) {
+          bad |= (sv[j] & there) + 0x03ff03ffu;   // (bit 15 of a NaN's half)
+          sv[j] = number2(sv[j] & there);
+        }
+        sts_words<kG>(at, sv);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // before the stage's next copy
+        __syncwarp();
+        const int first = __reduce_min_sync(0xffffffffu, bad & 0x8000u ? key : (int)bad < 0 ? key + 1 : INT_MAX);
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          if (first <= see[c]) l_run[c] = NAN;
+      }
       page = smem + warp * C::kRing + stage * C::kHalf - C::kHalf;   // (the V half's offsets count from the page)
 #pragma unroll
       for (int mt = 0; mt < 4; ++mt) {
@@ -592,33 +634,15 @@ page_attn_kernel(const PagesDev p, const PageAttend a) {
         lds_words<kG>(page + K::kV + (((2 * mt + 1) * 8 + g) * 4 + t) * kG * 4, v1);
         lds_words<kG>(page + K::kVs + ((mt * 4 + t) * 2 + 0) * kG * 4, s0);
         lds_words<kG>(page + K::kVs + ((mt * 4 + t) * 2 + 1) * kG * 4, s1);
-        uint32_t b0[kG], b1[kG];
-#pragma unroll
-        for (int j = 0; j < kG; ++j) {
-          b0[j] = hmul2(pw[mt][0], s0[j]);
-          b1[j] = hmul2(pw[mt][1], s1[j]);
-        }
-        if (!whole) {
-          // a weight of zero takes nothing, whatever stands in a place behind the
-          // row's last key (an unwritten scale, a NaN)
-          const uint32_t p0 = pw[mt][0], p1 = pw[mt][1];
-          const uint32_t keep0 = ((p0 & 0xffffu) ? 0xffffu : 0u) | ((p0 >> 16) ? 0xffff0000u : 0u);
-          const uint32_t keep1 = ((p1 & 0xffffu) ? 0xffffu : 0u) | ((p1 >> 16) ? 0xffff0000u : 0u);
-#pragma unroll
-          for (int j = 0; j < kG; ++j) {
-            b0[j] &= keep0;
-            b1[j] &= keep1;
-          }
-        }
 #pragma unroll
         for (int j = 0; j < kG; ++j) {
           const uint32_t x0 = v0[j], x1 = v1[j], y0 = x0 >> 8, y1 = x1 >> 8;
-          const uint32_t e0 = centred_lo(x0, k1024), e1 = centred_hi(x0, k64), e2 = centred_lo(x1, k1024),
-                         e3 = centred_hi(x1, k64);
-          const uint32_t f0 = centred_lo(y0, k1024), f1 = centred_hi(y0, k64), f2 = centred_lo(y1, k1024),
-                         f3 = centred_hi(y1, k64);
-          mma(o[2 * j], e0, e1, e2, e3, b0[j], b1[j]);
-          mma(o[2 * j + 1], f0, f1, f2, f3, b0[j], b1[j]);
+          const uint32_t e0 = hmul2(centred_lo(x0, k1024), s0[j]), e1 = hmul2(centred_hi(x0, k64), s0[j]),
+                         e2 = hmul2(centred_lo(x1, k1024), s1[j]), e3 = hmul2(centred_hi(x1, k64), s1[j]);
+          const uint32_t f0 = hmul2(centred_lo(y0, k1024), s0[j]), f1 = hmul2(centred_hi(y0, k64), s0[j]),
+                         f2 = hmul2(centred_lo(y1, k1024), s1[j]), f3 = hmul2(centred_hi(y1, k64), s1[j]);
+          mma(o[2 * j], e0, e1, e2, e3, pw[mt][0], pw[mt][1]);
+          mma(o[2 * j + 1], f0, f1, f2, f3, pw[mt][0], pw[mt][1]);
         }
       }
       used();
@@ -708,7 +732,7 @@ page_attn_kernel(const PagesDev p, const PageAttend a) {
         }
         if (!alone && g == 0) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c) out.ml[2 * t + c] = make_float2(m_run[c], l[c]);
+          for (int c = 0; c < 2; ++c) out.ml[2 * t + c] = make_float2(ref_of(m_run[c]), l[c]);
         }
         if (!alone) {
           if (lane == 0) {
