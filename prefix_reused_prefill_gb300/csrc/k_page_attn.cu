@@ -17,7 +17,7 @@
 // drops is below 2^-38 of the largest weight in a run: attention stays linear in V.
 // (p sV instead has a quarter of the products with sV and took 71.8 instead of 74 us in
 // the first example below, but lost weights below 2^-27 / sV: the tail under a sink.)
-// q is scaled per row by a power of two so that any bf16 q is an fp16 number.
+// q is scaled per row by a power of two that brings its largest element to 2^10, and is fp16.
 //
 // Keys are the M side of both products (m16n8k16, S^T = K Q^T and O^T = V^T P^T):
 // the rows, at most 8 of a tile, fill the narrow N side.
@@ -666,10 +666,11 @@ page_attn_kernel(const PagesDev p, const PageAttend a) {
         }
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // 2^e with |q| 2^e in [2^10, 2^11); e from the exponent field, kept
-        // where both 2^e and its inverse are normal numbers
+        // 2^e with max|q| 2^e in [2^10, 2^11), e from the exponent field, for every finite q
+        // (-117 is that of the largest; where 100 is not enough, the scores are next to 0).
+        // What is 2^-25 of the row's largest or more is exact, the rest is rounded by 2^-35 of it.
         int e = 137 - (int)(__float_as_uint(top) >> 23);
-        e = top > 0.f ? max(-100, min(100, e)) : 0;
+        e = top > 0.f ? max(-117, min(100, e)) : 0;
         const float up = __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
         for (int j = 0; j < kG; ++j) {

@@ -11,8 +11,9 @@
 // of the first, and every product runs once for each: 5.6e-4 -> 2.6e-4 of the
 // outputs in the mean square at scores of deviation 2 (2.1e-4 is the output's rounding), for
 // 33.5 instead of 32 us in a mixed batch of 64-wide heads and 915 instead of 673 us
-// in the long prompts below.  q is scaled per row by a power of two so that any
-// bf16 q is an fp16 number; P is fp16 (2^-11).  Sums, maxima and O are fp32.
+// in the long prompts below.  q is scaled per row by a power of two that brings
+// its largest element to 2^10 (what is 2^-25 of that or more is exact), and is fp16; P is
+// fp16 (2^-11).  Sums, maxima and O are fp32.
 //
 // Writing a 4-bit block as fp16 costs about as many instructions as the softmax
 // of one 128-row tile over it, so a CTA runs two row tiles over each block: one
@@ -679,7 +680,7 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
         named_sync(pair, 64);
         top = fmaxf(top, exchange[t][h ^ 1][r]);
         int e = 137 - (int)(__float_as_uint(top) >> 23);
-        e = top > 0.f ? max(-100, min(100, e)) : 0;
+        e = top > 0.f ? max(-117, min(100, e)) : 0;
         const float up = __uint_as_float((uint32_t)(127 + e) << 23);
         f = __uint_as_float((uint32_t)(127 - e) << 23) * a.scale_log2;
 #pragma unroll 2

@@ -40,3 +40,17 @@ def test_nan_values_show_however_small_their_weight(where, rows, max_len):
         if not sees:
             assert not np.isnan(got[i]).any()
     assert not np.isnan(got[n:]).any()
+
+
+@pytest.mark.parametrize("rows", [1, 150])
+@pytest.mark.parametrize("log_q", [114, 117, 121, 125])
+def test_queries_next_to_the_largest_number(rows, log_q):
+    """q of about 2^log_q over small k, with a scale that leaves ordinary scores."""
+    w = World(8, 2, 64, "bf16", seed=15)
+    w.step([0], [200 + rows], k_scale=2.0 ** -20)
+    w.pg.kvr_page_plan(ints([200]), ints([rows]), rows)
+    w.keep, w.add, w.rows = [200], [rows], rows
+    q, scale = w.q(2.0 ** log_q), 2.0 ** (18 - log_q)
+    assert torch.isfinite(q).all()
+    w.check(q, w.pg.kvr_page_attend(1, q.cuda(), scale=scale), scale)
+    w.pg.kvr_pages_sync()
