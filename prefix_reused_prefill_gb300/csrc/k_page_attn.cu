@@ -40,6 +40,7 @@
 // parts and their merge; between them an SM takes about 415 cycles a page, 300 at
 // the copy's rate.  One sequence over 726: 10.0 us.  Four of 8 rows over 15360
 // (groups of 7): 55 us, where seven tiles of 8 rows each decode the pages anew.
+#include <cfloat>
 #include <climits>
 
 #include "kvr_pages.cuh"
@@ -667,10 +668,10 @@ page_attn_kernel(const PagesDev p, const PageAttend a) {
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         // 2^e with max|q| 2^e in [2^10, 2^11), e from the exponent field, for every finite q
-        // (-117 is that of the largest; where 100 is not enough, the scores are next to 0).
+        // (-117 is that of the largest; 126 leaves 2^-e a normal number).
         // What is 2^-25 of the row's largest or more is exact, the rest is rounded by 2^-35 of it.
         int e = 137 - (int)(__float_as_uint(top) >> 23);
-        e = top > 0.f ? max(-117, min(100, e)) : 0;
+        e = top > 0.f ? max(-117, min(126, e)) : 0;
         const float up = __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
         for (int j = 0; j < kG; ++j) {
@@ -681,7 +682,8 @@ page_attn_kernel(const PagesDev p, const PageAttend a) {
             qb[j][i] = dev::pack_act<true>(x.x * up, x.y * up);
           }
         }
-        const float back = __uint_as_float((uint32_t)(127 - e) << 23) * a.scale_log2;
+        // (a number above 0, as masked scores of -inf are multiplied by it)
+        const float back = fmaxf(__uint_as_float((uint32_t)(127 - e) << 23) * a.scale_log2, FLT_MIN);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int from = (2 * t + c) * 4;

@@ -55,6 +55,7 @@
 // slower too.)
 // 254 rows over 1668 tokens: 35.5 us, of which the run is about 11, the rest the start
 // (6k cycles to the first product), Q, the parts' way to memory and the merge.
+#include <cfloat>
 #include <type_traits>
 
 #include "kvr_pages.cuh"
@@ -680,9 +681,10 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
         named_sync(pair, 64);
         top = fmaxf(top, exchange[t][h ^ 1][r]);
         int e = 137 - (int)(__float_as_uint(top) >> 23);
-        e = top > 0.f ? max(-117, min(100, e)) : 0;
+        e = top > 0.f ? max(-117, min(126, e)) : 0;
         const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-        f = __uint_as_float((uint32_t)(127 - e) << 23) * a.scale_log2;
+        // (a number above 0, as masked scores of -inf are multiplied by it)
+        f = fmaxf(__uint_as_float((uint32_t)(127 - e) << 23) * a.scale_log2, FLT_MIN);
 #pragma unroll 2
         for (int c = 0; c < kHalfChunks; ++c) {
           const uint32_t at = row + (((first + c) ^ (r & 7)) << 4);

@@ -298,14 +298,16 @@ int kvr_page_attend(kvr_pages* c, int layer, const void* q, long long q_stride, 
   if (q == out) return fail(c, KVR_ERR_ARG, "out must not be q");
   if (!stride_ok(q_stride, (long long)d.Hq * d.d))
     return fail(c, KVR_ERR_ARG, "the row stride must cover a row and be a multiple of 8");
-  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(c, KVR_ERR_ARG, "scale must be a positive number");
+  const float scale_log2 = (float)((double)scale * 1.4426950408889634);
+  if (!(scale > 0.f) || !std::isfinite(scale_log2))
+    return fail(c, KVR_ERR_ARG, "scale must be a positive number of at most 2.3e38");
   PageAttend a = c->attend;
   a.q = q;
   a.qs = q_stride;
   a.out = out;
   a.out_f16 = out_f16 || d.f16;
   a.rows = rows;
-  a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  a.scale_log2 = scale_log2;
   const long long most = (long long)d.G * c->max_add;   // rows of a sequence and KV head, at most
   const long long tiles = ((long long)d.G * rows + 7) / 8 + c->n_seq;   // of 8 rows, at most
   const bool few = tiles * d.width * d.Hkv <= (long long)kPageFew * c->ctas;

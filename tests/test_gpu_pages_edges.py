@@ -54,3 +54,42 @@ def test_queries_next_to_the_largest_number(rows, log_q):
     assert torch.isfinite(q).all()
     w.check(q, w.pg.kvr_page_attend(1, q.cuda(), scale=scale), scale)
     w.pg.kvr_pages_sync()
+
+
+@pytest.mark.parametrize("rows", [2, 150])
+@pytest.mark.parametrize("q_size,scale", [(2.0 ** -100, 2.0 ** -60), (2.0 ** -120, 1e-38), (1.0, 1e-38), (2.0 ** -100, 2.0 ** 100),
+                                          (2.0 ** -110, 2.2e38)])
+def test_queries_and_scales_next_to_zero(rows, q_size, scale):
+    """Tiny q under tiny and large scales: scores next to equal, or far apart; rows that see only a part of a page among
+    them."""
+    w = World(8, 2, 64, "bf16", seed=16)
+    w.step([0], [200 + rows], k_scale=0.1)
+    w.pg.kvr_page_plan(ints([200]), ints([rows]), rows)
+    w.keep, w.add, w.rows = [200], [rows], rows
+    q = w.q(q_size)
+    out = w.pg.kvr_page_attend(1, q.cuda(), scale=scale)
+    w.pg.kvr_pages_sync()
+    if scale < 1e38:
+        return w.check(q, out, scale)
+    # Scores of 2^-110 2^127.4 0.1 sqrt(64) = 1.4e5: the bound holds to 90 only.  k rounded to fp16 (2^-11) moves such a
+    # score by tens, so any of several keys may have the weight; what is left is that the output is a mean of
+    # values: between the least and the largest of them, rounded by 2^-8 for the type, 2^-10 for weights and values.
+    got = f64(out)
+    for i in range(rows):
+        v = np.repeat(w.v[0][:, :201 + i], 4, axis=0)
+        top = np.abs(v).max()
+        assert (got[i] >= v.min(axis=1) - 2.0 ** -7 * top).all() and (got[i] <= v.max(axis=1) + 2.0 ** -7 * top).all()
+
+
+def test_a_scale_beyond_the_largest_is_refused():
+    from prefix_reused_prefill_gb300 import KvrError
+    pg = handle(8, 2, 64)
+    pg.kvr_page_plan(ints([0]), ints([1]), 1)
+    q, k, v = (torch.ones(1, h, 64, dtype=torch.bfloat16, device="cuda") for h in (8, 2, 2))
+    pg.kvr_page_append(0, None, k, v)
+    for scale in (3e38, float("inf")):
+        with pytest.raises(KvrError) as e:
+            pg.kvr_page_attend(0, q, scale=scale)
+        assert e.value.code == -1
+    pg.kvr_page_attend(0, q, scale=2.2e38)
+    pg.kvr_pages_sync()
