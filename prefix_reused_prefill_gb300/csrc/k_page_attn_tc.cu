@@ -70,6 +70,10 @@ constexpr int kKeys = 128;
 constexpr int kDecodeWarp = 16;
 constexpr int kThreads = 32 * (kDecodeWarp + 4);
 constexpr float kLazyMax = 8.0f;
+// Weights carry a factor of 2^7 (in O and in l alike), so that the largest, 2^8 over the
+// reference, is 2^15 and what fp16 drops is below 2^-31 of it.  References are whole numbers,
+// and every rounding goes the way that no weight is larger.
+constexpr float kHead = 7.0f;
 
 template <int D, bool F16>
 struct Tc {
@@ -710,7 +714,7 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
       // the earliest row of the tile sees everything up to here
       const int all_see = s.P + (int)((uint32_t)rho0 / (uint32_t)p.G);
       const int see = live ? s.P + tok : -1;
-      float m_ref = -INFINITY, l = 0.f, sub = 0.f;   // (sub: the reference, 0 before the first)
+      float m_ref = -INFINITY, l = 0.f, sub = 0.f;   // (sub: the weights' exponent, 0 before the first reference)
       // the 64 weights of one half row under the present reference, and the
       // largest score; the S columns stay as they are
       auto weights = [&](int j, auto masked, uint32_t* pk, float& sum) {
@@ -747,7 +751,7 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
         }
         part[0] = dev::add2(part[0], part[1]);
         sum = part[0].x + part[0].y;
-        return fmaxf(mx[0], mx[1]) * f;
+        return ceilf(__fmul_ru(fmaxf(mx[0], mx[1]), f));
       };
       for (int j = j0; j < j1; ++j) {
         if (ok) ok = all_wait(s_full[t], blocks);
@@ -760,14 +764,15 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
           if (ok) top = whole ? weights(j, std::false_type(), pk, sum) : weights(j, std::true_type(), pk, sum);
           // has a row's score passed its reference by more than 2^8?  (The first
           // block of a segment always does; the second vote on a block never.)
-          if (!any_of(pair, 64, ok && top > m_ref + kLazyMax)) break;
+          if (!any_of(pair, 64, ok && top > __fadd_rd(m_ref, kLazyMax))) break;
           exchange[t][h][r] = top;
           named_sync(pair, 64);
           top = fmaxf(top, exchange[t][h ^ 1][r]);
-          const float m_new = top > m_ref + kLazyMax ? top : m_ref;
-          const float factor = m_new != m_ref && m_ref != -INFINITY ? ex2_approx(m_ref - m_new) : 1.f;
+          const float m_new = top > __fadd_rd(m_ref, kLazyMax) ? top : m_ref;
+          const float sub_new = m_new == -INFINITY ? 0.f : __fadd_ru(m_new, -kHead);
+          const float factor = m_new != m_ref && m_ref != -INFINITY ? ex2_approx(sub - sub_new) : 1.f;
           m_ref = m_new;
-          sub = m_new == -INFINITY ? 0.f : m_new;
+          sub = sub_new;
           l *= factor;
           if (ok && j > j0) {
             ok = all_wait(pv_done[t], blocks - 1);
@@ -830,7 +835,8 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
       const bool whole_seg = j0 == 0 && j1 == s.nb;
       const float inv = whole_seg ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
       const long long slot = ((long long)cta * 2 + (j0 == 0 ? 1 : 0)) * kPairRows + kTile * t;
-      if (!whole_seg && h == 0) a.ml[slot + r] = live ? make_float2(m_ref, l) : make_float2(-INFINITY, 0.f);
+      if (!whole_seg && h == 0)
+        a.ml[slot + r] = live ? make_float2(m_ref == -INFINITY ? m_ref : sub, l) : make_float2(-INFINITY, 0.f);
       // 32 dims at a time through this warp's part of the Q tile (the last
       // scores are formed), so that stores to global memory are whole lines
       const uint32_t stage = q_tile + (uint32_t)(C::kQTile / 8) * (uint32_t)(warp & 7);

@@ -109,7 +109,7 @@ struct PageAttend {
   int many;
   float scale_log2;
   float* part;       // partial outputs
-  float2* ml;        // their (max in log2 units, sum)
+  float2* ml;        // their (the exponent that the weights are taken under, sum)
   int* counters;     // arrivals, zero between launches
   const PageShared* shared;   // [CTAs] of the tensor-memory kernel, null where it did not run
   const float* tc_part;
@@ -129,7 +129,7 @@ struct PageAttendTc {
   // parts of segments: [CTAs][2][256 rows], first the one that began in an
   // earlier CTA, then the one that goes on in the next
   float* part;       // [d]
-  float2* ml;        // (reference in log2 units, sum)
+  float2* ml;        // (the exponent that the weights are taken under, their sum)
   PageShared* shared;
 };
 constexpr int kPageTcRows = 256;
