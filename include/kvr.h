@@ -605,6 +605,8 @@ int kvr_page_read(kvr_pages* pages, int layer, void* k_out, void* v_out, int row
  *            (a multiple of 8); out [rows][n_q_heads][head_dim], apart from q.
  *   out_f16  1: the rows, rounded to the activation type, are stored as fp16.
  *   scale    a positive number, at most 2.3e38 (its product with log2(e) is a float).
+ * Scores (scale q k) are 32-bit numbers: a row with one above 1.8e8 reads NaN,
+ * and one below -1.8e8 has no weight.
  * The same call gives the same bits (no atomic adds).  rows must be the plan's.
  * A captured call keeps the max_add of the plan before it: replayed after a
  * plan with a larger one it may leave out the rows of long additions, which

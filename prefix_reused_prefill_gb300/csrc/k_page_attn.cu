@@ -499,7 +499,8 @@ page_attn_kernel(const PagesDev p, const PageAttend a) {
     int see[2];               // last key these rows see
     float m_run[2] = {-INFINITY, -INFINITY}, l_run[2];
     // The exponent that a row's weights are taken under: 15 below the maximum, which fp16 has
-    // room for (in O and in l alike).  Both are rounded up, so no weight passes 2^15.
+    // room for (in O and in l alike).  Both are rounded up, so no weight passes 2^15; whole
+    // numbers, so that rescaling is exact.
     auto ref_of = [](float m) { return __fadd_ru(m, -15.f); };
     float o[2 * kG][4];       // O^T tiles 2 j, 2 j + 1: rows g, g + 8 are dims 32 j + 4 g + 0, 1 and + 2, 3
     bool fresh = true;
@@ -579,10 +580,11 @@ page_attn_kernel(const PagesDev p, const PageAttend a) {
         float corr[2];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const float m_new = fmaxf(m_run[c], mx[c]);
+          float m_new = fmaxf(m_run[c], mx[c]);
+          if (m_new < -kScoreMax) m_new = -INFINITY;
           corr[c] = m_run[c] == -INFINITY ? 0.f : ex2_approx(ref_of(m_run[c]) - ref_of(m_new));
           m_run[c] = m_new;
-          l_run[c] *= corr[c];
+          l_run[c] = m_new >= kScoreMax ? NAN : l_run[c] * corr[c];
         }
 #pragma unroll
         for (int i = 0; i < 2 * kG; ++i)

@@ -751,7 +751,8 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
         }
         part[0] = dev::add2(part[0], part[1]);
         sum = part[0].x + part[0].y;
-        return ceilf(__fmul_ru(fmaxf(mx[0], mx[1]), f));
+        const float top = ceilf(__fmul_ru(fmaxf(mx[0], mx[1]), f));
+        return top < -kScoreMax ? -INFINITY : top;
       };
       for (int j = j0; j < j1; ++j) {
         if (ok) ok = all_wait(s_full[t], blocks);
@@ -773,7 +774,7 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
           const float factor = m_new != m_ref && m_ref != -INFINITY ? ex2_approx(sub - sub_new) : 1.f;
           m_ref = m_new;
           sub = sub_new;
-          l *= factor;
+          l = m_new >= kScoreMax ? NAN : l * factor;
           if (ok && j > j0) {
             ok = all_wait(pv_done[t], blocks - 1);
             fence_after();

@@ -9,6 +9,9 @@ constexpr int kPage = KVR_PAGE_TOKENS;   // tokens of a page
 constexpr int kPageGroup = 32;           // elements along the head dimension that share a scale
 constexpr float kPageScaleMax = 8188.f;  // 8 * 8188 = 65504: every value c * s has an fp16 number's magnitude
 constexpr int kPageMaxSeqs = 2048;
+// A score in log2 units that is larger makes its row NaN, one below minus it weighs nothing: 32
+// bits place such numbers 32 apart and more, which leaves no weights.
+constexpr float kScoreMax = 268435456.f;   // 2^28
 
 // One page of one KV head ("chunk"), in the order the tensor-core fragments
 // want it.  Key = token within the page, g = 0..7 and t = 0..3 the lane

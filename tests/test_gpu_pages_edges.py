@@ -93,3 +93,28 @@ def test_a_scale_beyond_the_largest_is_refused():
         assert e.value.code == -1
     pg.kvr_page_attend(0, q, scale=2.2e38)
     pg.kvr_pages_sync()
+
+
+@pytest.mark.parametrize("rows", [2, 150])
+@pytest.mark.parametrize("scale", [1e3, 1e4, 3e5, 1e7, 1e20, 1e33])
+def test_large_equal_scores(rows, scale):
+    """All keys alike: every score of a row is the same number, and the output the mean of the values.  (With equal weights
+    w the products' and sums' errors are relative to sum w|v|, as for any other scores.)  Scores above 1.8e8 read
+    NaN, those below -1.8e8 have no weight."""
+    w = World(8, 2, 64, "bf16", seed=18, max_rows=1024)
+
+    def alike(k, v):
+        k[:] = k[:1]
+    w.step([0], [500 + rows], edit=alike)
+    w.pg.kvr_page_plan(ints([500]), ints([rows]), rows)
+    w.keep, w.add, w.rows = [500], [rows], rows
+    q = w.q(2.0)
+    out = w.pg.kvr_page_attend(1, q.cuda(), scale=scale)
+    w.pg.kvr_pages_sync()
+    if scale <= 3e5:
+        return w.check(q, out, scale)
+    got, k = f64(out), np.repeat(w.k[0][:, 0], 4, axis=0)
+    score = scale * (f64(q) * k).sum(-1)                     # [rows][heads]
+    assert np.isnan(got[score > 1.87e8]).all() and (got[score < -1.87e8] == 0).all()
+    assert np.isfinite(got[np.abs(score) < 1.85e8]).all()
+    assert (np.abs(score) > 1e3).mean() > 0.9
