@@ -140,7 +140,7 @@ __device__ __forceinline__ __half quantise8(uint4 u, const float2* x, bool of_k,
 // two activation values: k is rounded to that type and then to a code, and on the
 // other side of both borders it would move by a whole scale, 1 / 7 of the
 // group's largest.
-// a + b = hi + lo, exactly
+// a + b = hi + lo, exactly (Knuth's sum of two numbers and its error)
 __device__ __forceinline__ void two_sum(float2 a, float2 b, float2& hi, float2& lo) {
   hi = dev::add2(a, b);
   const float2 v = dev::sub2(hi, a);
@@ -176,6 +176,7 @@ __device__ __forceinline__ float2 exact_rsqrt(const float2* x, float eps) {
   lo = fmaf(lo, 1.f / D, e);
   // one step of Newton's from the approximate root, the residual 1 - v r^2 formed
   // from the exact product v r
+  if (hi == INFINITY) return make_float2(0.f, 0.f);   // (the sum passed the largest number)
   const float r = rsqrtf(hi), p = hi * r, pe = fmaf(hi, r, -p);
   const float off = fmaf(-fmaf(lo, r, pe), r, fmaf(-p, r, 1.f));
   return make_float2(r, 0.5f * r * off);

@@ -118,3 +118,29 @@ def test_large_equal_scores(rows, scale):
     assert np.isnan(got[score > 1.87e8]).all() and (got[score < -1.87e8] == 0).all()
     assert np.isfinite(got[np.abs(score) < 1.85e8]).all()
     assert (np.abs(score) > 1e3).mean() > 0.9
+
+
+@pytest.mark.parametrize("act", ["bf16", "fp16"])
+def test_norms_of_the_largest_numbers(act):
+    """A head whose squares' sum passes the largest 32-bit number: it is normed to 0, k as q; an infinity is normed to
+    NaN in its own place only (and so in its group of the cache), other heads as ever."""
+    pg = handle(2, 2, 64, act)
+    pg.kvr_page_plan(ints([0]), ints([6]), 6)
+    x = torch.ones(6, 2, 64, dtype=torch.float32)
+    if act == "bf16":
+        x[1, 1] = 2.0 ** 70
+        x[2, 0, 3] = 2.0 ** 100
+        x[3, 0] = 3e38
+    x[4, 1, 40] = float("inf")
+    x = x.to(torch.bfloat16 if act == "bf16" else torch.float16)
+    g = torch.ones(64, dtype=x.dtype, device="cuda")
+    q = f64(pg.kvr_page_append(0, x.cuda(), x.cuda(), x.cuda(), g, g, rotate=False))
+    k = f64(pg.kvr_page_read(0)[0])
+    want = np.ones((6, 2, 64))
+    if act == "bf16":
+        want[1, 1] = want[2, 0] = want[3, 0] = 0
+    want[4, 1] = 0
+    want[4, 1, 40] = np.nan
+    assert np.allclose(q, want, rtol=2.0 ** -7, equal_nan=True)
+    want[4, 1, 32:] = np.nan
+    assert np.allclose(k, want, rtol=2.0 ** -7, equal_nan=True)
