@@ -1794,7 +1794,9 @@ int kvr_verify_accept_batch(kvr_ctx* c, int n_seq, const int* slots, const int* 
 int kvr_prefill_pages(kvr_ctx* c, kvr_pages* pages, int rows_n, const void* hidden, const kvr_layer_weights* w,
                       const void* const* norm_q, const void* const* norm_k, void* qkv, void* out, void* stream) {
   if (!c) return KVR_ERR_ARG;
-  if (!pages || !hidden || !qkv || !out) return fail(c, KVR_ERR_ARG, "null pages, hidden, qkv or out");
+  // (buffers of a step without rows may be null, as of an empty tensor)
+  if (!pages || (rows_n != 0 && (!hidden || !qkv || !out)))
+    return fail(c, KVR_ERR_ARG, "null pages, hidden, qkv or out");
   if (((uintptr_t)hidden & 15) || ((uintptr_t)out & 15) || ((uintptr_t)qkv & 15))
     return fail(c, KVR_ERR_ARG, "hidden, qkv and out must be 16-byte aligned");
   const kvr_config& k = c->cfg;
