@@ -418,7 +418,8 @@ class Kvr:
     def kvr_prefill_pages(self, pages, hidden, weights, norm_q=None, norm_k=None, out=None, qkv=None,
                           stream=None):
         """The rows that ``pages`` (a PagedKv) has planned through the stack, their K and V in its pages.
-        norm_q, norm_k: per layer a bf16 [head_dim] gain; out and qkv may be given to be reused."""
+        norm_q, norm_k: per layer a bf16 [head_dim] gain, or None for a layer without the norm; out and qkv may be
+        given to be reused."""
         c = self.cfg
         arr = weights[0] if isinstance(weights, tuple) else weights
         m, cols = hidden.shape[0], (c.n_q_heads + 2 * c.n_kv_heads) * c.head_dim
@@ -434,10 +435,11 @@ class Kvr:
         def gains(name, g):
             if g is None:
                 return None
-            if len(g) != c.n_layers or any(x.dtype != torch.bfloat16 or not x.is_cuda or not x.is_contiguous()
-                                           or x.shape != (c.head_dim,) for x in g):
-                raise KvrError(-1, f"{name} must be {c.n_layers} bf16 device tensors [{c.head_dim}]")
-            return (ctypes.c_void_p * c.n_layers)(*[x.data_ptr() for x in g])
+            if len(g) != c.n_layers or any(x is not None and (
+                    x.dtype != torch.bfloat16 or not x.is_cuda or not x.is_contiguous()
+                    or x.shape != (c.head_dim,)) for x in g):
+                raise KvrError(-1, f"{name} must be {c.n_layers} bf16 device tensors [{c.head_dim}] (or None)")
+            return (ctypes.c_void_p * c.n_layers)(*[None if x is None else x.data_ptr() for x in g])
 
         self._check(self.lib.kvr_prefill_pages(self.ctx, pages.ctx, m, hidden.data_ptr(), arr,
                                                gains("norm_q", norm_q), gains("norm_k", norm_k), qkv.data_ptr(),
