@@ -144,3 +144,34 @@ def test_norms_of_the_largest_numbers(act):
     assert np.allclose(q, want, rtol=2.0 ** -7, equal_nan=True)
     want[4, 1, 32:] = np.nan
     assert np.allclose(k, want, rtol=2.0 ** -7, equal_nan=True)
+
+
+TIMEOUT = -4
+
+
+@pytest.mark.parametrize("rows,max_len", [(1, 1 << 17), (3, 512), (150, 1 << 17)])
+def test_a_wait_that_gave_up(rows, max_len):
+    """The status word as a wait that gave up leaves it, with arrivals of an unfinished merge, written by the host: the
+    attention returns without a result, sync reports it once and clears both, and the next call is right."""
+    from prefix_reused_prefill_gb300 import KvrError
+    w = World(8, 1, 64, "bf16", seed=19, max_len=max_len, n_pages=96, max_rows=4608)
+    n = min(max_len, 4500) - rows
+    w.step([0], [n])
+    w.step([n], [rows])
+    q = w.q()
+    want = w.pg.kvr_page_attend(1, q.cuda())
+    w.pg.kvr_pages_sync()
+    w.check(q, want)
+    words = w.pg.work.view(torch.int32)            # status, then (from byte 512 on) the arrival counters
+    assert words[0] == 0 and (words[128:128 + 152] == 0).all()
+    words[0] = 1
+    words[128:128 + 152] = 1
+    out = torch.full_like(want, 7.0)
+    w.pg.kvr_page_attend(1, q.cuda(), out=out)
+    with pytest.raises(KvrError) as e:
+        w.pg.kvr_pages_sync()
+    assert e.value.code == TIMEOUT and (out == 7).all()
+    w.pg.kvr_pages_sync()
+    assert words[0] == 0 and (words[128:128 + 152] == 0).all()
+    assert torch.equal(w.pg.kvr_page_attend(1, q.cuda()), want)
+    w.pg.kvr_pages_sync()
