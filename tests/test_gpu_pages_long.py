@@ -14,6 +14,9 @@ element's group of 32 dims):
   of v, (n / 16 + 2) 2^-22 sum w|v|; the parts of the runs are joined by a few operations of 2^-24 more;
   (The tensor-memory kernel, for more than 64 rows of a KV head, holds the weight of a row's reference at 2^7, which
   the largest is at most a factor of 2 below: 2^-25 / 2^6.)
+  (That kernel also rounds c s of the keys to fp16 for bf16 activations: a score is off by the sum of d errors of at most
+  2^-11 each times scale q_d, at most 6 * 2^-11 scale |q k|_2 but for odds of 2 exp(-18) (Hoeffding), a weight by
+  twice that.)
 * the output is rounded once: u |o|, for fp16 half of its least number, 2^-25, at the least (below 2^-14 all fp16
   numbers are 2^-24 apart).
 """
@@ -67,11 +70,11 @@ class Long:
         self.pg.kvr_page_plan(ints([x - y for x, y in zip(lens, m)]), ints(m), self.rows, max(m))
         self.pg.kvr_pages_sync()
 
-    def check(self, q, run, lost=2.0 ** -38, scale=None):
-        """run: keys of a warp's run, at most; lost: of the largest weight, per key."""
-        got = self.pg.kvr_page_attend(0, q, scale=scale)
+    def check(self, q, run, lost=2.0 ** -38, rounds_k=False):
+        """run: keys of a warp's run, at most; lost: of the largest weight, per key; rounds_k: the keys are rounded."""
+        got = self.pg.kvr_page_attend(0, q)
         self.pg.kvr_pages_sync()
-        scale = self.d ** -0.5 if scale is None else scale
+        scale = self.d ** -0.5
         u, row, worst = torch.finfo(TYPES[self.act]).eps / 2, 0, 0.0
         group = self.heads // self.kv_heads
         for (k, v), n, m in zip(self.kv, self.lens, self.m):
@@ -83,7 +86,10 @@ class Long:
                 for h in range(j * group, (j + 1) * group):
                     w = torch.softmax((scale * qs[:, h] @ kk.T).masked_fill(~seen, -np.inf), -1)
                     ref, mag, w_max = w @ vv, w @ vv.abs(), w.amax(-1, keepdim=True)
-                    tol = ((2 * 2.0 ** -11 + 2.0 ** -13 + (run / 16 + 2) * 2.0 ** -22) * mag + n * lost * top * w_max
+                    spread = 0.0
+                    if rounds_k and self.act == "bf16":
+                        spread = scale * ((qs[:, h] ** 2) @ (kk ** 2).T).amax(-1, keepdim=True).sqrt()
+                    tol = ((12 * 2.0 ** -11 * spread + 2 * 2.0 ** -11 + 2.0 ** -13 + (run / 16 + 2) * 2.0 ** -22) * mag + n * lost * top * w_max
                            + u * ref.abs() + (2.0 ** -25 if self.act == "fp16" else 0.0))
                     off = ((gs[:, h] - ref).abs() / tol).nan_to_num(nan=np.inf)
                     worst = max(worst, off.max().item())
@@ -130,3 +136,50 @@ def test_many_rows_under_sinks(act, d):
     rows, heads, n = 20, 8, 2
     w = Long([131072, 130011], [rows] * n, heads, 1, d, act, with_sinks(1, d, act, 1.0, 4))
     w.check(sink_queries(n * rows, heads, d, act, (12, 19)), 128 * 16, lost=2.0 ** -31)
+
+
+def growing(kv_heads, d, act, seed):
+    """Keys whose scores spread more and more, so that a row's maximum moves again and again."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+
+    def make(b, n):
+        size = torch.linspace(0.3, 1.5, n, device="cuda")[:, None, None]
+        k = torch.randn(n, kv_heads, d, device="cuda", generator=g) * size
+        return k.to(TYPES[act]), torch.randn(n, kv_heads, d, device="cuda", generator=g).to(TYPES[act])
+    return make
+
+
+def some_queries(n, heads, d, act):
+    return torch.randn(n, heads, d, device="cuda", generator=torch.Generator(device="cuda").manual_seed(2)).to(TYPES[act])
+
+
+@pytest.mark.parametrize("act,d,heads,kv_heads,rows", [("bf16", 128, 8, 1, 8), ("bf16", 64, 8, 1, 8), ("fp16", 128, 8, 1, 8),
+                                                       ("fp16", 64, 8, 1, 8), ("bf16", 128, 16, 4, 1), ("fp16", 64, 8, 8, 1)])
+def test_runs_of_many_pages(act, d, heads, kv_heads, rows):
+    """More than 32 pages in every warp's run (its list of pages is fetched 32 at a time, its ring wraps many times), with
+    sequences of 1 to 900 pages: segments that end inside runs, that follow one another in them, and that
+    several CTAs share."""
+    rng = np.random.Generator(np.random.PCG64([d, rows]))
+    units_of = -(-rows * heads // kv_heads // 8) * kv_heads       # of a page: row tiles of 8, KV heads
+    lens, units = [], 0
+    while units < 36 * warps():
+        lens.append(rows + int(64 * 900 ** rng.random()))
+        units += units_of * -(-lens[-1] // 64)
+    w = Long(lens, [rows] * len(lens), heads, kv_heads, d, act, growing(kv_heads, d, act, 5))
+    w.check(some_queries(w.rows, heads, d, act), 64 * 40)
+
+
+@pytest.mark.parametrize("act,d,heads,kv_heads", [("bf16", 128, 7, 1), ("fp16", 64, 4, 1), ("bf16", 64, 8, 2)])
+@pytest.mark.parametrize("lens", [[20011], [131071], [70001, 3000, 65]])
+def test_one_row_over_a_long_history(act, d, heads, kv_heads, lens):
+    """Few pages a warp and many CTAs a segment: its parts are joined in the CTAs, then by the last of them."""
+    w = Long(lens, [1] * len(lens), heads, kv_heads, d, act, growing(kv_heads, d, act, 6))
+    w.check(some_queries(w.rows, heads, d, act), 131072 // 64)
+
+
+@pytest.mark.parametrize("act,d,heads,kv_heads", [("bf16", 128, 28, 4), ("fp16", 128, 8, 2), ("bf16", 64, 8, 2), ("fp16", 64, 7, 1)])
+@pytest.mark.parametrize("lens,rows", [([16001], [30]), ([16400], [130]), ([40000, 300, 5000], [33, 260, 1])])
+def test_many_rows_over_a_long_history(act, d, heads, kv_heads, lens, rows):
+    """The tensor-memory kernel, with segments of parts from many CTAs."""
+    w = Long(lens, rows, heads, kv_heads, d, act, growing(kv_heads, d, act, 7))
+    w.check(some_queries(w.rows, heads, d, act), 40000, lost=2.0 ** -31, rounds_k=True)
