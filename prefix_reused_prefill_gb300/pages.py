@@ -114,7 +114,7 @@ class PagedKv:
         s = x.stride()
         if s[2] != 1 or (heads > 1 and s[1] != d):
             raise KvrError(-1, f"{name}: the heads of a row must be contiguous")
-        return s[0] if self._rows > 1 else max(s[0], heads * d)
+        return s[0] if self._rows > 1 else heads * d   # (one row's stride means nothing)
 
     def _gain(self, name: str, x: Optional[torch.Tensor]) -> Optional[int]:
         if x is None:

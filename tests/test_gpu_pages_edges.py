@@ -175,3 +175,20 @@ def test_a_wait_that_gave_up(rows, max_len):
     assert words[0] == 0 and (words[128:128 + 152] == 0).all()
     assert torch.equal(w.pg.kvr_page_attend(1, q.cuda()), want)
     w.pg.kvr_pages_sync()
+
+
+def test_one_row_of_any_stride():
+    """One row out of a wider buffer: its stride says nothing, odd or not."""
+    pg = handle(8, 2, 64)
+    pg.kvr_page_plan(ints([0]), ints([1]), 1)
+    rng = np.random.Generator(np.random.PCG64(20))
+    q, k, v = (rand(rng, (1, h, 64), "bf16").cuda() for h in (8, 2, 2))
+    want = pg.kvr_page_attend(0, pg.kvr_page_append(0, q, k, v))
+    wide = []
+    for x in (q, k, v):
+        buf = torch.zeros(2, x.numel() + 5, dtype=torch.bfloat16, device="cuda")
+        buf[:1, :x.numel()] = x.flatten(1)
+        wide.append(buf[:1, :x.numel()].unflatten(1, (-1, 64)))
+        assert wide[-1].stride(0) % 8
+    assert torch.equal(pg.kvr_page_attend(0, pg.kvr_page_append(0, *wide)), want)
+    pg.kvr_pages_sync()
