@@ -188,7 +188,7 @@ def test_one_row_of_any_stride():
     for x in (q, k, v):
         buf = torch.zeros(2, x.numel() + 5, dtype=torch.bfloat16, device="cuda")
         buf[:1, :x.numel()] = x.flatten(1)
-        wide.append(buf[:1, :x.numel()].unflatten(1, (-1, 64)))
+        wide.append(torch.as_strided(buf, x.shape, (buf.shape[1], 64, 1)))
         assert wide[-1].stride(0) % 8
     assert torch.equal(pg.kvr_page_attend(0, pg.kvr_page_append(0, *wide)), want)
     pg.kvr_pages_sync()
