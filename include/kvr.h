@@ -586,7 +586,8 @@ int kvr_page_plan(kvr_pages* pages, int n_seq, const int32_t* keep, const int32_
  *   q, k, v   [rows] with the heads of a row contiguous and a row stride in
  *             elements (a multiple of 8): views of one projection output work.
  *             q and q_out may both be null (k and v only); q_out may be q if
- *             its stride is n_q_heads * head_dim.
+ *             its stride is n_q_heads * head_dim, and shares no memory with
+ *             k, v or other rows of q.
  * All pointers 16-byte aligned.  rows must be the plan's.
  */
 int kvr_page_append(kvr_pages* pages, int layer, const void* q, long long q_stride, const void* k,

@@ -133,6 +133,14 @@ int layer_call(kvr_pages* c, int layer, int rows, PagesDev* dev) {
   return KVR_OK;
 }
 
+// Do n rows of w bytes, s bytes apart from a on, share a byte with the len bytes from b on?
+bool overlap(const void* a, long long s, long long n, long long w, const void* b, long long len) {
+  const long long off = (long long)((uintptr_t)b - (uintptr_t)a);   // of b, from a
+  // the first row that ends behind b's start
+  const long long i = off < w ? 0 : (off - w) / s + 1;
+  return i < n && i * s < off + len;
+}
+
 bool stride_ok(long long stride, long long row) { return stride >= row && stride % 8 == 0 && stride < (1ll << 40); }
 
 }  // namespace
@@ -268,6 +276,11 @@ int kvr_page_append(kvr_pages* c, int layer, const void* q, long long q_stride, 
   if ((q && !stride_ok(q_stride, qr)) || !stride_ok(k_stride, kr) || !stride_ok(v_stride, kr))
     return fail(c, KVR_ERR_ARG, "row strides must cover a row and be multiples of 8");
   if (q && q == q_out && q_stride != qr) return fail(c, KVR_ERR_ARG, "q_out may be q only if q's rows are contiguous");
+  const long long q_bytes = 2 * qr * rows;
+  if (q && ((q != q_out && overlap(q, 2 * q_stride, rows, 2 * qr, q_out, q_bytes)) ||
+            overlap(k, 2 * k_stride, rows, 2 * kr, q_out, q_bytes) ||
+            overlap(v, 2 * v_stride, rows, 2 * kr, q_out, q_bytes)))
+    return fail(c, KVR_ERR_ARG, "q_out shares memory with k, v or other rows of q");
   const PageAppend a = {q,      k,     v,      q_stride,   k_stride, v_stride, norm_q,
                         norm_k, q_out, rotate, rows, c->cfg.norm_eps};
   OnDevice on(c->device);
@@ -282,6 +295,8 @@ int kvr_page_read(kvr_pages* c, int layer, void* k_out, void* v_out, int rows, v
   if (rows == 0) return KVR_OK;
   if (!k_out || !v_out || !aligned(k_out) || !aligned(v_out))
     return fail(c, KVR_ERR_ARG, "missing or misaligned output pointer");
+  const long long kr = 2ll * d.Hkv * d.d;
+  if (overlap(k_out, kr, rows, kr, v_out, kr * rows)) return fail(c, KVR_ERR_ARG, "k_out and v_out share memory");
   OnDevice on(c->device);
   const cudaError_t e = launch_page_read(d, k_out, v_out, rows, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? KVR_OK : cuda_fail(c, e, "page read launch");
@@ -295,9 +310,10 @@ int kvr_page_attend(kvr_pages* c, int layer, const void* q, long long q_stride, 
   if (rows == 0) return KVR_OK;
   if (!q || !out || !aligned(q) || !aligned(out))
     return fail(c, KVR_ERR_ARG, "missing or misaligned q or out pointer");
-  if (q == out) return fail(c, KVR_ERR_ARG, "out must not be q");
-  if (!stride_ok(q_stride, (long long)d.Hq * d.d))
+  const long long qr = (long long)d.Hq * d.d;
+  if (!stride_ok(q_stride, qr))
     return fail(c, KVR_ERR_ARG, "the row stride must cover a row and be a multiple of 8");
+  if (overlap(q, 2 * q_stride, rows, 2 * qr, out, 2 * qr * rows)) return fail(c, KVR_ERR_ARG, "out shares memory with q");
   const float scale_log2 = (float)((double)scale * 1.4426950408889634);
   if (!(scale > 0.f) || !std::isfinite(scale_log2))
     return fail(c, KVR_ERR_ARG, "scale must be a positive number of at most 2.3e38");

@@ -192,3 +192,37 @@ def test_one_row_of_any_stride():
         assert wide[-1].stride(0) % 8
     assert torch.equal(pg.kvr_page_attend(0, pg.kvr_page_append(0, *wide)), want)
     pg.kvr_pages_sync()
+
+
+def test_results_that_share_memory_with_inputs_are_refused():
+    """Rows are read and written by blocks in no order, so a result over an input would hold either; q in place (each
+    head by its own lanes) and a result between the rows of a strided input stay possible."""
+    from prefix_reused_prefill_gb300 import KvrError
+    pg = handle(2, 2, 64)
+    n, w = 6, 128
+    pg.kvr_page_plan(ints([0]), ints([n]), n)
+    rng = np.random.Generator(np.random.PCG64(22))
+    x = rand(rng, (3, n + 2, 2, 64), "bf16").cuda()
+    q, k, v = (y[:n] for y in x)
+    rot = pg.kvr_page_append(0, q, k, v)
+    want = pg.kvr_page_attend(0, rot)
+    pool, before = pg.pool.clone(), x.clone()
+    refused = [lambda: pg.kvr_page_append(0, q, k, v, out=k), lambda: pg.kvr_page_append(0, q, k, v, out=v),
+               lambda: pg.kvr_page_append(0, q, k, v, out=x[0, 1:n + 1]), lambda: pg.kvr_page_append(0, q, k, v, out=x[1, 2:]),
+               lambda: pg.kvr_page_attend(0, q, out=q), lambda: pg.kvr_page_attend(0, q, out=x[0, 2:]),
+               lambda: pg.kvr_page_attend(0, x[0, 1:n + 1], out=q),
+               lambda: pg._check(pg.lib.kvr_page_read(pg.ctx, 0, k.data_ptr(), x[1, 1:].data_ptr(), n, None))]
+    for i, call in enumerate(refused):
+        with pytest.raises(KvrError) as e:
+            call()
+        assert e.value.code == -1, i
+    assert torch.equal(x, before) and torch.equal(pg.pool, pool)
+    # rows of q far apart, the result between the first two of them, and right behind the last
+    wide = torch.zeros(n * (n + 1) * w + n * w, dtype=torch.bfloat16, device="cuda")
+    far = wide[:n * (n + 1) * w].view(n, (n + 1) * w)[:, :w].unflatten(1, (2, 64))
+    far.copy_(rot)
+    for at in (w, (n - 1) * (n + 1) * w + w):
+        out = wide[at:at + n * w].view(n, 2, 64)
+        assert torch.equal(pg.kvr_page_attend(0, far, out=out), want)
+        assert torch.equal(far, rot)
+    pg.kvr_pages_sync()
