@@ -441,6 +441,7 @@ class Kvr:
                 raise KvrError(-1, f"{name} must be {c.n_layers} bf16 device tensors [{c.head_dim}] (or None)")
             return (ctypes.c_void_p * c.n_layers)(*[None if x is None else x.data_ptr() for x in g])
 
+        pages._stream(stream)   # (its memory is used there)
         self._check(self.lib.kvr_prefill_pages(self.ctx, pages.ctx, m, hidden.data_ptr(), arr,
                                                gains("norm_q", norm_q), gains("norm_k", norm_k), qkv.data_ptr(),
                                                out.data_ptr(), self._stream(stream)))

@@ -66,6 +66,7 @@ class PagedKv:
             raise KvrError(rc, "kvr_pages_create failed")
         self.ctx = ctx
         self._rows = 0
+        self._streams = {torch.cuda.current_stream(device).cuda_stream}   # whose memory pool and work are
         self._scale = cfg.head_dim ** -0.5
         t = KvrPageTables()
         self.lib.kvr_pages_tables(ctx, ctypes.byref(t))
@@ -99,8 +100,15 @@ class PagedKv:
         if rc != KVR_OK:
             raise KvrError(rc, self.lib.kvr_pages_error(self.ctx).decode())
 
-    def _stream(self, stream):
-        return stream.cuda_stream if stream is not None else _raw_stream(self._index)
+    def _stream(self, stream=None):
+        raw = stream.cuda_stream if stream is not None else _raw_stream(self._index)
+        if raw not in self._streams:
+            # pool and work are not handed out anew before this stream's work is done
+            stream = stream if stream is not None else torch.cuda.current_stream(self.device)
+            self.pool.record_stream(stream)
+            self.work.record_stream(stream)
+            self._streams.add(raw)
+        return raw
 
     def _rows_arg(self, name: str, x: torch.Tensor, heads: int) -> int:
         """Row stride of x [rows][heads][head_dim], the heads of a row contiguous."""
@@ -144,8 +152,7 @@ class PagedKv:
                 or add.get_device() != self._index or keep.dim() != 1 or add.dim() != 1 or add.numel() != n \
                 or not keep.is_contiguous() or not add.is_contiguous():
             raise KvrError(-1, f"keep and add must be contiguous int32 vectors of one length on {self.device}")
-        rc = self.lib.kvr_page_plan(self.ctx, n, keep.data_ptr(), add.data_ptr(), rows, max_add,
-                                    stream.cuda_stream if stream is not None else _raw_stream(self._index))
+        rc = self.lib.kvr_page_plan(self.ctx, n, keep.data_ptr(), add.data_ptr(), rows, max_add, self._stream(stream))
         if rc:
             self._check(rc)
         self._rows = rows

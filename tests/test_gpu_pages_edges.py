@@ -226,3 +226,29 @@ def test_results_that_share_memory_with_inputs_are_refused():
         assert torch.equal(pg.kvr_page_attend(0, far, out=out), want)
         assert torch.equal(far, rot)
     pg.kvr_pages_sync()
+
+
+@pytest.mark.parametrize("given", [True, False])
+def test_a_handle_dropped_while_another_stream_works(given):
+    """Its pool and work area are not handed out again before that stream is done.  (Only addresses are looked at: nothing
+    writes to the memory that the stream's call still uses.)"""
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    pg = handle(8, 2, 64, n_pages=4096, max_rows=64)
+    keep, add = ints([0]), ints([5])
+    pool, work = (t.data_ptr() for t in (pg.pool, pg.work))
+    sizes = pg.pool.numel(), pg.work.numel()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(1_000_000_000)
+    if given:
+        pg.kvr_page_plan(keep, add, 5, stream=side)
+    else:
+        with torch.cuda.stream(side):
+            pg.kvr_page_plan(keep, add, 5)
+    del pg
+    late = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes]
+    assert not side.query()
+    assert late[0].data_ptr() != pool and late[1].data_ptr() != work
+    torch.cuda.synchronize()
