@@ -5,7 +5,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
-#include <string>
+#include <new>
 
 #include "kvr_pages.cuh"
 
@@ -20,7 +20,7 @@ struct kvr_pages {
   int ctas = 0;           // one per SM
   int rows = 0, max_add = 0, n_seq = 0;   // of the last plan
   size_t layer_bytes = 0;
-  std::string err;
+  char err[256] = "";
 };
 
 namespace {
@@ -98,12 +98,10 @@ Layout layout(const kvr_pages_config* c) {
 }
 
 int fail(kvr_pages* c, int code, const char* fmt, ...) {
-  char buf[256];
   va_list ap;
   va_start(ap, fmt);
-  vsnprintf(buf, sizeof buf, fmt, ap);
+  vsnprintf(c->err, sizeof c->err, fmt, ap);
   va_end(ap);
-  c->err = buf;
   return code;
 }
 int cuda_fail(kvr_pages* c, cudaError_t e, const char* what) {
@@ -165,7 +163,8 @@ int kvr_pages_create(const kvr_pages_config* cfg, void* pool, size_t pool_bytes,
   if (!valid(cfg) || !pool || !work || ((uintptr_t)pool & 255) || ((uintptr_t)work & 255)) return KVR_ERR_ARG;
   const Layout L = layout(cfg);
   if (pool_bytes < kvr_pages_pool_bytes(cfg) || work_bytes < L.total) return KVR_ERR_CAPACITY;
-  kvr_pages* c = new kvr_pages();
+  kvr_pages* c = new (std::nothrow) kvr_pages();   // (no exception leaves a C entry)
+  if (!c) return KVR_ERR_CAPACITY;
   c->cfg = *cfg;
   uint8_t* w = static_cast<uint8_t*>(work);
   PagesDev& d = c->dev;
@@ -374,6 +373,6 @@ int kvr_pages_sync(kvr_pages* c, void* stream) {
   return KVR_OK;
 }
 
-const char* kvr_pages_error(const kvr_pages* c) { return c ? c->err.c_str() : "null handle"; }
+const char* kvr_pages_error(const kvr_pages* c) { return c ? c->err : "null handle"; }
 
 }  // extern "C"
