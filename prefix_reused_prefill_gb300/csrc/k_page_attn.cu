@@ -49,6 +49,12 @@ namespace kvr {
 
 namespace {
 
+using dev::ex2_approx;
+using dev::hadd2;
+using dev::held;
+using dev::hmul2;
+using dev::number2;
+
 // 16 warps: one alone waits for its loads and products most of the time.  (Tiles of
 // 16 rows, with the registers of 8 warps, take 830 cycles a page instead of 430 and
 // had half the warps for start and merge: 14 rows over 15360 tokens 51 us, 19 so.)
@@ -70,11 +76,6 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
       "l"(src), "r"(bytes), "r"(bar)
       : "memory");
-}
-__device__ __forceinline__ float ex2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 // d += a (16x16 fp16) * b (16x8 fp16).  (Not volatile, and the loads below are
 // ordinary ones: the compiler interleaves the products of several keys and dims
@@ -101,26 +102,8 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  __half2 r = __hmul2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
-  return *reinterpret_cast<uint32_t*>(&r);
-}
-__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
-  __half2 r = __hadd2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
-  return *reinterpret_cast<uint32_t*>(&r);
-}
-// a number or, for NaN, 0 (scales are not negative)
-__device__ __forceinline__ uint32_t number2(uint32_t s) {
-  __half2 r = __hmax2(*reinterpret_cast<__half2*>(&s), __float2half2_rn(0.f));
-  return *reinterpret_cast<uint32_t*>(&r);
-}
 // the halves of a pair that the first n of two stand for
 __device__ __forceinline__ uint32_t first_of_pair(int n) { return n > 1 ? 0xffffffffu : n == 1 ? 0xffffu : 0u; }
-// a register with a constant that the compiler does not form anew at each use
-__device__ __forceinline__ uint32_t held(uint32_t x) {
-  asm volatile("" : "+r"(x));
-  return x;
-}
 // codes in bits 0-3 (4-7) of both halves as the fp16 numbers c - 8; k1024 and k64
 // hold those numbers in both halves
 template <uint32_t kMask>

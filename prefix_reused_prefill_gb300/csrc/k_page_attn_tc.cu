@@ -64,6 +64,12 @@ namespace kvr {
 
 namespace {
 
+using dev::ex2_approx;
+using dev::hadd2;
+using dev::held;
+using dev::hmul2;
+using dev::number2;
+
 constexpr int kTile = 128;
 constexpr int kPairRows = kPageTcRows;
 constexpr int kKeys = 128;
@@ -144,11 +150,6 @@ __device__ __forceinline__ void commit(uint32_t elected, uint32_t bar) {
       "r"(elected)
       : "memory");
 }
-__device__ __forceinline__ float ex2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -203,23 +204,6 @@ __device__ __forceinline__ bool any_of(int id, int n, bool p) {
 }
 __device__ __forceinline__ void named_sync(int id, int n) {
   asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
-}
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  __half2 r = __hmul2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
-  return *reinterpret_cast<uint32_t*>(&r);
-}
-__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
-  __half2 r = __hadd2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
-  return *reinterpret_cast<uint32_t*>(&r);
-}
-// a number or, for NaN, 0 (scales are not negative)
-__device__ __forceinline__ uint32_t number2(uint32_t s) {
-  __half2 r = __hmax2(*reinterpret_cast<__half2*>(&s), __float2half2_rn(0.f));
-  return *reinterpret_cast<uint32_t*>(&r);
-}
-__device__ __forceinline__ uint32_t held(uint32_t x) {
-  asm volatile("" : "+r"(x));
-  return x;
 }
 // a b - c, rounded once
 __device__ __forceinline__ uint32_t hfms2(uint32_t a, uint32_t b, uint32_t c) {

@@ -207,6 +207,30 @@ __device__ __forceinline__ uint32_t pack_act(float lo, float hi) {
   return pack_bf16x2(lo, hi);
 }
 
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  __half2 r = __hmul2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+  return *reinterpret_cast<uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
+  __half2 r = __hadd2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+  return *reinterpret_cast<uint32_t*>(&r);
+}
+// a number or, for NaN, 0 (scales are not negative)
+__device__ __forceinline__ uint32_t number2(uint32_t s) {
+  __half2 r = __hmax2(*reinterpret_cast<__half2*>(&s), __float2half2_rn(0.f));
+  return *reinterpret_cast<uint32_t*>(&r);
+}
+// a register with a constant that the compiler does not form anew at each use
+__device__ __forceinline__ uint32_t held(uint32_t x) {
+  asm volatile("" : "+r"(x));
+  return x;
+}
+
 }  // namespace dev
 }  // namespace kvr
 #endif
