@@ -482,8 +482,8 @@ page_attn_kernel(const PagesDev p, const PageAttend a) {
     int see[2];               // last key these rows see
     float m_run[2] = {-INFINITY, -INFINITY}, l_run[2];
     // The exponent that a row's weights are taken under: 15 below the maximum, which fp16 has
-    // room for (in O and in l alike).  Both are rounded up, so no weight passes 2^15; whole
-    // numbers, so that rescaling is exact.
+    // room for (in O and in l alike).  Both are rounded up, so no weight passes 2^15, and the
+    // largest, which often is most of the sum, is 2^15 without a rounding.
     auto ref_of = [](float m) { return __fadd_ru(m, -15.f); };
     float o[2 * kG][4];       // O^T tiles 2 j, 2 j + 1: rows g, g + 8 are dims 32 j + 4 g + 0, 1 and + 2, 3
     bool fresh = true;
@@ -556,7 +556,7 @@ page_attn_kernel(const PagesDev p, const PageAttend a) {
       for (int c = 0; c < 2; ++c) {
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], d));
-        mx[c] = ceilf(__fmul_ru(mx[c], f[c]));
+        mx[c] = __fmul_ru(mx[c], f[c]);
       }
       const bool moved = mx[0] > m_run[0] || mx[1] > m_run[1];
       if (__any_sync(0xffffffffu, moved)) {

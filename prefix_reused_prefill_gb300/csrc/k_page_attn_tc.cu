@@ -77,8 +77,8 @@ constexpr int kDecodeWarp = 16;
 constexpr int kThreads = 32 * (kDecodeWarp + 4);
 constexpr float kLazyMax = 8.0f;
 // Weights carry a factor of 2^7 (in O and in l alike), so that the largest, 2^8 over the
-// reference, is 2^15 and what fp16 drops is below 2^-31 of it.  References are whole numbers,
-// and every rounding goes the way that no weight is larger.
+// reference, is 2^15 and what fp16 drops is below 2^-31 of it.  Every rounding of a reference
+// goes the way that no weight is larger.
 constexpr float kHead = 7.0f;
 
 template <int D, bool F16>
@@ -735,7 +735,7 @@ page_attn_tc_kernel(const PagesDev p, const PageAttendTc a) {
         }
         part[0] = dev::add2(part[0], part[1]);
         sum = part[0].x + part[0].y;
-        const float top = ceilf(__fmul_ru(fmaxf(mx[0], mx[1]), f));
+        const float top = __fmul_ru(fmaxf(mx[0], mx[1]), f);
         return top < -kScoreMax ? -INFINITY : top;
       };
       for (int j = j0; j < j1; ++j) {
