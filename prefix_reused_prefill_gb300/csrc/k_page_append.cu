@@ -14,10 +14,11 @@
 // holds two tokens) meet in one 32-byte sector.
 //
 // 8.2k rows of 32 + 2 * 8 heads of 128 with norms: 42.9 us, 4.1 TB/s of 176 MB, 61 %
-// of a plain copy's rate.  Of that k's second floats take 6 us (with them k is
-// that of 64 bits in all of 50 million values, in 32 bits two or three codes
-// in 8 million moved), the rest is arithmetic too, and more loads in flight
-// (through shared memory) or more CTAs for q change nothing.  q, k and v in one loop
+// of a plain copy's rate, with the issue slots 63 % busy and waits for loads the longest
+// (3.0 warps of 6.5 an issue): each CTA has one row group and little after its start of
+// dependent loads.  k's second floats take 6 us (with them k is that of 64 bits in all
+// of 50 million values, in 32 bits two or three codes in 8 million moved); more loads
+// in flight (through shared memory) or more CTAs for q change nothing.  q, k and v in one loop
 // of the same CTAs: 47.8.  One to 254 rows: 3 to 4 us, a launch.
 #include "kvr_pages.cuh"
 

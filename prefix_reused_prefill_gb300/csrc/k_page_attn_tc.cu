@@ -10,10 +10,12 @@
 // scores' twice as large, so K and V are two fp16 terms each, the second the exact rest
 // of the first, and every product runs once for each: 5.6e-4 -> 2.6e-4 of the
 // outputs in the mean square at scores of deviation 2 (2.1e-4 is the output's rounding), for
-// 33.5 instead of 32 us in a mixed batch of 64-wide heads and 915 instead of 673 us
-// in the long prompts below.  q is scaled per row by a power of two that brings
-// its largest element to 2^10 (what is 2^-25 of that or more is exact), and is fp16; P is
-// fp16 (2^-11).  Sums, maxima and O are fp32.
+// 31.4 instead of 30.3 us in a mixed batch of 64-wide heads and 897 instead of 667 us
+// in the long prompts below (twice the products, one stage of K and V, and 88 bytes a
+// thread of spilled registers; the other forms spill 8 to 28).  q is scaled per row by a
+// power of two that brings its largest element to 2^10 (what is 2^-25 of that or more is
+// exact), and is fp16; P is fp16 with a factor of 2^7 (2^-11, and nothing above 2^-31 of
+// the largest is lost).  Sums, maxima and O are fp32.
 //
 // Writing a 4-bit block as fp16 costs about as many instructions as the softmax
 // of one 128-row tile over it, so a CTA runs two row tiles over each block: one
@@ -44,7 +46,7 @@
 // Every wait is bounded; a CTA whose wait gave up frees its tensor memory.
 //
 // Two prompts of up to 2047 rows over up to 14001 tokens (32 heads in groups of 4,
-// d = 128, bf16, 766 GFLOP): 673 us, 1.14 PFLOP/s, 61 % of what a library product
+// d = 128, bf16, 766 GFLOP): 667 us, 1.15 PFLOP/s, 60 % of what a library product
 // reaches.  A block of 128 keys takes a CTA about 4000 cycles, 2080 of them
 // products.  Each tile's chain is what lasts so long: 2000 of softmax (1400 for the weights,
 // the other tile and the writing warps on the same schedulers), 940 until P V is

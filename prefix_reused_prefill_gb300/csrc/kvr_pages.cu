@@ -27,23 +27,24 @@ namespace {
 
 constexpr size_t kAlign = 256;
 // Rows of a sequence and KV head (rows * group) up to which the split kernel
-// takes the sequence: 64 where every sequence of the step has so few (four
-// conversations of 8 rows, group 7, over 15k tokens: 50 us, 55 us by the
-// tensor-memory kernel), but 16 where that kernel runs anyway (12 conversations
-// of 1 to 120 rows, group 4, over up to 4k tokens: 31 us, 36 us with 32; large
-// batches lean the other way: 48 of 7 to 70 rows, group 7, over up to 8k 135 us,
-// 124 with 32).
+// takes the sequence: 64 where every sequence of the step has so few, but 16 where
+// the tensor-memory kernel runs anyway.  Four conversations over 15k tokens take, by
+// this and by that kernel: of 4 rows in groups of 7, 35 and 52 us, of 8 in groups of 4,
+// 57 and 74, of 8 in groups of 7, 52 and 52; of 16 in groups of 4, 102 and 74, where
+// the split kernel costs more but takes the keys of bf16 rows unrounded.  12 conversations
+// of 1 to 120 rows, group 4, over up to 4k tokens: 31 us, 37 with 32; large batches lean
+// the other way: 64 of 7 to 70 rows, group 7, over up to 16k 274 us, 258 with 32.
 constexpr int kPageMany = 64, kPageManyBeside = 16;
 // Pages (of one KV head and 8 rows) per CTA up to which the split kernel takes all
 // the step's rows: it needs one launch and about 12 us, the tensor-memory kernel
-// two and 22, but a page costs it 430 cycles for each 8 rows.  126 rows (group 7)
-// over 1024 / 8192 / 16000 / 32000 tokens, 7 to 213 pages a CTA: 12.1 / 23.6 / 34.4 /
-// 55.7 us, by the tensor-memory kernel 22.4 / 29.5 / 34.6 / 39.6.  (The host
+// two and 22, but a page costs it 450 cycles for each 8 rows.  126 rows (group 7)
+// over 1024 / 8192 / 16000 / 32000 tokens, 7 to 213 pages a CTA: 12.6 / 24.3 / 36.1 /
+// 59.0 us, by the tensor-memory kernel 22.5 / 29.5 / 34.7 / 39.7.  (The host
 // knows how long the sequences can be, not how long they are.)
 constexpr int kPageFew = 100;
 // key blocks a CTA of the tensor-memory kernel takes at least: 254 rows over
-// 1668 tokens take 37.8 us with 2, 38.3 with 3 and 39.7 with 5, where fewer CTAs
-// run longer but leave fewer parts to merge; 18 rows over 2048: 24.0, 25.0, 27.6
+// 1668 tokens take 35.4 us with 2, 36.2 with 3 and 38.1 with 5, where fewer CTAs
+// run longer but leave fewer parts to merge; 18 rows over 2048: 23.7, 24.7, 27.3
 constexpr int kPageMinUnits = 2;
 inline size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
