@@ -15,7 +15,9 @@
 // thread of spilled registers; the other forms spill 8 to 28).  q is scaled per row by a
 // power of two that brings its largest element to 2^10 (what is 2^-25 of that or more is
 // exact), and is fp16; P is fp16 with a factor of 2^7 (2^-11, and nothing above 2^-31 of
-// the largest is lost).  Sums, maxima and O are fp32.
+// the largest is lost).  Sums, maxima and O are fp32.  (The tensor core cuts its sums, so that
+// with weights and values all alike an output is low by 0.2 % after a CTA's run of 0.44
+// million keys, two terms each, and by 0.34 % after 1.8 million.)
 //
 // Writing a 4-bit block as fp16 costs about as many instructions as the softmax
 // of one 128-row tile over it, so a CTA runs two row tiles over each block: one
