@@ -646,6 +646,92 @@ int kvr_prefill_pages(kvr_ctx* ctx, kvr_pages* pages, int rows, const void* hidd
 int kvr_pages_sync(kvr_pages* pages, void* stream);
 const char* kvr_pages_error(const kvr_pages* pages);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Requests of one batch that differ: sampling.  (The pages' speculative step
+ * "must give the same words as plain decoding"; for requests that sample, the
+ * same in distribution.  The random numbers are the caller's, so a step can
+ * be repeated.)
+ *
+ * The distribution of a row.  The tokens stand in descending order of their
+ * logits x, equal ones in that of their index, and weigh
+ *   w = exp((x - max) / temperature);   temperature 0: 1 for the first, else 0.
+ * Kept are the first top_k of them, as far as w >= min_p; and of those the
+ * shortest run from the first that holds at least top_p of their weight.  The
+ * distribution p is w over the kept tokens, divided by its sum.
+ *   temperature  0, or 2^-64 .. 2^64.
+ *   top_k        <= 0: every token.
+ *   min_p        <= 0: every token; above 1 as 1.
+ *   top_p        >= 1: every token; <= 0: the first one.
+ * A logit of -infinity is never drawn; tokens at +infinity share the row
+ * alone.  A row that holds a NaN, only -infinity, a setting out of its range or
+ * NaN, or a random number outside [0, 1) has no distribution: its token is -1.
+ * Weights are summed as whole numbers of 2^-44 of the largest, so the sums
+ * (and with them the tokens) do not depend on the launch.
+ *
+ * The calls have no handle: they hold nothing between calls, work only in the
+ * memory that they are given, and may run at the same time on several streams;
+ * they can be captured.  The device of the memory has to be the current one.
+ * Errors: a negative code, kvr_batch_error says why (the calling thread's last
+ * failure).  A refused call launches nothing.
+ */
+#define KVR_ACT_F32 2   /* type of logits, besides KVR_ACT_BF16 and KVR_ACT_F16 */
+
+/* Settings, device arrays with one entry per request; null for the default. */
+typedef struct kvr_sampling {
+  const float* temperature; /* 1 */
+  const int32_t* top_k;     /* 0 */
+  const float* min_p;       /* 0 */
+  const float* top_p;       /* 1 */
+} kvr_sampling;
+
+/*
+ * A token of each row: the first kept one, in the order above, whose running
+ * weight is more than u times the kept weight.
+ *   logits     [rows][vocab] of `type`, row stride in elements (>= vocab); vocab
+ *              1 .. KVR_MAX_VOCAB.
+ *   settings   arrays of [rows], or null.
+ *   u          float [rows] in [0, 1).
+ *   token      int32 [rows]; -1 for a row without a distribution.
+ *   prob       float [rows], the token's share p (0 for -1), or null.
+ *   dist       float [rows][vocab], row stride dist_stride: p of every token (all 0
+ *              for a row without a distribution), or null.
+ * token, prob and dist share no memory with the inputs.
+ */
+int kvr_sample(const void* logits, int type, long long stride, int rows, int vocab,
+               const kvr_sampling* settings, const float* u, int32_t* token, float* prob, float* dist,
+               long long dist_stride, void* stream);
+
+/*
+ * Speculative sampling of several sequences, the form of kvr_verify_accept for
+ * requests that sample.  Rows cu_rows[b] .. cu_rows[b + 1] - 1 are sequence b's:
+ * tokens holds [t0, d1 .. dk], and a row's logits those of the token after it.
+ * Draft d after row i stays when u[i] * q(d) < p(d), p being row i's
+ * distribution and q the one that d was drawn from.  At the first draft that does
+ * not stay the next token is drawn from max(p - q, 0) (from p if that is zero
+ * everywhere), after the last row from p, by u_next[b], as in kvr_sample.
+ * So every token is distributed as if it had been sampled from p.
+ *   rows         of the buffers; cu_rows[n_seq] may be smaller (a padded batch).
+ *   settings     arrays of [n_seq], or null.
+ *   cu_rows      device int32 [n_seq + 1], not decreasing; n_seq 1 .. 65536.
+ *   tokens       device int32 [rows].  A draft outside the vocabulary does not stay.
+ *   draft_probs  float [rows][vocab], row stride draft_stride: q of the draft after each
+ *                row (no last row of a sequence is read); null: each draft was certain
+ *                (looked up, or taken greedily): q = 1 at d.
+ *   u            float [rows] (last rows' are not read); u_next float [n_seq].
+ *   accepted     int32 [n_seq], drafts that stay.  next: int32 [n_seq], the token after
+ *                them, -1 where that row has no distribution; both for a sequence
+ *                without rows: 0 and -1.
+ *   work         kvr_accept_work_bytes(rows) bytes, 16-byte aligned, for this call alone.
+ */
+size_t kvr_accept_work_bytes(int rows);
+int kvr_accept(const void* logits, int type, long long stride, int rows, int vocab,
+               const kvr_sampling* settings, int n_seq, const int32_t* cu_rows, const int32_t* tokens,
+               const float* draft_probs, long long draft_stride, const float* u, const float* u_next,
+               int32_t* accepted, int32_t* next, void* work, size_t work_bytes, void* stream);
+
+const char* kvr_batch_error(void);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,121 @@
+// C ABI of what the requests of one batch differ by (include/kvr.h): checks of
+// arguments, then the launches of k_sample.cu.
+#include <algorithm>
+#include <cstdarg>
+#include <cstdio>
+
+#include "kvr_batch.cuh"
+
+using namespace kvr;
+
+namespace {
+
+thread_local char g_error[256] = "";
+
+int fail(int code, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_error, sizeof g_error, fmt, ap);
+  va_end(ap);
+  return code;
+}
+int cuda_fail(cudaError_t e, const char* what) { return fail(KVR_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e)); }
+
+// SMs of the current device
+cudaError_t device_sms(int* sms) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  return e;
+}
+
+constexpr int kMaxSampleRows = 1 << 20;
+
+int type_bytes(int type) { return type == KVR_ACT_F32 ? 4 : 2; }
+bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+int logits_check(const void* logits, int type, long long stride, int rows, int vocab, const kvr_sampling* s) {
+  if (type != KVR_ACT_F32 && type != KVR_ACT_BF16 && type != KVR_ACT_F16)
+    return fail(KVR_ERR_ARG, "logits of type %d", type);
+  if (rows < 0 || rows > kMaxSampleRows) return fail(KVR_ERR_ARG, "%d rows outside [0, %d]", rows, kMaxSampleRows);
+  if (vocab < 1 || vocab > KVR_MAX_VOCAB) return fail(KVR_ERR_ARG, "vocab %d outside [1, %d]", vocab, KVR_MAX_VOCAB);
+  if (rows > 1 && stride < vocab) return fail(KVR_ERR_ARG, "the row stride must cover a row");
+  if (rows && (!logits || !aligned(logits, type_bytes(type)))) return fail(KVR_ERR_ARG, "missing or misaligned logits");
+  if (s && !(aligned(s->temperature, 4) && aligned(s->top_k, 4) && aligned(s->min_p, 4) && aligned(s->top_p, 4)))
+    return fail(KVR_ERR_ARG, "misaligned settings");
+  return KVR_OK;
+}
+
+int run_sample(const SampleParams& p, void* stream) {
+  int sms = 0;
+  cudaError_t e = device_sms(&sms);
+  if (e == cudaSuccess) e = launch_sample(p, sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KVR_OK : cuda_fail(e, "sample launch");
+}
+
+}  // namespace
+
+extern "C" {
+
+int kvr_sample(const void* logits, int type, long long stride, int rows, int vocab, const kvr_sampling* settings,
+               const float* u, int32_t* token, float* prob, float* dist, long long dist_stride, void* stream) {
+  if (int rc = logits_check(logits, type, stride, rows, vocab, settings)) return rc;
+  if (rows == 0) return KVR_OK;
+  if (!u || !token || !aligned(u, 4) || !aligned(token, 4) || !aligned(prob, 4) || !aligned(dist, 4))
+    return fail(KVR_ERR_ARG, "missing or misaligned u, token, prob or dist");
+  if (dist && rows > 1 && dist_stride < vocab) return fail(KVR_ERR_ARG, "dist's row stride must cover a row");
+  SampleParams p = {};
+  p.logits = logits;
+  p.stride = stride;
+  p.rows = rows;
+  p.vocab = vocab;
+  p.type = type;
+  if (settings) p.s = *settings;
+  p.u = u;
+  p.token = token;
+  p.prob = prob;
+  p.dist = dist;
+  p.dist_stride = dist_stride;
+  return run_sample(p, stream);
+}
+
+size_t kvr_accept_work_bytes(int rows) { return rows < 0 || rows > kMaxSampleRows ? 0 : (size_t)std::max(rows, 1) * 4; }
+
+int kvr_accept(const void* logits, int type, long long stride, int rows, int vocab, const kvr_sampling* settings,
+               int n_seq, const int32_t* cu_rows, const int32_t* tokens, const float* draft_probs,
+               long long draft_stride, const float* u, const float* u_next, int32_t* accepted, int32_t* next,
+               void* work, size_t work_bytes, void* stream) {
+  if (int rc = logits_check(logits, type, stride, rows, vocab, settings)) return rc;
+  if (n_seq < 1 || n_seq > 65536) return fail(KVR_ERR_ARG, "%d sequences outside [1, 65536]", n_seq);
+  if (!cu_rows || !u_next || !accepted || !next || (rows && (!tokens || !u)))
+    return fail(KVR_ERR_ARG, "null cu_rows, tokens, u, u_next, accepted or next");
+  for (const void* q : {(const void*)cu_rows, (const void*)tokens, (const void*)u, (const void*)u_next,
+                        (const void*)accepted, (const void*)next, (const void*)draft_probs})
+    if (!aligned(q, 4)) return fail(KVR_ERR_ARG, "misaligned pointer");
+  if (draft_probs && rows > 1 && draft_stride < vocab)
+    return fail(KVR_ERR_ARG, "the drafts' row stride must cover a row");
+  if (!work || !aligned(work, 16) || work_bytes < kvr_accept_work_bytes(rows))
+    return fail(KVR_ERR_CAPACITY, "work area missing, misaligned or smaller than %zu bytes", kvr_accept_work_bytes(rows));
+  SampleParams p = {};
+  p.logits = logits;
+  p.stride = stride;
+  p.rows = rows;
+  p.vocab = vocab;
+  p.type = type;
+  if (settings) p.s = *settings;
+  p.u = u;
+  p.cu = cu_rows;
+  p.n_seq = n_seq;
+  p.tokens = tokens;
+  p.q = draft_probs;
+  p.q_stride = draft_stride;
+  p.u_next = u_next;
+  p.outcome = static_cast<int32_t*>(work);
+  p.accepted = accepted;
+  p.next = next;
+  return run_sample(p, stream);
+}
+
+const char* kvr_batch_error(void) { return g_error; }
+
+}  // extern "C"

@@ -34,7 +34,8 @@ EXPORTED = ["kvr_arena_bytes", "kvr_scratch_bytes", "kvr_ctx_create", "kvr_ctx_i
             "kvr_prefill_batch", "kvr_selftest_wait", "kvr_verify_accept_batch",
             "kvr_pages_pool_bytes", "kvr_pages_work_bytes", "kvr_pages_create", "kvr_pages_destroy",
             "kvr_pages_tables", "kvr_pages_sync", "kvr_pages_error", "kvr_page_plan", "kvr_page_append",
-            "kvr_page_read", "kvr_page_attend", "kvr_prefill_pages"]
+            "kvr_page_read", "kvr_page_attend", "kvr_prefill_pages",
+            "kvr_sample", "kvr_accept", "kvr_accept_work_bytes", "kvr_batch_error"]
 
 
 class KvrError(RuntimeError):
@@ -70,6 +71,10 @@ class KvrPagesConfig(ctypes.Structure):
                 ("n_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("max_seqs", ctypes.c_int),
                 ("max_len", ctypes.c_int), ("max_rows", ctypes.c_int), ("act", ctypes.c_int),
                 ("rope_theta", ctypes.c_float), ("norm_eps", ctypes.c_float)]
+
+
+class KvrSampling(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_void_p) for f in ("temperature", "top_k", "min_p", "top_p")]
 
 
 class KvrPageTables(ctypes.Structure):
@@ -133,6 +138,10 @@ def load_library(path: str = LIB_PATH):
         "kvr_page_read": (I, [V, I, V, V, I, V]),
         "kvr_prefill_pages": (I, [V, V, I, V, P(KvrLayerWeights), P(V), P(V), V, V, V]),
         "kvr_page_attend": (I, [V, I, V, LL, V, I, ctypes.c_float, I, V]),
+        "kvr_sample": (I, [V, I, LL, I, I, P(KvrSampling), V, V, V, V, LL, V]),
+        "kvr_accept": (I, [V, I, LL, I, I, P(KvrSampling), I, V, V, V, LL, V, V, V, V, V, Z, V]),
+        "kvr_accept_work_bytes": (Z, [I]),
+        "kvr_batch_error": (ctypes.c_char_p, []),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
