@@ -648,7 +648,7 @@ const char* kvr_pages_error(const kvr_pages* pages);
 
 /*
  * ---------------------------------------------------------------------------
- * Requests of one batch that differ: sampling.  (The pages' speculative step
+ * Requests of one batch that differ: sampling and adapters.  (The pages' speculative step
  * "must give the same words as plain decoding"; for requests that sample, the
  * same in distribution.  The random numbers are the caller's, so a step can
  * be repeated.)
@@ -729,6 +729,55 @@ int kvr_accept(const void* logits, int type, long long stride, int rows, int voc
                const kvr_sampling* settings, int n_seq, const int32_t* cu_rows, const int32_t* tokens,
                const float* draft_probs, long long draft_stride, const float* u, const float* u_next,
                int32_t* accepted, int32_t* next, void* work, size_t work_bytes, void* stream);
+
+/*
+ * Low-rank adapters beside a shared projection: each sequence of a batch may have
+ * one of its own.  For row r of a sequence with adapter a
+ *   out[r][n] = base[r][n] + scale sum_j B[n][j] (sum_k A[part(n) rank + j][k] x[r][k]),
+ * rows of sequences without an adapter are base's.
+ *
+ * A projection ("site") may have up to three outputs that share their input
+ * (q, k and v; gate and up): parts, side by side in out, each with an A of its own.
+ *   a   [n_parts * rank][k], part after part;  b  [sum of cols][rank].
+ */
+typedef struct kvr_adapter {
+  const void* a;   /* device, 16-byte aligned, type of the site    */
+  const void* b;
+  int rank;        /* a multiple of 8, 8 .. the site's max_rank    */
+  float scale;
+} kvr_adapter;
+
+typedef struct kvr_adapter_site {
+  const kvr_adapter* table; /* device [n_adapters]; an entry out of its range adapts nothing */
+  int n_adapters;
+  int max_rank;             /* a multiple of 8, at most KVR_MAX_RANK                         */
+  int k;                    /* inputs, a multiple of 8                                       */
+  int n_parts;              /* 1 .. 3                                                        */
+  int cols[3];              /* outputs of each part, multiples of 8                          */
+  int type;                 /* KVR_ACT_BF16 or KVR_ACT_F16: a, b and x                       */
+} kvr_adapter_site;
+#define KVR_MAX_RANK 128
+
+/*
+ *   x          [rows][k], row stride in elements (a multiple of 8).
+ *   cu_rows    device int32 [n_seq + 1], not decreasing: sequence b has the rows
+ *              cu_rows[b] .. cu_rows[b + 1] - 1; rows before the first and behind the last
+ *              one are left as they were.  n_seq 1 .. 2048.
+ *   which      device int32 [n_seq], the sequence's adapter; others than 0 ..
+ *              n_adapters - 1 stand for none.
+ *   base, out  [rows][sum of cols] of `out_type` (the site's type or KVR_ACT_F32), row
+ *              strides in elements (multiples of 8).  base may be out (the same stride
+ *              then) or null (zeros); otherwise out shares no memory with the inputs.
+ *   work       kvr_adapt_work_bytes(site, rows) bytes, 16-byte aligned, for this call alone.
+ * x, base and out are 16-byte aligned.  Sums are 32-bit.  The low-rank product
+ * goes on in terms of the site's type, two (fp16: 22 bits) or, for bf16, two or,
+ * with 32-bit outputs, three (16 or 24 bits); out is rounded once.  A row whose
+ * low-rank product is not finite reads NaN.
+ */
+size_t kvr_adapt_work_bytes(const kvr_adapter_site* site, int rows);
+int kvr_adapt(const kvr_adapter_site* site, const void* x, long long x_stride, const int32_t* cu_rows,
+              const int32_t* which, int n_seq, int rows, const void* base, long long base_stride, void* out,
+              long long out_stride, int out_type, void* work, size_t work_bytes, void* stream);
 
 const char* kvr_batch_error(void);
 

@@ -1,5 +1,5 @@
 // C ABI of what the requests of one batch differ by (include/kvr.h): checks of
-// arguments, then the launches of k_sample.cu.
+// arguments, then the launches of k_sample.cu and k_adapt.cu.
 #include <algorithm>
 #include <cstdarg>
 #include <cstdio>
@@ -44,6 +44,18 @@ int logits_check(const void* logits, int type, long long stride, int rows, int v
   if (s && !(aligned(s->temperature, 4) && aligned(s->top_k, 4) && aligned(s->min_p, 4) && aligned(s->top_p, 4)))
     return fail(KVR_ERR_ARG, "misaligned settings");
   return KVR_OK;
+}
+
+constexpr int kMaxAdaptRows = 1 << 22;
+
+bool site_ok(const kvr_adapter_site* s) {
+  if (!s || !s->table || !aligned(s->table, 8) || s->n_adapters < 1 || s->max_rank < 8 || s->max_rank > KVR_MAX_RANK ||
+      s->max_rank % 8 || s->k < 8 || s->k % 8 || s->k > 1 << 20 || s->n_parts < 1 || s->n_parts > 3 ||
+      (s->type != KVR_ACT_BF16 && s->type != KVR_ACT_F16))
+    return false;
+  for (int j = 0; j < s->n_parts; ++j)
+    if (s->cols[j] < 8 || s->cols[j] % 8 || s->cols[j] > 1 << 20) return false;
+  return true;
 }
 
 int run_sample(const SampleParams& p, void* stream) {
@@ -114,6 +126,60 @@ int kvr_accept(const void* logits, int type, long long stride, int rows, int voc
   p.accepted = accepted;
   p.next = next;
   return run_sample(p, stream);
+}
+
+size_t kvr_adapt_work_bytes(const kvr_adapter_site* site, int rows) {
+  if (!site_ok(site) || rows < 0 || rows > kMaxAdaptRows) return 0;
+  return adapt_work_bytes(*site, std::max(rows, 1));
+}
+
+int kvr_adapt(const kvr_adapter_site* site, const void* x, long long x_stride, const int32_t* cu_rows,
+              const int32_t* which, int n_seq, int rows, const void* base, long long base_stride, void* out,
+              long long out_stride, int out_type, void* work, size_t work_bytes, void* stream) {
+  if (!site_ok(site))
+    return fail(KVR_ERR_ARG, "a site's table, adapters, ranks, widths or type are out of their range");
+  if (rows < 0 || rows > kMaxAdaptRows) return fail(KVR_ERR_ARG, "%d rows outside [0, %d]", rows, kMaxAdaptRows);
+  if (n_seq < 1 || n_seq > kAdaptMaxSeqs) return fail(KVR_ERR_ARG, "%d sequences outside [1, %d]", n_seq, kAdaptMaxSeqs);
+  if (out_type != site->type && out_type != KVR_ACT_F32) return fail(KVR_ERR_ARG, "outputs of type %d", out_type);
+  if (rows == 0) return KVR_OK;
+  if (!x || !cu_rows || !which || !out) return fail(KVR_ERR_ARG, "null x, cu_rows, which or out");
+  if (!aligned(x, 16) || !aligned(base, 16) || !aligned(out, 16) || !aligned(cu_rows, 4) || !aligned(which, 4))
+    return fail(KVR_ERR_ARG, "x, base and out must be 16-byte aligned");
+  long long n = 0;
+  for (int j = 0; j < site->n_parts; ++j) n += site->cols[j];
+  if (rows == 1) x_stride = site->k, base_stride = out_stride = n;   // (one row's stride means nothing)
+  if (x_stride < site->k || x_stride % 8 || out_stride < n || out_stride % 8 ||
+      (base && (base_stride < n || base_stride % 8)))
+    return fail(KVR_ERR_ARG, "row strides must cover a row and be multiples of 8");
+  if (base == out && base_stride != out_stride) return fail(KVR_ERR_ARG, "base is out, but its stride is another");
+  const long long size = out_type == KVR_ACT_F32 ? 4 : 2;
+  const auto apart = [&](const void* a, long long bytes) {
+    const uintptr_t p = (uintptr_t)a, q = (uintptr_t)out;
+    return p + bytes <= q || q + ((rows - 1) * out_stride + n) * size <= p;
+  };
+  if (!apart(x, ((rows - 1) * x_stride + site->k) * 2) ||
+      (base && base != out && !apart(base, ((rows - 1) * base_stride + n) * size)))
+    return fail(KVR_ERR_ARG, "out shares memory with x or other rows of base");
+  if (!work || !aligned(work, 16) || work_bytes < adapt_work_bytes(*site, rows))
+    return fail(KVR_ERR_CAPACITY, "work area missing, misaligned or smaller than %zu bytes", adapt_work_bytes(*site, rows));
+  AdaptParams p = {};
+  p.site = *site;
+  p.x = x;
+  p.x_stride = x_stride;
+  p.cu = cu_rows;
+  p.which = which;
+  p.n_seq = n_seq;
+  p.rows = rows;
+  p.base = base;
+  p.base_stride = base_stride;
+  p.out = out;
+  p.out_stride = out_stride;
+  p.out_type = out_type;
+  p.part = static_cast<float*>(work);
+  int sms = 0;
+  cudaError_t e = device_sms(&sms);
+  if (e == cudaSuccess) e = launch_adapt(p, sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KVR_OK : cuda_fail(e, "adapt launch");
 }
 
 const char* kvr_batch_error(void) { return g_error; }

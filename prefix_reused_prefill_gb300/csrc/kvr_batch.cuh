@@ -34,4 +34,25 @@ constexpr int kStays = -2;
 
 cudaError_t launch_sample(const SampleParams& p, int sms, cudaStream_t st);
 
+constexpr int kAdaptMaxSeqs = 2048;
+constexpr int kAdaptMaxSplit = 32;
+constexpr int kAdaptRows = 8;        // rows of a tile
+struct AdaptParams {
+  kvr_adapter_site site;
+  const void* x;
+  long long x_stride;
+  int x16;                 // x is fp16 that holds the site's bf16 values
+  const int32_t *cu, *which;
+  int n_seq, rows;
+  const void* base;        // or null
+  long long base_stride;
+  void* out;
+  long long out_stride;
+  int out_type;
+  float* part;             // [ksplit][rows][n_parts * max_rank] parts of the low-rank products
+  int ksplit;
+};
+size_t adapt_work_bytes(const kvr_adapter_site& s, int rows);
+cudaError_t launch_adapt(AdaptParams p, int sms, cudaStream_t st);
+
 }  // namespace kvr

@@ -35,7 +35,8 @@ EXPORTED = ["kvr_arena_bytes", "kvr_scratch_bytes", "kvr_ctx_create", "kvr_ctx_i
             "kvr_pages_pool_bytes", "kvr_pages_work_bytes", "kvr_pages_create", "kvr_pages_destroy",
             "kvr_pages_tables", "kvr_pages_sync", "kvr_pages_error", "kvr_page_plan", "kvr_page_append",
             "kvr_page_read", "kvr_page_attend", "kvr_prefill_pages",
-            "kvr_sample", "kvr_accept", "kvr_accept_work_bytes", "kvr_batch_error"]
+            "kvr_sample", "kvr_accept", "kvr_accept_work_bytes", "kvr_batch_error",
+            "kvr_adapt", "kvr_adapt_work_bytes"]
 
 
 class KvrError(RuntimeError):
@@ -75,6 +76,11 @@ class KvrPagesConfig(ctypes.Structure):
 
 class KvrSampling(ctypes.Structure):
     _fields_ = [(f, ctypes.c_void_p) for f in ("temperature", "top_k", "min_p", "top_p")]
+
+
+class KvrAdapterSite(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("n_adapters", ctypes.c_int), ("max_rank", ctypes.c_int),
+                ("k", ctypes.c_int), ("n_parts", ctypes.c_int), ("cols", ctypes.c_int * 3), ("type", ctypes.c_int)]
 
 
 class KvrPageTables(ctypes.Structure):
@@ -141,6 +147,8 @@ def load_library(path: str = LIB_PATH):
         "kvr_sample": (I, [V, I, LL, I, I, P(KvrSampling), V, V, V, V, LL, V]),
         "kvr_accept": (I, [V, I, LL, I, I, P(KvrSampling), I, V, V, V, LL, V, V, V, V, V, Z, V]),
         "kvr_accept_work_bytes": (Z, [I]),
+        "kvr_adapt": (I, [P(KvrAdapterSite), V, LL, V, V, I, I, V, LL, V, LL, I, V, Z, V]),
+        "kvr_adapt_work_bytes": (Z, [P(KvrAdapterSite), I]),
         "kvr_batch_error": (ctypes.c_char_p, []),
     }
     for name, (res, args) in sig.items():
