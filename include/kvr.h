@@ -39,7 +39,7 @@
  * loads it, the fixed staging array of kvr_slot_match_static.  All calls that take a
  * stream are asynchronous on it, except kvr_slot_match (it waits for the
  * stream to read back the match lengths), kvr_verify_accept (it returns the
- * decision to the host) and kvr_sync_status.
+ * decision to the host; kvr_verify_sample_batch too) and kvr_sync_status.
  *
  * Errors.  Every int-returning call returns KVR_OK (0) or a negative code;
  * kvr_last_error() says why.  A call refused by its checks launches nothing
@@ -778,6 +778,49 @@ size_t kvr_adapt_work_bytes(const kvr_adapter_site* site, int rows);
 int kvr_adapt(const kvr_adapter_site* site, const void* x, long long x_stride, const int32_t* cu_rows,
               const int32_t* which, int n_seq, int rows, const void* base, long long base_stride, void* out,
               long long out_stride, int out_type, void* work, size_t work_bytes, void* stream);
+
+/*
+ * The stack of a context for conversations with adapters of their own.  Every
+ * projection of a layer is a site; a site without a table is not adapted.
+ * A conversation's cached K and V are those of its adapter: kvr_slot_match knows
+ * nothing of adapters, so keep their slots (or contexts) apart.
+ */
+#define KVR_SITE_QKV 0      /* k = hidden, parts n_q_heads, n_kv_heads, n_kv_heads * head_dim */
+#define KVR_SITE_O 1        /* k = n_q_heads * head_dim, one part: hidden                     */
+#define KVR_SITE_GATE_UP 2  /* k = hidden, parts ffn, ffn                                     */
+#define KVR_SITE_DOWN 3     /* k = ffn, one part: hidden                                      */
+#define KVR_SITES 4
+typedef struct kvr_adapters {
+  const kvr_adapter_site* sites; /* host [n_layers][KVR_SITES], KVR_ACT_BF16                  */
+  void* work;                    /* device, 256-byte aligned, one call's at a time            */
+  size_t work_bytes;             /* kvr_adapters_work_bytes(cfg, sites, rows of the call)     */
+} kvr_adapters;
+size_t kvr_adapters_work_bytes(const kvr_config* cfg, const kvr_adapter_site* sites, int rows);
+
+/* kvr_prefill_batch with adapter which[j] (host [n_seq]; others than the sites'
+ * own: none) for conversation j.  What an adapter adds is formed from the
+ * projection's bf16 input in 32 bits and joins its output before that is rounded,
+ * rotated or multiplied.  Full layers only (KVR_ERR_UNSUPPORTED otherwise). */
+int kvr_prefill_batch_adapted(kvr_ctx* ctx, int n_seq, const int* slots, const int* lens, const int32_t* tokens,
+                              const void* hidden, const kvr_layer_weights* weights, const kvr_adapters* adapters,
+                              const int* which, void* out, void* stream);
+
+/* kvr_verify_accept_batch for conversations that sample: the rows run as one
+ * batch (with adapters, unless null), the output head forms every row's logits,
+ * and kvr_accept decides.  int4 or K-quant weights, at most 64 rows in all.
+ *   settings     host arrays of [n_seq], or null.  u, u_next: host [sum of lens], [n_seq].
+ *   draft_probs  device float [sum of lens][vocab] as in kvr_accept, or null.
+ *   logits       device float [sum of lens][head->vocab], 16-byte aligned: receives them.
+ *   next_tokens  host [n_seq]: the token after the drafts that stay (-1 without a distribution).
+ *   accepted     host [n_seq].  Slot slots[j] is cut back to its length before the call + 1 +
+ *                accepted[j].
+ * Synchronises the stream.  On an error after the rows ran every slot keeps its
+ * length before the call. */
+int kvr_verify_sample_batch(kvr_ctx* ctx, int n_seq, const int* slots, const int* lens, const int32_t* tokens,
+                            const void* hidden, const kvr_layer_weights* weights, const kvr_adapters* adapters,
+                            const int* which, const kvr_head_weights* head, const kvr_sampling* settings,
+                            const float* draft_probs, long long draft_stride, const float* u, const float* u_next,
+                            float* logits, void* out, int32_t* next_tokens, int* accepted, void* stream);
 
 const char* kvr_batch_error(void);
 

@@ -192,7 +192,8 @@ __global__ void __launch_bounds__(256, 4) epi_qkv_kernel(const float* part, long
                                                       int ldo, int c0, int mb, RowMap rows, int Hq,
                                                       int Hkv, const float2* rope, __nv_bfloat16* q,
                                                       __nv_bfloat16* arena, long long k_off,
-                                                      long long v_off, long long slot_stride, int cap) {
+                                                      long long v_off, long long slot_stride, int cap,
+                                                      const float* add) {
   dev::pdl_trigger();
   dev::pdl_wait();
   constexpr int kHalf = D / 2;
@@ -228,6 +229,14 @@ __global__ void __launch_bounds__(256, 4) epi_qkv_kernel(const float* part, long
       x1[4] += a1.x; x1[5] += a1.y; x1[6] += a1.z; x1[7] += a1.w;
       x2[0] += b0.x; x2[1] += b0.y; x2[2] += b0.z; x2[3] += b0.w;
       x2[4] += b1.x; x2[5] += b1.y; x2[6] += b1.z; x2[7] += b1.w;
+    }
+    if (add) {
+      const float* a = add + (long long)i * ldo + (long long)hd * D + j0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        x1[e] += a[e];
+        x2[e] += a[kHalf + e];
+      }
     }
   }
   if (hd < Hq + Hkv) {
@@ -365,14 +374,18 @@ __global__ void __launch_bounds__(kResidThreads, V <= 2 ? 2 : 1) epi_resid_kerne
 }
 
 __global__ void epi_swiglu_kernel(const float* part, long long plane, int ksplit, int ldo, int c0,
-                                  int mb, int F, __nv_bfloat16* z) {
+                                  int mb, int F, __nv_bfloat16* z, const float* add) {
   dev::pdl_trigger();
   dev::pdl_wait();
   const long long idx = (long long)blockIdx.x * blockDim.x + threadIdx.x;
   if (idx >= (long long)mb * F) return;
   const int t = (int)(idx / F), n = (int)(idx % F);
-  const float g = split_sum(part, plane, ksplit, (long long)t * ldo + n);
-  const float u = split_sum(part, plane, ksplit, (long long)t * ldo + F + n);
+  float g = split_sum(part, plane, ksplit, (long long)t * ldo + n);
+  float u = split_sum(part, plane, ksplit, (long long)t * ldo + F + n);
+  if (add) {
+    g += add[(long long)(c0 + t) * ldo + n];
+    u += add[(long long)(c0 + t) * ldo + F + n];
+  }
   const float sg = g / (1.f + expf(-g));
   z[(long long)(c0 + t) * F + n] = __float2bfloat16_rn(sg * u);
 }
@@ -459,16 +472,16 @@ cudaError_t launch_wait_probe(int* status, cudaStream_t st) {
 cudaError_t launch_epi_qkv(const float* part, long long plane, int ksplit, int ldo, int c0, int mb,
                            const RowMap& rows, int Hq, int Hkv, int d, const float2* rope,
                            __nv_bfloat16* q, __nv_bfloat16* arena, long long k_off,
-                           long long v_off, long long slot_stride, int cap, cudaStream_t st) {
+                           long long v_off, long long slot_stride, int cap, const float* add, cudaStream_t st) {
   const int heads = Hq + 2 * Hkv;
   if (d == 128) {
     const dim3 grid((mb + 15) / 16, heads);
     return launch_k(epi_qkv_kernel<128>, grid, 256, 0, st, part, plane, ksplit, ldo, c0, mb, rows, Hq,
-                    Hkv, rope, q, arena, k_off, v_off, slot_stride, cap);
+                    Hkv, rope, q, arena, k_off, v_off, slot_stride, cap, add);
   } else if (d == 64) {
     const dim3 grid((mb + 31) / 32, heads);
     return launch_k(epi_qkv_kernel<64>, grid, 256, 0, st, part, plane, ksplit, ldo, c0, mb, rows, Hq,
-                    Hkv, rope, q, arena, k_off, v_off, slot_stride, cap);
+                    Hkv, rope, q, arena, k_off, v_off, slot_stride, cap, add);
   }
   return cudaErrorInvalidValue;
 }
@@ -491,9 +504,9 @@ cudaError_t launch_epi_resid(const float* part, long long plane, int ksplit, int
 }
 
 cudaError_t launch_epi_swiglu(const float* part, long long plane, int ksplit, int ldo, int c0,
-                              int mb, int F, __nv_bfloat16* z, cudaStream_t st) {
+                              int mb, int F, __nv_bfloat16* z, const float* add, cudaStream_t st) {
   return launch_k(epi_swiglu_kernel, blocks_for((long long)mb * F, 256), 256, 0, st, part, plane,
-                  ksplit, ldo, c0, mb, F, z);
+                  ksplit, ldo, c0, mb, F, z, add);
 }
 
 cudaError_t launch_epi_cast(const float* part, long long plane, int ksplit, int ldo, int c0,

@@ -549,8 +549,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_int4_tc_kernel(const __grid_
 #pragma unroll
             for (int k = kp; k < 32; k += 2) {
               if (c0 + k < p.m) {
-                const float g = xch[r * 33 + k];
-                const float u = xch[(64 + r) * 33 + k];
+                float g = xch[r * 33 + k];
+                float u = xch[(64 + r) * 33 + k];
+                if (p.add) {   // the row's adapter
+                  const float* a = p.add + (long long)(p.t0 + c0 + k) * 2 * p.F + n;
+                  g += a[0];
+                  u += a[p.F];
+                }
                 const float sg = __fdividef(g, 1.f + __expf(-g));
                 dev::store_act(p.z + (long long)(p.t0 + c0 + k) * p.F + n, sg * u, p.z16 != 0);
               }

@@ -576,13 +576,29 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 1 : 2) gemv_int4_kernel(co
             v.x += w[j].x; v.y += w[j].y; v.z += w[j].z; v.w += w[j].w;
           }
       }
-      if (EPI == kGemvEpiResid) {   // epilogue in place: no trip through shared memory
+      if ((EPI == kGemvEpiQKV || kPair) && p.add) {   // the row's adapter
+        const int n = row0 + (kPair ? r4 & 63 : r4);
+        if (n < (kPair ? p.F : p.seg[s].N)) {
+          const int col = kPair ? (r4 >> 6) * p.F + n : p.seg[s].col0 + n;
+          const float4 a = __ldcg(reinterpret_cast<const float4*>(p.add + (long long)(p.c0 + tok) * p.ldadd + col));
+          v.x += a.x; v.y += a.y; v.z += a.z; v.w += a.w;
+        }
+      }
+      if (EPI == kGemvEpiLogits) {
+        // (rows of any width: single stores)
+        float* dst = p.h + (long long)(p.c0 + tok) * p.H + row0 + r4;
+        const int left = p.H - row0 - r4;
+        if (left > 0) dst[0] = v.x;
+        if (left > 1) dst[1] = v.y;
+        if (left > 2) dst[2] = v.z;
+        if (left > 3) dst[3] = v.w;
+      } else if (EPI == kGemvEpiResid) {   // epilogue in place: no trip through shared memory
         if (r4 < nv_h) resid_apply(p, row0, p.c0 + tok, r4, h_old, v);
       } else {
         *reinterpret_cast<float4*>(ct + tok * kTileLd + r4) = v;
       }
     }
-    if (EPI == kGemvEpiResid) continue;
+    if (EPI == kGemvEpiResid || EPI == kGemvEpiLogits) continue;
     consumers_sync();
     if (EPI == kGemvEpiQKV) epi_qkv(p, p.seg[s], s, row0, ct, kRopeS ? rope_s : p.rope + (long long)p.c0 * (p.d >> 1), tid);
     else if (EPI == kGemvEpiSwiglu) epi_swiglu(p, row0, ct, tid);
@@ -639,7 +655,7 @@ __global__ void __launch_bounds__(256) gemv_bf16_kernel(const __grid_constant__ 
 
 namespace {
 // resident CTAs per SM of each (NT, EPI, FMT) variant, from the occupancy API
-int g_per_sm[3][5][2];
+int g_per_sm[3][6][2];
 }  // namespace
 
 int gemv_int4_per_sm(int nt, int epi, int fmt) {
@@ -650,18 +666,19 @@ namespace {
 
 template <int NT>
 cudaError_t setup_nt() {
-  void (*ks[10])(GemvParams) = {
+  // (the output head is int4 in every configuration)
+  void (*ks[11])(GemvParams) = {
       gemv_int4_kernel<NT, 0, kFmtInt4>, gemv_int4_kernel<NT, 1, kFmtInt4>, gemv_int4_kernel<NT, 2, kFmtInt4>,
-      gemv_int4_kernel<NT, 3, kFmtInt4>, gemv_int4_kernel<NT, 4, kFmtInt4>, gemv_int4_kernel<NT, 0, kFmtQ4K>,
-      gemv_int4_kernel<NT, 1, kFmtQ4K>, gemv_int4_kernel<NT, 2, kFmtQ4K>, gemv_int4_kernel<NT, 3, kFmtQ4K>,
-      gemv_int4_kernel<NT, 4, kFmtQ4K>};
+      gemv_int4_kernel<NT, 3, kFmtInt4>, gemv_int4_kernel<NT, 4, kFmtInt4>, gemv_int4_kernel<NT, 5, kFmtInt4>,
+      gemv_int4_kernel<NT, 0, kFmtQ4K>, gemv_int4_kernel<NT, 1, kFmtQ4K>, gemv_int4_kernel<NT, 2, kFmtQ4K>,
+      gemv_int4_kernel<NT, 3, kFmtQ4K>, gemv_int4_kernel<NT, 4, kFmtQ4K>};
   const int ni = NT == 1 ? 0 : (NT == 2 ? 1 : 2);
-  for (int i = 0; i < 10; ++i) {
+  for (int i = 0; i < 11; ++i) {
     cudaError_t e = cudaFuncSetAttribute(ks[i], cudaFuncAttributeMaxDynamicSharedMemorySize, GemvCfg<NT>::kSmem);
     int n = 0;
     if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, ks[i], kThreads, GemvCfg<NT>::kSmem);
     if (e != cudaSuccess) return e;
-    g_per_sm[ni][i % 5][i / 5] = n;
+    g_per_sm[ni][i % 6][i / 6] = n;
   }
   return cudaSuccess;
 }
@@ -674,6 +691,9 @@ cudaError_t launch_fmt(const GemvParams& p, dim3 grid, cudaStream_t st) {
     case kGemvEpiSwiglu: return launch_k(gemv_int4_kernel<NT, 2, FMT>, grid, kThreads, GemvCfg<NT>::kSmem, st, p);
     case kGemvEpiCast: return launch_k(gemv_int4_kernel<NT, 3, FMT>, grid, kThreads, GemvCfg<NT>::kSmem, st, p);
     case kGemvEpiArgmax: return launch_k(gemv_int4_kernel<NT, 4, FMT>, grid, kThreads, GemvCfg<NT>::kSmem, st, p);
+    case kGemvEpiLogits:
+      if (FMT != kFmtInt4) break;
+      return launch_k(gemv_int4_kernel<NT, 5, kFmtInt4>, grid, kThreads, GemvCfg<NT>::kSmem, st, p);
   }
   return cudaErrorInvalidValue;
 }

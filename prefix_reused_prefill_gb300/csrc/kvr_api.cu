@@ -8,6 +8,7 @@
 // memory -- it carves the caller's arena and scratch buffers.
 #include <algorithm>
 #include <cstdarg>
+#include <cstddef>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
@@ -18,6 +19,7 @@
 
 #include <cudaTypedefs.h>
 
+#include "kvr_batch.cuh"
 #include "kvr_internal.cuh"
 #include "kvr_pages.cuh"
 
@@ -101,9 +103,22 @@ int attn_nsplit(int Hkv, int R, int kend_max, int target) {
   return std::max(1, std::min(ns, kMaxSplits));
 }
 
+// What the host says of a batch's requests, and what comes back (one copy each way).
+struct RequestsDev {
+  int32_t cu[KVR_MAX_BRANCHES + 1], which[KVR_MAX_BRANCHES];
+  int32_t tokens[kVerifyMaxRows];
+  float u[kVerifyMaxRows], u_next[KVR_MAX_BRANCHES];
+  float temperature[KVR_MAX_BRANCHES], min_p[KVR_MAX_BRANCHES], top_p[KVR_MAX_BRANCHES];
+  int32_t top_k[KVR_MAX_BRANCHES];
+  int32_t outcome[kVerifyMaxRows];
+  struct Result {
+    int32_t accepted[KVR_MAX_BRANCHES], next[KVR_MAX_BRANCHES];
+  } result;
+};
+
 struct ScratchLayout {
   size_t status, counters, prompt, slot_len, match_out, rope, h, a, q, o, z, part, opart, ml, best, next;
-  size_t pass_layers, pass_done, pass_ss, pass_diag, total;
+  size_t pass_layers, pass_done, pass_ss, pass_diag, requests, total;
   size_t part_floats, opart_floats, ml_count;
 };
 
@@ -153,6 +168,7 @@ ScratchLayout scratch_layout(const kvr_config* c) {
   L.pass_done = take(((size_t)c->n_layers * kPassPhases + 8) * 4);
   L.pass_ss = take((size_t)kPassRows * ((H + kGemvRows - 1) / kGemvRows) * 4);
   L.pass_diag = take((size_t)kPassMaxCtas * 2 * 4);
+  L.requests = take(sizeof(RequestsDev));
   L.total = off;
   return L;
 }
@@ -212,6 +228,7 @@ struct kvr_ctx {
   bool pass_uploaded = false;
   int* pass_done = nullptr;
   float* pass_ss = nullptr;
+  RequestsDev* requests = nullptr;
   int* pass_diag = nullptr;   // [kPassMaxCtas][2] where the pass's waits gave up
   unsigned pass_epoch = 0;
   bool use_pass = false;    // KVR_PASS=1 routes small m through the persistent pass
@@ -358,9 +375,10 @@ enum class Act { A, O, Z };
 // q and k feed the softmax, which can amplify a weight's fp16 rounding).
 template <class Epi>
 int project_gemm(kvr_ctx* c, cudaStream_t st, const Seg* segs, int nseg, const CUtensorMap* tmx,
-                 int K, int m, bool swiglu, bool exact, Epi epi) {
+                 int K, int m, bool swiglu, bool exact, const float* add, Epi epi) {
   GemmParams p;
   memset(&p, 0, sizeof p);
+  p.add = swiglu ? add : nullptr;   // (others' epilogues add it)
   p.K = K;
   p.kchunks = K / 128;
   p.status = c->status;
@@ -443,6 +461,9 @@ struct Fused {
   float2* best = nullptr;                 // Argmax
   int fmt = -1;                           // WeightFmt; -1: the layers' format
   int ldout = 0;                          // Cast: row stride of out (0: hidden)
+  const float* add = nullptr;             // QKV, SwiGLU: [m][ldadd] added to y
+  int ldadd = 0;
+  float* logits = nullptr;                // Logits: [m][vocab]
 };
 
 // Small-m int4 passes: the GEMV with its fused epilogue.  A residual
@@ -502,6 +523,12 @@ int project_gemv_int4(kvr_ctx* c, cudaStream_t st, const Seg* segs, int nseg, co
   p.d = cfg.head_dim;
   p.h = c->h;
   p.H = cfg.hidden;
+  if (fz.logits) {
+    p.h = fz.logits;
+    p.H = segs[0].N;
+  }
+  p.add = fz.add;
+  p.ldadd = fz.ldadd;
   p.out = fz.out;
   p.ldout = fz.ldout ? fz.ldout : cfg.hidden;
   p.z = c->z;
@@ -556,7 +583,7 @@ int project(kvr_ctx* c, cudaStream_t st, const Seg* segs, int nseg, Act act, int
   const kvr_config& cfg = c->cfg;
   const CUtensorMap* tmx = act == Act::A ? c->tm_a : (act == Act::O ? c->tm_o : c->tm_z);
   if (packed4(cfg) && gemv_path(c, m)) return project_gemv_int4(c, st, segs, nseg, tmx, K, m, fz);
-  if (packed4(cfg)) return project_gemm(c, st, segs, nseg, tmx, K, m, swiglu, exact, epi);
+  if (packed4(cfg)) return project_gemm(c, st, segs, nseg, tmx, K, m, swiglu, exact, fz.add, epi);
   // bf16 weights: plain GEMV into partials, then the row-wise epilogue kernel
   GemvParams p;
   memset(&p, 0, sizeof p);
@@ -948,14 +975,55 @@ int paged_layer(kvr_ctx* c, cudaStream_t st, const Paged& pg, const kvr_layer_we
   return rc ? fail(c, rc, "attend: %s", kvr_pages_error(pg.pages)) : KVR_OK;
 }
 
+// The requests of a batch with adapters of their own: each layer's sites, the
+// sequences' rows and adapters on the device, and memory for what they add.
+struct Adapted {
+  const kvr_adapter_site* sites;   // [n_layers][KVR_SITES]
+  const int32_t *cu, *which;
+  int n_seq;
+  float *add, *part;
+};
+
+// What the rows' adapters add at a site: to `into` [m][ld] (into += ..., the
+// residual stream), or, where that is null, to ad.add as rows of their own.
+// Returns the rows to be added by the projection's epilogue in *add (null: none).
+int adapt_site(kvr_ctx* c, cudaStream_t st, const Adapted& ad, int layer, int site, const __nv_bfloat16* x, int m,
+               float* into, const float** add, int* ld) {
+  const kvr_adapter_site& s = ad.sites[layer * KVR_SITES + site];
+  *add = nullptr;
+  *ld = 0;
+  for (int j = 0; j < s.n_parts; ++j) *ld += s.cols[j];
+  if (!s.table) return KVR_OK;
+  AdaptParams p;
+  memset(&p, 0, sizeof p);
+  p.site = s;
+  p.x = x;
+  p.x_stride = s.k;
+  p.x16 = c->act16 ? 1 : 0;
+  p.cu = ad.cu;
+  p.which = ad.which;
+  p.n_seq = ad.n_seq;
+  p.rows = m;
+  p.base = into;
+  p.out = into ? into : ad.add;
+  p.base_stride = p.out_stride = *ld;
+  p.out_type = KVR_ACT_F32;
+  p.part = ad.part;
+  Timed t(c, kEpi, st);
+  const cudaError_t e = launch_adapt(p, c->n_sms, st);
+  if (e != cudaSuccess) return cuda_fail(c, e, "adapt launch");
+  if (!into) *add = ad.add;
+  return KVR_OK;
+}
+
 // The layer stack for the rows of one call.
 // out (bf16 [m][hidden]) may be null; head_gain: RMSNorm the last layer's rows
 // with it into c->a (the output head's input); pg: K and V in pages (rows then
 // only counts them)
 int run_stack(kvr_ctx* c, const RowMap& rows, const void* hidden,
               const kvr_layer_weights* w, void* out, cudaStream_t st,
-              const __nv_bfloat16* head_gain = nullptr, const Paged* pg = nullptr) {
-  if (!pg && pass_fits(c, rows)) return run_pass(c, rows, hidden, w, out, st, head_gain);
+              const __nv_bfloat16* head_gain = nullptr, const Paged* pg = nullptr, const Adapted* ad = nullptr) {
+  if (!pg && !ad && pass_fits(c, rows)) return run_pass(c, rows, hidden, w, out, st, head_gain);
   const kvr_config& k = c->cfg;
   const int m = rows.m, H = k.hidden, d = k.head_dim;
   const int Hq = k.n_q_heads, Hkv = k.n_kv_heads, F = k.ffn;
@@ -993,10 +1061,14 @@ int run_stack(kvr_ctx* c, const RowMap& rows, const void* hidden,
       fz.rows = &rows;
       fz.k_off = koff;
       fz.v_off = voff;
+      if (ad) {
+        rc = adapt_site(c, st, *ad, l, KVR_SITE_QKV, c->a, m, nullptr, &fz.add, &fz.ldadd);
+        if (rc) return rc;
+      }
       rc = project(c, st, segs, 3, Act::A, H, m, [&](const float* part, long long plane, int ks,
                                                           int ldo, int c0, int mb) {
         return launch_epi_qkv(part, plane, ks, ldo, c0, mb, rows, Hq, Hkv, d, c->rope, c->q, arena,
-                              koff, voff, sstride, k.capacity, st);
+                              koff, voff, sstride, k.capacity, fz.add, st);
       }, fz, /*swiglu=*/false, /*exact=*/true);
       if (rc) return rc;
     }
@@ -1042,6 +1114,12 @@ int run_stack(kvr_ctx* c, const RowMap& rows, const void* hidden,
       Fused fz;
       fz.epi = kGemvEpiResid;
       fz.norm_gain = static_cast<const __nv_bfloat16*>(W.norm_ffn);
+      if (ad) {   // (into the residual stream, before the projection)
+        const float* none;
+        int ld;
+        rc = adapt_site(c, st, *ad, l, KVR_SITE_O, c->o, m, c->h, &none, &ld);
+        if (rc) return rc;
+      }
       rc = project(c, st, &so, 1, Act::O, Hq * d, m,
                    [&](const float* part, long long plane, int ks, int ldo, int c0, int mb) {
                      return launch_epi_resid(part, plane, ks, ldo, c0, mb, H, c->h,
@@ -1055,9 +1133,13 @@ int run_stack(kvr_ctx* c, const RowMap& rows, const void* hidden,
       Seg gu[2] = {{W.wg, W.sg, F}, {W.wu, W.su, F}};
       Fused fz;
       fz.epi = kGemvEpiSwiglu;
+      if (ad) {
+        rc = adapt_site(c, st, *ad, l, KVR_SITE_GATE_UP, c->a, m, nullptr, &fz.add, &fz.ldadd);
+        if (rc) return rc;
+      }
       rc = project(c, st, gu, 2, Act::A, H, m,
                    [&](const float* part, long long plane, int ks, int ldo, int c0, int mb) {
-                     return launch_epi_swiglu(part, plane, ks, ldo, c0, mb, F, c->z, st);
+                     return launch_epi_swiglu(part, plane, ks, ldo, c0, mb, F, c->z, fz.add, st);
                    },
                    fz, /*swiglu=*/true);
       if (rc) return rc;
@@ -1071,6 +1153,12 @@ int run_stack(kvr_ctx* c, const RowMap& rows, const void* hidden,
       fz.epi = kGemvEpiResid;
       fz.norm_gain = gain;
       fz.out = last ? static_cast<__nv_bfloat16*>(out) : nullptr;
+      if (ad) {
+        const float* none;
+        int ld;
+        rc = adapt_site(c, st, *ad, l, KVR_SITE_DOWN, c->z, m, c->h, &none, &ld);
+        if (rc) return rc;
+      }
       rc = project(c, st, &sd, 1, Act::Z, F, m,
                    [&](const float* part, long long plane, int ks, int ldo, int c0, int mb) {
                      // the output head's input stays bf16 (the head runs on the GEMV)
@@ -1168,6 +1256,16 @@ int head_check(kvr_ctx* c, const kvr_head_weights* head, const void* next_tokens
   for (const void* q : {head->norm, head->w, head->s})
     if (!q || (reinterpret_cast<uintptr_t>(q) & 15)) return fail(c, KVR_ERR_ARG, "missing or misaligned head pointer");
   return KVR_OK;
+}
+
+// logits = a * lm^T over the m normed rows in c->a, to fp32 rows
+int head_logits(kvr_ctx* c, cudaStream_t st, int m, const kvr_head_weights* head, float* logits) {
+  Seg seg = {head->w, head->s, head->vocab};
+  Fused fz;
+  fz.epi = kGemvEpiLogits;
+  fz.fmt = kFmtInt4;
+  fz.logits = logits;
+  return project_gemv_int4(c, st, &seg, 1, c->tm_a, c->cfg.hidden, m, fz);
 }
 
 // logits = a * lm^T over the m normed rows in c->a, each tile's best, each
@@ -1325,9 +1423,40 @@ cudaError_t copy_slot_kv(kvr_ctx* c, int slot, int len, uint8_t* host, bool to_h
   return cudaSuccess;
 }
 
+// floats that a batch's adapters add to a projection, at most
+size_t adapted_add_bytes(const kvr_config& k, int rows) {
+  return align_up((size_t)rows * std::max(qkv_cols(&k), 2 * k.ffn) * sizeof(float));
+}
+size_t adapted_part_bytes(const kvr_config& k, const kvr_adapter_site* sites, int rows) {
+  size_t most = 0;
+  for (int i = 0; i < k.n_layers * KVR_SITES; ++i)
+    if (sites[i].table) most = std::max(most, adapt_work_bytes(sites[i], rows));
+  return align_up(most);
+}
+// every layer's sites have the projections' widths; says which does not
+bool adapters_fit(const kvr_config& k, const kvr_adapter_site* sites, int* bad) {
+  const int qd = k.n_q_heads * k.head_dim, kd = k.n_kv_heads * k.head_dim;
+  const int in[KVR_SITES] = {k.hidden, qd, k.hidden, k.ffn};
+  const int parts[KVR_SITES] = {3, 1, 2, 1};
+  const int cols[KVR_SITES][3] = {{qd, kd, kd}, {k.hidden}, {k.ffn, k.ffn}, {k.hidden}};
+  for (int i = 0; i < k.n_layers * KVR_SITES; ++i) {
+    const kvr_adapter_site& s = sites[i];
+    if (!s.table) continue;
+    const int t = i % KVR_SITES;
+    bool ok = adapter_site_ok(&s) && s.type == KVR_ACT_BF16 && s.k == in[t] && s.n_parts == parts[t];
+    for (int j = 0; ok && j < parts[t]; ++j) ok = s.cols[j] == cols[t][j];
+    if (!ok) {
+      *bad = i;
+      return false;
+    }
+  }
+  return true;
+}
+
 int batch_common(kvr_ctx* c, int n_seq, const int* slots, const int* lens, const int32_t* tokens,
                  const void* hidden, const kvr_layer_weights* w, void* out, void* stream, int max_m,
-                 const __nv_bfloat16* head_gain) {
+                 const __nv_bfloat16* head_gain, const kvr_adapters* adapters = nullptr, const int* which = nullptr,
+                 RequestsDev* requests = nullptr) {
   if (!c) return KVR_ERR_ARG;
   if (n_seq < 1 || n_seq > KVR_MAX_BRANCHES || !slots || !lens || !tokens || !hidden || (!out && !head_gain))
     return fail(c, KVR_ERR_ARG, "bad batch arguments");
@@ -1356,9 +1485,38 @@ int batch_common(kvr_ctx* c, int n_seq, const int* slots, const int* lens, const
   rows.m = total;
   if (total > c->cfg.max_rows) return fail(c, KVR_ERR_CAPACITY, "%d rows exceed max_rows %d", total, c->cfg.max_rows);
   if (total > max_m) return fail(c, KVR_ERR_ARG, "%d rows exceed %d for this call", total, max_m);
+  Adapted ad;
+  if (adapters) {
+    if (c->cfg.attn_only) return fail(c, KVR_ERR_UNSUPPORTED, "adapters need the full decoder layer");
+    int bad = 0;
+    if (!adapters->sites || !which || !adapters->work || ((uintptr_t)adapters->work & 255))
+      return fail(c, KVR_ERR_ARG, "null sites, which or work, or a misaligned work area");
+    if (!adapters_fit(c->cfg, adapters->sites, &bad))
+      return fail(c, KVR_ERR_ARG, "layer %d, site %d does not fit the projection or is not bf16", bad / KVR_SITES,
+                  bad % KVR_SITES);
+    const size_t add = adapted_add_bytes(c->cfg, total);
+    if (adapters->work_bytes < add + adapted_part_bytes(c->cfg, adapters->sites, total))
+      return fail(c, KVR_ERR_CAPACITY, "the adapters' work area is smaller than %zu bytes",
+                  add + adapted_part_bytes(c->cfg, adapters->sites, total));
+    ad.sites = adapters->sites;
+    ad.cu = c->requests->cu;
+    ad.which = c->requests->which;
+    ad.n_seq = n_seq;
+    ad.add = static_cast<float*>(adapters->work);
+    ad.part = reinterpret_cast<float*>(static_cast<uint8_t*>(adapters->work) + add);
+  }
   if (c->fault == 2) return fail(c, KVR_ERR_FAULT, "injected launch fault");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  int rc = run_stack(c, rows, hidden, w, out, st, head_gain);
+  if (adapters || requests) {
+    RequestsDev host;
+    if (!requests) memset(requests = &host, 0, sizeof host);
+    for (int j = 0; j <= n_seq; ++j) requests->cu[j] = rows.off[j];
+    for (int j = 0; j < n_seq && which; ++j) requests->which[j] = which[j];
+    // (from pageable memory: copied before the call returns)
+    const cudaError_t e = cudaMemcpyAsync(c->requests, requests, offsetof(RequestsDev, outcome), cudaMemcpyHostToDevice, st);
+    if (e != cudaSuccess) return cuda_fail(c, e, "requests upload");
+  }
+  int rc = run_stack(c, rows, hidden, w, out, st, head_gain, nullptr, adapters ? &ad : nullptr);
   if (rc) return rc;
   for (int j = 0; j < n_seq; ++j) {
     rc = upload_tokens(c, slots[j], rows.pre[j], tokens + rows.off[j], lens[j], st);
@@ -1458,6 +1616,7 @@ int kvr_ctx_create(const kvr_config* cfg, void* kv_arena, size_t arena_bytes, vo
   c->pass_done = reinterpret_cast<int*>(s + c->sl.pass_done);
   c->pass_ss = reinterpret_cast<float*>(s + c->sl.pass_ss);
   c->pass_diag = reinterpret_cast<int*>(s + c->sl.pass_diag);
+  c->requests = reinterpret_cast<RequestsDev*>(s + c->sl.requests);
 
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1787,6 +1946,102 @@ int kvr_verify_accept_batch(kvr_ctx* c, int n_seq, const int* slots, const int* 
     accepted[j] = greedy_accept(tokens + at, next_tokens + at, lens[j]);
     c->slots[slots[j]].tokens.resize(p0[j] + 1 + accepted[j]);
     at += lens[j];
+  }
+  return KVR_OK;
+}
+
+size_t kvr_adapters_work_bytes(const kvr_config* cfg, const kvr_adapter_site* sites, int rows) {
+  int bad;
+  if (!valid_config(cfg, nullptr) || cfg->attn_only || !sites || rows < 1 || rows > cfg->max_rows ||
+      !adapters_fit(*cfg, sites, &bad))
+    return 0;
+  return adapted_add_bytes(*cfg, rows) + adapted_part_bytes(*cfg, sites, rows);
+}
+
+int kvr_prefill_batch_adapted(kvr_ctx* c, int n_seq, const int* slots, const int* lens, const int32_t* tokens,
+                              const void* hidden, const kvr_layer_weights* w, const kvr_adapters* adapters,
+                              const int* which, void* out, void* stream) {
+  if (!c) return KVR_ERR_ARG;
+  if (!adapters) return fail(c, KVR_ERR_ARG, "null adapters");
+  return batch_common(c, n_seq, slots, lens, tokens, hidden, w, out, stream, 1 << 30, nullptr, adapters, which);
+}
+
+int kvr_verify_sample_batch(kvr_ctx* c, int n_seq, const int* slots, const int* lens, const int32_t* tokens,
+                            const void* hidden, const kvr_layer_weights* w, const kvr_adapters* adapters,
+                            const int* which, const kvr_head_weights* head, const kvr_sampling* settings,
+                            const float* draft_probs, long long draft_stride, const float* u, const float* u_next,
+                            float* logits, void* out, int32_t* next_tokens, int* accepted, void* stream) {
+  if (!c) return KVR_ERR_ARG;
+  int rc = head_check(c, head, next_tokens, accepted);
+  if (rc) return rc;
+  if (n_seq < 1 || n_seq > KVR_MAX_BRANCHES || !slots || !lens || !tokens || !u || !u_next || !logits ||
+      ((uintptr_t)logits & 15) || ((uintptr_t)draft_probs & 3))
+    return fail(c, KVR_ERR_ARG, "bad batch arguments");
+  int p0[KVR_MAX_BRANCHES], total = 0;
+  for (int j = 0; j < n_seq; ++j) {
+    if (slots[j] < 0 || slots[j] >= c->granted) return fail(c, KVR_ERR_ARG, "bad slot %d", slots[j]);
+    if (lens[j] <= 0 || lens[j] > kVerifyMaxRows) return fail(c, KVR_ERR_ARG, "conversation %d has %d rows", j, lens[j]);
+    p0[j] = (int)c->slots[slots[j]].tokens.size();
+    total += lens[j];
+  }
+  if (total > kVerifyMaxRows) return fail(c, KVR_ERR_ARG, "%d rows exceed %d for this call", total, kVerifyMaxRows);
+  if (draft_probs && total > 1 && draft_stride < head->vocab)
+    return fail(c, KVR_ERR_ARG, "the drafts' row stride must cover a row");
+  RequestsDev req;
+  memset(&req, 0, sizeof req);
+  for (int i = 0; i < total; ++i) {
+    req.tokens[i] = tokens[i];
+    req.u[i] = u[i];
+  }
+  const kvr_sampling none = {};
+  const kvr_sampling& s = settings ? *settings : none;
+  for (int j = 0; j < n_seq; ++j) {
+    req.u_next[j] = u_next[j];
+    req.temperature[j] = s.temperature ? s.temperature[j] : 1.f;
+    req.top_k[j] = s.top_k ? s.top_k[j] : 0;
+    req.min_p[j] = s.min_p ? s.min_p[j] : 0.f;
+    req.top_p[j] = s.top_p ? s.top_p[j] : 1.f;
+  }
+  rc = batch_common(c, n_seq, slots, lens, tokens, hidden, w, out, stream, kVerifyMaxRows,
+                    static_cast<const __nv_bfloat16*>(head->norm), adapters, which, &req);
+  if (rc) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  rc = head_logits(c, st, total, head, logits);
+  RequestsDev* d = c->requests;
+  if (!rc) {
+    SampleParams p = {};
+    p.logits = logits;
+    p.stride = p.vocab = head->vocab;
+    p.rows = total;
+    p.type = KVR_ACT_F32;
+    p.s = {d->temperature, d->top_k, d->min_p, d->top_p};
+    p.u = d->u;
+    p.cu = d->cu;
+    p.n_seq = n_seq;
+    p.tokens = d->tokens;
+    p.q = draft_probs;
+    p.q_stride = draft_stride;
+    p.u_next = d->u_next;
+    p.outcome = d->outcome;
+    p.accepted = d->result.accepted;
+    p.next = d->result.next;
+    Timed t(c, kEpi, st);
+    const cudaError_t e = launch_sample(p, c->n_sms, st);
+    if (e != cudaSuccess) rc = cuda_fail(c, e, "sample launch");
+  }
+  if (!rc) {
+    const cudaError_t e = cudaMemcpyAsync(&req.result, &d->result, sizeof req.result, cudaMemcpyDeviceToHost, st);
+    if (e != cudaSuccess) rc = cuda_fail(c, e, "result readback");
+  }
+  if (!rc) rc = kvr_sync_status(c, stream);
+  if (rc) {
+    for (int j = 0; j < n_seq; ++j) c->slots[slots[j]].tokens.resize(p0[j]);
+    return rc;
+  }
+  for (int j = 0; j < n_seq; ++j) {
+    accepted[j] = req.result.accepted[j];
+    next_tokens[j] = req.result.next[j];
+    c->slots[slots[j]].tokens.resize(p0[j] + 1 + accepted[j]);
   }
   return KVR_OK;
 }

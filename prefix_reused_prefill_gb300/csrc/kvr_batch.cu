@@ -48,16 +48,6 @@ int logits_check(const void* logits, int type, long long stride, int rows, int v
 
 constexpr int kMaxAdaptRows = 1 << 22;
 
-bool site_ok(const kvr_adapter_site* s) {
-  if (!s || !s->table || !aligned(s->table, 8) || s->n_adapters < 1 || s->max_rank < 8 || s->max_rank > KVR_MAX_RANK ||
-      s->max_rank % 8 || s->k < 8 || s->k % 8 || s->k > 1 << 20 || s->n_parts < 1 || s->n_parts > 3 ||
-      (s->type != KVR_ACT_BF16 && s->type != KVR_ACT_F16))
-    return false;
-  for (int j = 0; j < s->n_parts; ++j)
-    if (s->cols[j] < 8 || s->cols[j] % 8 || s->cols[j] > 1 << 20) return false;
-  return true;
-}
-
 int run_sample(const SampleParams& p, void* stream) {
   int sms = 0;
   cudaError_t e = device_sms(&sms);
@@ -66,6 +56,16 @@ int run_sample(const SampleParams& p, void* stream) {
 }
 
 }  // namespace
+
+bool kvr::adapter_site_ok(const kvr_adapter_site* s) {
+  if (!s || !s->table || !aligned(s->table, 8) || s->n_adapters < 1 || s->max_rank < 8 || s->max_rank > KVR_MAX_RANK ||
+      s->max_rank % 8 || s->k < 8 || s->k % 8 || s->k > 1 << 20 || s->n_parts < 1 || s->n_parts > 3 ||
+      (s->type != KVR_ACT_BF16 && s->type != KVR_ACT_F16))
+    return false;
+  for (int j = 0; j < s->n_parts; ++j)
+    if (s->cols[j] < 8 || s->cols[j] % 8 || s->cols[j] > 1 << 20) return false;
+  return true;
+}
 
 extern "C" {
 
@@ -129,14 +129,14 @@ int kvr_accept(const void* logits, int type, long long stride, int rows, int voc
 }
 
 size_t kvr_adapt_work_bytes(const kvr_adapter_site* site, int rows) {
-  if (!site_ok(site) || rows < 0 || rows > kMaxAdaptRows) return 0;
+  if (!adapter_site_ok(site) || rows < 0 || rows > kMaxAdaptRows) return 0;
   return adapt_work_bytes(*site, std::max(rows, 1));
 }
 
 int kvr_adapt(const kvr_adapter_site* site, const void* x, long long x_stride, const int32_t* cu_rows,
               const int32_t* which, int n_seq, int rows, const void* base, long long base_stride, void* out,
               long long out_stride, int out_type, void* work, size_t work_bytes, void* stream) {
-  if (!site_ok(site))
+  if (!adapter_site_ok(site))
     return fail(KVR_ERR_ARG, "a site's table, adapters, ranks, widths or type are out of their range");
   if (rows < 0 || rows > kMaxAdaptRows) return fail(KVR_ERR_ARG, "%d rows outside [0, %d]", rows, kMaxAdaptRows);
   if (n_seq < 1 || n_seq > kAdaptMaxSeqs) return fail(KVR_ERR_ARG, "%d sequences outside [1, %d]", n_seq, kAdaptMaxSeqs);

@@ -52,6 +52,7 @@ struct AdaptParams {
   float* part;             // [ksplit][rows][n_parts * max_rank] parts of the low-rank products
   int ksplit;
 };
+bool adapter_site_ok(const kvr_adapter_site* s);
 size_t adapt_work_bytes(const kvr_adapter_site& s, int rows);
 cudaError_t launch_adapt(AdaptParams p, int sms, cudaStream_t st);
 

@@ -104,6 +104,7 @@ enum GemvEpi : int {
   kGemvEpiSwiglu = 2,  // tile = 64 gate rows + the same 64 up rows: z = bf16(silu(g) * u)
   kGemvEpiCast = 3,    // out = bf16(y)
   kGemvEpiArgmax = 4,  // per token, the tile's largest y and its row (lowest on ties) -> best
+  kGemvEpiLogits = 5,  // h = y (fp32 rows of their own width; the int4 output head)
 };
 
 // int4 weight formats of the GEMV and the tcgen05 GEMM (include/kvr.h):
@@ -138,8 +139,10 @@ struct GemvParams {
   long long k_off, v_off;   // QKV: the layer's K and V^T in slot 0
   long long slot_stride;    // QKV: arena elements per slot
   int cap, Hq, Hkv, d;
-  float* h;             // Resid: [max_rows][H]
+  float* h;             // Resid: [max_rows][H]; Logits: [m][H]
   int H;
+  const float* add;     // QKV, Swiglu: [m][ldadd] added to y (the rows' adapters), or null
+  int ldadd;
   __nv_bfloat16* out;   // Resid (last layer) / Cast: bf16 [m][ldout], or null
   int ldout;
   __nv_bfloat16* z;     // Swiglu: [max_rows][F]
@@ -174,6 +177,7 @@ struct GemmParams {
   int F;
   long long plane;
   float* part;      // [ksplit][256][ldo]
+  const float* add; // SwiGLU: [m][2 F] added to gate and up (the rows' adapters), or null
   __nv_bfloat16* z; // [max_rows][F]
   int z16;          // z holds fp16 (the next GEMM's operand type)
   int* status;
@@ -346,13 +350,13 @@ cudaError_t launch_epi_qkv(const float* part, long long plane, int ksplit, int l
                            int mb, const RowMap& rows, int Hq, int Hkv, int d,
                            const float2* rope, __nv_bfloat16* q, __nv_bfloat16* arena,
                            long long k_off, long long v_off, long long slot_stride, int cap,
-                           cudaStream_t st);
+                           const float* add, cudaStream_t st);   // add: [m][ldo] added to y, or null
 // a16: a_out holds fp16 (as launch_embed); final_out is always bf16
 cudaError_t launch_epi_resid(const float* part, long long plane, int ksplit, int ldo, int c0,
                              int mb, int H, float* h, const __nv_bfloat16* gain, float eps,
                              __nv_bfloat16* a_out, bool a16, __nv_bfloat16* final_out, cudaStream_t st);
 cudaError_t launch_epi_swiglu(const float* part, long long plane, int ksplit, int ldo, int c0,
-                              int mb, int F, __nv_bfloat16* z, cudaStream_t st);
+                              int mb, int F, __nv_bfloat16* z, const float* add, cudaStream_t st);
 // f16: out holds fp16 (a later layer's tcgen05 GEMM input)
 cudaError_t launch_epi_cast(const float* part, long long plane, int ksplit, int ldo, int c0,
                             int mb, int N, __nv_bfloat16* out, bool f16, cudaStream_t st);

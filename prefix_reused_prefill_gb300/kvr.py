@@ -36,7 +36,8 @@ EXPORTED = ["kvr_arena_bytes", "kvr_scratch_bytes", "kvr_ctx_create", "kvr_ctx_i
             "kvr_pages_tables", "kvr_pages_sync", "kvr_pages_error", "kvr_page_plan", "kvr_page_append",
             "kvr_page_read", "kvr_page_attend", "kvr_prefill_pages",
             "kvr_sample", "kvr_accept", "kvr_accept_work_bytes", "kvr_batch_error",
-            "kvr_adapt", "kvr_adapt_work_bytes"]
+            "kvr_adapt", "kvr_adapt_work_bytes", "kvr_adapters_work_bytes", "kvr_prefill_batch_adapted",
+            "kvr_verify_sample_batch"]
 
 
 class KvrError(RuntimeError):
@@ -54,6 +55,7 @@ class KvrConfig(ctypes.Structure):
                 ("rms_eps", ctypes.c_float), ("vocab", ctypes.c_int)]
 
 
+_SITES = ("qkv", "o", "gate_up", "down")
 _W_FIELDS = ["wq", "wk", "wv", "wo", "wg", "wu", "wd", "sq", "sk", "sv", "so", "sg", "su", "sd",
              "norm_attn", "norm_ffn"]
 
@@ -81,6 +83,10 @@ class KvrSampling(ctypes.Structure):
 class KvrAdapterSite(ctypes.Structure):
     _fields_ = [("table", ctypes.c_void_p), ("n_adapters", ctypes.c_int), ("max_rank", ctypes.c_int),
                 ("k", ctypes.c_int), ("n_parts", ctypes.c_int), ("cols", ctypes.c_int * 3), ("type", ctypes.c_int)]
+
+
+class KvrAdapters(ctypes.Structure):
+    _fields_ = [("sites", ctypes.POINTER(KvrAdapterSite)), ("work", ctypes.c_void_p), ("work_bytes", ctypes.c_size_t)]
 
 
 class KvrPageTables(ctypes.Structure):
@@ -149,6 +155,10 @@ def load_library(path: str = LIB_PATH):
         "kvr_accept_work_bytes": (Z, [I]),
         "kvr_adapt": (I, [P(KvrAdapterSite), V, LL, V, V, I, I, V, LL, V, LL, I, V, Z, V]),
         "kvr_adapt_work_bytes": (Z, [P(KvrAdapterSite), I]),
+        "kvr_adapters_work_bytes": (Z, [P(KvrConfig), P(KvrAdapterSite), I]),
+        "kvr_prefill_batch_adapted": (I, [V, I, P(I), P(I), i32p, V, P(KvrLayerWeights), P(KvrAdapters), P(I), V, V]),
+        "kvr_verify_sample_batch": (I, [V, I, P(I), P(I), i32p, V, P(KvrLayerWeights), P(KvrAdapters), P(I),
+                                        P(KvrHeadWeights), P(KvrSampling), V, LL, V, V, V, V, i32p, P(I), V]),
         "kvr_batch_error": (ctypes.c_char_p, []),
     }
     for name, (res, args) in sig.items():
@@ -395,6 +405,100 @@ class Kvr:
         self._check(self.lib.kvr_prefill_batch(self.ctx, n, slots_c, lens_c, _i32(sum(token_lists, [])),
                                                hidden.data_ptr(), arr, out.data_ptr(), self._stream(stream)))
         return out
+
+    def adapters(self, layers):
+        """Per layer a dict of Adapters ("qkv", "o", "gate_up", "down"; a missing one is not adapted) as
+        kvr_prefill_batch_adapted and kvr_verify_sample_batch take them; made once."""
+        if len(layers) != self.cfg.n_layers:
+            raise KvrError(-1, f"{len(layers)} layers of adapters, the stack has {self.cfg.n_layers}")
+        sites = (KvrAdapterSite * (4 * len(layers)))()
+        for l, sites_of in enumerate(layers):
+            for name, a in sites_of.items():
+                if name not in _SITES or a.device != self.arena.device:
+                    raise KvrError(-1, f"layer {l}: site {name}: one of {_SITES}, on {self.arena.device}")
+                sites[4 * l + _SITES.index(name)] = a.site
+        return sites, layers
+
+    def _adapted(self, adapters, which, n, rows, stream):
+        """(struct, which) of one call, with work memory of its own."""
+        if adapters is None:
+            return None, None, None
+        if len(which) != n:
+            raise KvrError(-1, f"which must name an adapter (or -1) for each of {n} conversations")
+        wb = self.lib.kvr_adapters_work_bytes(ctypes.byref(self.cfg), adapters[0], rows)
+        if wb == 0:
+            raise KvrError(-1, "the adapters do not fit the stack's projections")
+        with torch.cuda.stream(stream):   # (where one is given) memory that it may write at once
+            work = torch.empty(wb, dtype=torch.uint8, device=self.device)
+        return KvrAdapters(adapters[0], work.data_ptr(), wb), (ctypes.c_int * n)(*[int(w) for w in which]), work
+
+    def kvr_prefill_batch_adapted(self, slots, token_lists, hidden, weights, adapters, which, out=None, stream=None):
+        """kvr_prefill_batch with adapter which[j] (-1: none) of ``adapters`` (of Kvr.adapters) for conversation j."""
+        arr = weights[0] if isinstance(weights, tuple) else weights
+        lens = [len(t) for t in token_lists]
+        m, n = sum(lens), len(slots)
+        self._hidden(hidden, m)
+        if out is None:
+            with torch.cuda.stream(stream):
+                out = torch.empty((m, self.cfg.hidden), dtype=torch.bfloat16, device=self.device)
+        ad, which_c, _work = self._adapted(adapters, which, n, m, stream)
+        slots_c, lens_c = (ctypes.c_int * max(n, 1))(*[int(s) for s in slots]), (ctypes.c_int * max(n, 1))(*lens)
+        self._check(self.lib.kvr_prefill_batch_adapted(
+            self.ctx, n, slots_c, lens_c, _i32(sum(token_lists, [])), hidden.data_ptr(), arr,
+            None if ad is None else ctypes.byref(ad), which_c, out.data_ptr(), self._stream(stream)))
+        return out
+
+    def _hidden(self, hidden, m):
+        if hidden.dtype != torch.bfloat16 or not hidden.is_cuda or not hidden.is_contiguous() \
+                or hidden.shape != (m, self.cfg.hidden):
+            raise KvrError(-1, f"hidden must be a contiguous bf16 device tensor [{m}][{self.cfg.hidden}]")
+
+    def kvr_verify_sample_batch(self, slots, token_lists, hidden, weights, head, u, u_next, adapters=None, which=None,
+                                temperature=None, top_k=None, min_p=None, top_p=None, draft_probs=None, logits=None,
+                                out=None, stream=None):
+        """Speculative sampling of conversation j's rows token_lists[j] ([t0, d1 .. dk]) on slot slots[j], all in one
+        call: settings, u (one per row) and u_next (one per conversation) are host sequences.  draft_probs: float32
+        device [rows][vocab], the distribution of the draft after each row (None: the drafts were certain); logits:
+        float32 device [rows][vocab] to receive them.  Returns per conversation (the next token, the drafts kept)."""
+        arr = weights[0] if isinstance(weights, tuple) else weights
+        hs, _keep = head_weight_struct(head)
+        lens = [len(t) for t in token_lists]
+        m, n = sum(lens), len(slots)
+        self._hidden(hidden, m)
+        f32 = lambda name, v, k: self._host(name, v, k, ctypes.c_float)
+        st = KvrSampling()
+        keep = {name: self._host(name, v, n, ctypes.c_int32 if name == "top_k" else ctypes.c_float)
+                for name, v in (("temperature", temperature), ("top_k", top_k), ("min_p", min_p), ("top_p", top_p))
+                if v is not None}
+        for name, v in keep.items():
+            setattr(st, name, ctypes.addressof(v))
+        qp, qs = None, hs.vocab
+        if draft_probs is not None:
+            if draft_probs.dtype != torch.float32 or not draft_probs.is_cuda or draft_probs.shape != (m, hs.vocab) \
+                    or (draft_probs.stride(1) != 1 and hs.vocab > 1):
+                raise KvrError(-1, f"draft_probs must be a float32 device tensor [{m}][{hs.vocab}]")
+            qp, qs = draft_probs.data_ptr(), draft_probs.stride(0) if m > 1 else hs.vocab
+        if logits is None:
+            with torch.cuda.stream(stream):
+                logits = torch.empty((m, hs.vocab), dtype=torch.float32, device=self.device)
+        elif logits.dtype != torch.float32 or not logits.is_cuda or not logits.is_contiguous() \
+                or logits.shape != (m, hs.vocab):
+            raise KvrError(-1, f"logits must be a contiguous float32 device tensor [{m}][{hs.vocab}]")
+        ad, which_c, _work = self._adapted(adapters, which, n, m, stream)
+        slots_c, lens_c = (ctypes.c_int * max(n, 1))(*[int(s) for s in slots]), (ctypes.c_int * max(n, 1))(*lens)
+        nxt, acc = (ctypes.c_int32 * max(n, 1))(), (ctypes.c_int * max(n, 1))()
+        self._check(self.lib.kvr_verify_sample_batch(
+            self.ctx, n, slots_c, lens_c, _i32(sum(token_lists, [])), hidden.data_ptr(), arr,
+            None if ad is None else ctypes.byref(ad), which_c, ctypes.byref(hs), ctypes.byref(st), qp, qs,
+            f32("u", u, m), f32("u_next", u_next, n), logits.data_ptr(), _ptr(out), nxt, acc, self._stream(stream)))
+        return list(nxt[:n]), list(acc[:n])
+
+    @staticmethod
+    def _host(name, v, n, ctype):
+        v = v.tolist() if hasattr(v, "tolist") else list(v)
+        if len(v) != n:
+            raise KvrError(-1, f"{name} must have {n} entries")
+        return (ctype * max(n, 1))(*v)
 
     def kvr_selftest_wait(self, stream=None):
         self._check(self.lib.kvr_selftest_wait(self.ctx, self._stream(stream)))
