@@ -3,10 +3,14 @@
 // A row's tokens are never sorted.  Everything asked of their order is of one kind:
 // the shortest run from the largest logit that holds a count (top_k) or a weight
 // (top_p; the drawn token ends the run that holds more than u of the weight).  So
-// one pass files every token under its logit's distance from the maximum, in bins
+// one pass files the tokens under their logit's distance from the maximum, in bins
 // of 1/32 of a binary order that hold the count and the weight; running sums over
-// the bins name the bin in which a run ends, and only that bin's tokens are put in
-// order.
+// the bins name the bin in which a run ends, and only the tokens up to it, where
+// they are few, or that bin's are put in order.
+//
+// The bins hold 32 binary orders at a time: what is further from the maximum is summed
+// in registers, and filed in a later pass only if a run ends there.  Where top_k
+// bounds the kept tokens the first pass only counts.
 //
 // A token's place is one 50-bit number, its logit's bits above its inverted
 // index, so equal logits need no care.  Weights are formed to 2^-46 in pairs
@@ -14,6 +18,8 @@
 // one sum in any order, so shared-memory atomics serve and every pass, CTA and
 // launch agrees on where a run ends.
 #include <cooperative_groups.h>
+
+#include <utility>
 
 #include "kvr_batch.cuh"
 
@@ -27,13 +33,18 @@ using u64 = unsigned long long;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kBins = 1536;
-constexpr float kBinScale = 32.f;
-constexpr float kOrders = kBins / kBinScale;   // what is further from the maximum weighs nothing (last bin)
-constexpr int kCopies = 4;           // of the bins, by lane: equal logits are neighbours in a bin
+constexpr int kBins = 1024;          // held at a time, two a thread
 constexpr int kFix = 44;
+constexpr int kOrders = 48;          // binary orders from the maximum on which a token weighs nothing
+// Bins of a binary order: where weights are filed 32, so that 32 orders are held at a time and a bin
+// of the bulk of 262144 tokens is about as many as can be put in order; where tokens are only
+// counted 16, so that one pass holds all.
+constexpr float kFine = 32.f, kCoarse = 16.f;
+constexpr int kCopies = 2;           // of the bins, by lane: equal logits meet in one
 constexpr int kCap = 2048;           // tokens that one CTA puts in order
+constexpr int kCount = 512;          // as many by counting the larger ones
 constexpr int kDigit = 10;           // bits of a place taken at a time where a bin holds more
+static_assert(kBins == 2 * kThreads && kBins == 1 << kDigit && kCount <= kThreads, "bins and digits two a thread");
 constexpr int kPlaceBits = 32 + kSampleIndexBits;
 constexpr uint32_t kIndexMask = (1u << kSampleIndexBits) - 1;
 
@@ -67,25 +78,31 @@ struct Bins {
 struct Smem {
   float2 pow2[1024];
   Bins bins;
-  // of the cluster's first CTA: running weights and counts over the row's bins, over the parts of one bin,
-  // and the tokens of one bin
+  u64 mine[kCap];           // this CTA's tokens of a bin
+  int filled;               // how many
+  u64 front_w, rest_w;      // this CTA's tokens in front of the bins and behind them
+  uint32_t front_c, rest_c;
+  double min_orders;        // temperature * ln(min_p)
+  // what the cluster's CTAs tell one another
+  uint32_t best_key[kMaxCluster], best_i[kMaxCluster];
+  u64 warp_w[kWarps];
+  uint32_t warp_c[kWarps], warp_i[kWarps];
+  // of the cluster's first CTA: running weights and counts over the bins and over the parts of one bin,
+  // those of the row, and the tokens to be put in order
   u64 sum_w[kBins], part_w[kBins];
   uint32_t sum_c[kBins], part_c[kBins];
+  u64 before_w, total_w;
+  uint32_t before_c, total_c;
   u64 place[kCap], weight[kCap];
-  u64 warp_w[kWarps];
-  uint32_t warp_c[kWarps];
-  // what the CTAs tell one another
-  float max_[kMaxCluster];
-  int bad_[kMaxCluster];
-  int n, bin;             // tokens of the bin in which a run ends
-  u64 base_w;             // weight and count before it
+  int bin, n;               // the bin in which a run ends and its tokens; kLower, kHigher: not in these
+  u64 base_w;               // weight and count in front of it
   uint32_t base_c;
-  u64 from;               // first place of a part of it
-  u64 run_place, run_w;   // the end of a run, its weight and that of its last token
-  u64 last_w;
-  int fill;
-  int stays;
+  u64 from;                 // first place of a part of it
+  u64 run_place, run_w;     // the end of a run, its weight
+  u64 kept, kept_w;         // the row's distribution
+  int found, stays;
 };
+constexpr int kLower = -1, kHigher = -2;
 
 // What a row's tokens weigh.
 struct Row {
@@ -96,6 +113,8 @@ struct Row {
   const float* q;       // null: all weight of `draft` goes
   double total;
   int draft;
+  bool draft_in;        // within the vocabulary; its logit
+  float draft_x;
   u64 kept;             // places from here on
   bool rest;
 
@@ -110,7 +129,7 @@ struct Row {
     const float dl = (max - (d - b)) - (x + b);
     yh = d * ch;
     yl = fmaf(d, ch, -yh) + fmaf(d, cl, dl * ch);
-    return yh < kOrders;
+    return yh < (float)kOrders;
   }
 };
 
@@ -120,16 +139,22 @@ __device__ __forceinline__ u64 place_of(float x, int i) {
   return ((u64)k << kSampleIndexBits) | (kIndexMask - (uint32_t)i);
 }
 
-// 2^-(yh + yl) = (s + r) 2^-n: the nearest of 1024 steps from the table, the
-// rest by its series, whose first term is a pair of floats.
+__device__ __forceinline__ float logit_of(u64 place) {
+  const uint32_t k = (uint32_t)(place >> kSampleIndexBits);
+  return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
+}
+__device__ __forceinline__ int token_of(u64 place) { return (int)(kIndexMask - (uint32_t)(place & kIndexMask)); }
+
+// 2^-(yh + yl) = (s + r) 2^-n: the step of 1024 below from the table, the rest
+// by its series, whose first term is a pair of floats.
 __device__ __forceinline__ void pow2_neg(const float2* tab, float yh, float yl, float& s, float& r, int& n) {
   constexpr float kLn2h = 0.693147182464599609375f;
   constexpr float kLn2l = -1.904654323148236e-09f;
-  const int j = __float2int_rn(yh * 1024.f);
+  const int j = __float2int_rd(yh * 1024.f);
   const float f = fmaf((float)j, -1.f / 1024.f, yh);
   const float zh = -f * kLn2h;
   const float zl = fmaf(-f, kLn2h, -zh) - fmaf(f, kLn2l, yl * kLn2h);
-  const float e = fmaf(zh * zh, fmaf(zh, 1.f / 6.f, 0.5f), zl);
+  const float e = fmaf(zh * zh, fmaf(zh, fmaf(zh, 1.f / 24.f, 1.f / 6.f), 0.5f), zl);
   const float2 t = tab[j & 1023];
   n = j >> 10;
   const float a = t.x * zh;
@@ -139,30 +164,59 @@ __device__ __forceinline__ void pow2_neg(const float2* tab, float yh, float yl, 
   r = (a - (s - t.x)) + al;
 }
 
+// in units of 2^-44, for yh below kOrders
 __device__ __forceinline__ u64 weight_fixed(const float2* tab, float yh, float yl) {
   float s, r;
   int n;
   pow2_neg(tab, yh, yl, s, r, n);
-  const float scale = __int_as_float((kFix - n + 127) << 23);
-  return (u64)(__float2ll_rn(s * scale) + (long long)__float2int_rn(r * scale));
+  const u64 v = ((u64)__float2uint_rn(s * 0x1p31f) << (kFix - 31)) + (long long)__float2int_rn(r * 0x1p44f);
+  return (v + ((1ull << n) >> 1)) >> n;
 }
 
-__device__ __forceinline__ int bin_of(float yh) { return min((int)(yh * kBinScale), kBins - 1); }
+// total as a pair of floats
+__device__ __forceinline__ float2 pair_of(u64 total) {
+  const float h = __ull2float_rn(total);
+  return make_float2(h * 0x1p-44f, __ll2float_rn((long long)(total - __float2ull_rn(h))) * 0x1p-44f);
+}
+// (s + r) 2^-n / total, rounded to a float but for 2^-46 of it
+__device__ __forceinline__ float share_of(float s, float r, int n, float2 total) {
+  const float q = s / total.x;
+  const float v = q + (fmaf(-q, total.x, s) + fmaf(-q, total.y, r)) / total.x;
+  // (in two steps, of which only the second may leave the normal numbers)
+  const int m = min(n, 100);
+  return v * __int_as_float((127 - m) << 23) * __int_as_float((127 - (n - m)) << 23);
+}
 
-// f(logit, token) over the CTA's part [lo, hi) of a row: 16-byte loads but at the ends.
-template <class T, class F>
+// f(logits, token of the first) over the CTA's part [lo, hi) of a row, four at a
+// time (16-byte loads, U in flight) but at the ends.
+template <int U, class T, class F>
 __device__ __forceinline__ void for_tokens(const T* row, int lo, int hi, F f) {
   constexpr int kV = 16 / sizeof(T);
   const int skip = (int)((16 - ((uintptr_t)(row + lo) & 15)) & 15) / (int)sizeof(T);
   const int a = min(lo + skip, hi), b = a + (hi - a) / kV * kV;
-  for (int i = lo + threadIdx.x; i < a; i += kThreads) f(to_float(row[i]), i);
-  for (int i = a + threadIdx.x * kV; i < b; i += kThreads * kV) {
-    const uint4 v = *reinterpret_cast<const uint4*>(row + i);
+  auto one = [&](int i) {
+    const float x[1] = {to_float(row[i])};
+    f(x, i);
+  };
+  for (int i = lo + threadIdx.x; i < a; i += kThreads) one(i);
+  auto some = [&](const uint4& v, int i) {
     const T* e = reinterpret_cast<const T*>(&v);
 #pragma unroll
-    for (int k = 0; k < kV; ++k) f(to_float(e[k]), i + k);
+    for (int k = 0; k < kV; k += 4) {
+      const float x[4] = {to_float(e[k]), to_float(e[k + 1]), to_float(e[k + 2]), to_float(e[k + 3])};
+      f(x, i + k);
+    }
+  };
+  int i = a + threadIdx.x * kV;
+  for (; i + (U - 1) * kThreads * kV < b; i += U * kThreads * kV) {
+    uint4 v[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) v[k] = *reinterpret_cast<const uint4*>(row + i + k * kThreads * kV);
+#pragma unroll
+    for (int k = 0; k < U; ++k) some(v[k], i + k * kThreads * kV);
   }
-  for (int i = b + threadIdx.x; i < hi; i += kThreads) f(to_float(row[i]), i);
+  for (; i < b; i += kThreads * kV) some(*reinterpret_cast<const uint4*>(row + i), i);
+  for (int j = b + threadIdx.x; j < hi; j += kThreads) one(j);
 }
 
 // ceil(total * p) and floor(total * u) + 1 for p, u in [0, 1), exactly
@@ -183,6 +237,61 @@ __device__ __forceinline__ u64 share(u64 total, float p, bool up) {
   return whole + (up ? left != 0 : 1);
 }
 
+// Sums and searches over n ordered weights, four a thread: by one warp, or by the CTA.
+constexpr int kPer = kCap / kThreads;
+template <int THREADS>
+struct Scan {
+  Smem& sm;
+  int at, n;
+  u64 v[kPer], before;
+  __device__ __forceinline__ int entry(int k) const { return (threadIdx.x % THREADS) * kPer + k; }
+  __device__ __forceinline__ static void sync() {
+    if (THREADS == 32) __syncwarp();
+    else __syncthreads();
+  }
+  __device__ __forceinline__ void sum() {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) v[k] = (entry(k) < n ? sm.weight[at + entry(k)] : 0) + (k ? v[k - 1] : 0);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    u64 r = v[kPer - 1];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const u64 a = __shfl_up_sync(0xffffffffu, r, o);
+      if (lane >= o) r += a;
+    }
+    before = r - v[kPer - 1];
+    if (THREADS == 32) return;
+    __syncthreads();
+    if (lane == 31) sm.warp_w[warp] = r;
+    __syncthreads();
+    for (int k = 0; k < warp; ++k) before += sm.warp_w[k];
+  }
+  __device__ __forceinline__ u64 total() {
+    if (THREADS == 32) return __shfl_sync(0xffffffffu, before + v[kPer - 1], 31);
+    if (threadIdx.x == kThreads - 1) sm.run_w = before + v[kPer - 1];
+    __syncthreads();
+    const u64 t = sm.run_w;
+    __syncthreads();
+    return t;
+  }
+  // the entry at which the weight reaches `mass`, and the weight there
+  __device__ __forceinline__ int reach(u64 mass, u64& weight) {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const u64 iw = before + v[k], pw = before + (k ? v[k - 1] : 0);
+      if (entry(k) < n && iw >= mass && pw < mass) {
+        sm.found = entry(k);
+        sm.run_w = iw;
+      }
+    }
+    sync();
+    const int i = sm.found;
+    weight = sm.run_w;
+    sync();
+    return i;
+  }
+};
+
 template <class T>
 struct Sampler {
   Smem& sm;
@@ -190,112 +299,221 @@ struct Sampler {
   const cg::cluster_group& cluster;
   const T* row;
   int lo, hi;           // this CTA's tokens
-  int rank;
+  int rank, ctas;
   Row w;
+  float scale;          // bins of a binary order
+  int bin0;             // the first one held
 
-  __device__ __forceinline__ void clear_bins() {
-    uint32_t* b = reinterpret_cast<uint32_t*>(&sm.bins);
-    for (int i = threadIdx.x; i < (int)(sizeof(Bins) / 4); i += kThreads) b[i] = 0;
+  // (bins are told apart by the logit's distance alone, so equal logits share one)
+  __device__ __forceinline__ int bin_of(float yh) const { return yh < 64.f ? (int)(yh * scale) : (int)(64 * scale) - 1; }
+
+  // A token's weight: what a draft left of it, where the row is such a one.
+  __device__ __forceinline__ u64 weigh(int i, float yh, float yl) const {
+    if (!(yh < (float)kOrders)) return 0;
+    return left(weight_fixed(sm.pow2, yh, yl), i);
+  }
+  __device__ __forceinline__ u64 left(u64 v, int i) const {
+    if (!w.rest) return v;
+    if (!w.q) return i == w.draft ? 0 : v;
+    const double d = (double)v - (double)w.q[i] * w.total;
+    return d > 0. ? (u64)__double2ll_rn(d) : 0;
+  }
+  // whether a token is one of the row's
+  __device__ __forceinline__ bool in_row(float x, int i) const {
+    return x >= w.floor && (!w.rest || place_of(x, i) >= w.kept);
+  }
+  __device__ __forceinline__ void sync() {
+    if (ctas > 1) cluster.sync();
+    else __syncthreads();
+  }
+
+  __device__ __forceinline__ void clear_bins(bool mass) {
+    uint4* b = reinterpret_cast<uint4*>(&sm.bins);
+    const int n = (int)((mass ? sizeof(Bins) : sizeof(sm.bins.cnt)) / 16);
+    for (int i = threadIdx.x; i < n; i += kThreads) b[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (threadIdx.x == 0) {
+      sm.front_w = sm.rest_w = 0;
+      sm.front_c = sm.rest_c = 0;
+    }
     __syncthreads();
   }
   __device__ __forceinline__ void add(int bin, u64 v) {
     const int c = threadIdx.x % kCopies;
     atomicAdd(&sm.bins.cnt[c][bin], 1u);
     const uint32_t l = (uint32_t)v, h = (uint32_t)(v >> 32);
-    if (l) {
-      const uint32_t old = atomicAdd(&sm.bins.lo[c][bin], l);
-      const uint32_t carry = old + l < old ? 1u : 0u;
-      if (h + carry) atomicAdd(&sm.bins.hi[c][bin], h + carry);
-    } else if (h) {
-      atomicAdd(&sm.bins.hi[c][bin], h);
-    }
+    const uint32_t old = atomicAdd(&sm.bins.lo[c][bin], l);
+    const uint32_t up = h + (old + l < old ? 1u : 0u);
+    if (up) atomicAdd(&sm.bins.hi[c][bin], up);
   }
 
-  // Running sums over the cluster's bins, to the first CTA's sum_w and sum_c.
-  __device__ __forceinline__ void sum_bins(u64* sum_w, uint32_t* sum_c) {
+  // Running sums over the cluster's bins, after what is in front of them, to the
+  // first CTA's sum_w and sum_c.  The others return once it may read theirs.
+  template <bool MASS>
+  __device__ __forceinline__ void sum_bins(u64* sum_w, uint32_t* sum_c, const u64* front_w, const uint32_t* front_c) {
     __syncthreads();
-    for (int b = threadIdx.x; b < kBins; b += kThreads) {
-      uint32_t c = 0, l = 0, h = 0;
-#pragma unroll
-      for (int k = 0; k < kCopies; ++k) {
-        c += sm.bins.cnt[k][b];
-        const uint32_t o = l;
-        l += sm.bins.lo[k][b];
-        h += sm.bins.hi[k][b] + (l < o ? 1u : 0u);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = 2 * threadIdx.x;
+    u64 v[2] = {0, 0};
+    uint32_t c[2] = {0, 0};
+    auto take = [&](const Bins& o, int copy) {
+      const uint2 n = *reinterpret_cast<const uint2*>(&o.cnt[copy][b]);
+      c[0] += n.x;
+      c[1] += n.y;
+      if (MASS) {
+        const uint2 l = *reinterpret_cast<const uint2*>(&o.lo[copy][b]);
+        const uint2 h = *reinterpret_cast<const uint2*>(&o.hi[copy][b]);
+        v[0] += (u64)h.x << 32 | l.x;
+        v[1] += (u64)h.y << 32 | l.y;
       }
-      sm.bins.cnt[0][b] = c;
-      sm.bins.lo[0][b] = l;
-      sm.bins.hi[0][b] = h;
-    }
-    cluster.sync();
-    if (rank == 0) {
-      constexpr int kPer = kBins / kThreads;
-      u64 v[kPer];
-      uint32_t c[kPer];
+    };
 #pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        const int b = threadIdx.x * kPer + k;
-        v[k] = 0;
-        c[k] = 0;
-        for (int j = 0; j < (int)cluster.num_blocks(); ++j) {
-          const Bins& o = cluster.map_shared_rank(&sm, j)->bins;
-          v[k] += (u64)o.hi[0][b] << 32 | o.lo[0][b];
-          c[k] += o.cnt[0][b];
-        }
-        if (k) {
-          v[k] += v[k - 1];
-          c[k] += c[k - 1];
+    for (int k = 0; k < kCopies; ++k) take(sm.bins, k);
+    if (ctas > 1) {
+      if (rank) {
+        *reinterpret_cast<uint2*>(&sm.bins.cnt[0][b]) = make_uint2(c[0], c[1]);
+        if (MASS) {
+          *reinterpret_cast<uint2*>(&sm.bins.lo[0][b]) = make_uint2((uint32_t)v[0], (uint32_t)v[1]);
+          *reinterpret_cast<uint2*>(&sm.bins.hi[0][b]) = make_uint2((uint32_t)(v[0] >> 32), (uint32_t)(v[1] >> 32));
         }
       }
-      u64 bv;
-      uint32_t bc;
-      block_before(v[kPer - 1], c[kPer - 1], bv, bc);
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        sum_w[threadIdx.x * kPer + k] = bv + v[k];
-        sum_c[threadIdx.x * kPer + k] = bc + c[k];
-      }
-      __syncthreads();
+      cluster.sync();
+      if (rank) return;
+#pragma unroll 4
+      for (int j = 1; j < ctas; ++j) take(cluster.map_shared_rank(&sm, j)->bins, 0);
     }
-  }
-
-  // sums of the threads in front
-  __device__ __forceinline__ void block_before(u64 v, uint32_t c, u64& bv, uint32_t& bc) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    u64 rv = v;
-    uint32_t rc = c;
+    if (front_w == &sm.before_w && threadIdx.x == 0) {
+      u64 fw = 0, rw = 0;
+      uint32_t fc = 0, rc = 0;
+      for (int j = 0; j < ctas; ++j) {
+        const Smem* o = cluster.map_shared_rank(&sm, j);
+        fw += o->front_w;
+        rw += o->rest_w;
+        fc += o->front_c;
+        rc += o->rest_c;
+      }
+      sm.before_w = fw;
+      sm.before_c = fc;
+      sm.total_w = rw;
+      sm.total_c = rc;
+    }
+    v[1] += v[0];
+    c[1] += c[0];
+    u64 rv = v[1];
+    uint32_t rc = c[1];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const u64 a = __shfl_up_sync(0xffffffffu, rv, o);
-      const uint32_t b = __shfl_up_sync(0xffffffffu, rc, o);
-      if (lane >= o) {
-        rv += a;
-        rc += b;
+      const uint32_t y = __shfl_up_sync(0xffffffffu, rc, o);
+      if (lane >= o) rc += y;
+      if (MASS) {
+        const u64 x = __shfl_up_sync(0xffffffffu, rv, o);
+        if (lane >= o) rv += x;
       }
     }
-    __syncthreads();
     if (lane == 31) {
-      sm.warp_w[warp] = rv;
       sm.warp_c[warp] = rc;
+      sm.warp_w[warp] = rv;
     }
     __syncthreads();
-    bv = rv - v;
-    bc = rc - c;
+    u64 bv = *front_w + rv - v[1];
+    uint32_t bc = *front_c + rc - c[1];
     for (int k = 0; k < warp; ++k) {
-      bv += sm.warp_w[k];
       bc += sm.warp_c[k];
+      if (MASS) bv += sm.warp_w[k];
     }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      sum_w[b + k] = bv + v[k];
+      sum_c[b + k] = bc + c[k];
+    }
+    if (front_w == &sm.before_w && threadIdx.x == kThreads - 1) {
+      sm.total_w += bv + v[1];
+      sm.total_c += bc + c[1];
+    }
+    __syncthreads();
   }
 
-  // The bin in which the run that holds `count` tokens or (count 0) `mass` ends, by
-  // the bins' running sums and what stands in front of them.  First CTA only.
-  __device__ __forceinline__ void find_bin(const u64* sum_w, const uint32_t* sum_c, uint32_t count, u64 mass,
-                                           u64 before_w, uint32_t before_c) {
-    for (int b = threadIdx.x; b < kBins; b += kThreads) {
-      const u64 iw = before_w + sum_w[b], pw = before_w + (b ? sum_w[b - 1] : 0);
-      const uint32_t ic = before_c + sum_c[b], pc = before_c + (b ? sum_c[b - 1] : 0);
+  // The row's tokens into the bins from `to` on, with their weights or only counted,
+  // and the running sums (the first CTA's, until the next sync).
+  template <bool MASS>
+  __device__ __forceinline__ void file(int to) {
+    bin0 = to;
+    scale = MASS ? kFine : kCoarse;
+    clear_bins(MASS);
+    u64 front_w = 0, rest_w = 0;
+    uint32_t front_c = 0, rest_c = 0;
+    for_tokens<2>(row, lo, hi, [&](const auto& x, int i) {
+      constexpr int N = sizeof(x) / sizeof(float);
+      float yh[N], yl[N];
+      bool in[N], near = false;
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        w.orders(x[k], yh[k], yl[k]);
+        in[k] = in_row(x[k], i + k);
+        near |= in[k] && yh[k] < (float)kOrders;
+      }
+      if (!MASS) {
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+          if (in[k]) atomicAdd(&sm.bins.cnt[threadIdx.x % kCopies][bin_of(yh[k])], 1u);
+      } else if (!near) {
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+          if (in[k]) {
+            const int b = bin_of(yh[k]) - bin0;
+            if (b < kBins) atomicAdd(&sm.bins.cnt[threadIdx.x % kCopies][b], 1u);   // (b >= 0: the last orders)
+            else ++rest_c;
+          }
+      } else {
+        u64 v[N];
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] = yh[k] < (float)kOrders ? weight_fixed(sm.pow2, yh[k], yl[k]) : 0;
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+          if (in[k]) {
+            const u64 m = left(v[k], i + k);
+            const int b = bin_of(yh[k]) - bin0;
+            if ((unsigned)b < kBins) {
+              add(b, m);
+            } else if (b < 0) {
+              ++front_c;
+              front_w += m;
+            } else {
+              ++rest_c;
+              rest_w += m;
+            }
+          }
+      }
+    });
+    if (MASS) {
+      front_c = __reduce_add_sync(0xffffffffu, front_c);
+      rest_c = __reduce_add_sync(0xffffffffu, rest_c);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        if (bin0) front_w += __shfl_xor_sync(0xffffffffu, front_w, o);
+        rest_w += __shfl_xor_sync(0xffffffffu, rest_w, o);
+      }
+      if ((threadIdx.x & 31) == 0) {
+        if (front_c) atomicAdd(&sm.front_c, front_c);
+        if (rest_c) atomicAdd(&sm.rest_c, rest_c);
+        if (front_w) atomicAdd(&sm.front_w, front_w);
+        if (rest_w) atomicAdd(&sm.rest_w, rest_w);
+      }
+    }
+    sum_bins<MASS>(sm.sum_w, sm.sum_c, &sm.before_w, &sm.before_c);
+  }
+
+  // The bin (of those held, or of one bin's parts) in which the run that holds
+  // `count` tokens or (count 0) `mass` ends.  First CTA only.
+  __device__ __forceinline__ void find_bin(const u64* sum_w, const uint32_t* sum_c, u64 before_w, uint32_t before_c,
+                                           uint32_t count, u64 mass, int offset) {
+    if (threadIdx.x == 0) sm.bin = (count ? count <= before_c : mass <= before_w) ? kLower : kHigher;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int b = 2 * threadIdx.x + k;
+      const u64 iw = sum_w[b], pw = b ? sum_w[b - 1] : before_w;
+      const uint32_t ic = sum_c[b], pc = b ? sum_c[b - 1] : before_c;
       if (count ? ic >= count && pc < count : iw >= mass && pw < mass) {
-        sm.bin = b;
+        sm.bin = offset + b;
         sm.n = (int)(ic - pc);
         sm.base_w = pw;
         sm.base_c = pc;
@@ -304,158 +522,235 @@ struct Sampler {
     __syncthreads();
   }
 
-  // n tokens (place, weight) of the first CTA's list, in descending order of their places
-  __device__ __forceinline__ void order(int n) {
-    int size = 2;
-    while (size < n) size <<= 1;
-    for (int i = n + threadIdx.x; i < size; i += kThreads) {
-      sm.place[i] = 0;
-      sm.weight[i] = 0;
+  // The tokens of bins b0 .. b1 (in [from, from + 2^shift) of their places), n in
+  // all, in order in the first CTA's list, from the entry that it returns on.
+  __device__ __forceinline__ int gather(int b0, int b1, u64 from, int shift, int n) {
+    if (threadIdx.x == 0) sm.filled = 0;
+    __syncthreads();
+    for_tokens<4>(row, lo, hi, [&](const auto& x, int i) {
+#pragma unroll
+      for (int k = 0; k < (int)(sizeof(x) / sizeof(float)); ++k) {
+        float yh, yl;
+        w.orders(x[k], yh, yl);
+        const int b = bin_of(yh);
+        if (b < b0 || b > b1 || !in_row(x[k], i + k)) continue;
+        const u64 p = place_of(x[k], i + k);
+        if (p < from || (p - from) >> shift) continue;
+        const int at = atomicAdd(&sm.filled, 1);
+        if (at < kCap) sm.mine[at] = p;
+      }
+    });
+    sync();
+    if (rank == 0) {
+      int at = 0;
+      for (int j = 0; j < ctas; ++j) {
+        const Smem* o = cluster.map_shared_rank(&sm, j);
+        const int m = o->filled;
+        for (int i = threadIdx.x; i < m; i += kThreads)
+          if (at + i < kCap) sm.place[at + i] = o->mine[i];
+        at += m;
+      }
+      __syncthreads();
+    }
+    if (ctas > 1) {   // (the others' lists are read; they go on)
+      auto token = cluster.barrier_arrive();
+      if (rank == 0) n = order(n);
+      cluster.barrier_wait(std::move(token));
+    } else {
+      n = order(n);
+    }
+    return n;
+  }
+  __device__ __forceinline__ int order(int n) {
+    int at = 0;
+    if (n <= kCount) {
+      // by counting the larger ones
+      const int i = threadIdx.x;
+      if (i < n) {
+        const u64 p = sm.place[i];
+        int above = 0;
+#pragma unroll 8
+        for (int j = 0; j < n; ++j) above += sm.place[j] > p;
+        sm.place[kCount + above] = p;
+      }
+      at = kCount;
+      __syncthreads();
+    } else {
+      int size = 2 * kCount;
+      while (size < n) size <<= 1;
+      for (int i = n + threadIdx.x; i < size; i += kThreads) sm.place[i] = 0;
+      __syncthreads();
+      for (int k = 2; k <= size; k <<= 1)
+        for (int j = k >> 1; j > 0; j >>= 1) {
+          for (int t = threadIdx.x; t < size / 2; t += kThreads) {
+            const int i = 2 * j * (t / j) + t % j;
+            const u64 a = sm.place[i], b = sm.place[i + j];
+            if ((a < b) == ((i & k) == 0)) {
+              sm.place[i] = b;
+              sm.place[i + j] = a;
+            }
+          }
+          __syncthreads();
+        }
+    }
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+      float yh, yl;
+      w.orders(logit_of(sm.place[at + i]), yh, yl);
+      sm.weight[at + i] = weigh(token_of(sm.place[at + i]), yh, yl);
     }
     __syncthreads();
-    for (int k = 2; k <= size; k <<= 1)
-      for (int j = k >> 1; j > 0; j >>= 1) {
-        for (int t = threadIdx.x; t < size / 2; t += kThreads) {
-          const int i = 2 * j * (t / j) + t % j;
-          const u64 a = sm.place[i], b = sm.place[i + j];
-          if ((a < b) == ((i & k) == 0)) {
-            sm.place[i] = b;
-            sm.place[i + j] = a;
-            const u64 x = sm.weight[i];
-            sm.weight[i] = sm.weight[i + j];
-            sm.weight[i + j] = x;
-          }
-        }
-        __syncthreads();
-      }
-  }
-
-  // Whether a token belongs to a bin (and, where the row's weight is what a draft
-  // left, is kept); its distance from the maximum.
-  __device__ __forceinline__ bool member(float x, int i, int bin, float& yh, float& yl) const {
-    if (!(x >= w.floor)) return false;
-    const bool some = w.orders(x, yh, yl);
-    if ((some ? bin_of(yh) : kBins - 1) != bin) return false;
-    return !w.rest || (some && place_of(x, i) >= w.kept);
-  }
-  __device__ __forceinline__ u64 weigh(float x, int i, float yh, float yl) const {
-    if (!(yh < kOrders)) return 0;
-    const u64 v = weight_fixed(sm.pow2, yh, yl);
-    if (!w.rest) return v;
-    if (!w.q) return i == w.draft ? 0 : v;
-    const double left = (double)v - (double)w.q[i] * w.total;
-    return left > 0. ? (u64)__double2ll_rn(left) : 0;
-  }
-
-  // The row's tokens into the bins, and the bins' running sums.  With `rest`
-  // only what weighs: tokens that a draft's row no longer has are none.
-  __device__ __forceinline__ void file() {
-    clear_bins();
-    uint32_t behind = 0;
-    for_tokens(row, lo, hi, [&](float x, int i) {
-      if (!(x >= w.floor)) return;
-      float yh, yl;
-      if (!w.orders(x, yh, yl)) {
-        ++behind;
-        return;
-      }
-      if (w.rest && place_of(x, i) < w.kept) return;
-      add(bin_of(yh), weigh(x, i, yh, yl));
-    });
-    behind = w.rest ? 0 : __reduce_add_sync(0xffffffffu, behind);
-    if ((threadIdx.x & 31) == 0 && behind) atomicAdd(&sm.bins.cnt[0][kBins - 1], behind);
-    sum_bins(sm.sum_w, sm.sum_c);
-    cluster.sync();
+    return at;
   }
 
   // The end of the shortest run that holds `count` tokens, or weighs `mass` (count 0;
-  // both within what there is): its place, its weight, its last token's weight.
-  // All CTAs of the cluster take part; the results are in the first one's memory.
+  // both within what there is): its place and its weight, in the first CTA's memory.
+  // All CTAs of the cluster take part; the bins hold weights.
   __device__ __forceinline__ void find_run(uint32_t count, u64 mass) {
-    if (rank == 0) {
-      find_bin(sm.sum_w, sm.sum_c, count, mass, 0, 0);
-      if (threadIdx.x == 0) sm.fill = 0;
+    for (;;) {
+      if (rank == 0) find_bin(sm.sum_w, sm.sum_c, sm.before_w, sm.before_c, count, mass, bin0);
+      sync();
+      const int to = first.bin;
+      if (to >= 0) break;
+      file<true>(to == kLower ? bin0 - kBins : bin0 + kBins);
     }
-    cluster.sync();
     const int bin = first.bin;
     int n = first.n, shift = kPlaceBits;
     u64 from = 0;
     // more tokens than can be put in order: by the next bits of their places
     while (n > kCap) {
-      shift -= kDigit;
-      clear_bins();
-      for_tokens(row, lo, hi, [&](float x, int i) {
-        float yh, yl;
-        if (!member(x, i, bin, yh, yl)) return;
-        const u64 p = place_of(x, i);
-        if (p < from || (p - from) >> (shift + kDigit)) return;
-        add((1 << kDigit) - 1 - (int)((p - from) >> shift), weigh(x, i, yh, yl));
+      const int was = shift;
+      shift = max(shift - kDigit, 0);
+      clear_bins(true);
+      for_tokens<2>(row, lo, hi, [&](const auto& x, int i) {
+#pragma unroll
+        for (int k = 0; k < (int)(sizeof(x) / sizeof(float)); ++k) {
+          float yh, yl;
+          w.orders(x[k], yh, yl);
+          if (bin_of(yh) != bin || !in_row(x[k], i + k)) continue;
+          const u64 p = place_of(x[k], i + k);
+          if (p >= from && !((p - from) >> was))
+            add(kBins - 1 - (int)((p - from) >> shift), weigh(i + k, yh, yl));
+        }
       });
-      sum_bins(sm.part_w, sm.part_c);
+      sum_bins<true>(sm.part_w, sm.part_c, &sm.base_w, &sm.base_c);
       if (rank == 0) {
-        find_bin(sm.part_w, sm.part_c, count, mass, sm.base_w, sm.base_c);
-        if (threadIdx.x == 0) sm.from = from + ((u64)((1 << kDigit) - 1 - sm.bin) << shift);
+        find_bin(sm.part_w, sm.part_c, sm.base_w, sm.base_c, count, mass, 0);
+        if (threadIdx.x == 0) sm.from = from + ((u64)(kBins - 1 - sm.bin) << shift);
       }
-      cluster.sync();
+      sync();
       n = first.n;
       from = first.from;
     }
-    for_tokens(row, lo, hi, [&](float x, int i) {
-      float yh, yl;
-      if (!member(x, i, bin, yh, yl)) return;
-      const u64 p = place_of(x, i);
-      if (p < from || (p - from) >> shift) return;
-      const int at = atomicAdd(&first.fill, 1);
-      if (at < kCap) {
-        first.place[at] = p;
-        first.weight[at] = weigh(x, i, yh, yl);
-      }
-    });
-    cluster.sync();
+    const int at = gather(bin, bin, from, shift, n);
     if (rank == 0) {
-      order(n);
-      constexpr int kPer = kCap / kThreads;
-      u64 v[kPer];
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        const int i = threadIdx.x * kPer + k;
-        v[k] = (i < n ? sm.weight[i] : 0) + (k ? v[k - 1] : 0);
+      Scan<kThreads> sc{sm, at, n};
+      u64 weight;
+      int i;
+      if (count) {
+        i = (int)(count - sm.base_c) - 1;
+        sc.n = i + 1;
+        sc.sum();
+        weight = sc.total();
+      } else {
+        sc.sum();
+        i = sc.reach(mass - sm.base_w, weight);
       }
-      u64 bv;
-      uint32_t bc;
-      block_before(v[kPer - 1], 0, bv, bc);
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        const int i = threadIdx.x * kPer + k;
-        const u64 iw = sm.base_w + bv + v[k], pw = sm.base_w + bv + (k ? v[k - 1] : 0);
-        if (i < n && (count ? sm.base_c + i + 1 == count : iw >= mass && pw < mass)) {
-          sm.run_place = sm.place[i];
-          sm.run_w = iw;
-        }
+      if (threadIdx.x == 0) {
+        sm.run_place = sm.place[at + i];
+        sm.run_w = sm.base_w + weight;
       }
     }
-    cluster.sync();
+    sync();
   }
 };
 
-// exp((x - max) / temperature) / total of one token, in 64 bits
-__device__ double share_of(double x, double max, double heat, u64 total) {
-  const double w = x == max ? 1. : exp((x - max) / heat);
-  return w / ((double)total * (1. / (double)(1ull << kFix)));
+// What a row wants of its distribution.
+struct Wanted {
+  int top_k;
+  float top_p, u, u_next;
+  bool last;      // no draft follows: draw
+};
+
+// Whether a draft of weight (s + r) 2^-n, or none, stays.
+__device__ __forceinline__ bool draft_stays(const Smem& sm, const Row& w, float x, int draft, bool kept, u64 total,
+                                            float u) {
+  if (!kept) return false;
+  float yh, yl, s, r;
+  int n;
+  w.orders(x, yh, yl);
+  if (!(yh < 1024.f)) return false;
+  pow2_neg(sm.pow2, yh, yl, s, r, n);
+  const double q = w.q ? (double)w.q[draft] : 1.;
+  // u q < w / total
+  return (double)u * q * ((double)total * 0x1p-44) < scalbn((double)s + (double)r, -n);
+}
+
+// The rest of a row whose kept tokens are among the n of the first CTA's list, by
+// one warp or the CTA: what is kept, and the token.  -1: the draft stays.
+template <int THREADS, class T>
+__device__ __forceinline__ u64 decide(Sampler<T>& s, const Wanted& want, int at, int n, u64& total, u64& kept,
+                                      bool& stays) {
+  Smem& sm = s.sm;
+  if (want.top_k > 0) n = min(n, want.top_k);
+  Scan<THREADS> sc{sm, at, n};
+  sc.sum();
+  if (want.top_k > 0) total = sc.total();
+  if (want.top_p < 1.f) {
+    u64 weight;
+    sc.n = n = sc.reach(max(share(total, want.top_p, true), 1ull), weight) + 1;
+    total = weight;
+  }
+  kept = sm.place[at + n - 1];
+  stays = false;
+  if (!want.last) {
+    if (threadIdx.x == 0) {
+      const int d = s.w.draft;
+      const float x = s.w.draft_x;
+      sm.stays = draft_stays(sm, s.w, x, d, s.w.draft_in && x >= s.w.floor && place_of(x, d) >= kept, total, want.u);
+    }
+    Scan<THREADS>::sync();
+    stays = sm.stays != 0;
+    if (stays) return 0;
+    // what the draft left of the kept tokens, if anything
+    s.w.rest = true;
+    s.w.total = (double)total;
+    u64 mine[kPer], some = 0;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int i = sc.entry(k);
+      mine[k] = i < n ? s.left(sm.weight[at + i], token_of(sm.place[at + i])) : 0;
+      some |= mine[k];
+    }
+    if (THREADS == 32 ? __any_sync(0xffffffffu, some != 0) : __syncthreads_or(some != 0)) {
+      Scan<THREADS>::sync();
+#pragma unroll
+      for (int k = 0; k < kPer; ++k)
+        if (sc.entry(k) < n) sm.weight[at + sc.entry(k)] = mine[k];
+      Scan<THREADS>::sync();
+      sc.sum();
+      total = sc.total();
+    }
+  }
+  u64 weight;
+  return sm.place[at + sc.reach(share(total, want.u_next, false), weight)];
 }
 
 template <class T>
-__global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams p) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams p) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
   const cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
   const int r = blockIdx.x / ctas;   // row
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  dev::pdl_trigger();
+  for (int i = threadIdx.x; i < 1024; i += kThreads) sm.pow2[i] = make_float2(kPow2.hi[i], kPow2.lo[i]);
+  dev::pdl_wait();
 
   // the row's request, and the draft after it (-1: none, the sequence's last row)
   int req = r, draft = -1;
-  bool last = true;
+  Wanted want;
+  want.last = true;
   if (p.cu) {
     int a = 0, b = p.n_seq + 1;       // first entry above r
     while (a < b) {
@@ -465,168 +760,247 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
     }
     req = a - 1;
     if (req < 0 || req >= p.n_seq) return;   // (the whole cluster)
-    last = r + 1 >= min(p.cu[req + 1], p.rows);
-    if (!last) draft = p.tokens[r + 1];
+    want.last = r + 1 >= min(p.cu[req + 1], p.rows);
+    if (!want.last) draft = p.tokens[r + 1];
   }
+  // (every CTA of the cluster runs before its memory is written: waited for below)
+  auto arrived = cluster.barrier_arrive();
   float heat = p.s.temperature ? p.s.temperature[req] : 1.f;
-  int top_k = p.s.top_k ? p.s.top_k[req] : 0;
+  want.top_k = p.s.top_k ? p.s.top_k[req] : 0;
   const float min_p = p.s.min_p ? p.s.min_p[req] : 0.f;
-  const float top_p = p.s.top_p ? p.s.top_p[req] : 1.f;
-  const float u = !p.cu ? p.u[r] : last ? 0.f : p.u[r];
-  const float u_next = p.cu ? p.u_next[req] : u;
-  bool bad = !(heat == 0.f || (heat >= 0x1p-64f && heat <= 0x1p64f)) || min_p != min_p || top_p != top_p ||
-             !(u >= 0.f && u < 1.f) || !(u_next >= 0.f && u_next < 1.f);
-  if (heat == 0.f) {
-    heat = 1.f;
-    top_k = 1;
-  }
-
-  cluster.sync();   // every CTA of the cluster runs: its memory may be written
-  for (int i = threadIdx.x; i < 1024; i += kThreads) sm.pow2[i] = make_float2(kPow2.hi[i], kPow2.lo[i]);
-
+  want.top_p = p.s.top_p ? p.s.top_p[req] : 1.f;
+  want.u = p.cu && want.last ? 0.f : p.u[r];
+  want.u_next = p.cu ? p.u_next[req] : want.u;
   const T* row = static_cast<const T*>(p.logits) + p.stride * r;
   const int per = (p.vocab + ctas - 1) / ctas;
   const int lo = min(rank * per, p.vocab), hi = min(lo + per, p.vocab);
 
-  // the largest logit
+  // the largest logit, the first of them
   float best = -INFINITY;
-  bool nan = false;
-  for_tokens(row, lo, hi, [&](float x, int) {
-    best = fmaxf(best, x);
-    nan |= x != x;
-  });
+  int best_i = lo;
+  bool bad = false;
+  for_tokens<4>(row, lo, hi, [&](const auto& x, int i) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
-  float* red = reinterpret_cast<float*>(sm.warp_w);
-  if (lane == 0) red[warp] = best;
-  nan = __syncthreads_or(nan);
-  if (threadIdx.x == 0) {
-    for (int k = 1; k < kWarps; ++k) best = fmaxf(best, red[k]);
-    for (int j = 0; j < ctas; ++j) {
-      Smem* o = cluster.map_shared_rank(&sm, j);
-      o->max_[rank] = best;
-      o->bad_[rank] = nan;
+    for (int k = 0; k < (int)(sizeof(x) / sizeof(float)); ++k) {
+      if (x[k] > best) {
+        best = x[k];
+        best_i = i + k;
+      }
+      bad |= x[k] != x[k];
     }
+  });
+  bad |= !(heat == 0.f || (heat >= 0x1p-64f && heat <= 0x1p64f)) || min_p != min_p || want.top_p != want.top_p ||
+         !(want.u >= 0.f && want.u < 1.f) || !(want.u_next >= 0.f && want.u_next < 1.f);
+  if (heat == 0.f) {
+    heat = 1.f;
+    want.top_k = 1;
   }
-  cluster.sync();
-  best = sm.max_[0];
-  bad |= sm.bad_[0] != 0;
-  for (int j = 1; j < ctas; ++j) {
-    best = fmaxf(best, sm.max_[j]);
-    bad |= sm.bad_[j] != 0;
+  if (warp == 1 && lane == 0 && min_p > 0.f) sm.min_orders = (double)heat * log((double)fminf(min_p, 1.f));
+  // (a row without a distribution: no key is that large)
+  auto join = [](uint32_t& key, uint32_t& i) {
+    const uint32_t k = __reduce_max_sync(0xffffffffu, key);
+    i = __reduce_min_sync(0xffffffffu, key == k ? i : 0xffffffffu);
+    key = k;
+  };
+  uint32_t key = bad ? 0xffffffffu : (uint32_t)(place_of(best, 0) >> kSampleIndexBits), key_i = (uint32_t)best_i;
+  join(key, key_i);
+  if (lane == 0) {
+    sm.warp_c[warp] = key;
+    sm.warp_i[warp] = key_i;
   }
-  bad |= best == -INFINITY;
+  __syncthreads();
+  key = sm.warp_c[lane % kWarps];
+  key_i = sm.warp_i[lane % kWarps];
+  join(key, key_i);
+  cluster.barrier_wait(std::move(arrived));
+  if (threadIdx.x < ctas) {
+    Smem* o = cluster.map_shared_rank(&sm, threadIdx.x);
+    o->best_key[rank] = key;
+    o->best_i[rank] = key_i;
+  }
+  if (ctas > 1) cluster.sync();
+  else __syncthreads();
+  key = lane < ctas ? sm.best_key[lane] : 0;
+  key_i = lane < ctas ? sm.best_i[lane] : 0xffffffffu;
+  join(key, key_i);
+  const int top_token = (int)key_i;
+  best = logit_of((u64)key << kSampleIndexBits);
+  bad = key == 0xffffffffu || best == -INFINITY;
   float* dist = p.dist ? p.dist + p.dist_stride * r : nullptr;
-  if (bad) {   // (every CTA of the cluster alike)
+  // (of what follows every CTA of the cluster decides alike)
+  const bool certain = want.top_k == 1 || want.top_p <= 0.f;   // only the first token is kept
+  if (bad || (certain && !p.cu)) {
     if (dist)
-      for (int i = lo + threadIdx.x; i < hi; i += kThreads) dist[i] = 0.f;
+      for (int i = lo + threadIdx.x; i < hi; i += kThreads) dist[i] = !bad && i == top_token ? 1.f : 0.f;
     if (rank == 0 && threadIdx.x == 0) {
       if (p.cu) {
         p.outcome[r] = -1;
       } else {
-        p.token[r] = -1;
-        if (p.prob) p.prob[r] = 0.f;
+        p.token[r] = bad ? -1 : top_token;
+        if (p.prob) p.prob[r] = bad ? 0.f : 1.f;
       }
     }
     return;
   }
 
-  const double c = 1.4426950408889634074 / (double)heat;
-  Row w;
-  w.max = best;
-  w.ch = (float)c;
-  w.cl = (float)(c - (double)w.ch);
-  w.floor = min_p > 0.f ? __double2float_ru((double)best + (double)heat * log((double)fminf(min_p, 1.f))) : -INFINITY;
-  w.rest = false;
-  w.kept = 0;
-  w.q = p.q ? p.q + p.q_stride * r : nullptr;
-  w.draft = draft;
-  w.total = 0.;
-  Sampler<T> s{sm, *cluster.map_shared_rank(&sm, 0), cluster, row, lo, hi, rank, w};
-  s.file();
-  u64 total = s.first.sum_w[kBins - 1];
-  const uint32_t tokens = s.first.sum_c[kBins - 1];
-  u64 kept = 0;
-  if (top_k > 0 && (uint32_t)top_k < tokens) {
-    s.find_run(top_k, 0);
-    kept = s.first.run_place;
-    total = s.first.run_w;
+  Sampler<T> s{sm, *cluster.map_shared_rank(&sm, 0), cluster, row, lo, hi, rank, ctas};
+  s.w.max = best;
+  {
+    constexpr float kLog2eH = 1.44269502162933349609375f, kLog2eL = 1.92596299112661746887e-08f;
+    s.w.ch = kLog2eH / heat;
+    s.w.cl = (fmaf(-s.w.ch, heat, kLog2eH) + kLog2eL) / heat;
   }
-  if (top_p < 1.f) {
-    const u64 t = top_p > 0.f ? share(total, top_p, true) : 1;
-    s.find_run(0, t);
-    kept = s.first.run_place;
-    total = s.first.run_w;
-  }
+  s.w.floor = min_p > 0.f ? __double2float_ru((double)best + sm.min_orders) : -INFINITY;
+  s.w.rest = false;
+  s.w.kept = 0;
+  s.w.q = p.q ? p.q + p.q_stride * r : nullptr;
+  s.w.draft = draft;
+  s.w.draft_in = draft >= 0 && draft < p.vocab;
+  s.w.draft_x = s.w.draft_in ? to_float(row[draft]) : 0.f;
+  s.w.total = 0.;
 
-  if (p.cu && !last) {
-    // does the draft stay?
-    if (rank == 0 && threadIdx.x == 0) {
-      double pd = 0.;
-      if (draft >= 0 && draft < p.vocab) {
-        const float x = to_float(row[draft]);
-        if (x >= w.floor && place_of(x, draft) >= kept) pd = share_of(x, best, heat, total);
-      }
-      const double qd = !s.w.q ? 1. : draft >= 0 && draft < p.vocab ? (double)s.w.q[draft] : 1.;
-      sm.stays = (double)u * qd < pd;
-      if (sm.stays) p.outcome[r] = kStays;
+  u64 kept = 0, total = 1ull << kFix;
+  bool listed = certain;            // the kept tokens are in the first CTA's list, in order
+  int at = 0, n = 1;
+  if (certain) {
+    if (threadIdx.x == 0) {
+      sm.place[0] = place_of(best, top_token);
+      sm.weight[0] = total;
     }
-    cluster.sync();
-    const bool stays = s.first.stays != 0;
-    if (!stays) {
-      s.w.rest = true;
-      s.w.kept = kept;
-      s.w.total = (double)total;
-      s.file();
-      const u64 left = s.first.sum_w[kBins - 1];
-      if (left) {
-        total = left;
+    __syncthreads();
+  } else {
+    if (want.top_k > 0) s.template file<false>(0);
+    else s.template file<true>(0);
+    // few tokens up to the end of the kept ones: they are all that the rest needs
+    if (rank == 0 && (want.top_k > 0 || want.top_p < 1.f))
+      s.find_bin(sm.sum_w, sm.sum_c, sm.before_w, sm.before_c,
+                 want.top_k > 0 ? min((uint32_t)want.top_k, sm.total_c) : 0,
+                 want.top_k > 0 ? 0 : share(sm.total_w, want.top_p, true), 0);
+    s.sync();
+    const uint32_t tokens = s.first.total_c;
+    total = s.first.total_w;
+    if (want.top_k > 0 || want.top_p < 1.f) {
+      const int bin = s.first.bin;
+      n = bin >= 0 ? s.first.base_c + s.first.n : kCap + 1;
+      listed = n <= kCap;
+      if (listed) {
+        at = s.gather(0, bin, 0, kPlaceBits, n);
       } else {
-        cluster.sync();   // (everyone has read it)
-        s.w.rest = false;
-        s.file();
+        s.sync();   // (the first CTA's memory has been read)
+        if (want.top_k > 0) {
+          s.template file<true>(0);
+          s.sync();
+          total = s.first.total_w;
+        }
+        if (want.top_k > 0 && (uint32_t)want.top_k < tokens) {
+          s.find_run(want.top_k, 0);
+          kept = s.first.run_place;
+          total = s.first.run_w;
+        }
+        if (want.top_p < 1.f) {
+          s.find_run(0, share(total, want.top_p, true));
+          kept = s.first.run_place;
+          total = s.first.run_w;
+        }
       }
-    }
-    if (stays) {
-      cluster.sync();     // (the first CTA's memory has been read)
-      return;
     }
   }
-  s.find_run(0, share(total, u_next, false));
-  const u64 place = s.first.run_place;
+  bool stays = false;
+  u64 place = 0;
+  if (listed) {
+    if (rank && !dist) return;   // (the first CTA has what it needs)
+    if (rank == 0) {
+      if (n <= 32 * kPer) {
+        if (warp == 0) place = decide<32>(s, want, at, n, total, kept, stays);
+      } else {
+        place = decide<kThreads>(s, want, at, n, total, kept, stays);
+      }
+    }
+    if (dist) {   // (no drafts then: the row's own distribution)
+      if (rank == 0 && threadIdx.x == 0) {
+        sm.kept = kept;
+        sm.kept_w = total;
+      }
+      s.sync();
+      kept = s.first.kept;
+      total = s.first.kept_w;
+    }
+  } else {
+    if (!want.last) {
+      // does the draft stay?
+      if (threadIdx.x == 0)
+        sm.stays = draft_stays(sm, s.w, s.w.draft_x, draft,
+                               s.w.draft_in && s.w.draft_x >= s.w.floor && place_of(s.w.draft_x, draft) >= kept, total,
+                               want.u);
+      __syncthreads();
+      stays = sm.stays != 0;   // (every CTA finds the same)
+      if (!stays) {
+        s.sync();
+        s.w.rest = true;
+        s.w.kept = kept;
+        s.w.total = (double)total;
+        s.template file<true>(0);
+        s.sync();
+        const u64 left = s.first.total_w;
+        if (left) {
+          total = left;
+        } else {
+          s.sync();         // (everyone has read it)
+          s.w.rest = false;
+          s.template file<true>(0);
+          s.sync();
+        }
+      }
+    }
+    if (!stays) {
+      s.find_run(0, share(total, want.u_next, false));
+      place = s.first.run_place;
+    }
+  }
   if (rank == 0 && threadIdx.x == 0) {
-    const int token = (int)(kIndexMask - (uint32_t)(place & kIndexMask));
+    const int token = token_of(place);
     if (p.cu) {
-      p.outcome[r] = token;
+      p.outcome[r] = stays ? kStays : token;
     } else {
       p.token[r] = token;
-      if (p.prob) p.prob[r] = (float)share_of(to_float(row[token]), best, heat, total);
+      if (p.prob) {
+        float yh, yl, a, b;
+        int m;
+        s.w.orders(logit_of(place), yh, yl);
+        pow2_neg(sm.pow2, yh, yl, a, b, m);
+        p.prob[r] = share_of(a, b, m, pair_of(total));
+      }
     }
   }
   if (dist) {
-    const double inv = (double)(1ull << kFix) / (double)total;
-    const float ih = (float)inv, il = (float)(inv - (double)ih);
-    for_tokens(row, lo, hi, [&](float x, int i) {
-      float v = 0.f, yh, yl;
-      s.w.orders(x, yh, yl);
-      if (x >= w.floor && yh < 152.f && place_of(x, i) >= kept) {
-        float a, b;
-        int n;
-        pow2_neg(sm.pow2, yh, yl, a, b, n);
-        const float h = a * ih;
-        v = h + (fmaf(a, ih, -h) + fmaf(a, il, b * ih));
-        // (in two steps, of which only the second may leave the normal numbers)
-        const int m = min(n, 100);
-        v = v * __int_as_float((127 - m) << 23) * __int_as_float((127 - (n - m)) << 23);
+    const float2 sum = pair_of(total);
+    const float ih = 1.f / sum.x, il = (fmaf(-ih, sum.x, 1.f) - ih * sum.y) * ih;
+    for_tokens<2>(row, lo, hi, [&](const auto& x, int i) {
+#pragma unroll
+      for (int k = 0; k < (int)(sizeof(x) / sizeof(float)); ++k) {
+        float v = 0.f, yh, yl;
+        s.w.orders(x[k], yh, yl);
+        if (x[k] >= s.w.floor && yh < 152.f && place_of(x[k], i + k) >= kept) {
+          float a, b;
+          int m;
+          pow2_neg(sm.pow2, yh, yl, a, b, m);
+          const float h = a * ih;
+          v = h + (fmaf(a, ih, -h) + fmaf(a, il, b * ih));
+          // (in two steps, of which only the second may leave the normal numbers)
+          const int q = min(m, 100);
+          v = v * __int_as_float((127 - q) << 23) * __int_as_float((127 - (m - q)) << 23);
+        }
+        dist[i + k] = v;
       }
-      dist[i] = v;
     });
   }
-  cluster.sync();
+  if (ctas > 1 && (!listed || dist)) cluster.sync();   // (the first CTA's memory is read to the end)
 }
 
 // One warp per sequence: the first row whose draft does not stay.
 __global__ void __launch_bounds__(256) accept_kernel(const SampleParams p) {
+  dev::pdl_trigger();
+  dev::pdl_wait();
   const int b = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (b >= p.n_seq) return;
   const int r0 = max(p.cu[b], 0), r1 = min(p.cu[b + 1], p.rows);
@@ -656,27 +1030,28 @@ cudaError_t launch(const SampleParams& p, int ctas, cudaStream_t st) {
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = sizeof(Smem);
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim = {(unsigned)ctas, 1, 1};
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = pdl_enabled() ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, sample_kernel<T>, p);
 }
 
 }  // namespace
 
 cudaError_t launch_sample(const SampleParams& p, int sms, cudaStream_t st) {
-  // CTAs of a row: as many as fill the SMs once, with 2048 tokens each at least
+  // CTAs of a row: as many as two on each SM, with 2048 tokens each at least
   int ctas = 1;
-  while (ctas < kMaxCluster && (long long)p.rows * ctas * 2 <= sms && p.vocab >= 4096 * ctas) ctas *= 2;
+  while (ctas < kMaxCluster && (long long)p.rows * ctas <= sms && p.vocab >= 4096 * ctas) ctas *= 2;
   cudaError_t e = p.rows == 0             ? cudaSuccess
                   : p.type == KVR_ACT_F32 ? launch<float>(p, ctas, st)
                   : p.type == KVR_ACT_BF16 ? launch<__nv_bfloat16>(p, ctas, st)
                                            : launch<__half>(p, ctas, st);
   if (e != cudaSuccess || !p.cu) return e;
-  accept_kernel<<<(p.n_seq + 7) / 8, 256, 0, st>>>(p);
-  return cudaGetLastError();
+  return launch_k(accept_kernel, dim3((p.n_seq + 7) / 8), dim3(256), 0, st, p);
 }
 
 }  // namespace kvr
