@@ -32,14 +32,14 @@ using u64 = unsigned long long;
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
 constexpr int kBins = 1024;          // held at a time, two a thread
 constexpr int kFix = 44;
-constexpr int kOrders = 48;          // binary orders from the maximum on which a token weighs nothing
-// Bins of a binary order: where weights are filed 32, so that 32 orders are held at a time and a bin
-// of the bulk of 262144 tokens is about as many as can be put in order; where tokens are only
-// counted 16, so that one pass holds all.
-constexpr float kFine = 32.f, kCoarse = 16.f;
+constexpr float kNothing = 46.f;     // binary orders from the maximum on which a token weighs nothing
+// Steps (1/1024 of a binary order) of a bin, by their logarithm: where weights are filed 32, so that
+// 32 orders are held at a time and a bin of the bulk of 262144 tokens is about as many as can be put
+// in order; where tokens are only counted 64, so that one pass holds all.
+constexpr int kFine = 5, kCoarse = 6;
 constexpr int kCopies = 2;           // of the bins, by lane: equal logits meet in one
 constexpr int kCap = 2048;           // tokens that one CTA puts in order
 constexpr int kCount = 512;          // as many by counting the larger ones
@@ -105,8 +105,9 @@ struct Smem {
 constexpr int kLower = -1, kHigher = -2;
 
 // What a row's tokens weigh.
+constexpr float kFinite = 3.4028234663852886e38f;
 struct Row {
-  float max;
+  float max;            // (where it is infinite, the largest number: `floor` then leaves the infinite ones)
   float ch, cl;         // log2(e) / temperature
   float floor;          // logits below weigh less than min_p
   // of a rejected draft's row: weight beyond the drafter's
@@ -118,18 +119,15 @@ struct Row {
   u64 kept;             // places from here on
   bool rest;
 
-  // binary orders below the maximum, as a pair; false where a token weighs nothing
-  __device__ __forceinline__ bool orders(float x, float& yh, float& yl) const {
-    if (x == max) {     // (also at infinity)
-      yh = yl = 0.f;
-      return true;
-    }
+  // binary orders below the maximum, as a pair (of what is at infinity only the
+  // first number counts)
+  __device__ __forceinline__ void orders(float x, float& yh, float& yl) const {
+    x = fminf(x, kFinite);
     const float d = max - x;
     const float b = d - max;
     const float dl = (max - (d - b)) - (x + b);
     yh = d * ch;
     yl = fmaf(d, ch, -yh) + fmaf(d, cl, dl * ch);
-    return yh < (float)kOrders;
   }
 };
 
@@ -145,8 +143,7 @@ __device__ __forceinline__ float logit_of(u64 place) {
 }
 __device__ __forceinline__ int token_of(u64 place) { return (int)(kIndexMask - (uint32_t)(place & kIndexMask)); }
 
-// 2^-(yh + yl) = (s + r) 2^-n: the step of 1024 below from the table, the rest
-// by its series, whose first term is a pair of floats.
+// 2^-(yh + yl) = (s + r) 2^-n for distances of any size, as below.
 __device__ __forceinline__ void pow2_neg(const float2* tab, float yh, float yl, float& s, float& r, int& n) {
   constexpr float kLn2h = 0.693147182464599609375f;
   constexpr float kLn2l = -1.904654323148236e-09f;
@@ -164,11 +161,31 @@ __device__ __forceinline__ void pow2_neg(const float2* tab, float yh, float yl, 
   r = (a - (s - t.x)) + al;
 }
 
-// in units of 2^-44, for yh below kOrders
+// Distances in steps of 1/1024 of an order: the low bits of the float that has a
+// step as its unit.  Distances of 64 orders and more count as the last bin's.
+constexpr float kStepOne = 12582912.f;   // 1.5 * 2^23
+__device__ __forceinline__ uint32_t steps_of(float yh) {
+  return __float_as_uint(fmaf(fminf(yh, 63.96875f), 1024.f, kStepOne)) - __float_as_uint(kStepOne);
+}
+
+// The weight in units of 2^-44, as 2^-(yh + yl) = (s + r) 2^-n with the nearest
+// step from the table and the rest by its series, whose first term is a pair of
+// floats.  (One function: wherever a token is weighed it weighs the same.)
 __device__ __forceinline__ u64 weight_fixed(const float2* tab, float yh, float yl) {
-  float s, r;
-  int n;
-  pow2_neg(tab, yh, yl, s, r, n);
+  constexpr float kLn2h = 0.693147182464599609375f;
+  constexpr float kLn2l = -1.904654323148236e-09f;
+  yh = fminf(yh, 63.96875f);
+  const float t = fmaf(yh, 1024.f, kStepOne);
+  const uint32_t j = __float_as_uint(t) - __float_as_uint(kStepOne);
+  const float f = fmaf(t - kStepOne, -1.f / 1024.f, yh);
+  const float zh = -f * kLn2h;
+  const float zl = fmaf(-f, kLn2h, -zh) - fmaf(f, kLn2l, yl * kLn2h);
+  const float e = fmaf(zh * zh, fmaf(zh, 1.f / 6.f, 0.5f), zl);   // (z^4 / 24 is below 2^-50)
+  const float2 p = tab[j & 1023];
+  const float a = p.x * zh;
+  const float s = p.x + a;
+  const float r = (a - (s - p.x)) + (fmaf(p.y, zh, fmaf(p.x, zh, -a)) + fmaf(p.x, e, p.y));
+  const int n = j >> 10;
   const u64 v = ((u64)__float2uint_rn(s * 0x1p31f) << (kFix - 31)) + (long long)__float2int_rn(r * 0x1p44f);
   return (v + ((1ull << n) >> 1)) >> n;
 }
@@ -301,16 +318,15 @@ struct Sampler {
   int lo, hi;           // this CTA's tokens
   int rank, ctas;
   Row w;
-  float scale;          // bins of a binary order
+  int shift;            // log2 of the steps of a bin
   int bin0;             // the first one held
 
   // (bins are told apart by the logit's distance alone, so equal logits share one)
-  __device__ __forceinline__ int bin_of(float yh) const { return yh < 64.f ? (int)(yh * scale) : (int)(64 * scale) - 1; }
+  __device__ __forceinline__ int bin_of(float yh) const { return (int)(steps_of(yh) >> shift); }
 
   // A token's weight: what a draft left of it, where the row is such a one.
   __device__ __forceinline__ u64 weigh(int i, float yh, float yl) const {
-    if (!(yh < (float)kOrders)) return 0;
-    return left(weight_fixed(sm.pow2, yh, yl), i);
+    return yh < kNothing ? left(weight_fixed(sm.pow2, yh, yl), i) : 0;
   }
   __device__ __forceinline__ u64 left(u64 v, int i) const {
     if (!w.rest) return v;
@@ -337,13 +353,23 @@ struct Sampler {
     }
     __syncthreads();
   }
-  __device__ __forceinline__ void add(int bin, u64 v) {
+  // N tokens into their bins (< 0: none), the atomics in flight together
+  template <int N>
+  __device__ __forceinline__ void add(const int (&bin)[N], const u64 (&v)[N]) {
     const int c = threadIdx.x % kCopies;
-    atomicAdd(&sm.bins.cnt[c][bin], 1u);
-    const uint32_t l = (uint32_t)v, h = (uint32_t)(v >> 32);
-    const uint32_t old = atomicAdd(&sm.bins.lo[c][bin], l);
-    const uint32_t up = h + (old + l < old ? 1u : 0u);
-    if (up) atomicAdd(&sm.bins.hi[c][bin], up);
+    uint32_t old[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (bin[k] >= 0) {
+        atomicAdd(&sm.bins.cnt[c][bin[k]], 1u);
+        old[k] = atomicAdd(&sm.bins.lo[c][bin[k]], (uint32_t)v[k]);
+      }
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (bin[k] >= 0) {
+        const uint32_t up = (uint32_t)(v[k] >> 32) + (old[k] + (uint32_t)v[k] < old[k] ? 1u : 0u);
+        if (up) atomicAdd(&sm.bins.hi[c][bin[k]], up);
+      }
   }
 
   // Running sums over the cluster's bins, after what is in front of them, to the
@@ -377,23 +403,35 @@ struct Sampler {
       }
       cluster.sync();
       if (rank) return;
-#pragma unroll 4
-      for (int j = 1; j < ctas; ++j) take(cluster.map_shared_rank(&sm, j)->bins, 0);
+#pragma unroll
+      for (int j = 1; j < kMaxCluster; ++j)
+        if (j < ctas) take(cluster.map_shared_rank(&sm, j)->bins, 0);
     }
-    if (front_w == &sm.before_w && threadIdx.x == 0) {
+    if (front_w == &sm.before_w && warp == 0) {
       u64 fw = 0, rw = 0;
       uint32_t fc = 0, rc = 0;
-      for (int j = 0; j < ctas; ++j) {
-        const Smem* o = cluster.map_shared_rank(&sm, j);
-        fw += o->front_w;
-        rw += o->rest_w;
-        fc += o->front_c;
-        rc += o->rest_c;
+      if (MASS && lane < ctas) {
+        const Smem* o = cluster.map_shared_rank(&sm, lane);
+        fw = o->front_w;
+        rw = o->rest_w;
+        fc = o->front_c;
+        rc = o->rest_c;
       }
-      sm.before_w = fw;
-      sm.before_c = fc;
-      sm.total_w = rw;
-      sm.total_c = rc;
+      if (MASS) {
+        fc = __reduce_add_sync(0xffffffffu, fc);
+        rc = __reduce_add_sync(0xffffffffu, rc);
+#pragma unroll
+        for (int o = kMaxCluster / 2; o > 0; o >>= 1) {
+          fw += __shfl_xor_sync(0xffffffffu, fw, o);
+          rw += __shfl_xor_sync(0xffffffffu, rw, o);
+        }
+      }
+      if (lane == 0) {
+        sm.before_w = fw;
+        sm.before_c = fc;
+        sm.total_w = rw;
+        sm.total_c = rc;
+      }
     }
     v[1] += v[0];
     c[1] += c[0];
@@ -436,7 +474,7 @@ struct Sampler {
   template <bool MASS>
   __device__ __forceinline__ void file(int to) {
     bin0 = to;
-    scale = MASS ? kFine : kCoarse;
+    shift = MASS ? kFine : kCoarse;
     clear_bins(MASS);
     u64 front_w = 0, rest_w = 0;
     uint32_t front_c = 0, rest_c = 0;
@@ -448,7 +486,7 @@ struct Sampler {
       for (int k = 0; k < N; ++k) {
         w.orders(x[k], yh[k], yl[k]);
         in[k] = in_row(x[k], i + k);
-        near |= in[k] && yh[k] < (float)kOrders;
+        near |= in[k] && yh[k] < kNothing;
       }
       if (!MASS) {
 #pragma unroll
@@ -465,22 +503,25 @@ struct Sampler {
       } else {
         u64 v[N];
 #pragma unroll
-        for (int k = 0; k < N; ++k) v[k] = yh[k] < (float)kOrders ? weight_fixed(sm.pow2, yh[k], yl[k]) : 0;
+        for (int k = 0; k < N; ++k) v[k] = weight_fixed(sm.pow2, yh[k], yl[k]);
+        int b[N];
 #pragma unroll
-        for (int k = 0; k < N; ++k)
+        for (int k = 0; k < N; ++k) {
+          b[k] = -1;
           if (in[k]) {
-            const u64 m = left(v[k], i + k);
-            const int b = bin_of(yh[k]) - bin0;
-            if ((unsigned)b < kBins) {
-              add(b, m);
-            } else if (b < 0) {
-              ++front_c;
-              front_w += m;
-            } else {
+            v[k] = left(v[k], i + k);
+            b[k] = bin_of(yh[k]) - bin0;
+            if (b[k] >= kBins) {
+              b[k] = -1;
               ++rest_c;
-              rest_w += m;
+              rest_w += v[k];
+            } else if (b[k] < 0) {
+              ++front_c;
+              front_w += v[k];
             }
           }
+        }
+        add(b, v);
       }
     });
     if (MASS) {
@@ -522,33 +563,42 @@ struct Sampler {
     __syncthreads();
   }
 
-  // The tokens of bins b0 .. b1 (in [from, from + 2^shift) of their places), n in
+  // The tokens of bins b0 .. b1 (in [from, from + 2^width) of their places), n in
   // all, in order in the first CTA's list, from the entry that it returns on.
-  __device__ __forceinline__ int gather(int b0, int b1, u64 from, int shift, int n) {
+  __device__ __forceinline__ int gather(int b0, int b1, u64 from, int width, int n) {
     if (threadIdx.x == 0) sm.filled = 0;
     __syncthreads();
+    // (a bin's bounds are floats; behind the last one nothing is)
+    const float y0 = ((float)(b0 << shift) - 0.5f) / 1024.f;
+    const float y1 = (b1 + 1) << shift < 65536 ? ((float)((b1 + 1) << shift) - 0.5f) / 1024.f
+                                                     : __int_as_float(0x7fffffff);
     for_tokens<4>(row, lo, hi, [&](const auto& x, int i) {
 #pragma unroll
       for (int k = 0; k < (int)(sizeof(x) / sizeof(float)); ++k) {
-        float yh, yl;
-        w.orders(x[k], yh, yl);
-        const int b = bin_of(yh);
-        if (b < b0 || b > b1 || !in_row(x[k], i + k)) continue;
+        const float yh = (w.max - fminf(x[k], kFinite)) * w.ch;
+        if (yh < y0 || yh >= y1 || !in_row(x[k], i + k)) continue;
         const u64 p = place_of(x[k], i + k);
-        if (p < from || (p - from) >> shift) continue;
+        if (p < from || (p - from) >> width) continue;
         const int at = atomicAdd(&sm.filled, 1);
         if (at < kCap) sm.mine[at] = p;
       }
     });
     sync();
     if (rank == 0) {
-      int at = 0;
-      for (int j = 0; j < ctas; ++j) {
-        const Smem* o = cluster.map_shared_rank(&sm, j);
-        const int m = o->filled;
-        for (int i = threadIdx.x; i < m; i += kThreads)
-          if (at + i < kCap) sm.place[at + i] = o->mine[i];
-        at += m;
+      int end[kMaxCluster];   // of each CTA's tokens in the list
+#pragma unroll
+      for (int j = 0; j < kMaxCluster; ++j) end[j] = j < ctas ? cluster.map_shared_rank(&sm, j)->filled : 0;
+#pragma unroll
+      for (int j = 1; j < kMaxCluster; ++j) end[j] += end[j - 1];
+      for (int i = threadIdx.x; i < n; i += kThreads) {
+        int j = 0, at = 0;
+#pragma unroll
+        for (int k = 0; k + 1 < kMaxCluster; ++k)
+          if (i >= end[k]) {
+            j = k + 1;
+            at = end[k];
+          }
+        sm.place[i] = cluster.map_shared_rank(&sm, j)->mine[i - at];
       }
       __syncthreads();
     }
@@ -614,12 +664,12 @@ struct Sampler {
       file<true>(to == kLower ? bin0 - kBins : bin0 + kBins);
     }
     const int bin = first.bin;
-    int n = first.n, shift = kPlaceBits;
+    int n = first.n, width = kPlaceBits;
     u64 from = 0;
     // more tokens than can be put in order: by the next bits of their places
     while (n > kCap) {
-      const int was = shift;
-      shift = max(shift - kDigit, 0);
+      const int was = width;
+      width = max(width - kDigit, 0);
       clear_bins(true);
       for_tokens<2>(row, lo, hi, [&](const auto& x, int i) {
 #pragma unroll
@@ -628,20 +678,23 @@ struct Sampler {
           w.orders(x[k], yh, yl);
           if (bin_of(yh) != bin || !in_row(x[k], i + k)) continue;
           const u64 p = place_of(x[k], i + k);
-          if (p >= from && !((p - from) >> was))
-            add(kBins - 1 - (int)((p - from) >> shift), weigh(i + k, yh, yl));
+          if (p >= from && !((p - from) >> was)) {
+            const int b[1] = {kBins - 1 - (int)((p - from) >> width)};
+            const u64 v[1] = {weigh(i + k, yh, yl)};
+            add(b, v);
+          }
         }
       });
       sum_bins<true>(sm.part_w, sm.part_c, &sm.base_w, &sm.base_c);
       if (rank == 0) {
         find_bin(sm.part_w, sm.part_c, sm.base_w, sm.base_c, count, mass, 0);
-        if (threadIdx.x == 0) sm.from = from + ((u64)(kBins - 1 - sm.bin) << shift);
+        if (threadIdx.x == 0) sm.from = from + ((u64)(kBins - 1 - sm.bin) << width);
       }
       sync();
       n = first.n;
       from = first.from;
     }
-    const int at = gather(bin, bin, from, shift, n);
+    const int at = gather(bin, bin, from, width, n);
     if (rank == 0) {
       Scan<kThreads> sc{sm, at, n};
       u64 weight;
@@ -844,13 +897,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   }
 
   Sampler<T> s{sm, *cluster.map_shared_rank(&sm, 0), cluster, row, lo, hi, rank, ctas};
-  s.w.max = best;
+  s.w.max = fminf(best, kFinite);
   {
     constexpr float kLog2eH = 1.44269502162933349609375f, kLog2eL = 1.92596299112661746887e-08f;
     s.w.ch = kLog2eH / heat;
     s.w.cl = (fmaf(-s.w.ch, heat, kLog2eH) + kLog2eL) / heat;
   }
-  s.w.floor = min_p > 0.f ? __double2float_ru((double)best + sm.min_orders) : -INFINITY;
+  s.w.floor = best == INFINITY ? INFINITY
+              : min_p > 0.f    ? __double2float_ru((double)best + sm.min_orders)
+                               : -INFINITY;
   s.w.rest = false;
   s.w.kept = 0;
   s.w.q = p.q ? p.q + p.q_stride * r : nullptr;
@@ -1024,6 +1079,7 @@ __global__ void __launch_bounds__(256) accept_kernel(const SampleParams p) {
 template <class T>
 cudaError_t launch(const SampleParams& p, int ctas, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Smem));
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.rows * ctas);
