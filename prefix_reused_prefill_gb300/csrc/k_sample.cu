@@ -19,6 +19,7 @@
 // launch agrees on where a run ends.
 #include <cooperative_groups.h>
 
+#include <type_traits>
 #include <utility>
 
 #include "kvr_batch.cuh"
@@ -32,7 +33,7 @@ using u64 = unsigned long long;
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxCluster = 16;
+constexpr int kMaxCluster = 8;
 constexpr int kBins = 1024;          // held at a time, two a thread
 constexpr int kFix = 44;
 constexpr float kNothing = 46.f;     // binary orders from the maximum on which a token weighs nothing
@@ -42,7 +43,7 @@ constexpr float kNothing = 46.f;     // binary orders from the maximum on which 
 constexpr int kFine = 5, kCoarse = 6;
 constexpr int kCopies = 2;           // of the bins, by lane: equal logits meet in one
 constexpr int kCap = 2048;           // tokens that one CTA puts in order
-constexpr int kCount = 512;          // as many by counting the larger ones
+constexpr int kCount = 128;          // as many by counting the larger ones
 constexpr int kDigit = 10;           // bits of a place taken at a time where a bin holds more
 static_assert(kBins == 2 * kThreads && kBins == 1 << kDigit && kCount <= kThreads, "bins and digits two a thread");
 constexpr int kPlaceBits = 32 + kSampleIndexBits;
@@ -204,36 +205,71 @@ __device__ __forceinline__ float share_of(float s, float r, int n, float2 total)
   return v * __int_as_float((127 - m) << 23) * __int_as_float((127 - (n - m)) << 23);
 }
 
-// f(logits, token of the first) over the CTA's part [lo, hi) of a row, four at a
-// time (16-byte loads, U in flight) but at the ends.
+// A CTA's tokens [lo, hi) of a row, four at a time where they are aligned to it.
+template <class T>
+struct Tokens {
+  const T* row;
+  int lo, hi, a, fours, items;
+  __device__ __forceinline__ Tokens(const T* row_, int lo_, int hi_) : row(row_), lo(lo_), hi(hi_) {
+    constexpr int kBytes = 4 * sizeof(T);
+    const int skip = (int)((kBytes - ((uintptr_t)(row + lo) & (kBytes - 1))) & (kBytes - 1)) / (int)sizeof(T);
+    a = min(lo + skip, hi);
+    fours = (hi - a) / 4;
+    items = fours + (hi - lo - 4 * fours);
+  }
+  // item t: its tokens from i on, n of them (4, or 1)
+  __device__ __forceinline__ void load(int t, float (&x)[4], int& i, int& n) const {
+    if (t < fours) {
+      i = a + 4 * t;
+      n = 4;
+      typename std::conditional<sizeof(T) == 4, uint4, uint2>::type v;
+      v = *reinterpret_cast<const decltype(v)*>(row + i);
+      const T* e = reinterpret_cast<const T*>(&v);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] = to_float(e[k]);
+    } else {
+      const int left = t - fours;
+      i = left < a - lo ? lo + left : a + 4 * fours + left - (a - lo);
+      n = 1;
+      x[0] = to_float(row[i]);
+      x[1] = x[2] = x[3] = 0.f;
+    }
+  }
+};
+
+// f(logits, token of the first, how many) over the CTA's tokens, U times four in flight.
 template <int U, class T, class F>
 __device__ __forceinline__ void for_tokens(const T* row, int lo, int hi, F f) {
-  constexpr int kV = 16 / sizeof(T);
-  const int skip = (int)((16 - ((uintptr_t)(row + lo) & 15)) & 15) / (int)sizeof(T);
-  const int a = min(lo + skip, hi), b = a + (hi - a) / kV * kV;
-  auto one = [&](int i) {
-    const float x[1] = {to_float(row[i])};
-    f(x, i);
-  };
-  for (int i = lo + threadIdx.x; i < a; i += kThreads) one(i);
-  auto some = [&](const uint4& v, int i) {
-    const T* e = reinterpret_cast<const T*>(&v);
+  const Tokens<T> tk(row, lo, hi);
+  int t = threadIdx.x;
+  float x[U][4];
+  int i[U], n[U];
+  if constexpr (U == 1) {
+    // (much to do for each: one copy of it, the next four on their way)
+    if (t < tk.items) tk.load(t, x[0], i[0], n[0]);
+    while (t < tk.items) {
+      float y[4];
+      int j = 0, m = 0;
+      if (t + kThreads < tk.items) tk.load(t + kThreads, y, j, m);
+      f(x[0], i[0], n[0]);
 #pragma unroll
-    for (int k = 0; k < kV; k += 4) {
-      const float x[4] = {to_float(e[k]), to_float(e[k + 1]), to_float(e[k + 2]), to_float(e[k + 3])};
-      f(x, i + k);
+      for (int k = 0; k < 4; ++k) x[0][k] = y[k];
+      i[0] = j;
+      n[0] = m;
+      t += kThreads;
     }
-  };
-  int i = a + threadIdx.x * kV;
-  for (; i + (U - 1) * kThreads * kV < b; i += U * kThreads * kV) {
-    uint4 v[U];
+  } else {
+    for (; t < tk.items; t += U * kThreads) {
 #pragma unroll
-    for (int k = 0; k < U; ++k) v[k] = *reinterpret_cast<const uint4*>(row + i + k * kThreads * kV);
+      for (int k = 0; k < U; ++k) {
+        n[k] = 0;
+        if (t + k * kThreads < tk.items) tk.load(t + k * kThreads, x[k], i[k], n[k]);
+      }
 #pragma unroll
-    for (int k = 0; k < U; ++k) some(v[k], i + k * kThreads * kV);
+      for (int k = 0; k < U; ++k)
+        if (n[k]) f(x[k], i[k], n[k]);
+    }
   }
-  for (; i < b; i += kThreads * kV) some(*reinterpret_cast<const uint4*>(row + i), i);
-  for (int j = b + threadIdx.x; j < hi; j += kThreads) one(j);
 }
 
 // ceil(total * p) and floor(total * u) + 1 for p, u in [0, 1), exactly
@@ -355,7 +391,7 @@ struct Sampler {
   }
   // N tokens into their bins (< 0: none), the atomics in flight together
   template <int N>
-  __device__ __forceinline__ void add(const int (&bin)[N], const u64 (&v)[N]) {
+  __device__ __forceinline__ void add(const int (&bin)[N], const u64 (&v)[N]) const {
     const int c = threadIdx.x % kCopies;
     uint32_t old[N];
 #pragma unroll
@@ -476,41 +512,42 @@ struct Sampler {
     bin0 = to;
     shift = MASS ? kFine : kCoarse;
     clear_bins(MASS);
+    const Sampler c = *this;   // (in registers)
     u64 front_w = 0, rest_w = 0;
     uint32_t front_c = 0, rest_c = 0;
-    for_tokens<2>(row, lo, hi, [&](const auto& x, int i) {
-      constexpr int N = sizeof(x) / sizeof(float);
+    for_tokens<1>(c.row, c.lo, c.hi, [&](const float (&x)[4], int i, int n) {
+      constexpr int N = 4;
       float yh[N], yl[N];
       bool in[N], near = false;
 #pragma unroll
       for (int k = 0; k < N; ++k) {
-        w.orders(x[k], yh[k], yl[k]);
-        in[k] = in_row(x[k], i + k);
+        c.w.orders(x[k], yh[k], yl[k]);
+        in[k] = k < n && c.in_row(x[k], i + k);
         near |= in[k] && yh[k] < kNothing;
       }
       if (!MASS) {
 #pragma unroll
         for (int k = 0; k < N; ++k)
-          if (in[k]) atomicAdd(&sm.bins.cnt[threadIdx.x % kCopies][bin_of(yh[k])], 1u);
+          if (in[k]) atomicAdd(&c.sm.bins.cnt[threadIdx.x % kCopies][c.bin_of(yh[k])], 1u);
       } else if (!near) {
 #pragma unroll
         for (int k = 0; k < N; ++k)
           if (in[k]) {
-            const int b = bin_of(yh[k]) - bin0;
-            if (b < kBins) atomicAdd(&sm.bins.cnt[threadIdx.x % kCopies][b], 1u);   // (b >= 0: the last orders)
+            const int b = c.bin_of(yh[k]) - c.bin0;
+            if (b < kBins) atomicAdd(&c.sm.bins.cnt[threadIdx.x % kCopies][b], 1u);   // (b >= 0: the last orders)
             else ++rest_c;
           }
       } else {
         u64 v[N];
 #pragma unroll
-        for (int k = 0; k < N; ++k) v[k] = weight_fixed(sm.pow2, yh[k], yl[k]);
+        for (int k = 0; k < N; ++k) v[k] = weight_fixed(c.sm.pow2, yh[k], yl[k]);
         int b[N];
 #pragma unroll
         for (int k = 0; k < N; ++k) {
           b[k] = -1;
           if (in[k]) {
-            v[k] = left(v[k], i + k);
-            b[k] = bin_of(yh[k]) - bin0;
+            v[k] = c.left(v[k], i + k);
+            b[k] = c.bin_of(yh[k]) - c.bin0;
             if (b[k] >= kBins) {
               b[k] = -1;
               ++rest_c;
@@ -521,7 +558,7 @@ struct Sampler {
             }
           }
         }
-        add(b, v);
+        c.add(b, v);
       }
     });
     if (MASS) {
@@ -563,25 +600,41 @@ struct Sampler {
     __syncthreads();
   }
 
+  // Distances of bins b0 .. b1 (behind the last one nothing is): their bounds are floats.
+  __device__ __forceinline__ float2 bounds(int b0, int b1) const {
+    return make_float2(((float)(b0 << shift) - 0.5f) / 1024.f,
+                       (b1 + 1) << shift < 65536 ? ((float)((b1 + 1) << shift) - 0.5f) / 1024.f
+                                                 : __int_as_float(0x7fffffff));
+  }
+  // f(logit, token, place) for the CTA's tokens of bins b0 .. b1, in [from, from + 2^width) of their places
+  template <class F>
+  __device__ __forceinline__ void members(int b0, int b1, u64 from, int width, F f) const {
+    const Sampler c = *this;   // (in registers)
+    const float2 y = bounds(b0, b1);
+    for_tokens<4>(c.row, c.lo, c.hi, [&](const float (&x)[4], int i, int m) {
+      uint32_t hits = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float yh = (c.w.max - fminf(x[k], kFinite)) * c.w.ch;
+        hits |= (k < m && !(yh < y.x) && !(yh >= y.y) && x[k] >= c.w.floor ? 1u : 0u) << k;
+      }
+      while (hits) {
+        const int k = __ffs(hits) - 1;
+        hits &= hits - 1;
+        const float xk = k == 0 ? x[0] : k == 1 ? x[1] : k == 2 ? x[2] : x[3];
+        const u64 p = place_of(xk, i + k);
+        if (p >= from && !((p - from) >> width) && !(c.w.rest && p < c.w.kept)) f(xk, i + k, p);
+      }
+    });
+  }
   // The tokens of bins b0 .. b1 (in [from, from + 2^width) of their places), n in
   // all, in order in the first CTA's list, from the entry that it returns on.
   __device__ __forceinline__ int gather(int b0, int b1, u64 from, int width, int n) {
     if (threadIdx.x == 0) sm.filled = 0;
     __syncthreads();
-    // (a bin's bounds are floats; behind the last one nothing is)
-    const float y0 = ((float)(b0 << shift) - 0.5f) / 1024.f;
-    const float y1 = (b1 + 1) << shift < 65536 ? ((float)((b1 + 1) << shift) - 0.5f) / 1024.f
-                                                     : __int_as_float(0x7fffffff);
-    for_tokens<4>(row, lo, hi, [&](const auto& x, int i) {
-#pragma unroll
-      for (int k = 0; k < (int)(sizeof(x) / sizeof(float)); ++k) {
-        const float yh = (w.max - fminf(x[k], kFinite)) * w.ch;
-        if (yh < y0 || yh >= y1 || !in_row(x[k], i + k)) continue;
-        const u64 p = place_of(x[k], i + k);
-        if (p < from || (p - from) >> width) continue;
-        const int at = atomicAdd(&sm.filled, 1);
-        if (at < kCap) sm.mine[at] = p;
-      }
+    members(b0, b1, from, width, [&](float, int, u64 p) {
+      const int at = atomicAdd(&sm.filled, 1);
+      if (at < kCap) sm.mine[at] = p;
     });
     sync();
     if (rank == 0) {
@@ -590,7 +643,7 @@ struct Sampler {
       for (int j = 0; j < kMaxCluster; ++j) end[j] = j < ctas ? cluster.map_shared_rank(&sm, j)->filled : 0;
 #pragma unroll
       for (int j = 1; j < kMaxCluster; ++j) end[j] += end[j - 1];
-      for (int i = threadIdx.x; i < n; i += kThreads) {
+      for (int i = threadIdx.x; i < min(n, end[kMaxCluster - 1]); i += kThreads) {
         int j = 0, at = 0;
 #pragma unroll
         for (int k = 0; k + 1 < kMaxCluster; ++k)
@@ -611,6 +664,7 @@ struct Sampler {
     }
     return n;
   }
+  // The list's n tokens in descending order of their places, with their weights.
   __device__ __forceinline__ int order(int n) {
     int at = 0;
     if (n <= kCount) {
@@ -626,22 +680,61 @@ struct Sampler {
       at = kCount;
       __syncthreads();
     } else {
-      int size = 2 * kCount;
-      while (size < n) size <<= 1;
-      for (int i = n + threadIdx.x; i < size; i += kThreads) sm.place[i] = 0;
+      // into 1024 parts of their range (of their logits, or indexes where those are equal), and by
+      // counting the larger ones of a part
+      const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+      uint32_t* start = sm.part_c;
+      uint32_t* fill = sm.bins.cnt[0];
+      uint32_t low = 0xffffffffu, top = 0;
+      for (int i = threadIdx.x; i < n; i += kThreads) {
+        const uint32_t k = (uint32_t)(sm.place[i] >> kSampleIndexBits);
+        low = min(low, k);
+        top = max(top, k);
+      }
+      low = __reduce_min_sync(0xffffffffu, low);
+      top = __reduce_max_sync(0xffffffffu, top);
+      if (lane == 0) {
+        sm.warp_c[warp] = low;
+        sm.warp_i[warp] = top;
+      }
+      fill[2 * threadIdx.x] = fill[2 * threadIdx.x + 1] = 0;
       __syncthreads();
-      for (int k = 2; k <= size; k <<= 1)
-        for (int j = k >> 1; j > 0; j >>= 1) {
-          for (int t = threadIdx.x; t < size / 2; t += kThreads) {
-            const int i = 2 * j * (t / j) + t % j;
-            const u64 a = sm.place[i], b = sm.place[i + j];
-            if ((a < b) == ((i & k) == 0)) {
-              sm.place[i] = b;
-              sm.place[i + j] = a;
-            }
-          }
-          __syncthreads();
-        }
+      low = __reduce_min_sync(0xffffffffu, sm.warp_c[lane % kWarps]);
+      top = __reduce_max_sync(0xffffffffu, sm.warp_i[lane % kWarps]);
+      const int width = top > low ? max(32 - __clz(top - low) - kDigit, 0) : kSampleIndexBits - kDigit;
+      const auto part = [&](u64 p) {
+        const uint32_t k = top > low ? (uint32_t)(p >> kSampleIndexBits) - low : (uint32_t)p & kIndexMask;
+        return kBins - 1 - (int)(k >> width);
+      };
+      for (int i = threadIdx.x; i < n; i += kThreads) atomicAdd(&fill[part(sm.place[i])], 1u);
+      __syncthreads();
+      const uint32_t a = fill[2 * threadIdx.x], b = fill[2 * threadIdx.x + 1];
+      uint32_t run = a + b;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += v;
+      }
+      if (lane == 31) sm.warp_i[warp] = run;
+      __syncthreads();
+      run -= a + b;
+      for (int k = 0; k < warp; ++k) run += sm.warp_i[k];
+      start[2 * threadIdx.x] = fill[2 * threadIdx.x] = run;
+      start[2 * threadIdx.x + 1] = fill[2 * threadIdx.x + 1] = run + a;
+      __syncthreads();
+      for (int i = threadIdx.x; i < n; i += kThreads) {
+        const u64 p = sm.place[i];
+        sm.mine[atomicAdd(&fill[part(p)], 1u)] = p;
+      }
+      __syncthreads();
+      for (int i = threadIdx.x; i < n; i += kThreads) {
+        const u64 p = sm.mine[i];
+        const int b0 = start[part(p)], b1 = fill[part(p)];
+        int above = b0;
+        for (int j = b0; j < b1; ++j) above += sm.mine[j] > p;
+        sm.place[above] = p;
+      }
+      __syncthreads();
     }
     for (int i = threadIdx.x; i < n; i += kThreads) {
       float yh, yl;
@@ -656,7 +749,7 @@ struct Sampler {
   // both within what there is): its place and its weight, in the first CTA's memory.
   // All CTAs of the cluster take part; the bins hold weights.
   __device__ __forceinline__ void find_run(uint32_t count, u64 mass) {
-    for (;;) {
+    for (int tries = 0; tries <= 2; ++tries) {   // (two windows hold everything)
       if (rank == 0) find_bin(sm.sum_w, sm.sum_c, sm.before_w, sm.before_c, count, mass, bin0);
       sync();
       const int to = first.bin;
@@ -666,24 +759,27 @@ struct Sampler {
     const int bin = first.bin;
     int n = first.n, width = kPlaceBits;
     u64 from = 0;
-    // more tokens than can be put in order: by the next bits of their places
-    while (n > kCap) {
+    // more tokens than can be put in order: by their places in the bin's range, again by the parts'
+    if (n > kCap) {
+      const float2 y = bounds(bin, bin);
+      // (a little more than the range on both sides)
+      const float room = fabsf(w.max) * 0x1p-20f + y.x / w.ch * 0x1p-18f;
+      const float top = w.max - y.x / w.ch + room, low = w.max - y.y / w.ch - room;
+      if (top < kFinite && low > -kFinite) {   // (the last bin has no lower bound)
+        from = place_of(low, (int)kIndexMask);
+        width = 64 - __clzll((long long)(place_of(top, 0) - from));
+      }
+    }
+    while (n > kCap && width > 0) {
       const int was = width;
       width = max(width - kDigit, 0);
       clear_bins(true);
-      for_tokens<2>(row, lo, hi, [&](const auto& x, int i) {
-#pragma unroll
-        for (int k = 0; k < (int)(sizeof(x) / sizeof(float)); ++k) {
-          float yh, yl;
-          w.orders(x[k], yh, yl);
-          if (bin_of(yh) != bin || !in_row(x[k], i + k)) continue;
-          const u64 p = place_of(x[k], i + k);
-          if (p >= from && !((p - from) >> was)) {
-            const int b[1] = {kBins - 1 - (int)((p - from) >> width)};
-            const u64 v[1] = {weigh(i + k, yh, yl)};
-            add(b, v);
-          }
-        }
+      members(bin, bin, from, was, [&](float x, int i, u64 p) {
+        float yh, yl;
+        w.orders(x, yh, yl);
+        const int b[1] = {kBins - 1 - (int)((p - from) >> width)};
+        const u64 v[1] = {weigh(i, yh, yl)};
+        add(b, v);
       });
       sum_bins<true>(sm.part_w, sm.part_c, &sm.base_w, &sm.base_c);
       if (rank == 0) {
@@ -694,6 +790,7 @@ struct Sampler {
       n = first.n;
       from = first.from;
     }
+    n = min(n, kCap);   // (places are all different)
     const int at = gather(bin, bin, from, width, n);
     if (rank == 0) {
       Scan<kThreads> sc{sm, at, n};
@@ -830,17 +927,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
 
   // the largest logit, the first of them
   float best = -INFINITY;
-  int best_i = lo;
+  int best_i = hi;
   bool bad = false;
-  for_tokens<4>(row, lo, hi, [&](const auto& x, int i) {
+  for_tokens<4>(row, lo, hi, [&](const float (&x)[4], int i, int n) {
 #pragma unroll
-    for (int k = 0; k < (int)(sizeof(x) / sizeof(float)); ++k) {
-      if (x[k] > best) {
-        best = x[k];
-        best_i = i + k;
+    for (int k = 0; k < 4; ++k)
+      if (k < n) {
+        if (x[k] > best || (x[k] == best && i + k < best_i)) {   // (the ends come after the middle)
+          best = x[k];
+          best_i = i + k;
+        }
+        bad |= x[k] != x[k];
       }
-      bad |= x[k] != x[k];
-    }
   });
   bad |= !(heat == 0.f || (heat >= 0x1p-64f && heat <= 0x1p64f)) || min_p != min_p || want.top_p != want.top_p ||
          !(want.u >= 0.f && want.u < 1.f) || !(want.u_next >= 0.f && want.u_next < 1.f);
@@ -1030,9 +1128,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   if (dist) {
     const float2 sum = pair_of(total);
     const float ih = 1.f / sum.x, il = (fmaf(-ih, sum.x, 1.f) - ih * sum.y) * ih;
-    for_tokens<2>(row, lo, hi, [&](const auto& x, int i) {
+    for_tokens<1>(row, lo, hi, [&](const float (&x)[4], int i, int n) {
 #pragma unroll
-      for (int k = 0; k < (int)(sizeof(x) / sizeof(float)); ++k) {
+      for (int k = 0; k < 4; ++k) {
         float v = 0.f, yh, yl;
         s.w.orders(x[k], yh, yl);
         if (x[k] >= s.w.floor && yh < 152.f && place_of(x[k], i + k) >= kept) {
@@ -1045,7 +1143,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
           const int q = min(m, 100);
           v = v * __int_as_float((127 - q) << 23) * __int_as_float((127 - (m - q)) << 23);
         }
-        dist[i + k] = v;
+        if (k < n) dist[i + k] = v;
       }
     });
   }
@@ -1079,7 +1177,6 @@ __global__ void __launch_bounds__(256) accept_kernel(const SampleParams p) {
 template <class T>
 cudaError_t launch(const SampleParams& p, int ctas, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Smem));
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.rows * ctas);
