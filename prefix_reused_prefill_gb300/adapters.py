@@ -14,7 +14,7 @@ import numpy as np
 import torch
 
 from .kvr import KvrAdapterSite, KvrError, load_library
-from .sampling import _On, _check, _raw_stream, _vec
+from .sampling import _check, _elsewhere, _raw_stream, _vec
 
 MAX_RANK = 128
 _TYPES = {torch.bfloat16: 0, torch.float16: 1}
@@ -65,26 +65,27 @@ class Adapters:
                   base: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """base (zeros of x's type if None) + the sequences' adapters of x [rows][k].  cu_rows [n_seq + 1] and which
         [n_seq] are device int32; base and out are [rows][sum of cols] of x's type or float32, and may be one."""
-        rows, types = x.shape[0] if x.dim() == 2 else -1, (self.dtype, torch.float32)
+        if _elsewhere(self._index, stream):   # (memory that the stream may write at once)
+            with torch.cuda.device(self._index), torch.cuda.stream(stream):
+                return self.kvr_adapt(x, cu_rows, which, base, out)
+        types = (self.dtype, torch.float32)
         xs = self._rows("x", x, self.k, (self.dtype,))
-        n_seq = which.numel()
+        rows, n_seq = x.shape[0], which.numel()
         wp, cp = _vec("which", which, n_seq, torch.int32, self._index), _vec("cu_rows", cu_rows, n_seq + 1, torch.int32,
                                                                              self._index)
         bp, bs = None, self.n
         if base is not None:
             bs, bp = self._rows("base", base, self.n, types), base.data_ptr()
-        like = base if base is not None else out
-        dtype = self.dtype if like is None else like.dtype
-        with _On(self._index), torch.cuda.stream(stream):   # (where one is given) memory that it may write at once
-            if out is None:
-                out = torch.empty((rows, self.n), dtype=dtype, device=self.device)
-            os = self._rows("out", out, self.n, (dtype,) if dtype in types else types)
-            if out.shape[0] != rows or (base is not None and base.shape[0] != rows):
-                raise KvrError(-1, f"base and out must have x's {rows} rows")
-            wb = self.lib.kvr_adapt_work_bytes(ctypes.byref(self.site), rows)
-            work = torch.empty(wb, dtype=torch.uint8, device=self.device)
-            _check(self.lib, self.lib.kvr_adapt(
-                ctypes.byref(self.site), x.data_ptr(), xs, cp, wp, n_seq, rows, bp, bs, out.data_ptr(), os,
-                2 if dtype is torch.float32 else self.site.type, work.data_ptr(), wb,
-                stream.cuda_stream if stream is not None else _raw_stream(self._index)))
+        if out is None:
+            out = torch.empty((rows, self.n), dtype=self.dtype if base is None else base.dtype, device=self.device)
+        os = self._rows("out", out, self.n, types if base is None else (base.dtype,))
+        if out.shape[0] != rows or (base is not None and base.shape[0] != rows):
+            raise KvrError(-1, f"base and out must have x's {rows} rows")
+        wb = self.lib.kvr_adapt_work_bytes(self.site, rows)
+        work = torch.empty(wb, dtype=torch.uint8, device=self.device)
+        rc = self.lib.kvr_adapt(self.site, x.data_ptr(), xs, cp, wp, n_seq, rows, bp, bs, out.data_ptr(), os,
+                                2 if out.dtype is torch.float32 else self.site.type, work.data_ptr(), wb,
+                                _raw_stream(self._index))
+        if rc:
+            _check(self.lib, rc)
         return out

@@ -9,10 +9,14 @@
 // rows of x or s as their N side.  Lanes load operands straight from global
 // memory, 16 or 8 bytes each: which inputs share a fragment does not matter as
 // long as both operands agree.
+#include <cooperative_groups.h>
+
 #include <algorithm>
 #include <type_traits>
 
 #include "kvr_batch.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace kvr {
 namespace {
@@ -51,6 +55,14 @@ template <class T>
 __device__ __forceinline__ T to(float x) {
   if constexpr (std::is_same<T, __half>::value) return __float2half_rn(x);
   else return __float2bfloat16_rn(x);
+}
+
+// The power of two by which a row whose largest element is `big` is held in terms of T
+// (`down` scales it to below 2), and NaN in `down` for a row that is not finite.
+__device__ __forceinline__ float scale_of(float big, float& down) {
+  const int e = min(max((int)(__float_as_uint(big) >> 23), 27), 253) - 127;
+  down = big < INFINITY ? __int_as_float((127 - e) << 23) : __int_as_float(0x7fffffff);
+  return __int_as_float((e + 127) << 23);
 }
 
 constexpr int kNone = -1;      // a row without an adapter
@@ -220,9 +232,8 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(const AdaptParams p) {
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-      // (a row that is not finite is NaN as a whole)
-      const int e = min(max((int)(__float_as_uint(big) >> 23), 27), 253) - 127;
-      const float down = big < INFINITY ? __int_as_float((127 - e) << 23) : __int_as_float(0x7fffffff);
+      float down;
+      const float up = scale_of(big, down);
 #pragma unroll
       for (int i = 0; i < KVR_MAX_RANK / 32; ++i) {
         const int j = lane + 32 * i;
@@ -235,7 +246,7 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(const AdaptParams p) {
             x -= from(h);
           }
       }
-      if (lane == 0) factor[r] = rows.ad[r].scale * __int_as_float((e + 127) << 23);
+      if (lane == 0) factor[r] = rows.ad[r].scale * up;
     }
   }
   __syncthreads();
@@ -291,6 +302,417 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(const AdaptParams p) {
   }
 }
 
+// ---------------------------------------------------------------- many rows a sequence
+// Tiles of 64 rows of one sequence.  shrink_tiles_kernel streams x and A through
+// shared memory (a cluster cuts the inputs, its CTAs' sums are joined in distributed
+// shared memory) and leaves s in terms of T; expand_tiles_kernel multiplies them
+// with 64 x 128 outputs' B while base is on its way.
+constexpr int TR = 64;
+constexpr int kStep = 64;       // inputs of a stage: 128 bytes a row
+constexpr int kStages = 3;
+constexpr int kMaxCluster = 8;
+constexpr int kTileN = 128;     // outputs of an expand CTA
+
+__host__ __device__ inline int round16(int r) { return (r + 15) & ~15; }
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool valid) {
+  const int bytes = valid ? 16 : 0;   // (0: zeros, nothing is read)
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+struct Tile {
+  int row0, rows;      // 0 rows: none
+  int id;              // adapter, or kNone
+  kvr_adapter ad;
+};
+// Tile `t` of the batch: sequences in order, each in tiles of TR rows.
+__device__ __forceinline__ void find_tile(const AdaptParams& p, int t, Tile& tile) {
+  __shared__ int warp_sum[kWarps];
+  constexpr int kPer = kAdaptMaxSeqs / kThreads;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int per = (p.n_seq + kThreads - 1) / kThreads;   // sequences a thread, 1 .. kPer
+  const int b0 = threadIdx.x * per;
+  if (threadIdx.x == 0) tile.rows = 0;
+  int n[kPer], sum = 0;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    n[k] = 0;
+    if (k < per && b0 + k < p.n_seq) {
+      const int r0 = max(p.cu[b0 + k], 0), r1 = min(p.cu[b0 + k + 1], p.rows);
+      n[k] = r1 > r0 ? (r1 - r0 + TR - 1) / TR : 0;
+    }
+    sum += n[k];
+  }
+  int run = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, run, o);
+    if (lane >= o) run += v;
+  }
+  if (lane == 31) warp_sum[warp] = run;
+  __syncthreads();
+  int at = run - sum;
+  for (int k = 0; k < warp; ++k) at += warp_sum[k];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    if (t >= at && t < at + n[k]) {
+      const int b = b0 + k;
+      const int r0 = max(p.cu[b], 0), r1 = min(p.cu[b + 1], p.rows);
+      tile.row0 = r0 + (t - at) * TR;
+      tile.rows = min(r1 - tile.row0, TR);
+      int id = p.which[b];
+      if (id < 0 || id >= p.site.n_adapters) id = kNone;
+      if (id != kNone) {
+        const kvr_adapter e = p.site.table[id];
+        if (e.rank < 8 || e.rank > p.site.max_rank || e.rank % 8 || !e.a || !e.b) id = kNone;
+        tile.ad = e;
+      }
+      tile.id = id;
+    }
+    at += n[k];
+  }
+  __syncthreads();
+}
+
+// The low-rank products of the tiles: terms [k][row][part * round16(max_rank)] and
+// a factor for each row and part, behind one another in p.part.
+struct Terms {
+  int ld, rows, count;
+  uint8_t* base;
+  __host__ __device__ Terms(const AdaptParams& p, int count_)
+      : ld(p.site.n_parts * round16(p.site.max_rank)), rows(p.rows), count(count_),
+        base(reinterpret_cast<uint8_t*>(p.part)) {}
+  template <class T>
+  __device__ __forceinline__ T* term(int k, int row) const {
+    return reinterpret_cast<T*>(base) + ((long long)k * rows + row) * ld;
+  }
+  __device__ __forceinline__ float* factor(int row) const {
+    return reinterpret_cast<float*>(base + (long long)count * rows * ld * 2) + row * 3;
+  }
+  __host__ __device__ size_t bytes() const { return (size_t)count * rows * ld * 2 + (size_t)rows * 12; }
+};
+
+// One chunk of NC stacked rows of A (all parts, or one) of one tile and one part of the inputs.
+template <class T, int NC, int TERMS>
+__global__ void __launch_bounds__(kThreads) shrink_tiles_kernel(const AdaptParams p, int ks) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ Tile tile;
+  constexpr int kXBytes = TR * 128, kStage = kXBytes + NC * 128;
+  constexpr int kNT = NC / 32;    // tiles of 8 ranks a warp
+  constexpr int kLd = NC + 4;
+  static_assert(TR * kLd * 4 <= kStages * kStage, "the sums fit where the stages were");
+  dev::pdl_trigger();
+  dev::pdl_wait();
+  const int part_k = blockIdx.x % ks;
+  find_tile(p, blockIdx.x / ks, tile);
+  if (tile.rows == 0 || tile.id == kNone) return;   // (the whole cluster)
+  const int rank = tile.ad.rank;
+  const bool whole = gridDim.z == 1;
+  const int q0 = whole ? 0 : blockIdx.z * rank, nq = whole ? p.site.n_parts * rank : rank;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int wr = warp & 1, wn = warp >> 1;
+  const int K = p.site.k, steps = (K + kStep - 1) / kStep;
+  const int s0 = (int)((long long)steps * part_k / ks), s1 = (int)((long long)steps * (part_k + 1) / ks);
+  const uint32_t base = dev::smem_u32(smem);
+  const T* x = static_cast<const T*>(p.x) + p.x_stride * tile.row0;
+  const T* A = static_cast<const T*>(tile.ad.a) + (long long)q0 * K;
+  auto load = [&](int s) {
+    const uint32_t st = base + (s - s0) % kStages * kStage;
+    for (int i = threadIdx.x; i < (TR + NC) * 8; i += kThreads) {
+      const int r = i >> 3, c = i & 7, k = s * kStep + 8 * c;
+      if (r < TR)
+        cp16(st + dev::swz128(r, c), r < tile.rows && k < K ? x + p.x_stride * r + k : x, r < tile.rows && k < K);
+      else
+        cp16(st + kXBytes + dev::swz128(r - TR, c), r - TR < nq && k < K ? A + (long long)(r - TR) * K + k : A,
+             r - TR < nq && k < K);
+    }
+  };
+  float acc[2][kNT][4];
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int n = 0; n < kNT; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.f;
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) {
+    if (s0 + i < s1) load(s0 + i);
+    cp_commit();
+  }
+  for (int s = s0; s < s1; ++s) {
+    cp_wait<kStages - 2>();
+    __syncthreads();
+    if (s + kStages - 1 < s1) load(s + kStages - 1);
+    cp_commit();
+    const uint32_t st = base + (s - s0) % kStages * kStage;
+#pragma unroll
+    for (int kk = 0; kk < kStep / 16; ++kk) {
+      uint32_t a[2][4];
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const int r = wr * 32 + m * 16 + (lane & 15);
+        dev::ldmatrix_x4(st + dev::swz128(r, 2 * kk + (lane >> 4)), a[m][0], a[m][1], a[m][2], a[m][3]);
+        if (std::is_same<T, __nv_bfloat16>::value && p.x16)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) a[m][e] = bf16_of_half2(a[m][e]);
+      }
+#pragma unroll
+      for (int n = 0; n < kNT; n += 2) {
+        uint32_t b[4];   // ranks 8 n .. + 15: (first eight, low and high inputs), (second eight, ...)
+        const int r = wn * (NC / 4) + 8 * n + (lane & 7) + ((lane >> 4) << 3);
+        dev::ldmatrix_x4(st + kXBytes + dev::swz128(r, 2 * kk + ((lane >> 3) & 1)), b[0], b[1], b[2], b[3]);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          mma<T>(acc[m][n], a[m][0], a[m][1], a[m][2], a[m][3], b[0], b[1]);
+          mma<T>(acc[m][n + 1], a[m][0], a[m][1], a[m][2], a[m][3], b[2], b[3]);
+        }
+      }
+    }
+  }
+  cp_wait<0>();
+  __syncthreads();
+  // the cluster's sums, a share of the rows each, a warp a row
+  float* sums = reinterpret_cast<float*>(smem);
+  const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int n = 0; n < kNT; ++n) {
+      float* d = sums + (wr * 32 + m * 16 + g) * kLd + wn * (NC / 4) + 8 * n + 2 * t;
+      d[0] = acc[m][n][0];
+      d[1] = acc[m][n][1];
+      d[8 * kLd] = acc[m][n][2];
+      d[8 * kLd + 1] = acc[m][n][3];
+    }
+  const cg::cluster_group cluster = cg::this_cluster();
+  if (ks > 1) cluster.sync();
+  else __syncthreads();
+  const float* from_[kMaxCluster];
+#pragma unroll
+  for (int j = 0; j < kMaxCluster; ++j) from_[j] = cluster.map_shared_rank(sums, j < ks ? j : 0);
+  const Terms terms(p, TERMS);
+  const int r0 = TR * part_k / ks, r1 = min(TR * (part_k + 1) / ks, tile.rows);
+  const int parts = whole ? p.site.n_parts : 1;
+  for (int r = r0 + warp; r < r1; r += kWarps)
+    for (int j = 0; j < parts; ++j) {
+      float v[KVR_MAX_RANK / 32], big = 0.f;
+#pragma unroll
+      for (int i = 0; i < KVR_MAX_RANK / 32; ++i) {
+        const int q = lane + 32 * i;
+        v[i] = 0.f;
+        if (q < rank) {
+#pragma unroll
+          for (int c = 0; c < kMaxCluster; ++c)
+            if (c < ks) v[i] += from_[c][r * kLd + j * rank + q];
+        }
+        big = fmaxf(big, fabsf(v[i]));
+        if (v[i] != v[i]) big = INFINITY;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+      float down;
+      const float up = scale_of(big, down);
+      const int pj = whole ? j : blockIdx.z;
+#pragma unroll
+      for (int i = 0; i < KVR_MAX_RANK / 32; ++i) {
+        const int q = lane + 32 * i;
+        float y = v[i] * down;
+        if (q < round16(rank))
+#pragma unroll
+          for (int k = 0; k < TERMS; ++k) {
+            const T h = to<T>(y);
+            terms.term<T>(k, tile.row0 + r)[pj * round16(p.site.max_rank) + q] = h;
+            y -= from(h);
+          }
+      }
+      if (lane == 0) terms.factor(tile.row0 + r)[pj] = tile.ad.scale * up;
+    }
+  if (ks > 1) cluster.sync();   // (the others' sums are read)
+}
+
+template <class T, class O, int TERMS>
+__global__ void __launch_bounds__(kThreads, 2) expand_tiles_kernel(const AdaptParams p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ Tile tile;
+  __shared__ float factor[TR];
+  dev::pdl_trigger();
+  dev::pdl_wait();
+  find_tile(p, blockIdx.x, tile);
+  if (tile.rows == 0 || (tile.id == kNone && p.base == p.out)) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int wr = warp & 1, wn = warp >> 1;
+  int part = 0, col = blockIdx.y, left = 0;
+  for (;; ++part) {
+    const int tiles = (p.site.cols[part] + kTileN - 1) / kTileN;
+    if (col < tiles) break;
+    col -= tiles;
+    left += p.site.cols[part];
+  }
+  col *= kTileN;
+  const int cols = min(kTileN, p.site.cols[part] - col);
+  const bool adapted = tile.id != kNone;
+  const int rank = adapted ? tile.ad.rank : 0, r16 = round16(rank), pitch = 2 * r16 + 16;
+  constexpr int kOPitch = kTileN * (int)sizeof(O) + 16, kOChunk = 16 / (int)sizeof(O);
+  const uint32_t so = dev::smem_u32(smem), sb = so + TR * kOPitch, ss = sb + kTileN * pitch;
+  const Terms terms(p, TERMS);
+  if (adapted) {
+    const T* B = static_cast<const T*>(tile.ad.b) + (long long)(left + col) * rank;
+    const int per = r16 / 8;
+    for (int i = threadIdx.x; i < kTileN * per; i += kThreads) {
+      const int r = i / per, c = i % per;
+      const bool in = r < cols && 8 * c < rank;
+      cp16(sb + r * pitch + 16 * c, in ? B + (long long)r * rank + 8 * c : B, in);
+    }
+#pragma unroll
+    for (int k = 0; k < TERMS; ++k)
+      for (int i = threadIdx.x; i < TR * per; i += kThreads) {
+        const int r = i / per, c = i % per;
+        const T* src = terms.term<T>(k, tile.row0 + min(r, tile.rows - 1)) + part * round16(p.site.max_rank) + 8 * c;
+        cp16(ss + (k * TR + r) * pitch + 16 * c, src, r < tile.rows);
+      }
+    if (threadIdx.x < tile.rows) factor[threadIdx.x] = terms.factor(tile.row0 + threadIdx.x)[part];
+  }
+  cp_commit();
+  const long long at = left + col;
+  if (p.base) {
+    const O* base = static_cast<const O*>(p.base) + p.base_stride * tile.row0 + at;
+    for (int i = threadIdx.x; i < TR * (kTileN / kOChunk); i += kThreads) {
+      const int r = i / (kTileN / kOChunk), c = i % (kTileN / kOChunk) * kOChunk;
+      const bool in = r < tile.rows && c < cols;
+      cp16(so + r * kOPitch + c * (int)sizeof(O), in ? base + p.base_stride * r + c : base, in);
+    }
+  }
+  cp_commit();
+  float acc[2][4][4];
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int n = 0; n < 4; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.f;
+  cp_wait<1>();
+  __syncthreads();
+#pragma unroll 2
+  for (int kk = 0; kk < r16 / 16; ++kk) {
+    uint32_t b[2][4];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const int r = wn * 32 + 16 * n + (lane & 7) + ((lane >> 4) << 3);
+      dev::ldmatrix_x4(sb + r * pitch + 32 * kk + 16 * ((lane >> 3) & 1), b[n][0], b[n][1], b[n][2], b[n][3]);
+    }
+#pragma unroll
+    for (int k = TERMS - 1; k >= 0; --k)
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        uint32_t a[4];
+        const int r = wr * 32 + m * 16 + (lane & 15);
+        dev::ldmatrix_x4(ss + (k * TR + r) * pitch + 32 * kk + 16 * (lane >> 4), a[0], a[1], a[2], a[3]);
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+          mma<T>(acc[m][n], a[0], a[1], a[2], a[3], b[n >> 1][2 * (n & 1)], b[n >> 1][2 * (n & 1) + 1]);
+      }
+  }
+  cp_wait<0>();
+  __syncthreads();
+  // into base's place in shared memory, then out in whole rows
+  if (adapted)
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = wr * 32 + m * 16 + 8 * h + g;
+        if (r >= tile.rows) continue;
+        const float f = factor[r];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          O* o = reinterpret_cast<O*>(smem + r * kOPitch) + wn * 32 + 8 * n + 2 * t;
+          const float y0 = acc[m][n][2 * h] * f, y1 = acc[m][n][2 * h + 1] * f;
+          if constexpr (std::is_same<O, float>::value) {
+            float2 v = p.base ? *reinterpret_cast<float2*>(o) : make_float2(0.f, 0.f);
+            v.x += y0;
+            v.y += y1;
+            *reinterpret_cast<float2*>(o) = v;
+          } else {
+            o[0] = to<O>((p.base ? from(o[0]) : 0.f) + y0);
+            o[1] = to<O>((p.base ? from(o[1]) : 0.f) + y1);
+          }
+        }
+      }
+  __syncthreads();
+  O* out = static_cast<O*>(p.out) + p.out_stride * tile.row0 + at;
+  for (int i = threadIdx.x; i < TR * (kTileN / kOChunk); i += kThreads) {
+    const int r = i / (kTileN / kOChunk), c = i % (kTileN / kOChunk) * kOChunk;
+    if (r < tile.rows && c < cols) {
+      uint4 v = *reinterpret_cast<const uint4*>(smem + r * kOPitch + c * sizeof(O));
+      if (!adapted && !p.base) v = make_uint4(0u, 0u, 0u, 0u);
+      *reinterpret_cast<uint4*>(out + p.out_stride * r + c) = v;
+    }
+  }
+}
+
+template <class O>
+int expand_tiles_smem(int max_rank, int terms) {
+  return TR * (kTileN * (int)sizeof(O) + 16) + (kTileN + terms * TR) * (2 * round16(max_rank) + 16);
+}
+template <int NC>
+constexpr int shrink_tiles_smem() {
+  return kStages * (TR + NC) * 128;
+}
+
+template <class T, int NC, int TERMS>
+cudaError_t launch_shrink_tiles(const AdaptParams& p, int tiles, int chunks, int sms, cudaStream_t st) {
+  // CTAs of a tile: as many as fill the SMs twice, with 256 inputs each at least
+  int ks = 1;
+  while (ks < kMaxCluster && tiles * chunks * ks * 2 <= 2 * sms && p.site.k >= 512 * ks) ks *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * ks), 1, (unsigned)chunks);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = shrink_tiles_smem<NC>();
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {(unsigned)ks, 1, 1};
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, shrink_tiles_kernel<T, NC, TERMS>, p, ks);
+}
+
+template <class T, class O, int TERMS>
+cudaError_t launch_tiles(const AdaptParams& p, int sms, cudaStream_t st) {
+  const int tiles = p.rows / TR + std::min(p.n_seq, p.rows);   // at most
+  const int stacked = p.site.n_parts * p.site.max_rank;
+  cudaError_t e = stacked <= 64    ? launch_shrink_tiles<T, 64, TERMS>(p, tiles, 1, sms, st)
+                  : stacked <= 128 ? launch_shrink_tiles<T, 128, TERMS>(p, tiles, 1, sms, st)
+                  : stacked <= 192 ? launch_shrink_tiles<T, 192, TERMS>(p, tiles, 1, sms, st)
+                                   : launch_shrink_tiles<T, 128, TERMS>(p, tiles, p.site.n_parts, sms, st);
+  if (e != cudaSuccess) return e;
+  int cols = 0;
+  for (int j = 0; j < p.site.n_parts; ++j) cols += (p.site.cols[j] + kTileN - 1) / kTileN;
+  return launch_k(expand_tiles_kernel<T, O, TERMS>, dim3(tiles, cols), dim3(kThreads),
+                  expand_tiles_smem<O>(p.site.max_rank, TERMS), st, p);
+}
+
+template <class T, int TERMS>
+cudaError_t setup_shrink() {
+  cudaError_t e = cudaFuncSetAttribute(shrink_tiles_kernel<T, 64, TERMS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       shrink_tiles_smem<64>());
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(shrink_tiles_kernel<T, 128, TERMS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             shrink_tiles_smem<128>());
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(shrink_tiles_kernel<T, 192, TERMS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             shrink_tiles_smem<192>());
+  return e;
+}
+template <class T, class O, int TERMS>
+cudaError_t setup_expand() {
+  return cudaFuncSetAttribute(expand_tiles_kernel<T, O, TERMS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              expand_tiles_smem<O>(KVR_MAX_RANK, TERMS));
+}
+
 template <class T>
 cudaError_t launch(const AdaptParams& p, cudaStream_t st) {
   const int blocks = (p.rows + R - 1) / R;
@@ -304,6 +726,9 @@ cudaError_t launch(const AdaptParams& p, cudaStream_t st) {
   return launch_k(expand_kernel<T, float, kTerms>, grid, kThreads, 0, st, p);
 }
 
+// Rows of a sequence, on average, from which tiles of 64 rows pay.
+constexpr int kManyRows = 24;
+
 int adapt_split(const kvr_adapter_site& s, int rows, int sms) {
   const int blocks = (rows + R - 1) / R;
   const int most = std::max(1, std::min(kAdaptMaxSplit, s.k / 128));
@@ -312,12 +737,33 @@ int adapt_split(const kvr_adapter_site& s, int rows, int sms) {
 
 }  // namespace
 
+cudaError_t adapt_setup() {
+  cudaError_t e = setup_shrink<__nv_bfloat16, 2>();
+  if (e == cudaSuccess) e = setup_shrink<__nv_bfloat16, 3>();
+  if (e == cudaSuccess) e = setup_shrink<__half, 2>();
+  if (e == cudaSuccess) e = setup_expand<__nv_bfloat16, __nv_bfloat16, 2>();
+  if (e == cudaSuccess) e = setup_expand<__nv_bfloat16, float, 3>();
+  if (e == cudaSuccess) e = setup_expand<__half, __half, 2>();
+  if (e == cudaSuccess) e = setup_expand<__half, float, 2>();
+  return e;
+}
+
 size_t adapt_work_bytes(const kvr_adapter_site& s, int rows) {
-  // (of any number of SMs)
-  return (size_t)adapt_split(s, rows, 1024) * rows * s.n_parts * s.max_rank * sizeof(float);
+  // (of any number of SMs, for few or many rows a sequence)
+  AdaptParams p = {};
+  p.site = s;
+  p.rows = rows;
+  return std::max((size_t)adapt_split(s, rows, 1024) * rows * s.n_parts * s.max_rank * sizeof(float),
+                  Terms(p, 3).bytes());
 }
 
 cudaError_t launch_adapt(AdaptParams p, int sms, cudaStream_t st) {
+  if (p.rows >= kManyRows * (long long)p.n_seq) {
+    if (p.site.type == KVR_ACT_F16)
+      return p.out_type == KVR_ACT_F32 ? launch_tiles<__half, float, 2>(p, sms, st) : launch_tiles<__half, __half, 2>(p, sms, st);
+    return p.out_type == KVR_ACT_F32 ? launch_tiles<__nv_bfloat16, float, 3>(p, sms, st)
+                                     : launch_tiles<__nv_bfloat16, __nv_bfloat16, 2>(p, sms, st);
+  }
   p.ksplit = adapt_split(p.site, p.rows, std::min(sms, 1024));
   return p.site.type == KVR_ACT_F16 ? launch<__half>(p, st) : launch<__nv_bfloat16>(p, st);
 }

@@ -1176,8 +1176,6 @@ __global__ void __launch_bounds__(256) accept_kernel(const SampleParams p) {
 
 template <class T>
 cudaError_t launch(const SampleParams& p, int ctas, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Smem));
-  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.rows * ctas);
   cfg.blockDim = dim3(kThreads);
@@ -1194,6 +1192,15 @@ cudaError_t launch(const SampleParams& p, int ctas, cudaStream_t st) {
 }
 
 }  // namespace
+
+cudaError_t sample_setup() {
+  void (*ks[3])(SampleParams) = {sample_kernel<float>, sample_kernel<__nv_bfloat16>, sample_kernel<__half>};
+  for (auto k : ks) {
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Smem));
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
 
 cudaError_t launch_sample(const SampleParams& p, int sms, cudaStream_t st) {
   // CTAs of a row: as many as two on each SM, with 2048 tokens each at least

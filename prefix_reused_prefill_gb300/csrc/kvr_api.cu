@@ -1625,6 +1625,8 @@ int kvr_ctx_create(const kvr_config* cfg, void* kv_arena, size_t arena_bytes, vo
   if (e == cudaSuccess) e = gemm_tc_setup();
   if (e == cudaSuccess) e = attn_setup();
   if (e == cudaSuccess) e = attn_tc_setup();
+  if (e == cudaSuccess) e = sample_setup();
+  if (e == cudaSuccess) e = adapt_setup();
   // the persistent pass is optional: without room for it, small m keeps the
   // per-step launches
   if (e == cudaSuccess && pass_setup() != cudaSuccess) {

@@ -1,6 +1,7 @@
 // C ABI of what the requests of one batch differ by (include/kvr.h): checks of
 // arguments, then the launches of k_sample.cu and k_adapt.cu.
 #include <algorithm>
+#include <atomic>
 #include <cstdarg>
 #include <cstdio>
 
@@ -21,11 +22,18 @@ int fail(int code, const char* fmt, ...) {
 }
 int cuda_fail(cudaError_t e, const char* what) { return fail(KVR_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e)); }
 
-// SMs of the current device
+// SMs of the current device, whose kernels are set up on its first call
+constexpr int kMaxDevices = 64;
+std::atomic<int> g_sms[kMaxDevices];
 cudaError_t device_sms(int* sms) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  if (dev < kMaxDevices && (*sms = g_sms[dev].load(std::memory_order_acquire)) != 0) return cudaSuccess;
+  e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) e = sample_setup();
+  if (e == cudaSuccess) e = adapt_setup();
+  if (e == cudaSuccess && dev < kMaxDevices) g_sms[dev].store(*sms, std::memory_order_release);
   return e;
 }
 

@@ -32,6 +32,7 @@ struct SampleParams {
 };
 constexpr int kStays = -2;
 
+cudaError_t sample_setup();   // of the current device, before its first launch
 cudaError_t launch_sample(const SampleParams& p, int sms, cudaStream_t st);
 
 constexpr int kAdaptMaxSeqs = 2048;
@@ -52,6 +53,7 @@ struct AdaptParams {
   float* part;             // [ksplit][rows][n_parts * max_rank] parts of the low-rank products
   int ksplit;
 };
+cudaError_t adapt_setup();    // of the current device, before its first launch
 bool adapter_site_ok(const kvr_adapter_site* s);
 size_t adapt_work_bytes(const kvr_adapter_site& s, int rows);
 cudaError_t launch_adapt(AdaptParams p, int sms, cudaStream_t st);

@@ -16,23 +16,14 @@ import torch
 from .kvr import KvrError, KvrSampling, load_library
 
 _TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_current_device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream   # the current stream's handle (a Stream object costs 2 us)
 Setting = Optional[Union[torch.Tensor, float, int]]
 
 
-class _On:
-    """The tensors' device for the length of a call, where another one is current."""
-
-    def __init__(self, index: int):
-        self.other = torch.cuda.device(index) if index != torch.cuda.current_device() else None
-
-    def __enter__(self):
-        if self.other is not None:
-            self.other.__enter__()
-
-    def __exit__(self, *args):
-        if self.other is not None:
-            self.other.__exit__(*args)
+def _elsewhere(index: int, stream) -> bool:
+    """Whether a call has to make the tensors' device, or the given stream, the current one first."""
+    return stream is not None or _current_device() != index
 
 
 def _check(lib, rc: int):
@@ -56,17 +47,15 @@ def _vec(name: str, x: torch.Tensor, n: int, dtype, index: int) -> int:
     return x.data_ptr()
 
 
-def _settings(n: int, index: int, **given):
-    st, keep = KvrSampling(), []
-    for name, x in given.items():
-        if x is None:
-            continue
-        dtype = torch.int32 if name == "top_k" else torch.float32
-        if not isinstance(x, torch.Tensor):
-            x = torch.full((n,), x, dtype=dtype, device=index)
-        setattr(st, name, _vec(name, x, n, dtype, index))
-        keep.append(x)
-    return st, keep
+def _settings(n: int, index: int, temperature, top_k, min_p, top_p):
+    """The struct, and what it points to (kept until the call is made)."""
+    keep = [None if x is None else x if isinstance(x, torch.Tensor) else torch.full((n,), x, dtype=t, device=index)
+            for x, t in ((temperature, torch.float32), (top_k, torch.int32), (min_p, torch.float32), (top_p, torch.float32))]
+    t, k, m, p = keep
+    return KvrSampling(None if t is None else _vec("temperature", t, n, torch.float32, index),
+                       None if k is None else _vec("top_k", k, n, torch.int32, index),
+                       None if m is None else _vec("min_p", m, n, torch.float32, index),
+                       None if p is None else _vec("top_p", p, n, torch.float32, index)), keep
 
 
 def _logits(x: torch.Tensor) -> Tuple[int, int]:
@@ -81,25 +70,26 @@ def kvr_sample(logits: torch.Tensor, u: torch.Tensor, temperature: Setting = Non
     """A token of each row of logits [rows][vocab] (fp32, bf16 or fp16) by u [rows] in [0, 1): (token int32, its
     probability float32), and with ``dist`` (True, or a float32 tensor to fill) every token's probability.  Settings:
     [rows].  A row without a distribution has token -1."""
-    lib = load_library()
     index, ls = _logits(logits)
+    if _elsewhere(index, stream):   # (memory that the stream may write at once)
+        with torch.cuda.device(index), torch.cuda.stream(stream):
+            return kvr_sample(logits, u, temperature, top_k, min_p, top_p, dist)
+    lib = load_library()
     rows, vocab = logits.shape
     up = _vec("u", u, rows, torch.float32, index)
-    with _On(index), torch.cuda.stream(stream):   # (where one is given) memory that it may write at once
-        st, keep = _settings(rows, index, temperature=temperature, top_k=top_k, min_p=min_p, top_p=top_p)
-        token = torch.empty(rows, dtype=torch.int32, device=logits.device)
-        prob = torch.empty(rows, dtype=torch.float32, device=logits.device)
-        ds = vocab
+    st, keep = _settings(rows, index, temperature, top_k, min_p, top_p)
+    token = torch.empty(rows, dtype=torch.int32, device=logits.device)
+    prob = torch.empty(rows, dtype=torch.float32, device=logits.device)
+    ds, dp = vocab, None
+    if dist is not False:
         if dist is True:
             dist = torch.empty((rows, vocab), dtype=torch.float32, device=logits.device)
-        elif dist is False:
-            dist = None
-        else:
-            ds = _rows("dist", dist, (rows, vocab), (torch.float32,), index)
-        _check(lib, lib.kvr_sample(logits.data_ptr(), _TYPES[logits.dtype], ls, rows, vocab, ctypes.byref(st), up,
-                                   token.data_ptr(), prob.data_ptr(), None if dist is None else dist.data_ptr(), ds,
-                                   stream.cuda_stream if stream is not None else _raw_stream(index)))
-    return (token, prob) if dist is None else (token, prob, dist)
+        ds, dp = _rows("dist", dist, (rows, vocab), (torch.float32,), index), dist.data_ptr()
+    rc = lib.kvr_sample(logits.data_ptr(), _TYPES[logits.dtype], ls, rows, vocab, st, up, token.data_ptr(),
+                        prob.data_ptr(), dp, ds, _raw_stream(index))
+    if rc:
+        _check(lib, rc)
+    return (token, prob) if dp is None else (token, prob, dist)
 
 
 def kvr_accept(logits: torch.Tensor, tokens: torch.Tensor, cu_rows: torch.Tensor, u: torch.Tensor,
@@ -109,24 +99,27 @@ def kvr_accept(logits: torch.Tensor, tokens: torch.Tensor, cu_rows: torch.Tensor
     last committed token, then the drafts) are sequence b's.  Returns per sequence (drafts that stay, the token after
     them), int32.  u [rows] judges the drafts, u_next [n_seq] draws; draft_probs: float32 [rows][vocab], the
     distribution of the draft after each row (None: the drafts were certain).  Settings: [n_seq]."""
-    lib = load_library()
     index, ls = _logits(logits)
+    if _elsewhere(index, stream):
+        with torch.cuda.device(index), torch.cuda.stream(stream):
+            return kvr_accept(logits, tokens, cu_rows, u, u_next, draft_probs, temperature, top_k, min_p, top_p)
+    lib = load_library()
     rows, vocab = logits.shape
     n = cu_rows.numel() - 1
     if n < 1:
         raise KvrError(-1, "cu_rows must have an entry more than there are sequences")
-    args = (_vec("cu_rows", cu_rows, n + 1, torch.int32, index), _vec("tokens", tokens, rows, torch.int32, index))
-    us = (_vec("u", u, rows, torch.float32, index), _vec("u_next", u_next, n, torch.float32, index))
+    cp, tp = _vec("cu_rows", cu_rows, n + 1, torch.int32, index), _vec("tokens", tokens, rows, torch.int32, index)
+    up, np = _vec("u", u, rows, torch.float32, index), _vec("u_next", u_next, n, torch.float32, index)
     qp, qs = None, vocab
     if draft_probs is not None:
         qs, qp = _rows("draft_probs", draft_probs, (rows, vocab), (torch.float32,), index), draft_probs.data_ptr()
-    with _On(index), torch.cuda.stream(stream):
-        st, keep = _settings(n, index, temperature=temperature, top_k=top_k, min_p=min_p, top_p=top_p)
-        accepted = torch.empty(n, dtype=torch.int32, device=logits.device)
-        following = torch.empty(n, dtype=torch.int32, device=logits.device)
-        wb = lib.kvr_accept_work_bytes(rows)
-        work = torch.empty(wb, dtype=torch.uint8, device=logits.device)
-        _check(lib, lib.kvr_accept(logits.data_ptr(), _TYPES[logits.dtype], ls, rows, vocab, ctypes.byref(st), n,
-                                   *args, qp, qs, *us, accepted.data_ptr(), following.data_ptr(), work.data_ptr(), wb,
-                                   stream.cuda_stream if stream is not None else _raw_stream(index)))
+    st, keep = _settings(n, index, temperature, top_k, min_p, top_p)
+    accepted = torch.empty(n, dtype=torch.int32, device=logits.device)
+    following = torch.empty(n, dtype=torch.int32, device=logits.device)
+    wb = lib.kvr_accept_work_bytes(rows)
+    work = torch.empty(wb, dtype=torch.uint8, device=logits.device)
+    rc = lib.kvr_accept(logits.data_ptr(), _TYPES[logits.dtype], ls, rows, vocab, st, n, cp, tp, qp, qs, up, np,
+                        accepted.data_ptr(), following.data_ptr(), work.data_ptr(), wb, _raw_stream(index))
+    if rc:
+        _check(lib, rc)
     return accepted, following
