@@ -68,122 +68,129 @@ __device__ __forceinline__ float scale_of(float big, float& down) {
 constexpr int kNone = -1;      // a row without an adapter
 constexpr int kOutside = -2;   // a row of no sequence
 
-// The tile's rows: the adapter of each, and its entry.
+// A tile's rows, their runs that share an adapter, and the runs' steps of 16 ranks.
+struct Run {
+  const void *a, *b;
+  float scale;
+  int rank, first, end;
+};
 struct Rows {
   int id[R];
   kvr_adapter ad[R];
+  Run run[R];
+  int runs, steps;
+  uint8_t step_run[R * KVR_MAX_RANK * 3 / 16], step_j[R * KVR_MAX_RANK * 3 / 16];
 };
-__device__ __forceinline__ void find_rows(const AdaptParams& p, int row0, int* cu, Rows& rows) {
-  for (int i = threadIdx.x; i <= p.n_seq; i += kThreads) cu[i] = p.cu[i];
+// per_rank: stacked ranks of an adapter's rank (shrink: its parts, expand: one)
+__device__ __forceinline__ void find_rows(const AdaptParams& p, int row0, int per_rank, int* cu, int* which, Rows& rows) {
+  for (int i = threadIdx.x; i <= p.n_seq; i += kThreads) {
+    cu[i] = p.cu[i];
+    if (i < p.n_seq) which[i] = p.which[i];
+  }
   __syncthreads();
-  if (threadIdx.x < R) {
-    const int r = row0 + threadIdx.x;
-    int a = 0, b = p.n_seq + 1;   // first entry above r
-    while (a < b) {
-      const int m = (a + b) >> 1;
-      if (cu[m] <= r) a = m + 1;
-      else b = m;
-    }
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x, r = row0 + lane;
     int id = kOutside;
-    if (r < p.rows && a > 0 && a <= p.n_seq) {
-      id = p.which[a - 1];
-      if (id < 0 || id >= p.site.n_adapters) id = kNone;
-      if (id != kNone) {
-        const kvr_adapter e = p.site.table[id];
-        if (e.rank < 8 || e.rank > p.site.max_rank || e.rank % 8 || !e.a || !e.b) id = kNone;
-        rows.ad[threadIdx.x] = e;
+    kvr_adapter e = {};
+    if (lane < R) {
+      int a = 0, b = p.n_seq + 1;   // first entry above r
+      while (a < b) {
+        const int m = (a + b) >> 1;
+        if (cu[m] <= r) a = m + 1;
+        else b = m;
+      }
+      if (r < p.rows && a > 0 && a <= p.n_seq) {
+        id = which[a - 1];
+        if (id < 0 || id >= p.site.n_adapters) id = kNone;
+        if (id != kNone) {
+          e = p.site.table[id];
+          if (e.rank < 8 || e.rank > p.site.max_rank || e.rank % 8 || !e.a || !e.b) id = kNone;
+        }
+      }
+      rows.id[lane] = id;
+    }
+    // runs: a row that differs from the one before starts one
+    const int before = __shfl_up_sync(0xffffffffu, id, 1);
+    const bool starts = lane < R && id >= 0 && (lane == 0 || before != id);
+    const uint32_t all = __ballot_sync(0xffffffffu, starts), same = __ballot_sync(0xffffffffu, lane < R && id >= 0 && !starts);
+    const int steps = starts ? (e.rank * per_rank + 15) / 16 : 0;
+    int at = steps;
+#pragma unroll
+    for (int o = 1; o < R; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, at, o);
+      if (lane >= o) at += v;
+    }
+    if (starts) {
+      const int k = __popc(all & ((1u << lane) - 1));
+      const uint32_t after = ~(same >> (lane + 1));
+      rows.run[k] = {e.a, e.b, e.scale, e.rank, lane, lane + __ffs(after)};
+      for (int j = 0; j < steps; ++j) {
+        rows.step_run[at - steps + j] = (uint8_t)k;
+        rows.step_j[at - steps + j] = (uint8_t)j;
       }
     }
-    rows.id[threadIdx.x] = id;
+    at = __shfl_sync(0xffffffffu, at, R - 1);
+    if (lane == 0) {
+      rows.runs = __popc(all);
+      rows.steps = at;
+    }
   }
   __syncthreads();
 }
-// the next run [first, at) of rows that share an adapter; false behind the last one
-__device__ __forceinline__ bool next_run(const Rows& rows, int& at, int& first) {
-  while (at < R && rows.id[at] < 0) ++at;
-  if (at == R) return false;
-  first = at;
-  while (at < R && rows.id[at] == rows.id[first]) ++at;
-  return true;
-}
 
-// s = A x of one tile of rows and one part of the inputs.  A warp takes a run, or
-// a share of its inputs where there are fewer runs than warps.
-constexpr int kRankTiles = 4;   // 16 rows of A each, in registers at a time
+// s = A x of one tile of rows and one part of the inputs: a warp takes 16 rows of A
+// of a run at a time.  (So a row's sums are formed in one order, whatever shares its tile.)
 template <class T>
 __global__ void __launch_bounds__(kThreads) shrink_kernel(const AdaptParams p) {
-  __shared__ int cu[kAdaptMaxSeqs + 1];
+  __shared__ int cu[kAdaptMaxSeqs + 1], which[kAdaptMaxSeqs];
   __shared__ Rows rows;
-  __shared__ float red[kWarps][kRankTiles][16 * R];
   dev::pdl_trigger();
   dev::pdl_wait();
   const int row0 = blockIdx.x * R, split = blockIdx.y;
-  find_rows(p, row0, cu, rows);
+  find_rows(p, row0, p.site.n_parts, cu, which, rows);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int ld = p.site.n_parts * p.site.max_rank;
-  int runs = 0, most = 0;
-  for (int at = 0, f; next_run(rows, at, f); ++runs) most = max(most, rows.ad[f].rank);
-  if (runs == 0) return;
-  const int per_run = kWarps / runs, sub = warp % per_run;
-  int first = 0, end = 0, at = 0;
-  const bool mine = warp / per_run < runs;
-  for (int k = 0; mine && k <= warp / per_run; ++k) {
-    next_run(rows, at, first);
-    end = at;
-  }
   const int K = p.site.k, chunks = (K + 31) / 32;
   const int c0 = (int)((long long)chunks * split / p.ksplit), c1 = (int)((long long)chunks * (split + 1) / p.ksplit);
-  const int ranks = mine ? p.site.n_parts * rows.ad[first].rank : 0;
-  const T* A = mine ? static_cast<const T*>(rows.ad[first].a) : nullptr;
-  const bool in_run = mine && g >= first && g < end;
   const uint4* xr = reinterpret_cast<const uint4*>(static_cast<const T*>(p.x) + p.x_stride * (row0 + g));
   float* part = p.part + ((long long)split * p.rows + row0) * ld;
-  for (int j0 = 0; j0 < p.site.n_parts * most; j0 += 16 * kRankTiles) {
-    float acc[kRankTiles][4];
+  for (int s = warp; s < rows.steps; s += kWarps) {
+    const Run& run = rows.run[rows.step_run[s]];
+    const int q = 16 * rows.step_j[s] + g, ranks = p.site.n_parts * run.rank;
+    const bool in_run = g >= run.first && g < run.end;
+    const T* lo_at = static_cast<const T*>(run.a) + (long long)q * K;
+    const T* hi_at = lo_at + 8ll * K;
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    // eight chunks of 32 inputs in flight
+    constexpr int kFlight = 8;
+    for (int c = c0; c < c1; c += kFlight) {
+      const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+      uint4 xv[kFlight], lo[kFlight], hi[kFlight];
 #pragma unroll
-    for (int j = 0; j < kRankTiles; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
-    if (j0 < ranks) {
-#pragma unroll 2
-      for (int c = c0 + sub; c < c1; c += per_run) {
-        const int k = 32 * c + 8 * t;
-        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-        uint4 xv = in_run && k < K ? xr[k >> 3] : zero;
-        uint4 lo[kRankTiles], hi[kRankTiles];
+      for (int f = 0; f < kFlight; ++f) {
+        const int k = 32 * (c + f) + 8 * t;
+        const bool in = c + f < c1 && k < K;
+        lo[f] = in && q < ranks ? *reinterpret_cast<const uint4*>(lo_at + k) : zero;
+        hi[f] = in && q + 8 < ranks ? *reinterpret_cast<const uint4*>(hi_at + k) : zero;
+        xv[f] = in && in_run ? xr[k >> 3] : zero;
+      }
 #pragma unroll
-        for (int j = 0; j < kRankTiles; ++j) {
-          const int q = j0 + 16 * j + g;
-          lo[j] = q < ranks && k < K ? *reinterpret_cast<const uint4*>(A + (long long)q * K + k) : zero;
-          hi[j] = q + 8 < ranks && k < K ? *reinterpret_cast<const uint4*>(A + (long long)(q + 8) * K + k) : zero;
-        }
+      for (int f = 0; f < kFlight; ++f) {
         if (std::is_same<T, __nv_bfloat16>::value && p.x16) {
-          xv.x = bf16_of_half2(xv.x);
-          xv.y = bf16_of_half2(xv.y);
-          xv.z = bf16_of_half2(xv.z);
-          xv.w = bf16_of_half2(xv.w);
+          xv[f].x = bf16_of_half2(xv[f].x);
+          xv[f].y = bf16_of_half2(xv[f].y);
+          xv[f].z = bf16_of_half2(xv[f].z);
+          xv[f].w = bf16_of_half2(xv[f].w);
         }
-#pragma unroll
-        for (int j = 0; j < kRankTiles; ++j) {
-          if (j0 + 16 * j >= ranks) break;
-          mma<T>(acc[j], lo[j].x, hi[j].x, lo[j].y, hi[j].y, xv.x, xv.y);
-          mma<T>(acc[j], lo[j].z, hi[j].z, lo[j].w, hi[j].w, xv.z, xv.w);
-        }
+        mma<T>(acc, lo[f].x, hi[f].x, lo[f].y, hi[f].y, xv[f].x, xv[f].y);
+        mma<T>(acc, lo[f].z, hi[f].z, lo[f].w, hi[f].w, xv[f].z, xv[f].w);
       }
     }
-    // acc[j]: rows j0 + 16 j + g (and + 8) of A, rows 2 t and 2 t + 1 of x
-    __syncthreads();
+    // rows q and q + 8 of A, rows 2 t and 2 t + 1 of x
 #pragma unroll
-    for (int j = 0; j < kRankTiles; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) red[warp][j][(2 * t + (e & 1)) * 16 + g + 8 * (e >> 1)] = acc[j][e];
-    __syncthreads();
-    if (mine && sub == 0) {
-      for (int i = lane; i < kRankTiles * 16 * (end - first); i += 32) {
-        const int q = i % (16 * kRankTiles), r = first + i / (16 * kRankTiles);
-        if (j0 + q >= ranks) continue;
-        float v = 0.f;
-        for (int w = 0; w < per_run; ++w) v += red[warp + w][q >> 4][r * 16 + (q & 15)];
-        part[(long long)r * ld + j0 + q] = v;
-      }
+    for (int e = 0; e < 4; ++e) {
+      const int r = 2 * t + (e & 1), j = q + 8 * (e >> 1);
+      if (r >= run.first && r < run.end && j < ranks) part[(long long)r * ld + j] = acc[e];
     }
   }
 }
@@ -192,7 +199,7 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const AdaptParams p) {
 template <class T, class O, int TERMS>
 __global__ void __launch_bounds__(kThreads) expand_kernel(const AdaptParams p) {
   constexpr int kS = KVR_MAX_RANK + 8;   // (rows shifted against one another in the banks)
-  __shared__ int cu[kAdaptMaxSeqs + 1];
+  __shared__ int cu[kAdaptMaxSeqs + 1], which[kAdaptMaxSeqs];
   __shared__ Rows rows;
   __shared__ __align__(16) T terms[TERMS][R][kS];
   __shared__ float factor[R];
@@ -200,7 +207,7 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(const AdaptParams p) {
   dev::pdl_trigger();
   dev::pdl_wait();
   const int row0 = blockIdx.x * R;
-  find_rows(p, row0, cu, rows);
+  find_rows(p, row0, 1, cu, which, rows);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   // the CTA's part, its outputs' place in it and in out
   int part = 0, col = blockIdx.y, left = 0;
@@ -213,86 +220,119 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(const AdaptParams p) {
   col *= kTileCols;
   const int cols = min(kTileCols, p.site.cols[part] - col);
   const int ld = p.site.n_parts * p.site.max_rank;
+  const int c = 16 * warp + g;
+
+  // B of the first steps, and base, are on their way while s is added up
+  constexpr int kFlight = 8;
+  uint2 lo[kFlight], hi[kFlight];
+  auto fetch = [&](int s, uint2& l, uint2& h) {
+    l = h = make_uint2(0u, 0u);
+    if (s >= rows.steps) return;
+    const Run& run = rows.run[rows.step_run[s]];
+    const int j = 16 * rows.step_j[s] + 4 * t;
+    const T* B = static_cast<const T*>(run.b) + (long long)(left + col + c) * run.rank + j;
+    if (j < run.rank && c < cols) l = *reinterpret_cast<const uint2*>(B);
+    if (j < run.rank && c + 8 < cols) h = *reinterpret_cast<const uint2*>(B + 8ll * run.rank);
+  };
+#pragma unroll
+  for (int f = 0; f < kFlight; ++f) fetch(f, lo[f], hi[f]);
+  const int r = warp, i = 4 * lane;   // (the row and the outputs that this lane writes)
+  const int id = rows.id[r];
+  const long long at = left + col + i;
+  const bool writes = id != kOutside && i < cols && !(id == kNone && p.base == p.out);
+  O* out = static_cast<O*>(p.out) + p.out_stride * (row0 + r) + at;
+  const O* base = p.base && writes ? static_cast<const O*>(p.base) + p.base_stride * (row0 + r) + at : nullptr;
+  float4 base_f = make_float4(0.f, 0.f, 0.f, 0.f);
+  uint2 base_h = make_uint2(0u, 0u);
+  if (base) {
+    if constexpr (std::is_same<O, float>::value) base_f = *reinterpret_cast<const float4*>(base);
+    else base_h = *reinterpret_cast<const uint2*>(base);
+  }
 
   // s of row `warp`: the parts' sum, scaled by a power of two to below 2, in terms of T
-  {
-    const int r = warp;
-    if (rows.id[r] >= 0) {
-      const int rank = rows.ad[r].rank;
-      const float* src = p.part + (long long)(row0 + r) * ld + part * rank;
-      float v[KVR_MAX_RANK / 32], big = 0.f;
+  if (id >= 0) {
+    int k = 0;
+    while (r >= rows.run[k].end) ++k;
+    const int rank = rows.run[k].rank;
+    const float* src = p.part + (long long)(row0 + r) * ld + part * rank;
+    const long long plane = (long long)p.rows * ld;
+    float v[KVR_MAX_RANK / 32], big = 0.f;
 #pragma unroll
-      for (int i = 0; i < KVR_MAX_RANK / 32; ++i) {
-        const int j = lane + 32 * i;
-        v[i] = 0.f;
-        if (j < rank)
-          for (int s = 0; s < p.ksplit; ++s) v[i] += src[(long long)s * p.rows * ld + j];
-        big = fmaxf(big, fabsf(v[i]));
-        if (v[i] != v[i]) big = INFINITY;
+    for (int n = 0; n < KVR_MAX_RANK / 32; ++n) {
+      const int j = lane + 32 * n;
+      v[n] = 0.f;
+      if (j < rank) {
+        for (int s0 = 0; s0 < p.ksplit; s0 += 16) {
+          float w[16];
+#pragma unroll
+          for (int s = 0; s < 16; ++s) w[s] = s0 + s < p.ksplit ? src[(s0 + s) * plane + j] : 0.f;
+#pragma unroll
+          for (int s = 0; s < 16; ++s) v[n] += w[s];
+        }
       }
+      big = fmaxf(big, fabsf(v[n]));
+      if (v[n] != v[n]) big = INFINITY;
+    }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-      float down;
-      const float up = scale_of(big, down);
+    for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+    float down;
+    const float up = scale_of(big, down);
 #pragma unroll
-      for (int i = 0; i < KVR_MAX_RANK / 32; ++i) {
-        const int j = lane + 32 * i;
-        float x = v[i] * down;
-        if (j < (rank + 15) / 16 * 16)
+    for (int n = 0; n < KVR_MAX_RANK / 32; ++n) {
+      const int j = lane + 32 * n;
+      float x = v[n] * down;
+      if (j < (rank + 15) / 16 * 16)
 #pragma unroll
-          for (int k = 0; k < TERMS; ++k) {
-            const T h = to<T>(x);
-            terms[k][r][j] = h;
-            x -= from(h);
+        for (int m = 0; m < TERMS; ++m) {
+          const T h = to<T>(x);
+          terms[m][r][j] = h;
+          x -= from(h);
+        }
+    }
+    if (lane == 0) factor[r] = rows.run[k].scale * up;
+  }
+  __syncthreads();
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int s0 = 0; s0 < rows.steps; s0 += kFlight) {
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f) {
+      const int s = s0 + f;
+      if (s < rows.steps) {
+        const int k = rows.step_run[s], j = 16 * rows.step_j[s] + 4 * t;
+        const bool in_run = g >= rows.run[k].first && g < rows.run[k].end;
+        const uint2 l = lo[f], h = hi[f];
+        fetch(s + kFlight, lo[f], hi[f]);
+#pragma unroll
+        for (int m = TERMS - 1; m >= 0; --m) {
+          const uint2 y = in_run ? *reinterpret_cast<const uint2*>(&terms[m][g][j]) : make_uint2(0u, 0u);
+          mma<T>(acc, l.x, h.x, l.y, h.y, y.x, y.y);
+        }
+        if (s + 1 == rows.steps || rows.step_run[s + 1] != k) {   // the run's last
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int row = 2 * t + (e & 1);
+            if (row >= rows.run[k].first && row < rows.run[k].end) tile[row][c + 8 * (e >> 1)] = acc[e] * factor[row];
+            acc[e] = 0.f;
           }
+        }
       }
-      if (lane == 0) factor[r] = rows.ad[r].scale * up;
     }
   }
   __syncthreads();
-  const int c = 16 * warp + g;
-  for (int at = 0, first; next_run(rows, at, first);) {
-    const int rank = rows.ad[first].rank;
-    const T* B = static_cast<const T*>(rows.ad[first].b) + (long long)(left + col) * rank;
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    const bool in_run = g >= first && g < at;
-#pragma unroll 2
-    for (int j0 = 0; j0 < rank; j0 += 16) {
-      const int j = j0 + 4 * t;
-      const uint2 zero = make_uint2(0u, 0u);
-      const uint2 lo = j < rank && c < cols ? *reinterpret_cast<const uint2*>(B + (long long)c * rank + j) : zero;
-      const uint2 hi = j < rank && c + 8 < cols ? *reinterpret_cast<const uint2*>(B + (long long)(c + 8) * rank + j) : zero;
-#pragma unroll
-      for (int k = TERMS - 1; k >= 0; --k) {
-        const uint2 s = in_run ? *reinterpret_cast<const uint2*>(&terms[k][g][j]) : zero;
-        mma<T>(acc, lo.x, hi.x, lo.y, hi.y, s.x, s.y);
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int r = 2 * t + (e & 1);
-      if (r >= first && r < at) tile[r][c + 8 * (e >> 1)] = acc[e] * factor[r];
-    }
-  }
-  __syncthreads();
-  // a warp's row, four outputs a lane
-  const int r = warp, i = 4 * lane;
-  if (rows.id[r] == kOutside || i >= cols || (rows.id[r] == kNone && p.base == p.out)) return;
-  float4 v = rows.id[r] >= 0 ? *reinterpret_cast<const float4*>(&tile[r][i]) : make_float4(0.f, 0.f, 0.f, 0.f);
-  const long long at = left + col + i;
-  O* out = static_cast<O*>(p.out) + p.out_stride * (row0 + r) + at;
-  const O* base = p.base ? static_cast<const O*>(p.base) + p.base_stride * (row0 + r) + at : nullptr;
+  if (!writes) return;
+  const float4 v = id >= 0 ? *reinterpret_cast<const float4*>(&tile[r][i]) : make_float4(0.f, 0.f, 0.f, 0.f);
   if constexpr (std::is_same<O, float>::value) {
-    if (base) {
-      const float4 b = *reinterpret_cast<const float4*>(base);
-      if (rows.id[r] < 0) v = b;   // (base's own bits)
-      else { v.x += b.x; v.y += b.y; v.z += b.z; v.w += b.w; }
+    if (id >= 0) {   // (else base's own bits)
+      base_f.x += v.x;
+      base_f.y += v.y;
+      base_f.z += v.z;
+      base_f.w += v.w;
     }
-    *reinterpret_cast<float4*>(out) = v;
+    *reinterpret_cast<float4*>(out) = base_f;
   } else {
-    __align__(8) O w[4] = {to<O>(0.f), to<O>(0.f), to<O>(0.f), to<O>(0.f)};
-    if (base) *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(base);
-    if (rows.id[r] >= 0) {
+    __align__(8) O w[4];
+    *reinterpret_cast<uint2*>(w) = base_h;
+    if (id >= 0) {
       w[0] = to<O>(from(w[0]) + v.x);
       w[1] = to<O>(from(w[1]) + v.y);
       w[2] = to<O>(from(w[2]) + v.z);
@@ -533,8 +573,10 @@ __global__ void __launch_bounds__(kThreads) shrink_tiles_kernel(const AdaptParam
   if (ks > 1) cluster.sync();   // (the others' sums are read)
 }
 
+// 64 rows and `per` tiles of 128 outputs of one part: the terms stay, the next
+// tile's B and base are on their way while one is multiplied and stored.
 template <class T, class O, int TERMS>
-__global__ void __launch_bounds__(kThreads, 2) expand_tiles_kernel(const AdaptParams p) {
+__global__ void __launch_bounds__(kThreads, 2) expand_tiles_kernel(const AdaptParams p, int per) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Tile tile;
   __shared__ float factor[TR];
@@ -544,116 +586,131 @@ __global__ void __launch_bounds__(kThreads, 2) expand_tiles_kernel(const AdaptPa
   if (tile.rows == 0 || (tile.id == kNone && p.base == p.out)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int wr = warp & 1, wn = warp >> 1;
-  int part = 0, col = blockIdx.y, left = 0;
+  int part = 0, c0 = blockIdx.y, left = 0;
   for (;; ++part) {
-    const int tiles = (p.site.cols[part] + kTileN - 1) / kTileN;
-    if (col < tiles) break;
-    col -= tiles;
+    const int n = ((p.site.cols[part] + kTileN - 1) / kTileN + per - 1) / per;
+    if (c0 < n) break;
+    c0 -= n;
     left += p.site.cols[part];
   }
-  col *= kTileN;
-  const int cols = min(kTileN, p.site.cols[part] - col);
+  const int c_end = min((c0 + 1) * per * kTileN, p.site.cols[part]);
   const bool adapted = tile.id != kNone;
   const int rank = adapted ? tile.ad.rank : 0, r16 = round16(rank), pitch = 2 * r16 + 16;
-  constexpr int kOPitch = kTileN * (int)sizeof(O) + 16, kOChunk = 16 / (int)sizeof(O);
-  const uint32_t so = dev::smem_u32(smem), sb = so + TR * kOPitch, ss = sb + kTileN * pitch;
-  const Terms terms(p, TERMS);
+  constexpr int kOPitch = kTileN * (int)sizeof(O) + 16, kOChunk = 16 / (int)sizeof(O), kOChunks = kTileN / kOChunk;
+  const int stage = TR * kOPitch + kTileN * pitch;   // base, then B
+  uint8_t* const terms_at = smem + 2 * stage;
+  const uint32_t ss = dev::smem_u32(terms_at);
+  const int chunks = r16 / 8;
   if (adapted) {
-    const T* B = static_cast<const T*>(tile.ad.b) + (long long)(left + col) * rank;
-    const int per = r16 / 8;
-    for (int i = threadIdx.x; i < kTileN * per; i += kThreads) {
-      const int r = i / per, c = i % per;
-      const bool in = r < cols && 8 * c < rank;
-      cp16(sb + r * pitch + 16 * c, in ? B + (long long)r * rank + 8 * c : B, in);
-    }
+    const Terms terms(p, TERMS);
 #pragma unroll
     for (int k = 0; k < TERMS; ++k)
-      for (int i = threadIdx.x; i < TR * per; i += kThreads) {
-        const int r = i / per, c = i % per;
+      for (int i = threadIdx.x; i < TR * chunks; i += kThreads) {
+        const int r = i / chunks, c = i % chunks;
         const T* src = terms.term<T>(k, tile.row0 + min(r, tile.rows - 1)) + part * round16(p.site.max_rank) + 8 * c;
         cp16(ss + (k * TR + r) * pitch + 16 * c, src, r < tile.rows);
       }
     if (threadIdx.x < tile.rows) factor[threadIdx.x] = terms.factor(tile.row0 + threadIdx.x)[part];
   }
-  cp_commit();
-  const long long at = left + col;
-  if (p.base) {
-    const O* base = static_cast<const O*>(p.base) + p.base_stride * tile.row0 + at;
-    for (int i = threadIdx.x; i < TR * (kTileN / kOChunk); i += kThreads) {
-      const int r = i / (kTileN / kOChunk), c = i % (kTileN / kOChunk) * kOChunk;
-      const bool in = r < tile.rows && c < cols;
-      cp16(so + r * kOPitch + c * (int)sizeof(O), in ? base + p.base_stride * r + c : base, in);
-    }
-  }
-  cp_commit();
-  float acc[2][4][4];
-#pragma unroll
-  for (int m = 0; m < 2; ++m)
-#pragma unroll
-    for (int n = 0; n < 4; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.f;
-  cp_wait<1>();
-  __syncthreads();
-#pragma unroll 2
-  for (int kk = 0; kk < r16 / 16; ++kk) {
-    uint32_t b[2][4];
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      const int r = wn * 32 + 16 * n + (lane & 7) + ((lane >> 4) << 3);
-      dev::ldmatrix_x4(sb + r * pitch + 32 * kk + 16 * ((lane >> 3) & 1), b[n][0], b[n][1], b[n][2], b[n][3]);
-    }
-#pragma unroll
-    for (int k = TERMS - 1; k >= 0; --k)
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        uint32_t a[4];
-        const int r = wr * 32 + m * 16 + (lane & 15);
-        dev::ldmatrix_x4(ss + (k * TR + r) * pitch + 32 * kk + 16 * (lane >> 4), a[0], a[1], a[2], a[3]);
-#pragma unroll
-        for (int n = 0; n < 4; ++n)
-          mma<T>(acc[m][n], a[0], a[1], a[2], a[3], b[n >> 1][2 * (n & 1)], b[n >> 1][2 * (n & 1) + 1]);
+  const O* base = p.base ? static_cast<const O*>(p.base) + p.base_stride * tile.row0 + left : nullptr;
+  O* out = static_cast<O*>(p.out) + p.out_stride * tile.row0 + left;
+  const T* B = adapted ? static_cast<const T*>(tile.ad.b) + (long long)left * rank : nullptr;
+  auto load = [&](int col, int buf) {
+    const uint32_t so = dev::smem_u32(smem) + buf * stage, sb = so + TR * kOPitch;
+    if (base)
+      for (int i = threadIdx.x; i < TR * kOChunks; i += kThreads) {
+        const int r = i / kOChunks, c = i % kOChunks * kOChunk;
+        const bool in = r < tile.rows && col + c < c_end;
+        cp16(so + r * kOPitch + c * (int)sizeof(O), in ? base + p.base_stride * r + col + c : base, in);
       }
-  }
-  cp_wait<0>();
-  __syncthreads();
-  // into base's place in shared memory, then out in whole rows
-  if (adapted)
+    if (adapted)
+      for (int i = threadIdx.x; i < kTileN * chunks; i += kThreads) {
+        const int r = i / chunks, c = i % chunks;
+        const bool in = col + r < c_end && 8 * c < rank;
+        cp16(sb + r * pitch + 16 * c, in ? B + (long long)(col + r) * rank + 8 * c : B, in);
+      }
+  };
+  int buf = 0;
+  load(c0 * per * kTileN, 0);
+  cp_commit();
+  for (int col = c0 * per * kTileN; col < c_end; col += kTileN, buf ^= 1) {
+    if (col + kTileN < c_end) load(col + kTileN, buf ^ 1);
+    cp_commit();
+    cp_wait<1>();
+    __syncthreads();
+    uint8_t* const so = smem + buf * stage;
+    if (adapted) {
+      const uint32_t sb = dev::smem_u32(so) + TR * kOPitch;
+      float acc[2][4][4];
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+      for (int m = 0; m < 2; ++m)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = wr * 32 + m * 16 + 8 * h + g;
-        if (r >= tile.rows) continue;
-        const float f = factor[r];
+        for (int n = 0; n < 4; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.f;
+#pragma unroll 2
+      for (int kk = 0; kk < r16 / 16; ++kk) {
+        uint32_t b[2][4];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          O* o = reinterpret_cast<O*>(smem + r * kOPitch) + wn * 32 + 8 * n + 2 * t;
-          const float y0 = acc[m][n][2 * h] * f, y1 = acc[m][n][2 * h + 1] * f;
-          if constexpr (std::is_same<O, float>::value) {
-            float2 v = p.base ? *reinterpret_cast<float2*>(o) : make_float2(0.f, 0.f);
-            v.x += y0;
-            v.y += y1;
-            *reinterpret_cast<float2*>(o) = v;
-          } else {
-            o[0] = to<O>((p.base ? from(o[0]) : 0.f) + y0);
-            o[1] = to<O>((p.base ? from(o[1]) : 0.f) + y1);
+        for (int n = 0; n < 2; ++n) {
+          const int r = wn * 32 + 16 * n + (lane & 7) + ((lane >> 4) << 3);
+          dev::ldmatrix_x4(sb + r * pitch + 32 * kk + 16 * ((lane >> 3) & 1), b[n][0], b[n][1], b[n][2], b[n][3]);
+        }
+#pragma unroll
+        for (int k = TERMS - 1; k >= 0; --k)
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            uint32_t a[4];
+            const int r = wr * 32 + m * 16 + (lane & 15);
+            dev::ldmatrix_x4(ss + (k * TR + r) * pitch + 32 * kk + 16 * (lane >> 4), a[0], a[1], a[2], a[3]);
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+              mma<T>(acc[m][n], a[0], a[1], a[2], a[3], b[n >> 1][2 * (n & 1)], b[n >> 1][2 * (n & 1) + 1]);
+          }
+      }
+      // into base's place in shared memory, then out in whole rows
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = wr * 32 + m * 16 + 8 * h + g;
+          if (r >= tile.rows) continue;
+          const float f = factor[r];
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            O* o = reinterpret_cast<O*>(so + r * kOPitch) + wn * 32 + 8 * n + 2 * t;
+            const float y0 = acc[m][n][2 * h] * f, y1 = acc[m][n][2 * h + 1] * f;
+            if constexpr (std::is_same<O, float>::value) {
+              float2 v = base ? *reinterpret_cast<float2*>(o) : make_float2(0.f, 0.f);
+              v.x += y0;
+              v.y += y1;
+              *reinterpret_cast<float2*>(o) = v;
+            } else {
+              __align__(4) O v[2] = {to<O>(0.f), to<O>(0.f)};
+              if (base) *reinterpret_cast<uint32_t*>(v) = *reinterpret_cast<const uint32_t*>(o);
+              v[0] = to<O>(from(v[0]) + y0);
+              v[1] = to<O>(from(v[1]) + y1);
+              *reinterpret_cast<uint32_t*>(o) = *reinterpret_cast<const uint32_t*>(v);
+            }
           }
         }
-      }
-  __syncthreads();
-  O* out = static_cast<O*>(p.out) + p.out_stride * tile.row0 + at;
-  for (int i = threadIdx.x; i < TR * (kTileN / kOChunk); i += kThreads) {
-    const int r = i / (kTileN / kOChunk), c = i % (kTileN / kOChunk) * kOChunk;
-    if (r < tile.rows && c < cols) {
-      uint4 v = *reinterpret_cast<const uint4*>(smem + r * kOPitch + c * sizeof(O));
-      if (!adapted && !p.base) v = make_uint4(0u, 0u, 0u, 0u);
-      *reinterpret_cast<uint4*>(out + p.out_stride * r + c) = v;
+      __syncthreads();
     }
+    for (int i = threadIdx.x; i < TR * kOChunks; i += kThreads) {
+      const int r = i / kOChunks, c = i % kOChunks * kOChunk;
+      if (r < tile.rows && col + c < c_end) {
+        uint4 v = *reinterpret_cast<const uint4*>(so + r * kOPitch + c * sizeof(O));
+        if (!adapted && !base) v = make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(out + p.out_stride * r + col + c) = v;
+      }
+    }
+    __syncthreads();   // (the next loads overwrite it)
   }
+  cp_wait<0>();
 }
 
 template <class O>
 int expand_tiles_smem(int max_rank, int terms) {
-  return TR * (kTileN * (int)sizeof(O) + 16) + (kTileN + terms * TR) * (2 * round16(max_rank) + 16);
+  return 2 * (TR * (kTileN * (int)sizeof(O) + 16) + kTileN * (2 * round16(max_rank) + 16)) +
+         terms * TR * (2 * round16(max_rank) + 16);
 }
 template <int NC>
 constexpr int shrink_tiles_smem() {
@@ -689,10 +746,13 @@ cudaError_t launch_tiles(const AdaptParams& p, int sms, cudaStream_t st) {
                   : stacked <= 192 ? launch_shrink_tiles<T, 192, TERMS>(p, tiles, 1, sms, st)
                                    : launch_shrink_tiles<T, 128, TERMS>(p, tiles, p.site.n_parts, sms, st);
   if (e != cudaSuccess) return e;
-  int cols = 0;
+  int cols = 0, ctas = 0;
   for (int j = 0; j < p.site.n_parts; ++j) cols += (p.site.cols[j] + kTileN - 1) / kTileN;
-  return launch_k(expand_tiles_kernel<T, O, TERMS>, dim3(tiles, cols), dim3(kThreads),
-                  expand_tiles_smem<O>(p.site.max_rank, TERMS), st, p);
+  // tiles of outputs a CTA: few enough that the CTAs fill the SMs, of two each, twice
+  const int per = (int)std::max(1ll, std::min<long long>(cols, (long long)tiles * cols / (4 * sms)));
+  for (int j = 0; j < p.site.n_parts; ++j) ctas += ((p.site.cols[j] + kTileN - 1) / kTileN + per - 1) / per;
+  return launch_k(expand_tiles_kernel<T, O, TERMS>, dim3(tiles, ctas), dim3(kThreads),
+                  expand_tiles_smem<O>(p.site.max_rank, TERMS), st, p, per);
 }
 
 template <class T, int TERMS>

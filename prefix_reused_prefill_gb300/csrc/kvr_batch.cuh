@@ -36,7 +36,7 @@ cudaError_t sample_setup();   // of the current device, before its first launch
 cudaError_t launch_sample(const SampleParams& p, int sms, cudaStream_t st);
 
 constexpr int kAdaptMaxSeqs = 2048;
-constexpr int kAdaptMaxSplit = 32;
+constexpr int kAdaptMaxSplit = 48;
 constexpr int kAdaptRows = 8;        // rows of a tile
 struct AdaptParams {
   kvr_adapter_site site;
