@@ -57,6 +57,22 @@ __device__ __forceinline__ T to(float x) {
   else return __float2bfloat16_rn(x);
 }
 
+// pairs of T
+template <class T>
+__device__ __forceinline__ float2 pair_from(uint32_t v) {
+  if constexpr (std::is_same<T, __half>::value) return __half22float2(*reinterpret_cast<const __half2*>(&v));
+  else return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+template <class T>
+__device__ __forceinline__ uint32_t pair_to(float lo, float hi) {
+  if constexpr (std::is_same<T, __half>::value) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    return dev::pack_bf16x2(lo, hi);
+  }
+}
+
 // The power of two by which a row whose largest element is `big` is held in terms of T
 // (`down` scales it to below 2), and NaN in `down` for a row that is not finite.
 __device__ __forceinline__ float scale_of(float big, float& down) {
@@ -254,21 +270,23 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(const AdaptParams p) {
     int k = 0;
     while (r >= rows.run[k].end) ++k;
     const int rank = rows.run[k].rank;
-    const float* src = p.part + (long long)(row0 + r) * ld + part * rank;
-    const long long plane = (long long)p.rows * ld;
+    const int plane = p.rows * ld;   // (below 2^31: what few rows a sequence and 2048 sequences make)
     float v[KVR_MAX_RANK / 32], big = 0.f;
 #pragma unroll
     for (int n = 0; n < KVR_MAX_RANK / 32; ++n) {
       const int j = lane + 32 * n;
       v[n] = 0.f;
       if (j < rank) {
-        for (int s0 = 0; s0 < p.ksplit; s0 += 16) {
-          float w[16];
+        const float* src = p.part + (long long)(row0 + r) * ld + part * rank + j;
+        int s = 0;
+        for (; s + 8 <= p.ksplit; s += 8, src += 8ll * plane) {
+          float w[8];
 #pragma unroll
-          for (int s = 0; s < 16; ++s) w[s] = s0 + s < p.ksplit ? src[(s0 + s) * plane + j] : 0.f;
+          for (int k2 = 0; k2 < 8; ++k2) w[k2] = src[k2 * (long long)plane];
 #pragma unroll
-          for (int s = 0; s < 16; ++s) v[n] += w[s];
+          for (int k2 = 0; k2 < 8; ++k2) v[n] += w[k2];
         }
+        for (; s < p.ksplit; ++s, src += plane) v[n] += *src;
       }
       big = fmaxf(big, fabsf(v[n]));
       if (v[n] != v[n]) big = INFINITY;
@@ -438,8 +456,9 @@ struct Terms {
 };
 
 // One chunk of NC stacked rows of A (all parts, or one) of one tile and one part of the inputs.
-template <class T, int NC, int TERMS>
-__global__ void __launch_bounds__(kThreads) shrink_tiles_kernel(const AdaptParams p, int ks) {
+// X16: x is fp16 that holds bf16 values.
+template <class T, int NC, int TERMS, bool X16>
+__global__ void __launch_bounds__(kThreads, 2) shrink_tiles_kernel(const AdaptParams p, int ks) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Tile tile;
   constexpr int kXBytes = TR * 128, kStage = kXBytes + NC * 128;
@@ -459,19 +478,36 @@ __global__ void __launch_bounds__(kThreads) shrink_tiles_kernel(const AdaptParam
   const int K = p.site.k, steps = (K + kStep - 1) / kStep;
   const int s0 = (int)((long long)steps * part_k / ks), s1 = (int)((long long)steps * (part_k + 1) / ks);
   const uint32_t base = dev::smem_u32(smem);
-  const T* x = static_cast<const T*>(p.x) + p.x_stride * tile.row0;
-  const T* A = static_cast<const T*>(tile.ad.a) + (long long)q0 * K;
-  auto load = [&](int s) {
-    const uint32_t st = base + (s - s0) % kStages * kStage;
-    for (int i = threadIdx.x; i < (TR + NC) * 8; i += kThreads) {
-      const int r = i >> 3, c = i & 7, k = s * kStep + 8 * c;
-      if (r < TR)
-        cp16(st + dev::swz128(r, c), r < tile.rows && k < K ? x + p.x_stride * r + k : x, r < tile.rows && k < K);
-      else
-        cp16(st + kXBytes + dev::swz128(r - TR, c), r - TR < nq && k < K ? A + (long long)(r - TR) * K + k : A,
-             r - TR < nq && k < K);
+  // a thread copies 16 bytes of every 32nd row: where from and where to moves with the stage only
+  constexpr int kRowStep = kThreads / 8;
+  const int lr = threadIdx.x >> 3, lc = threadIdx.x & 7;
+  const uint32_t to_smem = base + dev::swz128(lr, lc);
+  const T* x = static_cast<const T*>(p.x) + p.x_stride * (tile.row0 + lr) + 8 * lc;
+  const T* A = static_cast<const T*>(tile.ad.a) + (long long)(q0 + lr) * K + 8 * lc;
+  const long long x_step = p.x_stride * kRowStep, a_step = (long long)K * kRowStep;
+  const int x_rows = tile.rows - lr, a_rows = nq - lr;
+  auto load = [&](int s, int at) {
+    const uint32_t st = to_smem + at * kStage;
+    const int k = s * kStep;
+    const bool in = k + 8 * lc < K;
+#pragma unroll
+    for (int j = 0; j < TR / kRowStep; ++j) {
+      const bool v = in && j * kRowStep < x_rows;
+      cp16(st + j * kRowStep * 128, v ? x + j * x_step + k : p.x, v);
+    }
+#pragma unroll
+    for (int j = 0; j < NC / kRowStep; ++j) {
+      const bool v = in && j * kRowStep < a_rows;
+      cp16(st + kXBytes + j * kRowStep * 128, v ? A + j * a_step + k : tile.ad.a, v);
     }
   };
+  // a lane's 16-byte chunks of its operand rows, by the 16 inputs of a product
+  uint32_t a_at[kStep / 16], b_at[kStep / 16];
+#pragma unroll
+  for (int kk = 0; kk < kStep / 16; ++kk) {
+    a_at[kk] = base + dev::swz128(wr * 32 + (lane & 15), 2 * kk + (lane >> 4));
+    b_at[kk] = base + kXBytes + dev::swz128(wn * (NC / 4) + (lane & 7) + ((lane >> 4) << 3), 2 * kk + ((lane >> 3) & 1));
+  }
   float acc[2][kNT][4];
 #pragma unroll
   for (int m = 0; m < 2; ++m)
@@ -479,31 +515,31 @@ __global__ void __launch_bounds__(kThreads) shrink_tiles_kernel(const AdaptParam
     for (int n = 0; n < kNT; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.f;
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) {
-    if (s0 + i < s1) load(s0 + i);
+    if (s0 + i < s1) load(s0 + i, i);
     cp_commit();
   }
+  int at = 0;
   for (int s = s0; s < s1; ++s) {
     cp_wait<kStages - 2>();
     __syncthreads();
-    if (s + kStages - 1 < s1) load(s + kStages - 1);
+    if (s + kStages - 1 < s1) load(s + kStages - 1, at == 0 ? kStages - 1 : at - 1);
     cp_commit();
-    const uint32_t st = base + (s - s0) % kStages * kStage;
+    const uint32_t st = at * kStage;
+    at = at + 1 == kStages ? 0 : at + 1;
 #pragma unroll
     for (int kk = 0; kk < kStep / 16; ++kk) {
       uint32_t a[2][4];
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
-        const int r = wr * 32 + m * 16 + (lane & 15);
-        dev::ldmatrix_x4(st + dev::swz128(r, 2 * kk + (lane >> 4)), a[m][0], a[m][1], a[m][2], a[m][3]);
-        if (std::is_same<T, __nv_bfloat16>::value && p.x16)
+        dev::ldmatrix_x4(a_at[kk] + st + m * 16 * 128, a[m][0], a[m][1], a[m][2], a[m][3]);
+        if (X16)
 #pragma unroll
           for (int e = 0; e < 4; ++e) a[m][e] = bf16_of_half2(a[m][e]);
       }
 #pragma unroll
       for (int n = 0; n < kNT; n += 2) {
         uint32_t b[4];   // ranks 8 n .. + 15: (first eight, low and high inputs), (second eight, ...)
-        const int r = wn * (NC / 4) + 8 * n + (lane & 7) + ((lane >> 4) << 3);
-        dev::ldmatrix_x4(st + kXBytes + dev::swz128(r, 2 * kk + ((lane >> 3) & 1)), b[0], b[1], b[2], b[3]);
+        dev::ldmatrix_x4(b_at[kk] + st + n * 8 * 128, b[0], b[1], b[2], b[3]);
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
           mma<T>(acc[m][n], a[m][0], a[m][1], a[m][2], a[m][3], b[0], b[1]);
@@ -536,18 +572,29 @@ __global__ void __launch_bounds__(kThreads) shrink_tiles_kernel(const AdaptParam
   const Terms terms(p, TERMS);
   const int r0 = TR * part_k / ks, r1 = min(TR * (part_k + 1) / ks, tile.rows);
   const int parts = whole ? p.site.n_parts : 1;
-  for (int r = r0 + warp; r < r1; r += kWarps)
-    for (int j = 0; j < parts; ++j) {
-      float v[KVR_MAX_RANK / 32], big = 0.f;
+  for (int r = r0 + warp; r < r1; r += kWarps) {
+    // (a row's ranks 32 at a time, all on their way before any is used)
+    constexpr int kRank32 = NC == 64 ? 2 : NC == 192 ? 3 : 4, kParts = 3;   // (192: of two parts at least)
+    float sum[kParts][kRank32];
 #pragma unroll
-      for (int i = 0; i < KVR_MAX_RANK / 32; ++i) {
+    for (int j = 0; j < kParts; ++j)
+#pragma unroll
+      for (int i = 0; i < kRank32; ++i) {
         const int q = lane + 32 * i;
-        v[i] = 0.f;
-        if (q < rank) {
+        sum[j][i] = 0.f;
+        if (j < parts && q < rank) {
 #pragma unroll
           for (int c = 0; c < kMaxCluster; ++c)
-            if (c < ks) v[i] += from_[c][r * kLd + j * rank + q];
+            if (c < ks) sum[j][i] += from_[c][r * kLd + j * rank + q];
         }
+      }
+#pragma unroll
+    for (int j = 0; j < kParts; ++j) {
+      if (j >= parts) break;
+      float (&v)[kRank32] = sum[j];
+      float big = 0.f;
+#pragma unroll
+      for (int i = 0; i < kRank32; ++i) {
         big = fmaxf(big, fabsf(v[i]));
         if (v[i] != v[i]) big = INFINITY;
       }
@@ -557,7 +604,7 @@ __global__ void __launch_bounds__(kThreads) shrink_tiles_kernel(const AdaptParam
       const float up = scale_of(big, down);
       const int pj = whole ? j : blockIdx.z;
 #pragma unroll
-      for (int i = 0; i < KVR_MAX_RANK / 32; ++i) {
+      for (int i = 0; i < kRank32; ++i) {
         const int q = lane + 32 * i;
         float y = v[i] * down;
         if (q < round16(rank))
@@ -570,6 +617,7 @@ __global__ void __launch_bounds__(kThreads) shrink_tiles_kernel(const AdaptParam
       }
       if (lane == 0) terms.factor(tile.row0 + r)[pj] = tile.ad.scale * up;
     }
+  }
   if (ks > 1) cluster.sync();   // (the others' sums are read)
 }
 
@@ -600,36 +648,55 @@ __global__ void __launch_bounds__(kThreads, 2) expand_tiles_kernel(const AdaptPa
   const int stage = TR * kOPitch + kTileN * pitch;   // base, then B
   uint8_t* const terms_at = smem + 2 * stage;
   const uint32_t ss = dev::smem_u32(terms_at);
-  const int chunks = r16 / 8;
+  // a thread's 16 bytes of a row of ranks (a power of two of them, the last ones without work)
+  const int chunks = r16 / 8, shift = chunks > 1 ? 32 - __clz(chunks - 1) : 0;
+  const int lr = threadIdx.x >> shift, lc = threadIdx.x & ((1 << shift) - 1), lstep = kThreads >> shift;
   if (adapted) {
     const Terms terms(p, TERMS);
 #pragma unroll
     for (int k = 0; k < TERMS; ++k)
-      for (int i = threadIdx.x; i < TR * chunks; i += kThreads) {
-        const int r = i / chunks, c = i % chunks;
-        const T* src = terms.term<T>(k, tile.row0 + min(r, tile.rows - 1)) + part * round16(p.site.max_rank) + 8 * c;
-        cp16(ss + (k * TR + r) * pitch + 16 * c, src, r < tile.rows);
+      for (int r = lr; r < TR && lc < chunks; r += lstep) {
+        const T* src = terms.term<T>(k, tile.row0 + min(r, tile.rows - 1)) + part * round16(p.site.max_rank) + 8 * lc;
+        cp16(ss + (k * TR + r) * pitch + 16 * lc, src, r < tile.rows);
       }
     if (threadIdx.x < tile.rows) factor[threadIdx.x] = terms.factor(tile.row0 + threadIdx.x)[part];
   }
   const O* base = p.base ? static_cast<const O*>(p.base) + p.base_stride * tile.row0 + left : nullptr;
   O* out = static_cast<O*>(p.out) + p.out_stride * tile.row0 + left;
   const T* B = adapted ? static_cast<const T*>(tile.ad.b) + (long long)left * rank : nullptr;
+  constexpr int kORows = kThreads / kOChunks;   // rows of base that the threads copy at once
+  const int orow = threadIdx.x / kOChunks, ocol = threadIdx.x % kOChunks * kOChunk;
+  const uint32_t s_base = dev::smem_u32(smem);
+  const uint32_t o_at = orow * kOPitch + ocol * (int)sizeof(O);
+  const long long base_step = p.base_stride * kORows, out_step = p.out_stride * kORows;
   auto load = [&](int col, int buf) {
-    const uint32_t so = dev::smem_u32(smem) + buf * stage, sb = so + TR * kOPitch;
-    if (base)
-      for (int i = threadIdx.x; i < TR * kOChunks; i += kThreads) {
-        const int r = i / kOChunks, c = i % kOChunks * kOChunk;
-        const bool in = r < tile.rows && col + c < c_end;
-        cp16(so + r * kOPitch + c * (int)sizeof(O), in ? base + p.base_stride * r + col + c : base, in);
+    const uint32_t so = s_base + buf * stage, sb = so + TR * kOPitch;
+    if (base) {
+      const O* src = base + p.base_stride * orow + col + ocol;
+      const bool in = col + ocol < c_end;
+#pragma unroll
+      for (int j = 0; j < TR / kORows; ++j) {
+        const bool v = in && orow + j * kORows < tile.rows;
+        cp16(so + o_at + j * kORows * kOPitch, v ? src + j * base_step : base, v);
       }
-    if (adapted)
-      for (int i = threadIdx.x; i < kTileN * chunks; i += kThreads) {
-        const int r = i / chunks, c = i % chunks;
-        const bool in = col + r < c_end && 8 * c < rank;
-        cp16(sb + r * pitch + 16 * c, in ? B + (long long)(col + r) * rank + 8 * c : B, in);
+    }
+    if (adapted && lc < chunks) {
+      const T* src = B + (long long)(col + lr) * rank + 8 * lc;
+      const int step = lstep * rank;
+      uint32_t dst = sb + lr * pitch + 16 * lc;
+      const bool in = 8 * lc < rank;
+#pragma unroll 4
+      for (int r = lr; r < kTileN; r += lstep) {
+        const bool v = in && col + r < c_end;
+        cp16(dst, v ? src : B, v);
+        src += step;
+        dst += lstep * pitch;
       }
+    }
   };
+  // a lane's operand rows
+  const uint32_t a_at = ss + (wr * 32 + (lane & 15)) * pitch + 16 * (lane >> 4);
+  const uint32_t b_at = s_base + TR * kOPitch + (wn * 32 + (lane & 7) + ((lane >> 4) << 3)) * pitch + 16 * ((lane >> 3) & 1);
   int buf = 0;
   load(c0 * per * kTileN, 0);
   cp_commit();
@@ -640,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 2) expand_tiles_kernel(const AdaptPa
     __syncthreads();
     uint8_t* const so = smem + buf * stage;
     if (adapted) {
-      const uint32_t sb = dev::smem_u32(so) + TR * kOPitch;
+      const uint32_t b_buf = b_at + buf * stage;
       float acc[2][4][4];
 #pragma unroll
       for (int m = 0; m < 2; ++m)
@@ -650,17 +717,14 @@ __global__ void __launch_bounds__(kThreads, 2) expand_tiles_kernel(const AdaptPa
       for (int kk = 0; kk < r16 / 16; ++kk) {
         uint32_t b[2][4];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const int r = wn * 32 + 16 * n + (lane & 7) + ((lane >> 4) << 3);
-          dev::ldmatrix_x4(sb + r * pitch + 32 * kk + 16 * ((lane >> 3) & 1), b[n][0], b[n][1], b[n][2], b[n][3]);
-        }
+        for (int n = 0; n < 2; ++n)
+          dev::ldmatrix_x4(b_buf + 16 * n * pitch + 32 * kk, b[n][0], b[n][1], b[n][2], b[n][3]);
 #pragma unroll
         for (int k = TERMS - 1; k >= 0; --k)
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
             uint32_t a[4];
-            const int r = wr * 32 + m * 16 + (lane & 15);
-            dev::ldmatrix_x4(ss + (k * TR + r) * pitch + 32 * kk + 16 * (lane >> 4), a[0], a[1], a[2], a[3]);
+            dev::ldmatrix_x4(a_at + (k * TR + m * 16) * pitch + 32 * kk, a[0], a[1], a[2], a[3]);
 #pragma unroll
             for (int n = 0; n < 4; ++n)
               mma<T>(acc[m][n], a[0], a[1], a[2], a[3], b[n >> 1][2 * (n & 1)], b[n >> 1][2 * (n & 1) + 1]);
@@ -677,30 +741,27 @@ __global__ void __launch_bounds__(kThreads, 2) expand_tiles_kernel(const AdaptPa
 #pragma unroll
           for (int n = 0; n < 4; ++n) {
             O* o = reinterpret_cast<O*>(so + r * kOPitch) + wn * 32 + 8 * n + 2 * t;
-            const float y0 = acc[m][n][2 * h] * f, y1 = acc[m][n][2 * h + 1] * f;
+            float2 v = make_float2(0.f, 0.f);
             if constexpr (std::is_same<O, float>::value) {
-              float2 v = base ? *reinterpret_cast<float2*>(o) : make_float2(0.f, 0.f);
-              v.x += y0;
-              v.y += y1;
-              *reinterpret_cast<float2*>(o) = v;
+              if (base) v = *reinterpret_cast<const float2*>(o);
+              *reinterpret_cast<float2*>(o) = make_float2(fmaf(acc[m][n][2 * h], f, v.x), fmaf(acc[m][n][2 * h + 1], f, v.y));
             } else {
-              __align__(4) O v[2] = {to<O>(0.f), to<O>(0.f)};
-              if (base) *reinterpret_cast<uint32_t*>(v) = *reinterpret_cast<const uint32_t*>(o);
-              v[0] = to<O>(from(v[0]) + y0);
-              v[1] = to<O>(from(v[1]) + y1);
-              *reinterpret_cast<uint32_t*>(o) = *reinterpret_cast<const uint32_t*>(v);
+              if (base) v = pair_from<O>(*reinterpret_cast<const uint32_t*>(o));
+              *reinterpret_cast<uint32_t*>(o) = pair_to<O>(fmaf(acc[m][n][2 * h], f, v.x), fmaf(acc[m][n][2 * h + 1], f, v.y));
             }
           }
         }
       __syncthreads();
     }
-    for (int i = threadIdx.x; i < TR * kOChunks; i += kThreads) {
-      const int r = i / kOChunks, c = i % kOChunks * kOChunk;
-      if (r < tile.rows && col + c < c_end) {
-        uint4 v = *reinterpret_cast<const uint4*>(so + r * kOPitch + c * sizeof(O));
-        if (!adapted && !base) v = make_uint4(0u, 0u, 0u, 0u);
-        *reinterpret_cast<uint4*>(out + p.out_stride * r + col + c) = v;
-      }
+    if (col + ocol < c_end) {
+      O* dst = out + p.out_stride * orow + col + ocol;
+#pragma unroll
+      for (int j = 0; j < TR / kORows; ++j)
+        if (orow + j * kORows < tile.rows) {
+          uint4 v = *reinterpret_cast<const uint4*>(so + o_at + j * kORows * kOPitch);
+          if (!adapted && !base) v = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(dst + j * out_step) = v;
+        }
     }
     __syncthreads();   // (the next loads overwrite it)
   }
@@ -719,9 +780,9 @@ constexpr int shrink_tiles_smem() {
 
 template <class T, int NC, int TERMS>
 cudaError_t launch_shrink_tiles(const AdaptParams& p, int tiles, int chunks, int sms, cudaStream_t st) {
-  // CTAs of a tile: as many as fill the SMs twice, with 256 inputs each at least
+  // CTAs of a tile: as many as fill the SMs three times, with 256 inputs each at least
   int ks = 1;
-  while (ks < kMaxCluster && tiles * chunks * ks * 2 <= 2 * sms && p.site.k >= 512 * ks) ks *= 2;
+  while (ks < kMaxCluster && tiles * chunks * ks * 2 <= 3 * sms && p.site.k >= 512 * ks) ks *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * ks), 1, (unsigned)chunks);
   cfg.blockDim = dim3(kThreads);
@@ -734,7 +795,9 @@ cudaError_t launch_shrink_tiles(const AdaptParams& p, int tiles, int chunks, int
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, shrink_tiles_kernel<T, NC, TERMS>, p, ks);
+  if constexpr (TERMS == 3)
+    if (p.x16) return cudaLaunchKernelEx(&cfg, shrink_tiles_kernel<T, NC, TERMS, true>, p, ks);
+  return cudaLaunchKernelEx(&cfg, shrink_tiles_kernel<T, NC, TERMS, false>, p, ks);
 }
 
 template <class T, class O, int TERMS>
@@ -755,16 +818,14 @@ cudaError_t launch_tiles(const AdaptParams& p, int sms, cudaStream_t st) {
                   expand_tiles_smem<O>(p.site.max_rank, TERMS), st, p, per);
 }
 
-template <class T, int TERMS>
+template <class T, int TERMS, bool X16>
 cudaError_t setup_shrink() {
-  cudaError_t e = cudaFuncSetAttribute(shrink_tiles_kernel<T, 64, TERMS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       shrink_tiles_smem<64>());
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(shrink_tiles_kernel<T, 128, TERMS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             shrink_tiles_smem<128>());
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(shrink_tiles_kernel<T, 192, TERMS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             shrink_tiles_smem<192>());
+  const auto set = [](void (*k)(AdaptParams, int), int bytes) {
+    return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  };
+  cudaError_t e = set(shrink_tiles_kernel<T, 64, TERMS, X16>, shrink_tiles_smem<64>());
+  if (e == cudaSuccess) e = set(shrink_tiles_kernel<T, 128, TERMS, X16>, shrink_tiles_smem<128>());
+  if (e == cudaSuccess) e = set(shrink_tiles_kernel<T, 192, TERMS, X16>, shrink_tiles_smem<192>());
   return e;
 }
 template <class T, class O, int TERMS>
@@ -798,9 +859,10 @@ int adapt_split(const kvr_adapter_site& s, int rows, int sms) {
 }  // namespace
 
 cudaError_t adapt_setup() {
-  cudaError_t e = setup_shrink<__nv_bfloat16, 2>();
-  if (e == cudaSuccess) e = setup_shrink<__nv_bfloat16, 3>();
-  if (e == cudaSuccess) e = setup_shrink<__half, 2>();
+  cudaError_t e = setup_shrink<__nv_bfloat16, 2, false>();
+  if (e == cudaSuccess) e = setup_shrink<__nv_bfloat16, 3, false>();
+  if (e == cudaSuccess) e = setup_shrink<__nv_bfloat16, 3, true>();   // (the layer stack's: 32-bit outputs)
+  if (e == cudaSuccess) e = setup_shrink<__half, 2, false>();
   if (e == cudaSuccess) e = setup_expand<__nv_bfloat16, __nv_bfloat16, 2>();
   if (e == cudaSuccess) e = setup_expand<__nv_bfloat16, float, 3>();
   if (e == cudaSuccess) e = setup_expand<__half, __half, 2>();
