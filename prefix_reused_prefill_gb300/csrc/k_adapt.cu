@@ -170,15 +170,15 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const AdaptParams p) {
   const int c0 = (int)((long long)chunks * split / p.ksplit), c1 = (int)((long long)chunks * (split + 1) / p.ksplit);
   const uint4* xr = reinterpret_cast<const uint4*>(static_cast<const T*>(p.x) + p.x_stride * (row0 + g));
   float* part = p.part + ((long long)split * p.rows + row0) * ld;
-  for (int s = warp; s < rows.steps; s += kWarps) {
+  for (int s = warp + kWarps * blockIdx.z; s < rows.steps; s += kWarps * gridDim.z) {
     const Run& run = rows.run[rows.step_run[s]];
     const int q = 16 * rows.step_j[s] + g, ranks = p.site.n_parts * run.rank;
     const bool in_run = g >= run.first && g < run.end;
     const T* lo_at = static_cast<const T*>(run.a) + (long long)q * K;
     const T* hi_at = lo_at + 8ll * K;
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    // eight chunks of 32 inputs in flight
-    constexpr int kFlight = 8;
+    // four chunks of 32 inputs in flight
+    constexpr int kFlight = 4;
     for (int c = c0; c < c1; c += kFlight) {
       const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
       uint4 xv[kFlight], lo[kFlight], hi[kFlight];
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const AdaptParams p) {
 
 // out = base + scale B s of one tile of rows and 16 outputs a warp.
 template <class T, class O, int TERMS>
-__global__ void __launch_bounds__(kThreads) expand_kernel(const AdaptParams p) {
+__global__ void __launch_bounds__(kThreads, 2) expand_kernel(const AdaptParams p) {
   constexpr int kS = KVR_MAX_RANK + 8;   // (rows shifted against one another in the banks)
   __shared__ int cu[kAdaptMaxSeqs + 1], which[kAdaptMaxSeqs];
   __shared__ Rows rows;
@@ -236,22 +236,26 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(const AdaptParams p) {
   col *= kTileCols;
   const int cols = min(kTileCols, p.site.cols[part] - col);
   const int ld = p.site.n_parts * p.site.max_rank;
-  const int c = 16 * warp + g;
 
-  // B of the first steps, and base, are on their way while s is added up
-  constexpr int kFlight = 8;
-  uint2 lo[kFlight], hi[kFlight];
-  auto fetch = [&](int s, uint2& l, uint2& h) {
-    l = h = make_uint2(0u, 0u);
-    if (s >= rows.steps) return;
-    const Run& run = rows.run[rows.step_run[s]];
-    const int j = 16 * rows.step_j[s] + 4 * t;
-    const T* B = static_cast<const T*>(run.b) + (long long)(left + col + c) * run.rank + j;
-    if (j < run.rank && c < cols) l = *reinterpret_cast<const uint2*>(B);
-    if (j < run.rank && c + 8 < cols) h = *reinterpret_cast<const uint2*>(B + 8ll * run.rank);
-  };
+  // A warp takes a run, or a share of its outputs where there are fewer runs than
+  // warps.  Its first B, and base, are on their way while s is added up.
+  const int share = rows.runs > 4 ? 1 : rows.runs > 2 ? 2 : rows.runs > 1 ? 4 : 8;   // warps of a run
+  const int mine = warp / share;
+  const Run run = rows.run[mine < rows.runs ? mine : 0];
+  const int tiles = mine < rows.runs ? kWarps / share : 0, tile0 = warp % share * (kWarps / share);
+  const T* B = static_cast<const T*>(run.b) + (long long)(left + col + 16 * tile0 + g) * run.rank + 4 * t;
+  uint2 lo[kWarps], hi[kWarps];
+  auto fetch = [&](int j0) {
 #pragma unroll
-  for (int f = 0; f < kFlight; ++f) fetch(f, lo[f], hi[f]);
+    for (int n = 0; n < kWarps; ++n) {
+      lo[n] = hi[n] = make_uint2(0u, 0u);
+      const int c = 16 * (tile0 + n) + g;
+      const bool in = n < tiles && j0 + 4 * t < run.rank;
+      if (in && c < cols) lo[n] = *reinterpret_cast<const uint2*>(B + (long long)(16 * n) * run.rank + j0);
+      if (in && c + 8 < cols) hi[n] = *reinterpret_cast<const uint2*>(B + (long long)(16 * n + 8) * run.rank + j0);
+    }
+  };
+  fetch(0);
   const int r = warp, i = 4 * lane;   // (the row and the outputs that this lane writes)
   const int id = rows.id[r];
   const long long at = left + col + i;
@@ -310,30 +314,34 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(const AdaptParams p) {
     if (lane == 0) factor[r] = rows.run[k].scale * up;
   }
   __syncthreads();
-  float acc[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int s0 = 0; s0 < rows.steps; s0 += kFlight) {
+  if (tiles) {
+    float acc[kWarps][4];
 #pragma unroll
-    for (int f = 0; f < kFlight; ++f) {
-      const int s = s0 + f;
-      if (s < rows.steps) {
-        const int k = rows.step_run[s], j = 16 * rows.step_j[s] + 4 * t;
-        const bool in_run = g >= rows.run[k].first && g < rows.run[k].end;
-        const uint2 l = lo[f], h = hi[f];
-        fetch(s + kFlight, lo[f], hi[f]);
+    for (int n = 0; n < kWarps; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+    const bool in_run = g >= run.first && g < run.end;
+    for (int j0 = 0; j0 < run.rank; j0 += 16) {
+      if (j0) fetch(j0);
+      uint2 y[TERMS];
 #pragma unroll
-        for (int m = TERMS - 1; m >= 0; --m) {
-          const uint2 y = in_run ? *reinterpret_cast<const uint2*>(&terms[m][g][j]) : make_uint2(0u, 0u);
-          mma<T>(acc, l.x, h.x, l.y, h.y, y.x, y.y);
+      for (int m = 0; m < TERMS; ++m)
+        y[m] = in_run ? *reinterpret_cast<const uint2*>(&terms[m][g][j0 + 4 * t]) : make_uint2(0u, 0u);
+#pragma unroll
+      for (int n = 0; n < kWarps; ++n)
+        if (n < tiles)
+#pragma unroll
+          for (int m = TERMS - 1; m >= 0; --m) mma<T>(acc[n], lo[n].x, hi[n].x, lo[n].y, hi[n].y, y[m].x, y[m].y);
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int row = 2 * t + e;
+      if (row < run.first || row >= run.end) continue;
+      const float f = factor[row];
+#pragma unroll
+      for (int n = 0; n < kWarps; ++n)
+        if (n < tiles) {
+          tile[row][16 * (tile0 + n) + g] = acc[n][e] * f;
+          tile[row][16 * (tile0 + n) + g + 8] = acc[n][2 + e] * f;
         }
-        if (s + 1 == rows.steps || rows.step_run[s + 1] != k) {   // the run's last
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int row = 2 * t + (e & 1);
-            if (row >= rows.run[k].first && row < rows.run[k].end) tile[row][c + 8 * (e >> 1)] = acc[e] * factor[row];
-            acc[e] = 0.f;
-          }
-        }
-      }
     }
   }
   __syncthreads();
@@ -384,6 +392,7 @@ __device__ __forceinline__ void cp_wait() {
 }
 
 struct Tile {
+  int tiles;           // of the batch
   int row0, rows;      // 0 rows: none
   int id;              // adapter, or kNone
   kvr_adapter ad;
@@ -416,6 +425,7 @@ __device__ __forceinline__ void find_tile(const AdaptParams& p, int t, Tile& til
   __syncthreads();
   int at = run - sum;
   for (int k = 0; k < warp; ++k) at += warp_sum[k];
+  if (threadIdx.x == kThreads - 1) tile.tiles = at + sum;
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
     if (t >= at && t < at + n[k]) {
@@ -566,82 +576,84 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_tiles_kernel(const AdaptPa
   const cg::cluster_group cluster = cg::this_cluster();
   if (ks > 1) cluster.sync();
   else __syncthreads();
-  const float* from_[kMaxCluster];
+  const int r0 = TR * part_k / ks, r1 = TR * (part_k + 1) / ks;
+  if (ks > 1) {
+    // the cluster's sums of this CTA's rows, in the order of the inputs: four at a
+    // time, all CTAs' on their way together
+    float4 sum[TR * NC / 4 / 2 / kThreads];   // (at most half of the rows)
+    constexpr int kQuads = NC / 4;
+#pragma unroll 1
+    for (int i = threadIdx.x, n = 0; i < (r1 - r0) * kQuads; i += kThreads, ++n) {
+      const int at = (r0 + i / kQuads) * kLd + i % kQuads * 4;
+      float4 v[kMaxCluster];
 #pragma unroll
-  for (int j = 0; j < kMaxCluster; ++j) from_[j] = cluster.map_shared_rank(sums, j < ks ? j : 0);
+      for (int c = 0; c < kMaxCluster; ++c)
+        v[c] = *reinterpret_cast<const float4*>(cluster.map_shared_rank(sums, c < ks ? c : 0) + at);
+      float4 t = v[0];
+#pragma unroll
+      for (int c = 1; c < kMaxCluster; ++c)
+        if (c < ks) {
+          t.x += v[c].x;
+          t.y += v[c].y;
+          t.z += v[c].z;
+          t.w += v[c].w;
+        }
+#pragma unroll
+      for (int k = 0; k < (int)(sizeof(sum) / sizeof(float4)); ++k)
+        if (k == n) sum[k] = t;
+    }
+    cluster.sync();   // (everyone has read them)
+#pragma unroll
+    for (int n = 0; n < (int)(sizeof(sum) / sizeof(float4)); ++n) {
+      const int i = threadIdx.x + n * kThreads;
+      if (i < (r1 - r0) * kQuads)
+        *reinterpret_cast<float4*>(sums + (r0 + i / kQuads) * kLd + i % kQuads * 4) = sum[n];
+    }
+    __syncthreads();
+  }
   const Terms terms(p, TERMS);
-  const int r0 = TR * part_k / ks, r1 = min(TR * (part_k + 1) / ks, tile.rows);
-  const int parts = whole ? p.site.n_parts : 1;
-  for (int r = r0 + warp; r < r1; r += kWarps) {
-    // (a row's ranks 32 at a time, all on their way before any is used)
-    constexpr int kRank32 = NC == 64 ? 2 : NC == 192 ? 3 : 4, kParts = 3;   // (192: of two parts at least)
-    float sum[kParts][kRank32];
+  const int parts = whole ? p.site.n_parts : 1, mr16 = round16(p.site.max_rank);
+  for (int i = r0 * parts + warp; i < min(r1, tile.rows) * parts; i += kWarps) {
+    const int r = i / parts, j = i % parts;
+    float v[KVR_MAX_RANK / 32], big = 0.f;
 #pragma unroll
-    for (int j = 0; j < kParts; ++j)
+    for (int n = 0; n < KVR_MAX_RANK / 32; ++n) {
+      const int q = lane + 32 * n;
+      v[n] = q < rank ? sums[r * kLd + j * rank + q] : 0.f;
+      big = fmaxf(big, fabsf(v[n]));
+      if (v[n] != v[n]) big = INFINITY;
+    }
 #pragma unroll
-      for (int i = 0; i < kRank32; ++i) {
-        const int q = lane + 32 * i;
-        sum[j][i] = 0.f;
-        if (j < parts && q < rank) {
+    for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+    float down;
+    const float up = scale_of(big, down);
+    const int pj = whole ? j : blockIdx.z;
 #pragma unroll
-          for (int c = 0; c < kMaxCluster; ++c)
-            if (c < ks) sum[j][i] += from_[c][r * kLd + j * rank + q];
+    for (int k = 0; k < TERMS; ++k) {
+      T* dst = terms.term<T>(k, tile.row0 + r) + pj * mr16;
+#pragma unroll
+      for (int n = 0; n < KVR_MAX_RANK / 32; ++n) {
+        const int q = lane + 32 * n;
+        if (q < round16(rank)) {
+          const float y = k == 0 ? v[n] * down : v[n];
+          const T h = to<T>(y);
+          dst[q] = h;
+          v[n] = y - from(h);
         }
       }
-#pragma unroll
-    for (int j = 0; j < kParts; ++j) {
-      if (j >= parts) break;
-      float (&v)[kRank32] = sum[j];
-      float big = 0.f;
-#pragma unroll
-      for (int i = 0; i < kRank32; ++i) {
-        big = fmaxf(big, fabsf(v[i]));
-        if (v[i] != v[i]) big = INFINITY;
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-      float down;
-      const float up = scale_of(big, down);
-      const int pj = whole ? j : blockIdx.z;
-#pragma unroll
-      for (int i = 0; i < kRank32; ++i) {
-        const int q = lane + 32 * i;
-        float y = v[i] * down;
-        if (q < round16(rank))
-#pragma unroll
-          for (int k = 0; k < TERMS; ++k) {
-            const T h = to<T>(y);
-            terms.term<T>(k, tile.row0 + r)[pj * round16(p.site.max_rank) + q] = h;
-            y -= from(h);
-          }
-      }
-      if (lane == 0) terms.factor(tile.row0 + r)[pj] = tile.ad.scale * up;
     }
+    if (lane == 0) terms.factor(tile.row0 + r)[pj] = tile.ad.scale * up;
   }
-  if (ks > 1) cluster.sync();   // (the others' sums are read)
 }
 
-// 64 rows and `per` tiles of 128 outputs of one part: the terms stay, the next
-// tile's B and base are on their way while one is multiplied and stored.
+// `c1 - c0` tiles of 128 outputs of one part, of a tile of rows.
 template <class T, class O, int TERMS>
-__global__ void __launch_bounds__(kThreads, 2) expand_tiles_kernel(const AdaptParams p, int per) {
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ Tile tile;
-  __shared__ float factor[TR];
-  dev::pdl_trigger();
-  dev::pdl_wait();
-  find_tile(p, blockIdx.x, tile);
-  if (tile.rows == 0 || (tile.id == kNone && p.base == p.out)) return;
+__device__ __forceinline__ void expand_run(const AdaptParams& p, const Tile& tile, float* factor, uint8_t* smem, int part,
+                                           int left, int c0, int c1) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int wr = warp & 1, wn = warp >> 1;
-  int part = 0, c0 = blockIdx.y, left = 0;
-  for (;; ++part) {
-    const int n = ((p.site.cols[part] + kTileN - 1) / kTileN + per - 1) / per;
-    if (c0 < n) break;
-    c0 -= n;
-    left += p.site.cols[part];
-  }
-  const int c_end = min((c0 + 1) * per * kTileN, p.site.cols[part]);
+  const int c_end = min(c1 * kTileN, p.site.cols[part]);
+  if (tile.id == kNone && p.base == p.out) return;
   const bool adapted = tile.id != kNone;
   const int rank = adapted ? tile.ad.rank : 0, r16 = round16(rank), pitch = 2 * r16 + 16;
   constexpr int kOPitch = kTileN * (int)sizeof(O) + 16, kOChunk = 16 / (int)sizeof(O), kOChunks = kTileN / kOChunk;
@@ -698,9 +710,9 @@ __global__ void __launch_bounds__(kThreads, 2) expand_tiles_kernel(const AdaptPa
   const uint32_t a_at = ss + (wr * 32 + (lane & 15)) * pitch + 16 * (lane >> 4);
   const uint32_t b_at = s_base + TR * kOPitch + (wn * 32 + (lane & 7) + ((lane >> 4) << 3)) * pitch + 16 * ((lane >> 3) & 1);
   int buf = 0;
-  load(c0 * per * kTileN, 0);
+  load(c0 * kTileN, 0);
   cp_commit();
-  for (int col = c0 * per * kTileN; col < c_end; col += kTileN, buf ^= 1) {
+  for (int col = c0 * kTileN; col < c_end; col += kTileN, buf ^= 1) {
     if (col + kTileN < c_end) load(col + kTileN, buf ^ 1);
     cp_commit();
     cp_wait<1>();
@@ -768,6 +780,41 @@ __global__ void __launch_bounds__(kThreads, 2) expand_tiles_kernel(const AdaptPa
   cp_wait<0>();
 }
 
+// The tiles of 64 rows times their tiles of 128 outputs in equal runs, one a CTA:
+// while 64 rows and a part last the terms stay, and the next outputs' B and base
+// are on their way while some are multiplied and stored.
+template <class T, class O, int TERMS>
+__global__ void __launch_bounds__(kThreads, 2) expand_tiles_kernel(const AdaptParams p, int col_tiles) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ Tile tile;
+  __shared__ float factor[TR];
+  dev::pdl_trigger();
+  dev::pdl_wait();
+  find_tile(p, 0, tile);
+  const int units = tile.tiles * col_tiles;
+  int u = (int)((long long)units * blockIdx.x / gridDim.x);
+  const int u1 = (int)((long long)units * (blockIdx.x + 1) / gridDim.x);
+  int now = 0;
+  while (u < u1) {
+    if (u / col_tiles != now) {
+      now = u / col_tiles;
+      __syncthreads();   // (the last one has been read)
+      find_tile(p, now, tile);
+    }
+    const int first = u % col_tiles, n = min(u1 - u, col_tiles - first);
+    int part = 0, before = 0, left = 0, tiles = 0;
+    for (;; ++part) {
+      tiles = (p.site.cols[part] + kTileN - 1) / kTileN;
+      if (first < before + tiles) break;
+      before += tiles;
+      left += p.site.cols[part];
+    }
+    const int c0 = first - before, c1 = min(c0 + n, tiles);   // of this part
+    u += c1 - c0;
+    expand_run<T, O, TERMS>(p, tile, factor, smem, part, left, c0, c1);
+  }
+}
+
 template <class O>
 int expand_tiles_smem(int max_rank, int terms) {
   return 2 * (TR * (kTileN * (int)sizeof(O) + 16) + kTileN * (2 * round16(max_rank) + 16)) +
@@ -809,13 +856,12 @@ cudaError_t launch_tiles(const AdaptParams& p, int sms, cudaStream_t st) {
                   : stacked <= 192 ? launch_shrink_tiles<T, 192, TERMS>(p, tiles, 1, sms, st)
                                    : launch_shrink_tiles<T, 128, TERMS>(p, tiles, p.site.n_parts, sms, st);
   if (e != cudaSuccess) return e;
-  int cols = 0, ctas = 0;
+  int cols = 0;
   for (int j = 0; j < p.site.n_parts; ++j) cols += (p.site.cols[j] + kTileN - 1) / kTileN;
-  // tiles of outputs a CTA: few enough that the CTAs fill the SMs, of two each, twice
-  const int per = (int)std::max(1ll, std::min<long long>(cols, (long long)tiles * cols / (4 * sms)));
-  for (int j = 0; j < p.site.n_parts; ++j) ctas += ((p.site.cols[j] + kTileN - 1) / kTileN + per - 1) / per;
-  return launch_k(expand_tiles_kernel<T, O, TERMS>, dim3(tiles, ctas), dim3(kThreads),
-                  expand_tiles_smem<O>(p.site.max_rank, TERMS), st, p, per);
+  const int smem = expand_tiles_smem<O>(p.site.max_rank, TERMS);
+  const int per_sm = smem <= 110 * 1024 ? 2 : 1;
+  const int ctas = (int)std::min<long long>((long long)sms * per_sm, (long long)tiles * cols);
+  return launch_k(expand_tiles_kernel<T, O, TERMS>, dim3(ctas), dim3(kThreads), smem, st, p, cols);
 }
 
 template <class T, int TERMS, bool X16>
@@ -837,7 +883,12 @@ cudaError_t setup_expand() {
 template <class T>
 cudaError_t launch(const AdaptParams& p, cudaStream_t st) {
   const int blocks = (p.rows + R - 1) / R;
-  cudaError_t e = launch_k(shrink_kernel<T>, dim3(blocks, p.ksplit), kThreads, 0, st, p);
+  // CTAs of a tile's part: enough that a warp has one step, if all sequences are alike and differ in
+  // their adapters
+  const int runs = std::min(R, (R * p.n_seq + p.rows - 1) / p.rows);
+  const int steps = runs * ((p.site.n_parts * p.site.max_rank + 15) / 16);
+  const dim3 shrink_grid(blocks, p.ksplit, std::min((steps + kWarps - 1) / kWarps, 4));
+  cudaError_t e = launch_k(shrink_kernel<T>, shrink_grid, dim3(kThreads), 0, st, p);
   if (e != cudaSuccess) return e;
   int tiles = 0;
   for (int j = 0; j < p.site.n_parts; ++j) tiles += (p.site.cols[j] + kTileCols - 1) / kTileCols;
