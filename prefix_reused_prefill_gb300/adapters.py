@@ -14,7 +14,7 @@ import numpy as np
 import torch
 
 from .kvr import KvrAdapterSite, KvrError, load_library
-from .sampling import _check, _elsewhere, _raw_stream, _vec
+from .sampling import _check, _current_device, _raw_stream
 
 MAX_RANK = 128
 _TYPES = {torch.bfloat16: 0, torch.float16: 1}
@@ -53,39 +53,47 @@ class Adapters:
                                    (ctypes.c_int * 3)(*cols), _TYPES[self.dtype])
         if self.lib.kvr_adapt_work_bytes(ctypes.byref(self.site), 1) == 0:
             raise KvrError(-1, "a site's adapters, ranks, widths or type are out of their range")
+        self._site = ctypes.byref(self.site)
+        self._call, self._work_bytes = self.lib.kvr_adapt, self.lib.kvr_adapt_work_bytes
         torch.cuda.current_stream(self.device).synchronize()   # the table is there for every stream
 
-    def _rows(self, name: str, x: torch.Tensor, n: int, dtypes) -> int:
-        if x.dtype not in dtypes or x.get_device() != self._index or x.dim() != 2 or x.shape[1] != n \
-                or (n > 1 and x.numel() and x.stride(1) != 1):
-            raise KvrError(-1, f"{name} must be [rows][{n}] of {dtypes} on {self.device}, a row's elements contiguous")
-        return x.stride(0) if x.shape[0] > 1 else n   # (one row's stride means nothing)
+    def _stride(self, x: torch.Tensor, rows: int, n: int) -> int:
+        """Row stride of x [rows][n], -1 where it is none."""
+        if x.get_device() != self._index or x.shape != (rows, n):
+            return -1
+        if x.is_contiguous():
+            return n
+        return x.stride(0) if x.stride(1) == 1 or n == 1 else -1
+
+    def _vector(self, x: torch.Tensor, n: int) -> bool:
+        return x.dtype is torch.int32 and x.get_device() == self._index and x.shape == (n,) and x.is_contiguous()
 
     def kvr_adapt(self, x: torch.Tensor, cu_rows: torch.Tensor, which: torch.Tensor,
                   base: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """base (zeros of x's type if None) + the sequences' adapters of x [rows][k].  cu_rows [n_seq + 1] and which
         [n_seq] are device int32; base and out are [rows][sum of cols] of x's type or float32, and may be one."""
-        if _elsewhere(self._index, stream):   # (memory that the stream may write at once)
-            with torch.cuda.device(self._index), torch.cuda.stream(stream):
+        index = self._index
+        if stream is not None or _current_device() != index:   # (memory that the stream may write at once)
+            with torch.cuda.device(index), torch.cuda.stream(stream):
                 return self.kvr_adapt(x, cu_rows, which, base, out)
-        types = (self.dtype, torch.float32)
-        xs = self._rows("x", x, self.k, (self.dtype,))
-        rows, n_seq = x.shape[0], which.numel()
-        wp, cp = _vec("which", which, n_seq, torch.int32, self._index), _vec("cu_rows", cu_rows, n_seq + 1, torch.int32,
-                                                                             self._index)
-        bp, bs = None, self.n
-        if base is not None:
-            bs, bp = self._rows("base", base, self.n, types), base.data_ptr()
+        rows, n_seq = x.shape[0] if x.dim() == 2 else -1, which.numel()
+        like = self.dtype if base is None else base.dtype
         if out is None:
-            out = torch.empty((rows, self.n), dtype=self.dtype if base is None else base.dtype, device=self.device)
-        os = self._rows("out", out, self.n, types if base is None else (base.dtype,))
-        if out.shape[0] != rows or (base is not None and base.shape[0] != rows):
-            raise KvrError(-1, f"base and out must have x's {rows} rows")
-        wb = self.lib.kvr_adapt_work_bytes(self.site, rows)
+            out = torch.empty((rows, self.n), dtype=like, device=self.device) if rows >= 0 else x
+        elif base is None:
+            like = out.dtype
+        xs, os = self._stride(x, rows, self.k), self._stride(out, rows, self.n)
+        bs, bp = (self.n, None) if base is None else (self._stride(base, rows, self.n), base.data_ptr())
+        if xs < 0 or os < 0 or bs < 0 or x.dtype is not self.dtype or out.dtype is not like \
+                or (like is not self.dtype and like is not torch.float32) or not self._vector(cu_rows, n_seq + 1) \
+                or not self._vector(which, n_seq):
+            raise KvrError(-1, f"x [rows][{self.k}] of {self.dtype}, base and out [rows][{self.n}] of it or float32, cu_rows "
+                               f"[n_seq + 1] and which [n_seq] of int32, all on {self.device}, a row's elements contiguous")
+        wb = self._work_bytes(self._site, rows)
         work = torch.empty(wb, dtype=torch.uint8, device=self.device)
-        rc = self.lib.kvr_adapt(self.site, x.data_ptr(), xs, cp, wp, n_seq, rows, bp, bs, out.data_ptr(), os,
-                                2 if out.dtype is torch.float32 else self.site.type, work.data_ptr(), wb,
-                                _raw_stream(self._index))
+        rc = self._call(self._site, x.data_ptr(), xs, cu_rows.data_ptr(), which.data_ptr(), n_seq, rows, bp, bs,
+                        out.data_ptr(), os, 2 if like is torch.float32 else self.site.type, work.data_ptr(), wb,
+                        _raw_stream(index))
         if rc:
             _check(self.lib, rc)
         return out
