@@ -105,6 +105,31 @@ struct Smem {
 };
 constexpr int kLower = -1, kHigher = -2;
 
+// Two floats in one register pair, and the instructions that take them (each rounded as alone).
+__device__ __forceinline__ u64 two(float lo, float hi) {
+  u64 v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  return v;
+}
+__device__ __forceinline__ u64 two(float x) { return two(x, x); }
+__device__ __forceinline__ void split(u64 v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ u64 add2(u64 a, u64 b) {
+  u64 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ u64 mul2(u64 a, u64 b) {
+  u64 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
+  u64 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ u64 sub2(u64 a, u64 b) { return fma2(b, two(-1.f), a); }
+
 // What a row's tokens weigh.
 constexpr float kFinite = 3.4028234663852886e38f;
 struct Row {
@@ -129,6 +154,15 @@ struct Row {
     const float dl = (max - (d - b)) - (x + b);
     yh = d * ch;
     yl = fmaf(d, ch, -yh) + fmaf(d, cl, dl * ch);
+  }
+  // two at once
+  __device__ __forceinline__ void orders(u64 x, u64& yh, u64& yl) const {
+    const u64 m = two(max);
+    const u64 d = sub2(m, x);
+    const u64 b = sub2(d, m);
+    const u64 dl = sub2(sub2(m, sub2(d, b)), add2(x, b));
+    yh = mul2(d, two(ch));
+    yl = add2(fma2(d, two(ch), mul2(d, two(-ch))), fma2(d, two(cl), mul2(dl, two(ch))));
   }
 };
 
@@ -169,26 +203,41 @@ __device__ __forceinline__ uint32_t steps_of(float yh) {
   return __float_as_uint(fmaf(fminf(yh, 63.96875f), 1024.f, kStepOne)) - __float_as_uint(kStepOne);
 }
 
-// The weight in units of 2^-44, as 2^-(yh + yl) = (s + r) 2^-n with the nearest
+// Two weights in units of 2^-44, as 2^-(yh + yl) = (s + r) 2^-n with the nearest
 // step from the table and the rest by its series, whose first term is a pair of
-// floats.  (One function: wherever a token is weighed it weighs the same.)
-__device__ __forceinline__ u64 weight_fixed(const float2* tab, float yh, float yl) {
+// floats; yh in [0, 63.96875] (`steps`: those of yh, as above, with the float's own bits).
+__device__ __forceinline__ void weights_of_two(const float2* tab, u64 yh, u64 yl, u64 steps, u64& v0, u64& v1) {
   constexpr float kLn2h = 0.693147182464599609375f;
   constexpr float kLn2l = -1.904654323148236e-09f;
+  const u64 f = fma2(add2(steps, two(-kStepOne)), two(-1.f / 1024.f), yh);
+  const u64 zh = mul2(f, two(-kLn2h)), zn = mul2(f, two(kLn2h));
+  const u64 zl = sub2(fma2(f, two(-kLn2h), zn), fma2(f, two(kLn2l), mul2(yl, two(kLn2h))));
+  const u64 e = fma2(mul2(zh, zh), fma2(zh, two(1.f / 6.f), two(0.5f)), zl);   // (z^4 / 24 is below 2^-50)
+  const uint32_t j0 = (uint32_t)steps, j1 = (uint32_t)(steps >> 32);
+  const float2 t0 = tab[j0 & 1023], t1 = tab[j1 & 1023];
+  const u64 px = two(t0.x, t1.x), py = two(t0.y, t1.y);
+  const u64 a = mul2(px, zh);
+  const u64 s = add2(px, a);
+  const u64 rest = add2(fma2(py, zh, fma2(px, zh, mul2(px, zn))), fma2(px, e, py));
+  const u64 r = add2(sub2(a, sub2(s, px)), rest);
+  float s0, s1, r0, r1;
+  split(mul2(s, two(0x1p31f)), s0, s1);
+  split(mul2(r, two(0x1p44f)), r0, r1);
+  const auto whole = [](float s, float r, uint32_t j) {
+    const int n = (j >> 10) & 63;
+    const u64 v = ((u64)__float2uint_rn(s) << (kFix - 31)) + (long long)__float2int_rn(r);
+    return (v + ((1ull << n) >> 1)) >> n;
+  };
+  v0 = whole(s0, r0, j0);
+  v1 = whole(s1, r1, j1);
+}
+
+// One of them.  (One arithmetic: wherever a token is weighed it weighs the same.)
+__device__ __forceinline__ u64 weight_fixed(const float2* tab, float yh, float yl) {
   yh = fminf(yh, 63.96875f);
-  const float t = fmaf(yh, 1024.f, kStepOne);
-  const uint32_t j = __float_as_uint(t) - __float_as_uint(kStepOne);
-  const float f = fmaf(t - kStepOne, -1.f / 1024.f, yh);
-  const float zh = -f * kLn2h;
-  const float zl = fmaf(-f, kLn2h, -zh) - fmaf(f, kLn2l, yl * kLn2h);
-  const float e = fmaf(zh * zh, fmaf(zh, 1.f / 6.f, 0.5f), zl);   // (z^4 / 24 is below 2^-50)
-  const float2 p = tab[j & 1023];
-  const float a = p.x * zh;
-  const float s = p.x + a;
-  const float r = (a - (s - p.x)) + (fmaf(p.y, zh, fmaf(p.x, zh, -a)) + fmaf(p.x, e, p.y));
-  const int n = j >> 10;
-  const u64 v = ((u64)__float2uint_rn(s * 0x1p31f) << (kFix - 31)) + (long long)__float2int_rn(r * 0x1p44f);
-  return (v + ((1ull << n) >> 1)) >> n;
+  u64 v0, v1;
+  weights_of_two(tab, two(yh), two(yl), two(fmaf(yh, 1024.f, kStepOne)), v0, v1);
+  return v0;
 }
 
 // total as a pair of floats
@@ -439,9 +488,27 @@ struct Sampler {
       }
       cluster.sync();
       if (rank) return;
+      // (all CTAs' on their way together; the first one stands in for those that there are not)
+      uint2 n[kMaxCluster], l[kMaxCluster], h[kMaxCluster];
+#pragma unroll
+      for (int j = 1; j < kMaxCluster; ++j) {
+        const Bins& o = cluster.map_shared_rank(&sm, j < ctas ? j : 0)->bins;
+        n[j] = *reinterpret_cast<const uint2*>(&o.cnt[0][b]);
+        if (MASS) {
+          l[j] = *reinterpret_cast<const uint2*>(&o.lo[0][b]);
+          h[j] = *reinterpret_cast<const uint2*>(&o.hi[0][b]);
+        }
+      }
 #pragma unroll
       for (int j = 1; j < kMaxCluster; ++j)
-        if (j < ctas) take(cluster.map_shared_rank(&sm, j)->bins, 0);
+        if (j < ctas) {
+          c[0] += n[j].x;
+          c[1] += n[j].y;
+          if (MASS) {
+            v[0] += (u64)h[j].x << 32 | l[j].x;
+            v[1] += (u64)h[j].y << 32 | l[j].y;
+          }
+        }
     }
     if (front_w == &sm.before_w && warp == 0) {
       u64 fw = 0, rw = 0;
@@ -517,48 +584,59 @@ struct Sampler {
     uint32_t front_c = 0, rest_c = 0;
     for_tokens<1>(c.row, c.lo, c.hi, [&](const float (&x)[4], int i, int n) {
       constexpr int N = 4;
-      float yh[N], yl[N];
-      bool in[N], near = false;
-#pragma unroll
-      for (int k = 0; k < N; ++k) {
-        c.w.orders(x[k], yh[k], yl[k]);
-        in[k] = k < n && c.in_row(x[k], i + k);
-        near |= in[k] && yh[k] < kNothing;
-      }
+      bool in[N];
       if (!MASS) {
 #pragma unroll
         for (int k = 0; k < N; ++k)
-          if (in[k]) atomicAdd(&c.sm.bins.cnt[threadIdx.x % kCopies][c.bin_of(yh[k])], 1u);
-      } else if (!near) {
+          if (k < n && c.in_row(x[k], i + k))
+            atomicAdd(&c.sm.bins.cnt[threadIdx.x % kCopies][c.bin_of((c.w.max - fminf(x[k], kFinite)) * c.w.ch)], 1u);
+        return;
+      }
+      u64 yh[N / 2], yl[N / 2], steps[N / 2];
+      uint32_t j[N];
+      bool near = false;
 #pragma unroll
-        for (int k = 0; k < N; ++k)
-          if (in[k]) {
-            const int b = c.bin_of(yh[k]) - c.bin0;
-            if (b < kBins) atomicAdd(&c.sm.bins.cnt[threadIdx.x % kCopies][b], 1u);   // (b >= 0: the last orders)
-            else ++rest_c;
-          }
-      } else {
-        u64 v[N];
+      for (int k = 0; k < N; k += 2) {
+        c.w.orders(two(fminf(x[k], kFinite), fminf(x[k + 1], kFinite)), yh[k / 2], yl[k / 2]);
+        float y0, y1;
+        split(yh[k / 2], y0, y1);
+        in[k] = k < n && c.in_row(x[k], i + k);
+        in[k + 1] = k + 1 < n && c.in_row(x[k + 1], i + k + 1);
+        near |= (in[k] && y0 < kNothing) || (in[k + 1] && y1 < kNothing);
+        yh[k / 2] = two(fminf(y0, 63.96875f), fminf(y1, 63.96875f));
+        steps[k / 2] = fma2(yh[k / 2], two(1024.f), two(kStepOne));
+        j[k] = (uint32_t)steps[k / 2];
+        j[k + 1] = (uint32_t)(steps[k / 2] >> 32);
+      }
+      u64 v[N] = {0, 0, 0, 0};
+      if (near) {
 #pragma unroll
-        for (int k = 0; k < N; ++k) v[k] = weight_fixed(c.sm.pow2, yh[k], yl[k]);
-        int b[N];
+        for (int k = 0; k < N; k += 2)
+          weights_of_two(c.sm.pow2, yh[k / 2], yl[k / 2], steps[k / 2], v[k], v[k + 1]);
+      }
+      int b[N];
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-          b[k] = -1;
-          if (in[k]) {
-            v[k] = c.left(v[k], i + k);
-            b[k] = c.bin_of(yh[k]) - c.bin0;
-            if (b[k] >= kBins) {
-              b[k] = -1;
-              ++rest_c;
-              rest_w += v[k];
-            } else if (b[k] < 0) {
-              ++front_c;
-              front_w += v[k];
-            }
+      for (int k = 0; k < N; ++k) {
+        b[k] = -1;
+        if (in[k]) {
+          if (c.w.rest) v[k] = c.left(v[k], i + k);
+          b[k] = (int)((j[k] - __float_as_uint(kStepOne)) >> kFine) - c.bin0;
+          if (b[k] >= kBins) {
+            b[k] = -1;
+            ++rest_c;
+            rest_w += v[k];
+          } else if (b[k] < 0) {
+            ++front_c;
+            front_w += v[k];
           }
         }
+      }
+      if (near) {
         c.add(b, v);
+      } else {
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+          if (b[k] >= 0) atomicAdd(&c.sm.bins.cnt[threadIdx.x % kCopies][b[k]], 1u);
       }
     });
     if (MASS) {
@@ -640,7 +718,9 @@ struct Sampler {
     if (rank == 0) {
       int end[kMaxCluster];   // of each CTA's tokens in the list
 #pragma unroll
-      for (int j = 0; j < kMaxCluster; ++j) end[j] = j < ctas ? cluster.map_shared_rank(&sm, j)->filled : 0;
+      for (int j = 0; j < kMaxCluster; ++j) end[j] = cluster.map_shared_rank(&sm, j < ctas ? j : 0)->filled;
+#pragma unroll
+      for (int j = 0; j < kMaxCluster; ++j) end[j] = j < ctas ? end[j] : 0;
 #pragma unroll
       for (int j = 1; j < kMaxCluster; ++j) end[j] += end[j - 1];
       for (int i = threadIdx.x; i < min(n, end[kMaxCluster - 1]); i += kThreads) {
