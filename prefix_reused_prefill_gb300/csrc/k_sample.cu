@@ -74,7 +74,7 @@ __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162f
 __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
 
 struct Bins {
-  uint32_t cnt[kCopies][kBins], lo[kCopies][kBins], hi[kCopies][kBins];
+  uint32_t cnt[kCopies][kBins + 32], lo[kCopies][kBins + 32], hi[kCopies][kBins + 32];   // (Sampler::add)
 };
 struct Smem {
   float2 pow2[1024];
@@ -196,9 +196,17 @@ __device__ __forceinline__ void pow2_neg(const float2* tab, float yh, float yl, 
   r = (a - (s - t.x)) + al;
 }
 
+// the larger of two, NaN if one is
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
+
 // Distances in steps of 1/1024 of an order: the low bits of the float that has a
 // step as its unit.  Distances of 64 orders and more count as the last bin's.
 constexpr float kStepOne = 12582912.f;   // 1.5 * 2^23
+constexpr uint32_t kStepBin = 0x4b400000u >> kFine;   // (its bits: the steps are added to them)
 __device__ __forceinline__ uint32_t steps_of(float yh) {
   return __float_as_uint(fmaf(fminf(yh, 63.96875f), 1024.f, kStepOne)) - __float_as_uint(kStepOne);
 }
@@ -221,12 +229,14 @@ __device__ __forceinline__ void weights_of_two(const float2* tab, u64 yh, u64 yl
   const u64 rest = add2(fma2(py, zh, fma2(px, zh, mul2(px, zn))), fma2(px, e, py));
   const u64 r = add2(sub2(a, sub2(s, px)), rest);
   float s0, s1, r0, r1;
-  split(mul2(s, two(0x1p31f)), s0, s1);
+  split(mul2(s, two(0x1p30f)), s0, s1);
   split(mul2(r, two(0x1p44f)), r0, r1);
   const auto whole = [](float s, float r, uint32_t j) {
-    const int n = (j >> 10) & 63;
-    const u64 v = ((u64)__float2uint_rn(s) << (kFix - 31)) + (long long)__float2int_rn(r);
-    return (v + ((1ull << n) >> 1)) >> n;
+    // (half a unit, 2^(n - 1), joins r: what that leaves of a weight below 2^-32 is a quarter of a unit
+    // in the last 2^-14 of a row)
+    const float half = __uint_as_float(((j << 13) & 0x1f800000u) + (126u << 23));
+    const long long v = (long long)__float2int_rn(s) * (1ll << (kFix - 30)) + __float2int_rn(r + half);
+    return (u64)v >> ((j >> 10) & 63);
   };
   v0 = whole(s0, r0, j0);
   v1 = whole(s1, r1, j1);
@@ -281,7 +291,7 @@ struct Tokens {
       i = left < a - lo ? lo + left : a + 4 * fours + left - (a - lo);
       n = 1;
       x[0] = to_float(row[i]);
-      x[1] = x[2] = x[3] = 0.f;
+      x[1] = x[2] = x[3] = __int_as_float(0x7fffffff);   // (NaN: never one of a row's)
     }
   }
 };
@@ -438,23 +448,21 @@ struct Sampler {
     }
     __syncthreads();
   }
-  // N tokens into their bins (< 0: none), the atomics in flight together
+  // N tokens into their bins (< 0: none), without a branch and the atomics in flight
+  // together: a lane has a bin of its own for what goes nowhere.
   template <int N>
   __device__ __forceinline__ void add(const int (&bin)[N], const u64 (&v)[N]) const {
-    const int c = threadIdx.x % kCopies;
-    uint32_t old[N];
+    const int c = threadIdx.x % kCopies, none = kBins + (threadIdx.x & 31);
+    uint32_t old[N], at[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      at[k] = bin[k] >= 0 ? bin[k] : none;
+      atomicAdd(&sm.bins.cnt[c][at[k]], 1u);
+      old[k] = atomicAdd(&sm.bins.lo[c][at[k]], (uint32_t)v[k]);
+    }
 #pragma unroll
     for (int k = 0; k < N; ++k)
-      if (bin[k] >= 0) {
-        atomicAdd(&sm.bins.cnt[c][bin[k]], 1u);
-        old[k] = atomicAdd(&sm.bins.lo[c][bin[k]], (uint32_t)v[k]);
-      }
-#pragma unroll
-    for (int k = 0; k < N; ++k)
-      if (bin[k] >= 0) {
-        const uint32_t up = (uint32_t)(v[k] >> 32) + (old[k] + (uint32_t)v[k] < old[k] ? 1u : 0u);
-        if (up) atomicAdd(&sm.bins.hi[c][bin[k]], up);
-      }
+      atomicAdd(&sm.bins.hi[c][at[k]], (uint32_t)(v[k] >> 32) + (old[k] + (uint32_t)v[k] < old[k] ? 1u : 0u));
   }
 
   // Running sums over the cluster's bins, after what is in front of them, to the
@@ -584,60 +592,69 @@ struct Sampler {
     uint32_t front_c = 0, rest_c = 0;
     for_tokens<1>(c.row, c.lo, c.hi, [&](const float (&x)[4], int i, int n) {
       constexpr int N = 4;
-      bool in[N];
       if (!MASS) {
 #pragma unroll
         for (int k = 0; k < N; ++k)
-          if (k < n && c.in_row(x[k], i + k))
+          if (c.in_row(x[k], i + k))
             atomicAdd(&c.sm.bins.cnt[threadIdx.x % kCopies][c.bin_of((c.w.max - fminf(x[k], kFinite)) * c.w.ch)], 1u);
         return;
       }
       u64 yh[N / 2], yl[N / 2], steps[N / 2];
-      uint32_t j[N];
-      bool near = false;
+      int b[N];
+      float least = 64.f;
 #pragma unroll
       for (int k = 0; k < N; k += 2) {
         c.w.orders(two(fminf(x[k], kFinite), fminf(x[k + 1], kFinite)), yh[k / 2], yl[k / 2]);
         float y0, y1;
         split(yh[k / 2], y0, y1);
-        in[k] = k < n && c.in_row(x[k], i + k);
-        in[k + 1] = k + 1 < n && c.in_row(x[k + 1], i + k + 1);
-        near |= (in[k] && y0 < kNothing) || (in[k + 1] && y1 < kNothing);
-        yh[k / 2] = two(fminf(y0, 63.96875f), fminf(y1, 63.96875f));
+        y0 = fminf(y0, 63.96875f);
+        y1 = fminf(y1, 63.96875f);
+        least = fminf(least, fminf(y0, y1));
+        yh[k / 2] = two(y0, y1);
         steps[k / 2] = fma2(yh[k / 2], two(1024.f), two(kStepOne));
-        j[k] = (uint32_t)steps[k / 2];
-        j[k + 1] = (uint32_t)(steps[k / 2] >> 32);
+        // (a token that is not the row's has bin -1; the others' are 0 and more)
+        b[k] = x[k] >= c.w.floor ? (int)(((uint32_t)steps[k / 2] >> kFine) - kStepBin) : -1;
+        b[k + 1] = x[k + 1] >= c.w.floor ? (int)(((uint32_t)(steps[k / 2] >> 32) >> kFine) - kStepBin) : -1;
       }
       u64 v[N] = {0, 0, 0, 0};
-      if (near) {
+      if (least < kNothing) {
 #pragma unroll
         for (int k = 0; k < N; k += 2)
           weights_of_two(c.sm.pow2, yh[k / 2], yl[k / 2], steps[k / 2], v[k], v[k + 1]);
-      }
-      int b[N];
+      } else if (!c.bin0) {   // (far behind the first bins, and without weight)
 #pragma unroll
-      for (int k = 0; k < N; ++k) {
-        b[k] = -1;
-        if (in[k]) {
-          if (c.w.rest) v[k] = c.left(v[k], i + k);
-          b[k] = (int)((j[k] - __float_as_uint(kStepOne)) >> kFine) - c.bin0;
+        for (int k = 0; k < N; ++k) rest_c += b[k] >= 0 ? 1 : 0;
+        return;
+      }
+      if (c.w.rest) {
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+          if (b[k] >= 0) {
+            if (place_of(x[k], i + k) < c.w.kept) b[k] = -1;
+            else v[k] = c.left(v[k], i + k);
+          }
+      }
+      if (c.bin0) {
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+          if (b[k] >= 0) {
+            b[k] -= c.bin0;
+            if (b[k] < 0) {
+              ++front_c;
+              front_w += v[k];
+            }
+          }
+      }
+      if (max(max(b[0], b[1]), max(b[2], b[3])) >= kBins) {   // behind the bins
+#pragma unroll
+        for (int k = 0; k < N; ++k)
           if (b[k] >= kBins) {
             b[k] = -1;
             ++rest_c;
             rest_w += v[k];
-          } else if (b[k] < 0) {
-            ++front_c;
-            front_w += v[k];
           }
-        }
       }
-      if (near) {
-        c.add(b, v);
-      } else {
-#pragma unroll
-        for (int k = 0; k < N; ++k)
-          if (b[k] >= 0) atomicAdd(&c.sm.bins.cnt[threadIdx.x % kCopies][b[k]], 1u);
-      }
+      c.add(b, v);
     });
     if (MASS) {
       front_c = __reduce_add_sync(0xffffffffu, front_c);
@@ -690,11 +707,14 @@ struct Sampler {
     const Sampler c = *this;   // (in registers)
     const float2 y = bounds(b0, b1);
     for_tokens<4>(c.row, c.lo, c.hi, [&](const float (&x)[4], int i, int m) {
+      // (the nearest of the four first: most have nothing near enough)
+      const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+      if (!(top >= c.w.floor) || (c.w.max - fminf(top, kFinite)) * c.w.ch >= y.y) return;
       uint32_t hits = 0;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const float yh = (c.w.max - fminf(x[k], kFinite)) * c.w.ch;
-        hits |= (k < m && !(yh < y.x) && !(yh >= y.y) && x[k] >= c.w.floor ? 1u : 0u) << k;
+        hits |= (!(yh < y.x) && !(yh >= y.y) && x[k] >= c.w.floor ? 1u : 0u) << k;
       }
       while (hits) {
         const int k = __ffs(hits) - 1;
@@ -1005,61 +1025,55 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   const int per = (p.vocab + ctas - 1) / ctas;
   const int lo = min(rank * per, p.vocab), hi = min(lo + per, p.vocab);
 
-  // the largest logit, the first of them
+  // the largest logit (NaN if there is one)
   float best = -INFINITY;
-  int best_i = hi;
-  bool bad = false;
   for_tokens<4>(row, lo, hi, [&](const float (&x)[4], int i, int n) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (k < n) {
-        if (x[k] > best || (x[k] == best && i + k < best_i)) {   // (the ends come after the middle)
-          best = x[k];
-          best_i = i + k;
-        }
-        bad |= x[k] != x[k];
-      }
+    best = max_nan(best, x[0]);
+    if (n > 1) best = max_nan(max_nan(best, x[1]), max_nan(x[2], x[3]));
   });
-  bad |= !(heat == 0.f || (heat >= 0x1p-64f && heat <= 0x1p64f)) || min_p != min_p || want.top_p != want.top_p ||
-         !(want.u >= 0.f && want.u < 1.f) || !(want.u_next >= 0.f && want.u_next < 1.f);
+  bool bad = best != best || !(heat == 0.f || (heat >= 0x1p-64f && heat <= 0x1p64f)) || min_p != min_p ||
+             want.top_p != want.top_p || !(want.u >= 0.f && want.u < 1.f) || !(want.u_next >= 0.f && want.u_next < 1.f);
   if (heat == 0.f) {
     heat = 1.f;
     want.top_k = 1;
   }
   if (warp == 1 && lane == 0 && min_p > 0.f) sm.min_orders = (double)heat * log((double)fminf(min_p, 1.f));
   // (a row without a distribution: no key is that large)
-  auto join = [](uint32_t& key, uint32_t& i) {
-    const uint32_t k = __reduce_max_sync(0xffffffffu, key);
-    i = __reduce_min_sync(0xffffffffu, key == k ? i : 0xffffffffu);
-    key = k;
-  };
-  uint32_t key = bad ? 0xffffffffu : (uint32_t)(place_of(best, 0) >> kSampleIndexBits), key_i = (uint32_t)best_i;
-  join(key, key_i);
-  if (lane == 0) {
-    sm.warp_c[warp] = key;
-    sm.warp_i[warp] = key_i;
-  }
+  uint32_t key = bad ? 0xffffffffu : (uint32_t)(place_of(best, 0) >> kSampleIndexBits);
+  key = __reduce_max_sync(0xffffffffu, key);
+  if (lane == 0) sm.warp_c[warp] = key;
   __syncthreads();
-  key = sm.warp_c[lane % kWarps];
-  key_i = sm.warp_i[lane % kWarps];
-  join(key, key_i);
+  key = __reduce_max_sync(0xffffffffu, sm.warp_c[lane % kWarps]);
   cluster.barrier_wait(std::move(arrived));
   if (threadIdx.x < ctas) {
     Smem* o = cluster.map_shared_rank(&sm, threadIdx.x);
     o->best_key[rank] = key;
-    o->best_i[rank] = key_i;
   }
   if (ctas > 1) cluster.sync();
   else __syncthreads();
-  key = lane < ctas ? sm.best_key[lane] : 0;
-  key_i = lane < ctas ? sm.best_i[lane] : 0xffffffffu;
-  join(key, key_i);
-  const int top_token = (int)key_i;
+  key = __reduce_max_sync(0xffffffffu, lane < ctas ? sm.best_key[lane] : 0);
   best = logit_of((u64)key << kSampleIndexBits);
   bad = key == 0xffffffffu || best == -INFINITY;
   float* dist = p.dist ? p.dist + p.dist_stride * r : nullptr;
   // (of what follows every CTA of the cluster decides alike)
   const bool certain = want.top_k == 1 || want.top_p <= 0.f;   // only the first token is kept
+  int top_token = 0;
+  if (certain && !bad) {
+    uint32_t at = kIndexMask;
+    for_tokens<4>(row, lo, hi, [&](const float (&x)[4], int i, int n) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (x[k] == best) at = min(at, (uint32_t)(i + k));
+    });
+    at = __reduce_min_sync(0xffffffffu, at);
+    if (lane == 0) sm.warp_i[warp] = at;
+    __syncthreads();
+    at = __reduce_min_sync(0xffffffffu, sm.warp_i[lane % kWarps]);
+    if (threadIdx.x < ctas) cluster.map_shared_rank(&sm, threadIdx.x)->best_i[rank] = at;
+    if (ctas > 1) cluster.sync();
+    else __syncthreads();
+    top_token = (int)__reduce_min_sync(0xffffffffu, lane < ctas ? sm.best_i[lane] : kIndexMask);
+  }
   if (bad || (certain && !p.cu)) {
     if (dist)
       for (int i = lo + threadIdx.x; i < hi; i += kThreads) dist[i] = !bad && i == top_token ? 1.f : 0.f;
