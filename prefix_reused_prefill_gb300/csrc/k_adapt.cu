@@ -646,7 +646,38 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_tiles_kernel(const AdaptPa
   }
 }
 
-// `c1 - c0` tiles of 128 outputs of one part, of a tile of rows.
+// Eight outputs of a row: base's, and what is added to them.
+template <class O>
+struct Eight {
+  uint4 v[sizeof(O) / 2];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int k = 0; k < (int)sizeof(O) / 2; ++k) v[k] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  __device__ __forceinline__ void load(const O* p) {
+#pragma unroll
+    for (int k = 0; k < (int)sizeof(O) / 2; ++k) v[k] = reinterpret_cast<const uint4*>(p)[k];
+  }
+  __device__ __forceinline__ void store(O* p) const {
+#pragma unroll
+    for (int k = 0; k < (int)sizeof(O) / 2; ++k) reinterpret_cast<uint4*>(p)[k] = v[k];
+  }
+  // pair k += (y0, y1) f
+  __device__ __forceinline__ void add(int k, float y0, float y1, float f) {
+    uint32_t* w = reinterpret_cast<uint32_t*>(v);
+    if constexpr (std::is_same<O, float>::value) {
+      w[2 * k] = __float_as_uint(fmaf(y0, f, __uint_as_float(w[2 * k])));
+      w[2 * k + 1] = __float_as_uint(fmaf(y1, f, __uint_as_float(w[2 * k + 1])));
+    } else {
+      const float2 b = pair_from<O>(w[k]);
+      w[k] = pair_to<O>(fmaf(y0, f, b.x), fmaf(y1, f, b.y));
+    }
+  }
+};
+
+// `c1 - c0` tiles of 128 outputs of one part, of a tile of rows.  The outputs that
+// stand beside one another in a lane's products are chosen: its four pairs are eight
+// in a row, so base and out need no way through shared memory.
 template <class T, class O, int TERMS>
 __device__ __forceinline__ void expand_run(const AdaptParams& p, const Tile& tile, float* factor, uint8_t* smem, int part,
                                            int left, int c0, int c1) {
@@ -656,10 +687,8 @@ __device__ __forceinline__ void expand_run(const AdaptParams& p, const Tile& til
   if (tile.id == kNone && p.base == p.out) return;
   const bool adapted = tile.id != kNone;
   const int rank = adapted ? tile.ad.rank : 0, r16 = round16(rank), pitch = 2 * r16 + 16;
-  constexpr int kOPitch = kTileN * (int)sizeof(O) + 16, kOChunk = 16 / (int)sizeof(O), kOChunks = kTileN / kOChunk;
-  const int stage = TR * kOPitch + kTileN * pitch;   // base, then B
-  uint8_t* const terms_at = smem + 2 * stage;
-  const uint32_t ss = dev::smem_u32(terms_at);
+  const int stage = kTileN * pitch;
+  const uint32_t s_base = dev::smem_u32(smem), ss = s_base + 2 * stage;
   // a thread's 16 bytes of a row of ranks (a power of two of them, the last ones without work)
   const int chunks = r16 / 8, shift = chunks > 1 ? 32 - __clz(chunks - 1) : 0;
   const int lr = threadIdx.x >> shift, lc = threadIdx.x & ((1 << shift) - 1), lstep = kThreads >> shift;
@@ -673,51 +702,46 @@ __device__ __forceinline__ void expand_run(const AdaptParams& p, const Tile& til
       }
     if (threadIdx.x < tile.rows) factor[threadIdx.x] = terms.factor(tile.row0 + threadIdx.x)[part];
   }
-  const O* base = p.base ? static_cast<const O*>(p.base) + p.base_stride * tile.row0 + left : nullptr;
-  O* out = static_cast<O*>(p.out) + p.out_stride * tile.row0 + left;
   const T* B = adapted ? static_cast<const T*>(tile.ad.b) + (long long)left * rank : nullptr;
-  constexpr int kORows = kThreads / kOChunks;   // rows of base that the threads copy at once
-  const int orow = threadIdx.x / kOChunks, ocol = threadIdx.x % kOChunks * kOChunk;
-  const uint32_t s_base = dev::smem_u32(smem);
-  const uint32_t o_at = orow * kOPitch + ocol * (int)sizeof(O);
-  const long long base_step = p.base_stride * kORows, out_step = p.out_stride * kORows;
   auto load = [&](int col, int buf) {
-    const uint32_t so = s_base + buf * stage, sb = so + TR * kOPitch;
-    if (base) {
-      const O* src = base + p.base_stride * orow + col + ocol;
-      const bool in = col + ocol < c_end;
-#pragma unroll
-      for (int j = 0; j < TR / kORows; ++j) {
-        const bool v = in && orow + j * kORows < tile.rows;
-        cp16(so + o_at + j * kORows * kOPitch, v ? src + j * base_step : base, v);
-      }
-    }
-    if (adapted && lc < chunks) {
-      const T* src = B + (long long)(col + lr) * rank + 8 * lc;
-      const int step = lstep * rank;
-      uint32_t dst = sb + lr * pitch + 16 * lc;
-      const bool in = 8 * lc < rank;
+    if (!adapted || lc >= chunks) return;
+    const T* src = B + (long long)(col + lr) * rank + 8 * lc;
+    const int step = lstep * rank;
+    const uint32_t dst = s_base + buf * stage + 16 * lc;
+    const bool in = 8 * lc < rank;
+    // output 8 t + 2 n + e of 32 is column 2 t + e of the n-th product
 #pragma unroll 4
-      for (int r = lr; r < kTileN; r += lstep) {
-        const bool v = in && col + r < c_end;
-        cp16(dst, v ? src : B, v);
-        src += step;
-        dst += lstep * pitch;
-      }
+    for (int r = lr; r < kTileN; r += lstep) {
+      const bool v = in && col + r < c_end;
+      cp16(dst + ((r & ~31) | (r & 6) << 2 | (r & 24) >> 2 | (r & 1)) * pitch, v ? src : B, v);
+      src += step;
     }
   };
   // a lane's operand rows
   const uint32_t a_at = ss + (wr * 32 + (lane & 15)) * pitch + 16 * (lane >> 4);
-  const uint32_t b_at = s_base + TR * kOPitch + (wn * 32 + (lane & 7) + ((lane >> 4) << 3)) * pitch + 16 * ((lane >> 3) & 1);
+  const uint32_t b_at = s_base + (wn * 32 + (lane & 7) + 8 * (lane >> 4)) * pitch + 16 * ((lane >> 3) & 1);
+  const int row = wr * 32 + g, ocol = wn * 32 + 8 * t;
+  const O* base = p.base ? static_cast<const O*>(p.base) + p.base_stride * (tile.row0 + row) + left + ocol : nullptr;
+  O* out = static_cast<O*>(p.out) + p.out_stride * (tile.row0 + row) + left + ocol;
+  const long long base8 = 8 * p.base_stride, out8 = 8 * p.out_stride;
+  auto fetch = [&](int col, Eight<O> (&next)[4]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {   // rows 8 k further
+      if (base && col + ocol < c_end && row + 8 * k < tile.rows) next[k].load(base + col + k * base8);
+      else next[k].clear();
+    }
+  };
   int buf = 0;
   load(c0 * kTileN, 0);
   cp_commit();
   for (int col = c0 * kTileN; col < c_end; col += kTileN, buf ^= 1) {
     if (col + kTileN < c_end) load(col + kTileN, buf ^ 1);
     cp_commit();
+    const bool in = col + ocol < c_end;
+    Eight<O> o[4];
+    fetch(col, o);
     cp_wait<1>();
     __syncthreads();
-    uint8_t* const so = smem + buf * stage;
     if (adapted) {
       const uint32_t b_buf = b_at + buf * stage;
       float acc[2][4][4];
@@ -729,7 +753,7 @@ __device__ __forceinline__ void expand_run(const AdaptParams& p, const Tile& til
       for (int kk = 0; kk < r16 / 16; ++kk) {
         uint32_t b[2][4];
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < 2; ++n)   // products 2 n and 2 n + 1
           dev::ldmatrix_x4(b_buf + 16 * n * pitch + 32 * kk, b[n][0], b[n][1], b[n][2], b[n][3]);
 #pragma unroll
         for (int k = TERMS - 1; k >= 0; --k)
@@ -742,40 +766,18 @@ __device__ __forceinline__ void expand_run(const AdaptParams& p, const Tile& til
               mma<T>(acc[m][n], a[0], a[1], a[2], a[3], b[n >> 1][2 * (n & 1)], b[n >> 1][2 * (n & 1) + 1]);
           }
       }
-      // into base's place in shared memory, then out in whole rows
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+      for (int k = 0; k < 4; ++k) {
+        const float f = factor[row + 8 * k];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int r = wr * 32 + m * 16 + 8 * h + g;
-          if (r >= tile.rows) continue;
-          const float f = factor[r];
-#pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            O* o = reinterpret_cast<O*>(so + r * kOPitch) + wn * 32 + 8 * n + 2 * t;
-            float2 v = make_float2(0.f, 0.f);
-            if constexpr (std::is_same<O, float>::value) {
-              if (base) v = *reinterpret_cast<const float2*>(o);
-              *reinterpret_cast<float2*>(o) = make_float2(fmaf(acc[m][n][2 * h], f, v.x), fmaf(acc[m][n][2 * h + 1], f, v.y));
-            } else {
-              if (base) v = pair_from<O>(*reinterpret_cast<const uint32_t*>(o));
-              *reinterpret_cast<uint32_t*>(o) = pair_to<O>(fmaf(acc[m][n][2 * h], f, v.x), fmaf(acc[m][n][2 * h + 1], f, v.y));
-            }
-          }
-        }
-      __syncthreads();
+        for (int n = 0; n < 4; ++n) o[k].add(n, acc[k >> 1][n][2 * (k & 1)], acc[k >> 1][n][2 * (k & 1) + 1], f);
+      }
     }
-    if (col + ocol < c_end) {
-      O* dst = out + p.out_stride * orow + col + ocol;
+    if (in)
 #pragma unroll
-      for (int j = 0; j < TR / kORows; ++j)
-        if (orow + j * kORows < tile.rows) {
-          uint4 v = *reinterpret_cast<const uint4*>(so + o_at + j * kORows * kOPitch);
-          if (!adapted && !base) v = make_uint4(0u, 0u, 0u, 0u);
-          *reinterpret_cast<uint4*>(dst + j * out_step) = v;
-        }
-    }
-    __syncthreads();   // (the next loads overwrite it)
+      for (int k = 0; k < 4; ++k)
+        if (row + 8 * k < tile.rows) o[k].store(out + col + k * out8);
+    __syncthreads();   // (the next loads overwrite B)
   }
   cp_wait<0>();
 }
@@ -815,10 +817,8 @@ __global__ void __launch_bounds__(kThreads, 2) expand_tiles_kernel(const AdaptPa
   }
 }
 
-template <class O>
 int expand_tiles_smem(int max_rank, int terms) {
-  return 2 * (TR * (kTileN * (int)sizeof(O) + 16) + kTileN * (2 * round16(max_rank) + 16)) +
-         terms * TR * (2 * round16(max_rank) + 16);
+  return (2 * kTileN + terms * TR) * (2 * round16(max_rank) + 16);
 }
 template <int NC>
 constexpr int shrink_tiles_smem() {
@@ -858,7 +858,7 @@ cudaError_t launch_tiles(const AdaptParams& p, int sms, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   int cols = 0;
   for (int j = 0; j < p.site.n_parts; ++j) cols += (p.site.cols[j] + kTileN - 1) / kTileN;
-  const int smem = expand_tiles_smem<O>(p.site.max_rank, TERMS);
+  const int smem = expand_tiles_smem(p.site.max_rank, TERMS);
   const int per_sm = smem <= 110 * 1024 ? 2 : 1;
   const int ctas = (int)std::min<long long>((long long)sms * per_sm, (long long)tiles * cols);
   return launch_k(expand_tiles_kernel<T, O, TERMS>, dim3(ctas), dim3(kThreads), smem, st, p, cols);
@@ -877,7 +877,7 @@ cudaError_t setup_shrink() {
 template <class T, class O, int TERMS>
 cudaError_t setup_expand() {
   return cudaFuncSetAttribute(expand_tiles_kernel<T, O, TERMS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              expand_tiles_smem<O>(KVR_MAX_RANK, TERMS));
+                              expand_tiles_smem(KVR_MAX_RANK, TERMS));
 }
 
 template <class T>
