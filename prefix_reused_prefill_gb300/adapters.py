@@ -14,7 +14,7 @@ import numpy as np
 import torch
 
 from .kvr import KvrAdapterSite, KvrError, load_library
-from .sampling import _check, _current_device, _raw_stream
+from .sampling import _check, _current_device, _raw_stream, _work_alloc, _work_free
 
 MAX_RANK = 128
 _TYPES = {torch.bfloat16: 0, torch.float16: 1}
@@ -89,11 +89,11 @@ class Adapters:
                 or not self._vector(which, n_seq):
             raise KvrError(-1, f"x [rows][{self.k}] of {self.dtype}, base and out [rows][{self.n}] of it or float32, cu_rows "
                                f"[n_seq + 1] and which [n_seq] of int32, all on {self.device}, a row's elements contiguous")
-        wb = self._work_bytes(self._site, rows)
-        work = torch.empty(wb, dtype=torch.uint8, device=self.device)
+        raw, wb = _raw_stream(index), self._work_bytes(self._site, rows)
+        work = _work_alloc(max(wb, 16), raw)
         rc = self._call(self._site, x.data_ptr(), xs, cu_rows.data_ptr(), which.data_ptr(), n_seq, rows, bp, bs,
-                        out.data_ptr(), os, 2 if like is torch.float32 else self.site.type, work.data_ptr(), wb,
-                        _raw_stream(index))
+                        out.data_ptr(), os, 2 if like is torch.float32 else self.site.type, work, wb, raw)
+        _work_free(work)
         if rc:
             _check(self.lib, rc)
         return out

@@ -18,6 +18,9 @@ from .kvr import KvrError, KvrSampling, load_library
 _TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _current_device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream   # the current stream's handle (a Stream object costs 2 us)
+# A call's working memory: from torch's allocator without a tensor around it (which costs as much as a
+# launch), given back when the call has been made; work on the stream that follows may have it then.
+_work_alloc, _work_free = torch._C._cuda_cudaCachingAllocator_raw_alloc, torch._C._cuda_cudaCachingAllocator_raw_delete
 Setting = Optional[Union[torch.Tensor, float, int]]
 
 
@@ -125,10 +128,11 @@ def kvr_accept(logits: torch.Tensor, tokens: torch.Tensor, cu_rows: torch.Tensor
     st, keep = _settings(shape, index, temperature, top_k, min_p, top_p)
     accepted = torch.empty(shape, dtype=i32, device=device)
     following = torch.empty(shape, dtype=i32, device=device)
-    wb = lib.kvr_accept_work_bytes(rows)
-    work = torch.empty(wb, dtype=torch.uint8, device=device)
+    raw, wb = _raw_stream(index), lib.kvr_accept_work_bytes(rows)
+    work = _work_alloc(max(wb, 16), raw)
     rc = lib.kvr_accept(logits.data_ptr(), kind, ls, rows, vocab, st, n, cp, tp, qp, qs, up, np, accepted.data_ptr(),
-                        following.data_ptr(), work.data_ptr(), wb, _raw_stream(index))
+                        following.data_ptr(), work, wb, raw)
+    _work_free(work)
     if rc:
         _check(lib, rc)
     return accepted, following
