@@ -717,12 +717,14 @@ int kvr_sample(const void* logits, int type, long long stride, int rows, int voc
  *   tokens       device int32 [rows].  A draft outside the vocabulary does not stay.
  *   draft_probs  float [rows][vocab], row stride draft_stride: q of the draft after each
  *                row (no last row of a sequence is read); null: each draft was certain
- *                (looked up, or taken greedily): q = 1 at d.
+ *                (looked up, or taken greedily): q = 1 at d.  An entry that is below 0
+ *                or NaN counts as 0 in p - q.
  *   u            float [rows] (last rows' are not read); u_next float [n_seq].
  *   accepted     int32 [n_seq], drafts that stay.  next: int32 [n_seq], the token after
  *                them, -1 where that row has no distribution; both for a sequence
  *                without rows: 0 and -1.
  *   work         kvr_accept_work_bytes(rows) bytes, 16-byte aligned, for this call alone.
+ * accepted, next and work share no memory with the inputs.
  */
 size_t kvr_accept_work_bytes(int rows);
 int kvr_accept(const void* logits, int type, long long stride, int rows, int vocab,

@@ -47,8 +47,9 @@ class Adapters:
                         or x.data_ptr() % 16:
                     raise KvrError(-1, f"adapter {i}: contiguous {self.dtype} matrices on {self.device}")
             table[i] = (a.data_ptr(), b.data_ptr(), rank, scale)
-        self._keep = [t for a, b, _ in adapters for t in (a, b)]
         self._table = torch.from_numpy(table.view(np.uint8)).to(self.device)
+        self._keep = [self._table] + [t for a, b, _ in adapters for t in (a, b)]
+        self._streams = set()
         self.site = KvrAdapterSite(self._table.data_ptr(), len(adapters), int(table["rank"].max()), self.k, len(cols),
                                    (ctypes.c_int * 3)(*cols), _TYPES[self.dtype])
         if self.lib.kvr_adapt_work_bytes(ctypes.byref(self.site), 1) == 0:
@@ -56,6 +57,15 @@ class Adapters:
         self._site = ctypes.byref(self.site)
         self._call, self._work_bytes = self.lib.kvr_adapt, self.lib.kvr_adapt_work_bytes
         torch.cuda.current_stream(self.device).synchronize()   # the table is there for every stream
+
+    def used_on(self, raw: int):
+        """Work on the current stream (handle raw) reads the adapters: their memory is not handed out anew before it
+        is done."""
+        if raw not in self._streams:
+            stream = torch.cuda.current_stream(self.device)
+            for t in self._keep:
+                t.record_stream(stream)
+            self._streams.add(raw)
 
     def _stride(self, x: torch.Tensor, rows: int, n: int) -> int:
         """Row stride of x [rows][n], -1 where it is none."""
@@ -90,10 +100,14 @@ class Adapters:
             raise KvrError(-1, f"x [rows][{self.k}] of {self.dtype}, base and out [rows][{self.n}] of it or float32, cu_rows "
                                f"[n_seq + 1] and which [n_seq] of int32, all on {self.device}, a row's elements contiguous")
         raw, wb = _raw_stream(index), self._work_bytes(self._site, rows)
+        if raw not in self._streams:
+            self.used_on(raw)
         work = _work_alloc(max(wb, 16), raw)
-        rc = self._call(self._site, x.data_ptr(), xs, cu_rows.data_ptr(), which.data_ptr(), n_seq, rows, bp, bs,
-                        out.data_ptr(), os, 2 if like is torch.float32 else self.site.type, work, wb, raw)
-        _work_free(work)
+        try:
+            rc = self._call(self._site, x.data_ptr(), xs, cu_rows.data_ptr(), which.data_ptr(), n_seq, rows, bp, bs,
+                            out.data_ptr(), os, 2 if like is torch.float32 else self.site.type, work, wb, raw)
+        finally:
+            _work_free(work)
         if rc:
             _check(self.lib, rc)
         return out

@@ -793,7 +793,8 @@ __global__ void __launch_bounds__(kThreads, 2) expand_tiles_kernel(const AdaptPa
   dev::pdl_trigger();
   dev::pdl_wait();
   find_tile(p, 0, tile);
-  const int units = tile.tiles * col_tiles;
+  // (no more tiles than sequences in their order can have)
+  const int units = min(tile.tiles, p.rows / TR + min(p.n_seq, p.rows)) * col_tiles;
   int u = (int)((long long)units * blockIdx.x / gridDim.x);
   const int u1 = (int)((long long)units * (blockIdx.x + 1) / gridDim.x);
   int now = 0;

@@ -397,7 +397,7 @@ struct Scan {
       }
     }
     sync();
-    const int i = sm.found;
+    const int i = min(max(sm.found, 0), max(n - 1, 0));   // (an entry, whatever the weights were)
     weight = sm.run_w;
     sync();
     return i;
@@ -426,7 +426,7 @@ struct Sampler {
   __device__ __forceinline__ u64 left(u64 v, int i) const {
     if (!w.rest) return v;
     if (!w.q) return i == w.draft ? 0 : v;
-    const double d = (double)v - (double)w.q[i] * w.total;
+    const double d = (double)v - fmax((double)w.q[i], 0.) * w.total;   // (never more than the token's own weight)
     return d > 0. ? (u64)__double2ll_rn(d) : 0;
   }
   // whether a token is one of the row's

@@ -103,13 +103,15 @@ int attn_nsplit(int Hkv, int R, int kend_max, int target) {
   return std::max(1, std::min(ns, kMaxSplits));
 }
 
-// What the host says of a batch's requests, and what comes back (one copy each way).
-struct RequestsDev {
+// What the host says of a batch's requests (a kernel's argument), and what comes back (one copy).
+struct Requests {
   int32_t cu[KVR_MAX_BRANCHES + 1], which[KVR_MAX_BRANCHES];
   int32_t tokens[kVerifyMaxRows];
   float u[kVerifyMaxRows], u_next[KVR_MAX_BRANCHES];
   float temperature[KVR_MAX_BRANCHES], min_p[KVR_MAX_BRANCHES], top_p[KVR_MAX_BRANCHES];
   int32_t top_k[KVR_MAX_BRANCHES];
+};
+struct RequestsDev : Requests {
   int32_t outcome[kVerifyMaxRows];
   struct Result {
     int32_t accepted[KVR_MAX_BRANCHES], next[KVR_MAX_BRANCHES];
@@ -1453,10 +1455,18 @@ bool adapters_fit(const kvr_config& k, const kvr_adapter_site* sites, int* bad) 
   return true;
 }
 
+static_assert(sizeof(Requests) % 4 == 0 && sizeof(Requests) <= 4000, "they travel as a kernel's argument");
+__global__ void put_requests(const Requests in, Requests* to) {
+  dev::pdl_trigger();
+  dev::pdl_wait();
+  const int32_t* src = reinterpret_cast<const int32_t*>(&in);
+  for (int i = threadIdx.x; i < (int)(sizeof in / 4); i += blockDim.x) reinterpret_cast<int32_t*>(to)[i] = src[i];
+}
+
 int batch_common(kvr_ctx* c, int n_seq, const int* slots, const int* lens, const int32_t* tokens,
                  const void* hidden, const kvr_layer_weights* w, void* out, void* stream, int max_m,
                  const __nv_bfloat16* head_gain, const kvr_adapters* adapters = nullptr, const int* which = nullptr,
-                 RequestsDev* requests = nullptr) {
+                 Requests* requests = nullptr) {
   if (!c) return KVR_ERR_ARG;
   if (n_seq < 1 || n_seq > KVR_MAX_BRANCHES || !slots || !lens || !tokens || !hidden || (!out && !head_gain))
     return fail(c, KVR_ERR_ARG, "bad batch arguments");
@@ -1508,12 +1518,11 @@ int batch_common(kvr_ctx* c, int n_seq, const int* slots, const int* lens, const
   if (c->fault == 2) return fail(c, KVR_ERR_FAULT, "injected launch fault");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (adapters || requests) {
-    RequestsDev host;
+    Requests host;
     if (!requests) memset(requests = &host, 0, sizeof host);
     for (int j = 0; j <= n_seq; ++j) requests->cu[j] = rows.off[j];
     for (int j = 0; j < n_seq && which; ++j) requests->which[j] = which[j];
-    // (from pageable memory: copied before the call returns)
-    const cudaError_t e = cudaMemcpyAsync(c->requests, requests, offsetof(RequestsDev, outcome), cudaMemcpyHostToDevice, st);
+    const cudaError_t e = launch_k(put_requests, dim3(1), dim3(256), 0, st, *requests, static_cast<Requests*>(c->requests));
     if (e != cudaSuccess) return cuda_fail(c, e, "requests upload");
   }
   int rc = run_stack(c, rows, hidden, w, out, st, head_gain, nullptr, adapters ? &ad : nullptr);
@@ -1989,7 +1998,7 @@ int kvr_verify_sample_batch(kvr_ctx* c, int n_seq, const int* slots, const int* 
   if (total > kVerifyMaxRows) return fail(c, KVR_ERR_ARG, "%d rows exceed %d for this call", total, kVerifyMaxRows);
   if (draft_probs && total > 1 && draft_stride < head->vocab)
     return fail(c, KVR_ERR_ARG, "the drafts' row stride must cover a row");
-  RequestsDev req;
+  Requests req;
   memset(&req, 0, sizeof req);
   for (int i = 0; i < total; ++i) {
     req.tokens[i] = tokens[i];
@@ -2010,6 +2019,7 @@ int kvr_verify_sample_batch(kvr_ctx* c, int n_seq, const int* slots, const int* 
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   rc = head_logits(c, st, total, head, logits);
   RequestsDev* d = c->requests;
+  RequestsDev::Result result;
   if (!rc) {
     SampleParams p = {};
     p.logits = logits;
@@ -2032,7 +2042,7 @@ int kvr_verify_sample_batch(kvr_ctx* c, int n_seq, const int* slots, const int* 
     if (e != cudaSuccess) rc = cuda_fail(c, e, "sample launch");
   }
   if (!rc) {
-    const cudaError_t e = cudaMemcpyAsync(&req.result, &d->result, sizeof req.result, cudaMemcpyDeviceToHost, st);
+    const cudaError_t e = cudaMemcpyAsync(&result, &d->result, sizeof result, cudaMemcpyDeviceToHost, st);
     if (e != cudaSuccess) rc = cuda_fail(c, e, "result readback");
   }
   if (!rc) rc = kvr_sync_status(c, stream);
@@ -2041,8 +2051,8 @@ int kvr_verify_sample_batch(kvr_ctx* c, int n_seq, const int* slots, const int* 
     return rc;
   }
   for (int j = 0; j < n_seq; ++j) {
-    accepted[j] = req.result.accepted[j];
-    next_tokens[j] = req.result.next[j];
+    accepted[j] = result.accepted[j];
+    next_tokens[j] = result.next[j];
     c->slots[slots[j]].tokens.resize(p0[j] + 1 + accepted[j]);
   }
   return KVR_OK;

@@ -42,6 +42,35 @@ constexpr int kMaxSampleRows = 1 << 20;
 int type_bytes(int type) { return type == KVR_ACT_F32 ? 4 : 2; }
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
+// Rows of memory: n of `width` bytes, `stride` bytes apart (one row: any).
+struct Span {
+  const void* p;
+  long long n, stride, width;
+  Span(const void* p_, long long width_) : p(p_), n(1), stride(width_), width(width_) {}
+  Span(const void* p_, long long n_, long long stride_, long long width_) : p(p_), n(n_), stride(stride_), width(width_) {}
+  long long bytes() const { return (n - 1) * stride + width; }
+};
+// Whether two of them share a byte.  (Rows that stand among one another at different strides count as
+// sharing.)
+bool shared(const Span& a, const Span& b) {
+  if (!a.p || !b.p || a.n < 1 || b.n < 1) return false;
+  const long long off = (long long)((uintptr_t)b.p - (uintptr_t)a.p);   // of b, from a
+  if (off >= a.bytes() || -off >= b.bytes()) return false;
+  if (b.n == 1) {
+    const long long i = off < a.width ? 0 : (off - a.width) / a.stride + 1;   // the first row that ends behind b's start
+    return i < a.n && i * a.stride < off + b.width;
+  }
+  if (a.n == 1) return shared(b, a);
+  if (a.stride != b.stride) return true;
+  const long long in = ((off % a.stride) + a.stride) % a.stride;   // of b's rows, from the start of a's
+  return in < a.width || in + b.width > a.stride;
+}
+bool shared_with_any(const Span& out, const Span* in, int n) {
+  for (int i = 0; i < n; ++i)
+    if (shared(out, in[i])) return true;
+  return false;
+}
+
 int logits_check(const void* logits, int type, long long stride, int rows, int vocab, const kvr_sampling* s) {
   if (type != KVR_ACT_F32 && type != KVR_ACT_BF16 && type != KVR_ACT_F16)
     return fail(KVR_ERR_ARG, "logits of type %d", type);
@@ -85,12 +114,19 @@ int kvr_sample(const void* logits, int type, long long stride, int rows, int voc
     return fail(KVR_ERR_ARG, "missing or misaligned u, token, prob or dist");
   if (dist && rows > 1 && dist_stride < vocab) return fail(KVR_ERR_ARG, "dist's row stride must cover a row");
   SampleParams p = {};
+  if (settings) p.s = *settings;
+  const long long n = 4ll * rows, es = type_bytes(type);
+  const Span out[3] = {{token, n}, {prob, n}, {dist, rows, rows > 1 ? 4 * dist_stride : 4ll * vocab, 4ll * vocab}};
+  const Span in[6] = {{logits, rows, rows > 1 ? es * stride : es * vocab, es * vocab},
+                      {u, n}, {p.s.temperature, n}, {p.s.top_k, n}, {p.s.min_p, n}, {p.s.top_p, n}};
+  for (int i = 0; i < 3; ++i)
+    if (shared_with_any(out[i], in, 6) || shared_with_any(out[i], out, i))
+      return fail(KVR_ERR_ARG, "token, prob or dist shares memory with another argument");
   p.logits = logits;
   p.stride = stride;
   p.rows = rows;
   p.vocab = vocab;
   p.type = type;
-  if (settings) p.s = *settings;
   p.u = u;
   p.token = token;
   p.prob = prob;
@@ -117,12 +153,21 @@ int kvr_accept(const void* logits, int type, long long stride, int rows, int voc
   if (!work || !aligned(work, 16) || work_bytes < kvr_accept_work_bytes(rows))
     return fail(KVR_ERR_CAPACITY, "work area missing, misaligned or smaller than %zu bytes", kvr_accept_work_bytes(rows));
   SampleParams p = {};
+  if (settings) p.s = *settings;
+  const long long n = 4ll * rows, ns = 4ll * n_seq, es = type_bytes(type);
+  const Span out[3] = {{accepted, ns}, {next, ns}, {work, n}};
+  const Span in[10] = {{logits, rows, rows > 1 ? es * stride : es * vocab, es * vocab},
+                       {draft_probs, rows, rows > 1 ? 4 * draft_stride : 4ll * vocab, 4ll * vocab},
+                       {rows ? tokens : nullptr, n}, {rows ? u : nullptr, n}, {cu_rows, ns + 4}, {u_next, ns},
+                       {p.s.temperature, ns}, {p.s.top_k, ns}, {p.s.min_p, ns}, {p.s.top_p, ns}};
+  for (int i = 0; i < 3; ++i)
+    if (shared_with_any(out[i], in, 10) || shared_with_any(out[i], out, i))
+      return fail(KVR_ERR_ARG, "accepted, next or work shares memory with another argument");
   p.logits = logits;
   p.stride = stride;
   p.rows = rows;
   p.vocab = vocab;
   p.type = type;
-  if (settings) p.s = *settings;
   p.u = u;
   p.cu = cu_rows;
   p.n_seq = n_seq;
@@ -160,16 +205,16 @@ int kvr_adapt(const kvr_adapter_site* site, const void* x, long long x_stride, c
       (base && (base_stride < n || base_stride % 8)))
     return fail(KVR_ERR_ARG, "row strides must cover a row and be multiples of 8");
   if (base == out && base_stride != out_stride) return fail(KVR_ERR_ARG, "base is out, but its stride is another");
-  const long long size = out_type == KVR_ACT_F32 ? 4 : 2;
-  const auto apart = [&](const void* a, long long bytes) {
-    const uintptr_t p = (uintptr_t)a, q = (uintptr_t)out;
-    return p + bytes <= q || q + ((rows - 1) * out_stride + n) * size <= p;
-  };
-  if (!apart(x, ((rows - 1) * x_stride + site->k) * 2) ||
-      (base && base != out && !apart(base, ((rows - 1) * base_stride + n) * size)))
-    return fail(KVR_ERR_ARG, "out shares memory with x or other rows of base");
   if (!work || !aligned(work, 16) || work_bytes < adapt_work_bytes(*site, rows))
     return fail(KVR_ERR_CAPACITY, "work area missing, misaligned or smaller than %zu bytes", adapt_work_bytes(*site, rows));
+  const long long size = out_type == KVR_ACT_F32 ? 4 : 2;
+  const Span to[2] = {{out, rows, size * out_stride, size * n}, {work, (long long)adapt_work_bytes(*site, rows)}};
+  const Span in[5] = {{x, rows, 2 * x_stride, 2ll * site->k},
+                      {base == out ? nullptr : base, rows, size * base_stride, size * n},
+                      {cu_rows, 4ll * n_seq + 4}, {which, 4ll * n_seq},
+                      {site->table, (long long)sizeof(kvr_adapter) * site->n_adapters}};
+  if (shared_with_any(to[0], in, 5) || shared_with_any(to[1], in, 5) || shared(to[0], to[1]))
+    return fail(KVR_ERR_ARG, "out or work shares memory with another argument");
   AdaptParams p = {};
   p.site = *site;
   p.x = x;

@@ -430,6 +430,10 @@ class Kvr:
             raise KvrError(-1, "the adapters do not fit the stack's projections")
         with torch.cuda.stream(stream):   # (where one is given) memory that it may write at once
             work = torch.empty(wb, dtype=torch.uint8, device=self.device)
+            raw = torch.cuda.current_stream().cuda_stream
+            for sites_of in adapters[1]:
+                for a in sites_of.values():
+                    a.used_on(raw)
         return KvrAdapters(adapters[0], work.data_ptr(), wb), (ctypes.c_int * n)(*[int(w) for w in which]), work
 
     def kvr_prefill_batch_adapted(self, slots, token_lists, hidden, weights, adapters, which, out=None, stream=None):
@@ -437,10 +441,11 @@ class Kvr:
         arr = weights[0] if isinstance(weights, tuple) else weights
         lens = [len(t) for t in token_lists]
         m, n = sum(lens), len(slots)
-        self._hidden(hidden, m)
+        self._rows("hidden", hidden, (m, self.cfg.hidden))
         if out is None:
             with torch.cuda.stream(stream):
                 out = torch.empty((m, self.cfg.hidden), dtype=torch.bfloat16, device=self.device)
+        self._rows("out", out, (m, self.cfg.hidden))
         ad, which_c, _work = self._adapted(adapters, which, n, m, stream)
         slots_c, lens_c = (ctypes.c_int * max(n, 1))(*[int(s) for s in slots]), (ctypes.c_int * max(n, 1))(*lens)
         self._check(self.lib.kvr_prefill_batch_adapted(
@@ -448,10 +453,9 @@ class Kvr:
             None if ad is None else ctypes.byref(ad), which_c, out.data_ptr(), self._stream(stream)))
         return out
 
-    def _hidden(self, hidden, m):
-        if hidden.dtype != torch.bfloat16 or not hidden.is_cuda or not hidden.is_contiguous() \
-                or hidden.shape != (m, self.cfg.hidden):
-            raise KvrError(-1, f"hidden must be a contiguous bf16 device tensor [{m}][{self.cfg.hidden}]")
+    def _rows(self, name, x, shape, dtype=torch.bfloat16):
+        if x.dtype != dtype or x.device != self.arena.device or not x.is_contiguous() or x.shape != shape:
+            raise KvrError(-1, f"{name} must be a contiguous {dtype} tensor {list(shape)} on {self.arena.device}")
 
     def kvr_verify_sample_batch(self, slots, token_lists, hidden, weights, head, u, u_next, adapters=None, which=None,
                                 temperature=None, top_k=None, min_p=None, top_p=None, draft_probs=None, logits=None,
@@ -464,7 +468,9 @@ class Kvr:
         hs, _keep = head_weight_struct(head)
         lens = [len(t) for t in token_lists]
         m, n = sum(lens), len(slots)
-        self._hidden(hidden, m)
+        self._rows("hidden", hidden, (m, self.cfg.hidden))
+        if out is not None:
+            self._rows("out", out, (m, self.cfg.hidden))
         f32 = lambda name, v, k: self._host(name, v, k, ctypes.c_float)
         st = KvrSampling()
         keep = {name: self._host(name, v, n, ctypes.c_int32 if name == "top_k" else ctypes.c_float)
@@ -474,16 +480,15 @@ class Kvr:
             setattr(st, name, ctypes.addressof(v))
         qp, qs = None, hs.vocab
         if draft_probs is not None:
-            if draft_probs.dtype != torch.float32 or not draft_probs.is_cuda or draft_probs.shape != (m, hs.vocab) \
-                    or (draft_probs.stride(1) != 1 and hs.vocab > 1):
-                raise KvrError(-1, f"draft_probs must be a float32 device tensor [{m}][{hs.vocab}]")
+            if draft_probs.dtype != torch.float32 or draft_probs.device != self.arena.device \
+                    or draft_probs.shape != (m, hs.vocab) or (draft_probs.stride(1) != 1 and hs.vocab > 1):
+                raise KvrError(-1, f"draft_probs must be float32 [{m}][{hs.vocab}] on {self.arena.device}")
             qp, qs = draft_probs.data_ptr(), draft_probs.stride(0) if m > 1 else hs.vocab
         if logits is None:
             with torch.cuda.stream(stream):
                 logits = torch.empty((m, hs.vocab), dtype=torch.float32, device=self.device)
-        elif logits.dtype != torch.float32 or not logits.is_cuda or not logits.is_contiguous() \
-                or logits.shape != (m, hs.vocab):
-            raise KvrError(-1, f"logits must be a contiguous float32 device tensor [{m}][{hs.vocab}]")
+        else:
+            self._rows("logits", logits, (m, hs.vocab), torch.float32)
         ad, which_c, _work = self._adapted(adapters, which, n, m, stream)
         slots_c, lens_c = (ctypes.c_int * max(n, 1))(*[int(s) for s in slots]), (ctypes.c_int * max(n, 1))(*lens)
         nxt, acc = (ctypes.c_int32 * max(n, 1))(), (ctypes.c_int * max(n, 1))()

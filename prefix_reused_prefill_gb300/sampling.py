@@ -130,9 +130,11 @@ def kvr_accept(logits: torch.Tensor, tokens: torch.Tensor, cu_rows: torch.Tensor
     following = torch.empty(shape, dtype=i32, device=device)
     raw, wb = _raw_stream(index), lib.kvr_accept_work_bytes(rows)
     work = _work_alloc(max(wb, 16), raw)
-    rc = lib.kvr_accept(logits.data_ptr(), kind, ls, rows, vocab, st, n, cp, tp, qp, qs, up, np, accepted.data_ptr(),
-                        following.data_ptr(), work, wb, raw)
-    _work_free(work)
+    try:
+        rc = lib.kvr_accept(logits.data_ptr(), kind, ls, rows, vocab, st, n, cp, tp, qp, qs, up, np,
+                            accepted.data_ptr(), following.data_ptr(), work, wb, raw)
+    finally:
+        _work_free(work)
     if rc:
         _check(lib, rc)
     return accepted, following

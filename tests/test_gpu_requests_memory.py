@@ -1,0 +1,111 @@
+"""Memory of sampling and adapters: what shares bytes is refused, what lies between one another is not, and what another
+stream reads outlives its work (GB300)."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+DEV, BF = "cuda", torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    import __graft_entry__
+    __graft_entry__.build()
+
+
+def test_results_that_share_memory_are_refused():
+    from prefix_reused_prefill_gb300 import KvrError, kvr_sample
+    x, u = torch.randn(4, 64, device=DEV), torch.rand(4, device=DEV)
+    before = x.clone()
+    wide = torch.randn(4, 96, device=DEV)
+    for logits, dist in ((x, x), (wide[:, :64], wide[:, 32:]), (wide[:, 32:], wide[:, :64]), (x[:1], x[:1])):
+        with pytest.raises(KvrError):
+            kvr_sample(logits, u[:len(logits)], dist=dist)
+    torch.cuda.synchronize()
+    assert torch.equal(x, before)
+
+
+def test_c_entries_refuse_what_shares_memory():
+    from prefix_reused_prefill_gb300 import load_library
+    lib = load_library()
+    x, f = torch.randn(4, 64, device=DEV), torch.zeros(64, device=DEV)
+    i = torch.zeros(64, dtype=torch.int32, device=DEV)
+    w = torch.zeros(64, dtype=torch.int32, device=DEV)
+    p = lambda t, at=0: t.data_ptr() + 4 * at
+    sample = lambda **k: lib.kvr_sample(*{**dict(x=p(x), type=2, stride=64, rows=4, vocab=64, s=None, u=p(f), token=p(i),
+                                                 prob=p(f, 8), dist=None, ds=0, st=None), **k}.values())
+    assert sample() == 0
+    for k in (dict(token=p(f, 3)), dict(prob=p(f, 3)), dict(prob=p(i, 3)), dict(token=p(x, 255)), dict(dist=p(x), ds=64),
+              dict(dist=p(x, 32), ds=64)):
+        assert sample(**k) == -1, k
+    accept = lambda **k: lib.kvr_accept(*{**dict(x=p(x), type=2, stride=64, rows=4, vocab=64, s=None, n=2, cu=p(i),
+                                                 tokens=p(i, 8), q=None, qs=0, u=p(f), un=p(f, 8), acc=p(i, 16), nxt=p(i, 24),
+                                                 work=p(w), wb=16, st=None), **k}.values())
+    assert accept() == 0
+    for k in (dict(acc=p(i, 2)), dict(nxt=p(i, 17)), dict(acc=p(i, 11)), dict(work=p(i, 8)), dict(nxt=p(f, 9)), dict(acc=p(w, 3)),
+              dict(work=p(x)), dict(nxt=p(x, 200))):
+        assert accept(**k) == -1, k
+    torch.cuda.synchronize()
+
+
+def test_rows_between_one_another():
+    """Logits and their distribution, inputs and outputs, side by side in rows of one buffer."""
+    from prefix_reused_prefill_gb300 import Adapters, KvrError, kvr_sample
+    both = torch.randn(6, 200, device=DEV)
+    u = torch.rand(6, device=DEV)
+    want = kvr_sample(both[:, :100].contiguous(), u, top_p=0.9, dist=True)
+    got = kvr_sample(both[:, :100], u, top_p=0.9, dist=both[:, 100:])
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    g = torch.Generator().manual_seed(3)
+    site = Adapters([((torch.randn(16, 64, generator=g) / 8).to(BF).cuda(), torch.randn(32, 16, generator=g).to(BF).cuda(), 1.0)],
+                    [32])
+    buf = torch.randn(40, 96, generator=g).to(BF).cuda()
+    cu, which = torch.tensor([0, 40], dtype=torch.int32, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    want = site.kvr_adapt(buf[:, :64].contiguous(), cu, which)
+    assert torch.equal(site.kvr_adapt(buf[:, :64], cu, which, out=buf[:, 64:]), want)
+    with pytest.raises(KvrError):
+        site.kvr_adapt(buf[:, :64], cu, which, out=buf[:, 56:88])
+
+
+def test_draft_probabilities_below_zero_and_nan():
+    """They take nothing from what is left."""
+    from prefix_reused_prefill_gb300 import kvr_accept
+    g = torch.Generator().manual_seed(5)
+    rows, vocab = 6, 3000
+    logits = torch.randn(rows, vocab, generator=g).cuda()
+    tokens = torch.randint(0, vocab, (rows,), generator=g).int().cuda()
+    q = torch.rand(rows, vocab, generator=g).cuda() * (2.0 / vocab)
+    bad = q.clone()
+    bad[:, ::3] = -1e30
+    bad[:, 1::3] = float("nan")
+    q[:, ::3] = 0
+    q[:, 1::3] = 0
+    for r in range(rows - 1):
+        q[r, tokens[r + 1]] = bad[r, tokens[r + 1]] = 1.0
+    cu = torch.tensor([0, 2, 4, 6], dtype=torch.int32, device=DEV)
+    u, u_next = torch.full((rows,), 0.999, device=DEV), torch.rand(3, generator=g).cuda()
+    for settings in (dict(), dict(top_k=40), dict(top_p=0.99), dict(top_k=100, top_p=0.5)):
+        a, b = (kvr_accept(logits, tokens, cu, u, u_next, draft_probs=x, **settings) for x in (q, bad))
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) and (a[1] >= 0).all()
+
+
+def test_adapters_given_up_while_another_stream_reads_them():
+    from prefix_reused_prefill_gb300 import Adapters
+    g = torch.Generator().manual_seed(9)
+    make = lambda: Adapters([((torch.randn(64, 4096, generator=g) / 64).to(BF).cuda(),
+                              torch.randn(4096, 64, generator=g).to(BF).cuda(), 1.0)], [4096])
+    x = torch.randn(8, 4096, generator=g).to(BF).cuda()
+    cu, which = torch.tensor([0, 8], dtype=torch.int32, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    site = make()
+    want = site.kvr_adapt(x, cu, which)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)   # (some ten milliseconds of work in front)
+    out = site.kvr_adapt(x, cu, which, stream=side)
+    del site
+    for _ in range(4):   # the sizes that were given up, written at once
+        for n in (64 * 4096, 24):
+            torch.full((n,), float("nan"), dtype=BF, device=DEV)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
