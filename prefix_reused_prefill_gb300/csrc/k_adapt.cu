@@ -465,17 +465,62 @@ struct Terms {
   __host__ __device__ size_t bytes() const { return (size_t)count * rows * ld * 2 + (size_t)rows * 12; }
 };
 
+// The tensor memory's products: operands in shared memory, rows of 128 bytes in the 128-byte swizzle,
+// eight of them 1024 bytes apart; sums of row i in lane i.
+__device__ __forceinline__ uint64_t smem_operand(uint32_t at) {
+  return (uint64_t)((at >> 4) & 0x3FFFu) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+template <class T>
+__device__ __forceinline__ constexpr uint32_t product_of(int m, int n) {
+  constexpr uint32_t kType = std::is_same<T, __half>::value ? 0u : 1u;
+  return (1u << 4) | (kType << 7) | (kType << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+__device__ __forceinline__ void tc_mma(uint32_t sums, uint64_t a, uint64_t b, uint32_t what, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(sums),
+      "l"(a), "l"(b), "r"(what), "r"((uint32_t)add)
+      : "memory");
+}
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tc_load32(uint32_t at, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(at)
+      : "memory");
+#pragma unroll
+  for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(r[k]);
+}
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
 // One chunk of NC stacked rows of A (all parts, or one) of one tile and one part of the inputs.
 // X16: x is fp16 that holds bf16 values.
 template <class T, int NC, int TERMS, bool X16>
 __global__ void __launch_bounds__(kThreads, 2) shrink_tiles_kernel(const AdaptParams p, int ks) {
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ __align__(128) uint8_t smem_raw[];
   __shared__ Tile tile;
+  __shared__ __align__(8) uint64_t bars[kStages];   // of a stage's products
+  __shared__ uint32_t sums_slot;
+  constexpr bool kTc = !X16;                        // (x of another type than A goes through registers)
+  constexpr int kSumCols = NC <= 64 ? 64 : NC <= 128 ? 128 : 256;
   constexpr int kXBytes = TR * 128, kStage = kXBytes + NC * 128;
   constexpr int kNT = NC / 32;    // tiles of 8 ranks a warp
   constexpr int kLd = NC + 4;
   static_assert(TR * kLd * 4 <= kStages * kStage, "the sums fit where the stages were");
-  dev::pdl_trigger();
+  uint8_t* smem = smem_raw + ((1024u - (dev::smem_u32(smem_raw) & 1023u)) & 1023u);
+  if (!kTc) dev::pdl_trigger();
   dev::pdl_wait();
   const int part_k = blockIdx.x % ks;
   find_tile(p, blockIdx.x / ks, tile);
@@ -485,6 +530,24 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_tiles_kernel(const AdaptPa
   const int q0 = whole ? 0 : blockIdx.z * rank, nq = whole ? p.site.n_parts * rank : rank;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int wr = warp & 1, wn = warp >> 1;
+  uint32_t sums_at = 0;
+  if (kTc) {
+    if (warp == 0) {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dev::smem_u32(&sums_slot)),
+                   "r"(kSumCols));
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    } else if (threadIdx.x == 32) {
+#pragma unroll
+      for (int i = 0; i < kStages; ++i) dev::mbar_init(dev::smem_u32(&bars[i]), 1);
+      dev::fence_mbar_init();
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    sums_at = sums_slot;
+    // (only now: a kernel behind that takes tensor memory and waits for this one must not take it first)
+    dev::pdl_trigger();
+  }
   const int K = p.site.k, steps = (K + kStep - 1) / kStep;
   const int s0 = (int)((long long)steps * part_k / ks), s1 = (int)((long long)steps * (part_k + 1) / ks);
   const uint32_t base = dev::smem_u32(smem);
@@ -529,6 +592,35 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_tiles_kernel(const AdaptPa
     cp_commit();
   }
   int at = 0;
+  bool ok = true;
+  // products of step s are over
+  const auto over = [&](int s) {
+    ok = ok && dev::mbar_wait(dev::smem_u32(&bars[(s - s0) % kStages]), (uint32_t)((s - s0) / kStages) & 1u, nullptr);
+  };
+  if (kTc)
+    for (int s = s0; s < s1; ++s) {
+      cp_wait<kStages - 2>();
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        const uint32_t st = base + at * kStage;
+        // (128 rows: those behind the tile's 64 are of A, and their sums nobody reads)
+        const uint64_t xd = smem_operand(st), ad = smem_operand(st + kXBytes);
+        tc_after();
+#pragma unroll
+        for (int kk = 0; kk < kStep / 16; ++kk)
+          tc_mma(sums_at, xd + 2 * kk, ad + 2 * kk, product_of<T>(128, NC), s > s0 || kk > 0);
+        tc_commit(dev::smem_u32(&bars[at]));
+      }
+      // the stage of the step before, once its products are over
+      if (s + kStages - 1 < s1) {
+        if (s > s0) over(s - 1);
+        load(s + kStages - 1, at == 0 ? kStages - 1 : at - 1);
+      }
+      cp_commit();
+      at = at + 1 == kStages ? 0 : at + 1;
+    }
+  else
   for (int s = s0; s < s1; ++s) {
     cp_wait<kStages - 2>();
     __syncthreads();
@@ -559,10 +651,35 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_tiles_kernel(const AdaptPa
     }
   }
   cp_wait<0>();
+  if (kTc && s1 > s0) over(s1 - 1);   // (and with them all before)
   __syncthreads();
   // the cluster's sums, a share of the rows each, a warp a row
   float* sums = reinterpret_cast<float*>(smem);
   const int g = lane >> 2, t = lane & 3;
+  if (kTc) {
+    // a warp reads the 32 lanes that its number allows: 0, 1, 4 and 5 have rows of the tile
+    tc_after();
+    if ((warp & 3) < 2)
+#pragma unroll
+      for (int c = 0; c < NC / 2; c += 32) {
+        const int col = (warp >> 2) * (NC / 2) + c, r = 32 * (warp & 3) + lane;
+        float v[32];
+        tc_load32(sums_at + ((uint32_t)(32 * (warp & 3)) << 16) + col, v);
+#pragma unroll
+        for (int k = 0; k < 32; k += 4) {
+          float4 w = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+          if (s1 <= s0) w = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (!ok) w.x = w.y = w.z = w.w = __int_as_float(0x7fffffff);   // (a wait gave up)
+          *reinterpret_cast<float4*>(sums + r * kLd + col + k) = w;
+        }
+      }
+    tc_before();
+    __syncthreads();
+    if (warp == 0) {
+      tc_after();
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(sums_at), "r"(kSumCols));
+    }
+  } else
 #pragma unroll
   for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -823,7 +940,7 @@ int expand_tiles_smem(int max_rank, int terms) {
 }
 template <int NC>
 constexpr int shrink_tiles_smem() {
-  return kStages * (TR + NC) * 128;
+  return kStages * (TR + NC) * 128 + 1024;   // (stages start where their swizzle does)
 }
 
 template <class T, int NC, int TERMS>

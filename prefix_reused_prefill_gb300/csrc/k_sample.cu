@@ -1297,9 +1297,12 @@ cudaError_t sample_setup() {
 }
 
 cudaError_t launch_sample(const SampleParams& p, int sms, cudaStream_t st) {
-  // CTAs of a row: as many as two on each SM, with 2048 tokens each at least
+  // CTAs of a row: up to 8/3 on each SM (two run at a time, and rows are over at different times), with 2048
+  // tokens each at least.  More cost more to clear, sum and wait for than they share.  With 1, 2, 4, 8 a row,
+  // in us: 64 rows of 32000 49, 40, 33, 50; 100 of 128000 161, 122, 105, 131; 160 of 128000 216, 143,
+  // 156, 197; 300 of 32000 71, 81, 103, 167.
   int ctas = 1;
-  while (ctas < kMaxCluster && (long long)p.rows * ctas <= sms && p.vocab >= 4096 * ctas) ctas *= 2;
+  while (ctas < kMaxCluster && 3ll * p.rows * ctas <= 4 * sms && p.vocab >= 4096 * ctas) ctas *= 2;
   cudaError_t e = p.rows == 0             ? cudaSuccess
                   : p.type == KVR_ACT_F32 ? launch<float>(p, ctas, st)
                   : p.type == KVR_ACT_BF16 ? launch<__nv_bfloat16>(p, ctas, st)
