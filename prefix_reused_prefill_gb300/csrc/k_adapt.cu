@@ -1,14 +1,22 @@
 // Low-rank adapters beside a shared projection (include/kvr.h).
 //
-// Two launches.  shrink_kernel forms s = A x: the inputs are cut into parts so that
-// the CTAs fill the SMs whatever the rows are, and every part leaves its sums.
-// expand_kernel adds the parts in their order, and B s to base.  Both walk tiles
-// of consecutive rows, and in a tile the runs of rows that share an adapter.
+// Two launches, s = A x and out = base + scale B s: all outputs need all of s, and both
+// read their matrices once.  s is held scaled by a row's power of two, in two or three
+// terms of the type, so that B's products are those of 16-bit matrix units and what is
+// rounded away is far below the output's own rounding.
 //
-// The tensor cores take the adapters' rows (16 of A or B) as their M side and
-// rows of x or s as their N side.  Lanes load operands straight from global
-// memory, 16 or 8 bytes each: which inputs share a fragment does not matter as
-// long as both operands agree.
+// Few rows a sequence.  shrink_kernel cuts the inputs into parts so that the CTAs
+// fill the SMs whatever the rows are, and every part leaves its sums; expand_kernel
+// adds the parts in their order, and B s to base.  Both walk tiles of eight rows, and
+// in a tile the runs of rows that share an adapter: mma.sync takes the adapters'
+// rows (16 of A or B) as its M side and the tile's as its N side.  Lanes load operands
+// straight from global memory, 16 or 8 bytes each: which inputs share a fragment
+// does not matter as long as both operands agree.  Bound: the chain of loads (whose rows, which
+// adapter, where it is, its values), twice; where each row has its own adapter, the loads of A
+// and B.  q, k and v of 3584 inputs, one row of rank 16: 7.8 us; of 4096 inputs, 64 rows with an
+// adapter each: 21 us (40 MB).  Eight sequences of 8 rows, 18944 inputs, 32-bit outputs: 12.5 us.
+//
+// Many: tiles of one sequence's rows, below.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -97,8 +105,9 @@ struct Rows {
   int runs, steps;
   uint8_t step_run[R * KVR_MAX_RANK * 3 / 16], step_j[R * KVR_MAX_RANK * 3 / 16];
 };
-// per_rank: stacked ranks of an adapter's rank (shrink: its parts, expand: one)
-__device__ __forceinline__ void find_rows(const AdaptParams& p, int row0, int per_rank, int* cu, int* which, Rows& rows) {
+// STEPS: the runs' steps are wanted, of the adapters' stacked ranks.
+template <bool STEPS>
+__device__ __forceinline__ void find_rows(const AdaptParams& p, int row0, int* cu, int* which, Rows& rows) {
   for (int i = threadIdx.x; i <= p.n_seq; i += kThreads) {
     cu[i] = p.cu[i];
     if (i < p.n_seq) which[i] = p.which[i];
@@ -129,7 +138,7 @@ __device__ __forceinline__ void find_rows(const AdaptParams& p, int row0, int pe
     const int before = __shfl_up_sync(0xffffffffu, id, 1);
     const bool starts = lane < R && id >= 0 && (lane == 0 || before != id);
     const uint32_t all = __ballot_sync(0xffffffffu, starts), same = __ballot_sync(0xffffffffu, lane < R && id >= 0 && !starts);
-    const int steps = starts ? (e.rank * per_rank + 15) / 16 : 0;
+    const int steps = STEPS && starts ? (e.rank * p.site.n_parts + 15) / 16 : 0;
     int at = steps;
 #pragma unroll
     for (int o = 1; o < R; o <<= 1) {
@@ -163,7 +172,7 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const AdaptParams p) {
   dev::pdl_trigger();
   dev::pdl_wait();
   const int row0 = blockIdx.x * R, split = blockIdx.y;
-  find_rows(p, row0, p.site.n_parts, cu, which, rows);
+  find_rows<true>(p, row0, cu, which, rows);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int ld = p.site.n_parts * p.site.max_rank;
   const int K = p.site.k, chunks = (K + 31) / 32;
@@ -176,12 +185,13 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const AdaptParams p) {
     const bool in_run = g >= run.first && g < run.end;
     const T* lo_at = static_cast<const T*>(run.a) + (long long)q * K;
     const T* hi_at = lo_at + 8ll * K;
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    // four chunks of 32 inputs in flight
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    // four chunks of 32 inputs in flight, and in one chain of products (which cut their sums, kChain)
     constexpr int kFlight = 4;
     for (int c = c0; c < c1; c += kFlight) {
       const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
       uint4 xv[kFlight], lo[kFlight], hi[kFlight];
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int f = 0; f < kFlight; ++f) {
         const int k = 32 * (c + f) + 8 * t;
@@ -201,12 +211,14 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const AdaptParams p) {
         mma<T>(acc, lo[f].x, hi[f].x, lo[f].y, hi[f].y, xv[f].x, xv[f].y);
         mma<T>(acc, lo[f].z, hi[f].z, lo[f].w, hi[f].w, xv[f].z, xv[f].w);
       }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[e] += acc[e];
     }
     // rows q and q + 8 of A, rows 2 t and 2 t + 1 of x
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int r = 2 * t + (e & 1), j = q + 8 * (e >> 1);
-      if (r >= run.first && r < run.end && j < ranks) part[(long long)r * ld + j] = acc[e];
+      if (r >= run.first && r < run.end && j < ranks) part[(long long)r * ld + j] = sum[e];
     }
   }
 }
@@ -223,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 2) expand_kernel(const AdaptParams p
   dev::pdl_trigger();
   dev::pdl_wait();
   const int row0 = blockIdx.x * R;
-  find_rows(p, row0, 1, cu, which, rows);
+  find_rows<false>(p, row0, cu, which, rows);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   // the CTA's part, its outputs' place in it and in out
   int part = 0, col = blockIdx.y, left = 0;
@@ -369,15 +381,20 @@ __global__ void __launch_bounds__(kThreads, 2) expand_kernel(const AdaptParams p
 }
 
 // ---------------------------------------------------------------- many rows a sequence
-// Tiles of 64 rows of one sequence.  shrink_tiles_kernel streams x and A through
+// Tiles of one sequence's rows.  shrink_tiles_kernel streams 64 rows of x and A through
 // shared memory (a cluster cuts the inputs, its CTAs' sums are joined in distributed
-// shared memory) and leaves s in terms of T; expand_tiles_kernel multiplies them
-// with 64 x 128 outputs' B while base is on its way.
+// shared memory) and leaves s in terms of T; expand_tiles_kernel multiplies 128 rows of
+// them with 128 outputs' B while base is on its way.  Both on tcgen05, sums in tensor memory.
+// Addresses are the adapters', known on the device only, so copies are cp.async, not tensor maps'.
+// Bound: shrink by what it moves from L2 to the SMs (each 64 inputs of 64 rows bring up to 192 rows
+// of A; 64 rows of x instead of 128, since two CTAs an SM cover each other's start and end),
+// expand by base and out.  Four ragged prompts, 6.7k rows of 4096 inputs, rank 64, 6144 outputs:
+// 85 us (105 with mma.sync), of which a plain copy of x, base and out would take 33.
 constexpr int TR = 64;
 constexpr int kStep = 64;       // inputs of a stage: 128 bytes a row
 constexpr int kStages = 3;
 constexpr int kMaxCluster = 8;
-constexpr int kTileN = 128;     // outputs of an expand CTA
+constexpr int ER = 128, kTileN = 128;   // rows and outputs of a tile of expand
 
 __host__ __device__ inline int round16(int r) { return (r + 15) & ~15; }
 
@@ -397,7 +414,8 @@ struct Tile {
   int id;              // adapter, or kNone
   kvr_adapter ad;
 };
-// Tile `t` of the batch: sequences in order, each in tiles of TR rows.
+// Tile `t` of the batch: sequences in order, each in tiles of ROWS rows.
+template <int ROWS>
 __device__ __forceinline__ void find_tile(const AdaptParams& p, int t, Tile& tile) {
   __shared__ int warp_sum[kWarps];
   constexpr int kPer = kAdaptMaxSeqs / kThreads;
@@ -411,7 +429,7 @@ __device__ __forceinline__ void find_tile(const AdaptParams& p, int t, Tile& til
     n[k] = 0;
     if (k < per && b0 + k < p.n_seq) {
       const int r0 = max(p.cu[b0 + k], 0), r1 = min(p.cu[b0 + k + 1], p.rows);
-      n[k] = r1 > r0 ? (r1 - r0 + TR - 1) / TR : 0;
+      n[k] = r1 > r0 ? (r1 - r0 + ROWS - 1) / ROWS : 0;
     }
     sum += n[k];
   }
@@ -431,8 +449,8 @@ __device__ __forceinline__ void find_tile(const AdaptParams& p, int t, Tile& til
     if (t >= at && t < at + n[k]) {
       const int b = b0 + k;
       const int r0 = max(p.cu[b], 0), r1 = min(p.cu[b + 1], p.rows);
-      tile.row0 = r0 + (t - at) * TR;
-      tile.rows = min(r1 - tile.row0, TR);
+      tile.row0 = r0 + (t - at) * ROWS;
+      tile.rows = min(r1 - tile.row0, ROWS);
       int id = p.which[b];
       if (id < 0 || id >= p.site.n_adapters) id = kNone;
       if (id != kNone) {
@@ -502,28 +520,45 @@ __device__ __forceinline__ void tc_load32(uint32_t at, float (&v)[32]) {
 #pragma unroll
   for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(r[k]);
 }
+// 32 columns of 16 lanes, as mma.sync's sums of four products lie in a warp
+__device__ __forceinline__ void tc_load16x32(uint32_t at, float (&v)[4][4]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(at)
+      : "memory");
+#pragma unroll
+  for (int k = 0; k < 16; ++k) v[k / 4][k % 4] = __uint_as_float(r[k]);
+}
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
 // One chunk of NC stacked rows of A (all parts, or one) of one tile and one part of the inputs.
-// X16: x is fp16 that holds bf16 values.
-template <class T, int NC, int TERMS, bool X16>
+// X16: x is fp16 that holds bf16 values.  TC: on tcgen05, whose chain of products is the whole part.
+// Matrix units cut a sum's last bits at every product of 16 inputs instead of rounding them; over 4096 inputs in one
+// chain that is 2e-6 of the sum.  Outputs of 16 bits do not see it.  For those of 32 bits chains are kChain stages, added
+// up in registers: below 3e-7.
+constexpr int kChain = 2;
+template <class T, int NC, int TERMS, bool TC, bool X16>
 __global__ void __launch_bounds__(kThreads, 2) shrink_tiles_kernel(const AdaptParams p, int ks) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
   __shared__ Tile tile;
   __shared__ __align__(8) uint64_t bars[kStages];   // of a stage's products
   __shared__ uint32_t sums_slot;
-  constexpr bool kTc = !X16;                        // (x of another type than A goes through registers)
   constexpr int kSumCols = NC <= 64 ? 64 : NC <= 128 ? 128 : 256;
   constexpr int kXBytes = TR * 128, kStage = kXBytes + NC * 128;
   constexpr int kNT = NC / 32;    // tiles of 8 ranks a warp
   constexpr int kLd = NC + 4;
   static_assert(TR * kLd * 4 <= kStages * kStage, "the sums fit where the stages were");
   uint8_t* smem = smem_raw + ((1024u - (dev::smem_u32(smem_raw) & 1023u)) & 1023u);
-  if (!kTc) dev::pdl_trigger();
+  if (!TC) dev::pdl_trigger();
   dev::pdl_wait();
   const int part_k = blockIdx.x % ks;
-  find_tile(p, blockIdx.x / ks, tile);
+  find_tile<TR>(p, blockIdx.x / ks, tile);
   if (tile.rows == 0 || tile.id == kNone) return;   // (the whole cluster)
   const int rank = tile.ad.rank;
   const bool whole = gridDim.z == 1;
@@ -531,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_tiles_kernel(const AdaptPa
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int wr = warp & 1, wn = warp >> 1;
   uint32_t sums_at = 0;
-  if (kTc) {
+  if (TC) {
     if (warp == 0) {
       asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dev::smem_u32(&sums_slot)),
                    "r"(kSumCols));
@@ -581,11 +616,13 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_tiles_kernel(const AdaptPa
     a_at[kk] = base + dev::swz128(wr * 32 + (lane & 15), 2 * kk + (lane >> 4));
     b_at[kk] = base + kXBytes + dev::swz128(wn * (NC / 4) + (lane & 7) + ((lane >> 4) << 3), 2 * kk + ((lane >> 3) & 1));
   }
-  float acc[2][kNT][4];
+  float acc[2][kNT][4], sum[2][kNT][4];
 #pragma unroll
   for (int m = 0; m < 2; ++m)
 #pragma unroll
-    for (int n = 0; n < kNT; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.f;
+    for (int n = 0; n < kNT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[m][n][e] = sum[m][n][e] = 0.f;
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) {
     if (s0 + i < s1) load(s0 + i, i);
@@ -595,9 +632,9 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_tiles_kernel(const AdaptPa
   bool ok = true;
   // products of step s are over
   const auto over = [&](int s) {
-    ok = ok && dev::mbar_wait(dev::smem_u32(&bars[(s - s0) % kStages]), (uint32_t)((s - s0) / kStages) & 1u, nullptr);
+    ok = ok && dev::mbar_wait(dev::smem_u32(&bars[(s - s0) % kStages]), (uint32_t)((s - s0) / kStages) & 1u, p.status);
   };
-  if (kTc)
+  if constexpr (TC) {
     for (int s = s0; s < s1; ++s) {
       cp_wait<kStages - 2>();
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -620,43 +657,55 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_tiles_kernel(const AdaptPa
       cp_commit();
       at = at + 1 == kStages ? 0 : at + 1;
     }
-  else
-  for (int s = s0; s < s1; ++s) {
-    cp_wait<kStages - 2>();
-    __syncthreads();
-    if (s + kStages - 1 < s1) load(s + kStages - 1, at == 0 ? kStages - 1 : at - 1);
-    cp_commit();
-    const uint32_t st = at * kStage;
-    at = at + 1 == kStages ? 0 : at + 1;
+  } else {
+    for (int s = s0; s < s1; ++s) {
+      cp_wait<kStages - 2>();
+      __syncthreads();
+      if (s + kStages - 1 < s1) load(s + kStages - 1, at == 0 ? kStages - 1 : at - 1);
+      cp_commit();
+      const uint32_t st = at * kStage;
+      at = at + 1 == kStages ? 0 : at + 1;
+      if ((s - s0) % kChain == 0) {
 #pragma unroll
-    for (int kk = 0; kk < kStep / 16; ++kk) {
-      uint32_t a[2][4];
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        dev::ldmatrix_x4(a_at[kk] + st + m * 16 * 128, a[m][0], a[m][1], a[m][2], a[m][3]);
-        if (X16)
+          for (int n = 0; n < kNT; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) a[m][e] = bf16_of_half2(a[m][e]);
+            for (int e = 0; e < 4; ++e) {
+              sum[m][n][e] += acc[m][n][e];
+              acc[m][n][e] = 0.f;
+            }
       }
 #pragma unroll
-      for (int n = 0; n < kNT; n += 2) {
-        uint32_t b[4];   // ranks 8 n .. + 15: (first eight, low and high inputs), (second eight, ...)
-        dev::ldmatrix_x4(b_at[kk] + st + n * 8 * 128, b[0], b[1], b[2], b[3]);
+      for (int kk = 0; kk < kStep / 16; ++kk) {
+        uint32_t a[2][4];
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
-          mma<T>(acc[m][n], a[m][0], a[m][1], a[m][2], a[m][3], b[0], b[1]);
-          mma<T>(acc[m][n + 1], a[m][0], a[m][1], a[m][2], a[m][3], b[2], b[3]);
+          dev::ldmatrix_x4(a_at[kk] + st + m * 16 * 128, a[m][0], a[m][1], a[m][2], a[m][3]);
+          if (X16)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) a[m][e] = bf16_of_half2(a[m][e]);
+        }
+#pragma unroll
+        for (int n = 0; n < kNT; n += 2) {
+          uint32_t b[4];   // ranks 8 n .. + 15: (first eight, low and high inputs), (second eight, ...)
+          dev::ldmatrix_x4(b_at[kk] + st + n * 8 * 128, b[0], b[1], b[2], b[3]);
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            mma<T>(acc[m][n], a[m][0], a[m][1], a[m][2], a[m][3], b[0], b[1]);
+            mma<T>(acc[m][n + 1], a[m][0], a[m][1], a[m][2], a[m][3], b[2], b[3]);
+          }
         }
       }
     }
   }
   cp_wait<0>();
-  if (kTc && s1 > s0) over(s1 - 1);   // (and with them all before)
+  if (TC) over(s1 - 1);   // (and with them all before)
   __syncthreads();
   // the cluster's sums, a share of the rows each, a warp a row
   float* sums = reinterpret_cast<float*>(smem);
   const int g = lane >> 2, t = lane & 3;
-  if (kTc) {
+  if (TC) {
     // a warp reads the 32 lanes that its number allows: 0, 1, 4 and 5 have rows of the tile
     tc_after();
     if ((warp & 3) < 2)
@@ -668,7 +717,6 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_tiles_kernel(const AdaptPa
 #pragma unroll
         for (int k = 0; k < 32; k += 4) {
           float4 w = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
-          if (s1 <= s0) w = make_float4(0.f, 0.f, 0.f, 0.f);
           if (!ok) w.x = w.y = w.z = w.w = __int_as_float(0x7fffffff);   // (a wait gave up)
           *reinterpret_cast<float4*>(sums + r * kLd + col + k) = w;
         }
@@ -679,17 +727,18 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_tiles_kernel(const AdaptPa
       tc_after();
       asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(sums_at), "r"(kSumCols));
     }
-  } else
+  } else {
 #pragma unroll
-  for (int m = 0; m < 2; ++m)
+    for (int m = 0; m < 2; ++m)
 #pragma unroll
-    for (int n = 0; n < kNT; ++n) {
-      float* d = sums + (wr * 32 + m * 16 + g) * kLd + wn * (NC / 4) + 8 * n + 2 * t;
-      d[0] = acc[m][n][0];
-      d[1] = acc[m][n][1];
-      d[8 * kLd] = acc[m][n][2];
-      d[8 * kLd + 1] = acc[m][n][3];
-    }
+      for (int n = 0; n < kNT; ++n) {
+        float* d = sums + (wr * 32 + m * 16 + g) * kLd + wn * (NC / 4) + 8 * n + 2 * t;
+        d[0] = sum[m][n][0] + acc[m][n][0];
+        d[1] = sum[m][n][1] + acc[m][n][1];
+        d[8 * kLd] = sum[m][n][2] + acc[m][n][2];
+        d[8 * kLd + 1] = sum[m][n][3] + acc[m][n][3];
+      }
+  }
   const cg::cluster_group cluster = cg::this_cluster();
   if (ks > 1) cluster.sync();
   else __syncthreads();
@@ -792,126 +841,168 @@ struct Eight {
   }
 };
 
+// What a CTA keeps from run to run: its tensor memory (two tiles' sums), and their barriers' phases.
+struct Sums {
+  uint32_t at, bars;   // (bars: 8 bytes a tile)
+  uint32_t phases;     // (a bit a tile)
+};
+constexpr int kOperand = ER * 128;   // bytes of 128 rows of 64 ranks
+
 // `c1 - c0` tiles of 128 outputs of one part, of a tile of rows.  The outputs that
-// stand beside one another in a lane's products are chosen: its four pairs are eight
-// in a row, so base and out need no way through shared memory.
+// stand beside one another in a lane's sums are chosen: its four pairs are eight in
+// a row, so base and out need no way through shared memory.
 template <class T, class O, int TERMS>
-__device__ __forceinline__ void expand_run(const AdaptParams& p, const Tile& tile, float* factor, uint8_t* smem, int part,
-                                           int left, int c0, int c1) {
+__device__ __forceinline__ void expand_run(const AdaptParams& p, const Tile& tile, float* factor, uint32_t smem, Sums& sums,
+                                           int part, int left, int c0, int c1) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int wr = warp & 1, wn = warp >> 1;
-  const int c_end = min(c1 * kTileN, p.site.cols[part]);
+  const int c_end = min(c1 * kTileN, p.site.cols[part]), n = c1 - c0;
   if (tile.id == kNone && p.base == p.out) return;
   const bool adapted = tile.id != kNone;
-  const int rank = adapted ? tile.ad.rank : 0, r16 = round16(rank), pitch = 2 * r16 + 16;
-  const int stage = kTileN * pitch;
-  const uint32_t s_base = dev::smem_u32(smem), ss = s_base + 2 * stage;
+  const int rank = adapted ? tile.ad.rank : 0, r16 = round16(rank);
+  const int halves = (round16(p.site.max_rank) + 63) / 64;   // operands of 64 ranks
+  const uint32_t b_smem = smem + TERMS * halves * kOperand;
   // a thread's 16 bytes of a row of ranks (a power of two of them, the last ones without work)
   const int chunks = r16 / 8, shift = chunks > 1 ? 32 - __clz(chunks - 1) : 0;
   const int lr = threadIdx.x >> shift, lc = threadIdx.x & ((1 << shift) - 1), lstep = kThreads >> shift;
-  if (adapted) {
+  const uint32_t half = (lc >> 3) * kOperand;
+  // a lane's rows row0, + 8, + 16, + 24 and its outputs ocol .. + 7 and 32 further
+  const int row0 = (warp & 3) * 32 + g, ocol = (warp >> 2) * 64 + 8 * t;
+  const O* base = p.base ? static_cast<const O*>(p.base) + p.base_stride * (tile.row0 + row0) + left + ocol : nullptr;
+  O* out = static_cast<O*>(p.out) + p.out_stride * (tile.row0 + row0) + left + ocol;
+  const long long base8 = 8 * p.base_stride, out8 = 8 * p.out_stride;
+  const auto fetch = [&](int col, Eight<O> (&o)[4]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (base && col + ocol < c_end && row0 + 8 * k < tile.rows) o[k].load(base + col + k * base8);
+      else o[k].clear();
+    }
+  };
+  const auto store = [&](int col, const Eight<O> (&o)[4]) {
+    if (col + ocol >= c_end) return;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (row0 + 8 * k < tile.rows) o[k].store(out + col + k * out8);
+  };
+  if (!adapted) {
+    for (int col = c0 * kTileN; col < c_end; col += kTileN) {
+      Eight<O> o[2][4];
+      fetch(col, o[0]);
+      fetch(col + 32, o[1]);
+      store(col, o[0]);
+      store(col + 32, o[1]);
+    }
+    return;
+  }
+  const T* B = static_cast<const T*>(tile.ad.b) + (long long)left * rank;
+  const auto load = [&](int col, int buf) {
+    if (lc < chunks) {
+      const T* src = B + (long long)(col + lr) * rank + 8 * lc;
+      const int step = lstep * rank;
+      const uint32_t dst = b_smem + buf * halves * kOperand + half;
+      const bool in = 8 * lc < rank;
+      // output 8 t + 2 n + e of 32 is row 8 n + 2 t + e
+#pragma unroll 4
+      for (int r = lr; r < kTileN; r += lstep) {
+        const bool v = in && col + r < c_end;
+        cp16(dst + dev::swz128((r & ~31) | (r & 6) << 2 | (r & 24) >> 2 | (r & 1), lc & 7), v ? src : B, v);
+        src += step;
+      }
+    }
+    cp_commit();
+  };
+  // what the threads have copied, for the products: of buffer b into its sums
+  const auto multiply = [&](int b) {
+    cp_wait<0>();
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    tc_before();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      tc_after();
+      const uint64_t bd = smem_operand(b_smem + b * halves * kOperand);
+#pragma unroll 1
+      for (int k = TERMS - 1; k >= 0; --k) {   // (the smallest terms first)
+        const uint64_t sd = smem_operand(smem + k * halves * kOperand);
+        for (int kk = 0; kk < r16 / 16; ++kk) {
+          const int at = (kk >> 2) * (kOperand >> 4) + 2 * (kk & 3);
+          tc_mma(sums.at + b * kTileN, sd + at, bd + at, product_of<T>(ER, kTileN), k < TERMS - 1 || kk > 0);
+        }
+      }
+      tc_commit(sums.bars + 8 * b);
+    }
+  };
+  tc_before();
+  __syncthreads();   // (the last run's factors have been read)
+  {
     const Terms terms(p, TERMS);
 #pragma unroll
     for (int k = 0; k < TERMS; ++k)
-      for (int r = lr; r < TR && lc < chunks; r += lstep) {
+      for (int r = lr; r < ER && lc < chunks; r += lstep) {
         const T* src = terms.term<T>(k, tile.row0 + min(r, tile.rows - 1)) + part * round16(p.site.max_rank) + 8 * lc;
-        cp16(ss + (k * TR + r) * pitch + 16 * lc, src, r < tile.rows);
+        cp16(smem + k * halves * kOperand + half + dev::swz128(r, lc & 7), src, r < tile.rows);
       }
     if (threadIdx.x < tile.rows) factor[threadIdx.x] = terms.factor(tile.row0 + threadIdx.x)[part];
   }
-  const T* B = adapted ? static_cast<const T*>(tile.ad.b) + (long long)left * rank : nullptr;
-  auto load = [&](int col, int buf) {
-    if (!adapted || lc >= chunks) return;
-    const T* src = B + (long long)(col + lr) * rank + 8 * lc;
-    const int step = lstep * rank;
-    const uint32_t dst = s_base + buf * stage + 16 * lc;
-    const bool in = 8 * lc < rank;
-    // output 8 t + 2 n + e of 32 is column 2 t + e of the n-th product
-#pragma unroll 4
-    for (int r = lr; r < kTileN; r += lstep) {
-      const bool v = in && col + r < c_end;
-      cp16(dst + ((r & ~31) | (r & 6) << 2 | (r & 24) >> 2 | (r & 1)) * pitch, v ? src : B, v);
-      src += step;
-    }
-  };
-  // a lane's operand rows
-  const uint32_t a_at = ss + (wr * 32 + (lane & 15)) * pitch + 16 * (lane >> 4);
-  const uint32_t b_at = s_base + (wn * 32 + (lane & 7) + 8 * (lane >> 4)) * pitch + 16 * ((lane >> 3) & 1);
-  const int row = wr * 32 + g, ocol = wn * 32 + 8 * t;
-  const O* base = p.base ? static_cast<const O*>(p.base) + p.base_stride * (tile.row0 + row) + left + ocol : nullptr;
-  O* out = static_cast<O*>(p.out) + p.out_stride * (tile.row0 + row) + left + ocol;
-  const long long base8 = 8 * p.base_stride, out8 = 8 * p.out_stride;
-  auto fetch = [&](int col, Eight<O> (&next)[4]) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {   // rows 8 k further
-      if (base && col + ocol < c_end && row + 8 * k < tile.rows) next[k].load(base + col + k * base8);
-      else next[k].clear();
-    }
-  };
-  int buf = 0;
   load(c0 * kTileN, 0);
-  cp_commit();
-  for (int col = c0 * kTileN; col < c_end; col += kTileN, buf ^= 1) {
-    if (col + kTileN < c_end) load(col + kTileN, buf ^ 1);
-    cp_commit();
-    const bool in = col + ocol < c_end;
-    Eight<O> o[4];
-    fetch(col, o);
-    cp_wait<1>();
-    __syncthreads();
-    if (adapted) {
-      const uint32_t b_buf = b_at + buf * stage;
-      float acc[2][4][4];
+  multiply(0);
+  if (n > 1) load((c0 + 1) * kTileN, 1);
+  for (int i = 0; i < n; ++i) {
+    const int b = i & 1, col = (c0 + i) * kTileN;
+    if (i + 1 < n) multiply(b ^ 1);   // (its sums have been read: the last tile but one's)
+    Eight<O> o[2][4];
+    fetch(col, o[0]);
+    fetch(col + 32, o[1]);
+    const bool ok = dev::mbar_wait(sums.bars + 8 * b, (sums.phases >> b) & 1u, p.status);
+    sums.phases ^= 1u << b;
+    tc_after();
+    if (i + 2 < n) load(col + 2 * kTileN, b);
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+    for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int n = 0; n < 4; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.f;
-#pragma unroll 2
-      for (int kk = 0; kk < r16 / 16; ++kk) {
-        uint32_t b[2][4];
+      for (int h = 0; h < 2; ++h) {
+        float acc[4][4];
+        tc_load16x32(sums.at + ((uint32_t)((warp & 3) * 32 + 16 * m) << 16) + b * kTileN + (warp >> 2) * 64 + 32 * h, acc);
 #pragma unroll
-        for (int n = 0; n < 2; ++n)   // products 2 n and 2 n + 1
-          dev::ldmatrix_x4(b_buf + 16 * n * pitch + 32 * kk, b[n][0], b[n][1], b[n][2], b[n][3]);
+        for (int k = 0; k < 2; ++k) {
+          const float f = ok ? factor[row0 + 16 * m + 8 * k] : __int_as_float(0x7fffffff);   // (a wait gave up)
 #pragma unroll
-        for (int k = TERMS - 1; k >= 0; --k)
-#pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            uint32_t a[4];
-            dev::ldmatrix_x4(a_at + (k * TR + m * 16) * pitch + 32 * kk, a[0], a[1], a[2], a[3]);
-#pragma unroll
-            for (int n = 0; n < 4; ++n)
-              mma<T>(acc[m][n], a[0], a[1], a[2], a[3], b[n >> 1][2 * (n & 1)], b[n >> 1][2 * (n & 1) + 1]);
-          }
+          for (int j = 0; j < 4; ++j) o[h][2 * m + k].add(j, acc[j][2 * k], acc[j][2 * k + 1], f);
+        }
       }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float f = factor[row + 8 * k];
-#pragma unroll
-        for (int n = 0; n < 4; ++n) o[k].add(n, acc[k >> 1][n][2 * (k & 1)], acc[k >> 1][n][2 * (k & 1) + 1], f);
-      }
-    }
-    if (in)
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (row + 8 * k < tile.rows) o[k].store(out + col + k * out8);
-    __syncthreads();   // (the next loads overwrite B)
+    store(col, o[0]);
+    store(col + 32, o[1]);
   }
-  cp_wait<0>();
 }
 
-// The tiles of 64 rows times their tiles of 128 outputs in equal runs, one a CTA:
-// while 64 rows and a part last the terms stay, and the next outputs' B and base
-// are on their way while some are multiplied and stored.
+// The tiles of 128 rows times their tiles of 128 outputs in equal runs, one a CTA:
+// while 128 rows and a part last the terms stay, and the next outputs' products run
+// and B is on its way while some are added to base and stored.
 template <class T, class O, int TERMS>
 __global__ void __launch_bounds__(kThreads, 2) expand_tiles_kernel(const AdaptParams p, int col_tiles) {
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ __align__(128) uint8_t smem_raw[];
   __shared__ Tile tile;
-  __shared__ float factor[TR];
-  dev::pdl_trigger();
+  __shared__ float factor[ER];
+  __shared__ __align__(8) uint64_t bars[2];
+  __shared__ uint32_t sums_slot;
+  const uint32_t smem = (dev::smem_u32(smem_raw) + 1023u) & ~1023u;
   dev::pdl_wait();
-  find_tile(p, 0, tile);
+  Sums sums = {0, dev::smem_u32(bars), 0};
+  if (threadIdx.x < 32) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dev::smem_u32(&sums_slot)),
+                 "r"(2 * kTileN));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  } else if (threadIdx.x == 32) {
+    dev::mbar_init(sums.bars, 1);
+    dev::mbar_init(sums.bars + 8, 1);
+    dev::fence_mbar_init();
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  sums.at = sums_slot;
+  dev::pdl_trigger();   // (only now: see shrink_tiles_kernel)
+  find_tile<ER>(p, 0, tile);
   // (no more tiles than sequences in their order can have)
-  const int units = min(tile.tiles, p.rows / TR + min(p.n_seq, p.rows)) * col_tiles;
+  const int units = min(tile.tiles, p.rows / ER + min(p.n_seq, p.rows)) * col_tiles;
   int u = (int)((long long)units * blockIdx.x / gridDim.x);
   const int u1 = (int)((long long)units * (blockIdx.x + 1) / gridDim.x);
   int now = 0;
@@ -919,7 +1010,7 @@ __global__ void __launch_bounds__(kThreads, 2) expand_tiles_kernel(const AdaptPa
     if (u / col_tiles != now) {
       now = u / col_tiles;
       __syncthreads();   // (the last one has been read)
-      find_tile(p, now, tile);
+      find_tile<ER>(p, now, tile);
     }
     const int first = u % col_tiles, n = min(u1 - u, col_tiles - first);
     int part = 0, before = 0, left = 0, tiles = 0;
@@ -931,23 +1022,30 @@ __global__ void __launch_bounds__(kThreads, 2) expand_tiles_kernel(const AdaptPa
     }
     const int c0 = first - before, c1 = min(c0 + n, tiles);   // of this part
     u += c1 - c0;
-    expand_run<T, O, TERMS>(p, tile, factor, smem, part, left, c0, c1);
+    expand_run<T, O, TERMS>(p, tile, factor, smem, sums, part, left, c0, c1);
+  }
+  tc_before();
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    tc_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(sums.at), "r"(2 * kTileN));
   }
 }
 
 int expand_tiles_smem(int max_rank, int terms) {
-  return (2 * kTileN + terms * TR) * (2 * round16(max_rank) + 16);
+  return (round16(max_rank) + 63) / 64 * (terms + 2) * kOperand + 1024;   // (operands start where their swizzle does)
 }
 template <int NC>
 constexpr int shrink_tiles_smem() {
   return kStages * (TR + NC) * 128 + 1024;   // (stages start where their swizzle does)
 }
 
-template <class T, int NC, int TERMS>
+template <class T, int NC, int TERMS, bool TC>
 cudaError_t launch_shrink_tiles(const AdaptParams& p, int tiles, int chunks, int sms, cudaStream_t st) {
-  // CTAs of a tile: as many as fill the SMs three times, with 256 inputs each at least
+  // CTAs of a tile: as many as 3/2 an SM (two run at a time), with 256 inputs each at least.  Four prompts in
+  // 108 tiles: 96 us with two CTAs a tile, 101 with four, which then run in two waves; 254 rows the same either way.
   int ks = 1;
-  while (ks < kMaxCluster && tiles * chunks * ks * 2 <= 3 * sms && p.site.k >= 512 * ks) ks *= 2;
+  while (ks < kMaxCluster && 2 * (tiles * chunks * ks * 2) <= 3 * sms && p.site.k >= 512 * ks) ks *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * ks), 1, (unsigned)chunks);
   cfg.blockDim = dim3(kThreads);
@@ -961,35 +1059,41 @@ cudaError_t launch_shrink_tiles(const AdaptParams& p, int tiles, int chunks, int
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 2 : 1;
   if constexpr (TERMS == 3)
-    if (p.x16) return cudaLaunchKernelEx(&cfg, shrink_tiles_kernel<T, NC, TERMS, true>, p, ks);
-  return cudaLaunchKernelEx(&cfg, shrink_tiles_kernel<T, NC, TERMS, false>, p, ks);
+    if (p.x16) return cudaLaunchKernelEx(&cfg, shrink_tiles_kernel<T, NC, TERMS, TC, true>, p, ks);
+  return cudaLaunchKernelEx(&cfg, shrink_tiles_kernel<T, NC, TERMS, TC, false>, p, ks);
 }
 
 template <class T, class O, int TERMS>
 cudaError_t launch_tiles(const AdaptParams& p, int sms, cudaStream_t st) {
   const int tiles = p.rows / TR + std::min(p.n_seq, p.rows);   // at most
+  const int wide = p.rows / ER + std::min(p.n_seq, p.rows);
   const int stacked = p.site.n_parts * p.site.max_rank;
-  cudaError_t e = stacked <= 64    ? launch_shrink_tiles<T, 64, TERMS>(p, tiles, 1, sms, st)
-                  : stacked <= 128 ? launch_shrink_tiles<T, 128, TERMS>(p, tiles, 1, sms, st)
-                  : stacked <= 192 ? launch_shrink_tiles<T, 192, TERMS>(p, tiles, 1, sms, st)
-                                   : launch_shrink_tiles<T, 128, TERMS>(p, tiles, p.site.n_parts, sms, st);
+  // all parts at once, as far as a CTA's sums hold them
+  constexpr bool kTc = !std::is_same<O, float>::value;
+  cudaError_t e;
+  if (stacked <= 64) e = launch_shrink_tiles<T, 64, TERMS, kTc>(p, tiles, 1, sms, st);
+  else if (stacked <= 128) e = launch_shrink_tiles<T, 128, TERMS, kTc>(p, tiles, 1, sms, st);
+  else if (kTc && stacked <= 192) e = launch_shrink_tiles<T, kTc ? 192 : 128, TERMS, kTc>(p, tiles, 1, sms, st);
+  else if (p.site.max_rank <= 64) e = launch_shrink_tiles<T, 64, TERMS, kTc>(p, tiles, p.site.n_parts, sms, st);
+  else e = launch_shrink_tiles<T, 128, TERMS, kTc>(p, tiles, p.site.n_parts, sms, st);
   if (e != cudaSuccess) return e;
   int cols = 0;
   for (int j = 0; j < p.site.n_parts; ++j) cols += (p.site.cols[j] + kTileN - 1) / kTileN;
   const int smem = expand_tiles_smem(p.site.max_rank, TERMS);
   const int per_sm = smem <= 110 * 1024 ? 2 : 1;
-  const int ctas = (int)std::min<long long>((long long)sms * per_sm, (long long)tiles * cols);
+  const int ctas = (int)std::min<long long>((long long)sms * per_sm, (long long)wide * cols);
   return launch_k(expand_tiles_kernel<T, O, TERMS>, dim3(ctas), dim3(kThreads), smem, st, p, cols);
 }
 
-template <class T, int TERMS, bool X16>
+template <class T, int TERMS, bool TC, bool X16>
 cudaError_t setup_shrink() {
   const auto set = [](void (*k)(AdaptParams, int), int bytes) {
     return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   };
-  cudaError_t e = set(shrink_tiles_kernel<T, 64, TERMS, X16>, shrink_tiles_smem<64>());
-  if (e == cudaSuccess) e = set(shrink_tiles_kernel<T, 128, TERMS, X16>, shrink_tiles_smem<128>());
-  if (e == cudaSuccess) e = set(shrink_tiles_kernel<T, 192, TERMS, X16>, shrink_tiles_smem<192>());
+  cudaError_t e = set(shrink_tiles_kernel<T, 64, TERMS, TC, X16>, shrink_tiles_smem<64>());
+  if (e == cudaSuccess) e = set(shrink_tiles_kernel<T, 128, TERMS, TC, X16>, shrink_tiles_smem<128>());
+  if constexpr (TC)
+    if (e == cudaSuccess) e = set(shrink_tiles_kernel<T, 192, TERMS, TC, X16>, shrink_tiles_smem<192>());
   return e;
 }
 template <class T, class O, int TERMS>
@@ -1028,10 +1132,11 @@ int adapt_split(const kvr_adapter_site& s, int rows, int sms) {
 }  // namespace
 
 cudaError_t adapt_setup() {
-  cudaError_t e = setup_shrink<__nv_bfloat16, 2, false>();
-  if (e == cudaSuccess) e = setup_shrink<__nv_bfloat16, 3, false>();
-  if (e == cudaSuccess) e = setup_shrink<__nv_bfloat16, 3, true>();   // (the layer stack's: 32-bit outputs)
-  if (e == cudaSuccess) e = setup_shrink<__half, 2, false>();
+  cudaError_t e = setup_shrink<__nv_bfloat16, 2, true, false>();
+  if (e == cudaSuccess) e = setup_shrink<__nv_bfloat16, 3, false, false>();
+  if (e == cudaSuccess) e = setup_shrink<__nv_bfloat16, 3, false, true>();   // (the layer stack's: 32-bit outputs)
+  if (e == cudaSuccess) e = setup_shrink<__half, 2, true, false>();
+  if (e == cudaSuccess) e = setup_shrink<__half, 2, false, false>();
   if (e == cudaSuccess) e = setup_expand<__nv_bfloat16, __nv_bfloat16, 2>();
   if (e == cudaSuccess) e = setup_expand<__nv_bfloat16, float, 3>();
   if (e == cudaSuccess) e = setup_expand<__half, __half, 2>();

@@ -17,6 +17,17 @@
 // of floats and summed as whole numbers of 2^-44 of the largest: whole numbers have
 // one sum in any order, so shared-memory atomics serve and every pass, CTA and
 // launch agrees on where a run ends.
+//
+// A row is a cluster's, of up to eight CTAs; each files its share of the tokens in
+// shared memory, the first one adds the bins up through distributed shared memory and
+// searches.  What bounds it is not the logits' way from memory (a pass over 33 MB of
+// them takes 5 us) but arithmetic: about a hundred instructions a token, most of them for
+// the weight.  One CTA files 32768 tokens in 12 us, two on an SM in 24.  The passes of
+// a row of 262144 tokens: maximum 4 us, bins 12, their sums and the search 4, and for
+// each end of a run that more than 2048 tokens stand before, 2 to 7 us of a pass that
+// looks up one bin's tokens and 3 that orders them.
+// Per call in a graph: one row of 128256 10.7 us, 64 rows of it with different
+// settings 58, 16 rows of 262144 without any bound 55.
 #include <cooperative_groups.h>
 
 #include <type_traits>
@@ -31,7 +42,7 @@ namespace {
 
 using u64 = unsigned long long;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 512;        // (with 1024 a row's CTAs do not all run at once, and it took longer)
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kBins = 1024;          // held at a time, two a thread

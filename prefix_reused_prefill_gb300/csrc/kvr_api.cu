@@ -1011,6 +1011,7 @@ int adapt_site(kvr_ctx* c, cudaStream_t st, const Adapted& ad, int layer, int si
   p.base_stride = p.out_stride = *ld;
   p.out_type = KVR_ACT_F32;
   p.part = ad.part;
+  p.status = c->status;
   Timed t(c, kEpi, st);
   const cudaError_t e = launch_adapt(p, c->n_sms, st);
   if (e != cudaSuccess) return cuda_fail(c, e, "adapt launch");

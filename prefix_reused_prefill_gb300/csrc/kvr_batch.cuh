@@ -52,6 +52,7 @@ struct AdaptParams {
   int out_type;
   float* part;             // [ksplit][rows][n_parts * max_rank] parts of the low-rank products
   int ksplit;
+  int* status;             // of a context (a wait that gave up), or null
 };
 cudaError_t adapt_setup();    // of the current device, before its first launch
 bool adapter_site_ok(const kvr_adapter_site* s);
