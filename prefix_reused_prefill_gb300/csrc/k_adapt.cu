@@ -13,8 +13,8 @@
 // straight from global memory, 16 or 8 bytes each: which inputs share a fragment
 // does not matter as long as both operands agree.  Bound: the chain of loads (whose rows, which
 // adapter, where it is, its values), twice; where each row has its own adapter, the loads of A
-// and B.  q, k and v of 3584 inputs, one row of rank 16: 7.8 us; of 4096 inputs, 64 rows with an
-// adapter each: 21 us (40 MB).  Eight sequences of 8 rows, 18944 inputs, 32-bit outputs: 12.5 us.
+// and B.  q, k and v of 3584 inputs, one row of rank 16: 8.4 us; of 4096 inputs, 64 rows with an
+// adapter each: 19.5 us (40 MB).  Eight sequences of 8 rows, 18944 inputs, 32-bit outputs: 12 us.
 //
 // Many: tiles of one sequence's rows, below.
 #include <cooperative_groups.h>
@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 2) expand_kernel(const AdaptParams p
 // 85 us (105 with mma.sync), of which a plain copy of x, base and out would take 33.
 constexpr int TR = 64;
 constexpr int kStep = 64;       // inputs of a stage: 128 bytes a row
-constexpr int kStages = 3;
+constexpr int kStages = 3;      // (4 and 6 leave one CTA an SM: four prompts 107 us, with 3 100)
 constexpr int kMaxCluster = 8;
 constexpr int ER = 128, kTileN = 128;   // rows and outputs of a tile of expand
 
@@ -1120,12 +1120,16 @@ cudaError_t launch(const AdaptParams& p, cudaStream_t st) {
   return launch_k(expand_kernel<T, float, kTerms>, grid, kThreads, 0, st, p);
 }
 
-// Rows of a sequence, on average, from which tiles of 64 rows pay.
-constexpr int kManyRows = 24;
+// Rows of a sequence, on average, and in all, from which tiles of one sequence's rows pay.  Sequences x rows, tiles of
+// eight against these, us (q, k and v of 3584 inputs; rank 16): 32 x 8 22, 24; 32 x 16 38, 25; 64 x 16 78,
+// 37; 8 x 8 9, 15; 8 x 16 14, 15 (rank 64: 20, 18); 8 x 24 17, 15; 1 x 40 9, 13.
+constexpr int kManyRows = 16, kManyInAll = 128;
 
 int adapt_split(const kvr_adapter_site& s, int rows, int sms) {
+  // parts of the inputs: two CTAs an SM (8 x 8 rows of 18944 inputs: 12.0 us, one 14.3), of 192 inputs each at least
+  // (64 rows of 4096 inputs, an adapter each: 19.5 us, with 128 21.1; one row: 8.4 and 7.8)
   const int blocks = (rows + R - 1) / R;
-  const int most = std::max(1, std::min(kAdaptMaxSplit, s.k / 128));
+  const int most = std::max(1, std::min(kAdaptMaxSplit, s.k / 192));
   return std::max(1, std::min(most, 2 * sms / blocks));
 }
 
@@ -1154,7 +1158,7 @@ size_t adapt_work_bytes(const kvr_adapter_site& s, int rows) {
 }
 
 cudaError_t launch_adapt(AdaptParams p, int sms, cudaStream_t st) {
-  if (p.rows >= kManyRows * (long long)p.n_seq) {
+  if (p.rows >= kManyInAll && p.rows >= kManyRows * (long long)p.n_seq) {
     if (p.site.type == KVR_ACT_F16)
       return p.out_type == KVR_ACT_F32 ? launch_tiles<__half, float, 2>(p, sms, st) : launch_tiles<__half, __half, 2>(p, sms, st);
     return p.out_type == KVR_ACT_F32 ? launch_tiles<__nv_bfloat16, float, 3>(p, sms, st)

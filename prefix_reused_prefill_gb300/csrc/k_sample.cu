@@ -52,7 +52,6 @@ constexpr float kNothing = 46.f;     // binary orders from the maximum on which 
 // 32 orders are held at a time and a bin of the bulk of 262144 tokens is about as many as can be put
 // in order; where tokens are only counted 64, so that one pass holds all.
 constexpr int kFine = 5, kCoarse = 6;
-constexpr int kCopies = 2;           // of the bins, by lane: equal logits meet in one
 constexpr int kCap = 2048;           // tokens that one CTA puts in order
 constexpr int kCount = 128;          // as many by counting the larger ones
 constexpr int kDigit = 10;           // bits of a place taken at a time where a bin holds more
@@ -85,7 +84,7 @@ __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162f
 __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
 
 struct Bins {
-  uint32_t cnt[kCopies][kBins + 32], lo[kCopies][kBins + 32], hi[kCopies][kBins + 32];   // (Sampler::add)
+  uint32_t cnt[kBins + 32], lo[kBins + 32], hi[kBins + 32];   // (Sampler::add; two of each, by lane, were slower)
 };
 struct Smem {
   float2 pow2[1024];
@@ -149,12 +148,30 @@ struct Row {
   float floor;          // logits below weigh less than min_p
   // of a rejected draft's row: weight beyond the drafter's
   const float* q;       // null: all weight of `draft` goes
-  double total;
+  u64 total;            // of p, its first bit the highest; (zeros in front) + 126
+  int total_low;
   int draft;
   bool draft_in;        // within the vocabulary; its logit
   float draft_x;
   u64 kept;             // places from here on
   bool rest;
+
+  __device__ __forceinline__ void set_total(u64 t) {
+    const int zeros = __clzll((long long)t);
+    total = t << zeros;
+    total_low = zeros + 126;
+  }
+  // q total, to the next whole number (nothing for what is not a probability; in whole numbers, as 64-bit floats
+  // run at a thirtieth of their rate here: 40 us for a row's 32768 tokens)
+  __device__ __forceinline__ u64 taken(float q) const {
+    if (!(q >= 0x1p-126f)) return 0;
+    const uint32_t b = __float_as_uint(q), m = (b << 8) | 0x80000000u;
+    const u64 prod = (u64)(uint32_t)(total >> 32) * m + __umulhi((uint32_t)total, m);
+    const int s = total_low - (int)(b >> 23);
+    if (s <= 0) return s < 0 ? ~0ull : prod;   // (below: q above 1)
+    if (s > 64) return 0;
+    return (s < 64 ? prod >> s : 0) + ((prod >> (s - 1)) & 1);
+  }
 
   // binary orders below the maximum, as a pair (of what is at infinity only the
   // first number counts)
@@ -437,8 +454,8 @@ struct Sampler {
   __device__ __forceinline__ u64 left(u64 v, int i) const {
     if (!w.rest) return v;
     if (!w.q) return i == w.draft ? 0 : v;
-    const double d = (double)v - fmax((double)w.q[i], 0.) * w.total;   // (never more than the token's own weight)
-    return d > 0. ? (u64)__double2ll_rn(d) : 0;
+    const u64 t = w.taken(w.q[i]);
+    return v > t ? v - t : 0;
   }
   // whether a token is one of the row's
   __device__ __forceinline__ bool in_row(float x, int i) const {
@@ -463,17 +480,17 @@ struct Sampler {
   // together: a lane has a bin of its own for what goes nowhere.
   template <int N>
   __device__ __forceinline__ void add(const int (&bin)[N], const u64 (&v)[N]) const {
-    const int c = threadIdx.x % kCopies, none = kBins + (threadIdx.x & 31);
+    const int none = kBins + (threadIdx.x & 31);
     uint32_t old[N], at[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) {
       at[k] = bin[k] >= 0 ? bin[k] : none;
-      atomicAdd(&sm.bins.cnt[c][at[k]], 1u);
-      old[k] = atomicAdd(&sm.bins.lo[c][at[k]], (uint32_t)v[k]);
+      atomicAdd(&sm.bins.cnt[at[k]], 1u);
+      old[k] = atomicAdd(&sm.bins.lo[at[k]], (uint32_t)v[k]);
     }
 #pragma unroll
     for (int k = 0; k < N; ++k)
-      atomicAdd(&sm.bins.hi[c][at[k]], (uint32_t)(v[k] >> 32) + (old[k] + (uint32_t)v[k] < old[k] ? 1u : 0u));
+      atomicAdd(&sm.bins.hi[at[k]], (uint32_t)(v[k] >> 32) + (old[k] + (uint32_t)v[k] < old[k] ? 1u : 0u));
   }
 
   // Running sums over the cluster's bins, after what is in front of them, to the
@@ -484,27 +501,18 @@ struct Sampler {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = 2 * threadIdx.x;
     u64 v[2] = {0, 0};
     uint32_t c[2] = {0, 0};
-    auto take = [&](const Bins& o, int copy) {
-      const uint2 n = *reinterpret_cast<const uint2*>(&o.cnt[copy][b]);
-      c[0] += n.x;
-      c[1] += n.y;
+    {
+      const uint2 n = *reinterpret_cast<const uint2*>(&sm.bins.cnt[b]);
+      c[0] = n.x;
+      c[1] = n.y;
       if (MASS) {
-        const uint2 l = *reinterpret_cast<const uint2*>(&o.lo[copy][b]);
-        const uint2 h = *reinterpret_cast<const uint2*>(&o.hi[copy][b]);
-        v[0] += (u64)h.x << 32 | l.x;
-        v[1] += (u64)h.y << 32 | l.y;
+        const uint2 l = *reinterpret_cast<const uint2*>(&sm.bins.lo[b]);
+        const uint2 h = *reinterpret_cast<const uint2*>(&sm.bins.hi[b]);
+        v[0] = (u64)h.x << 32 | l.x;
+        v[1] = (u64)h.y << 32 | l.y;
       }
-    };
-#pragma unroll
-    for (int k = 0; k < kCopies; ++k) take(sm.bins, k);
+    }
     if (ctas > 1) {
-      if (rank) {
-        *reinterpret_cast<uint2*>(&sm.bins.cnt[0][b]) = make_uint2(c[0], c[1]);
-        if (MASS) {
-          *reinterpret_cast<uint2*>(&sm.bins.lo[0][b]) = make_uint2((uint32_t)v[0], (uint32_t)v[1]);
-          *reinterpret_cast<uint2*>(&sm.bins.hi[0][b]) = make_uint2((uint32_t)(v[0] >> 32), (uint32_t)(v[1] >> 32));
-        }
-      }
       cluster.sync();
       if (rank) return;
       // (all CTAs' on their way together; the first one stands in for those that there are not)
@@ -512,10 +520,10 @@ struct Sampler {
 #pragma unroll
       for (int j = 1; j < kMaxCluster; ++j) {
         const Bins& o = cluster.map_shared_rank(&sm, j < ctas ? j : 0)->bins;
-        n[j] = *reinterpret_cast<const uint2*>(&o.cnt[0][b]);
+        n[j] = *reinterpret_cast<const uint2*>(&o.cnt[b]);
         if (MASS) {
-          l[j] = *reinterpret_cast<const uint2*>(&o.lo[0][b]);
-          h[j] = *reinterpret_cast<const uint2*>(&o.hi[0][b]);
+          l[j] = *reinterpret_cast<const uint2*>(&o.lo[b]);
+          h[j] = *reinterpret_cast<const uint2*>(&o.hi[b]);
         }
       }
 #pragma unroll
@@ -607,7 +615,7 @@ struct Sampler {
 #pragma unroll
         for (int k = 0; k < N; ++k)
           if (c.in_row(x[k], i + k))
-            atomicAdd(&c.sm.bins.cnt[threadIdx.x % kCopies][c.bin_of((c.w.max - fminf(x[k], kFinite)) * c.w.ch)], 1u);
+            atomicAdd(&c.sm.bins.cnt[c.bin_of((c.w.max - fminf(x[k], kFinite)) * c.w.ch)], 1u);
         return;
       }
       u64 yh[N / 2], yl[N / 2], steps[N / 2];
@@ -795,7 +803,7 @@ struct Sampler {
       // counting the larger ones of a part
       const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
       uint32_t* start = sm.part_c;
-      uint32_t* fill = sm.bins.cnt[0];
+      uint32_t* fill = sm.bins.cnt;
       uint32_t low = 0xffffffffu, top = 0;
       for (int i = threadIdx.x; i < n; i += kThreads) {
         const uint32_t k = (uint32_t)(sm.place[i] >> kSampleIndexBits);
@@ -974,7 +982,7 @@ __device__ __forceinline__ u64 decide(Sampler<T>& s, const Wanted& want, int at,
     if (stays) return 0;
     // what the draft left of the kept tokens, if anything
     s.w.rest = true;
-    s.w.total = (double)total;
+    s.w.set_total(total);
     u64 mine[kPer], some = 0;
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
@@ -1111,13 +1119,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                                : -INFINITY;
   s.w.rest = false;
   s.w.kept = 0;
+  u64 kept = 0, total = 1ull << kFix;
   s.w.q = p.q ? p.q + p.q_stride * r : nullptr;
   s.w.draft = draft;
   s.w.draft_in = draft >= 0 && draft < p.vocab;
   s.w.draft_x = s.w.draft_in ? to_float(row[draft]) : 0.f;
-  s.w.total = 0.;
+  s.w.set_total(total);
 
-  u64 kept = 0, total = 1ull << kFix;
   bool listed = certain;            // the kept tokens are in the first CTA's list, in order
   int at = 0, n = 1;
   if (certain) {
@@ -1196,7 +1204,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         s.sync();
         s.w.rest = true;
         s.w.kept = kept;
-        s.w.total = (double)total;
+        s.w.set_total(total);
         s.template file<true>(0);
         s.sync();
         const u64 left = s.first.total_w;
