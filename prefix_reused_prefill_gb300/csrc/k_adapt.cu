@@ -947,10 +947,10 @@ __device__ __forceinline__ void expand_run(const AdaptParams& p, const Tile& til
   if (n > 1) load((c0 + 1) * kTileN, 1);
   for (int i = 0; i < n; ++i) {
     const int b = i & 1, col = (c0 + i) * kTileN;
-    if (i + 1 < n) multiply(b ^ 1);   // (its sums have been read: the last tile but one's)
     Eight<O> o[2][4];
     fetch(col, o[0]);
     fetch(col + 32, o[1]);
+    if (i + 1 < n) multiply(b ^ 1);   // (its sums have been read: the last tile but one's)
     const bool ok = dev::mbar_wait(sums.bars + 8 * b, (sums.phases >> b) & 1u, p.status);
     sums.phases ^= 1u << b;
     tc_after();
