@@ -773,9 +773,8 @@ typedef struct kvr_adapter_site {
  *   work       kvr_adapt_work_bytes(site, rows) bytes, 16-byte aligned, for this call alone.
  * x, base and out are 16-byte aligned.  Sums are 32-bit; for outputs of
  * 16 bits they may be the matrix units' own, whose last bits are cut.  The low-rank product
- * goes on in terms of the site's type, two (fp16: 22 bits) or, for bf16, two or,
- * with 32-bit outputs, three (16 or 24 bits); out is rounded once.  A row whose
- * low-rank product is not finite reads NaN.
+ * goes on in three terms of the site's type, whose sum is its value to 24 bits; out is
+ * rounded once.  A row whose low-rank product is not finite reads NaN.
  */
 size_t kvr_adapt_work_bytes(const kvr_adapter_site* site, int rows);
 int kvr_adapt(const kvr_adapter_site* site, const void* x, long long x_stride, const int32_t* cu_rows,

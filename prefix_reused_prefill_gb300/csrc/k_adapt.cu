@@ -1,9 +1,9 @@
 // Low-rank adapters beside a shared projection (include/kvr.h).
 //
 // Two launches, s = A x and out = base + scale B s: all outputs need all of s, and both
-// read their matrices once.  s is held scaled by a row's power of two, in two or three
-// terms of the type, so that B's products are those of 16-bit matrix units and what is
-// rounded away is far below the output's own rounding.
+// read their matrices once.  s is held scaled by a row's power of two, in three terms of the type
+// whose sum is s to 24 bits and more, so that B's products are those of 16-bit matrix units and s is held as
+// a 32-bit float would hold it.
 //
 // Few rows a sequence.  shrink_kernel cuts the inputs into parts so that the CTAs
 // fill the SMs whatever the rows are, and every part leaves its sums; expand_kernel
@@ -80,6 +80,10 @@ __device__ __forceinline__ uint32_t pair_to(float lo, float hi) {
     return dev::pack_bf16x2(lo, hi);
   }
 }
+
+// Terms of s: each leaves half a step of what the one before it left, 2^-8 for bf16, 2^-11 for fp16.  (With two,
+// bf16 outputs of 254 rows were 1e-4 of their norm from those of s in 32-bit floats, and 0.5 us faster of 17.)
+constexpr int kTerms = 3;
 
 // The power of two by which a row whose largest element is `big` is held in terms of T
 // (`down` scales it to below 2), and NaN in `down` for a row that is not finite.
@@ -224,12 +228,12 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const AdaptParams p) {
 }
 
 // out = base + scale B s of one tile of rows and 16 outputs a warp.
-template <class T, class O, int TERMS>
+template <class T, class O>
 __global__ void __launch_bounds__(kThreads, 2) expand_kernel(const AdaptParams p) {
   constexpr int kS = KVR_MAX_RANK + 8;   // (rows shifted against one another in the banks)
   __shared__ int cu[kAdaptMaxSeqs + 1], which[kAdaptMaxSeqs];
   __shared__ Rows rows;
-  __shared__ __align__(16) T terms[TERMS][R][kS];
+  __shared__ __align__(16) T terms[kTerms][R][kS];
   __shared__ float factor[R];
   __shared__ __align__(16) float tile[R][kTileCols + 4];
   dev::pdl_trigger();
@@ -317,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 2) expand_kernel(const AdaptParams p
       float x = v[n] * down;
       if (j < (rank + 15) / 16 * 16)
 #pragma unroll
-        for (int m = 0; m < TERMS; ++m) {
+        for (int m = 0; m < kTerms; ++m) {
           const T h = to<T>(x);
           terms[m][r][j] = h;
           x -= from(h);
@@ -333,15 +337,15 @@ __global__ void __launch_bounds__(kThreads, 2) expand_kernel(const AdaptParams p
     const bool in_run = g >= run.first && g < run.end;
     for (int j0 = 0; j0 < run.rank; j0 += 16) {
       if (j0) fetch(j0);
-      uint2 y[TERMS];
+      uint2 y[kTerms];
 #pragma unroll
-      for (int m = 0; m < TERMS; ++m)
+      for (int m = 0; m < kTerms; ++m)
         y[m] = in_run ? *reinterpret_cast<const uint2*>(&terms[m][g][j0 + 4 * t]) : make_uint2(0u, 0u);
 #pragma unroll
       for (int n = 0; n < kWarps; ++n)
         if (n < tiles)
 #pragma unroll
-          for (int m = TERMS - 1; m >= 0; --m) mma<T>(acc[n], lo[n].x, hi[n].x, lo[n].y, hi[n].y, y[m].x, y[m].y);
+          for (int m = kTerms - 1; m >= 0; --m) mma<T>(acc[n], lo[n].x, hi[n].x, lo[n].y, hi[n].y, y[m].x, y[m].y);
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -468,19 +472,18 @@ __device__ __forceinline__ void find_tile(const AdaptParams& p, int t, Tile& til
 // The low-rank products of the tiles: terms [k][row][part * round16(max_rank)] and
 // a factor for each row and part, behind one another in p.part.
 struct Terms {
-  int ld, rows, count;
+  int ld, rows;
   uint8_t* base;
-  __host__ __device__ Terms(const AdaptParams& p, int count_)
-      : ld(p.site.n_parts * round16(p.site.max_rank)), rows(p.rows), count(count_),
-        base(reinterpret_cast<uint8_t*>(p.part)) {}
+  __host__ __device__ explicit Terms(const AdaptParams& p)
+      : ld(p.site.n_parts * round16(p.site.max_rank)), rows(p.rows), base(reinterpret_cast<uint8_t*>(p.part)) {}
   template <class T>
   __device__ __forceinline__ T* term(int k, int row) const {
     return reinterpret_cast<T*>(base) + ((long long)k * rows + row) * ld;
   }
   __device__ __forceinline__ float* factor(int row) const {
-    return reinterpret_cast<float*>(base + (long long)count * rows * ld * 2) + row * 3;
+    return reinterpret_cast<float*>(base + (long long)kTerms * rows * ld * 2) + row * 3;
   }
-  __host__ __device__ size_t bytes() const { return (size_t)count * rows * ld * 2 + (size_t)rows * 12; }
+  __host__ __device__ size_t bytes() const { return (size_t)kTerms * rows * ld * 2 + (size_t)rows * 12; }
 };
 
 // The tensor memory's products: operands in shared memory, rows of 128 bytes in the 128-byte swizzle,
@@ -543,7 +546,7 @@ __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_
 // chain that is 2e-6 of the sum.  Outputs of 16 bits do not see it.  For those of 32 bits chains are kChain stages, added
 // up in registers: below 3e-7.
 constexpr int kChain = 2;
-template <class T, int NC, int TERMS, bool TC, bool X16>
+template <class T, int NC, bool TC, bool X16>
 __global__ void __launch_bounds__(kThreads, 2) shrink_tiles_kernel(const AdaptParams p, int ks) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
   __shared__ Tile tile;
@@ -777,7 +780,7 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_tiles_kernel(const AdaptPa
     }
     __syncthreads();
   }
-  const Terms terms(p, TERMS);
+  const Terms terms(p);
   const int parts = whole ? p.site.n_parts : 1, mr16 = round16(p.site.max_rank);
   for (int i = r0 * parts + warp; i < min(r1, tile.rows) * parts; i += kWarps) {
     const int r = i / parts, j = i % parts;
@@ -795,7 +798,7 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_tiles_kernel(const AdaptPa
     const float up = scale_of(big, down);
     const int pj = whole ? j : blockIdx.z;
 #pragma unroll
-    for (int k = 0; k < TERMS; ++k) {
+    for (int k = 0; k < kTerms; ++k) {
       T* dst = terms.term<T>(k, tile.row0 + r) + pj * mr16;
 #pragma unroll
       for (int n = 0; n < KVR_MAX_RANK / 32; ++n) {
@@ -851,7 +854,7 @@ constexpr int kOperand = ER * 128;   // bytes of 128 rows of 64 ranks
 // `c1 - c0` tiles of 128 outputs of one part, of a tile of rows.  The outputs that
 // stand beside one another in a lane's sums are chosen: its four pairs are eight in
 // a row, so base and out need no way through shared memory.
-template <class T, class O, int TERMS>
+template <class T, class O>
 __device__ __forceinline__ void expand_run(const AdaptParams& p, const Tile& tile, float* factor, uint32_t smem, Sums& sums,
                                            int part, int left, int c0, int c1) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -860,7 +863,7 @@ __device__ __forceinline__ void expand_run(const AdaptParams& p, const Tile& til
   const bool adapted = tile.id != kNone;
   const int rank = adapted ? tile.ad.rank : 0, r16 = round16(rank);
   const int halves = (round16(p.site.max_rank) + 63) / 64;   // operands of 64 ranks
-  const uint32_t b_smem = smem + TERMS * halves * kOperand;
+  const uint32_t b_smem = smem + kTerms * halves * kOperand;
   // a thread's 16 bytes of a row of ranks (a power of two of them, the last ones without work)
   const int chunks = r16 / 8, shift = chunks > 1 ? 32 - __clz(chunks - 1) : 0;
   const int lr = threadIdx.x >> shift, lc = threadIdx.x & ((1 << shift) - 1), lstep = kThreads >> shift;
@@ -920,11 +923,11 @@ __device__ __forceinline__ void expand_run(const AdaptParams& p, const Tile& til
       tc_after();
       const uint64_t bd = smem_operand(b_smem + b * halves * kOperand);
 #pragma unroll 1
-      for (int k = TERMS - 1; k >= 0; --k) {   // (the smallest terms first)
+      for (int k = kTerms - 1; k >= 0; --k) {   // (the smallest terms first)
         const uint64_t sd = smem_operand(smem + k * halves * kOperand);
         for (int kk = 0; kk < r16 / 16; ++kk) {
           const int at = (kk >> 2) * (kOperand >> 4) + 2 * (kk & 3);
-          tc_mma(sums.at + b * kTileN, sd + at, bd + at, product_of<T>(ER, kTileN), k < TERMS - 1 || kk > 0);
+          tc_mma(sums.at + b * kTileN, sd + at, bd + at, product_of<T>(ER, kTileN), k < kTerms - 1 || kk > 0);
         }
       }
       tc_commit(sums.bars + 8 * b);
@@ -933,9 +936,9 @@ __device__ __forceinline__ void expand_run(const AdaptParams& p, const Tile& til
   tc_before();
   __syncthreads();   // (the last run's factors have been read)
   {
-    const Terms terms(p, TERMS);
+    const Terms terms(p);
 #pragma unroll
-    for (int k = 0; k < TERMS; ++k)
+    for (int k = 0; k < kTerms; ++k)
       for (int r = lr; r < ER && lc < chunks; r += lstep) {
         const T* src = terms.term<T>(k, tile.row0 + min(r, tile.rows - 1)) + part * round16(p.site.max_rank) + 8 * lc;
         cp16(smem + k * halves * kOperand + half + dev::swz128(r, lc & 7), src, r < tile.rows);
@@ -976,7 +979,7 @@ __device__ __forceinline__ void expand_run(const AdaptParams& p, const Tile& til
 // The tiles of 128 rows times their tiles of 128 outputs in equal runs, one a CTA:
 // while 128 rows and a part last the terms stay, and the next outputs' products run
 // and B is on its way while some are added to base and stored.
-template <class T, class O, int TERMS>
+template <class T, class O>
 __global__ void __launch_bounds__(kThreads, 2) expand_tiles_kernel(const AdaptParams p, int col_tiles) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
   __shared__ Tile tile;
@@ -1022,7 +1025,7 @@ __global__ void __launch_bounds__(kThreads, 2) expand_tiles_kernel(const AdaptPa
     }
     const int c0 = first - before, c1 = min(c0 + n, tiles);   // of this part
     u += c1 - c0;
-    expand_run<T, O, TERMS>(p, tile, factor, smem, sums, part, left, c0, c1);
+    expand_run<T, O>(p, tile, factor, smem, sums, part, left, c0, c1);
   }
   tc_before();
   __syncthreads();
@@ -1032,15 +1035,15 @@ __global__ void __launch_bounds__(kThreads, 2) expand_tiles_kernel(const AdaptPa
   }
 }
 
-int expand_tiles_smem(int max_rank, int terms) {
-  return (round16(max_rank) + 63) / 64 * (terms + 2) * kOperand + 1024;   // (operands start where their swizzle does)
+int expand_tiles_smem(int max_rank) {
+  return (round16(max_rank) + 63) / 64 * (kTerms + 2) * kOperand + 1024;   // (operands start where their swizzle does)
 }
 template <int NC>
 constexpr int shrink_tiles_smem() {
   return kStages * (TR + NC) * 128 + 1024;   // (stages start where their swizzle does)
 }
 
-template <class T, int NC, int TERMS, bool TC>
+template <class T, int NC, bool TC>
 cudaError_t launch_shrink_tiles(const AdaptParams& p, int tiles, int chunks, int sms, cudaStream_t st) {
   // CTAs of a tile: as many as 3/2 an SM (two run at a time), with 256 inputs each at least.  Four prompts in
   // 108 tiles: 96 us with two CTAs a tile, 101 with four, which then run in two waves; 254 rows the same either way.
@@ -1058,12 +1061,12 @@ cudaError_t launch_shrink_tiles(const AdaptParams& p, int tiles, int chunks, int
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 2 : 1;
-  if constexpr (TERMS == 3)
-    if (p.x16) return cudaLaunchKernelEx(&cfg, shrink_tiles_kernel<T, NC, TERMS, TC, true>, p, ks);
-  return cudaLaunchKernelEx(&cfg, shrink_tiles_kernel<T, NC, TERMS, TC, false>, p, ks);
+  if constexpr (std::is_same<T, __nv_bfloat16>::value && !TC)
+    if (p.x16) return cudaLaunchKernelEx(&cfg, shrink_tiles_kernel<T, NC, TC, true>, p, ks);
+  return cudaLaunchKernelEx(&cfg, shrink_tiles_kernel<T, NC, TC, false>, p, ks);
 }
 
-template <class T, class O, int TERMS>
+template <class T, class O>
 cudaError_t launch_tiles(const AdaptParams& p, int sms, cudaStream_t st) {
   const int tiles = p.rows / TR + std::min(p.n_seq, p.rows);   // at most
   const int wide = p.rows / ER + std::min(p.n_seq, p.rows);
@@ -1071,35 +1074,35 @@ cudaError_t launch_tiles(const AdaptParams& p, int sms, cudaStream_t st) {
   // all parts at once, as far as a CTA's sums hold them
   constexpr bool kTc = !std::is_same<O, float>::value;
   cudaError_t e;
-  if (stacked <= 64) e = launch_shrink_tiles<T, 64, TERMS, kTc>(p, tiles, 1, sms, st);
-  else if (stacked <= 128) e = launch_shrink_tiles<T, 128, TERMS, kTc>(p, tiles, 1, sms, st);
-  else if (kTc && stacked <= 192) e = launch_shrink_tiles<T, kTc ? 192 : 128, TERMS, kTc>(p, tiles, 1, sms, st);
-  else if (p.site.max_rank <= 64) e = launch_shrink_tiles<T, 64, TERMS, kTc>(p, tiles, p.site.n_parts, sms, st);
-  else e = launch_shrink_tiles<T, 128, TERMS, kTc>(p, tiles, p.site.n_parts, sms, st);
+  if (stacked <= 64) e = launch_shrink_tiles<T, 64, kTc>(p, tiles, 1, sms, st);
+  else if (stacked <= 128) e = launch_shrink_tiles<T, 128, kTc>(p, tiles, 1, sms, st);
+  else if (kTc && stacked <= 192) e = launch_shrink_tiles<T, kTc ? 192 : 128, kTc>(p, tiles, 1, sms, st);
+  else if (p.site.max_rank <= 64) e = launch_shrink_tiles<T, 64, kTc>(p, tiles, p.site.n_parts, sms, st);
+  else e = launch_shrink_tiles<T, 128, kTc>(p, tiles, p.site.n_parts, sms, st);
   if (e != cudaSuccess) return e;
   int cols = 0;
   for (int j = 0; j < p.site.n_parts; ++j) cols += (p.site.cols[j] + kTileN - 1) / kTileN;
-  const int smem = expand_tiles_smem(p.site.max_rank, TERMS);
+  const int smem = expand_tiles_smem(p.site.max_rank);
   const int per_sm = smem <= 110 * 1024 ? 2 : 1;
   const int ctas = (int)std::min<long long>((long long)sms * per_sm, (long long)wide * cols);
-  return launch_k(expand_tiles_kernel<T, O, TERMS>, dim3(ctas), dim3(kThreads), smem, st, p, cols);
+  return launch_k(expand_tiles_kernel<T, O>, dim3(ctas), dim3(kThreads), smem, st, p, cols);
 }
 
-template <class T, int TERMS, bool TC, bool X16>
+template <class T, bool TC, bool X16>
 cudaError_t setup_shrink() {
   const auto set = [](void (*k)(AdaptParams, int), int bytes) {
     return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   };
-  cudaError_t e = set(shrink_tiles_kernel<T, 64, TERMS, TC, X16>, shrink_tiles_smem<64>());
-  if (e == cudaSuccess) e = set(shrink_tiles_kernel<T, 128, TERMS, TC, X16>, shrink_tiles_smem<128>());
+  cudaError_t e = set(shrink_tiles_kernel<T, 64, TC, X16>, shrink_tiles_smem<64>());
+  if (e == cudaSuccess) e = set(shrink_tiles_kernel<T, 128, TC, X16>, shrink_tiles_smem<128>());
   if constexpr (TC)
-    if (e == cudaSuccess) e = set(shrink_tiles_kernel<T, 192, TERMS, TC, X16>, shrink_tiles_smem<192>());
+    if (e == cudaSuccess) e = set(shrink_tiles_kernel<T, 192, TC, X16>, shrink_tiles_smem<192>());
   return e;
 }
-template <class T, class O, int TERMS>
+template <class T, class O>
 cudaError_t setup_expand() {
-  return cudaFuncSetAttribute(expand_tiles_kernel<T, O, TERMS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              expand_tiles_smem(KVR_MAX_RANK, TERMS));
+  return cudaFuncSetAttribute(expand_tiles_kernel<T, O>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              expand_tiles_smem(KVR_MAX_RANK));
 }
 
 template <class T>
@@ -1115,9 +1118,8 @@ cudaError_t launch(const AdaptParams& p, cudaStream_t st) {
   int tiles = 0;
   for (int j = 0; j < p.site.n_parts; ++j) tiles += (p.site.cols[j] + kTileCols - 1) / kTileCols;
   const dim3 grid(blocks, tiles);
-  if (p.out_type != KVR_ACT_F32) return launch_k(expand_kernel<T, T, 2>, grid, kThreads, 0, st, p);
-  constexpr int kTerms = std::is_same<T, __half>::value ? 2 : 3;
-  return launch_k(expand_kernel<T, float, kTerms>, grid, kThreads, 0, st, p);
+  if (p.out_type != KVR_ACT_F32) return launch_k(expand_kernel<T, T>, grid, kThreads, 0, st, p);
+  return launch_k(expand_kernel<T, float>, grid, kThreads, 0, st, p);
 }
 
 // Rows of a sequence, on average, and in all, from which tiles of one sequence's rows pay.  Sequences x rows, tiles of
@@ -1136,15 +1138,15 @@ int adapt_split(const kvr_adapter_site& s, int rows, int sms) {
 }  // namespace
 
 cudaError_t adapt_setup() {
-  cudaError_t e = setup_shrink<__nv_bfloat16, 2, true, false>();
-  if (e == cudaSuccess) e = setup_shrink<__nv_bfloat16, 3, false, false>();
-  if (e == cudaSuccess) e = setup_shrink<__nv_bfloat16, 3, false, true>();   // (the layer stack's: 32-bit outputs)
-  if (e == cudaSuccess) e = setup_shrink<__half, 2, true, false>();
-  if (e == cudaSuccess) e = setup_shrink<__half, 2, false, false>();
-  if (e == cudaSuccess) e = setup_expand<__nv_bfloat16, __nv_bfloat16, 2>();
-  if (e == cudaSuccess) e = setup_expand<__nv_bfloat16, float, 3>();
-  if (e == cudaSuccess) e = setup_expand<__half, __half, 2>();
-  if (e == cudaSuccess) e = setup_expand<__half, float, 2>();
+  cudaError_t e = setup_shrink<__nv_bfloat16, true, false>();
+  if (e == cudaSuccess) e = setup_shrink<__nv_bfloat16, false, false>();
+  if (e == cudaSuccess) e = setup_shrink<__nv_bfloat16, false, true>();   // (the layer stack's: 32-bit outputs)
+  if (e == cudaSuccess) e = setup_shrink<__half, true, false>();
+  if (e == cudaSuccess) e = setup_shrink<__half, false, false>();
+  if (e == cudaSuccess) e = setup_expand<__nv_bfloat16, __nv_bfloat16>();
+  if (e == cudaSuccess) e = setup_expand<__nv_bfloat16, float>();
+  if (e == cudaSuccess) e = setup_expand<__half, __half>();
+  if (e == cudaSuccess) e = setup_expand<__half, float>();
   return e;
 }
 
@@ -1154,15 +1156,15 @@ size_t adapt_work_bytes(const kvr_adapter_site& s, int rows) {
   p.site = s;
   p.rows = rows;
   return std::max((size_t)adapt_split(s, rows, 1024) * rows * s.n_parts * s.max_rank * sizeof(float),
-                  Terms(p, 3).bytes());
+                  Terms(p).bytes());
 }
 
 cudaError_t launch_adapt(AdaptParams p, int sms, cudaStream_t st) {
   if (p.rows >= kManyInAll && p.rows >= kManyRows * (long long)p.n_seq) {
     if (p.site.type == KVR_ACT_F16)
-      return p.out_type == KVR_ACT_F32 ? launch_tiles<__half, float, 2>(p, sms, st) : launch_tiles<__half, __half, 2>(p, sms, st);
-    return p.out_type == KVR_ACT_F32 ? launch_tiles<__nv_bfloat16, float, 3>(p, sms, st)
-                                     : launch_tiles<__nv_bfloat16, __nv_bfloat16, 2>(p, sms, st);
+      return p.out_type == KVR_ACT_F32 ? launch_tiles<__half, float>(p, sms, st) : launch_tiles<__half, __half>(p, sms, st);
+    return p.out_type == KVR_ACT_F32 ? launch_tiles<__nv_bfloat16, float>(p, sms, st)
+                                     : launch_tiles<__nv_bfloat16, __nv_bfloat16>(p, sms, st);
   }
   p.ksplit = adapt_split(p.site, p.rows, std::min(sms, 1024));
   return p.site.type == KVR_ACT_F16 ? launch<__half>(p, st) : launch<__nv_bfloat16>(p, st);
