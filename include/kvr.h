@@ -771,9 +771,8 @@ typedef struct kvr_adapter_site {
  *              strides in elements (multiples of 8).  base may be out (the same stride
  *              then) or null (zeros); otherwise out shares no memory with the inputs.
  *   work       kvr_adapt_work_bytes(site, rows) bytes, 16-byte aligned, for this call alone.
- * x, base and out are 16-byte aligned.  Sums are 32-bit; for outputs of
- * 16 bits they may be the matrix units' own, whose last bits are cut.  The low-rank product
- * goes on in three terms of the site's type, whose sum is its value to 24 bits; out is
+ * x, base and out are 16-byte aligned.  Sums are 32-bit, the matrix units' own (whose last
+ * bits are cut) over 128 inputs at most.  The low-rank product goes on in three terms of the site's type, whose sum is its value to 24 bits; out is
  * rounded once.  A row whose low-rank product is not finite reads NaN.
  */
 size_t kvr_adapt_work_bytes(const kvr_adapter_site* site, int rows);

@@ -487,7 +487,7 @@ struct Terms {
 };
 
 // The tensor memory's products: operands in shared memory, rows of 128 bytes in the 128-byte swizzle,
-// eight of them 1024 bytes apart; sums of row i in lane i.
+// eight of them 1024 bytes apart; sums of row i of 128 in lane i.
 __device__ __forceinline__ uint64_t smem_operand(uint32_t at) {
   return (uint64_t)((at >> 4) & 0x3FFFu) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
 }
@@ -507,23 +507,8 @@ __device__ __forceinline__ void tc_mma(uint32_t sums, uint64_t a, uint64_t b, ui
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void tc_load32(uint32_t at, float (&v)[32]) {
-  uint32_t r[32];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
-      "%30, %31}, [%32];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(at)
-      : "memory");
-#pragma unroll
-  for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(r[k]);
-}
-// 32 columns of 16 lanes, as mma.sync's sums of four products lie in a warp
+// 32 columns of 16 lanes, as mma.sync's sums of four products lie in a warp.  (Products of 64 rows have sixteen of them
+// in each 32 lanes.)
 __device__ __forceinline__ void tc_load16x32(uint32_t at, float (&v)[4][4]) {
   uint32_t r[16];
   asm volatile(
@@ -541,10 +526,9 @@ __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::befor
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
 // One chunk of NC stacked rows of A (all parts, or one) of one tile and one part of the inputs.
-// X16: x is fp16 that holds bf16 values.  TC: on tcgen05, whose chain of products is the whole part.
+// X16: x is fp16 that holds bf16 values.  TC: on tcgen05.
 // Matrix units cut a sum's last bits at every product of 16 inputs instead of rounding them; over 4096 inputs in one
-// chain that is 2e-6 of the sum.  Outputs of 16 bits do not see it.  For those of 32 bits chains are kChain stages, added
-// up in registers: below 3e-7.
+// chain that is 2e-6 of the sum.  So chains are kChain stages, added up in registers: below 3e-7.
 constexpr int kChain = 2;
 template <class T, int NC, bool TC, bool X16>
 __global__ void __launch_bounds__(kThreads, 2) shrink_tiles_kernel(const AdaptParams p, int ks) {
@@ -619,13 +603,13 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_tiles_kernel(const AdaptPa
     a_at[kk] = base + dev::swz128(wr * 32 + (lane & 15), 2 * kk + (lane >> 4));
     b_at[kk] = base + kXBytes + dev::swz128(wn * (NC / 4) + (lane & 7) + ((lane >> 4) << 3), 2 * kk + ((lane >> 3) & 1));
   }
-  float acc[2][kNT][4], sum[2][kNT][4];
+  // the chains' sums: TC: rows 16 (warp % 4) + g and + 8, outputs (warp / 4) NC / 2 + 8 n + 2 t and + 1
+  constexpr int kSums = TC ? NC / 16 : 2 * kNT;
+  float sum[kSums][4];
 #pragma unroll
-  for (int m = 0; m < 2; ++m)
+  for (int n = 0; n < kSums; ++n)
 #pragma unroll
-    for (int n = 0; n < kNT; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[m][n][e] = sum[m][n][e] = 0.f;
+    for (int e = 0; e < 4; ++e) sum[n][e] = 0.f;
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) {
     if (s0 + i < s1) load(s0 + i, i);
@@ -644,12 +628,11 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_tiles_kernel(const AdaptPa
       __syncthreads();
       if (threadIdx.x == 0) {
         const uint32_t st = base + at * kStage;
-        // (128 rows: those behind the tile's 64 are of A, and their sums nobody reads)
         const uint64_t xd = smem_operand(st), ad = smem_operand(st + kXBytes);
         tc_after();
 #pragma unroll
         for (int kk = 0; kk < kStep / 16; ++kk)
-          tc_mma(sums_at, xd + 2 * kk, ad + 2 * kk, product_of<T>(128, NC), s > s0 || kk > 0);
+          tc_mma(sums_at, xd + 2 * kk, ad + 2 * kk, product_of<T>(TR, NC), (s - s0) % kChain != 0 || kk > 0);
         tc_commit(dev::smem_u32(&bars[at]));
       }
       // the stage of the step before, once its products are over
@@ -659,8 +642,23 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_tiles_kernel(const AdaptPa
       }
       cp_commit();
       at = at + 1 == kStages ? 0 : at + 1;
+      if ((s - s0) % kChain == kChain - 1 || s + 1 == s1) {   // (the next chain's products wait for every warp's loads)
+        over(s);
+        tc_after();
+#pragma unroll
+        for (int c = 0; c < kSums; c += 4) {
+          float v[4][4];
+          tc_load16x32(sums_at + ((uint32_t)(32 * (warp & 3)) << 16) + (warp >> 2) * (NC / 2) + 8 * c, v);
+#pragma unroll
+          for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[c + n][e] += v[n][e];
+        }
+        tc_before();
+      }
     }
   } else {
+    float acc[2][kNT][4];
     for (int s = s0; s < s1; ++s) {
       cp_wait<kStages - 2>();
       __syncthreads();
@@ -668,17 +666,14 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_tiles_kernel(const AdaptPa
       cp_commit();
       const uint32_t st = at * kStage;
       at = at + 1 == kStages ? 0 : at + 1;
-      if ((s - s0) % kChain == 0) {
+      if ((s - s0) % kChain == 0)
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+        for (int n = 0; n < kSums; ++n)
 #pragma unroll
-          for (int n = 0; n < kNT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              sum[m][n][e] += acc[m][n][e];
-              acc[m][n][e] = 0.f;
-            }
-      }
+          for (int e = 0; e < 4; ++e) {
+            if (s > s0) sum[n][e] += acc[n / kNT][n % kNT][e];
+            acc[n / kNT][n % kNT][e] = 0.f;
+          }
 #pragma unroll
       for (int kk = 0; kk < kStep / 16; ++kk) {
         uint32_t a[2][4];
@@ -701,46 +696,28 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_tiles_kernel(const AdaptPa
         }
       }
     }
+#pragma unroll
+    for (int n = 0; n < kSums; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[n][e] += acc[n / kNT][n % kNT][e];
   }
   cp_wait<0>();
-  if (TC) over(s1 - 1);   // (and with them all before)
   __syncthreads();
   // the cluster's sums, a share of the rows each, a warp a row
   float* sums = reinterpret_cast<float*>(smem);
   const int g = lane >> 2, t = lane & 3;
-  if (TC) {
-    // a warp reads the 32 lanes that its number allows: 0, 1, 4 and 5 have rows of the tile
+#pragma unroll
+  for (int n = 0; n < kSums; ++n) {
+    const int r = TC ? 16 * (warp & 3) + g : wr * 32 + n / kNT * 16 + g;
+    const int q = TC ? (warp >> 2) * (NC / 2) + 8 * n : wn * (NC / 4) + n % kNT * 8;
+    float* d = sums + r * kLd + q + 2 * t;
+    if (!ok) sum[n][0] = sum[n][1] = sum[n][2] = sum[n][3] = __int_as_float(0x7fffffff);   // (a wait gave up)
+    *reinterpret_cast<float2*>(d) = make_float2(sum[n][0], sum[n][1]);
+    *reinterpret_cast<float2*>(d + 8 * kLd) = make_float2(sum[n][2], sum[n][3]);
+  }
+  if (TC && warp == 0) {   // (all warps' loads are over: the barrier above)
     tc_after();
-    if ((warp & 3) < 2)
-#pragma unroll
-      for (int c = 0; c < NC / 2; c += 32) {
-        const int col = (warp >> 2) * (NC / 2) + c, r = 32 * (warp & 3) + lane;
-        float v[32];
-        tc_load32(sums_at + ((uint32_t)(32 * (warp & 3)) << 16) + col, v);
-#pragma unroll
-        for (int k = 0; k < 32; k += 4) {
-          float4 w = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
-          if (!ok) w.x = w.y = w.z = w.w = __int_as_float(0x7fffffff);   // (a wait gave up)
-          *reinterpret_cast<float4*>(sums + r * kLd + col + k) = w;
-        }
-      }
-    tc_before();
-    __syncthreads();
-    if (warp == 0) {
-      tc_after();
-      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(sums_at), "r"(kSumCols));
-    }
-  } else {
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-      for (int n = 0; n < kNT; ++n) {
-        float* d = sums + (wr * 32 + m * 16 + g) * kLd + wn * (NC / 4) + 8 * n + 2 * t;
-        d[0] = sum[m][n][0] + acc[m][n][0];
-        d[1] = sum[m][n][1] + acc[m][n][1];
-        d[8 * kLd] = sum[m][n][2] + acc[m][n][2];
-        d[8 * kLd + 1] = sum[m][n][3] + acc[m][n][3];
-      }
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(sums_at), "r"(kSumCols));
   }
   const cg::cluster_group cluster = cg::this_cluster();
   if (ks > 1) cluster.sync();

@@ -56,3 +56,34 @@ def test_the_low_rank_product_goes_on_in_24_bits(dtype, out, lens):
     leave 2^-16, of fp16 2^-22."""
     off = relative_errors(lens, 64, 2048, dtype, out, len(lens))
     assert off.numel() > 200 and off.abs().max() <= 9 * STEP, (off.numel(), off.abs().max() / STEP)
+
+
+@pytest.mark.parametrize("lens,k", [([1, 1, 1], 8192), ([60, 250, 3], 8192), ([7424], 8192), ([3000, 900, 4000], 1000)])
+@pytest.mark.parametrize("dtype,out", [(BF, BF), (BF, F32), (HF, HF), (HF, F32)])
+def test_long_sums_lose_nothing_to_their_length(dtype, out, lens, k):
+    """Sums of equal signs, whose cut bits add up: the mean of the errors.  In steps of 2^-23 at most: chains of 128 inputs
+    are eight products, which on average are added to 9/16 of the chain, 4.5; three products with B, 3; additions and
+    roundings have no bias.  8 with room for what they leave.  (One chain of 8192 inputs would cut 512 times.)  7424 rows
+    are tiles enough that none shares its inputs with another CTA."""
+    off = relative_errors(lens, k, 2048 if sum(lens) < 100 else 64, dtype, out, k + len(lens))
+    assert off.numel() > 20 and off.mean().abs() <= 8 * STEP, (off.numel(), off.mean() / STEP)
+
+
+@pytest.mark.parametrize("lens", [[5, 2], [300, 40]])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_sums_of_either_sign(dtype, lens):
+    """Outputs of 32 bits, rms error over rms output.  A chain's eight sums are on average 0.57 of its last one, each cut by
+    half a step at most in the mean and all the same way: 0.57 x 8 x 2^-24; the chains' sums are added with errors
+    of 2^-25 of the running sum, 64 of them: 4 x 2^-24; three terms times the rank's products with B the same as one
+    chain of 3: 3 x 2^-24.  In all 11.6 x 2^-24 = 7e-7."""
+    from prefix_reused_prefill_gb300 import Adapters
+    g = torch.Generator(device=DEV).manual_seed(3)
+    k, rank, rows, cols = 8192, 16, sum(lens), 512
+    a = (torch.randn(2 * rank, k, generator=g, device=DEV) * k ** -0.5).to(dtype)
+    b = torch.randn(2 * cols, rank, generator=g, device=DEV).to(dtype)
+    x = torch.randn(rows, k, generator=g, device=DEV).to(dtype)
+    got = Adapters([(a, b, 1.0)], [cols, cols]).kvr_adapt(x, i32([0] + np.cumsum(lens).tolist()), i32([0] * len(lens)),
+                                                           out=torch.empty(rows, 2 * cols, device=DEV)).double()
+    s = x.double() @ a.double().t()
+    want = torch.cat([s[:, j * rank:(j + 1) * rank] @ b[j * cols:(j + 1) * cols].double().t() for j in (0, 1)], 1)
+    assert ((got - want).pow(2).mean() / want.pow(2).mean()).sqrt() <= 7e-7
