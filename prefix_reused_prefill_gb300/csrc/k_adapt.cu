@@ -85,10 +85,13 @@ __device__ __forceinline__ uint32_t pair_to(float lo, float hi) {
 // bf16 outputs of 254 rows were 1e-4 of their norm from those of s in 32-bit floats, and 0.5 us faster of 17.)
 constexpr int kTerms = 3;
 
-// The power of two by which a row whose largest element is `big` is held in terms of T
-// (`down` scales it to below 2), and NaN in `down` for a row that is not finite.
+// The power of two by which a row whose largest element is `big` is held in terms of T (`down` scales it to
+// below 2, for fp16 to below 2^15, where elements far below the largest still have all their bits: their terms end
+// at 2^-24), and NaN in `down` for a row that is not finite.
+template <class T>
 __device__ __forceinline__ float scale_of(float big, float& down) {
-  const int e = min(max((int)(__float_as_uint(big) >> 23), 27), 253) - 127;
+  constexpr int kTop = std::is_same<T, __half>::value ? 14 : 0;
+  const int e = min(max((int)(__float_as_uint(big) >> 23) - kTop, 15), 253) - 127;
   down = big < INFINITY ? __int_as_float((127 - e) << 23) : __int_as_float(0x7fffffff);
   return __int_as_float((e + 127) << 23);
 }
@@ -314,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 2) expand_kernel(const AdaptParams p
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
     float down;
-    const float up = scale_of(big, down);
+    const float up = scale_of<T>(big, down);
 #pragma unroll
     for (int n = 0; n < KVR_MAX_RANK / 32; ++n) {
       const int j = lane + 32 * n;
@@ -772,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_tiles_kernel(const AdaptPa
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
     float down;
-    const float up = scale_of(big, down);
+    const float up = scale_of<T>(big, down);
     const int pj = whole ? j : blockIdx.z;
 #pragma unroll
     for (int k = 0; k < kTerms; ++k) {

@@ -24,17 +24,21 @@ def i32(v):
     return torch.tensor(v, dtype=torch.int32, device=DEV)
 
 
-def relative_errors(lens, k, cols, dtype, out, seed):
+def relative_errors(lens, k, cols, dtype, out, seed, less=1.0):
     """Of the elements next to zero, (what the kernel adds - the exact product) / the product.  B has one element a row, so
-    an output is one element of the low-rank product, times a number of the type."""
+    an output is one element of the low-rank product, times a number of the type.  All of A but its first row is `less`
+    of the usual size, and B's part of it that much larger."""
     from prefix_reused_prefill_gb300 import Adapters
     g = torch.Generator(device=DEV).manual_seed(seed)
     pos = lambda *n: torch.randn(*n, generator=g, device=DEV).abs().clamp_min(0.05)
     rank, rows = 8, sum(lens)
-    a = (pos(rank, k) * k ** -0.5).to(dtype)
+    a = pos(rank, k) * k ** -0.5
+    a[1:] *= less
+    a = a.to(dtype)
     b = torch.zeros(cols, rank, device=DEV)
     at = torch.arange(cols, device=DEV)
     b[at, at % rank] = pos(cols)
+    b[:, 1:] /= less
     b = b.to(dtype)
     x = pos(rows, k).to(dtype)
     s = torch.cat([part.double() @ a.double().t() for part in x.split(2048)])
@@ -87,3 +91,11 @@ def test_sums_of_either_sign(dtype, lens):
     s = x.double() @ a.double().t()
     want = torch.cat([s[:, j * rank:(j + 1) * rank] @ b[j * cols:(j + 1) * cols].double().t() for j in (0, 1)], 1)
     assert ((got - want).pow(2).mean() / want.pow(2).mean()).sqrt() <= 7e-7
+
+
+@pytest.mark.parametrize("lens", [[20], [300, 40]])
+@pytest.mark.parametrize("dtype,out", [(BF, BF), (BF, F32), (HF, HF), (HF, F32)])
+def test_small_elements_beside_large_ones(dtype, out, lens):
+    """Elements of the low-rank product 2^-9 of their row's largest, by B as large as that one: as exact as alone."""
+    off = relative_errors(lens, 64, 2048, dtype, out, len(lens), less=2.0 ** -9)
+    assert off.numel() > 200 and off.abs().max() <= 9 * STEP, (off.numel(), off.abs().max() / STEP)
