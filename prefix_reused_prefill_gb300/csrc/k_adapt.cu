@@ -85,15 +85,18 @@ __device__ __forceinline__ uint32_t pair_to(float lo, float hi) {
 // bf16 outputs of 254 rows were 1e-4 of their norm from those of s in 32-bit floats, and 0.5 us faster of 17.)
 constexpr int kTerms = 3;
 
-// The power of two by which a row whose largest element is `big` is held in terms of T (`down` scales it to
+// What a row whose largest element is `big` is multiplied by to be held in terms of T (`down`, a power of two: to
 // below 2, for fp16 to below 2^15, where elements far below the largest still have all their bits: their terms end
-// at 2^-24), and NaN in `down` for a row that is not finite.
+// at 2^-24), and its product with B in the end (`factor`, with the adapter's scale).  Neither leaves the normal
+// numbers, whatever the row's and the scale's sizes are.  NaN in `down` for a row that is not finite.
 template <class T>
-__device__ __forceinline__ float scale_of(float big, float& down) {
+__device__ __forceinline__ void scale_of(float big, float scale, float& down, float& factor) {
   constexpr int kTop = std::is_same<T, __half>::value ? 14 : 0;
-  const int e = min(max((int)(__float_as_uint(big) >> 23) - kTop, 15), 253) - 127;
+  const int of_big = (int)(__float_as_uint(big) >> 23) - 127 - kTop;
+  const int of_scale = (int)(__float_as_uint(fabsf(scale)) >> 23) - 127;
+  const int e = min(max(of_big, max(-112, -125 - of_scale)), min(126, 126 - of_scale));
   down = big < INFINITY ? __int_as_float((127 - e) << 23) : __int_as_float(0x7fffffff);
-  return __int_as_float((e + 127) << 23);
+  factor = scale * __int_as_float((e + 127) << 23);
 }
 
 constexpr int kNone = -1;      // a row without an adapter
@@ -317,7 +320,8 @@ __global__ void __launch_bounds__(kThreads, 2) expand_kernel(const AdaptParams p
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
     float down;
-    const float up = scale_of<T>(big, down);
+    float f;
+    scale_of<T>(big, rows.run[k].scale, down, f);
 #pragma unroll
     for (int n = 0; n < KVR_MAX_RANK / 32; ++n) {
       const int j = lane + 32 * n;
@@ -330,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 2) expand_kernel(const AdaptParams p
           x -= from(h);
         }
     }
-    if (lane == 0) factor[r] = rows.run[k].scale * up;
+    if (lane == 0) factor[r] = f;
   }
   __syncthreads();
   if (tiles) {
@@ -775,7 +779,8 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_tiles_kernel(const AdaptPa
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
     float down;
-    const float up = scale_of<T>(big, down);
+    float factor;
+    scale_of<T>(big, tile.ad.scale, down, factor);
     const int pj = whole ? j : blockIdx.z;
 #pragma unroll
     for (int k = 0; k < kTerms; ++k) {
@@ -791,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_tiles_kernel(const AdaptPa
         }
       }
     }
-    if (lane == 0) terms.factor(tile.row0 + r)[pj] = tile.ad.scale * up;
+    if (lane == 0) terms.factor(tile.row0 + r)[pj] = factor;
   }
 }
 

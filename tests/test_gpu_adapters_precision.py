@@ -24,28 +24,29 @@ def i32(v):
     return torch.tensor(v, dtype=torch.int32, device=DEV)
 
 
-def relative_errors(lens, k, cols, dtype, out, seed, less=1.0):
+def relative_errors(lens, k, cols, dtype, out, seed, less=1.0, size=(0, 0, 0, 1.0)):
     """Of the elements next to zero, (what the kernel adds - the exact product) / the product.  B has one element a row, so
     an output is one element of the low-rank product, times a number of the type.  All of A but its first row is `less`
-    of the usual size, and B's part of it that much larger."""
+    times the usual size, and B's part of it that much larger; x, A and B are 2^size[:3] of theirs, and the adapter's
+    scale is size[3]."""
     from prefix_reused_prefill_gb300 import Adapters
     g = torch.Generator(device=DEV).manual_seed(seed)
     pos = lambda *n: torch.randn(*n, generator=g, device=DEV).abs().clamp_min(0.05)
     rank, rows = 8, sum(lens)
     a = pos(rank, k) * k ** -0.5
     a[1:] *= less
-    a = a.to(dtype)
+    a = (a * 2.0 ** size[1]).to(dtype)
     b = torch.zeros(cols, rank, device=DEV)
     at = torch.arange(cols, device=DEV)
     b[at, at % rank] = pos(cols)
     b[:, 1:] /= less
-    b = b.to(dtype)
-    x = pos(rows, k).to(dtype)
+    b = (b * 2.0 ** size[2]).to(dtype)
+    x = (pos(rows, k) * 2.0 ** size[0]).to(dtype)
     s = torch.cat([part.double() @ a.double().t() for part in x.split(2048)])
-    product = s @ b.double().t()
+    product = s @ b.double().t() * float(np.float32(size[3]))
     cu = i32([0] + np.cumsum(lens).tolist())
     base = None if out is F32 else (-product).to(out)
-    got = Adapters([(a, b, 1.0)], [cols]).kvr_adapt(x, cu, i32([0] * len(lens)), base,
+    got = Adapters([(a, b, size[3])], [cols]).kvr_adapt(x, cu, i32([0] * len(lens)), base,
                                                      out=torch.empty(rows, cols, dtype=out, device=DEV))
     left = product + (0 if base is None else base.double())
     off = (got.double() - left) / product
@@ -99,3 +100,14 @@ def test_small_elements_beside_large_ones(dtype, out, lens):
     """Elements of the low-rank product 2^-9 of their row's largest, by B as large as that one: as exact as alone."""
     off = relative_errors(lens, 64, 2048, dtype, out, len(lens), less=2.0 ** -9)
     assert off.numel() > 200 and off.abs().max() <= 9 * STEP, (off.numel(), off.abs().max() / STEP)
+
+
+@pytest.mark.parametrize("lens", [[20], [300, 40]])
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("size", [(60, 62, -110, 1000.0), (63, 60, -120, 3e20), (-58, -58, 100, 3e-12), (-40, -50, 120, 1e-38),
+                                  (0, 0, 100, 2e-38), (10, 0, -110, 1.7e38)])
+def test_magnitudes_whose_product_is_ordinary(size, out, lens):
+    """Low-rank products and scales next to the ends of the 32-bit floats' range, and B that brings them back.  One step
+    more than above: the scale is no power of two."""
+    off = relative_errors(lens, 64, 2048, BF, out, len(lens), size=size)
+    assert off.numel() > 200 and off.abs().max() <= 10 * STEP, (off.numel(), off.abs().max() / STEP)
