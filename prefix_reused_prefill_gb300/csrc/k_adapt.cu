@@ -99,6 +99,20 @@ __device__ __forceinline__ void scale_of(float big, float scale, float& down, fl
   factor = scale * __int_as_float((e + 127) << 23);
 }
 
+// One output's B s, with s as it is.  (For sums that are NaN: an infinity in B times a term that is 0, or of the other
+// sign than s, makes them so, where B s is infinite.)
+template <class T>
+__device__ __forceinline__ float one_sum(const T* b, const T* const (&terms)[kTerms], int rank) {
+  float sum = 0.f;
+  for (int j = 0; j < rank; ++j) {
+    float s = 0.f;
+#pragma unroll
+    for (int m = kTerms - 1; m >= 0; --m) s += from(terms[m][j]);
+    sum = fmaf(from(b[j]), s, sum);
+  }
+  return sum;
+}
+
 constexpr int kNone = -1;      // a row without an adapter
 constexpr int kOutside = -2;   // a row of no sequence
 
@@ -369,7 +383,23 @@ __global__ void __launch_bounds__(kThreads, 2) expand_kernel(const AdaptParams p
   }
   __syncthreads();
   if (!writes) return;
-  const float4 v = id >= 0 ? *reinterpret_cast<const float4*>(&tile[r][i]) : make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 v = id >= 0 ? *reinterpret_cast<const float4*>(&tile[r][i]) : make_float4(0.f, 0.f, 0.f, 0.f);
+  if (v.x != v.x || v.y != v.y || v.z != v.z || v.w != v.w) {
+    int k = 0;
+    while (r >= rows.run[k].end) ++k;
+    const int rank = rows.run[k].rank;
+    const T* const row[kTerms] = {terms[0][r], terms[1][r], terms[2][r]};
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      const float y = c == 0 ? v.x : c == 1 ? v.y : c == 2 ? v.z : v.w;
+      if (y == y) continue;
+      const float z = one_sum(static_cast<const T*>(rows.run[k].b) + (at + c) * rank, row, rank) * factor[r];
+      if (c == 0) v.x = z;
+      else if (c == 1) v.y = z;
+      else if (c == 2) v.z = z;
+      else v.w = z;
+    }
+  }
   if constexpr (std::is_same<O, float>::value) {
     if (id >= 0) {   // (else base's own bits)
       base_f.x += v.x;
@@ -829,6 +859,38 @@ struct Eight {
   }
 };
 
+// A warp's outputs of a tile one by one, where some of its sums are not finite: those that are NaN are formed anew
+// (one_sum).  `sums` and `b`: of the warp's and the lane's first output `col` of the part.
+template <class T, class O>
+__device__ __noinline__ void outputs_one_by_one(const AdaptParams& p, const Tile& tile, const float* factor, uint32_t sums,
+                                                const T* b, int part, int left, int col, int c_end, int row0) {
+  const Terms terms(p);
+  const int rank = tile.ad.rank;
+  for (int m = 0; m < 2; ++m)
+    for (int h = 0; h < 2; ++h) {
+      float acc[4][4];
+      tc_load16x32(sums + ((uint32_t)(16 * m) << 16) + 32 * h, acc);
+      if (col + 32 * h >= c_end) continue;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const int r = row0 + 16 * m + 8 * (k >> 1 & 1), n = 32 * h + 2 * (k >> 2) + (k & 1);
+        if (r >= tile.rows) continue;
+        const long long row = tile.row0 + r, at = left + col + n;
+        float y = acc[k / 4][k % 4];
+        if (y != y) {
+          const T* s[kTerms];
+#pragma unroll
+          for (int j = 0; j < kTerms; ++j) s[j] = terms.term<T>(j, tile.row0 + r) + part * round16(p.site.max_rank);
+          y = one_sum(b + (long long)n * rank, s, rank);
+        }
+        O* out = static_cast<O*>(p.out) + p.out_stride * row + at;
+        const O* base = static_cast<const O*>(p.base) + p.base_stride * row + at;
+        if constexpr (std::is_same<O, float>::value) *out = fmaf(y, factor[r], p.base ? *base : 0.f);
+        else *out = to<O>(fmaf(y, factor[r], p.base ? from(*base) : 0.f));
+      }
+    }
+}
+
 // What a CTA keeps from run to run: its tensor memory (two tiles' sums), and their barriers' phases.
 struct Sums {
   uint32_t at, bars;   // (bars: 8 bytes a tile)
@@ -939,10 +1001,11 @@ __device__ __forceinline__ void expand_run(const AdaptParams& p, const Tile& til
     fetch(col, o[0]);
     fetch(col + 32, o[1]);
     if (i + 1 < n) multiply(b ^ 1);   // (its sums have been read: the last tile but one's)
-    const bool ok = dev::mbar_wait(sums.bars + 8 * b, (sums.phases >> b) & 1u, p.status);
+    const bool ok = __all_sync(0xffffffffu, dev::mbar_wait(sums.bars + 8 * b, (sums.phases >> b) & 1u, p.status));
     sums.phases ^= 1u << b;
     tc_after();
     if (i + 2 < n) load(col + 2 * kTileN, b);
+    float z = 0.f;   // (NaN if a sum is not finite)
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -950,12 +1013,19 @@ __device__ __forceinline__ void expand_run(const AdaptParams& p, const Tile& til
         float acc[4][4];
         tc_load16x32(sums.at + ((uint32_t)((warp & 3) * 32 + 16 * m) << 16) + b * kTileN + (warp >> 2) * 64 + 32 * h, acc);
 #pragma unroll
+        for (int k = 0; k < 16; ++k) z = fmaf(acc[k / 4][k % 4], 0.f, z);
+#pragma unroll
         for (int k = 0; k < 2; ++k) {
           const float f = ok ? factor[row0 + 16 * m + 8 * k] : __int_as_float(0x7fffffff);   // (a wait gave up)
 #pragma unroll
           for (int j = 0; j < 4; ++j) o[h][2 * m + k].add(j, acc[j][2 * k], acc[j][2 * k + 1], f);
         }
       }
+    if (ok && __any_sync(0xffffffffu, z != z)) {
+      outputs_one_by_one<T, O>(p, tile, factor, sums.at + ((uint32_t)((warp & 3) * 32) << 16) + b * kTileN + (warp >> 2) * 64,
+                               B + (long long)(col + ocol) * rank, part, left, col + ocol, c_end, row0);
+      continue;
+    }
     store(col, o[0]);
     store(col + 32, o[1]);
   }

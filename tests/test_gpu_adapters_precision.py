@@ -111,3 +111,37 @@ def test_magnitudes_whose_product_is_ordinary(size, out, lens):
     more than above: the scale is no power of two."""
     off = relative_errors(lens, 64, 2048, BF, out, len(lens), size=size)
     assert off.numel() > 200 and off.abs().max() <= 10 * STEP, (off.numel(), off.abs().max() / STEP)
+
+
+@pytest.mark.parametrize("lens", [[1, 19], [300, 40]])
+@pytest.mark.parametrize("dtype,out", [(BF, BF), (BF, F32), (HF, HF), (HF, F32)])
+def test_infinities_of_b_are_those_of_the_formula(dtype, out, lens):
+    """An infinity in B is the output's, with the sign of its low-rank element; NaN where that is 0, where two of them
+    meet with other signs, and where B is NaN.  All other outputs are as they were."""
+    from prefix_reused_prefill_gb300 import Adapters
+    g = torch.Generator(device=DEV).manual_seed(8)
+    k, rank, rows, cols = 256, 16, sum(lens), [200, 72]
+    a = (torch.randn(2 * rank, k, generator=g, device=DEV) * k ** -0.5).to(dtype)
+    b = torch.randn(sum(cols), rank, generator=g, device=DEV).to(dtype)
+    x = torch.randn(rows, k, generator=g, device=DEV).to(dtype)
+    x[1] = 0
+    base = torch.randn(rows, sum(cols), generator=g, device=DEV).to(out)
+    cu, which = i32([0] + np.cumsum(lens).tolist()), i32([0, 0])
+    clean = Adapters([(a, b, -2.0)], cols).kvr_adapt(x, cu, which, base)
+    b = b.clone()
+    inf = float("inf")
+    for n, j, v in ((0, 0, inf), (7, 3, -inf), (64, 15, inf), (131, 8, inf), (131, 9, inf), (199, 1, float("nan")), (200, 0, inf),
+                    (271, 5, -inf)):
+        b[n, j] = v
+    for same in (False, True):
+        to = base.clone() if same else None
+        got = Adapters([(a, b, -2.0)], cols).kvr_adapt(x, cu, which, base if to is None else to, out=to).double().cpu()
+        s = (x.double() @ a.double().t()).cpu()
+        bd, hit = b.double().cpu(), [0, 7, 64, 131, 199, 200, 271]
+        for n in hit:
+            part = s[:, :rank] if n < 200 else s[:, rank:]
+            want = base[:, n].double().cpu() - 2.0 * (part * bd[n]).sum(1)
+            assert torch.equal(got[:, n].isnan(), want.isnan()), n
+            assert torch.equal(got[:, n][~want.isnan()], want[~want.isnan()]), n
+        rest = [n for n in range(sum(cols)) if n not in hit]
+        assert torch.equal(got[:, rest], clean.double().cpu()[:, rest])
