@@ -669,12 +669,20 @@ const char* kvr_pages_error(const kvr_pages* pages);
  * Weights are summed as whole numbers of 2^-44 of the largest, so the sums
  * (and with them the tokens) do not depend on the launch.
  *
- * The calls have no handle: they hold nothing between calls, work only in the
+ * The calls have no handle: they hold nothing between calls (but a device's status
+ * word: kvr_batch_sync), work only in the
  * memory that they are given, and may run at the same time on several streams;
  * they can be captured.  The device of the memory has to be the current one.
  * Errors: a negative code, kvr_batch_error says why (the calling thread's last
  * failure).  A refused call launches nothing.
  */
+
+/* Waits for the stream.  KVR_ERR_TIMEOUT if a wait in a kernel of kvr_adapt on the current device has given up since
+ * the last such report (never in normal operation): outputs of long sequences formed since then, on any stream, may read
+ * NaN.  kvr_batch_selftest_wait lets such a wait run out, as kvr_selftest_wait does. */
+int kvr_batch_sync(void* stream);
+int kvr_batch_selftest_wait(void* stream);
+
 #define KVR_ACT_F32 2   /* type of logits, besides KVR_ACT_BF16 and KVR_ACT_F16 */
 
 /* Settings, device arrays with one entry per request; null for the default. */

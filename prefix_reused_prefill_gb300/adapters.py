@@ -21,6 +21,14 @@ _TYPES = {torch.bfloat16: 0, torch.float16: 1}
 _ENTRY = np.dtype([("a", np.uint64), ("b", np.uint64), ("rank", np.int32), ("scale", np.float32)])
 
 
+def kvr_batch_sync(stream=None):
+    """Wait for the stream (None: the current one); raises KvrError if a wait in a kernel of kvr_adapt on its device has
+    given up since the last such report (what was formed since then may read NaN)."""
+    lib = load_library()
+    with torch.cuda.stream(stream):
+        _check(lib, lib.kvr_batch_sync(_raw_stream(_current_device())))
+
+
 class Adapters:
     """The adapters of one projection: entries (a [n_parts * rank][k], b [sum of cols][rank], scale), of one type
     (bf16 or fp16) on one device, contiguous; ``cols``: the outputs of its parts.  The tensors are kept alive."""

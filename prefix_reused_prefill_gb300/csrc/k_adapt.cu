@@ -103,7 +103,9 @@ __device__ __forceinline__ void scale_of(float big, float scale, float& down, fl
 // sign than s, makes them so, where B s is infinite.)
 template <class T>
 __device__ __forceinline__ float one_sum(const T* b, const T* const (&terms)[kTerms], int rank) {
-  float sum = 0.f;
+  float sum = from(terms[0][0]);
+  if (sum != sum) return sum;   // (a row that is not finite: all of its terms are NaN)
+  sum = 0.f;
   for (int j = 0; j < rank; ++j) {
     float s = 0.f;
 #pragma unroll
@@ -653,7 +655,9 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_tiles_kernel(const AdaptPa
     cp_commit();
   }
   int at = 0;
+  // A wait that gives up ends the CTA's copies and products; its rows read NaN.
   bool ok = true;
+  int issued = 0;   // steps whose products the first thread has issued
   // products of step s are over
   const auto over = [&](int s) {
     ok = ok && dev::mbar_wait(dev::smem_u32(&bars[(s - s0) % kStages]), (uint32_t)((s - s0) / kStages) & 1u, p.status);
@@ -663,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_tiles_kernel(const AdaptPa
       cp_wait<kStages - 2>();
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncthreads();
-      if (threadIdx.x == 0) {
+      if (threadIdx.x == 0 && ok) {
         const uint32_t st = base + at * kStage;
         const uint64_t xd = smem_operand(st), ad = smem_operand(st + kXBytes);
         tc_after();
@@ -671,11 +675,12 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_tiles_kernel(const AdaptPa
         for (int kk = 0; kk < kStep / 16; ++kk)
           tc_mma(sums_at, xd + 2 * kk, ad + 2 * kk, product_of<T>(TR, NC), (s - s0) % kChain != 0 || kk > 0);
         tc_commit(dev::smem_u32(&bars[at]));
+        ++issued;
       }
       // the stage of the step before, once its products are over
       if (s + kStages - 1 < s1) {
         if (s > s0) over(s - 1);
-        load(s + kStages - 1, at == 0 ? kStages - 1 : at - 1);
+        if (ok) load(s + kStages - 1, at == 0 ? kStages - 1 : at - 1);
       }
       cp_commit();
       at = at + 1 == kStages ? 0 : at + 1;
@@ -739,7 +744,17 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_tiles_kernel(const AdaptPa
       for (int e = 0; e < 4; ++e) sum[n][e] += acc[n / kNT][n % kNT][e];
   }
   cp_wait<0>();
-  __syncthreads();
+  if constexpr (TC) {
+    ok = __syncthreads_and(ok);
+    if (!ok) {   // (what is still under way reads the stages and writes the sums)
+      if (issued)
+        dev::mbar_wait_until(dev::smem_u32(&bars[(issued - 1) % kStages]), (uint32_t)((issued - 1) / kStages) & 1u,
+                             dev::globaltimer_ns() + kWaitLimitNs);
+      __syncthreads();
+    }
+  } else {
+    __syncthreads();
+  }
   // the cluster's sums, a share of the rows each, a warp a row
   float* sums = reinterpret_cast<float*>(smem);
   const int g = lane >> 2, t = lane & 3;
@@ -748,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_tiles_kernel(const AdaptPa
     const int r = TC ? 16 * (warp & 3) + g : wr * 32 + n / kNT * 16 + g;
     const int q = TC ? (warp >> 2) * (NC / 2) + 8 * n : wn * (NC / 4) + n % kNT * 8;
     float* d = sums + r * kLd + q + 2 * t;
-    if (!ok) sum[n][0] = sum[n][1] = sum[n][2] = sum[n][3] = __int_as_float(0x7fffffff);   // (a wait gave up)
+    if (!ok) sum[n][0] = sum[n][1] = sum[n][2] = sum[n][3] = __int_as_float(0x7fffffff);
     *reinterpret_cast<float2*>(d) = make_float2(sum[n][0], sum[n][1]);
     *reinterpret_cast<float2*>(d + 8 * kLd) = make_float2(sum[n][2], sum[n][3]);
   }
@@ -895,6 +910,8 @@ __device__ __noinline__ void outputs_one_by_one(const AdaptParams& p, const Tile
 struct Sums {
   uint32_t at, bars;   // (bars: 8 bytes a tile)
   uint32_t phases;     // (a bit a tile)
+  uint32_t issued;     // products that have not been waited for (the first thread's, a bit a tile)
+  bool ok;             // no wait has given up: then no more copies and products, and outputs read NaN
 };
 constexpr int kOperand = ER * 128;   // bytes of 128 rows of 64 ranks
 
@@ -945,7 +962,7 @@ __device__ __forceinline__ void expand_run(const AdaptParams& p, const Tile& til
   }
   const T* B = static_cast<const T*>(tile.ad.b) + (long long)left * rank;
   const auto load = [&](int col, int buf) {
-    if (lc < chunks) {
+    if (lc < chunks && sums.ok) {
       const T* src = B + (long long)(col + lr) * rank + 8 * lc;
       const int step = lstep * rank;
       const uint32_t dst = b_smem + buf * halves * kOperand + half;
@@ -965,8 +982,8 @@ __device__ __forceinline__ void expand_run(const AdaptParams& p, const Tile& til
     cp_wait<0>();
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     tc_before();
-    __syncthreads();
-    if (threadIdx.x == 0) {
+    sums.ok = __syncthreads_and(sums.ok);
+    if (threadIdx.x == 0 && sums.ok) {
       tc_after();
       const uint64_t bd = smem_operand(b_smem + b * halves * kOperand);
 #pragma unroll 1
@@ -978,11 +995,12 @@ __device__ __forceinline__ void expand_run(const AdaptParams& p, const Tile& til
         }
       }
       tc_commit(sums.bars + 8 * b);
+      sums.issued |= 1u << b;
     }
   };
   tc_before();
-  __syncthreads();   // (the last run's factors have been read)
-  {
+  sums.ok = __syncthreads_and(sums.ok);   // (the last run's factors have been read)
+  if (sums.ok) {
     const Terms terms(p);
 #pragma unroll
     for (int k = 0; k < kTerms; ++k)
@@ -1001,8 +1019,13 @@ __device__ __forceinline__ void expand_run(const AdaptParams& p, const Tile& til
     fetch(col, o[0]);
     fetch(col + 32, o[1]);
     if (i + 1 < n) multiply(b ^ 1);   // (its sums have been read: the last tile but one's)
-    const bool ok = __all_sync(0xffffffffu, dev::mbar_wait(sums.bars + 8 * b, (sums.phases >> b) & 1u, p.status));
-    sums.phases ^= 1u << b;
+    if (sums.ok && dev::mbar_wait(sums.bars + 8 * b, (sums.phases >> b) & 1u, p.status)) {
+      sums.phases ^= 1u << b;
+      sums.issued &= ~(1u << b);
+    } else {
+      sums.ok = false;
+    }
+    const bool ok = sums.ok = __all_sync(0xffffffffu, sums.ok);
     tc_after();
     if (i + 2 < n) load(col + 2 * kTileN, b);
     float z = 0.f;   // (NaN if a sum is not finite)
@@ -1016,7 +1039,7 @@ __device__ __forceinline__ void expand_run(const AdaptParams& p, const Tile& til
         for (int k = 0; k < 16; ++k) z = fmaf(acc[k / 4][k % 4], 0.f, z);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const float f = ok ? factor[row0 + 16 * m + 8 * k] : __int_as_float(0x7fffffff);   // (a wait gave up)
+          const float f = ok ? factor[row0 + 16 * m + 8 * k] : __int_as_float(0x7fffffff);
 #pragma unroll
           for (int j = 0; j < 4; ++j) o[h][2 * m + k].add(j, acc[j][2 * k], acc[j][2 * k + 1], f);
         }
@@ -1043,7 +1066,7 @@ __global__ void __launch_bounds__(kThreads, 2) expand_tiles_kernel(const AdaptPa
   __shared__ uint32_t sums_slot;
   const uint32_t smem = (dev::smem_u32(smem_raw) + 1023u) & ~1023u;
   dev::pdl_wait();
-  Sums sums = {0, dev::smem_u32(bars), 0};
+  Sums sums = {0, dev::smem_u32(bars), 0, 0, true};
   if (threadIdx.x < 32) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dev::smem_u32(&sums_slot)),
                  "r"(2 * kTileN));
@@ -1083,7 +1106,13 @@ __global__ void __launch_bounds__(kThreads, 2) expand_tiles_kernel(const AdaptPa
     expand_run<T, O>(p, tile, factor, smem, sums, part, left, c0, c1);
   }
   tc_before();
-  __syncthreads();
+  cp_wait<0>();
+  if (!__syncthreads_and(sums.ok)) {   // (what is still under way reads the operands and writes the sums)
+    for (int b = 0; b < 2; ++b)
+      if (sums.issued >> b & 1)
+        dev::mbar_wait_until(sums.bars + 8 * b, (sums.phases >> b) & 1u, dev::globaltimer_ns() + kWaitLimitNs);
+    __syncthreads();
+  }
   if (threadIdx.x < 32) {
     tc_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(sums.at), "r"(2 * kTileN));
@@ -1204,6 +1233,10 @@ cudaError_t adapt_setup() {
   if (e == cudaSuccess) e = setup_expand<__half, float>();
   return e;
 }
+
+__device__ int g_gave_up;   // non-zero once a wait of a call without a context's status word has given up
+
+cudaError_t adapt_status(int** word) { return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_gave_up); }
 
 size_t adapt_work_bytes(const kvr_adapter_site& s, int rows) {
   // (of any number of SMs, for few or many rows a sequence)

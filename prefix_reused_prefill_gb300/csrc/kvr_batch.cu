@@ -22,18 +22,26 @@ int fail(int code, const char* fmt, ...) {
 }
 int cuda_fail(cudaError_t e, const char* what) { return fail(KVR_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e)); }
 
-// SMs of the current device, whose kernels are set up on its first call
+// SMs and status word of the current device, whose kernels are set up on its first call
 constexpr int kMaxDevices = 64;
 std::atomic<int> g_sms[kMaxDevices];
-cudaError_t device_sms(int* sms) {
+std::atomic<int*> g_status[kMaxDevices];
+cudaError_t device_of_call(int* sms, int** status) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < kMaxDevices && (*sms = g_sms[dev].load(std::memory_order_acquire)) != 0) return cudaSuccess;
+  if (dev < kMaxDevices && (*sms = g_sms[dev].load(std::memory_order_acquire)) != 0) {
+    *status = g_status[dev].load(std::memory_order_relaxed);   // (stored before)
+    return cudaSuccess;
+  }
   e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
   if (e == cudaSuccess) e = sample_setup();
   if (e == cudaSuccess) e = adapt_setup();
-  if (e == cudaSuccess && dev < kMaxDevices) g_sms[dev].store(*sms, std::memory_order_release);
+  if (e == cudaSuccess) e = adapt_status(status);
+  if (e == cudaSuccess && dev < kMaxDevices) {
+    g_status[dev].store(*status, std::memory_order_relaxed);
+    g_sms[dev].store(*sms, std::memory_order_release);
+  }
   return e;
 }
 
@@ -86,8 +94,8 @@ int logits_check(const void* logits, int type, long long stride, int rows, int v
 constexpr int kMaxAdaptRows = 1 << 22;
 
 int run_sample(const SampleParams& p, void* stream) {
-  int sms = 0;
-  cudaError_t e = device_sms(&sms);
+  int sms = 0, *status = nullptr;
+  cudaError_t e = device_of_call(&sms, &status);
   if (e == cudaSuccess) e = launch_sample(p, sms, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? KVR_OK : cuda_fail(e, "sample launch");
 }
@@ -230,9 +238,30 @@ int kvr_adapt(const kvr_adapter_site* site, const void* x, long long x_stride, c
   p.out_type = out_type;
   p.part = static_cast<float*>(work);
   int sms = 0;
-  cudaError_t e = device_sms(&sms);
+  cudaError_t e = device_of_call(&sms, &p.status);
   if (e == cudaSuccess) e = launch_adapt(p, sms, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? KVR_OK : cuda_fail(e, "adapt launch");
+}
+
+int kvr_batch_sync(void* stream) {
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int sms = 0, word = 0, *status = nullptr;
+  cudaError_t e = device_of_call(&sms, &status);
+  if (e == cudaSuccess) e = cudaMemcpyAsync(&word, status, sizeof word, cudaMemcpyDeviceToHost, st);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  if (e == cudaSuccess && word) {
+    e = cudaMemsetAsync(status, 0, sizeof word, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    if (e == cudaSuccess) return fail(KVR_ERR_TIMEOUT, "a wait in a kernel of kvr_adapt gave up");
+  }
+  return e == cudaSuccess ? KVR_OK : cuda_fail(e, "status readback");
+}
+
+int kvr_batch_selftest_wait(void* stream) {
+  int sms = 0, *status = nullptr;
+  cudaError_t e = device_of_call(&sms, &status);
+  if (e == cudaSuccess) e = launch_wait_probe(status, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KVR_OK : cuda_fail(e, "wait probe launch");
 }
 
 const char* kvr_batch_error(void) { return g_error; }

@@ -52,9 +52,10 @@ struct AdaptParams {
   int out_type;
   float* part;             // [ksplit][rows][n_parts * max_rank] parts of the low-rank products
   int ksplit;
-  int* status;             // of a context (a wait that gave up), or null
+  int* status;             // of a context, or the device's (adapt_status): a wait that gave up
 };
 cudaError_t adapt_setup();    // of the current device, before its first launch
+cudaError_t adapt_status(int** word);   // where the current device's word is
 bool adapter_site_ok(const kvr_adapter_site* s);
 size_t adapt_work_bytes(const kvr_adapter_site& s, int rows);
 cudaError_t launch_adapt(AdaptParams p, int sms, cudaStream_t st);

@@ -37,7 +37,7 @@ EXPORTED = ["kvr_arena_bytes", "kvr_scratch_bytes", "kvr_ctx_create", "kvr_ctx_i
             "kvr_page_read", "kvr_page_attend", "kvr_prefill_pages",
             "kvr_sample", "kvr_accept", "kvr_accept_work_bytes", "kvr_batch_error",
             "kvr_adapt", "kvr_adapt_work_bytes", "kvr_adapters_work_bytes", "kvr_prefill_batch_adapted",
-            "kvr_verify_sample_batch"]
+            "kvr_verify_sample_batch", "kvr_batch_sync", "kvr_batch_selftest_wait"]
 
 
 class KvrError(RuntimeError):
@@ -160,6 +160,8 @@ def load_library(path: str = LIB_PATH):
         "kvr_verify_sample_batch": (I, [V, I, P(I), P(I), i32p, V, P(KvrLayerWeights), P(KvrAdapters), P(I),
                                         P(KvrHeadWeights), P(KvrSampling), V, LL, V, V, V, V, i32p, P(I), V]),
         "kvr_batch_error": (ctypes.c_char_p, []),
+        "kvr_batch_sync": (I, [V]),
+        "kvr_batch_selftest_wait": (I, [V]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)

@@ -109,3 +109,23 @@ def test_adapters_given_up_while_another_stream_reads_them():
             torch.full((n,), float("nan"), dtype=BF, device=DEV)
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+def test_a_wait_that_gave_up_is_reported_once():
+    from prefix_reused_prefill_gb300 import Adapters, KvrError, kvr_batch_sync, load_library
+    g = torch.Generator().manual_seed(11)
+    site = Adapters([((torch.randn(16, 512, generator=g) / 16).to(BF).cuda(), torch.randn(256, 16, generator=g).to(BF).cuda(), 1.0)],
+                    [256])
+    x = torch.randn(300, 512, generator=g).to(BF).cuda()
+    cu, which = torch.tensor([0, 300], dtype=torch.int32, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    want = site.kvr_adapt(x, cu, which)
+    kvr_batch_sync()
+    side = torch.cuda.Stream()
+    assert load_library().kvr_batch_selftest_wait(side.cuda_stream) == 0   # (one second)
+    with pytest.raises(KvrError) as e:
+        kvr_batch_sync(side)
+    assert e.value.code == -4 and "gave up" in str(e.value)
+    kvr_batch_sync(side)
+    kvr_batch_sync()
+    assert torch.equal(site.kvr_adapt(x, cu, which), want)
+    kvr_batch_sync()
