@@ -258,13 +258,11 @@ __device__ __forceinline__ void weights_of_two(const float2* tab, u64 yh, u64 yl
   const u64 r = add2(sub2(a, sub2(s, px)), rest);
   float s0, s1, r0, r1;
   split(mul2(s, two(0x1p30f)), s0, s1);
-  split(mul2(r, two(0x1p44f)), r0, r1);
+  split(mul2(r, two(0x1p45f)), r0, r1);
   const auto whole = [](float s, float r, uint32_t j) {
-    // (half a unit, 2^(n - 1), joins r: what that leaves of a weight below 2^-32 is a quarter of a unit
-    // in the last 2^-14 of a row)
-    const float half = __uint_as_float(((j << 13) & 0x1f800000u) + (126u << 23));
-    const long long v = (long long)__float2int_rn(s) * (1ll << (kFix - 30)) + __float2int_rn(r + half);
-    return (u64)v >> ((j >> 10) & 63);
+    // (in half units, and to the nearest unit: weights of a few units may be all that a rejected draft leaves)
+    const long long v = (long long)__float2int_rn(s) * (1ll << (kFix - 29)) + __float2int_rn(r);
+    return (((u64)v >> ((j >> 10) & 63)) + 1) >> 1;
   };
   v0 = whole(s0, r0, j0);
   v1 = whole(s1, r1, j1);
