@@ -809,7 +809,8 @@ size_t kvr_adapters_work_bytes(const kvr_config* cfg, const kvr_adapter_site* si
 /* kvr_prefill_batch with adapter which[j] (host [n_seq]; others than the sites'
  * own: none) for conversation j.  What an adapter adds is formed from the
  * projection's bf16 input in 32 bits and joins its output before that is rounded,
- * rotated or multiplied.  Full layers only (KVR_ERR_UNSUPPORTED otherwise). */
+ * rotated or multiplied.  Full layers only (KVR_ERR_UNSUPPORTED otherwise).  The work area shares no memory with hidden
+ * or out. */
 int kvr_prefill_batch_adapted(kvr_ctx* ctx, int n_seq, const int* slots, const int* lens, const int32_t* tokens,
                               const void* hidden, const kvr_layer_weights* weights, const kvr_adapters* adapters,
                               const int* which, void* out, void* stream);
@@ -823,6 +824,7 @@ int kvr_prefill_batch_adapted(kvr_ctx* ctx, int n_seq, const int* slots, const i
  *   next_tokens  host [n_seq]: the token after the drafts that stay (-1 without a distribution).
  *   accepted     host [n_seq].  Slot slots[j] is cut back to its length before the call + 1 +
  *                accepted[j].
+ * logits, draft_probs, out, hidden and the adapters' work area share no memory (but out with hidden).
  * Synchronises the stream.  On an error after the rows ran every slot keeps its
  * length before the call. */
 int kvr_verify_sample_batch(kvr_ctx* ctx, int n_seq, const int* slots, const int* lens, const int32_t* tokens,

@@ -1456,6 +1456,12 @@ bool adapters_fit(const kvr_config& k, const kvr_adapter_site* sites, int* bad) 
   return true;
 }
 
+// whether two runs of bytes meet (null: nowhere)
+bool meet(const void* a, size_t an, const void* b, size_t bn) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return a && b && x < y + bn && y < x + an;
+}
+
 static_assert(sizeof(Requests) % 4 == 0 && sizeof(Requests) <= 4000, "they travel as a kernel's argument");
 __global__ void put_requests(const Requests in, Requests* to) {
   dev::pdl_trigger();
@@ -1506,9 +1512,12 @@ int batch_common(kvr_ctx* c, int n_seq, const int* slots, const int* lens, const
       return fail(c, KVR_ERR_ARG, "layer %d, site %d does not fit the projection or is not bf16", bad / KVR_SITES,
                   bad % KVR_SITES);
     const size_t add = adapted_add_bytes(c->cfg, total);
-    if (adapters->work_bytes < add + adapted_part_bytes(c->cfg, adapters->sites, total))
-      return fail(c, KVR_ERR_CAPACITY, "the adapters' work area is smaller than %zu bytes",
-                  add + adapted_part_bytes(c->cfg, adapters->sites, total));
+    const size_t need = add + adapted_part_bytes(c->cfg, adapters->sites, total);
+    if (adapters->work_bytes < need)
+      return fail(c, KVR_ERR_CAPACITY, "the adapters' work area is smaller than %zu bytes", need);
+    const size_t io = (size_t)total * c->cfg.hidden * 2;
+    if (meet(adapters->work, need, hidden, io) || meet(adapters->work, need, out, io))
+      return fail(c, KVR_ERR_ARG, "the adapters' work area shares memory with hidden or out");
     ad.sites = adapters->sites;
     ad.cu = c->requests->cu;
     ad.which = c->requests->which;
@@ -1999,6 +2008,13 @@ int kvr_verify_sample_batch(kvr_ctx* c, int n_seq, const int* slots, const int* 
   if (total > kVerifyMaxRows) return fail(c, KVR_ERR_ARG, "%d rows exceed %d for this call", total, kVerifyMaxRows);
   if (draft_probs && total > 1 && draft_stride < head->vocab)
     return fail(c, KVR_ERR_ARG, "the drafts' row stride must cover a row");
+  const size_t row = (size_t)head->vocab * 4, io = (size_t)total * c->cfg.hidden * 2;
+  const size_t drafts = (size_t)(total - 1) * (total > 1 ? draft_stride : 0) * 4 + row;
+  const void* work = adapters ? adapters->work : nullptr;
+  const size_t work_bytes = adapters ? adapters->work_bytes : 0;
+  if (meet(logits, total * row, draft_probs, drafts) || meet(logits, total * row, hidden, io) || meet(logits, total * row, out, io) ||
+      meet(logits, total * row, work, work_bytes) || meet(draft_probs, drafts, out, io) || meet(draft_probs, drafts, work, work_bytes))
+    return fail(c, KVR_ERR_ARG, "logits, out or the adapters' work area shares memory with another argument");
   Requests req;
   memset(&req, 0, sizeof req);
   for (int i = 0; i < total; ++i) {

@@ -129,3 +129,52 @@ def test_a_wait_that_gave_up_is_reported_once():
     kvr_batch_sync()
     assert torch.equal(site.kvr_adapt(x, cu, which), want)
     kvr_batch_sync()
+
+
+def test_stack_calls_refuse_what_shares_memory():
+    """The logits' buffer in the place of another argument, and the adapters' work area in that of the rows."""
+    import ctypes
+
+    import workloads
+    from prefix_reused_prefill_gb300 import Adapters, Kvr, KvrError, config_for_shape
+    from prefix_reused_prefill_gb300.kvr import KvrAdapters, _i32
+    shape, vocab = workloads.SHAPES["small"], 512
+    lws = workloads.stack_weights(shape, 21)
+    kv = Kvr(config_for_shape(shape, 4, 256, 64, vocab=vocab), device="cuda")
+    w = kv.weights(workloads.weights_to(lws, "cuda"))
+    hw = workloads.head_weights(shape, 31, "cpu", vocab=vocab)
+    head = {"norm": hw["norm"].cuda(), "lm": workloads.Int4Matrix(hw["lm"].packed.cuda(), hw["lm"].scales.cuda(), None)}
+    rows, toks = 6, [[1, 2, 3], [4, 5, 6]]
+    x = workloads.hidden_for_tokens(sum(toks, []), shape.hidden, 5).cuda()
+    buf = torch.zeros(2 * rows, vocab, device=DEV)
+    u, un = [0.5] * rows, [0.5] * 2
+    step = lambda hid, **k: kv.kvr_verify_sample_batch([0, 1], toks, hid, w, head, u, un, **k)
+    # hidden and out in the logits' memory
+    words = buf.view(-1).view(BF)
+    inside = words[64:64 + rows * shape.hidden].view(rows, shape.hidden)
+    assert 64 + rows * shape.hidden <= words.numel()
+    for hid, k in ((x, dict(logits=buf[:rows], draft_probs=buf[:rows])), (x, dict(logits=buf[:rows], draft_probs=buf[rows - 1:-1])),
+                   (x, dict(logits=buf[:rows], draft_probs=buf[1:1 + rows])), (inside, dict(logits=buf[:rows])),
+                   (x, dict(logits=buf[:rows], out=inside)), (x, dict(draft_probs=buf[:rows], out=inside))):
+        with pytest.raises(KvrError) as e:
+            step(hid, **k)
+        assert e.value.code == -1
+    assert [kv.kvr_slot_len(s) for s in range(2)] == [0, 0]
+    nxt, _ = step(x, logits=buf[:rows], draft_probs=buf[rows:])   # side by side
+    assert min(nxt) >= 0
+    # the work area over hidden, and over out
+    g = torch.Generator().manual_seed(3)
+    site = Adapters([((torch.randn(8, shape.hidden, generator=g) / 30).to(BF).cuda(),
+                      torch.randn(shape.hidden, 8, generator=g).to(BF).cuda(), 1.0)], [shape.hidden])
+    sites, _keep = kv.adapters([{"o": site} if shape.n_q_heads * shape.head_dim == shape.hidden else {}] * shape.n_layers)
+    wb = kv.lib.kvr_adapters_work_bytes(ctypes.byref(kv.cfg), sites, 3)
+    one = torch.zeros(wb + (1 << 16), dtype=torch.uint8, device=DEV)
+    mine = one[:3 * shape.hidden * 2].view(BF).view(3, shape.hidden)
+    mine.copy_(x[:3])
+    out = torch.empty_like(mine)
+    call = lambda hid, to: kv.lib.kvr_prefill_batch_adapted(
+        kv.ctx, 1, (ctypes.c_int * 1)(3), (ctypes.c_int * 1)(3), _i32([1, 2, 3]), hid.data_ptr(), w[0],
+        ctypes.byref(KvrAdapters(sites, one.data_ptr(), wb)), (ctypes.c_int * 1)(0), to.data_ptr(), None)
+    assert call(mine, out) == -1 and call(x[:3], mine) == -1 and kv.kvr_slot_len(3) == 0
+    assert call(x[:3], out) == 0 and kv.kvr_slot_len(3) == 3
+    kv.kvr_sync_status()
