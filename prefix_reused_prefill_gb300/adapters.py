@@ -14,7 +14,7 @@ import numpy as np
 import torch
 
 from .kvr import KvrAdapterSite, KvrError, load_library
-from .sampling import _check, _current_device, _raw_stream, _work_alloc, _work_free
+from .sampling import _check, _check_stream, _current_device, _raw_stream, _work_alloc, _work_free
 
 MAX_RANK = 128
 _TYPES = {torch.bfloat16: 0, torch.float16: 1}
@@ -92,6 +92,7 @@ class Adapters:
         [n_seq] are device int32; base and out are [rows][sum of cols] of x's type or float32, and may be one."""
         index = self._index
         if stream is not None or _current_device() != index:   # (memory that the stream may write at once)
+            _check_stream(stream, index)
             with torch.cuda.device(index), torch.cuda.stream(stream):
                 return self.kvr_adapt(x, cu_rows, which, base, out)
         rows, n_seq = x.shape[0] if x.dim() == 2 else -1, which.numel()

@@ -29,6 +29,11 @@ def _check(lib, rc: int):
         raise KvrError(rc, lib.kvr_batch_error().decode())
 
 
+def _check_stream(stream, index: int):
+    if stream is not None and stream.device.index != index:
+        raise KvrError(-1, f"the stream is of {stream.device}, the tensors are on device {index}")
+
+
 def _refuse(what: str, x, shape, dtypes, index: int):
     raise KvrError(-1, f"{what} must be {shape} of {dtypes} on device {index}, a row's elements contiguous; it is "
                        f"{tuple(x.shape)} of {x.dtype} on {x.device}" if isinstance(x, torch.Tensor) else f"{what}: {x}")
@@ -82,6 +87,7 @@ def kvr_sample(logits: torch.Tensor, u: torch.Tensor, temperature: Setting = Non
     [rows].  A row without a distribution has token -1."""
     index, kind, ls = _logits(logits)
     if stream is not None or _current_device() != index:   # (memory that the stream may write at once)
+        _check_stream(stream, index)
         with torch.cuda.device(index), torch.cuda.stream(stream):
             return kvr_sample(logits, u, temperature, top_k, min_p, top_p, dist)
     lib = load_library()
@@ -114,6 +120,7 @@ def kvr_accept(logits: torch.Tensor, tokens: torch.Tensor, cu_rows: torch.Tensor
     distribution of the draft after each row (None: the drafts were certain).  Settings: [n_seq]."""
     index, kind, ls = _logits(logits)
     if stream is not None or _current_device() != index:
+        _check_stream(stream, index)
         with torch.cuda.device(index), torch.cuda.stream(stream):
             return kvr_accept(logits, tokens, cu_rows, u, u_next, draft_probs, temperature, top_k, min_p, top_p)
     lib = load_library()

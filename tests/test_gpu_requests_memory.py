@@ -178,3 +178,18 @@ def test_stack_calls_refuse_what_shares_memory():
     assert call(mine, out) == -1 and call(x[:3], mine) == -1 and kv.kvr_slot_len(3) == 0
     assert call(x[:3], out) == 0 and kv.kvr_slot_len(3) == 3
     kv.kvr_sync_status()
+
+
+def test_a_stream_of_another_device_is_refused():
+    import types
+
+    from prefix_reused_prefill_gb300 import Adapters, KvrError, kvr_accept, kvr_sample
+    other = types.SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=0)   # (this machine may have no such device)
+    x, u = torch.randn(4, 64, device=DEV), torch.rand(4, device=DEV)
+    i = torch.tensor([0, 4], dtype=torch.int32, device=DEV)
+    site = Adapters([(torch.zeros(8, 64, dtype=BF, device=DEV), torch.zeros(64, 8, dtype=BF, device=DEV), 1.0)], [64])
+    for call in (lambda: kvr_sample(x, u, stream=other),
+                 lambda: kvr_accept(x, torch.zeros(4, dtype=torch.int32, device=DEV), i, u, u[:1], stream=other),
+                 lambda: site.kvr_adapt(x.to(BF), i, i[:1], stream=other)):
+        with pytest.raises(KvrError):
+            call()
