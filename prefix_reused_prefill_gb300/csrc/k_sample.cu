@@ -54,8 +54,9 @@ constexpr float kNothing = 46.f;     // binary orders from the maximum on which 
 constexpr int kFine = 5, kCoarse = 6;
 constexpr int kCap = 2048;           // tokens that one CTA puts in order
 constexpr int kCount = 128;          // as many by counting the larger ones
+constexpr int kPart = 64;            // tokens of one part of a list from which on the list is sorted instead
 constexpr int kDigit = 10;           // bits of a place taken at a time where a bin holds more
-static_assert(kBins == 2 * kThreads && kBins == 1 << kDigit && kCount <= kThreads, "bins and digits two a thread");
+static_assert(kBins == 2 * kThreads && kBins == 1 << kDigit && kCount <= kThreads && (kCap & (kCap - 1)) == 0, "bins and digits two a thread");
 constexpr int kPlaceBits = 32 + kSampleIndexBits;
 constexpr uint32_t kIndexMask = (1u << kSampleIndexBits) - 1;
 
@@ -429,6 +430,22 @@ struct Scan {
     return i;
   }
 };
+
+// n numbers (a power of two of them) into descending order, by compare and exchange (2048: in 66 steps).
+__device__ __forceinline__ void sort_list(u64* list, int n) {
+  for (int k = 2; k <= n; k <<= 1)
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      for (int t = threadIdx.x; t < n / 2; t += kThreads) {
+        const int i = 2 * t - (t & (j - 1));
+        const u64 a = list[i], b = list[i + j];
+        if ((a < b) == ((i & k) == 0)) {
+          list[i] = b;
+          list[i + j] = a;
+        }
+      }
+      __syncthreads();
+    }
+}
 
 template <class T>
 struct Sampler {
@@ -826,32 +843,40 @@ struct Sampler {
       for (int i = threadIdx.x; i < n; i += kThreads) atomicAdd(&fill[part(sm.place[i])], 1u);
       __syncthreads();
       const uint32_t a = fill[2 * threadIdx.x], b = fill[2 * threadIdx.x + 1];
-      uint32_t run = a + b;
+      if (__syncthreads_or(max(a, b) > kPart)) {
+        // (many equal logits beside others: a call with 2000 of them behind one larger took 120 us, sorted 34)
+        const int size = 1 << (32 - __clz(n - 1));
+        for (int i = n + threadIdx.x; i < size; i += kThreads) sm.place[i] = 0;
+        __syncthreads();
+        sort_list(sm.place, size);
+      } else {
+        uint32_t run = a + b;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t v = __shfl_up_sync(0xffffffffu, run, o);
-        if (lane >= o) run += v;
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t v = __shfl_up_sync(0xffffffffu, run, o);
+          if (lane >= o) run += v;
+        }
+        if (lane == 31) sm.warp_i[warp] = run;
+        __syncthreads();
+        run -= a + b;
+        for (int k = 0; k < warp; ++k) run += sm.warp_i[k];
+        start[2 * threadIdx.x] = fill[2 * threadIdx.x] = run;
+        start[2 * threadIdx.x + 1] = fill[2 * threadIdx.x + 1] = run + a;
+        __syncthreads();
+        for (int i = threadIdx.x; i < n; i += kThreads) {
+          const u64 p = sm.place[i];
+          sm.mine[atomicAdd(&fill[part(p)], 1u)] = p;
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < n; i += kThreads) {
+          const u64 p = sm.mine[i];
+          const int b0 = start[part(p)], b1 = fill[part(p)];
+          int above = b0;
+          for (int j = b0; j < b1; ++j) above += sm.mine[j] > p;
+          sm.place[above] = p;
+        }
+        __syncthreads();
       }
-      if (lane == 31) sm.warp_i[warp] = run;
-      __syncthreads();
-      run -= a + b;
-      for (int k = 0; k < warp; ++k) run += sm.warp_i[k];
-      start[2 * threadIdx.x] = fill[2 * threadIdx.x] = run;
-      start[2 * threadIdx.x + 1] = fill[2 * threadIdx.x + 1] = run + a;
-      __syncthreads();
-      for (int i = threadIdx.x; i < n; i += kThreads) {
-        const u64 p = sm.place[i];
-        sm.mine[atomicAdd(&fill[part(p)], 1u)] = p;
-      }
-      __syncthreads();
-      for (int i = threadIdx.x; i < n; i += kThreads) {
-        const u64 p = sm.mine[i];
-        const int b0 = start[part(p)], b1 = fill[part(p)];
-        int above = b0;
-        for (int j = b0; j < b1; ++j) above += sm.mine[j] > p;
-        sm.place[above] = p;
-      }
-      __syncthreads();
     }
     for (int i = threadIdx.x; i < n; i += kThreads) {
       float yh, yl;
