@@ -13,8 +13,8 @@
 // straight from global memory, 16 or 8 bytes each: which inputs share a fragment
 // does not matter as long as both operands agree.  Bound: the chain of loads (whose rows, which
 // adapter, where it is, its values), twice; where each row has its own adapter, the loads of A
-// and B.  q, k and v of 3584 inputs, one row of rank 16: 8.0 us; of 4096 inputs, 64 rows with an
-// adapter each: 18.1 us (40 MB).  Eight sequences of 8 rows, 18944 inputs, 32-bit outputs: 11.2 us.
+// and B.  q, k and v of 3584 inputs, one row of rank 16: 8.4 us; of 4096 inputs, 64 rows with an
+// adapter each: 19.5 us (40 MB).  Eight sequences of 8 rows, 18944 inputs, 32-bit outputs: 12 us.
 //
 // Many: tiles of one sequence's rows, below.
 #include <cooperative_groups.h>
@@ -82,7 +82,7 @@ __device__ __forceinline__ uint32_t pair_to(float lo, float hi) {
 }
 
 // Terms of s: each leaves half a step of what the one before it left, 2^-8 for bf16, 2^-11 for fp16.  (With two,
-// bf16 outputs of 254 rows were 1e-4 of their norm from those of s in 32-bit floats.)
+// bf16 outputs of 254 rows were 1e-4 of their norm from those of s in 32-bit floats, and 0.5 us faster of 17.)
 constexpr int kTerms = 3;
 
 // What a row whose largest element is `big` is multiplied by to be held in terms of T (`down`, a power of two: to
@@ -426,16 +426,16 @@ __global__ void __launch_bounds__(kThreads, 2) expand_kernel(const AdaptParams p
 // ---------------------------------------------------------------- many rows a sequence
 // Tiles of one sequence's rows.  shrink_tiles_kernel streams 64 rows of x and A through
 // shared memory (a cluster cuts the inputs, its CTAs' sums are joined in distributed
-// shared memory) and leaves s in terms of T, by mma.sync; expand_tiles_kernel multiplies 128 rows of
-// them with 128 outputs' B while base is on its way, on tcgen05 with sums in tensor memory.
+// shared memory) and leaves s in terms of T; expand_tiles_kernel multiplies 128 rows of
+// them with 128 outputs' B while base is on its way.  Both on tcgen05, sums in tensor memory.
 // Addresses are the adapters', known on the device only, so copies are cp.async, not tensor maps'.
-// Bound: shrink by what it moves from L2 to the SMs (each 64 inputs of 64 rows bring up to 128 rows
+// Bound: shrink by what it moves from L2 to the SMs (each 64 inputs of 64 rows bring up to 192 rows
 // of A; 64 rows of x instead of 128, since two CTAs an SM cover each other's start and end),
 // expand by base and out.  Four ragged prompts, 6.7k rows of 4096 inputs, rank 64, 6144 outputs:
-// 86 us, of which a plain copy of x, base and out would take 33; with 32-bit base and out 117 of 57.
+// 85 us (105 with mma.sync), of which a plain copy of x, base and out would take 33.
 constexpr int TR = 64;
 constexpr int kStep = 64;       // inputs of a stage: 128 bytes a row
-constexpr int kStages = 3;      // (four prompts: 2 97 us, 3 and 4 86)
+constexpr int kStages = 3;      // (4 and 6 leave one CTA an SM: four prompts 107 us, with 3 100)
 constexpr int kMaxCluster = 8;
 constexpr int ER = 128, kTileN = 128;   // rows and outputs of a tile of expand
 
@@ -526,7 +526,7 @@ struct Terms {
 };
 
 // The tensor memory's products: operands in shared memory, rows of 128 bytes in the 128-byte swizzle,
-// eight of them 1024 bytes apart; sums of row i in lane i.
+// eight of them 1024 bytes apart; sums of row i of 128 in lane i.
 __device__ __forceinline__ uint64_t smem_operand(uint32_t at) {
   return (uint64_t)((at >> 4) & 0x3FFFu) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
 }
@@ -546,7 +546,8 @@ __device__ __forceinline__ void tc_mma(uint32_t sums, uint64_t a, uint64_t b, ui
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
-// 32 columns of 16 lanes, as mma.sync's sums of four products lie in a warp
+// 32 columns of 16 lanes, as mma.sync's sums of four products lie in a warp.  (Products of 64 rows have sixteen of them
+// in each 32 lanes.)
 __device__ __forceinline__ void tc_load16x32(uint32_t at, float (&v)[4][4]) {
   uint32_t r[16];
   asm volatile(
@@ -564,21 +565,23 @@ __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::befor
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
 // One chunk of NC stacked rows of A (all parts, or one) of one tile and one part of the inputs.
-// X16: x is fp16 that holds bf16 values.
+// X16: x is fp16 that holds bf16 values.  TC: on tcgen05.
 // Matrix units cut a sum's last bits at every product of 16 inputs instead of rounding them; over 4096 inputs in one
-// chain that is 2e-6 of the sum.  So chains are kChain stages, added up in registers: below 3e-7.  (On tcgen05, whose sums
-// have to be fetched at every chain's end, four prompts took 91 us, with mma.sync 86; 254 rows 18.4 and 16.9.)
+// chain that is 2e-6 of the sum.  So chains are kChain stages, added up in registers: below 3e-7.
 constexpr int kChain = 2;
-template <class T, int NC, bool X16>
+template <class T, int NC, bool TC, bool X16>
 __global__ void __launch_bounds__(kThreads, 2) shrink_tiles_kernel(const AdaptParams p, int ks) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
   __shared__ Tile tile;
+  __shared__ __align__(8) uint64_t bars[kStages];   // of a stage's products
+  __shared__ uint32_t sums_slot;
+  constexpr int kSumCols = NC <= 64 ? 64 : NC <= 128 ? 128 : 256;
   constexpr int kXBytes = TR * 128, kStage = kXBytes + NC * 128;
   constexpr int kNT = NC / 32;    // tiles of 8 ranks a warp
   constexpr int kLd = NC + 4;
   static_assert(TR * kLd * 4 <= kStages * kStage, "the sums fit where the stages were");
   uint8_t* smem = smem_raw + ((1024u - (dev::smem_u32(smem_raw) & 1023u)) & 1023u);
-  dev::pdl_trigger();
+  if (!TC) dev::pdl_trigger();
   dev::pdl_wait();
   const int part_k = blockIdx.x % ks;
   find_tile<TR>(p, blockIdx.x / ks, tile);
@@ -588,6 +591,24 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_tiles_kernel(const AdaptPa
   const int q0 = whole ? 0 : blockIdx.z * rank, nq = whole ? p.site.n_parts * rank : rank;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int wr = warp & 1, wn = warp >> 1;
+  uint32_t sums_at = 0;
+  if (TC) {
+    if (warp == 0) {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dev::smem_u32(&sums_slot)),
+                   "r"(kSumCols));
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    } else if (threadIdx.x == 32) {
+#pragma unroll
+      for (int i = 0; i < kStages; ++i) dev::mbar_init(dev::smem_u32(&bars[i]), 1);
+      dev::fence_mbar_init();
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    sums_at = sums_slot;
+    // (only now: a kernel behind that takes tensor memory and waits for this one must not take it first)
+    dev::pdl_trigger();
+  }
   const int K = p.site.k, steps = (K + kStep - 1) / kStep;
   const int s0 = (int)((long long)steps * part_k / ks), s1 = (int)((long long)steps * (part_k + 1) / ks);
   const uint32_t base = dev::smem_u32(smem);
@@ -621,65 +642,134 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_tiles_kernel(const AdaptPa
     a_at[kk] = base + dev::swz128(wr * 32 + (lane & 15), 2 * kk + (lane >> 4));
     b_at[kk] = base + kXBytes + dev::swz128(wn * (NC / 4) + (lane & 7) + ((lane >> 4) << 3), 2 * kk + ((lane >> 3) & 1));
   }
-  constexpr int kSums = 2 * kNT;
-  float acc[kSums][4], sum[kSums][4];   // of a chain, and of all before it
+  // the chains' sums: TC: rows 16 (warp % 4) + g and + 8, outputs (warp / 4) NC / 2 + 8 n + 2 t and + 1
+  constexpr int kSums = TC ? NC / 16 : 2 * kNT;
+  float sum[kSums][4];
 #pragma unroll
   for (int n = 0; n < kSums; ++n)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[n][e] = sum[n][e] = 0.f;
+    for (int e = 0; e < 4; ++e) sum[n][e] = 0.f;
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) {
     if (s0 + i < s1) load(s0 + i, i);
     cp_commit();
   }
   int at = 0;
-  for (int s = s0; s < s1; ++s) {
-    cp_wait<kStages - 2>();
-    __syncthreads();
-    if (s + kStages - 1 < s1) load(s + kStages - 1, at == 0 ? kStages - 1 : at - 1);
-    cp_commit();
-    const uint32_t st = at * kStage;
-    at = at + 1 == kStages ? 0 : at + 1;
-    if ((s - s0) % kChain == 0)
+  // A wait that gives up ends the CTA's copies and products; its rows read NaN.
+  bool ok = true;
+  int issued = 0;   // steps whose products the first thread has issued
+  // products of step s are over
+  const auto over = [&](int s) {
+    ok = ok && dev::mbar_wait(dev::smem_u32(&bars[(s - s0) % kStages]), (uint32_t)((s - s0) / kStages) & 1u, p.status);
+  };
+  if constexpr (TC) {
+    for (int s = s0; s < s1; ++s) {
+      cp_wait<kStages - 2>();
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncthreads();
+      if (threadIdx.x == 0 && ok) {
+        const uint32_t st = base + at * kStage;
+        const uint64_t xd = smem_operand(st), ad = smem_operand(st + kXBytes);
+        tc_after();
 #pragma unroll
-      for (int n = 0; n < kSums; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          sum[n][e] += acc[n][e];
-          acc[n][e] = 0.f;
-        }
-#pragma unroll
-    for (int kk = 0; kk < kStep / 16; ++kk) {
-      uint32_t a[2][4];
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        dev::ldmatrix_x4(a_at[kk] + st + m * 16 * 128, a[m][0], a[m][1], a[m][2], a[m][3]);
-        if (X16)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) a[m][e] = bf16_of_half2(a[m][e]);
+        for (int kk = 0; kk < kStep / 16; ++kk)
+          tc_mma(sums_at, xd + 2 * kk, ad + 2 * kk, product_of<T>(TR, NC), (s - s0) % kChain != 0 || kk > 0);
+        tc_commit(dev::smem_u32(&bars[at]));
+        ++issued;
       }
+      // the stage of the step before, once its products are over
+      if (s + kStages - 1 < s1) {
+        if (s > s0) over(s - 1);
+        if (ok) load(s + kStages - 1, at == 0 ? kStages - 1 : at - 1);
+      }
+      cp_commit();
+      at = at + 1 == kStages ? 0 : at + 1;
+      if ((s - s0) % kChain == kChain - 1 || s + 1 == s1) {   // (the next chain's products wait for every warp's loads)
+        over(s);
+        tc_after();
 #pragma unroll
-      for (int n = 0; n < kNT; n += 2) {
-        uint32_t b[4];   // ranks 8 n .. + 15: (first eight, low and high inputs), (second eight, ...)
-        dev::ldmatrix_x4(b_at[kk] + st + n * 8 * 128, b[0], b[1], b[2], b[3]);
+        for (int c = 0; c < kSums; c += 4) {
+          float v[4][4];
+          tc_load16x32(sums_at + ((uint32_t)(32 * (warp & 3)) << 16) + (warp >> 2) * (NC / 2) + 8 * c, v);
+#pragma unroll
+          for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[c + n][e] += v[n][e];
+        }
+        tc_before();
+      }
+    }
+  } else {
+    float acc[2][kNT][4];
+    for (int s = s0; s < s1; ++s) {
+      cp_wait<kStages - 2>();
+      __syncthreads();
+      if (s + kStages - 1 < s1) load(s + kStages - 1, at == 0 ? kStages - 1 : at - 1);
+      cp_commit();
+      const uint32_t st = at * kStage;
+      at = at + 1 == kStages ? 0 : at + 1;
+      if ((s - s0) % kChain == 0)
+#pragma unroll
+        for (int n = 0; n < kSums; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (s > s0) sum[n][e] += acc[n / kNT][n % kNT][e];
+            acc[n / kNT][n % kNT][e] = 0.f;
+          }
+#pragma unroll
+      for (int kk = 0; kk < kStep / 16; ++kk) {
+        uint32_t a[2][4];
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
-          mma<T>(acc[m * kNT + n], a[m][0], a[m][1], a[m][2], a[m][3], b[0], b[1]);
-          mma<T>(acc[m * kNT + n + 1], a[m][0], a[m][1], a[m][2], a[m][3], b[2], b[3]);
+          dev::ldmatrix_x4(a_at[kk] + st + m * 16 * 128, a[m][0], a[m][1], a[m][2], a[m][3]);
+          if (X16)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) a[m][e] = bf16_of_half2(a[m][e]);
+        }
+#pragma unroll
+        for (int n = 0; n < kNT; n += 2) {
+          uint32_t b[4];   // ranks 8 n .. + 15: (first eight, low and high inputs), (second eight, ...)
+          dev::ldmatrix_x4(b_at[kk] + st + n * 8 * 128, b[0], b[1], b[2], b[3]);
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            mma<T>(acc[m][n], a[m][0], a[m][1], a[m][2], a[m][3], b[0], b[1]);
+            mma<T>(acc[m][n + 1], a[m][0], a[m][1], a[m][2], a[m][3], b[2], b[3]);
+          }
         }
       }
     }
+#pragma unroll
+    for (int n = 0; n < kSums; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[n][e] += acc[n / kNT][n % kNT][e];
   }
   cp_wait<0>();
-  __syncthreads();
+  if constexpr (TC) {
+    ok = __syncthreads_and(ok);
+    if (!ok) {   // (what is still under way reads the stages and writes the sums)
+      if (issued)
+        dev::mbar_wait_until(dev::smem_u32(&bars[(issued - 1) % kStages]), (uint32_t)((issued - 1) / kStages) & 1u,
+                             dev::globaltimer_ns() + kWaitLimitNs);
+      __syncthreads();
+    }
+  } else {
+    __syncthreads();
+  }
   // the cluster's sums, a share of the rows each, a warp a row
   float* sums = reinterpret_cast<float*>(smem);
   const int g = lane >> 2, t = lane & 3;
 #pragma unroll
   for (int n = 0; n < kSums; ++n) {
-    float* d = sums + (wr * 32 + n / kNT * 16 + g) * kLd + wn * (NC / 4) + n % kNT * 8 + 2 * t;
-    *reinterpret_cast<float2*>(d) = make_float2(sum[n][0] + acc[n][0], sum[n][1] + acc[n][1]);
-    *reinterpret_cast<float2*>(d + 8 * kLd) = make_float2(sum[n][2] + acc[n][2], sum[n][3] + acc[n][3]);
+    const int r = TC ? 16 * (warp & 3) + g : wr * 32 + n / kNT * 16 + g;
+    const int q = TC ? (warp >> 2) * (NC / 2) + 8 * n : wn * (NC / 4) + n % kNT * 8;
+    float* d = sums + r * kLd + q + 2 * t;
+    if (!ok) sum[n][0] = sum[n][1] = sum[n][2] = sum[n][3] = __int_as_float(0x7fffffff);
+    *reinterpret_cast<float2*>(d) = make_float2(sum[n][0], sum[n][1]);
+    *reinterpret_cast<float2*>(d + 8 * kLd) = make_float2(sum[n][2], sum[n][3]);
+  }
+  if (TC && warp == 0) {   // (all warps' loads are over: the barrier above)
+    tc_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(sums_at), "r"(kSumCols));
   }
   const cg::cluster_group cluster = cg::this_cluster();
   if (ks > 1) cluster.sync();
@@ -990,8 +1080,7 @@ __global__ void __launch_bounds__(kThreads, 2) expand_tiles_kernel(const AdaptPa
   __syncthreads();
   tc_after();
   sums.at = sums_slot;
-  // (only now: a kernel behind that takes tensor memory and waits for this one must not take it first)
-  dev::pdl_trigger();
+  dev::pdl_trigger();   // (only now: see shrink_tiles_kernel)
   find_tile<ER>(p, 0, tile);
   // (no more tiles than sequences in their order can have)
   const int units = min(tile.tiles, p.rows / ER + min(p.n_seq, p.rows)) * col_tiles;
@@ -1038,10 +1127,10 @@ constexpr int shrink_tiles_smem() {
   return kStages * (TR + NC) * 128 + 1024;   // (stages start where their swizzle does)
 }
 
-template <class T, int NC>
+template <class T, int NC, bool TC>
 cudaError_t launch_shrink_tiles(const AdaptParams& p, int tiles, int chunks, int sms, cudaStream_t st) {
-  // CTAs of a tile: as many as 3/2 an SM (two run at a time), with 256 inputs each at least.  Twelve sequences of 1 to
-  // 120 rows: 34 us, with at most one an SM 39, two 34; four prompts 86 in any case.
+  // CTAs of a tile: as many as 3/2 an SM (two run at a time), with 256 inputs each at least.  Four prompts in
+  // 108 tiles: 96 us with two CTAs a tile, 101 with four, which then run in two waves; 254 rows the same either way.
   int ks = 1;
   while (ks < kMaxCluster && 2 * (tiles * chunks * ks * 2) <= 3 * sms && p.site.k >= 512 * ks) ks *= 2;
   cudaLaunchConfig_t cfg = {};
@@ -1056,9 +1145,9 @@ cudaError_t launch_shrink_tiles(const AdaptParams& p, int tiles, int chunks, int
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 2 : 1;
-  if constexpr (std::is_same<T, __nv_bfloat16>::value)
-    if (p.x16) return cudaLaunchKernelEx(&cfg, shrink_tiles_kernel<T, NC, true>, p, ks);
-  return cudaLaunchKernelEx(&cfg, shrink_tiles_kernel<T, NC, false>, p, ks);
+  if constexpr (std::is_same<T, __nv_bfloat16>::value && !TC)
+    if (p.x16) return cudaLaunchKernelEx(&cfg, shrink_tiles_kernel<T, NC, TC, true>, p, ks);
+  return cudaLaunchKernelEx(&cfg, shrink_tiles_kernel<T, NC, TC, false>, p, ks);
 }
 
 template <class T, class O>
@@ -1067,11 +1156,13 @@ cudaError_t launch_tiles(const AdaptParams& p, int sms, cudaStream_t st) {
   const int wide = p.rows / ER + std::min(p.n_seq, p.rows);
   const int stacked = p.site.n_parts * p.site.max_rank;
   // all parts at once, as far as a CTA's sums hold them
+  constexpr bool kTc = !std::is_same<O, float>::value;
   cudaError_t e;
-  if (stacked <= 64) e = launch_shrink_tiles<T, 64>(p, tiles, 1, sms, st);
-  else if (stacked <= 128) e = launch_shrink_tiles<T, 128>(p, tiles, 1, sms, st);
-  else if (p.site.max_rank <= 64) e = launch_shrink_tiles<T, 64>(p, tiles, p.site.n_parts, sms, st);
-  else e = launch_shrink_tiles<T, 128>(p, tiles, p.site.n_parts, sms, st);
+  if (stacked <= 64) e = launch_shrink_tiles<T, 64, kTc>(p, tiles, 1, sms, st);
+  else if (stacked <= 128) e = launch_shrink_tiles<T, 128, kTc>(p, tiles, 1, sms, st);
+  else if (kTc && stacked <= 192) e = launch_shrink_tiles<T, kTc ? 192 : 128, kTc>(p, tiles, 1, sms, st);
+  else if (p.site.max_rank <= 64) e = launch_shrink_tiles<T, 64, kTc>(p, tiles, p.site.n_parts, sms, st);
+  else e = launch_shrink_tiles<T, 128, kTc>(p, tiles, p.site.n_parts, sms, st);
   if (e != cudaSuccess) return e;
   int cols = 0;
   for (int j = 0; j < p.site.n_parts; ++j) cols += (p.site.cols[j] + kTileN - 1) / kTileN;
@@ -1081,13 +1172,16 @@ cudaError_t launch_tiles(const AdaptParams& p, int sms, cudaStream_t st) {
   return launch_k(expand_tiles_kernel<T, O>, dim3(ctas), dim3(kThreads), smem, st, p, cols);
 }
 
-template <class T, bool X16>
+template <class T, bool TC, bool X16>
 cudaError_t setup_shrink() {
   const auto set = [](void (*k)(AdaptParams, int), int bytes) {
     return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   };
-  const cudaError_t e = set(shrink_tiles_kernel<T, 64, X16>, shrink_tiles_smem<64>());
-  return e == cudaSuccess ? set(shrink_tiles_kernel<T, 128, X16>, shrink_tiles_smem<128>()) : e;
+  cudaError_t e = set(shrink_tiles_kernel<T, 64, TC, X16>, shrink_tiles_smem<64>());
+  if (e == cudaSuccess) e = set(shrink_tiles_kernel<T, 128, TC, X16>, shrink_tiles_smem<128>());
+  if constexpr (TC)
+    if (e == cudaSuccess) e = set(shrink_tiles_kernel<T, 192, TC, X16>, shrink_tiles_smem<192>());
+  return e;
 }
 template <class T, class O>
 cudaError_t setup_expand() {
@@ -1112,15 +1206,14 @@ cudaError_t launch(const AdaptParams& p, cudaStream_t st) {
   return launch_k(expand_kernel<T, float>, grid, kThreads, 0, st, p);
 }
 
-// Rows of a sequence, on average, and in all, from which tiles of one sequence's rows pay.  Sequences x rows (all of one
-// length), tiles of eight against these, us (q, k and v of 3584 inputs; rank 16): 32 x 8 20, 27; 32 x 16 34, 27; 64 x 16 68,
-// 42; 8 x 8 9, 16; 8 x 16 13, 16 (rank 64: 19, 20); 8 x 24 16, 16; 1 x 40 9, 14.  One rule for a batch is not the best
-// where lengths are unequal: 2048 rows and 150 single ones (14.6 on average) take 228 us, and 120 (17.9) 80.
+// Rows of a sequence, on average, and in all, from which tiles of one sequence's rows pay.  Sequences x rows, tiles of
+// eight against these, us (q, k and v of 3584 inputs; rank 16): 32 x 8 22, 24; 32 x 16 38, 25; 64 x 16 78,
+// 37; 8 x 8 9, 15; 8 x 16 14, 15 (rank 64: 20, 18); 8 x 24 17, 15; 1 x 40 9, 13.
 constexpr int kManyRows = 16, kManyInAll = 128;
 
 int adapt_split(const kvr_adapter_site& s, int rows, int sms) {
-  // parts of the inputs: two CTAs an SM (8 x 8 rows of 18944 inputs: 11.2 us, one 13.1), of 192 inputs each at least
-  // (64 rows of 4096 inputs, an adapter each: 18.1 us, with 128 19.6; one row: 8.0 and 7.4)
+  // parts of the inputs: two CTAs an SM (8 x 8 rows of 18944 inputs: 12.0 us, one 14.3), of 192 inputs each at least
+  // (64 rows of 4096 inputs, an adapter each: 19.5 us, with 128 21.1; one row: 8.4 and 7.8)
   const int blocks = (rows + R - 1) / R;
   const int most = std::max(1, std::min(kAdaptMaxSplit, s.k / 192));
   return std::max(1, std::min(most, 2 * sms / blocks));
@@ -1129,9 +1222,11 @@ int adapt_split(const kvr_adapter_site& s, int rows, int sms) {
 }  // namespace
 
 cudaError_t adapt_setup() {
-  cudaError_t e = setup_shrink<__nv_bfloat16, false>();
-  if (e == cudaSuccess) e = setup_shrink<__nv_bfloat16, true>();   // (the layer stack's)
-  if (e == cudaSuccess) e = setup_shrink<__half, false>();
+  cudaError_t e = setup_shrink<__nv_bfloat16, true, false>();
+  if (e == cudaSuccess) e = setup_shrink<__nv_bfloat16, false, false>();
+  if (e == cudaSuccess) e = setup_shrink<__nv_bfloat16, false, true>();   // (the layer stack's: 32-bit outputs)
+  if (e == cudaSuccess) e = setup_shrink<__half, true, false>();
+  if (e == cudaSuccess) e = setup_shrink<__half, false, false>();
   if (e == cudaSuccess) e = setup_expand<__nv_bfloat16, __nv_bfloat16>();
   if (e == cudaSuccess) e = setup_expand<__nv_bfloat16, float>();
   if (e == cudaSuccess) e = setup_expand<__half, __half>();
