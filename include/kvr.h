@@ -669,10 +669,10 @@ const char* kvr_pages_error(const kvr_pages* pages);
  * Weights are summed as whole numbers of 2^-44 of the largest, so the sums
  * (and with them the tokens) do not depend on the launch.
  *
- * The calls have no handle: they hold nothing between calls (but a device's status
- * word: kvr_batch_sync), work only in the
- * memory that they are given, and may run at the same time on several streams;
- * they can be captured.  The device of the memory has to be the current one.
+ * The calls have no handle: they hold nothing between calls but a device's status
+ * word (kvr_batch_sync), work only in the memory that they are given, and may run at
+ * the same time on several streams; they can be captured.  The device of the memory
+ * has to be the current one.
  * Errors: a negative code, kvr_batch_error says why (the calling thread's last
  * failure).  A refused call launches nothing.
  */

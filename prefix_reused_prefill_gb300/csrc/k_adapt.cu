@@ -13,8 +13,8 @@
 // straight from global memory, 16 or 8 bytes each: which inputs share a fragment
 // does not matter as long as both operands agree.  Bound: the chain of loads (whose rows, which
 // adapter, where it is, its values), twice; where each row has its own adapter, the loads of A
-// and B.  q, k and v of 3584 inputs, one row of rank 16: 8.4 us; of 4096 inputs, 64 rows with an
-// adapter each: 19.5 us (40 MB).  Eight sequences of 8 rows, 18944 inputs, 32-bit outputs: 12 us.
+// and B.  q, k and v of 3584 inputs, one row of rank 16: 8.0 us; of 4096 inputs, 64 rows with an
+// adapter each: 18.1 us (40 MB).  Eight sequences of 8 rows, 18944 inputs, 32-bit outputs: 11.2 us.
 //
 // Many: tiles of one sequence's rows, below.
 #include <cooperative_groups.h>
@@ -426,16 +426,16 @@ __global__ void __launch_bounds__(kThreads, 2) expand_kernel(const AdaptParams p
 // ---------------------------------------------------------------- many rows a sequence
 // Tiles of one sequence's rows.  shrink_tiles_kernel streams 64 rows of x and A through
 // shared memory (a cluster cuts the inputs, its CTAs' sums are joined in distributed
-// shared memory) and leaves s in terms of T; expand_tiles_kernel multiplies 128 rows of
-// them with 128 outputs' B while base is on its way.  Both on tcgen05, sums in tensor memory.
+// shared memory) and leaves s in terms of T, by tcgen05 or mma.sync (launch_tiles); expand_tiles_kernel
+// multiplies 128 rows of them with 128 outputs' B while base is on its way, on tcgen05.
 // Addresses are the adapters', known on the device only, so copies are cp.async, not tensor maps'.
 // Bound: shrink by what it moves from L2 to the SMs (each 64 inputs of 64 rows bring up to 192 rows
 // of A; 64 rows of x instead of 128, since two CTAs an SM cover each other's start and end),
 // expand by base and out.  Four ragged prompts, 6.7k rows of 4096 inputs, rank 64, 6144 outputs:
-// 85 us (105 with mma.sync), of which a plain copy of x, base and out would take 33.
+// 91 us, of which a plain copy of x, base and out would take 33; with 32-bit base and out 117 of 57.
 constexpr int TR = 64;
 constexpr int kStep = 64;       // inputs of a stage: 128 bytes a row
-constexpr int kStages = 3;      // (4 and 6 leave one CTA an SM: four prompts 107 us, with 3 100)
+constexpr int kStages = 3;      // (4 and 6 leave one CTA an SM for 192 rows of A: four prompts 103 us, with 3 91)
 constexpr int kMaxCluster = 8;
 constexpr int ER = 128, kTileN = 128;   // rows and outputs of a tile of expand
 
@@ -1129,10 +1129,10 @@ constexpr int shrink_tiles_smem() {
 
 template <class T, int NC, bool TC>
 cudaError_t launch_shrink_tiles(const AdaptParams& p, int tiles, int chunks, int sms, cudaStream_t st) {
-  // CTAs of a tile: as many as 3/2 an SM (two run at a time), with 256 inputs each at least.  Four prompts in
-  // 108 tiles: 96 us with two CTAs a tile, 101 with four, which then run in two waves; 254 rows the same either way.
+  // CTAs of a tile: as many as two an SM (they run at a time), with 256 inputs each at least.  2048 rows of 18944
+  // inputs, rank 32: 53 us, with up to 3/2 an SM 75; four prompts 91 either way, with up to 3 an SM 95.
   int ks = 1;
-  while (ks < kMaxCluster && 2 * (tiles * chunks * ks * 2) <= 3 * sms && p.site.k >= 512 * ks) ks *= 2;
+  while (ks < kMaxCluster && tiles * chunks * ks * 2 <= 2 * sms && p.site.k >= 512 * ks) ks *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * ks), 1, (unsigned)chunks);
   cfg.blockDim = dim3(kThreads);
@@ -1155,13 +1155,16 @@ cudaError_t launch_tiles(const AdaptParams& p, int sms, cudaStream_t st) {
   const int tiles = p.rows / TR + std::min(p.n_seq, p.rows);   // at most
   const int wide = p.rows / ER + std::min(p.n_seq, p.rows);
   const int stacked = p.site.n_parts * p.site.max_rank;
-  // all parts at once, as far as a CTA's sums hold them
+  // All parts at once, as far as a CTA's sums hold them.  On tcgen05 sums have to be fetched at the end of every chain:
+  // products with 64 of A are too small for that, and 32-bit outputs are faster without.  Us, mma.sync and
+  // tcgen05 (8192 rows): one output of 4096 inputs, rank 64, 60, 73; three of 3584, rank 64, 102, 84; four
+  // prompts with 32-bit outputs (4096 inputs, three of rank 64) 117, 132.
   constexpr bool kTc = !std::is_same<O, float>::value;
   cudaError_t e;
-  if (stacked <= 64) e = launch_shrink_tiles<T, 64, kTc>(p, tiles, 1, sms, st);
+  if (stacked <= 64) e = launch_shrink_tiles<T, 64, false>(p, tiles, 1, sms, st);
   else if (stacked <= 128) e = launch_shrink_tiles<T, 128, kTc>(p, tiles, 1, sms, st);
   else if (kTc && stacked <= 192) e = launch_shrink_tiles<T, kTc ? 192 : 128, kTc>(p, tiles, 1, sms, st);
-  else if (p.site.max_rank <= 64) e = launch_shrink_tiles<T, 64, kTc>(p, tiles, p.site.n_parts, sms, st);
+  else if (p.site.max_rank <= 64) e = launch_shrink_tiles<T, 64, false>(p, tiles, p.site.n_parts, sms, st);
   else e = launch_shrink_tiles<T, 128, kTc>(p, tiles, p.site.n_parts, sms, st);
   if (e != cudaSuccess) return e;
   int cols = 0;
@@ -1172,16 +1175,10 @@ cudaError_t launch_tiles(const AdaptParams& p, int sms, cudaStream_t st) {
   return launch_k(expand_tiles_kernel<T, O>, dim3(ctas), dim3(kThreads), smem, st, p, cols);
 }
 
-template <class T, bool TC, bool X16>
+template <class T, int NC, bool TC, bool X16>
 cudaError_t setup_shrink() {
-  const auto set = [](void (*k)(AdaptParams, int), int bytes) {
-    return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  };
-  cudaError_t e = set(shrink_tiles_kernel<T, 64, TC, X16>, shrink_tiles_smem<64>());
-  if (e == cudaSuccess) e = set(shrink_tiles_kernel<T, 128, TC, X16>, shrink_tiles_smem<128>());
-  if constexpr (TC)
-    if (e == cudaSuccess) e = set(shrink_tiles_kernel<T, 192, TC, X16>, shrink_tiles_smem<192>());
-  return e;
+  return cudaFuncSetAttribute(shrink_tiles_kernel<T, NC, TC, X16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              shrink_tiles_smem<NC>());
 }
 template <class T, class O>
 cudaError_t setup_expand() {
@@ -1206,14 +1203,15 @@ cudaError_t launch(const AdaptParams& p, cudaStream_t st) {
   return launch_k(expand_kernel<T, float>, grid, kThreads, 0, st, p);
 }
 
-// Rows of a sequence, on average, and in all, from which tiles of one sequence's rows pay.  Sequences x rows, tiles of
-// eight against these, us (q, k and v of 3584 inputs; rank 16): 32 x 8 22, 24; 32 x 16 38, 25; 64 x 16 78,
-// 37; 8 x 8 9, 15; 8 x 16 14, 15 (rank 64: 20, 18); 8 x 24 17, 15; 1 x 40 9, 13.
+// Rows of a sequence, on average, and in all, from which tiles of one sequence's rows pay.  Sequences x rows (all of one
+// length), tiles of eight against these, us (q, k and v of 3584 inputs; rank 16): 32 x 8 20, 27; 32 x 16 34, 27; 64 x 16 68,
+// 42; 8 x 8 9, 16; 8 x 16 13, 16 (rank 64: 19, 20); 8 x 24 16, 16; 1 x 40 9, 14.  One rule for a batch is not the best
+// where lengths are unequal: 2048 rows and 150 single ones (14.6 on average) take 226 us, and 120 (17.9) 85.
 constexpr int kManyRows = 16, kManyInAll = 128;
 
 int adapt_split(const kvr_adapter_site& s, int rows, int sms) {
-  // parts of the inputs: two CTAs an SM (8 x 8 rows of 18944 inputs: 12.0 us, one 14.3), of 192 inputs each at least
-  // (64 rows of 4096 inputs, an adapter each: 19.5 us, with 128 21.1; one row: 8.4 and 7.8)
+  // parts of the inputs: two CTAs an SM (8 x 8 rows of 18944 inputs: 11.2 us, one 13.1), of 192 inputs each at least
+  // (64 rows of 4096 inputs, an adapter each: 18.1 us, with 128 19.6; one row: 8.0 and 7.4)
   const int blocks = (rows + R - 1) / R;
   const int most = std::max(1, std::min(kAdaptMaxSplit, s.k / 192));
   return std::max(1, std::min(most, 2 * sms / blocks));
@@ -1222,11 +1220,16 @@ int adapt_split(const kvr_adapter_site& s, int rows, int sms) {
 }  // namespace
 
 cudaError_t adapt_setup() {
-  cudaError_t e = setup_shrink<__nv_bfloat16, true, false>();
-  if (e == cudaSuccess) e = setup_shrink<__nv_bfloat16, false, false>();
-  if (e == cudaSuccess) e = setup_shrink<__nv_bfloat16, false, true>();   // (the layer stack's: 32-bit outputs)
-  if (e == cudaSuccess) e = setup_shrink<__half, true, false>();
-  if (e == cudaSuccess) e = setup_shrink<__half, false, false>();
+  cudaError_t e = setup_shrink<__nv_bfloat16, 64, false, false>();
+  if (e == cudaSuccess) e = setup_shrink<__nv_bfloat16, 128, false, false>();
+  if (e == cudaSuccess) e = setup_shrink<__nv_bfloat16, 64, false, true>();   // (the layer stack's: 32-bit outputs)
+  if (e == cudaSuccess) e = setup_shrink<__nv_bfloat16, 128, false, true>();
+  if (e == cudaSuccess) e = setup_shrink<__nv_bfloat16, 128, true, false>();
+  if (e == cudaSuccess) e = setup_shrink<__nv_bfloat16, 192, true, false>();
+  if (e == cudaSuccess) e = setup_shrink<__half, 64, false, false>();
+  if (e == cudaSuccess) e = setup_shrink<__half, 128, false, false>();
+  if (e == cudaSuccess) e = setup_shrink<__half, 128, true, false>();
+  if (e == cudaSuccess) e = setup_shrink<__half, 192, true, false>();
   if (e == cudaSuccess) e = setup_expand<__nv_bfloat16, __nv_bfloat16>();
   if (e == cudaSuccess) e = setup_expand<__nv_bfloat16, float>();
   if (e == cudaSuccess) e = setup_expand<__half, __half>();
