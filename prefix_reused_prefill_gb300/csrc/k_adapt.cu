@@ -1204,8 +1204,8 @@ cudaError_t launch(const AdaptParams& p, cudaStream_t st) {
 }
 
 // Rows of a sequence, on average, and in all, from which tiles of one sequence's rows pay.  Sequences x rows (all of one
-// length), tiles of eight against these, us (q, k and v of 3584 inputs; rank 16): 32 x 8 20, 27; 32 x 16 34, 27; 64 x 16 68,
-// 42; 8 x 8 9, 16; 8 x 16 13, 16 (rank 64: 19, 20); 8 x 24 16, 16; 1 x 40 9, 14.  One rule for a batch is not the best
+// length), tiles of eight against these, us (q, k and v of 3584 inputs; rank 16): 32 x 8 20, 24; 32 x 16 34, 31; 64 x 16 67,
+// 47; 8 x 8 9, 15; 8 x 16 13, 15 (rank 64: 19, 20); 8 x 24 16, 16; 1 x 40 9, 13.  One rule for a batch is not the best
 // where lengths are unequal: 2048 rows and 150 single ones (14.6 on average) take 226 us, and 120 (17.9) 85.
 constexpr int kManyRows = 16, kManyInAll = 128;
 

@@ -26,8 +26,9 @@
 // a row of 262144 tokens: maximum 4 us, bins 12, their sums and the search 4, and for
 // each end of a run that more than 2048 tokens stand before, 2 to 7 us of a pass that
 // looks up one bin's tokens and 3 that orders them.
-// Per call in a graph: one row of 128256 10.7 us, 64 rows of it with different
-// settings 58, 16 rows of 262144 without any bound 55.
+// Per call in a graph: one row of 32000 10.5 us, 64 rows of 131072 with different
+// settings 57, 16 rows of 262144 without any bound 55 (15 clusters of eight fit alone; where two share their SMs
+// the passes take twice as long).
 #include <cooperative_groups.h>
 
 #include <type_traits>
