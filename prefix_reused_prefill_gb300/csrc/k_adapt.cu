@@ -575,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_tiles_kernel(const AdaptPa
   __shared__ Tile tile;
   __shared__ __align__(8) uint64_t bars[kStages];   // of a stage's products
   __shared__ uint32_t sums_slot;
-  constexpr int kSumCols = NC <= 64 ? 64 : NC <= 128 ? 128 : 256;
+  constexpr int kSumCols = NC <= 128 ? 128 : 256;   // (TC)
   constexpr int kXBytes = TR * 128, kStage = kXBytes + NC * 128;
   constexpr int kNT = NC / 32;    // tiles of 8 ranks a warp
   constexpr int kLd = NC + 4;
