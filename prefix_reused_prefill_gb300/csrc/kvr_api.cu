@@ -1456,12 +1456,6 @@ bool adapters_fit(const kvr_config& k, const kvr_adapter_site* sites, int* bad) 
   return true;
 }
 
-// whether two runs of bytes meet (null: nowhere)
-bool meet(const void* a, size_t an, const void* b, size_t bn) {
-  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-  return a && b && x < y + bn && y < x + an;
-}
-
 static_assert(sizeof(Requests) % 4 == 0 && sizeof(Requests) <= 4000, "they travel as a kernel's argument");
 __global__ void put_requests(const Requests in, Requests* to) {
   dev::pdl_trigger();
@@ -1515,8 +1509,9 @@ int batch_common(kvr_ctx* c, int n_seq, const int* slots, const int* lens, const
     const size_t need = add + adapted_part_bytes(c->cfg, adapters->sites, total);
     if (adapters->work_bytes < need)
       return fail(c, KVR_ERR_CAPACITY, "the adapters' work area is smaller than %zu bytes", need);
-    const size_t io = (size_t)total * c->cfg.hidden * 2;
-    if (meet(adapters->work, need, hidden, io) || meet(adapters->work, need, out, io))
+    const Span work(adapters->work, (long long)need);
+    const long long io = (long long)total * c->cfg.hidden * 2;
+    if (shared(work, {hidden, io}) || shared(work, {out, io}))
       return fail(c, KVR_ERR_ARG, "the adapters' work area shares memory with hidden or out");
     ad.sites = adapters->sites;
     ad.cu = c->requests->cu;
@@ -2008,12 +2003,11 @@ int kvr_verify_sample_batch(kvr_ctx* c, int n_seq, const int* slots, const int* 
   if (total > kVerifyMaxRows) return fail(c, KVR_ERR_ARG, "%d rows exceed %d for this call", total, kVerifyMaxRows);
   if (draft_probs && total > 1 && draft_stride < head->vocab)
     return fail(c, KVR_ERR_ARG, "the drafts' row stride must cover a row");
-  const size_t row = (size_t)head->vocab * 4, io = (size_t)total * c->cfg.hidden * 2;
-  const size_t drafts = (size_t)(total - 1) * (total > 1 ? draft_stride : 0) * 4 + row;
-  const void* work = adapters ? adapters->work : nullptr;
-  const size_t work_bytes = adapters ? adapters->work_bytes : 0;
-  if (meet(logits, total * row, draft_probs, drafts) || meet(logits, total * row, hidden, io) || meet(logits, total * row, out, io) ||
-      meet(logits, total * row, work, work_bytes) || meet(draft_probs, drafts, out, io) || meet(draft_probs, drafts, work, work_bytes))
+  const long long row = 4ll * head->vocab, io = (long long)total * c->cfg.hidden * 2;
+  const Span to(logits, total * row), drafts(draft_probs, total, total > 1 ? 4 * draft_stride : row, row), rows_in(hidden, io),
+      rows_out(out, io), work(adapters ? adapters->work : nullptr, adapters ? (long long)adapters->work_bytes : 0);
+  if (shared(to, drafts) || shared(to, rows_in) || shared(to, rows_out) || shared(to, work) || shared(drafts, rows_out) ||
+      shared(drafts, work))
     return fail(c, KVR_ERR_ARG, "logits, out or the adapters' work area shares memory with another argument");
   Requests req;
   memset(&req, 0, sizeof req);

@@ -50,29 +50,6 @@ constexpr int kMaxSampleRows = 1 << 20;
 int type_bytes(int type) { return type == KVR_ACT_F32 ? 4 : 2; }
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
-// Rows of memory: n of `width` bytes, `stride` bytes apart (one row: any).
-struct Span {
-  const void* p;
-  long long n, stride, width;
-  Span(const void* p_, long long width_) : p(p_), n(1), stride(width_), width(width_) {}
-  Span(const void* p_, long long n_, long long stride_, long long width_) : p(p_), n(n_), stride(stride_), width(width_) {}
-  long long bytes() const { return (n - 1) * stride + width; }
-};
-// Whether two of them share a byte.  (Rows that stand among one another at different strides count as
-// sharing.)
-bool shared(const Span& a, const Span& b) {
-  if (!a.p || !b.p || a.n < 1 || b.n < 1) return false;
-  const long long off = (long long)((uintptr_t)b.p - (uintptr_t)a.p);   // of b, from a
-  if (off >= a.bytes() || -off >= b.bytes()) return false;
-  if (b.n == 1) {
-    const long long i = off < a.width ? 0 : (off - a.width) / a.stride + 1;   // the first row that ends behind b's start
-    return i < a.n && i * a.stride < off + b.width;
-  }
-  if (a.n == 1) return shared(b, a);
-  if (a.stride != b.stride) return true;
-  const long long in = ((off % a.stride) + a.stride) % a.stride;   // of b's rows, from the start of a's
-  return in < a.width || in + b.width > a.stride;
-}
 bool shared_with_any(const Span& out, const Span* in, int n) {
   for (int i = 0; i < n; ++i)
     if (shared(out, in[i])) return true;
@@ -101,6 +78,20 @@ int run_sample(const SampleParams& p, void* stream) {
 }
 
 }  // namespace
+
+bool kvr::shared(const Span& a, const Span& b) {
+  if (!a.p || !b.p || a.n < 1 || b.n < 1) return false;
+  const long long off = (long long)((uintptr_t)b.p - (uintptr_t)a.p);   // of b, from a
+  if (off >= a.bytes() || -off >= b.bytes()) return false;
+  if (b.n == 1) {
+    const long long i = off < a.width ? 0 : (off - a.width) / a.stride + 1;   // the first row that ends behind b's start
+    return i < a.n && i * a.stride < off + b.width;
+  }
+  if (a.n == 1) return shared(b, a);
+  if (a.stride != b.stride) return true;
+  const long long in = ((off % a.stride) + a.stride) % a.stride;   // of b's rows, from the start of a's
+  return in < a.width || in + b.width > a.stride;
+}
 
 bool kvr::adapter_site_ok(const kvr_adapter_site* s) {
   if (!s || !s->table || !aligned(s->table, 8) || s->n_adapters < 1 || s->max_rank < 8 || s->max_rank > KVR_MAX_RANK ||

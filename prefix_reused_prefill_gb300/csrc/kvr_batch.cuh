@@ -6,6 +6,18 @@
 
 namespace kvr {
 
+// Rows of memory: n of `width` bytes, `stride` bytes apart (one row: any).
+struct Span {
+  const void* p;
+  long long n, stride, width;
+  Span(const void* p_, long long width_) : p(p_), n(1), stride(width_), width(width_) {}
+  Span(const void* p_, long long n_, long long stride_, long long width_) : p(p_), n(n_), stride(stride_), width(width_) {}
+  long long bytes() const { return (n - 1) * stride + width; }
+};
+// Whether two of them share a byte.  (Rows that stand among one another at different strides count as
+// sharing.)
+bool shared(const Span& a, const Span& b);
+
 constexpr int kSampleIndexBits = 18;   // KVR_MAX_VOCAB = 2^18
 static_assert(KVR_MAX_VOCAB <= 1 << kSampleIndexBits, "a token's index has to fit beside its logit");
 
