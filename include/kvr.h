@@ -39,7 +39,8 @@
  * loads it, the fixed staging array of kvr_slot_match_static.  All calls that take a
  * stream are asynchronous on it, except kvr_slot_match (it waits for the
  * stream to read back the match lengths), kvr_verify_accept (it returns the
- * decision to the host; kvr_verify_sample_batch too) and kvr_sync_status.
+ * decision to the host; kvr_verify_sample_batch too), kvr_sync_status,
+ * kvr_pages_sync and kvr_batch_sync.
  *
  * Errors.  Every int-returning call returns KVR_OK (0) or a negative code;
  * kvr_last_error() says why.  A call refused by its checks launches nothing
@@ -677,9 +678,10 @@ const char* kvr_pages_error(const kvr_pages* pages);
  * failure).  A refused call launches nothing.
  */
 
-/* Waits for the stream.  KVR_ERR_TIMEOUT if a wait in a kernel of kvr_adapt on the current device has given up since
- * the last such report (never in normal operation): outputs of long sequences formed since then, on any stream, may read
- * NaN.  kvr_batch_selftest_wait lets such a wait run out, as kvr_selftest_wait does. */
+/* Waits for the stream.  KVR_ERR_TIMEOUT if a wait in a kernel of kvr_adapt on the
+ * current device has given up since the last such report (never in normal operation):
+ * outputs of long sequences formed since then, on any stream, may read NaN.
+ * kvr_batch_selftest_wait lets such a wait run out, as kvr_selftest_wait does. */
 int kvr_batch_sync(void* stream);
 int kvr_batch_selftest_wait(void* stream);
 
@@ -780,8 +782,9 @@ typedef struct kvr_adapter_site {
  *              then) or null (zeros); otherwise out shares no memory with the inputs.
  *   work       kvr_adapt_work_bytes(site, rows) bytes, 16-byte aligned, for this call alone.
  * x, base and out are 16-byte aligned.  Sums are 32-bit, the matrix units' own (whose last
- * bits are cut) over 128 inputs at most.  The low-rank product goes on in three terms of the site's type, whose sum is its value to 24 bits; out is
- * rounded once.  A row whose low-rank product is not finite reads NaN.
+ * bits are cut) over 128 inputs at most.  The low-rank product goes on in three terms of
+ * the site's type, whose sum is its value to 24 bits; out is rounded once.  A row whose
+ * low-rank product is not finite reads NaN; infinities in b are those of the formula.
  */
 size_t kvr_adapt_work_bytes(const kvr_adapter_site* site, int rows);
 int kvr_adapt(const kvr_adapter_site* site, const void* x, long long x_stride, const int32_t* cu_rows,
@@ -809,8 +812,8 @@ size_t kvr_adapters_work_bytes(const kvr_config* cfg, const kvr_adapter_site* si
 /* kvr_prefill_batch with adapter which[j] (host [n_seq]; others than the sites'
  * own: none) for conversation j.  What an adapter adds is formed from the
  * projection's bf16 input in 32 bits and joins its output before that is rounded,
- * rotated or multiplied.  Full layers only (KVR_ERR_UNSUPPORTED otherwise).  The work area shares no memory with hidden
- * or out. */
+ * rotated or multiplied.  Full layers only (KVR_ERR_UNSUPPORTED otherwise).  The work
+ * area shares no memory with hidden or out. */
 int kvr_prefill_batch_adapted(kvr_ctx* ctx, int n_seq, const int* slots, const int* lens, const int32_t* tokens,
                               const void* hidden, const kvr_layer_weights* weights, const kvr_adapters* adapters,
                               const int* which, void* out, void* stream);
