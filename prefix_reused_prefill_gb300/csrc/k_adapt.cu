@@ -569,8 +569,9 @@ __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_
 // Matrix units cut a sum's last bits at every product of 16 inputs instead of rounding them; over 4096 inputs in one
 // chain that is 2e-6 of the sum.  So chains are kChain stages, added up in registers: below 3e-7.
 constexpr int kChain = 2;
+// (Three CTAs an SM where shared memory allows them: three parts of rank 128, 8192 rows, 115 us, with two 133; one part 80, 78.)
 template <class T, int NC, bool TC, bool X16>
-__global__ void __launch_bounds__(kThreads, 2) shrink_tiles_kernel(const AdaptParams p, int ks) {
+__global__ void __launch_bounds__(kThreads, TC && NC == 128 ? 3 : 2) shrink_tiles_kernel(const AdaptParams p, int ks) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
   __shared__ Tile tile;
   __shared__ __align__(8) uint64_t bars[kStages];   // of a stage's products
